@@ -59,7 +59,11 @@ typedef enum fa_status {
   FA_ERR_DEVICE_TIMEOUT = 4
 } fa_status;
 
-typedef enum fa_dtype { FA_BF16 = 0, FA_FP32 = 1 } fa_dtype;
+/* FA_E4M3 is a storage type of the paged cache only (fa_cache_append, fa_cache_gather, fa_decode_tree). */
+typedef enum fa_dtype { FA_BF16 = 0, FA_FP32 = 1, FA_E4M3 = 2 } fa_dtype;
+
+/* Which elements of a head's rotated part form a pair: (i, i + d_rot/2) or (2i, 2i + 1). */
+typedef enum fa_rope_layout { FA_ROPE_HALF = 0, FA_ROPE_INTERLEAVED = 1 } fa_rope_layout;
 
 /* Attention mask.  FA_MASK_CAUSAL is the causal mask the lesson's memory lab
  * uses (§5, is_causal=True), aligned to the bottom-right corner: query row i of
@@ -299,6 +303,108 @@ FA_API fa_status fa_backward_masked(const void* q, const void* k, const void* v,
                                     const void* dout, void* dq, void* dk, void* dv, int B, int H, int N, int d,
                                     fa_dtype dtype, float scale, void* workspace, size_t workspace_bytes,
                                     fa_mask mask, void* stream);
+
+/*
+ * fa_rope — rotary positions of the query and key heads, or their gradient.
+ *   Pair i of the first d_rot elements of every head turns by θ = p·w_i, p the
+ *   token's position and w_i = inv_freq[i]:
+ *     y₁ = μ(x₁ cos θ − x₂ sin θ),  y₂ = μ(x₂ cos θ + x₁ sin θ);
+ *   elements from d_rot on are copied.  With inverse = 1 it turns by −θ, which
+ *   with the same μ is the gradient: pass dq and dk for q and k.
+ *   q [B,H_q,N,d], k [B,H_k,N,d] (k and k_out NULL with H_k = 0), FA_BF16 or
+ *   FA_FP32; q_out, k_out alike, equal to q, k to work in place (with the same
+ *   strides), otherwise not overlapping them.
+ *   strides: NULL for contiguous tensors, or 12 element strides
+ *   {q_b, q_h, q_n, k_…, q_out_…, k_out_…} with d innermost; any stride >= 0 for
+ *   inputs, outputs must not overlap themselves.  No alignment beyond the
+ *   element's is needed (16-byte alignment throughout is faster).
+ *   positions: device int32, entry b·pos_stride_b + n (pos_stride_b = 0 shares
+ *   one row among the batch), or NULL for n; position0 is added.  Any int32
+ *   position is exact: angles are reduced in 64-bit fixed point.
+ *   inv_freq: d_rot/2 float64 values on the HOST, read during the call; scaled
+ *   contexts are scaled frequencies and a magnitude μ other than 1.
+ *   Supported: even d <= 256, even d_rot <= d.
+ */
+FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k, int N,
+                         int d, int d_rot, fa_dtype dtype, const int64_t* strides, const int32_t* positions,
+                         int64_t pos_stride_b, int position0, const double* inv_freq, float magnitude,
+                         fa_rope_layout layout, int inverse, void* stream);
+
+/*
+ * fa_cache_append — writes new keys and values into a paged cache.
+ *   k, v: bf16 [B,H_kv,N,d]; k_cache, v_cache, block_table as for
+ *   fa_decode_paged.  Token n of sequence b goes to logical position start[b] + n
+ *   for n < new_lens[b] (device int32 [B], NULL for N); later tokens are padding
+ *   and are not read.  No other slot of the cache is touched.
+ *   cache_dtype FA_BF16 copies rows.  FA_E4M3 quantises them: codes
+ *   c = rn(x·2^−k) in k_cache, v_cache (one byte each) and the byte k + 127 in
+ *   k_scale, v_scale [num_blocks, H_kv, block_size], with k >= −126 the smallest
+ *   whole number for which the row's largest finite magnitude is <= 448·2^k.
+ *   Infinities and NaN become NaN codes.  k_scale and v_scale are ignored for FA_BF16.
+ *   strides: NULL for contiguous k, v, or 6 element strides {k_b, k_h, k_n, v_…},
+ *   multiples of 8, >= 0.  Two tokens must not name the same slot in one call.
+ *   Page ids and positions outside the table, and new_lens outside [0, N], are
+ *   caught on the device: those tokens are not written and fa_device_status
+ *   then reports FA_ERR_INVALID_ARG.
+ *   Supported: d = 64 or 128, block_size ∈ {16, 32, 64, 128}.
+ */
+FA_API fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, uint8_t* k_scale,
+                                 uint8_t* v_scale, const int32_t* block_table, const int32_t* start,
+                                 const int32_t* new_lens, int B, int H_kv, int N, int num_blocks, int block_size,
+                                 int max_blocks, int d, fa_dtype cache_dtype, const int64_t* strides, void* stream);
+
+/*
+ * fa_cache_gather — reads the first N keys and values of every sequence back
+ *   as bf16 rows, e.g. for fa_forward over a cached prefix.
+ *   Arguments as for fa_cache_append, k and v [B,H_kv,N,d] being written; rows
+ *   n >= seq_lens[b] are set to zero.  E4M3 codes are multiplied by their row's
+ *   power of two, which is exact.  seq_lens outside [0, max_blocks·block_size]
+ *   and bad page ids give zero rows and FA_ERR_INVALID_ARG from fa_device_status.
+ */
+FA_API fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                                 const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* k,
+                                 void* v, int B, int H_kv, int N, int num_blocks, int block_size, int max_blocks,
+                                 int d, fa_dtype cache_dtype, const int64_t* strides, void* stream);
+
+/*
+ * fa_decode_tree_choose_splits — the split count the library would take for
+ *   fa_decode_tree with sequences of up to N_kv keys on the current device
+ *   (0 for bad arguments).  fa_decode_tree_workspace_size — bytes of workspace
+ *   for a split count (0 for bad arguments).
+ */
+FA_API int fa_decode_tree_choose_splits(int B, int H_q, int H_kv, int T, int N_kv);
+FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int T, int d, int n_splits);
+
+/*
+ * fa_decode_tree — attention of T drafted tokens per sequence over a paged
+ *   cache (T = 1 is plain decode), grouped query heads, bf16 or E4M3 cache.
+ *   The drafted tokens' keys and values are in the cache already
+ *   (fa_cache_append): sequence b holds seq_lens[b] keys, of which the last
+ *   m_b = draft_lens[b] (device int32 [B], NULL for T) belong to its drafted
+ *   tokens 0 … m_b − 1.  Token t < m_b sees the whole context (the first
+ *   seq_lens[b] − m_b keys) and drafted key u < m_b where
+ *   tree_mask[b·mask_stride_b + t·T + u] != 0 (device bytes; NULL: u <= t).  A
+ *   row that sees no key, padding rows t >= m_b among them, gives O = 0 and
+ *   LSE = −∞.  Keys a row does not see do not reach its results, whatever they
+ *   hold; slots past a sequence's end are not read into results.
+ *   q, o [B,H_q,T,d] bf16; strides NULL or 6 element strides {q_b, q_h, q_t, o_…},
+ *   multiples of 8, >= 0 (o must not overlap itself); lse [B,H_q,T] float32 or NULL.
+ *   Caches, scales and block_table as for fa_cache_append.
+ *   draft_lens outside [0, T], seq_lens outside [m_b, max_blocks·block_size]
+ *   and bad page ids are caught on the device (the sequence counts as empty,
+ *   page 0 is read) and reported by fa_device_status as FA_ERR_INVALID_ARG;
+ *   seq_lens[b] = 0 without draft_lens is an unused batch slot, not an error.
+ *   workspace: fa_decode_tree_workspace_size() bytes, 16-byte aligned, contents
+ *   on entry do not matter.
+ *   Supported: d = 64 or 128, block_size ∈ {16, 32, 64, 128}, H_q = G·H_kv with
+ *   G <= 128, T <= 256, 1 <= n_splits <= 256.
+ */
+FA_API fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                                const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* draft_lens, const uint8_t* tree_mask, int64_t mask_stride_b, void* o,
+                                float* lse, int B, int H_q, int H_kv, int T, int num_blocks, int block_size,
+                                int max_blocks, int d, fa_dtype cache_dtype, float scale, const int64_t* strides,
+                                int n_splits, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * fa_device_status — synchronises `stream`, then reports FA_ERR_DEVICE_TIMEOUT

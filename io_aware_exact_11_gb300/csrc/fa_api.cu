@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/fa.h"
 #include "fa_kernels.h"
@@ -930,6 +931,305 @@ fa_status fa_backward_masked(const void* q, const void* k, const void* v, const 
                        mask == FA_MASK_CAUSAL ? 1 : 0, stream);
 }
 
+}  // extern "C"
+
+// ------------------------------------- rotary positions, paged cache, drafted tokens
+
+namespace {
+
+// True if a [n0, n1, n2, d] tensor with these element strides stores every row in a place of its own.
+bool rows_distinct(int n0, int n1, int n2, int d, const int64_t* st) {
+  std::pair<int64_t, int64_t> dim[3] = {{st[0], n0}, {st[1], n1}, {st[2], n2}};
+  std::sort(dim, dim + 3);
+  int64_t extent = d;
+  for (const auto& x : dim) {
+    if (x.second == 1) continue;
+    if (x.first < extent) return false;
+    extent += x.first * (x.second - 1);
+  }
+  return true;
+}
+
+void contiguous_strides(int64_t* st, int H, int N, int d) {
+  st[0] = static_cast<int64_t>(H) * N * d;
+  st[1] = static_cast<int64_t>(N) * d;
+  st[2] = d;
+}
+
+// Checks shared by the paged-cache entry points.
+fa_status check_cache(const char* who, const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, const void* block_table, int B, int H_kv, int num_blocks, int block_size,
+                      int max_blocks, int d, fa_dtype dtype) {
+  if (!k_cache || !v_cache || !block_table) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (B <= 0 || H_kv <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks <= 0 || d <= 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (dtype != FA_BF16 && dtype != FA_FP32 && dtype != FA_E4M3)
+    return fail(FA_ERR_INVALID_ARG, "%s: unknown cache dtype %d", who, static_cast<int>(dtype));
+  if (dtype == FA_FP32) return fail(FA_ERR_UNSUPPORTED, "%s: only bf16 and E4M3 caches are built", who);
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "%s: head dim %d not built (64, 128)", who, d);
+  if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
+    return fail(FA_ERR_UNSUPPORTED, "%s: block_size must be 16, 32, 64 or 128 (got %d)", who, block_size);
+  if (B > 65535 || H_kv > 65535) return fail(FA_ERR_UNSUPPORTED, "%s: B and H_kv must be <= 65535", who);
+  if (static_cast<int64_t>(max_blocks) * block_size > (1 << 30))
+    return fail(FA_ERR_UNSUPPORTED, "%s: max_blocks * block_size too large", who);
+  if (static_cast<int64_t>(num_blocks) * H_kv > INT32_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "%s: num_blocks * H_kv too large", who);
+  if (dtype == FA_E4M3 && (!k_scale || !v_scale))
+    return fail(FA_ERR_INVALID_ARG, "%s: an E4M3 cache needs k_scale and v_scale", who);
+  if (!aligned16(k_cache) || !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(block_table) & 3u))
+    return fail(FA_ERR_INVALID_ARG, "%s: caches must be 16-byte aligned (block_table 4-byte)", who);
+  if (dtype == FA_E4M3 && (!aligned16(k_scale) || !aligned16(v_scale)))
+    return fail(FA_ERR_INVALID_ARG, "%s: k_scale and v_scale must be 16-byte aligned", who);
+  return FA_OK;
+}
+
+// Two bf16 row tensors [B, H, N, d] with strides that are multiples of 16 bytes.
+fa_status check_rows(const char* who, const int64_t* strides, int64_t* a, int64_t* b, int H, int N, int d) {
+  if (strides == nullptr) {
+    contiguous_strides(a, H, N, d);
+    contiguous_strides(b, H, N, d);
+    return FA_OK;
+  }
+  for (int i = 0; i < 6; ++i)
+    if (strides[i] < 0 || strides[i] % 8 != 0)
+      return fail(FA_ERR_INVALID_ARG, "%s: stride[%d]=%lld must be >= 0 and a multiple of 8 elements", who, i,
+                  static_cast<long long>(strides[i]));
+  memcpy(a, strides, 3 * sizeof(int64_t));
+  memcpy(b, strides + 3, 3 * sizeof(int64_t));
+  return FA_OK;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k, int N, int d,
+                  int d_rot, fa_dtype dtype, const int64_t* strides, const int32_t* positions, int64_t pos_stride_b,
+                  int position0, const double* inv_freq, float magnitude, fa_rope_layout layout, int inverse,
+                  void* stream) {
+  if (!q || !q_out || !inv_freq || (H_k > 0 && (!k || !k_out))) return fail(FA_ERR_INVALID_ARG, "fa_rope: null pointer");
+  if (B <= 0 || H_q <= 0 || H_k < 0 || N <= 0 || d <= 0 || d_rot <= 0)
+    return fail(FA_ERR_INVALID_ARG, "fa_rope: sizes must be positive (B=%d H_q=%d H_k=%d N=%d d=%d d_rot=%d)", B, H_q,
+                H_k, N, d, d_rot);
+  if (dtype != FA_BF16 && dtype != FA_FP32) return fail(FA_ERR_INVALID_ARG, "fa_rope: unknown dtype %d", dtype);
+  if (d % 2 != 0 || d > 256) return fail(FA_ERR_UNSUPPORTED, "fa_rope: head dim %d not built (even, <= 256)", d);
+  if (d_rot % 2 != 0 || d_rot > d)
+    return fail(FA_ERR_INVALID_ARG, "fa_rope: d_rot must be even and <= d (got %d of %d)", d_rot, d);
+  if (layout != FA_ROPE_HALF && layout != FA_ROPE_INTERLEAVED)
+    return fail(FA_ERR_INVALID_ARG, "fa_rope: unknown layout %d", static_cast<int>(layout));
+  if (inverse != 0 && inverse != 1) return fail(FA_ERR_INVALID_ARG, "fa_rope: inverse must be 0 or 1");
+  if (!(std::isfinite(magnitude) && magnitude > 0.f))
+    return fail(FA_ERR_INVALID_ARG, "fa_rope: magnitude must be finite and > 0");
+  if (B > 65535 || H_q > 32767 || H_k > 32767)
+    return fail(FA_ERR_UNSUPPORTED, "fa_rope: B must be <= 65535, H_q and H_k <= 32767");
+  const uintptr_t esz = dtype == FA_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(q) % esz || reinterpret_cast<uintptr_t>(k) % esz ||
+      reinterpret_cast<uintptr_t>(q_out) % esz || reinterpret_cast<uintptr_t>(k_out) % esz || misaligned4(positions))
+    return fail(FA_ERR_INVALID_ARG, "fa_rope: pointers must be aligned to their element");
+  if (positions && pos_stride_b < 0) return fail(FA_ERR_INVALID_ARG, "fa_rope: pos_stride_b must be >= 0");
+  fa::RopeParams p;
+  memset(&p, 0, sizeof(p));
+  if (strides == nullptr) {
+    contiguous_strides(p.sq, H_q, N, d);
+    contiguous_strides(p.sk, H_k, N, d);
+    contiguous_strides(p.sqo, H_q, N, d);
+    contiguous_strides(p.sko, H_k, N, d);
+  } else {
+    for (int i = 0; i < 12; ++i)
+      if (strides[i] < 0)
+        return fail(FA_ERR_INVALID_ARG, "fa_rope: stride[%d]=%lld must be >= 0", i, static_cast<long long>(strides[i]));
+    memcpy(p.sq, strides, sizeof(p.sq));
+    memcpy(p.sqo, strides + 6, sizeof(p.sqo));
+    if (H_k > 0) {
+      memcpy(p.sk, strides + 3, sizeof(p.sk));
+      memcpy(p.sko, strides + 9, sizeof(p.sko));
+    }
+  }
+  if (!rows_distinct(B, H_q, N, d, p.sqo) || (H_k > 0 && !rows_distinct(B, H_k, N, d, p.sko)))
+    return fail(FA_ERR_INVALID_ARG, "fa_rope: an output overlaps itself");
+  if ((q == q_out && memcmp(p.sq, p.sqo, sizeof(p.sq)) != 0) ||
+      (H_k > 0 && k == k_out && memcmp(p.sk, p.sko, sizeof(p.sk)) != 0))
+    return fail(FA_ERR_INVALID_ARG, "fa_rope: in place needs equal strides");
+  const bool in_place = q == q_out && (H_k == 0 || k == k_out);
+  for (int i = 0; i < d_rot / 2; ++i) {
+    if (!std::isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "fa_rope: inv_freq[%d] is not finite", i);
+    const double turns = inv_freq[i] / 6.283185307179586476925287;
+    const double part = std::ldexp(turns - std::floor(turns), 64);  // whole turns drop out: positions are whole
+    p.turns[i] = part < 18446744073709551616.0 ? static_cast<uint64_t>(part) : 0;
+  }
+  p.q = q;
+  p.k = H_k > 0 ? k : nullptr;
+  p.q_out = q_out;
+  p.k_out = H_k > 0 ? k_out : nullptr;
+  p.positions = positions;
+  p.pos_stride_b = pos_stride_b;
+  p.B = B;
+  p.Hq = H_q;
+  p.Hk = H_k;
+  p.N = N;
+  p.d = d;
+  p.rot = d_rot;
+  p.position0 = position0;
+  p.magnitude = magnitude;
+  p.sign = inverse ? -1.f : 1.f;
+  cudaError_t e = fa::launch_rope(p, dtype == FA_FP32, layout == FA_ROPE_INTERLEAVED, in_place,
+                                  static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_rope launch");
+  return check_launch("fa_rope", 1);
+}
+
+fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, uint8_t* k_scale,
+                          uint8_t* v_scale, const int32_t* block_table, const int32_t* start, const int32_t* new_lens,
+                          int B, int H_kv, int N, int num_blocks, int block_size, int max_blocks, int d,
+                          fa_dtype cache_dtype, const int64_t* strides, void* stream) {
+  const char* who = "fa_cache_append";
+  if (!k || !v || !start) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, num_blocks, block_size,
+                            max_blocks, d, cache_dtype);
+  if (r != FA_OK) return r;
+  if (N <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (!aligned16(k) || !aligned16(v) || misaligned4(start) || misaligned4(new_lens))
+    return fail(FA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned (start, new_lens 4-byte)", who);
+  fa::CacheParams p;
+  memset(&p, 0, sizeof(p));
+  if ((r = check_rows(who, strides, p.sk, p.sv, H_kv, N, d)) != FA_OK) return r;
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  p.k_rows = const_cast<void*>(k);
+  p.v_rows = const_cast<void*>(v);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.start = start;
+  p.lens = new_lens;
+  p.B = B;
+  p.Hkv = H_kv;
+  p.N = N;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  cudaError_t e = fa::launch_cache_append(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_cache_append launch");
+  return check_launch(who, 1);
+}
+
+fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                          const int32_t* block_table, const int32_t* seq_lens, void* k, void* v, int B, int H_kv,
+                          int N, int num_blocks, int block_size, int max_blocks, int d, fa_dtype cache_dtype,
+                          const int64_t* strides, void* stream) {
+  const char* who = "fa_cache_gather";
+  if (!k || !v || !seq_lens) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, num_blocks, block_size,
+                            max_blocks, d, cache_dtype);
+  if (r != FA_OK) return r;
+  if (N <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (!aligned16(k) || !aligned16(v) || misaligned4(seq_lens))
+    return fail(FA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned (seq_lens 4-byte)", who);
+  fa::CacheParams p;
+  memset(&p, 0, sizeof(p));
+  if ((r = check_rows(who, strides, p.sk, p.sv, H_kv, N, d)) != FA_OK) return r;
+  if (!rows_distinct(B, H_kv, N, d, p.sk) || !rows_distinct(B, H_kv, N, d, p.sv))
+    return fail(FA_ERR_INVALID_ARG, "%s: k or v overlaps itself", who);
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  p.k_rows = k;
+  p.v_rows = v;
+  p.k_cache = const_cast<void*>(k_cache);
+  p.v_cache = const_cast<void*>(v_cache);
+  p.k_scale = const_cast<uint8_t*>(k_scale);
+  p.v_scale = const_cast<uint8_t*>(v_scale);
+  p.block_table = block_table;
+  p.lens = seq_lens;
+  p.B = B;
+  p.Hkv = H_kv;
+  p.N = N;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  cudaError_t e = fa::launch_cache_gather(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_cache_gather launch");
+  return check_launch(who, 1);
+}
+
+int fa_decode_tree_choose_splits(int B, int H_q, int H_kv, int T, int N_kv) {
+  if (B <= 0 || H_q <= 0 || H_kv <= 0 || T <= 0 || N_kv <= 0 || H_q % H_kv != 0) return 0;
+  return std::max(1, std::min(16, (N_kv + 255) / 256));
+}
+
+size_t fa_decode_tree_workspace_size(int B, int H_q, int T, int d, int n_splits) {
+  if (B <= 0 || H_q <= 0 || T <= 0 || d <= 0 || n_splits <= 0) return 0;
+  const size_t slots = static_cast<size_t>(B) * H_q * T * n_splits;
+  return round256(slots * d * 4) + round256(slots * 2 * 4);
+}
+
+fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                         const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens,
+                         const int32_t* draft_lens, const uint8_t* tree_mask, int64_t mask_stride_b, void* o,
+                         float* lse, int B, int H_q, int H_kv, int T, int num_blocks, int block_size, int max_blocks,
+                         int d, fa_dtype cache_dtype, float scale, const int64_t* strides, int n_splits,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "fa_decode_tree";
+  if (!q || !o || !seq_lens || !workspace) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, num_blocks, block_size,
+                            max_blocks, d, cache_dtype);
+  if (r != FA_OK) return r;
+  if (H_q <= 0 || T <= 0 || n_splits <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (H_q % H_kv != 0) return fail(FA_ERR_INVALID_ARG, "%s: H_q (%d) must be a multiple of H_kv (%d)", who, H_q, H_kv);
+  if (H_q / H_kv > 128)
+    return fail(FA_ERR_UNSUPPORTED, "%s: at most 128 query heads per key/value head (got %d)", who, H_q / H_kv);
+  if (H_q > 65535) return fail(FA_ERR_UNSUPPORTED, "%s: H_q must be <= 65535", who);
+  if (T > 256) return fail(FA_ERR_UNSUPPORTED, "%s: at most 256 drafted tokens (got %d)", who, T);
+  if (n_splits > 256) return fail(FA_ERR_UNSUPPORTED, "%s: n_splits must be <= 256", who);
+  if (bad_scale(scale)) return fail(FA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || misaligned4(seq_lens) || misaligned4(draft_lens) ||
+      misaligned4(lse))
+    return fail(FA_ERR_INVALID_ARG, "%s: q, o and workspace must be 16-byte aligned (lengths, lse 4-byte)", who);
+  if (tree_mask && mask_stride_b != 0 && mask_stride_b < static_cast<int64_t>(T) * T)
+    return fail(FA_ERR_INVALID_ARG, "%s: mask_stride_b must be 0 or >= T*T", who);
+  fa::TreeParams p;
+  memset(&p, 0, sizeof(p));
+  if ((r = check_rows(who, strides, p.sq, p.so, H_q, T, d)) != FA_OK) return r;
+  if (!rows_distinct(B, H_q, T, d, p.so)) return fail(FA_ERR_INVALID_ARG, "%s: o overlaps itself", who);
+  const size_t need = fa_decode_tree_workspace_size(B, H_q, T, d, n_splits);
+  if (workspace_bytes < need)
+    return fail(FA_ERR_INVALID_ARG, "%s: workspace %zu bytes, need %zu", who, workspace_bytes, need);
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  const size_t slots = static_cast<size_t>(B) * H_q * T * n_splits;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.draft_lens = draft_lens;
+  p.mask = tree_mask;
+  p.mask_sb = mask_stride_b;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(slots * d * 4));
+  p.B = B;
+  p.Hq = H_q;
+  p.Hkv = H_kv;
+  p.G = H_q / H_kv;
+  p.T = T;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  p.n_splits = n_splits;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaError_t e = fa::launch_decode_tree(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_decode_tree launch");
+  return check_launch(who, 2);
+}
+
+}  // extern "C"
+
+extern "C" {
+
 fa_status fa_watchdog_selftest(void* stream) {
   unsigned int* word = nullptr;
   fa_status r = watchdog_ptr(&word);
@@ -950,6 +1250,13 @@ fa_status fa_device_status(void* stream) {
   if (code != 0) {
     const unsigned int zero = 0;
     cudaMemcpy(word, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if ((code >> 8) == fa::kKernTree || (code >> 8) == fa::kKernCache) {
+      const char* who = (code >> 8) == fa::kKernTree ? "decode tree" : "paged cache";
+      if ((code & 0xFFu) == fa::kSiteBadBlock)
+        return fail(FA_ERR_INVALID_ARG, "%s: a block-table entry is outside [0, num_blocks)", who);
+      if ((code & 0xFFu) == fa::kSiteBadLength)
+        return fail(FA_ERR_INVALID_ARG, "%s: a length or position is outside its range", who);
+    }
     if ((code & 0xFFu) == fa::kSiteBadBlock)
       return fail(FA_ERR_INVALID_ARG, "paged decode: a block-table entry is outside [0, num_blocks) (page 0 was read)");
     if ((code & 0xFFu) == fa::kSiteBadLength)

@@ -13,6 +13,8 @@ enum : unsigned int {
   kKernFwd = 1,
   kKernDecode = 2,
   kKernBwd = 3,
+  kKernTree = 4,
+  kKernCache = 5,
   kKernSelftest = 15,  // fa_watchdog_selftest
 };
 
@@ -105,6 +107,65 @@ struct BwdParams {
   CUtensorMap tm_dk;  // dK, dV as {d, N, H, B}, box {64, 128, 1, 1}, 128-byte swizzle (TMA stores)
   CUtensorMap tm_dv;
 };
+
+// Rotary positions of q and k (fa_rope.cu).
+struct RopeParams {
+  const void* q;
+  const void* k;        // null with Hk = 0
+  void* q_out;
+  void* k_out;
+  const int32_t* positions;  // positions[b·pos_stride_b + n], or null for n
+  int64_t pos_stride_b;
+  int64_t sq[3], sk[3], sqo[3], sko[3];  // element strides (b, h, n)
+  int B, Hq, Hk, N, d, rot;
+  int rot_cols, copy_cols, heads_per_thread;  // set by the launcher
+  int64_t position0;
+  float magnitude, sign;
+  uint64_t turns[128];  // w_i / 2π as 64-bit fractions of a turn
+};
+
+// Paged cache writes and reads (fa_cache.cu).
+struct CacheParams {
+  void* k_rows;  // [B, Hkv, N, d] bf16, read by the append and written by the gather
+  void* v_rows;
+  int64_t sk[3], sv[3];  // their element strides (b, h, n)
+  void* k_cache;  // [num_blocks, Hkv, block_size, d] bf16 or E4M3
+  void* v_cache;
+  uint8_t* k_scale;  // E4M3: [num_blocks, Hkv, block_size] E8M0 bytes
+  uint8_t* v_scale;
+  const int* block_table;  // [B, max_blocks]
+  const int* start;        // append: logical position of the first new token
+  const int* lens;         // append: new tokens (null: N each); gather: sequence lengths
+  int B, Hkv, N, num_blocks, block_size, max_blocks;
+  unsigned int* err;
+};
+
+// Attention of drafted tokens over a paged cache (fa_tree.cu).
+struct TreeParams {
+  const void* q;  // bf16, element strides sq (b, h, t)
+  void* o;        // bf16, so
+  float* lse;     // [B, Hq, T] or null
+  int64_t sq[3], so[3];
+  const void* k_cache;  // [num_blocks, Hkv, block_size, d] bf16 or E4M3
+  const void* v_cache;
+  const uint8_t* k_scale;  // E4M3: [num_blocks, Hkv, block_size] E8M0 bytes
+  const uint8_t* v_scale;
+  const int* block_table;  // [B, max_blocks]
+  const int* seq_lens;     // [B] keys, the drafted ones included
+  const int* draft_lens;   // [B] or null (T each)
+  const uint8_t* mask;     // mask[b·mask_sb + t·T + u], or null: u <= t
+  int64_t mask_sb;
+  float* part_o;   // [B·Hq·T, n_splits, d] fp32
+  float* part_ml;  // [B·Hq·T, n_splits, 2] fp32: (m in log2 units, ℓ)
+  int B, Hq, Hkv, G, T, num_blocks, block_size, max_blocks, n_splits;
+  float scale_log2;
+  unsigned int* err;
+};
+
+cudaError_t launch_rope(const RopeParams& p, bool fp32, bool inter, bool in_place, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheParams& p, int d, bool fp8, cudaStream_t s);
+cudaError_t launch_cache_gather(const CacheParams& p, int d, bool fp8, cudaStream_t s);
+cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s);
 
 cudaError_t launch_fwd_bf16(int d, const FwdParams& p, cudaStream_t s);
 // Unmasked bf16 forward at d = 64 with 3 or 4 query tiles of 128 rows per CTA

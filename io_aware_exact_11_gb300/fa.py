@@ -9,17 +9,21 @@ there is no fallback path.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 import threading
 
+import numpy as np
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfa.so")
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_DEVICE_TIMEOUT = range(5)
-FA_BF16, FA_FP32 = 0, 1
+FA_BF16, FA_FP32, FA_E4M3 = 0, 1, 2
 FA_MASK_NONE, FA_MASK_CAUSAL = 0, 1
+FA_ROPE_HALF, FA_ROPE_INTERLEAVED = 0, 1
 
 EXPORTED = (
     "fa_abi_version",
@@ -37,6 +41,12 @@ EXPORTED = (
     "fa_backward_workspace_size",
     "fa_backward",
     "fa_backward_masked",
+    "fa_rope",
+    "fa_cache_append",
+    "fa_cache_gather",
+    "fa_decode_tree_choose_splits",
+    "fa_decode_tree_workspace_size",
+    "fa_decode_tree",
     "fa_device_status",
     "fa_watchdog_selftest",
     "fa_status_string",
@@ -90,6 +100,18 @@ def lib() -> ctypes.CDLL:
         L.fa_backward.restype = i32
         L.fa_backward_masked.argtypes = [vp] * 9 + [i32, i32, i32, i32, i32, f32, vp, sz, i32, vp]
         L.fa_backward_masked.restype = i32
+        L.fa_rope.argtypes = [vp] * 4 + [i32] * 7 + [vp, vp, ctypes.c_int64, i32, vp, f32, i32, i32, vp]
+        L.fa_rope.restype = i32
+        L.fa_cache_append.argtypes = [vp] * 9 + [i32] * 8 + [vp, vp]
+        L.fa_cache_append.restype = i32
+        L.fa_cache_gather.argtypes = [vp] * 8 + [i32] * 8 + [vp, vp]
+        L.fa_cache_gather.restype = i32
+        L.fa_decode_tree_choose_splits.argtypes = [i32] * 5
+        L.fa_decode_tree_choose_splits.restype = i32
+        L.fa_decode_tree_workspace_size.argtypes = [i32] * 5
+        L.fa_decode_tree_workspace_size.restype = sz
+        L.fa_decode_tree.argtypes = [vp] * 9 + [ctypes.c_int64, vp, vp] + [i32] * 9 + [f32, vp, i32, vp, sz, vp]
+        L.fa_decode_tree.restype = i32
         L.fa_device_status.argtypes = [vp]
         L.fa_device_status.restype = i32
         L.fa_watchdog_selftest.argtypes = [vp]
@@ -457,3 +479,301 @@ def backward(q, k, v, o, lse, do, scale: float | None = None, dq=None, dk=None, 
     else:
         _check(lib().fa_backward(*args, _stream_ptr(stream)))
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- rotary positions, paged cache, drafted tokens
+#
+# These calls run on the tensors' own device.  Without ``stream`` they use that
+# device's current stream; with one, what they allocate belongs to that stream.
+
+
+def _device_of(*ts):
+    """The one CUDA device of the given tensors (None entries are skipped)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must live on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("all tensors must live on the same CUDA device")
+    return dev
+
+
+def _on(dev, stream):
+    """Context in which ``dev`` is current, and ``stream`` where one is given."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _strides(*ts):
+    """Element strides of all but the last dimension (which must be contiguous), or None if all are contiguous."""
+    if all(t.is_contiguous() for t in ts):
+        return None
+    for t in ts:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError("the head dim must be contiguous")
+    st = [x for t in ts for x in t.stride()[:-1]]
+    return (ctypes.c_int64 * len(st))(*st)
+
+
+def _check_out(name, t, shape, dtype, dev):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: int = 4096, low_turns: float = 1.0, high_turns: float = 32.0):
+    """Inverse frequencies for ``rope`` (float64 array of rot_dim/2) and the magnitude that goes with them.
+
+    w_i = base^(−2i/rot_dim), stretched for contexts ``factor`` times as long:
+      * ``"linear"``: every w_i divided by factor (positions interpolated);
+      * ``"base"``: base multiplied by factor^(rot_dim/(rot_dim − 2)), which leaves the fastest pair alone and
+        divides the slowest by factor;
+      * ``"ramp"``: pairs that make at least ``high_turns`` turns over ``original_len`` positions are left alone,
+        those with at most ``low_turns`` divided by factor, a straight line between; magnitude 0.1·ln(factor) + 1.
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not (math.isfinite(base) and base > 0 and math.isfinite(factor) and factor >= 1):
+        raise ValueError("base must be > 0 and factor >= 1")
+    if scaling not in ("none", "linear", "base", "ramp"):
+        raise ValueError(f"unknown scaling {scaling!r} (none, linear, base, ramp)")
+    i = np.arange(rot_dim // 2, dtype=np.float64)
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("scaling 'base' needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    w = base ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        return w / factor, 1.0
+    if scaling == "ramp":
+        if not (original_len > 0 and 0 <= low_turns < high_turns):
+            raise ValueError("ramp needs original_len > 0 and 0 <= low_turns < high_turns")
+        keep = np.clip((original_len * w / (2 * math.pi) - low_turns) / (high_turns - low_turns), 0.0, 1.0)
+        return w * keep + w / factor * (1.0 - keep), 0.1 * math.log(factor) + 1.0
+    return w, 1.0
+
+
+def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, stream, inverse):
+    torch = _torch()
+    dev = _device_of(q, k, positions, out_q, out_k)
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
+        raise ValueError("q must be [B, Hq, N, d] and k [B, Hk, N, d]")
+    B, Hq, N, d = q.shape
+    dtype = _dtype_code(q)
+    if k is not None and k.dtype != q.dtype:
+        raise TypeError("q and k must share a dtype")
+    if k is None and out_k is not None:
+        raise ValueError("out_k without k")
+    w = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if w.ndim != 1:
+        raise ValueError("inv_freq must be one row of rot_dim/2 values")
+    pos_sb = 0
+    if positions is not None:
+        if positions.dtype != torch.int32:
+            raise TypeError("positions must be int32")
+        if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be [N] or [B, N] with the last dim contiguous")
+        pos_sb = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    with _on(dev, stream):
+        if out_q is None:
+            out_q = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
+        else:
+            _check_out("out_q", out_q, q.shape, q.dtype, dev)
+        ts = (q, q, out_q, out_q)
+        if k is not None:
+            if out_k is None:
+                out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            else:
+                _check_out("out_k", out_k, k.shape, q.dtype, dev)
+            ts = (q, k, out_q, out_k)
+        st = _strides(*ts)
+        _check(lib().fa_rope(q.data_ptr(), _addr(k), out_q.data_ptr(), _addr(out_k), B, Hq,
+                             k.shape[1] if k is not None else 0, N, d, 2 * w.shape[0], dtype, st, _addr(positions),
+                             pos_sb, int(position0), w.ctypes.data, float(magnitude),
+                             FA_ROPE_INTERLEAVED if interleaved else FA_ROPE_HALF, inverse, _stream_ptr()))
+    return out_q, out_k
+
+
+def rope(q, k, inv_freq, positions=None, position0: int = 0, magnitude: float = 1.0, interleaved: bool = False,
+         out_q=None, out_k=None, stream=None):
+    """Rotary positions of q [B,Hq,N,d] and k [B,Hk,N,d] (k may be None), bf16 or fp32; returns (q', k').
+
+    Pair i of the first 2·len(inv_freq) elements turns by position·inv_freq[i] and is multiplied by ``magnitude``;
+    pairs are (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  ``positions`` is int32 [N] or [B, N] on the
+    device (None: 0 … N − 1), ``position0`` is added to it.  Strided inputs and outputs are taken as they are (the
+    head dim contiguous); ``out_q=q, out_k=k`` works in place.
+    """
+    return _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, stream, 0)
+
+
+def rope_backward(dq, dk, inv_freq, positions=None, position0: int = 0, magnitude: float = 1.0,
+                  interleaved: bool = False, out_q=None, out_k=None, stream=None):
+    """Gradients of ``rope``'s inputs from those of its outputs; same arguments as the forward call."""
+    return _rope(dq, dk, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, stream, 1)
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table):
+    """Checks a paged cache; returns (num_blocks, Hkv, block_size, d, dtype code)."""
+    torch = _torch()
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d]")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must share a dtype")
+    if k_cache.dtype == torch.bfloat16:
+        code = FA_BF16
+    elif k_cache.dtype in (torch.float8_e4m3fn, torch.uint8):
+        code = FA_E4M3
+        for s in (k_scale, v_scale):
+            if s is None or s.dtype != torch.uint8 or s.shape != k_cache.shape[:3]:
+                raise ValueError("an E4M3 cache needs uint8 k_scale and v_scale [num_blocks, Hkv, block_size]")
+    else:
+        raise TypeError(f"unsupported cache dtype {k_cache.dtype} (bfloat16, float8_e4m3fn or uint8 codes)")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise TypeError("block_table must be int32 [B, max_blocks]")
+    for t in (k_cache, v_cache, block_table) + ((k_scale, v_scale) if code == FA_E4M3 else ()):
+        if not t.is_contiguous():
+            raise ValueError("caches, scales and block_table must be contiguous")
+    nb, hkv, bs, d = k_cache.shape
+    return nb, hkv, bs, d, code
+
+
+def _check_lens(name, t, B):
+    torch = _torch()
+    if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous int32 [{B}]")
+
+
+def cache_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, k_scale=None, v_scale=None, stream=None):
+    """Write new keys and values k, v (bf16 [B,Hkv,N,d], strided or not) into a paged cache, in place.
+
+    Token n of sequence b goes to logical position start[b] + n (start: int32 [B]); with ``new_lens`` (int32 [B]) only
+    the first new_lens[b] are written.  k_cache/v_cache [num_blocks, Hkv, block_size, d]: bfloat16 takes the rows as
+    they are; float8_e4m3fn (or uint8 codes) quantises each row with the power of two whose E8M0 byte goes to
+    k_scale/v_scale (uint8 [num_blocks, Hkv, block_size]).
+    """
+    torch = _torch()
+    dev = _device_of(k, v, k_cache, v_cache, block_table, start, new_lens, k_scale, v_scale)
+    nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    B = block_table.shape[0]
+    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or k.shape[1] != hkv or k.shape[3] != d:
+        raise ValueError(f"k and v must be [{B}, {hkv}, N, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("k and v must be bfloat16")
+    _check_lens("start", start, B)
+    if new_lens is not None:
+        _check_lens("new_lens", new_lens, B)
+    with _on(dev, stream):
+        _check(lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                     _addr(k_scale), _addr(v_scale), block_table.data_ptr(), start.data_ptr(),
+                                     _addr(new_lens), B, hkv, k.shape[2], nb, bs, block_table.shape[1], d, code,
+                                     _strides(k, v), _stream_ptr()))
+
+
+def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, v_scale=None, out_k=None, out_v=None,
+                 stream=None):
+    """The first n keys and values of every sequence as bf16 [B,Hkv,n,d]; rows past seq_lens[b] are zero."""
+    torch = _torch()
+    dev = _device_of(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out_k, out_v)
+    nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    B = block_table.shape[0]
+    _check_lens("seq_lens", seq_lens, B)
+    n = int(n)
+    if n < 1:
+        raise ValueError("n must be at least 1")
+    with _on(dev, stream):
+        shape = (B, hkv, n, d)
+        if out_k is None:
+            out_k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if out_v is None:
+            out_v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        _check_out("out_k", out_k, shape, torch.bfloat16, dev)
+        _check_out("out_v", out_v, shape, torch.bfloat16, dev)
+        _check(lib().fa_cache_gather(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                     block_table.data_ptr(), seq_lens.data_ptr(), out_k.data_ptr(), out_v.data_ptr(),
+                                     B, hkv, n, nb, bs, block_table.shape[1], d, code, _strides(out_k, out_v),
+                                     _stream_ptr()))
+    return out_k, out_v
+
+
+def decode_tree_workspace_size(B: int, Hq: int, T: int, d: int, n_splits: int) -> int:
+    return int(lib().fa_decode_tree_workspace_size(B, Hq, T, d, n_splits))
+
+
+def decode_tree_choose_splits(B: int, Hq: int, Hkv: int, T: int, Nkv: int) -> int:
+    """The library's split count for ``decode_tree`` over sequences of up to Nkv keys."""
+    s = int(lib().fa_decode_tree_choose_splits(B, Hq, Hkv, T, Nkv))
+    if s <= 0:
+        raise FAError(FA_ERR_INVALID_ARG, f"no split count for B={B} Hq={Hq} Hkv={Hkv} T={T} Nkv={Nkv}")
+    return s
+
+
+def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draft_lens=None, k_scale=None,
+                v_scale=None, n_splits: int | None = None, scale: float | None = None, out=None, lse=None,
+                workspace=None, stream=None):
+    """Attention of T drafted tokens per sequence over a paged cache (T = 1: plain decode); returns (O, LSE).
+
+    q [B,Hq,T,d] bf16 (strided or not).  The drafted tokens' keys are in the cache: seq_lens[b] counts them, and the
+    last draft_lens[b] (int32 [B]; None: T) keys of sequence b are theirs.  Token t sees the context before them and
+    drafted key u where tree_mask[b, t, u] (bool or uint8 [B,T,T] or [T,T]; None: u <= t).  Rows that see nothing,
+    padding rows t >= draft_lens[b] among them, give O = 0 and LSE = −inf.  The cache is bfloat16, or float8_e4m3fn
+    with k_scale/v_scale as ``cache_append`` writes it.  O like q (contiguous), LSE fp32 [B,Hq,T].
+    """
+    torch = _torch()
+    dev = _device_of(q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, k_scale, v_scale, out, lse,
+                     workspace)
+    nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    if q.dim() != 4 or q.shape[0] != block_table.shape[0] or q.shape[3] != d:
+        raise ValueError(f"q must be [{block_table.shape[0]}, Hq, T, {d}], got {tuple(q.shape)}")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    B, Hq, T, _ = q.shape
+    _check_lens("seq_lens", seq_lens, B)
+    if draft_lens is not None:
+        _check_lens("draft_lens", draft_lens, B)
+    mask_sb = 0
+    if tree_mask is not None:
+        if tree_mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("tree_mask must be bool or uint8")
+        if tuple(tree_mask.shape) not in ((T, T), (B, T, T)) or (T > 1 and tree_mask.stride()[-2:] != (T, 1)):
+            raise ValueError("tree_mask must be [T, T] or [B, T, T] with contiguous rows")
+        mask_sb = tree_mask.stride(0) if tree_mask.dim() == 3 and B > 1 else 0
+    if n_splits is None:
+        n_splits = decode_tree_choose_splits(B, Hq, hkv, T, block_table.shape[1] * bs)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_out("out", out, q.shape, torch.bfloat16, dev)
+        if lse is None:
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        else:
+            _check_out("lse", lse, (B, Hq, T), torch.float32, dev)
+            if not lse.is_contiguous():
+                raise ValueError("lse must be contiguous")
+        if workspace is None:
+            workspace = torch.empty(max(decode_tree_workspace_size(B, Hq, T, d, n_splits), 16), dtype=torch.uint8,
+                                    device=dev)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        _check(lib().fa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
+                                    _addr(v_scale), block_table.data_ptr(), seq_lens.data_ptr(), _addr(draft_lens),
+                                    _addr(tree_mask), mask_sb, out.data_ptr(), lse.data_ptr(), B, Hq, hkv, T, nb, bs,
+                                    block_table.shape[1], d, code, float(scale), _strides(q, out), int(n_splits),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr()))
+    return out, lse
