@@ -58,8 +58,9 @@ namespace {
 thread_local char g_last_error[512] = "";
 std::atomic<uint64_t> g_launches{0};
 
-// One watchdog word per device: kernels write the site of a wait that gave up.
-__device__ unsigned int g_watchdog_word;
+// Two words per device: kernels write the site of a wait that gave up to the
+// first, and device-side argument checks that concern no wait to the second.
+__device__ unsigned int g_watchdog_word[2];
 
 fa_status fail(fa_status s, const char* fmt, ...) {
   va_list ap;
@@ -138,17 +139,18 @@ fa_status make_map(CUtensorMap* tm, const void* base, int B, int H, int N, int d
   EncodeTiledFn enc;
   fa_status s = get_encoder(&enc);
   if (s != FA_OK) return s;
+  const bool narrow = fp8 && d == 64;  // E4M3 heads of 64: 64-byte rows and swizzle
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(B)};
   // One box row is 128 bytes (the swizzle width): 64 bf16 or 128 E4M3 values.
   const int esz = fp8 ? 1 : 2;
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(sn) * esz, static_cast<cuuint64_t>(sh) * esz,
                            static_cast<cuuint64_t>(sb) * esz};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / esz), static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>((narrow ? 64 : 128) / esz), static_cast<cuuint32_t>(box_rows), 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(tm, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                   const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(FA_ERR_INVALID_ARG, "cuTensorMapEncodeTiled(%s) failed with %d", name, (int)r);
   return FA_OK;
@@ -1155,7 +1157,29 @@ fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_
 
 int fa_decode_tree_choose_splits(int B, int H_q, int H_kv, int T, int N_kv) {
   if (B <= 0 || H_q <= 0 || H_kv <= 0 || T <= 0 || N_kv <= 0 || H_q % H_kv != 0) return 0;
-  return std::max(1, std::min(16, (N_kv + 255) / 256));
+  int sms = 152, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms = 152;
+  cudaGetLastError();  // a failed query on a machine without a device is not an error here
+  const int64_t rows = static_cast<int64_t>(T) * (H_q / H_kv);
+  const int64_t tile = fa::tree_tile_rows(rows);
+  const int64_t units = static_cast<int64_t>(B) * H_kv * ((rows + tile - 1) / tile);
+  // One CTA runs on an SM at a time.  A split count costs its waves of CTAs times
+  // the longest chunk's 128-key tiles plus what a CTA costs besides (about eight
+  // tiles' time), and the joining of the chunks; the cheapest one is taken.
+  const int64_t tiles = (static_cast<int64_t>(N_kv) + 127) / 128;
+  int best = 1;
+  double best_cost = 0;
+  for (int s = 1; s <= 256 && s <= tiles; ++s) {
+    const int64_t waves = (units * s + sms - 1) / sms;
+    const double cost = static_cast<double>(waves) * (static_cast<double>((tiles + s - 1) / s) + 8) + (s > 1 ? 6 : 0) + 0.02 * s;
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
 }
 
 size_t fa_decode_tree_workspace_size(int B, int H_q, int T, int d, int n_splits) {
@@ -1221,9 +1245,25 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   p.max_blocks = max_blocks;
   p.n_splits = n_splits;
   p.scale_log2 = scale * 1.4426950408889634f;
+  const int64_t rows = static_cast<int64_t>(T) * p.G;
+  p.tile_rows = fa::tree_tile_rows(rows);
+  p.row_tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
+  if (cache_dtype == FA_BF16 && d == 128) {  // one box per page of one head
+    if ((r = make_page_map5(&p.tm_k, k_cache, num_blocks, H_kv, block_size, "k_cache")) != FA_OK) return r;
+    if ((r = make_page_map5(&p.tm_v, v_cache, num_blocks, H_kv, block_size, "v_cache")) != FA_OK) return r;
+  } else {
+    const int64_t page = static_cast<int64_t>(block_size) * d;
+    const bool fp8 = cache_dtype == FA_E4M3;
+    if ((r = make_map(&p.tm_k, k_cache, num_blocks, H_kv, block_size, d, H_kv * page, page, d, "k_cache", block_size,
+                      fp8)) != FA_OK)
+      return r;
+    if ((r = make_map(&p.tm_v, v_cache, num_blocks, H_kv, block_size, d, H_kv * page, page, d, "v_cache", block_size,
+                      fp8)) != FA_OK)
+      return r;
+  }
   cudaError_t e = fa::launch_decode_tree(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_decode_tree launch");
-  return check_launch(who, 2);
+  return check_launch(who, n_splits == 1 ? 1 : 2);
 }
 
 }  // extern "C"
@@ -1244,19 +1284,21 @@ fa_status fa_device_status(void* stream) {
   unsigned int* word = nullptr;
   fa_status r = watchdog_ptr(&word);
   if (r != FA_OK) return r;
-  unsigned int code = 0;
-  e = cudaMemcpy(&code, word, sizeof(code), cudaMemcpyDeviceToHost);
+  unsigned int codes[2] = {0, 0};
+  e = cudaMemcpy(codes, word, sizeof(codes), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "fa_device_status: read watchdog");
+  if (codes[0] != 0 || codes[1] != 0) {
+    const unsigned int zero[2] = {0, 0};
+    cudaMemcpy(word, zero, sizeof(zero), cudaMemcpyHostToDevice);
+  }
+  if (codes[0] == 0 && codes[1] != 0) {
+    const char* who = (codes[1] >> 8) == fa::kKernTree ? "decode tree" : "paged cache";
+    if ((codes[1] & 0xFFu) == fa::kSiteBadBlock)
+      return fail(FA_ERR_INVALID_ARG, "%s: a block-table entry is outside [0, num_blocks)", who);
+    return fail(FA_ERR_INVALID_ARG, "%s: a length or position is outside its range", who);
+  }
+  const unsigned int code = codes[0];
   if (code != 0) {
-    const unsigned int zero = 0;
-    cudaMemcpy(word, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-    if ((code >> 8) == fa::kKernTree || (code >> 8) == fa::kKernCache) {
-      const char* who = (code >> 8) == fa::kKernTree ? "decode tree" : "paged cache";
-      if ((code & 0xFFu) == fa::kSiteBadBlock)
-        return fail(FA_ERR_INVALID_ARG, "%s: a block-table entry is outside [0, num_blocks)", who);
-      if ((code & 0xFFu) == fa::kSiteBadLength)
-        return fail(FA_ERR_INVALID_ARG, "%s: a length or position is outside its range", who);
-    }
     if ((code & 0xFFu) == fa::kSiteBadBlock)
       return fail(FA_ERR_INVALID_ARG, "paged decode: a block-table entry is outside [0, num_blocks) (page 0 was read)");
     if ((code & 0xFFu) == fa::kSiteBadLength)

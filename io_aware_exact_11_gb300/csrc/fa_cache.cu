@@ -13,7 +13,7 @@
 // Bound: device memory.  Writing: 2·(2d) bytes read and 2·(d + 1) written per
 // token and head (bf16: 2·2d); d/8 lanes hold one row, 16 bytes of it each, and
 // the row maximum is log2(d/8) lane exchanges, so a row never leaves registers.
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "fa_kernels.h"
 #include "sm103.cuh"
@@ -24,7 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ void report(unsigned int* err, unsigned int what) {
-  atomicCAS(err, 0u, (kKernCache << 8) | what);
+  atomicCAS(err + 1, 0u, (kKernCache << 8) | what);
 }
 
 // The page of logical key t, or −1 (and a report) if the table's entry is no page.
@@ -33,13 +33,6 @@ __device__ __forceinline__ int page_of(const CacheParams& p, int b, int t) {
   if (blk >= 0 && blk < p.num_blocks) return blk;
   report(p.err, kSiteBadBlock);
   return -1;
-}
-
-// Two fp32 values as E4M3 codes, round to nearest even; the low byte holds `lo`.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // Writes 8 elements of a row; the lanes of the row (8 or 16 neighbours) hold the rest of it.
@@ -134,8 +127,7 @@ __device__ __forceinline__ uint4 dequantise8(uint2 c, uint32_t s) {
   const float f = s == 0 ? 5.877471754111438e-39f : __uint_as_float(s << 23);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))),
-                                                     __NV_E4M3);
+    const uint32_t h = e4m3x2_to_f16x2(w[i >> 1] >> (16 * (i & 1)));
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
     out[i] = pack_bf16x2(v.x * f, v.y * f);
   }

@@ -65,7 +65,10 @@ struct DecodeParams {
   int d = 128;  // head dim: 64 or 128
 };
 
-// Device-side argument checks report through the status word with these sites.
+// Device-side argument checks report with these sites: the decode kernels in the
+// watchdog word, the paged cache's and drafted tokens' ones in the word after it,
+// which no pipeline wait looks at (a bad page of one sequence leaves the others'
+// results, and other kernels, alone).
 enum : unsigned int { kSiteBadBlock = 0xE1, kSiteBadLength = 0xE2 };
 
 // Grouped-query split-KV decode on tensor cores (fa_decode_tc.cu).
@@ -142,6 +145,8 @@ struct CacheParams {
 
 // Attention of drafted tokens over a paged cache (fa_tree.cu).
 struct TreeParams {
+  CUtensorMap tm_k;  // pages of one head, as for DecodeTcParams; E4M3: {d bytes, bs, Hkv, num_blocks}, box {d, bs, 1, 1}
+  CUtensorMap tm_v;
   const void* q;  // bf16, element strides sq (b, h, t)
   void* o;        // bf16, so
   float* lse;     // [B, Hq, T] or null
@@ -158,6 +163,7 @@ struct TreeParams {
   float* part_o;   // [B·Hq·T, n_splits, d] fp32
   float* part_ml;  // [B·Hq·T, n_splits, 2] fp32: (m in log2 units, ℓ)
   int B, Hq, Hkv, G, T, num_blocks, block_size, max_blocks, n_splits;
+  int tile_rows, row_tiles;  // rows of one CTA (16, 32 or 64) and tiles of the T·G rows of a key/value head
   float scale_log2;
   unsigned int* err;
 };
@@ -165,6 +171,7 @@ struct TreeParams {
 cudaError_t launch_rope(const RopeParams& p, bool fp32, bool inter, bool in_place, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheParams& p, int d, bool fp8, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheParams& p, int d, bool fp8, cudaStream_t s);
+int tree_tile_rows(int64_t rows);
 cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s);
 
 cudaError_t launch_fwd_bf16(int d, const FwdParams& p, cudaStream_t s);
