@@ -367,13 +367,13 @@ FA_API fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const
                                  int d, fa_dtype cache_dtype, const int64_t* strides, void* stream);
 
 /*
- * fa_decode_tree_choose_splits — the split count the library would take for
- *   fa_decode_tree with sequences of up to N_kv keys on the current device
- *   (0 for bad arguments).  fa_decode_tree_workspace_size — bytes of workspace
- *   for a split count (0 for bad arguments).
+ * fa_decode_tree_workspace_size — bytes of workspace with which fa_decode_tree
+ *   cuts its work into as many parts as the current device has room for, or
+ *   into at most max_parts (0: no limit); 0 for bad arguments.  The call takes a
+ *   smaller workspace too, down to B·H_kv·8 bytes (rounded up to a multiple of
+ *   256), and cuts its work into fewer parts then.
  */
-FA_API int fa_decode_tree_choose_splits(int B, int H_q, int H_kv, int T, int N_kv);
-FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int T, int d, int n_splits);
+FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int d, int max_parts);
 
 /*
  * fa_decode_tree — attention of T drafted tokens per sequence over a paged
@@ -394,17 +394,22 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int T, int d, int n_
  *   and bad page ids are caught on the device (the sequence counts as empty,
  *   page 0 is read) and reported by fa_device_status as FA_ERR_INVALID_ARG;
  *   seq_lens[b] = 0 without draft_lens is an unused batch slot, not an error.
+ *   The 128-key tiles of all sequences and heads are cut into equal parts, one
+ *   per CTA (at most max_parts; 0: the library's choice), and the pieces of a
+ *   sequence that is cut are joined by a second kernel.  Where the cuts fall
+ *   depends on the lengths of the whole batch, so a sequence's results may
+ *   differ in their last bits with the batch around it; equal calls give equal bits.
  *   workspace: fa_decode_tree_workspace_size() bytes, 16-byte aligned, contents
  *   on entry do not matter.
  *   Supported: d = 64 or 128, block_size ∈ {16, 32, 64, 128}, H_q = G·H_kv with
- *   G <= 128, T <= 256, 1 <= n_splits <= 256.
+ *   G <= 128, T <= 256, max_parts <= 4096.
  */
 FA_API fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                                 const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens,
                                 const int32_t* draft_lens, const uint8_t* tree_mask, int64_t mask_stride_b, void* o,
                                 float* lse, int B, int H_q, int H_kv, int T, int num_blocks, int block_size,
                                 int max_blocks, int d, fa_dtype cache_dtype, float scale, const int64_t* strides,
-                                int n_splits, void* workspace, size_t workspace_bytes, void* stream);
+                                int max_parts, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * fa_device_status — synchronises `stream`, then reports FA_ERR_DEVICE_TIMEOUT

@@ -1001,6 +1001,34 @@ fa_status check_rows(const char* who, const int64_t* strides, int64_t* a, int64_
   return FA_OK;
 }
 
+// Layout of fa_decode_tree's workspace for a number of parts.
+struct TreeWorkspace {
+  bool by_pair;  // which of the two slot numberings is the shorter one
+  size_t part_o, part_ml, bytes;
+};
+TreeWorkspace tree_workspace(int B, int H_kv, int64_t rows, int d, int64_t parts) {
+  const int64_t pairs = static_cast<int64_t>(B) * H_kv;
+  TreeWorkspace w;
+  w.by_pair = pairs + parts - 1 < 2 * parts;
+  const size_t slots = parts == 1 ? 0 : static_cast<size_t>(w.by_pair ? pairs + parts - 1 : 2 * parts);
+  w.part_o = round256(static_cast<size_t>(pairs) * 8);
+  w.part_ml = w.part_o + round256(slots * rows * d * 4);
+  w.bytes = w.part_ml + round256(slots * rows * 2 * 4);
+  return w;
+}
+
+// Parts of fa_decode_tree's work: one CTA per SM and row tile, at least two key tiles each.
+int64_t tree_parts(int64_t rows, int max_parts, int64_t tiles) {
+  int sms = 152, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms = 152;
+  cudaGetLastError();  // a failed query on a machine without a device is not an error here
+  const int64_t row_tiles = (rows + fa::tree_cta_rows(rows) - 1) / fa::tree_cta_rows(rows);
+  int64_t parts = std::max<int64_t>(1, max_parts > 0 ? max_parts : sms / row_tiles);
+  return std::min(parts, tiles / 2 + 1);
+}
+
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 }  // namespace
@@ -1155,57 +1183,31 @@ fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_
   return check_launch(who, 1);
 }
 
-int fa_decode_tree_choose_splits(int B, int H_q, int H_kv, int T, int N_kv) {
-  if (B <= 0 || H_q <= 0 || H_kv <= 0 || T <= 0 || N_kv <= 0 || H_q % H_kv != 0) return 0;
-  int sms = 152, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    sms = 152;
-  cudaGetLastError();  // a failed query on a machine without a device is not an error here
+size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int d, int max_parts) {
+  if (B <= 0 || H_q <= 0 || H_kv <= 0 || T <= 0 || d <= 0 || max_parts < 0 || H_q % H_kv != 0) return 0;
   const int64_t rows = static_cast<int64_t>(T) * (H_q / H_kv);
-  const int64_t tile = fa::tree_tile_rows(rows);
-  const int64_t units = static_cast<int64_t>(B) * H_kv * ((rows + tile - 1) / tile);
-  // One CTA runs on an SM at a time.  A split count costs its waves of CTAs times
-  // the longest chunk's 128-key tiles plus what a CTA costs besides (about eight
-  // tiles' time), and the joining of the chunks; the cheapest one is taken.
-  const int64_t tiles = (static_cast<int64_t>(N_kv) + 127) / 128;
-  int best = 1;
-  double best_cost = 0;
-  for (int s = 1; s <= 256 && s <= tiles; ++s) {
-    const int64_t waves = (units * s + sms - 1) / sms;
-    const double cost = static_cast<double>(waves) * (static_cast<double>((tiles + s - 1) / s) + 8) + (s > 1 ? 6 : 0) + 0.02 * s;
-    if (s == 1 || cost < best_cost) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return best;
-}
-
-size_t fa_decode_tree_workspace_size(int B, int H_q, int T, int d, int n_splits) {
-  if (B <= 0 || H_q <= 0 || T <= 0 || d <= 0 || n_splits <= 0) return 0;
-  const size_t slots = static_cast<size_t>(B) * H_q * T * n_splits;
-  return round256(slots * d * 4) + round256(slots * 2 * 4);
+  return tree_workspace(B, H_kv, rows, d, tree_parts(rows, max_parts, INT64_MAX)).bytes;
 }
 
 fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                          const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens,
                          const int32_t* draft_lens, const uint8_t* tree_mask, int64_t mask_stride_b, void* o,
                          float* lse, int B, int H_q, int H_kv, int T, int num_blocks, int block_size, int max_blocks,
-                         int d, fa_dtype cache_dtype, float scale, const int64_t* strides, int n_splits,
+                         int d, fa_dtype cache_dtype, float scale, const int64_t* strides, int max_parts,
                          void* workspace, size_t workspace_bytes, void* stream) {
   const char* who = "fa_decode_tree";
   if (!q || !o || !seq_lens || !workspace) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
   fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, num_blocks, block_size,
                             max_blocks, d, cache_dtype);
   if (r != FA_OK) return r;
-  if (H_q <= 0 || T <= 0 || n_splits <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (H_q <= 0 || T <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (max_parts < 0) return fail(FA_ERR_INVALID_ARG, "%s: max_parts must be >= 0", who);
   if (H_q % H_kv != 0) return fail(FA_ERR_INVALID_ARG, "%s: H_q (%d) must be a multiple of H_kv (%d)", who, H_q, H_kv);
   if (H_q / H_kv > 128)
     return fail(FA_ERR_UNSUPPORTED, "%s: at most 128 query heads per key/value head (got %d)", who, H_q / H_kv);
   if (H_q > 65535) return fail(FA_ERR_UNSUPPORTED, "%s: H_q must be <= 65535", who);
   if (T > 256) return fail(FA_ERR_UNSUPPORTED, "%s: at most 256 drafted tokens (got %d)", who, T);
-  if (n_splits > 256) return fail(FA_ERR_UNSUPPORTED, "%s: n_splits must be <= 256", who);
+  if (max_parts > 4096) return fail(FA_ERR_UNSUPPORTED, "%s: max_parts must be <= 4096", who);
   if (bad_scale(scale)) return fail(FA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
   if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || misaligned4(seq_lens) || misaligned4(draft_lens) ||
       misaligned4(lse))
@@ -1216,11 +1218,15 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   memset(&p, 0, sizeof(p));
   if ((r = check_rows(who, strides, p.sq, p.so, H_q, T, d)) != FA_OK) return r;
   if (!rows_distinct(B, H_q, T, d, p.so)) return fail(FA_ERR_INVALID_ARG, "%s: o overlaps itself", who);
-  const size_t need = fa_decode_tree_workspace_size(B, H_q, T, d, n_splits);
-  if (workspace_bytes < need)
-    return fail(FA_ERR_INVALID_ARG, "%s: workspace %zu bytes, need %zu", who, workspace_bytes, need);
+  // A smaller workspace is taken with fewer parts; one part needs no room for pieces.
+  const int64_t rows = static_cast<int64_t>(T) * (H_q / H_kv);
+  const int64_t tiles = static_cast<int64_t>(B) * H_kv * ((static_cast<int64_t>(max_blocks) * block_size + 127) / 128);
+  int64_t parts = tree_parts(rows, max_parts, tiles);
+  while (parts > 1 && tree_workspace(B, H_kv, rows, d, parts).bytes > workspace_bytes) --parts;
+  const TreeWorkspace ws = tree_workspace(B, H_kv, rows, d, parts);
+  if (workspace_bytes < ws.bytes)
+    return fail(FA_ERR_INVALID_ARG, "%s: workspace %zu bytes, need at least %zu", who, workspace_bytes, ws.bytes);
   if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
-  const size_t slots = static_cast<size_t>(B) * H_q * T * n_splits;
   p.q = q;
   p.o = o;
   p.lse = lse;
@@ -1233,8 +1239,12 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   p.draft_lens = draft_lens;
   p.mask = tree_mask;
   p.mask_sb = mask_stride_b;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(slots * d * 4));
+  p.pieces = static_cast<int2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part_o);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part_ml);
+  p.parts = static_cast<int>(parts);
+  p.slots_by_pair = ws.by_pair ? 1 : 0;
+  p.row_tiles = static_cast<int>((rows + fa::tree_cta_rows(rows) - 1) / fa::tree_cta_rows(rows));
   p.B = B;
   p.Hq = H_q;
   p.Hkv = H_kv;
@@ -1243,11 +1253,7 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   p.num_blocks = num_blocks;
   p.block_size = block_size;
   p.max_blocks = max_blocks;
-  p.n_splits = n_splits;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int64_t rows = static_cast<int64_t>(T) * p.G;
-  p.tile_rows = fa::tree_tile_rows(rows);
-  p.row_tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
   if (cache_dtype == FA_BF16 && d == 128) {  // one box per page of one head
     if ((r = make_page_map5(&p.tm_k, k_cache, num_blocks, H_kv, block_size, "k_cache")) != FA_OK) return r;
     if ((r = make_page_map5(&p.tm_v, v_cache, num_blocks, H_kv, block_size, "v_cache")) != FA_OK) return r;
@@ -1263,7 +1269,7 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   }
   cudaError_t e = fa::launch_decode_tree(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_decode_tree launch");
-  return check_launch(who, n_splits == 1 ? 1 : 2);
+  return check_launch(who, 2);
 }
 
 }  // extern "C"

@@ -160,10 +160,13 @@ struct TreeParams {
   const int* draft_lens;   // [B] or null (T each)
   const uint8_t* mask;     // mask[b·mask_sb + t·T + u], or null: u <= t
   int64_t mask_sb;
-  float* part_o;   // [B·Hq·T, n_splits, d] fp32
-  float* part_ml;  // [B·Hq·T, n_splits, 2] fp32: (m in log2 units, ℓ)
-  int B, Hq, Hkv, G, T, num_blocks, block_size, max_blocks, n_splits;
-  int tile_rows, row_tiles;  // rows of one CTA (16, 32 or 64) and tiles of the T·G rows of a key/value head
+  int2* pieces;    // [B·Hkv]: first part of a pair and the number of parts it lies in
+  float* part_o;   // [slot, T·G, d] fp32: o/ℓ of a cut pair's pieces
+  float* part_ml;  // [slot, T·G, 2] fp32: (m in log2 units, ℓ)
+  int B, Hq, Hkv, G, T, num_blocks, block_size, max_blocks;
+  int row_tiles;      // CTA tiles of the T·G rows of a pair
+  int parts;          // equal parts that the line of key tiles is cut into
+  int slots_by_pair;  // a piece's slot: pair + part, else two per part
   float scale_log2;
   unsigned int* err;
 };
@@ -171,7 +174,7 @@ struct TreeParams {
 cudaError_t launch_rope(const RopeParams& p, bool fp32, bool inter, bool in_place, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheParams& p, int d, bool fp8, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheParams& p, int d, bool fp8, cudaStream_t s);
-int tree_tile_rows(int64_t rows);
+int tree_cta_rows(int64_t rows);  // rows one CTA takes, for T·G rows in all
 cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s);
 
 cudaError_t launch_fwd_bf16(int d, const FwdParams& p, cudaStream_t s);

@@ -6,38 +6,48 @@
 // where mask[t][u] is set (u ≤ t without a mask).  Rows that see nothing, the
 // padding rows t ≥ m among them, give O = 0 and LSE = −∞.
 //
-// The T·G query rows of one (b, key/value head) are cut into tiles of NR = 16,
-// 32 or 64 rows, the keys into n_splits chunks; a CTA takes one row tile over
-// one chunk.  Bound: the cache is read once per row tile; up to 64 rows that is
-// device memory, with more tiles the tensor cores and exponentials.
-//
-// Both products run transposed, with the keys (or the head dim) on the 128
-// matrix rows and the query rows on the N side:
+// Products.  Both run transposed, with the keys (or the head dim) on the 128
+// matrix rows and the T·G query rows of a key/value head on the N side:
 //   Sᵀ[key, row] = K Qᵀ,  Oᵀ[dim, row] += Vᵀ P̃ᵀ.
 // N is as small as the rows are few, where putting 1 … 64 query rows on the
 // 128-row side would pay for 128 rows of products and exponentials.  K and V go
 // from the pages into shared memory as they lie (a page of one head is one TMA
-// box) and are used as the A operand both times: K with its head dim
-// contiguous, V with its head dim along M.  A softmax thread owns one key of
-// the tile (TMEM lane) and walks over the rows (TMEM columns); P̃ᵀ goes to
-// shared memory as 128 bytes per key with the rows contiguous.
+// box) and are the A operand both times: K with its head dim contiguous, V with
+// its head dim along M.  A softmax thread owns one key of the tile (TMEM lane)
+// and walks over the rows (TMEM columns); P̃ᵀ goes to shared memory as 128 bytes
+// per key with the rows contiguous.
+//
+// Two streams.  A tile's softmax is a chain of waits (scores out of TMEM, the
+// group's vote, exponentials, P̃ into shared memory, the second product), so two
+// warpgroups run two of them at once, each with its own S, P̃, O and statistics.
+// Up to 64 rows they take alternate key tiles and are joined at the end; above,
+// they take two tiles of 64 rows over the same keys, so that K and V are fetched
+// once for 128 rows.
 //
 // Row maxima lie across threads in this layout, so they are not recomputed per
-// tile: a row keeps its reference m while every score is below m + 2^lazy, which
-// one barrier with an OR tells; only then the tile's maxima are exchanged and O
-// and ℓ rescaled.  ℓ stays in per-thread partial sums until the end.
+// tile: a row keeps its reference m while every score is less than 2^8 above it,
+// which one barrier with an OR tells; only then the tile's maxima are exchanged
+// and O and ℓ rescaled.  ℓ stays in per-thread partial sums until the end.
 //
-// bf16 cache: P̃ enters as two bf16 terms, p ≈ hi + lo, two MMAs into one
-// accumulator; p is then good to 2⁻¹⁷ at the price of N more columns, where one
-// term alone would add an error as large as O's own rounding to bf16.
+// Work.  The 128-key tiles of all (b, key/value head) pairs form one line that is
+// cut into equal parts, one per CTA (per CTA group where there are several row
+// tiles), so ragged batches load every SM alike and short ones spread over the
+// machine.  A CTA walks over its part without draining its pipeline between
+// pairs.  A pair that is cut leaves o/ℓ, m, ℓ of each piece in the workspace,
+// and a second kernel joins them.
+//
+// bf16 cache: up to 64 rows, where device memory bounds it, P̃ enters as two bf16
+// terms p ≈ hi + lo in separate columns (good to 2⁻¹⁷; one term alone adds an
+// error as large as O's own rounding to bf16).  Above 64 rows the products bound
+// it and P̃ is one bf16 term, as in the prefill forward.
 // E4M3 cache: K is multiplied as it is; q enters as two E4M3 terms
 // q·2⁻ᵃ = hi + lo/16 in separate columns (exact for elements down to 2⁻¹⁴ of the
 // row's largest, below that off by 2⁻²² of it), and the key's power of two
-// multiplies the score in fp32.  V is widened to fp16 (exact) by four converter
-// warps while the scores are worked on, so P̃ is fp16 (2⁻¹¹); the value row's
-// power of two is folded into P̃ relative to a running maximum.  fp16 P̃ is kept
-// near 2⁷ … 2¹⁵ by the reference m, so its subnormals begin 2⁻²¹ below a row's
-// largest weight.
+// multiplies the score in fp32.  V is widened to fp16 (exact) by the softmax
+// warps before they take up the tile's scores, so P̃ is fp16 (2⁻¹¹); the value
+// row's power of two is folded into P̃ relative to a running maximum.  The reference is
+// taken 2^3 below the maximum and P̃ stays below 2^15, so fp16's subnormals begin
+// 2⁻¹⁷ below a row's largest weight and weights are off by at most 2⁻²⁸ of it.
 //
 // Values in masked places.  Cache slots past the sequence end are zeroed in
 // shared memory before V is used.  A drafted key's value row is seen by some
@@ -45,6 +55,7 @@
 // non-finite elements of drafted rows are zeroed there too, and added to the
 // rows that do see them at the end.
 #include <cuda_fp16.h>
+#include <stddef.h>
 
 #include "fa_kernels.h"
 #include "sm103.cuh"
@@ -54,45 +65,63 @@ namespace {
 
 constexpr int kBN = 128;                 // keys per tile
 constexpr int kPBlock = kBN * 128;       // P̃ᵀ: one 128-byte row per key
-constexpr int kMaxStagedPages = 1024;
 constexpr int kMaxRing = 8;
+constexpr int kThreads = 384;            // warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11
+// Registers per thread at launch and after the warpgroups' split (2·208 + 88 = 3·168): a softmax thread holds its
+// scores and partial sums, 2·NR values, and a spilled one would go to L2, shared memory leaving no L1.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch && kThreads == 384, "register split");
 constexpr uint64_t kDrainNs = 200000000ull;
+constexpr int kScaleRing = 16;           // E4M3: tiles whose scale bytes are staged (V slots and four more)
+constexpr int kFRing = 4;                // pieces whose row factors may be live at once
+constexpr int kBadRing = 8;              // pieces whose flags of bad values may be
 
-template <int D, bool FP8, int NR>
+// NR rows per stream; TILES = 1: both streams work on the same rows, 2: on two tiles of rows.
+template <int D, bool FP8, int NR, int TILES>
 struct Cfg {
-  static constexpr int kThreads = FP8 ? 320 : 192;  // softmax 0–3, producer 4, MMA 5, converters 6–9
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
-  static constexpr int kRK = (FP8 ? 3 : 2) * (128 / D);  // K and V ring slots: 160 KB (bf16), 112 KB (E4M3)
-  static constexpr int kRV = (FP8 ? 4 : 3) * (128 / D);
-  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;     // one widened V tile, double buffered
-  static constexpr int kQ = FP8 ? 2 * NR * D : NR * D * 2;
+  static constexpr int kTerms = !FP8 && TILES == 1 ? 2 : 1;   // of P̃
+  static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
+  static constexpr int kP = (kPCols + 63) / 64 * kPBlock;     // of one stream
+  static constexpr int kQTile = FP8 ? 2 * NR * D : NR * D * 2;
+  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;          // one widened V tile, double buffered
+  static constexpr int kFixed = 2 * kV16 + 2 * kP + TILES * kQTile;
+  // K and V ring slots in what is left of 208 KB (V is needed later than K).
+  static constexpr int kRing = (208 * 1024 - kFixed) / kSlot < 14 ? (208 * 1024 - kFixed) / kSlot : 14;
+  static constexpr int kRK = kRing / 2;
+  static constexpr int kRV = kRing - kRK;
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kRK * kSlot;
   static constexpr int kOffV16 = kOffV + kRV * kSlot;
   static constexpr int kOffP = kOffV16 + 2 * kV16;
-  static constexpr int kOffQ = kOffP + kPBlock * (FP8 ? 1 : 2);
-  static constexpr int kOffPages = kOffQ + kQ;
-  static constexpr int kOffMisc = kOffPages + kMaxStagedPages * 4;
-  static constexpr int kSW = FP8 ? 2 * NR : NR;          // TMEM columns of one S buffer
-  static constexpr int kColO = 2 * kSW;
-  static constexpr uint32_t kTmemCols = kColO + NR <= 64 ? 64 : kColO + NR <= 128 ? 128 : kColO + NR <= 256 ? 256 : 512;
-  static_assert(kRK <= kMaxRing && kRV <= kMaxRing, "ring barriers");
-  static_assert(kQ % 1024 == 0 && kSlot % 1024 == 0, "swizzle atoms");
+  static constexpr int kOffQ = kOffP + 2 * kP;
+  static constexpr int kOffMisc = kOffQ + TILES * kQTile;
+  static constexpr int kSCols = FP8 ? 2 * NR : NR;            // TMEM columns of one stream's S
+  static constexpr int kColO = 2 * kSCols;
+  static constexpr int kCols = kColO + 2 * kPCols;
+  static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && kRV + 4 <= kScaleRing, "rings");
+  static_assert(kQTile % 1024 == 0 && kSlot % 1024 == 0 && kCols <= 512, "swizzle atoms, TMEM");
 };
 
 template <int NR>
 struct Misc {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t s_full[2], s_free[2], p_full, p_free, v16_full[2], v16_empty[2], drain;
-  alignas(16) float m[NR];  // reference maxima (log2 units), −∞ while a row has seen nothing
-  alignas(16) float f[NR];  // what a raw score is multiplied by (per row for E4M3)
-  float corr[NR];    // factor of the last rescale
-  float red[4][NR];  // per-warp maxima or sums
-  int64_t row[NR];   // (b·Hq + h)·T + t, or −1 for a row that is not there
-  int64_t o_off[NR]; // element offset of the row in O
-  int token[NR];
-  int kv_red[4];
-  uint32_t bad[8];   // drafted keys with non-finite values (one bit each)
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], v16_full[2], v16_empty[2];
+  uint64_t sc_full[kScaleRing], q_full, q_empty, drain;
+  alignas(16) float m[2][NR];          // reference maxima (log2 units), −∞ while a row has seen nothing
+  alignas(16) float f[kFRing][2][NR];  // E4M3: what a row's raw scores are multiplied by
+  float corr[2][NR];                   // factor of the last rescale; in the end what O is multiplied by
+  float red[2][4][NR];                 // per-warp maxima or sums
+  float lsum[2][NR];
+  int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
+  int64_t o_off[2][NR];                // its element offset in O
+  int kv_red[2][4], kv_ref[2];
+  alignas(16) uint8_t k_scale[kScaleRing][kBN];  // written by bulk copies
+  alignas(16) uint8_t v_scale[kScaleRing][kBN];
+  uint32_t bad[kBadRing][8];           // drafted keys with non-finite values (one bit each)
+  long long warp_sum[kThreads / 32];
+  int start_b, start_h, start_tile;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -110,6 +139,8 @@ __device__ __forceinline__ void seq_lengths(const TreeParams& p, int b, int& len
     len = drafts = 0;
   }
 }
+// Key tiles of a sequence; one without drafted tokens has no rows and needs none.
+__device__ __forceinline__ int seq_tiles(int len, int drafts) { return drafts > 0 ? (len + kBN - 1) / kBN : 0; }
 
 __device__ __forceinline__ int checked_page(const TreeParams& p, int b, int index) {
   const int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + index];
@@ -118,6 +149,48 @@ __device__ __forceinline__ int checked_page(const TreeParams& p, int b, int inde
   return 0;
 }
 
+// Tiles per part of the line of W tiles.  At least two, one for each stream.
+__device__ __forceinline__ long long part_tiles(long long W, int parts) {
+  const long long per = (W + parts - 1) / parts;
+  return per < 2 ? 2 : per;
+}
+
+// A CTA's walk over its part: one (b, key/value head) pair, or a piece of it, per step.
+struct Walk {
+  const TreeParams& p;
+  long long left;   // tiles of the part that remain, this piece's excluded
+  int b, h, len, drafts, tiles;
+  int t0, t1;       // the piece: tiles [t0, t1) of the pair
+  int index;        // pieces before this one
+
+  __device__ __forceinline__ Walk(const TreeParams& p_, int b0, int h0, int tile, long long count) : p(p_) {
+    b = b0;
+    h = h0;
+    seq_lengths(p, b, len, drafts);
+    tiles = seq_tiles(len, drafts);
+    t0 = tile;
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + count));
+    left = count - (t1 - t0);
+    index = 0;
+  }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    if (++h == p.Hkv) {
+      h = 0;
+      do {
+        if (++b >= p.B) return false;
+        seq_lengths(p, b, len, drafts);
+        tiles = seq_tiles(len, drafts);
+      } while (tiles == 0);
+    }
+    t0 = 0;
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
+    left -= t1;
+    ++index;
+    return true;
+  }
+};
+
 struct OpMax {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
@@ -125,16 +198,16 @@ struct OpAdd {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
 
-// Reduces each of NR columns over the warp's 32 lanes by halving: at every step
-// a lane hands over the half of its columns that its partner keeps.  Ends with
-// max(1, NR/32) totals in v[0 …], of the columns from the returned one on.
-template <int NR, class Op>
-__device__ __forceinline__ int reduce_cols(float (&v)[NR], int lane, Op op) {
+// Reduces each of N columns over the warp's 32 lanes by halving: at every step a
+// lane hands over the half of its columns that its partner keeps.  The totals go
+// to out[0 … N − 1].
+template <int N, class Op>
+__device__ __forceinline__ void reduce_cols(float (&v)[N], int lane, Op op, float* out) {
   int base = 0;
 #pragma unroll
   for (int step = 0; step < 5; ++step) {
     const int mask = 16 >> step;
-    const int half = NR >> (step + 1);
+    const int half = N >> (step + 1);
     if (half >= 1) {
       const bool up = (lane & mask) != 0;
 #pragma unroll
@@ -148,105 +221,175 @@ __device__ __forceinline__ int reduce_cols(float (&v)[NR], int lane, Op op) {
       v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], mask));
     }
   }
-  return base;
-}
-
-// One tile's raw scores of this thread's key, all rows.
-template <bool FP8, int NR>
-__device__ __forceinline__ void load_scores(uint32_t addr, float (&s)[NR]) {
-  constexpr int C = NR < 32 ? NR : 32;
+  if (N >= 32 || (lane & (32 / (N < 32 ? N : 32) - 1)) == 0) {
 #pragma unroll
-  for (int c = 0; c < NR; c += C) {
-    uint32_t a[C];
-    if constexpr (C == 32) tmem_ld32(addr + c, a); else tmem_ld16(addr + c, a);
-    if constexpr (FP8) {
-      uint32_t b[C];
-      if constexpr (C == 32) tmem_ld32(addr + NR + c, b); else tmem_ld16(addr + NR + c, b);
-      tmem_wait_ld();
-      reg_fence(a);
-      reg_fence(b);
-#pragma unroll
-      for (int i = 0; i < C; i += 2)
-        ffma2(s[c + i], s[c + i + 1], __uint_as_float(b[i]), __uint_as_float(b[i + 1]), 0.0625f, 0.0625f,
-              __uint_as_float(a[i]), __uint_as_float(a[i + 1]));
-    } else {
-      tmem_wait_ld();
-      reg_fence(a);
-#pragma unroll
-      for (int i = 0; i < C; ++i) s[c + i] = __uint_as_float(a[i]);
-    }
+    for (int i = 0; i < (N >= 32 ? N / 32 : 1); ++i) out[base + i] = v[i];
   }
 }
 
-template <int D, bool FP8, int NR>
-__global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-  using C = Cfg<D, FP8, NR>;
+// Widens chunks [C0, C0 + N) of 16 E4M3 codes of one value row of D codes to fp16.
+// src: the row in its slot, swizzled as TMA wrote it; dst: the row in the first
+// 64-column block of the fp16 tile.  EDGE: the row may be a drafted one, whose NaN
+// codes are taken out and reported by the result, or lie past the end (dead).
+template <int D, int N, bool EDGE>
+__device__ __forceinline__ bool widen_row(const uint8_t* src, uint8_t* dst, int r, int c0, bool drafted, bool dead) {
+  const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+  bool bad = false;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const int ch = c0 + c;
+    const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (EDGE && drafted) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (((w[e] >> (8 * q)) & 0x7f) == 0x7f) w[e] &= ~(0xffu << (8 * q)), bad = true;
+    }
+    if (EDGE && dead) w[0] = w[1] = w[2] = w[3] = 0;
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = e4m3x2_to_f16x2(w[e >> 1] >> (16 * (e & 1)));
+    uint8_t* block = dst + (ch >> 2) * kBN * 128;  // 64 elements per 128-byte row
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  return bad;
+}
+
+// Multiplies N columns of this thread's lane by w[i]·k.
+template <int N>
+__device__ __forceinline__ void rescale_cols(uint32_t addr, const float* w, float k) {
+  constexpr int C = N < 32 ? N : 32;
+#pragma unroll
+  for (int c = 0; c < N; c += C) {
+    uint32_t r[C];
+    tmem_ld(addr + c, r);
+    tmem_wait_ld();
+    reg_fence(r);
+#pragma unroll
+    for (int i = 0; i < C; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (w[c + i] * k));
+    tmem_st(addr + c, r);
+  }
+  tmem_wait_st();
+}
+
+// True on one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred = 0;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+  return pred != 0;
+}
+
+// Position in a ring of N slots and the parity of its passes.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// The query rows of a piece as a K-major operand (rows that are not there as
+// zeros), by NT threads.  E4M3: two terms per element and the factor of the row.
+template <int D, bool FP8, int NR, int TILES, int NT>
+__device__ __forceinline__ void load_q(const TreeParams& p, const Walk& w, uint8_t* q_smem, float (*f)[NR], int row0,
+                                       int id) {
+  using C = Cfg<D, FP8, NR, TILES>;
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+  constexpr int kPer = (TILES * NR * kChunks + NT - 1) / NT;
+  constexpr int kBatch = kPer < 8 ? kPer : 8;  // loads in flight per thread
+  const int live = w.drafts * p.G - row0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kPer; i0 += kBatch) {
+    uint4 q4[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = (i0 + e) * NT + id;
+      const int n = i / kChunks, ch = i % kChunks;
+      q4[e] = make_uint4(0, 0, 0, 0);
+      if (n < live) {
+        const int rr = row0 + n;
+        const int t = rr / p.G;
+        q4[e] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + w.b * p.sq[0] +
+                                                (w.h * p.G + rr - t * p.G) * p.sq[1] + t * p.sq[2] + ch * 8);
+      }
+    }
+#pragma unroll
+    for (int e8 = 0; e8 < kBatch; ++e8) {
+      const int i = (i0 + e8) * NT + id;
+      const int n = i / kChunks, ch = i % kChunks;
+      const int tile = n / NR, r = n % NR;
+      if (n >= TILES * NR) continue;  // whole warps: a row is held by neighbouring lanes
+      const uint4 v = q4[e8];
+      uint8_t* qt = q_smem + tile * C::kQTile;
+      if constexpr (!FP8) {
+        *reinterpret_cast<uint4*>(qt + (ch >> 3) * NR * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+      } else {
+        // 2⁻ᵃ brings the row's largest magnitude to at most 448.
+        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+        float x[8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = __uint_as_float(e & 1 ? w4[e >> 1] & 0xffff0000u : w4[e >> 1] << 16);
+          const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
+          if (a < 0x7f800000u) top = max(top, a);
+          else x[e] = __uint_as_float(0x7fffffffu);
+        }
+#pragma unroll
+        for (int mk = kChunks / 2; mk > 0; mk >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, mk));
+        const int a = max(-126, static_cast<int>(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float y0 = x[e] * inv, y1 = x[e + 1] * inv;
+          const uint32_t h = pack_e4m3x2(y0, y1);
+          const uint32_t back = e4m3x2_to_f16x2(h);
+          const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          hi[e >> 2] |= h << ((e & 2) * 8);
+          lo[e >> 2] |= pack_e4m3x2((y0 - z.x) * 16.f, (y1 - z.y) * 16.f) << ((e & 2) * 8);
+        }
+        // Rows of D bytes; chunk of 16 bytes XORed with the row (128-byte rows) or half of it (64-byte rows).
+        const int sw = D == 128 ? r & 7 : (r >> 1) & 3;  // NR is a multiple of 16: the same for rows r and NR + r
+        uint8_t* dst = qt + r * D + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + NR * D) = make_uint2(lo[0], lo[1]);
+        if (ch == 0) f[tile][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+template <int D, bool FP8, int NR, int TILES>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  using C = Cfg<D, FP8, NR, TILES>;
   constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
   constexpr int kSlot = C::kSlot;
-  // Rescale once a score exceeds the reference by this; the reference is taken kBase below the maximum.
+  // Rescale once a score exceeds the reference by kLazy; the reference is taken kBase below the maximum.
   constexpr float kLazy = FP8 ? 11.f : 8.f;
-  constexpr float kBase = FP8 ? 7.f : 0.f;
+  constexpr float kBase = FP8 ? 3.f : 0.f;
   constexpr int kKvLazy = 4;  // fp16 P̃ stays below 2^(11 + 4)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   Misc<NR>* ms = reinterpret_cast<Misc<NR>*>(smem + C::kOffMisc);
-  int* staged = reinterpret_cast<int*>(smem + C::kOffPages);
   volatile int* abort_flag = &ms->abort_flag;
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // broadcast: known to be the same in the warp
   const int lane = tid & 31;
-  // Row tiles of one chunk are neighbours in the grid, so that they share its keys in L2.
-  int idx = blockIdx.x;
-  const int rt = idx % p.row_tiles;
-  idx /= p.row_tiles;
-  const int c = idx % p.n_splits;
-  idx /= p.n_splits;
-  const int hkv = idx % p.Hkv;
-  const int b = idx / p.Hkv;
-
-  int len, drafts;
-  seq_lengths(p, b, len, drafts);
-  const int context = len - drafts;
-  const int chunk = (((len + p.n_splits - 1) / p.n_splits) + kBN - 1) & ~(kBN - 1);
-  const int key0 = min(c * chunk, len);
-  const int kend = min(len, key0 + chunk);
-  const int row0 = rt * NR;
-  const int live_rows = drafts * p.G - row0;  // rows of this tile that belong to a drafted token
-  const int nt = live_rows > 0 ? (kend - key0 + kBN - 1) / kBN : 0;
-
-  if (tid < NR) {
-    const int rr = row0 + tid;
-    const int t = rr / p.G;
-    const int h = hkv * p.G + (rr - t * p.G);
-    const bool there = t < p.T;
-    ms->row[tid] = there ? (static_cast<int64_t>(b) * p.Hq + h) * p.T + t : -1;
-    ms->o_off[tid] = b * p.so[0] + h * p.so[1] + static_cast<int64_t>(t) * p.so[2];
-    ms->token[tid] = t;
-    ms->m[tid] = -INFINITY;
-    ms->f[tid] = p.scale_log2;
-    if (nt == 0 && there) {  // nothing to see in this chunk
-      if (p.n_splits > 1) {
-        p.part_ml[(ms->row[tid] * p.n_splits + c) * 2 + 0] = -INFINITY;
-        p.part_ml[(ms->row[tid] * p.n_splits + c) * 2 + 1] = 0.f;
-      } else if (p.lse != nullptr) {
-        p.lse[ms->row[tid]] = -INFINITY;
-      }
-    }
-  }
-  if (nt == 0) {
-    if (p.n_splits == 1) {
-      __syncthreads();
-      for (int i = tid; i < NR * (D / 8); i += C::kThreads) {
-        const int n = i / (D / 8);
-        if (ms->row[n] >= 0)
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + ms->o_off[n] + (i % (D / 8)) * 8) =
-              make_uint4(0, 0, 0, 0);
-      }
-    }
-    return;
-  }
+  const int rt = blockIdx.x % p.row_tiles;   // neighbours share their keys in L2
+  const int part = blockIdx.x / p.row_tiles;
+  const int row0 = rt * NR * TILES;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this grid's end
 
   if (tid == 0) {
     for (int s = 0; s < C::kRK; ++s) {
@@ -255,551 +398,648 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
     }
     for (int s = 0; s < C::kRV; ++s) {
       mbar_init(&ms->v_full[s], 1);
-      mbar_init(&ms->v_empty[s], FP8 ? 4 : 1);
+      mbar_init(&ms->v_empty[s], FP8 ? 4 * TILES : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
       mbar_init(&ms->s_free[s], 128);
-      mbar_init(&ms->v16_full[s], 128);
+      mbar_init(&ms->p_full[s], 128);
+      mbar_init(&ms->p_free[s], 1);
+      mbar_init(&ms->v16_full[s], 256);
       mbar_init(&ms->v16_empty[s], 1);
     }
-    mbar_init(&ms->p_full, 128);
-    mbar_init(&ms->p_free, 1);
+    for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
+    mbar_init(&ms->q_full, 32);
+    mbar_init(&ms->q_empty, 1);
     mbar_init(&ms->drain, 1);
     ms->abort_flag = 0;
-    for (int i = 0; i < 8; ++i) ms->bad[i] = 0;
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (tid < kBadRing * 8) ms->bad[tid >> 3][tid & 7] = 0;
+  if (warp == 9) {
     tmem_alloc(&ms->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-  // The chunk's page ids, checked.
-  const int page0 = key0 / p.block_size;
-  const int npages = (kend - 1) / p.block_size - page0 + 1;
-  for (int i = tid; i < min(npages, kMaxStagedPages); i += C::kThreads) staged[i] = checked_page(p, b, page0 + i);
-  auto page_id = [&](int key) -> int {
-    const int rel = key / p.block_size - page0;
-    return rel < kMaxStagedPages ? staged[rel] : checked_page(p, b, page0 + rel);
-  };
-  // The tile's query rows as a K-major operand (rows that are not there as zeros).
-  for (int i0 = 0; i0 < NR * (D / 8); i0 += C::kThreads) {
-    const int i = i0 + tid;
-    const bool in = i < NR * (D / 8);
-    const int n = in ? i / (D / 8) : 0, ch = i % (D / 8);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (in && n < live_rows) {
-      const int rr = row0 + n;
-      const int t = rr / p.G;
-      v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + b * p.sq[0] +
-                                          (hkv * p.G + rr - t * p.G) * p.sq[1] + t * p.sq[2] + ch * 8);
-    }
-    if constexpr (!FP8) {
-      if (in)
-        *reinterpret_cast<uint4*>(smem + C::kOffQ + (ch >> 3) * NR * 128 + n * 128 + (((ch & 7) ^ (n & 7)) << 4)) = v;
-    } else {
-      // 2⁻ᵃ brings the row's largest magnitude to at most 448.
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float x[8];
-      uint32_t top = 0;
+
+  // This CTA's part of the line of tiles: sums over the sequences, one block of them per thread.
+  const int per_thread = (p.B + kThreads - 1) / kThreads;
+  const int sb0 = min(p.B, tid * per_thread), sb1 = min(p.B, sb0 + per_thread);
+  long long mine = 0;
+  for (int b = sb0; b < sb1; ++b) {
+    int len, drafts;
+    seq_lengths(p, b, len, drafts);
+    mine += seq_tiles(len, drafts);
+  }
+  long long incl = mine;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-        const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
-        if (a < 0x7f800000u) top = max(top, a);
-        else x[e] = __uint_as_float(0x7fffffffu);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) ms->warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += ms->warp_sum[w];
+    total += ms->warp_sum[w];
+  }
+  total *= p.Hkv;
+  before *= p.Hkv;
+  const long long per = part_tiles(total, p.parts);
+  const long long first = part * per;
+  const long long count = min(per, total - first);
+  if (first >= before && first < before + mine * p.Hkv) {
+    long long at = first - before;
+    for (int b = sb0; b < sb1; ++b) {
+      int len, drafts;
+      seq_lengths(p, b, len, drafts);
+      const int n = seq_tiles(len, drafts);
+      if (at < static_cast<long long>(n) * p.Hkv) {
+        ms->start_b = b;
+        ms->start_h = static_cast<int>(at / n);
+        ms->start_tile = static_cast<int>(at % n);
+        break;
       }
-#pragma unroll
-      for (int mk = D / 16; mk > 0; mk >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, mk));
-      const int a = max(-126, static_cast<int>(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
-      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float y0 = x[e] * inv, y1 = x[e + 1] * inv;
-        const uint32_t h = pack_e4m3x2(y0, y1);
-        const uint32_t back = e4m3x2_to_f16x2(h);
-        const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&back));
-        hi[e >> 2] |= h << ((e & 2) * 8);
-        lo[e >> 2] |= pack_e4m3x2((y0 - z.x) * 16.f, (y1 - z.y) * 16.f) << ((e & 2) * 8);
-      }
-      if (in) {
-        // Rows of D bytes; chunk of 16 bytes XORed with the row (128-byte rows) or half of it (64-byte rows).
-        const int sw = D == 128 ? n & 7 : (n >> 1) & 3;  // NR is a multiple of 16: the same for rows n and NR + n
-        uint8_t* dst = smem + C::kOffQ + n * D + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(dst + NR * D) = make_uint2(lo[0], lo[1]);
-        if (ch == 0) ms->f[n] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
-      }
+      at -= static_cast<long long>(n) * p.Hkv;
     }
   }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem_base;
+  const int bshift = 31 - __clz(p.block_size);  // a power of two
 
-  if (warp == 4) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
-    }
-    int ki = 0, vi = 0;
+  if (count <= 0) {
+    // nothing left for this CTA
+  } else if (warp == 8 || warp == 10) {
+    reg_dealloc<kRegsOther>();
+    // ------------------------------------------- loads of K (warp 8) and V (warp 10)
+    const bool is_v = warp == 10;
+    const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
+    uint64_t* full = is_v ? ms->v_full : ms->k_full;
+    uint64_t* empty = is_v ? ms->v_empty : ms->k_empty;
+    uint8_t* dst = smem + (is_v ? C::kOffV : C::kOffK) + lane * p.block_size * (kSlot / kBN);
+    const int ring = is_v ? C::kRV : C::kRK;
+    if (lane == 0) tma_prefetch_desc(tm);
+    const int npt = kBN >> bshift;  // pages per tile
+    int slot = 0, sc = 0, issued = 0;
+    uint32_t parity = 1;
     bool ok = true;
-    const int bs = p.block_size;
-    auto load = [&](bool is_v) {
-      const int j = is_v ? vi : ki;
-      const int ring = is_v ? C::kRV : C::kRK;
-      const int slot = j % ring;
-      uint64_t* full = is_v ? &ms->v_full[slot] : &ms->k_full[slot];
-      uint64_t* empty = is_v ? &ms->v_empty[slot] : &ms->k_empty[slot];
-      bool got = true;
-      if (lane == 0) {
-        got = mbar_wait(empty, ((j / ring) & 1) ^ 1, abort_flag, p.err, site(is_v ? 2 : 1));
-        if (got) mbar_arrive_expect_tx(full, kSlot);
-      }
-      ok = __shfl_sync(0xffffffffu, got, 0);
-      if (!ok) return;
-      const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
-      uint8_t* dst = smem + (is_v ? C::kOffV : C::kOffK) + slot * kSlot;
-      if (lane < kBN / bs) {
-        const int t0 = key0 + j * kBN + lane * bs;
-        int blk = 0, row = bs;  // a row past the page: TMA fills the box with zeros
-        if (t0 < kend) {
-          blk = page_id(t0);
-          row = 0;
-        }
-        if constexpr (kPg5)
-          tma_load_5d(dst + lane * bs * 256, tm, full, 0, 0, 0, row >> 3, blk * p.Hkv + hkv);
-        else
-          tma_load_4d(dst + lane * bs * (kSlot / kBN), tm, full, 0, row, hkv, blk);
-      }
-      (is_v ? vi : ki) += 1;
-    };
-    load(false);
-    for (int j = 0; ok && j < nt; ++j) {
-      if (j + 1 < nt) load(false);
-      if (ok) load(true);
-    }
-    if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA ends
-      for (int j = max(0, ki - C::kRK); j < ki; ++j)
-        mbar_wait_drain(&ms->k_full[j % C::kRK], (j / C::kRK) & 1, kDrainNs);
-      for (int j = max(0, vi - C::kRV); j < vi; ++j)
-        mbar_wait_drain(&ms->v_full[j % C::kRV], (j / C::kRV) & 1, kDrainNs);
-    }
-  } else if (warp == 5) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
-      constexpr uint32_t kIdescO = FP8 ? idesc_f16_f32(128, NR, true, true) : idesc_bf16_f32(128, NR, true, true);
-      const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK), sP = smem_u32(smem + C::kOffP);
-      auto issue_pv = [&](int j) -> bool {
-        const int slot = j % C::kRV;
-        if (!mbar_wait(&ms->p_full, j & 1, abort_flag, p.err, site(3))) return false;
-        if constexpr (FP8) {
-          if (!mbar_wait(&ms->v16_full[j & 1], (j >> 1) & 1, abort_flag, p.err, site(4))) return false;
-        } else {
-          if (!mbar_wait(&ms->v_full[slot], (j / C::kRV) & 1, abort_flag, p.err, site(4))) return false;
-        }
-        tc_fence_after();
-        const uint32_t sV = smem_u32(smem + (FP8 ? C::kOffV16 + (j & 1) * C::kV16 : C::kOffV + slot * kSlot));
-#pragma unroll
-        for (int term = 0; term < (FP8 ? 1 : 2); ++term)
-#pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk) {
-            // A: 16 keys, the head dim along M in 64-element blocks (D = 64: the one block twice, the upper
-            // 64 rows of the result are not read).  B: 16 keys of P̃ᵀ.
-            const uint64_t ad = kPg5 ? sdesc_sw128(sV + kk * 4096, 1024, 2048)
-                                     : sdesc_sw128(sV + kk * 2048, D == 128 ? kBN * 128 : 0, 1024);
-            const uint64_t bd = sdesc_sw128(sP + term * kPBlock + kk * 2048, kPBlock, 1024);
-            mma_bf16_ss(tmem + C::kColO, ad, bd, kIdescO, (j > 0 || term > 0 || kk > 0) ? 1u : 0u);
+    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
+    do {
+      const int pages = (w.len + p.block_size - 1) >> bshift;
+      const int32_t* table = p.block_table + static_cast<int64_t>(w.b) * p.max_blocks;
+      // The ids of 32 pages at a time, one per lane, loaded one group ahead and checked when they are due.
+      int page = w.t0 * npt + lane;
+      int id = 0, ahead = page < pages ? table[page] : 0;
+      int at = 32;  // the tile's first page in the group
+      for (int i = w.t0; ok && i < w.t1; ++i) {
+        if (at == 32) {
+          at = 0;
+          id = page < pages ? ahead : -1;  // −1: past the end
+          if (page < pages && (id < 0 || id >= p.num_blocks)) {
+            atomicCAS(p.err + 1, 0u, (kKernTree << 8) | kSiteBadBlock);
+            id = 0;
           }
-        mma_commit(&ms->p_free);
-        mma_commit(FP8 ? &ms->v16_empty[j & 1] : &ms->v_empty[slot]);
+          page += 32;
+          ahead = page < pages ? table[page] : 0;
+        }
+        const int blk = __shfl_sync(0xffffffffu, id, at + lane);
+        at += npt;
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, site(is_v ? 2 : 1)));
+        if (!ok) break;
+        const bool real = lane < npt && blk >= 0;
+        const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[slot], kSlot);
+          // The slot is free: the tile kRV before it has been widened, so the tile kRV + 3 before is done with, and
+          // so are its scale bytes.
+          if (FP8 && is_v) mbar_arrive_expect_tx(&ms->sc_full[sc], 2 * n_real * p.block_size);
+        }
+        __syncwarp();
+        if (lane < npt) {
+          const int row = real ? 0 : p.block_size;  // a row past the page: TMA fills the box with zeros
+          const int head = (real ? blk : 0) * p.Hkv + w.h;
+          if constexpr (kPg5)
+            tma_load_5d(dst + slot * kSlot, tm, &full[slot], 0, 0, 0, row >> 3, head);
+          else
+            tma_load_4d(dst + slot * kSlot, tm, &full[slot], 0, row, w.h, real ? blk : 0);
+          if (FP8 && is_v && real) {
+            const int64_t from = static_cast<int64_t>(head) << bshift;
+            bulk_load(&ms->k_scale[sc][lane << bshift], p.k_scale + from, p.block_size, &ms->sc_full[sc]);
+            bulk_load(&ms->v_scale[sc][lane << bshift], p.v_scale + from, p.block_size, &ms->sc_full[sc]);
+          }
+        }
+        ++issued;
+        sc = (sc + 1) % kScaleRing;
+        if (++slot == ring) {
+          slot = 0;
+          parity ^= 1u;
+        }
+      }
+    } while (ok && w.next());
+    if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA ends
+      for (int n = max(0, issued - ring); n < issued; ++n) {
+        mbar_wait_drain_inl(&full[n % ring], (n / ring) & 1, kDrainNs);
+        if (FP8 && is_v) mbar_wait_drain_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, kDrainNs);
+      }
+    }
+  } else if (warp == 9) {
+    reg_dealloc<kRegsOther>();
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
+    constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
+    constexpr uint32_t kIdescO = FP8 ? idesc_f16_f32(128, NR, true, true) : idesc_bf16_f32(128, C::kPCols, true, true);
+    const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK), sP = smem_u32(smem + C::kOffP);
+    const uint32_t sV = smem_u32(smem + C::kOffV), sV16 = smem_u32(smem + C::kOffV16);
+    const bool leader = elect_one();
+    auto agree = [](bool v) { return static_cast<bool>(__all_sync(0xffffffffu, v)); };
+    Ring<C::kRK> rk;
+    Ring<C::kRV> rv;
+    Ring<2> r16;                 // two row tiles: the widened V tile
+    uint32_t s_par = 3, p_par = 0;  // parities of s_free and p_full to wait for, a bit per stream
+    bool ok = true;
+    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
+    do {
+      // Step s: stream s & 1, tile s (or s / 2).  Broadcast, like the walk's end below, to keep the loop uniform.
+      const int steps = __shfl_sync(0xffffffffu, (w.t1 - w.t0) * TILES, 0);
+      ok = agree(mbar_wait_inl(&ms->q_full, w.index & 1, abort_flag, p.err, site(14)));
+      auto issue_s = [&](int s) -> bool {
+        const int g = s & 1;
+        const bool k_done = TILES == 1 || g == 1;  // the last use of the K tile
+        if (!agree(mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, site(5)) &&
+                   mbar_wait_inl(&ms->s_free[g], (s_par >> g) & 1u, abort_flag, p.err, site(6))))
+          return false;
+        s_par ^= 1u << g;
+        tc_fence_after();
+        const uint32_t kb = sK + rk.slot * kSlot;
+        const uint32_t qb = sQ + (TILES == 1 ? 0 : g * C::kQTile);
+        const uint32_t ds = tmem + g * C::kSCols;
+        if (leader) {
+          // Descriptors of the k-steps differ from the first ones by their start addresses alone.
+          if constexpr (FP8) {
+            const uint64_t ad = D == 128 ? sdesc_sw128(kb, 16, 1024) : sdesc_sw64(kb, 16, 512);
+            const uint64_t bd = D == 128 ? sdesc_sw128(qb, 16, 1024) : sdesc_sw64(qb, 16, 512);
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) mma_e4m3_ss(ds, ad + kk * 2, bd + kk * 2, kIdescS, kk > 0 ? 1u : 0u);
+          } else {
+            const uint64_t ad = sdesc_sw128(kb, 16, kPg5 ? 2048 : 1024);
+            const uint64_t bd = sdesc_sw128(qb, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ss(ds, ad + (kk >> 2) * 64 + (kk & 3) * 2, bd + (kk >> 2) * (NR * 8) + (kk & 3) * 2, kIdescS,
+                          kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&ms->s_full[g]);
+          if (k_done) mma_commit(&ms->k_empty[rk.slot]);
+          if (s == steps - 1) mma_commit(&ms->q_empty);
+        }
+        if (k_done) rk.advance();
         return true;
       };
-      bool ok = true;
-      for (int j = 0; ok && j < nt; ++j) {
-        const int slot = j % C::kRK;
-        ok = mbar_wait(&ms->k_full[slot], (j / C::kRK) & 1, abort_flag, p.err, site(5)) &&
-             mbar_wait(&ms->s_free[j & 1], ((j >> 1) & 1) ^ 1, abort_flag, p.err, site(6));
-        if (!ok) break;
+      auto issue_pv = [&](int s) -> bool {
+        const int g = s & 1;
+        const bool v_done = TILES == 1 || g == 1;  // the last use of the V tile
+        bool ready = mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, site(3));
+        if constexpr (!FP8)
+          ready = mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, site(4)) && ready;
+        else if constexpr (TILES == 2)
+          ready = mbar_wait_inl(&ms->v16_full[r16.slot], r16.parity, abort_flag, p.err, site(4)) && ready;
+        if (!agree(ready)) return false;
+        p_par ^= 1u << g;
         tc_fence_after();
-        const uint32_t kb = sK + slot * kSlot;
-        const uint32_t ds = tmem + (j & 1) * C::kSW;
-        if constexpr (FP8) {
+        const uint32_t vb = FP8 ? sV16 + (TILES == 1 ? g : r16.slot) * C::kV16 : sV + rv.slot * kSlot;
+        const uint32_t pb = sP + g * C::kP;
+        const uint32_t dst = tmem + C::kColO + g * C::kPCols;
+        if (leader) {
+          // A: 16 keys per k-step, the head dim along M in 64-element blocks (D = 64: the one block twice, the upper 64
+          // rows of the result are not read).  B: 16 keys of P̃ᵀ.
+          const uint64_t ad = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, D == 128 ? kBN * 128 : 0, 1024);
+          const uint64_t bd = sdesc_sw128(pb, kPBlock, 1024);
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            if constexpr (D == 128)
-              mma_e4m3_ss(ds, sdesc_sw128(kb + kk * 32, 16, 1024), sdesc_sw128(sQ + kk * 32, 16, 1024), kIdescS,
-                          kk > 0 ? 1u : 0u);
-            else
-              mma_e4m3_ss(ds, sdesc_sw64(kb + kk * 32, 16, 512), sdesc_sw64(sQ + kk * 32, 16, 512), kIdescS,
-                          kk > 0 ? 1u : 0u);
-          }
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t ad = kPg5 ? sdesc_sw128(kb + (kk >> 2) * 1024 + (kk & 3) * 32, 16, 2048)
-                                     : sdesc_sw128(kb + kk * 32, 16, 1024);
-            const uint64_t bd = sdesc_sw128(sQ + (kk >> 2) * NR * 128 + (kk & 3) * 32, 16, 1024);
-            mma_bf16_ss(ds, ad, bd, kIdescS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + kk * 128, kIdescO, (s >= 2 || kk > 0) ? 1u : 0u);
+          mma_commit(&ms->p_free[g]);
+          if (v_done) {
+            if constexpr (!FP8) mma_commit(&ms->v_empty[rv.slot]);
+            else if constexpr (TILES == 2) mma_commit(&ms->v16_empty[r16.slot]);
           }
         }
-        mma_commit(&ms->s_full[j & 1]);
-        mma_commit(&ms->k_empty[slot]);
-        if (j >= 1) ok = issue_pv(j - 1);
+        if (v_done) {
+          rv.advance();
+          r16.advance();
+        }
+        return true;
+      };
+      // S runs two steps ahead, so that a stream's next scores are ready when it has stored P̃.
+      ok = ok && issue_s(0);
+      if (ok && steps > 1) ok = issue_s(1);
+      for (int s = 0; ok && s < steps; ++s) {
+        if (s + 2 < steps) ok = issue_s(s + 2);
+        ok = ok && issue_pv(s);
       }
-      if (ok) issue_pv(nt - 1);
-      if (*abort_flag) {
-        mma_commit(&ms->drain);
-        mbar_wait_drain(&ms->drain, 0, kDrainNs);
-      }
+    } while (ok && __shfl_sync(0xffffffffu, w.next(), 0));
+    if (*abort_flag && leader) {
+      mma_commit(&ms->drain);
+      mbar_wait_drain_inl(&ms->drain, 0, kDrainNs);
     }
-  } else if (warp < 4) {
-    // --------------------------------------- softmax: one key per thread, all rows
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    float l[NR];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) l[n] = 0.f;
-    int kv_ref = -1024;
+  } else if (warp < 8) {
+    reg_alloc<kRegsSoftmax>();
+    // ------------------------------------- softmax: one key per thread, NR rows
+    const int g = warp >> 2;
+    const int bar = 1 + g;
+    const int kt = tid & 127;  // key in the tile, TMEM lane, head dim of O
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + g * C::kSCols;
+    const uint32_t o_addr = tmem + lane_base + C::kColO + g * C::kPCols;
+    float* m_ref = ms->m[g];
+    float* corr = ms->corr[g];
+    int tile0 = 0;             // tiles of the pieces before, and those of this stream
+    int used = 0;
     bool ok = true;
-    // E4M3: the scale bytes of this thread's key, two tiles ahead.
-    int sk[3] = {0, 0, 0}, sv[3] = {0, 0, 0};
-    auto fetch_scales = [&](int j, int& a, int& v) {
-      const int key = key0 + j * kBN + tid;
-      if (key < kend) {
-        const int64_t at = (static_cast<int64_t>(page_id(key)) * p.Hkv + hkv) * p.block_size + key % p.block_size;
-        a = p.k_scale[at];
-        v = p.v_scale[at];
+    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
+    load_q<D, FP8, NR, TILES, 256>(p, w, smem + C::kOffQ, ms->f[0], row0, tid);
+    named_sync(3, 256);
+    if (warp == 0) mbar_arrive(&ms->q_full);
+    do {
+      const int n_tiles = w.t1 - w.t0;
+      const int context = w.len - w.drafts;
+      const int my_row0 = row0 + (TILES == 1 ? 0 : g * NR);
+      const int live = w.drafts * p.G - my_row0;  // rows of this tile that belong to a drafted token
+      if (kt < NR) {
+        const int rr = my_row0 + kt;
+        const int t = rr / p.G;
+        const int h = w.h * p.G + (rr - t * p.G);
+        ms->row[g][kt] = kt < live ? (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t : -1;
+        ms->o_off[g][kt] = w.b * p.so[0] + h * p.so[1] + static_cast<int64_t>(t) * p.so[2];
+        m_ref[kt] = -INFINITY;
       }
-    };
-    if constexpr (FP8) {
-      fetch_scales(0, sk[0], sv[0]);
-      fetch_scales(1, sk[1], sv[1]);
-    }
-    for (int j = 0; j < nt; ++j) {
-      if constexpr (FP8) fetch_scales(j + 2, sk[2], sv[2]);
-      const int key = key0 + j * kBN + tid;
-      const bool tail = key0 + (j + 1) * kBN > context;  // the tile holds drafted keys or the end
-      // Which rows see this key (bit per row); context keys are seen by all.
-      uint64_t seen = ~0ull;
-      if (tail && key >= context) {
-        seen = 0;
-        const int u = key - context;
-        if (key < kend) {
-          bool sees = false;
-          int last = -1;
-          for (int n = 0; n < NR; ++n) {
-            const int t = ms->token[n];
-            if (t >= drafts) break;
-            if (t != last) {
-              sees = p.mask != nullptr ? p.mask[b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t;
-              last = t;
-            }
-            seen |= static_cast<uint64_t>(sees) << n;
-          }
-        }
-      }
-      ok = mbar_wait(&ms->s_full[j & 1], (j >> 1) & 1, abort_flag, p.err, site(7));
-      tc_fence_after();
-      const uint32_t sa = tmem + lane_base + (j & 1) * C::kSW;
-      // 2^(k of the key) for E4M3; s = 0 stands for 2^−127, which only its double times ½ can build.
-      float ks = 1.f;
-      int kv = -1024;
-      if constexpr (FP8) {
-        ks = sk[0] == 0 ? 5.877471754111438e-39f : __uint_as_float(static_cast<uint32_t>(sk[0]) << 23);
-        if (key < kend) kv = sv[0] - 127;
-      }
-      // x = score − reference, masked to −∞ where the row does not see the key.
-      float x[NR];
-      auto scores = [&](bool relative) {
-        load_scores<FP8, NR>(sa, x);
+      // Does row n of this tile (a live one) see drafted key u?
+      auto sees = [&](int n, int u) -> bool {
+        const int t = (my_row0 + n) / p.G;
+        return p.mask != nullptr ? p.mask[w.b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t;
+      };
+      named_sync(bar, 128);
+      float l[NR];
 #pragma unroll
-        for (int n = 0; n < NR; n += 4) {
-          const float4 m4 = relative ? *reinterpret_cast<const float4*>(&ms->m[n]) : make_float4(0.f, 0.f, 0.f, 0.f);
-          float4 f4;
-          if constexpr (FP8) {
-            f4 = *reinterpret_cast<const float4*>(&ms->f[n]);
-            fmul2(f4.x, f4.y, f4.x, f4.y, ks, ks);
-            fmul2(f4.z, f4.w, f4.z, f4.w, ks, ks);
-          } else {
-            f4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+      for (int n = 0; n < NR; ++n) l[n] = 0.f;
+      int kv_ref = -1024;
+      int done = 0;  // tiles of this piece that this stream has worked on
+      const float* f_row = ms->f[w.index % kFRing][TILES == 1 ? 0 : g];
+      for (int i = TILES == 1 ? g : 0; i < n_tiles; i += TILES == 1 ? 2 : 1, ++done) {
+        const int tile = tile0 + i;
+        const int u = used + done;
+        const int key = (w.t0 + i) * kBN + kt;
+        const bool tail = (w.t0 + i + 1) * kBN > context;  // the tile holds drafted keys or the end
+        // Which rows see this key (bit per row); context keys are seen by all.
+        uint64_t seen = ~0ull;
+        if (tail && key >= context) {
+          seen = 0;
+          if (key < w.len && live > 0) {
+            // Token by token: one byte of the mask stands for G rows.
+            const int ta = my_row0 / p.G;
+            const int tb = min(w.drafts - 1, (my_row0 + min(NR, live) - 1) / p.G);
+            const uint8_t* mk = p.mask != nullptr ? p.mask + w.b * p.mask_sb + (key - context) : nullptr;
+#pragma unroll 4
+            for (int t = ta; t <= tb; ++t) {
+              const bool on = mk != nullptr ? mk[static_cast<int64_t>(t) * p.T] != 0 : key - context <= t;
+              const int lo = max(0, t * p.G - my_row0), hi = min(NR, (t + 1) * p.G - my_row0);  // its rows
+              const uint64_t bits = (hi - lo >= 64 ? ~0ull : (1ull << (hi - lo)) - 1) << lo;
+              seen |= on ? bits : 0;
+            }
           }
-          ffma2(x[n], x[n + 1], x[n], x[n + 1], f4.x, f4.y, -m4.x, -m4.y);
-          ffma2(x[n + 2], x[n + 3], x[n + 2], x[n + 3], f4.z, f4.w, -m4.z, -m4.w);
         }
-        if (tail) {
+        // E4M3: the powers of two of the key (byte 0 stands for 2^−127, below the normal numbers) and the value row.
+        float ks = 1.f;
+        int kv = -1024;
+        if constexpr (FP8) {
+          ok = mbar_wait_inl(&ms->sc_full[tile % kScaleRing], (tile / kScaleRing) & 1, abort_flag, p.err, site(13)) && ok;
+          const uint32_t sk = ms->k_scale[tile % kScaleRing][kt];
+          ks = sk == 0 ? 5.877471754111438e-39f : __uint_as_float(sk << 23);
+          if (key < w.len) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
+        }
+        if constexpr (FP8) {
+          // This key's value row (two row tiles: the stream's half of it) to fp16, while the scores are made.
+          constexpr int kN = D / 16 / TILES;
+          const int buf = TILES == 1 ? g : tile & 1;
+          const int slot = tile % C::kRV;
+          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, site(11)) && ok;
+          if constexpr (TILES == 1) {
+            if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, site(8)) && ok;
+          } else {
+            ok = mbar_wait_inl(&ms->v16_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, site(12)) && ok;
+          }
+          const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
+          uint8_t* dst = smem + C::kOffV16 + buf * C::kV16 + kt * 128;
+          const int c0 = TILES == 1 ? 0 : g * kN;
+          if (!tail) {
+            widen_row<D, kN, false>(src, dst, kt, c0, false, false);
+          } else if (widen_row<D, kN, true>(src, dst, kt, c0, key >= context, key >= w.len) && key < w.len) {
+            atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
+          }
+          fence_proxy_async_smem();
+          if constexpr (TILES == 2) mbar_arrive(&ms->v16_full[buf]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
+        }
+        ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, site(7)) && ok;
+        tc_fence_after();
+        // x = score − reference, masked to −∞ where the row does not see the key.
+        float x[NR];
+        auto scores = [&](bool relative) {
+          // 16 rows at a time, the next ones on their way from TMEM meanwhile.
+          constexpr int kC = 16;
+          uint32_t hi[2][kC], lo[2][kC];
+          tmem_ld(s_addr, hi[0]);
+          if constexpr (FP8) tmem_ld(s_addr + NR, lo[0]);  // the columns of q's second terms
+#pragma unroll
+          for (int c = 0; c < NR; c += kC) {
+            const int now = (c / kC) & 1;
+            tmem_wait_ld();
+            reg_fence(hi[now]);
+            if constexpr (FP8) reg_fence(lo[now]);
+            if (c + kC < NR) {
+              tmem_ld(s_addr + c + kC, hi[now ^ 1]);
+              if constexpr (FP8) tmem_ld(s_addr + NR + c + kC, lo[now ^ 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < kC; e += 4) {
+              const int n = c + e;
+              float4 r4 = make_float4(__uint_as_float(hi[now][e]), __uint_as_float(hi[now][e + 1]),
+                                      __uint_as_float(hi[now][e + 2]), __uint_as_float(hi[now][e + 3]));
+              float4 f4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+              if constexpr (FP8) {
+                ffma2(r4.x, r4.y, __uint_as_float(lo[now][e]), __uint_as_float(lo[now][e + 1]), 0.0625f, 0.0625f, r4.x,
+                      r4.y);
+                ffma2(r4.z, r4.w, __uint_as_float(lo[now][e + 2]), __uint_as_float(lo[now][e + 3]), 0.0625f, 0.0625f,
+                      r4.z, r4.w);
+                f4 = *reinterpret_cast<const float4*>(&f_row[n]);
+                fmul2(f4.x, f4.y, f4.x, f4.y, ks, ks);
+                fmul2(f4.z, f4.w, f4.z, f4.w, ks, ks);
+              }
+              const float4 m4 =
+                  relative ? *reinterpret_cast<const float4*>(&m_ref[n]) : make_float4(0.f, 0.f, 0.f, 0.f);
+              ffma2(x[n], x[n + 1], r4.x, r4.y, f4.x, f4.y, -m4.x, -m4.y);
+              ffma2(x[n + 2], x[n + 3], r4.z, r4.w, f4.z, f4.w, -m4.z, -m4.w);
+            }
+          }
+          if (tail) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+              if (!((seen >> n) & 1)) x[n] = -INFINITY;
+          }
+        };
+        scores(true);
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int n = 4; n < NR; n += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = n + 4 + e < NR ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NR]) : fmaxf(mx[e], x[n + e]);
+        const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        const bool over = top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
+        if (named_any(bar, 128, over || !ok)) {
+          // A reference moves (the first tile always does): exchange the tile's maxima, rescale ℓ and O.
+          if (named_any(bar, 128, !ok)) {
+            ok = false;
+            break;
+          }
+          scores(false);
+          reduce_cols<NR>(x, lane, OpMax(), ms->red[g][warp & 3]);
+          if constexpr (FP8) {
+            const int top_kv = __reduce_max_sync(0xffffffffu, kv);
+            if (lane == 0) ms->kv_red[g][warp & 3] = top_kv;
+          }
+          named_sync(bar, 128);
+          int kv_new = kv_ref;
+          if constexpr (FP8) {
+            const int* kr = ms->kv_red[g];
+            kv_new = max(kv_ref, max(max(kr[0], kr[1]), max(kr[2], kr[3])));
+          }
+          if (kt < NR) {
+            const float old = m_ref[kt];
+            const float now = fmaxf(fmaxf(ms->red[g][0][kt], ms->red[g][1][kt]), fmaxf(ms->red[g][2][kt], ms->red[g][3][kt]));
+            const bool up = now > -INFINITY && now - kBase > old;
+            corr[kt] = up ? exp2f(old - (now - kBase)) : 1.f;  // 0 from −∞: nothing was summed yet
+            if (up) m_ref[kt] = now - kBase;
+          }
+          named_sync(bar, 128);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) l[n] *= corr[n];
+          if (done > 0) {
+            ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, site(8)) && ok;
+            tc_fence_after();
+            const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
+            rescale_cols<NR>(o_addr, corr, kf);
+            if constexpr (C::kTerms == 2) rescale_cols<NR>(o_addr + NR, corr, kf);
+          }
+          kv_ref = kv_new;
+          scores(true);
+          // A row that has seen nothing has the reference −∞, and only masked scores: −∞ − (−∞) is −∞ here.
 #pragma unroll
           for (int n = 0; n < NR; ++n)
-            if (!((seen >> n) & 1)) x[n] = -INFINITY;
+            if (m_ref[n] == -INFINITY) x[n] = -INFINITY;
         }
-      };
-      scores(true);
-      float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int n = 4; n < NR; n += 4)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[n + i]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool over = top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
-      if (named_any(1, 128, over || !ok)) {
-        // A reference moves (the first tile always does): exchange the tile's maxima, rescale ℓ and O.
-        if (named_any(1, 128, !ok)) {
-          ok = false;
-          break;
-        }
-        scores(false);
-        const int col = reduce_cols<NR>(x, lane, OpMax());
-        if (NR >= 32 || !(lane & 1)) {
-#pragma unroll
-          for (int i = 0; i < (NR >= 32 ? NR / 32 : 1); ++i) ms->red[warp][col + i] = x[i];
-        }
-        if constexpr (FP8) {
-          const int top_kv = __reduce_max_sync(0xffffffffu, kv);
-          if (lane == 0) ms->kv_red[warp] = top_kv;
-        }
-        named_sync(1, 128);
-        int kv_new = kv_ref;
-        if constexpr (FP8)
-          kv_new = max(kv_ref, max(max(ms->kv_red[0], ms->kv_red[1]), max(ms->kv_red[2], ms->kv_red[3])));
-        if (tid < NR) {
-          const float old = ms->m[tid];
-          const float now = fmaxf(fmaxf(ms->red[0][tid], ms->red[1][tid]), fmaxf(ms->red[2][tid], ms->red[3][tid]));
-          const bool up = now > -INFINITY && now - kBase > old;
-          ms->corr[tid] = up ? exp2f(old - (now - kBase)) : 1.f;  // 0 from −∞: nothing was summed yet
-          if (up) ms->m[tid] = now - kBase;
-        }
-        named_sync(1, 128);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) l[n] *= ms->corr[n];
-        if (j > 0) {
-          ok = mbar_wait(&ms->p_free, (j - 1) & 1, abort_flag, p.err, site(8));
-          tc_fence_after();
-          const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
-          constexpr int W = NR < 32 ? NR : 32;
-#pragma unroll
-          for (int cc = 0; cc < NR; cc += W) {
-            uint32_t r[W];
-            const uint32_t oa = tmem + lane_base + C::kColO + cc;
-            if constexpr (W == 32) tmem_ld32(oa, r); else tmem_ld16(oa, r);
-            tmem_wait_ld();
-            reg_fence(r);
-#pragma unroll
-            for (int i = 0; i < W; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (ms->corr[cc + i] * kf));
-            if constexpr (W == 32) tmem_st32(oa, r); else tmem_st16(oa, r);
-          }
-          tmem_wait_st();
-        }
-        kv_ref = kv_new;
-        scores(true);
-        // A row that has seen nothing has the reference −∞, and only masked scores: −∞ − (−∞) is −∞ here.
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-          if (ms->m[n] == -INFINITY) x[n] = -INFINITY;
-      }
-      tc_fence_before();
-      mbar_arrive(&ms->s_free[j & 1]);
+        tc_fence_before();
+        mbar_arrive(&ms->s_free[g]);
 
+        // P̃'s buffer is free once the product of the stream's tile before has run.
+        if ((!FP8 || TILES == 2) && u > 0)
+          ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, site(8)) && ok;
+        // E4M3: the value row's scale relative to the running maximum, a power of two, at most 2^kKvLazy.
+        const float wv = !FP8 ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
+        uint8_t* prow = smem + C::kOffP + g * C::kP + kt * 128;
 #pragma unroll
-      for (int n = 0; n < NR; n += 2) {
-        x[n] = ex2_approx(x[n]);
-        x[n + 1] = ex2_approx(x[n + 1]);
-        fadd2(l[n], l[n + 1], l[n], l[n + 1], x[n], x[n + 1]);
-      }
-      // P̃ᵀ in the matrix type, 8 rows per 16-byte chunk.
-      uint32_t hi[NR / 2], lo[FP8 ? 1 : NR / 2];
-      if constexpr (FP8) {
-        // The value row's scale relative to the running maximum: a power of two, at most 2^kKvLazy.
-        const float w = kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
+        for (int ch = 0; ch < NR / 8; ++ch) {  // 8 rows per 16-byte chunk
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int n = 0; n < NR; n += 2) {
-          float a, d;
-          fmul2(a, d, x[n], x[n + 1], w, w);
-          hi[n / 2] = pack_f16x2(a, d);
+          for (int e = 0; e < 4; ++e) {
+            const int n = ch * 8 + e * 2;
+            x[n] = ex2_approx(x[n]);
+            x[n + 1] = ex2_approx(x[n + 1]);
+            fadd2(l[n], l[n + 1], l[n], l[n + 1], x[n], x[n + 1]);
+            if constexpr (FP8) {
+              float a, d;
+              fmul2(a, d, x[n], x[n + 1], wv, wv);
+              hi[e] = pack_f16x2(a, d);
+            } else {
+              hi[e] = pack_bf16x2(x[n], x[n + 1]);
+              if constexpr (C::kTerms == 2)
+                lo[e] = pack_bf16x2(x[n] - __uint_as_float(hi[e] << 16), x[n + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+            }
+          }
+          *reinterpret_cast<uint4*>(prow + ((ch ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if constexpr (C::kTerms == 2) {
+            const int c2 = ch + NR / 8;  // column chunk of the second term
+            *reinterpret_cast<uint4*>(prow + (c2 >> 3) * kPBlock + (((c2 & 7) ^ (kt & 7)) << 4)) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
-      } else {
+        if (!FP8 && tail && key >= context && (TILES == 1 || g == 0)) {
+          // This key's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
+          // (Two row tiles: the first stream does it for both, its product is issued first.)
+          const int slot = tile % C::kRV;
+          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, site(9)) && ok;
+          uint8_t* vt = smem + C::kOffV + slot * kSlot;
+          bool bad = false;
 #pragma unroll
-        for (int n = 0; n < NR; n += 2) {
-          hi[n / 2] = pack_bf16x2(x[n], x[n + 1]);
-          lo[n / 2] = pack_bf16x2(x[n] - __uint_as_float(hi[n / 2] << 16),
-                                  x[n + 1] - __uint_as_float(hi[n / 2] & 0xffff0000u));
+          for (int kb = 0; kb < D / 64; ++kb) {
+            uint8_t* vr = kPg5 ? vt + (kt >> 3) * 2048 + kb * 1024 + (kt & 7) * 128 : vt + kt * 128;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              uint4* at = reinterpret_cast<uint4*>(vr + q * 16);
+              uint32_t v4[4] = {0, 0, 0, 0};
+              if (key < w.len) {
+                const uint4 v = *at;
+                v4[0] = v.x, v4[1] = v.y, v4[2] = v.z, v4[3] = v.w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((v4[e] & 0x7f80u) == 0x7f80u) v4[e] &= 0xffff0000u, bad = true;
+                  if ((v4[e] & 0x7f800000u) == 0x7f800000u) v4[e] &= 0xffffu, bad = true;
+                }
+              }
+              *at = make_uint4(v4[0], v4[1], v4[2], v4[3]);
+            }
+          }
+          if (bad) atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
         }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&ms->p_full[g]);
       }
-      // P̃'s buffer is free once the product of the tile before has run.
-      if (j > 0) ok = mbar_wait(&ms->p_free, (j - 1) & 1, abort_flag, p.err, site(8)) && ok;
-      uint8_t* prow = smem + C::kOffP + tid * 128;
+      tile0 += n_tiles;
+      used += done;
+      // ------------------------------------------------------------ end of the piece
+      // (Its barriers are joined by all threads whatever the waits said.)
+      if (done > 0) ok = ok && mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, site(10));
+      reduce_cols<NR>(l, lane, OpAdd(), ms->red[g][warp & 3]);
+      if (kt == 0) ms->kv_ref[g] = kv_ref;
+      tc_fence_before();
+      named_sync(TILES == 1 ? 3 : bar, TILES == 1 ? 256 : 128);
+      tc_fence_after();
+      const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+      // The slot of a piece: numbered along the line, or two per part (a part has a piece at each end at most).
+      const long long pair = static_cast<long long>(w.b) * p.Hkv + w.h;
+      const long long slot = p.slots_by_pair ? pair + part : 2ll * part + (w.t0 > 0 ? 0 : 1);
+      if (kt < NR) {
+        // Both streams' sums in a fixed order: the same result every time.
+        float m = -INFINITY, sum = 0.f, wgt[2] = {0.f, 0.f};
+        if constexpr (TILES == 1) m = fmaxf(ms->m[0][kt], ms->m[1][kt]); else m = m_ref[kt];
 #pragma unroll
-      for (int ch = 0; ch < NR / 8; ++ch) {
-        *reinterpret_cast<uint4*>(prow + ((ch ^ (tid & 7)) << 4)) =
-            make_uint4(hi[4 * ch], hi[4 * ch + 1], hi[4 * ch + 2], hi[4 * ch + 3]);
-        if constexpr (!FP8)
-          *reinterpret_cast<uint4*>(prow + kPBlock + ((ch ^ (tid & 7)) << 4)) =
-              make_uint4(lo[4 * ch], lo[4 * ch + 1], lo[4 * ch + 2], lo[4 * ch + 3]);
+        for (int e = 0; e < 2; ++e) {
+          if (TILES == 2 && e != g) continue;
+          const float s = (ms->red[e][0][kt] + ms->red[e][1][kt]) + (ms->red[e][2][kt] + ms->red[e][3][kt]);
+          wgt[e] = s == 0.f ? 0.f : exp2f(ms->m[e][kt] - m);
+          sum += s * wgt[e];
+        }
+        const int64_t r = ms->row[g][kt];
+        if (ok && r >= 0 && (TILES == 2 || g == 0)) {
+          if (!whole) {
+            float* ml = p.part_ml + (slot * p.T * p.G + my_row0 + kt) * 2;
+            ml[0] = m;
+            ml[1] = sum;
+          } else if (p.lse != nullptr) {
+            p.lse[r] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+        // What the streams' O is multiplied by.
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (e == g)
+            ms->lsum[e][kt] =
+                wgt[e] * inv * (FP8 ? exp2f(static_cast<float>(max(ms->kv_ref[e], -300))) : 1.f);
       }
-      if (!FP8 && tail && key >= context) {
-        // This key's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
-        const int slot = j % C::kRV;
-        ok = mbar_wait(&ms->v_full[slot], (j / C::kRV) & 1, abort_flag, p.err, site(9)) && ok;
-        uint8_t* vt = smem + C::kOffV + slot * kSlot;
-        bool bad = false;
+      if (w.t0 == 0 && rt == 0 && tid == 0) {
+        // For the joining kernel: the pair's first part and how many parts it lies in.
+        const long long start = static_cast<long long>(part) * per + (count - w.left - (w.t1 - w.t0));
+        p.pieces[pair] = make_int2(part, static_cast<int>((start + w.tiles - 1) / per) - part + 1);
+      }
+      named_sync(TILES == 1 ? 3 : bar, TILES == 1 ? 256 : 128);
+      const uint32_t* bad = ms->bad[w.index % kBadRing];
+      bool any_bad = false;
+      for (int e = 0; e < 8; ++e) any_bad = any_bad || bad[e] != 0;
+      // Rows of this group: half of the shared ones, or its own, 16 or 32 at a time.
+      constexpr int kOut = TILES == 1 ? NR / 2 : NR;
+      constexpr int kStep = kOut < 32 ? kOut : 32;
+      if (__all_sync(0xffffffffu, ok) && kt < D) {
 #pragma unroll
-        for (int kb = 0; kb < D / 64; ++kb) {
-          uint8_t* vr = vt + (kPg5 ? (tid >> 3) * 2048 + kb * 1024 + (tid & 7) * 128 : tid * 128);
+        for (int cc = 0; cc < kOut; cc += kStep) {
+          const int c0 = (TILES == 1 ? g * kOut : 0) + cc;
+          float o[kStep];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint4* at = reinterpret_cast<uint4*>(vr + q * 16);
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (key < kend) {
-              const uint4 v = *at;
-              w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+          for (int e = 0; e < kStep; ++e) o[e] = 0.f;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, bad = true;
-                if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, bad = true;
+          for (int e = 0; e < 2; ++e) {  // streams
+            if (TILES == 2 && e != g) continue;
+#pragma unroll
+            for (int term = 0; term < C::kTerms; ++term) {
+              uint32_t r[kStep];
+              tmem_ld(tmem + lane_base + C::kColO + e * C::kPCols + term * NR + c0, r);
+              tmem_wait_ld();
+              reg_fence(r);
+#pragma unroll
+              for (int q = 0; q < kStep; ++q) {
+                const float k = ms->lsum[e][c0 + q];
+                if (k != 0.f) o[q] += __uint_as_float(r[q]) * k;  // 0: a stream without keys has left O unwritten
               }
             }
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        }
-        if (bad) atomicOr(&ms->bad[(key - context) >> 5], 1u << ((key - context) & 31));
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(&ms->p_full);
-      sk[0] = sk[1], sk[1] = sk[2];
-      sv[0] = sv[1], sv[1] = sv[2];
-    }
-    // ------------------------------------------------------------ epilogue
-    // (Barrier 1 is joined by all 128 threads whatever the waits said.)
-    ok = ok && mbar_wait(&ms->p_free, (nt - 1) & 1, abort_flag, p.err, site(10));
-    tc_fence_after();
-    {
-      const int col = reduce_cols<NR>(l, lane, OpAdd());
-      if (NR >= 32 || !(lane & 1)) {
+          if (any_bad) {
+            for (int u = 0; u < w.drafts; ++u) {
+              if (!((bad[u >> 5] >> (u & 31)) & 1)) continue;
+              const int key = context + u;
+              const int64_t at = ((static_cast<int64_t>(checked_page(p, w.b, key >> bshift)) * p.Hkv + w.h) * p.block_size +
+                                  (key & (p.block_size - 1))) * D + kt;
+              float v;
+              if (FP8)
+                v = (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
+              else
+                v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
+              if (fabsf(v) <= 3.4028234663852886e38f) continue;
 #pragma unroll
-        for (int i = 0; i < (NR >= 32 ? NR / 32 : 1); ++i) ms->red[warp][col + i] = l[i];
-      }
-    }
-    named_sync(1, 128);
-    if (tid < NR) {  // fixed order: the same sums every time
-      const float sum = (ms->red[0][tid] + ms->red[1][tid]) + (ms->red[2][tid] + ms->red[3][tid]);
-      const int64_t r = ms->row[tid];
-      const bool live = tid < live_rows;
-      if (ok && r >= 0) {
-        const float m = live ? ms->m[tid] : -INFINITY;
-        const float s = live ? sum : 0.f;
-        if (p.n_splits > 1) {
-          p.part_ml[(r * p.n_splits + c) * 2 + 0] = m;
-          p.part_ml[(r * p.n_splits + c) * 2 + 1] = s;
-        } else if (p.lse != nullptr) {
-          p.lse[r] = s != 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
-        }
-      }
-      ms->corr[tid] = live && sum != 0.f ? 1.f / sum : 0.f;
-    }
-    named_sync(1, 128);
-    const bool mine = __all_sync(0xffffffffu, ok) && tid < D;
-    if (__any_sync(0xffffffffu, mine)) {
-      const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref, -300))) : 1.f;
-      bool any_bad = false;
-      for (int i = 0; i < 8; ++i) any_bad = any_bad || ms->bad[i] != 0;
-      constexpr int W = NR < 32 ? NR : 32;
+              for (int q = 0; q < kStep; ++q)
+                if (c0 + q < live && sees(c0 + q, u)) o[q] += v;
+            }
+          }
 #pragma unroll
-      for (int cc = 0; cc < NR; cc += W) {
-        uint32_t r[W];
-        if constexpr (W == 32) tmem_ld32(tmem + lane_base + C::kColO + cc, r);
-        else tmem_ld16(tmem + lane_base + C::kColO + cc, r);
-        tmem_wait_ld();
-        reg_fence(r);
-        if (any_bad) {
-          for (int u = 0; u < drafts; ++u) {
-            if (!((ms->bad[u >> 5] >> (u & 31)) & 1)) continue;
-            const int key = context + u;
-            const int64_t at =
-                ((static_cast<int64_t>(page_id(key)) * p.Hkv + hkv) * p.block_size + key % p.block_size) * D + tid;
-            float v;
-            if (FP8)
-              v = (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
-            else
-              v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
-            if (fabsf(v) <= 3.4028234663852886e38f) continue;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const int t = ms->token[cc + i];
-              if (t < drafts &&
-                  (p.mask != nullptr ? p.mask[b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t))
-                r[i] = __float_as_uint(__uint_as_float(r[i]) + v);
+          for (int q = 0; q < kStep; ++q) {
+            if (ms->row[g][c0 + q] >= 0) {
+              if (!whole)
+                p.part_o[(slot * p.T * p.G + my_row0 + c0 + q) * D + kt] = o[q];
+              else
+                static_cast<__nv_bfloat16*>(p.o)[ms->o_off[g][c0 + q] + kt] = __float2bfloat16_rn(o[q]);
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const int n = cc + i;
-          const int64_t row = ms->row[n];
-          if (row >= 0) {
-            const float f = ms->corr[n];
-            const float o = f != 0.f ? __uint_as_float(r[i]) * f * kf : 0.f;
-            if (p.n_splits > 1)
-              p.part_o[(row * p.n_splits + c) * D + tid] = o;
-            else
-              static_cast<__nv_bfloat16*>(p.o)[ms->o_off[n] + tid] = __float2bfloat16_rn(o);
-          }
-        }
       }
-    }
-  } else if constexpr (FP8) {
-    // ------------------------------------------ converters: one value row per thread
-    const int r = tid - 192;
-    for (int j = 0; j < nt; ++j) {
-      const int slot = j % C::kRV;
-      bool ok = mbar_wait(&ms->v_full[slot], (j / C::kRV) & 1, abort_flag, p.err, site(11)) &&
-                mbar_wait(&ms->v16_empty[j & 1], ((j >> 1) & 1) ^ 1, abort_flag, p.err, site(12));
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int key = key0 + j * kBN + r;
-      const uint8_t* src = smem + C::kOffV + slot * kSlot + r * D;
-      uint8_t* dst = smem + C::kOffV16 + (j & 1) * C::kV16 + r * 128;
-      bool bad = false;
-#pragma unroll
-      for (int ch = 0; ch < D / 16; ++ch) {
-        const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
-        const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        if (key >= context) {  // drafted keys: NaN codes out; past the end: everything out
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (((w[i] >> (8 * q)) & 0x7f) == 0x7f) w[i] &= ~(0xffu << (8 * q)), bad = key < kend;
-            if (key >= kend) w[i] = 0;
-          }
-        }
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = e4m3x2_to_f16x2(w[i >> 1] >> (16 * (i & 1)));
-        uint8_t* half = dst + (ch >> 2) * kBN * 128;  // 64 elements per 128-byte row
-        *reinterpret_cast<uint4*>(half + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(half + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      if (bad) atomicOr(&ms->bad[(key - context) >> 5], 1u << ((key - context) & 31));
-      fence_proxy_async_smem();
-      mbar_arrive(&ms->v16_full[j & 1]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
+      tc_fence_before();
+      // All have read O and the statistics; any failed wait ends the walk for all.
+      ok = !named_any(TILES == 1 ? 3 : bar, TILES == 1 ? 256 : 128, !ok);
+      // The flags of three pieces ago: the other stream may still be at the piece before.
+      if (tid < 8) ms->bad[(w.index + kBadRing - 3) % kBadRing][tid] = 0;
+    } while (ok && w.next());
+  } else {
+    reg_dealloc<kRegsOther>();
+    // ------------------------- Q of every piece but the first, which the streams load
+    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
+    while (w.next()) {
+      // Once the first products of the piece before are done.
+      if (!__all_sync(0xffffffffu, mbar_wait_inl(&ms->q_empty, (w.index & 1) ^ 1, abort_flag, p.err, site(15)))) break;
+      load_q<D, FP8, NR, TILES, 32>(p, w, smem + C::kOffQ, ms->f[w.index % kFRing], row0, lane);
+      mbar_arrive(&ms->q_full);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-// Joins a row's chunks, which hold o_c/ℓ_c: weights w_c = 2^(m_c − m)·ℓ_c, O = Σ w_c (o_c/ℓ_c) / Σ w_c.
-// One warp per row.
+// Joins the pieces of a cut pair, which hold o/ℓ: weights w = 2^(m − max)·ℓ, O = Σ w·(o/ℓ) / Σ w.  Rows that see
+// nothing are written here too.  One warp per row (b, h, t).
 constexpr int kMergeWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeParams p) {
@@ -811,56 +1051,92 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   const int64_t bh = r / p.T;
   const int h = static_cast<int>(bh % p.Hq);
   const int b = static_cast<int>(bh / p.Hq);
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + r * p.n_splits;
-  float m = -INFINITY;
-  for (int c = 0; c < p.n_splits; ++c) m = fmaxf(m, ml[c].x);
-  float l = 0.f, o[E];
+  int len, drafts;
+  seq_lengths(p, b, len, drafts);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + b * p.so[0] + h * p.so[1] + t * p.so[2] + lane * E;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int c = 0; c < p.n_splits; ++c) {
-    const float2 x = ml[c];
-    if (x.y == 0.f) continue;
-    const float w = exp2f(x.x - m) * x.y;
-    l += w;
+  float m = -INFINITY, l = 0.f;
+  if (t < drafts) {
+    const int64_t pair = static_cast<int64_t>(b) * p.Hkv + h / p.G;
+    const int2 pieces = p.pieces[pair];
+    if (pieces.y == 1) return;  // not cut: the first kernel has written it
+    const int64_t rows = static_cast<int64_t>(p.T) * p.G;
+    const int64_t rr = static_cast<int64_t>(t) * p.G + h % p.G;
+    auto slot = [&](int i) -> int64_t {
+      return p.slots_by_pair ? pair + pieces.x + i : 2ll * (pieces.x + i) + (i > 0 ? 0 : 1);
+    };
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    for (int i = 0; i < pieces.y; ++i) m = fmaxf(m, ml[slot(i) * rows + rr].x);
+#pragma unroll 4
+    for (int i = 0; i < pieces.y; ++i) {
+      const float2 x = ml[slot(i) * rows + rr];
+      const float* src = p.part_o + (slot(i) * rows + rr) * D + lane * E;
+      float v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += w * p.part_o[(r * p.n_splits + c) * D + lane * E + e];
+      for (int e = 0; e < E; ++e) v[e] = src[e];
+      if (x.y == 0.f) continue;
+      const float w = exp2f(x.x - m) * x.y;
+      l += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += w * v[e];
+    }
   }
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + b * p.so[0] + h * p.so[1] + t * p.so[2] + lane * E;
   const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16_rn(l != 0.f ? o[e] * inv : 0.f);
   if (p.lse != nullptr && lane == 0) p.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D, bool FP8, int NR>
-cudaError_t launch_rows(const TreeParams& p, int64_t blocks, cudaStream_t s) {
-  constexpr int kSmem = Cfg<D, FP8, NR>::kOffMisc + static_cast<int>(sizeof(Misc<NR>)) + 1024;
+template <int D, bool FP8, int NR, int TILES>
+cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
+  constexpr int kSmem = Cfg<D, FP8, NR, TILES>::kOffMisc + static_cast<int>(sizeof(Misc<NR>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  cudaError_t e =
-      cudaFuncSetAttribute(tree_kernel<D, FP8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  using M = Misc<NR>;
+  static_assert(Cfg<D, FP8, NR, TILES>::kOffMisc % 16 == 0 && offsetof(M, m) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
+                    offsetof(M, k_scale) % 16 == 0 && offsetof(M, v_scale) % 16 == 0,
+                "16-byte accesses and bulk copies");
+  // The register split draws on what the block was launched with.
+  cudaFuncAttributes a;
+  cudaError_t e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR, TILES>);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, FP8, NR><<<static_cast<unsigned>(blocks), Cfg<D, FP8, NR>::kThreads, kSmem, s>>>(p);
+  if (a.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  tree_kernel<D, FP8, NR, TILES><<<static_cast<unsigned>(p.parts) * p.row_tiles, kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool FP8>
 cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
-  const int64_t blocks = static_cast<int64_t>(p.B) * p.Hkv * p.n_splits * p.row_tiles;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaError_t e = p.tile_rows == 16   ? launch_rows<D, FP8, 16>(p, blocks, s)
-                  : p.tile_rows == 32 ? launch_rows<D, FP8, 32>(p, blocks, s)
-                                      : launch_rows<D, FP8, 64>(p, blocks, s);
-  if (e != cudaSuccess || p.n_splits == 1) return e;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.T;
-  tree_merge_kernel<D><<<static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  const int64_t rows = static_cast<int64_t>(p.T) * p.G;
+  cudaError_t e = rows <= 16   ? launch_rows<D, FP8, 16, 1>(p, s)
+                  : rows <= 32 ? launch_rows<D, FP8, 32, 1>(p, s)
+                  : rows <= 64 ? launch_rows<D, FP8, 64, 1>(p, s)
+                               : launch_rows<D, FP8, 64, 2>(p, s);
+  if (e != cudaSuccess) return e;
+  // The joining kernel's blocks may come up while the first kernel runs; they wait for its end.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.B) * p.Hq * p.T + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p);
 }
 
 }  // namespace
 
-int tree_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int tree_cta_rows(int64_t rows) { return rows <= 64 ? 64 : 128; }
 
 cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s) {
+  if (static_cast<int64_t>(p.B) * p.Hq * p.T > (1ll << 32) || static_cast<int64_t>(p.parts) * p.row_tiles > 0x7fffffff)
+    return cudaErrorInvalidValue;
   if (d == 128) return fp8 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
   if (d == 64) return fp8 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
   return cudaErrorInvalidValue;

@@ -44,7 +44,6 @@ EXPORTED = (
     "fa_rope",
     "fa_cache_append",
     "fa_cache_gather",
-    "fa_decode_tree_choose_splits",
     "fa_decode_tree_workspace_size",
     "fa_decode_tree",
     "fa_device_status",
@@ -106,9 +105,7 @@ def lib() -> ctypes.CDLL:
         L.fa_cache_append.restype = i32
         L.fa_cache_gather.argtypes = [vp] * 8 + [i32] * 8 + [vp, vp]
         L.fa_cache_gather.restype = i32
-        L.fa_decode_tree_choose_splits.argtypes = [i32] * 5
-        L.fa_decode_tree_choose_splits.restype = i32
-        L.fa_decode_tree_workspace_size.argtypes = [i32] * 5
+        L.fa_decode_tree_workspace_size.argtypes = [i32] * 6
         L.fa_decode_tree_workspace_size.restype = sz
         L.fa_decode_tree.argtypes = [vp] * 9 + [ctypes.c_int64, vp, vp] + [i32] * 9 + [f32, vp, i32, vp, sz, vp]
         L.fa_decode_tree.restype = i32
@@ -709,28 +706,22 @@ def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, 
     return out_k, out_v
 
 
-def decode_tree_workspace_size(B: int, Hq: int, T: int, d: int, n_splits: int) -> int:
-    return int(lib().fa_decode_tree_workspace_size(B, Hq, T, d, n_splits))
-
-
-def decode_tree_choose_splits(B: int, Hq: int, Hkv: int, T: int, Nkv: int) -> int:
-    """The library's split count for ``decode_tree`` over sequences of up to Nkv keys."""
-    s = int(lib().fa_decode_tree_choose_splits(B, Hq, Hkv, T, Nkv))
-    if s <= 0:
-        raise FAError(FA_ERR_INVALID_ARG, f"no split count for B={B} Hq={Hq} Hkv={Hkv} T={T} Nkv={Nkv}")
-    return s
+def decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, d: int, max_parts: int = 0) -> int:
+    """Workspace bytes with which ``decode_tree`` uses the whole current device (or at most ``max_parts`` CTAs)."""
+    return int(lib().fa_decode_tree_workspace_size(B, Hq, Hkv, T, d, max_parts))
 
 
 def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draft_lens=None, k_scale=None,
-                v_scale=None, n_splits: int | None = None, scale: float | None = None, out=None, lse=None,
-                workspace=None, stream=None):
+                v_scale=None, max_parts: int = 0, scale: float | None = None, out=None, lse=None, workspace=None,
+                stream=None):
     """Attention of T drafted tokens per sequence over a paged cache (T = 1: plain decode); returns (O, LSE).
 
     q [B,Hq,T,d] bf16 (strided or not).  The drafted tokens' keys are in the cache: seq_lens[b] counts them, and the
     last draft_lens[b] (int32 [B]; None: T) keys of sequence b are theirs.  Token t sees the context before them and
     drafted key u where tree_mask[b, t, u] (bool or uint8 [B,T,T] or [T,T]; None: u <= t).  Rows that see nothing,
     padding rows t >= draft_lens[b] among them, give O = 0 and LSE = −inf.  The cache is bfloat16, or float8_e4m3fn
-    with k_scale/v_scale as ``cache_append`` writes it.  O like q (contiguous), LSE fp32 [B,Hq,T].
+    with k_scale/v_scale as ``cache_append`` writes it.  O like q (contiguous), LSE fp32 [B,Hq,T].  The work is cut
+    into equal parts over the machine (at most ``max_parts``, 0: no limit), fewer where a given workspace is small.
     """
     torch = _torch()
     dev = _device_of(q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, k_scale, v_scale, out, lse,
@@ -751,8 +742,6 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
         if tuple(tree_mask.shape) not in ((T, T), (B, T, T)) or (T > 1 and tree_mask.stride()[-2:] != (T, 1)):
             raise ValueError("tree_mask must be [T, T] or [B, T, T] with contiguous rows")
         mask_sb = tree_mask.stride(0) if tree_mask.dim() == 3 and B > 1 else 0
-    if n_splits is None:
-        n_splits = decode_tree_choose_splits(B, Hq, hkv, T, block_table.shape[1] * bs)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     with _on(dev, stream):
@@ -767,13 +756,13 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
             if not lse.is_contiguous():
                 raise ValueError("lse must be contiguous")
         if workspace is None:
-            workspace = torch.empty(max(decode_tree_workspace_size(B, Hq, T, d, n_splits), 16), dtype=torch.uint8,
+            workspace = torch.empty(max(decode_tree_workspace_size(B, Hq, hkv, T, d, max_parts), 16), dtype=torch.uint8,
                                     device=dev)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         _check(lib().fa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
                                     _addr(v_scale), block_table.data_ptr(), seq_lens.data_ptr(), _addr(draft_lens),
                                     _addr(tree_mask), mask_sb, out.data_ptr(), lse.data_ptr(), B, Hq, hkv, T, nb, bs,
-                                    block_table.shape[1], d, code, float(scale), _strides(q, out), int(n_splits),
+                                    block_table.shape[1], d, code, float(scale), _strides(q, out), int(max_parts),
                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr()))
     return out, lse

@@ -93,10 +93,10 @@ def test_cache_gather_refuses(L, kw, status):
 
 @pytest.mark.parametrize("kw,status", CACHE_BAD + [
     (dict(q=None), INV), (dict(o=None), INV), (dict(lens=None), INV), (dict(ws=None), INV), (dict(Hq=0), INV),
-    (dict(T=0), INV), (dict(ns=0), INV), (dict(Hq=30), INV), (dict(Hq=516), UNS), (dict(T=257), UNS),
-    (dict(ns=257), UNS), (dict(scale=0.0), INV), (dict(scale=float("nan")), INV), (dict(q=FAKE + 8), INV),
+    (dict(T=0), INV), (dict(ns=-1), INV), (dict(Hq=30), INV), (dict(Hq=516), UNS), (dict(T=257), UNS),
+    (dict(ns=4097), UNS), (dict(scale=0.0), INV), (dict(scale=float("nan")), INV), (dict(q=FAKE + 8), INV),
     (dict(o=FAKE + 8), INV), (dict(ws=FAKE + 8), INV), (dict(lse=FAKE + 2), INV), (dict(dl=FAKE + 2), INV),
-    (dict(mask=FAKE, msb=3), INV), (dict(wsb=64), INV), (dict(st=_st(4096, 1024, 128, 4096, 1024, 4)), INV),
+    (dict(mask=FAKE, msb=3), INV), (dict(wsb=63), INV), (dict(st=_st(4096, 1024, 128, 4096, 1024, 4)), INV),
     (dict(st=_st(0, 1024, 128, 0, 1024, 128)), INV)])
 def test_decode_tree_refuses(L, kw, status):
     a = dict(q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, table=FAKE, lens=FAKE, dl=None, mask=None, msb=0, o=FAKE,
@@ -109,16 +109,18 @@ def test_decode_tree_refuses(L, kw, status):
     assert b"fa_decode_tree" in L.fa_get_last_error()
 
 
-def test_decode_tree_workspace_and_splits(L):
-    slots = 2 * 28 * 8 * 3
-    assert L.fa_decode_tree_workspace_size(2, 28, 8, 128, 3) >= slots * 130 * 4
-    assert L.fa_decode_tree_workspace_size(0, 28, 8, 128, 3) == 0
-    assert L.fa_decode_tree_workspace_size(2, 28, 8, 128, 0) == 0
-    for B, Hq, Hkv, T, N in ((1, 28, 4, 5, 777), (64, 28, 4, 1, 8192), (1, 1, 1, 1, 1 << 20), (8, 32, 8, 64, 32768)):
-        assert 1 <= L.fa_decode_tree_choose_splits(B, Hq, Hkv, T, N) <= 256
-    assert L.fa_decode_tree_choose_splits(1, 28, 4, 1, 100) == 1      # a short sequence is not split
-    assert L.fa_decode_tree_choose_splits(1, 28, 5, 1, 100) == 0
-    assert L.fa_decode_tree_choose_splits(1, 28, 4, 0, 100) == 0
+def test_decode_tree_workspace(L):
+    size = L.fa_decode_tree_workspace_size
+    # one part: a pair of words per (sequence, key/value head) and no pieces
+    assert size(2, 28, 4, 8, 128, 1) == 256
+    # three parts of eight pairs: two slots per part beat 8 + 2; of 7·8 rows, 128 values and (m, ℓ)
+    assert size(2, 28, 4, 8, 128, 3) == 256 + 6 * 56 * 128 * 4 + -(-6 * 56 * 8 // 256) * 256
+    # three parts of one pair: slots 0, 1, 2
+    assert size(1, 4, 1, 1, 64, 3) == 256 + 3 * 4 * 64 * 4 + 256
+    assert size(2, 28, 4, 8, 128, 0) == size(2, 28, 4, 8, 128, 152)         # no device here: 152 SMs
+    assert size(1, 8, 1, 64, 128, 0) == size(1, 8, 1, 64, 128, 152 // 4)    # 512 rows: four CTAs of 128 per part
+    for bad in ((0, 28, 4, 8, 128, 0), (2, 28, 5, 8, 128, 0), (2, 28, 4, 0, 128, 0), (2, 28, 4, 8, 128, -1)):
+        assert size(*bad) == 0
 
 
 def test_binding_refuses_host_tensors():

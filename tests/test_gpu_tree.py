@@ -31,7 +31,7 @@ def _mask(m):
     return None if m is None else torch.from_numpy(m).cuda()
 
 
-def _run(seed, lens, Hq, hkv, T, d, bs, cache, mask=None, drafts=None, splits=None, heads=None, q_scale=1.0, edit=None, **kw):
+def _run(seed, lens, Hq, hkv, T, d, bs, cache, mask=None, drafts=None, parts=0, heads=None, q_scale=1.0, edit=None, **kw):
     rng = np.random.default_rng(seed)
     p = Paged(rng, lens, hkv, d, bs, cache, edit=edit)
     q = bf16(rng.standard_normal((len(lens), Hq, T, d)) * q_scale).cuda()
@@ -39,7 +39,7 @@ def _run(seed, lens, Hq, hkv, T, d, bs, cache, mask=None, drafts=None, splits=No
         mask = random_tree(rng, len(lens), T, empty={"tree": 0.0, "holes": 0.4}[mask])
     scale = kw.pop("scale", 1 / math.sqrt(d))
     o, lse = fa.decode_tree(q, *p.args(), tree_mask=_mask(mask), draft_lens=None if drafts is None else _i32(drafts),
-                            n_splits=splits, scale=scale, **p.kw(), **kw)
+                            max_parts=parts, scale=scale, **p.kw(), **kw)
     fa.device_status()
     real = drafts if drafts is not None else [T if n else 0 for n in lens]
     check_tree(o, lse, q, p, real, mask, scale, heads)
@@ -59,14 +59,14 @@ def _run(seed, lens, Hq, hkv, T, d, bs, cache, mask=None, drafts=None, splits=No
     ([300], 2, 1, 130, 16, "holes", None),
     ([256], 1, 1, 256, 128, None, None)])
 def test_tree(cache, d, lens, Hq, hkv, T, bs, mask, drafts):
-    for splits in (None, 1, 3):
-        _run(T * d, lens, Hq, hkv, T, d, bs, cache, mask, drafts, splits, heads=sorted({0, Hq // 2, Hq - 1}))
+    for parts in (0, 1, 3):
+        _run(T * d, lens, Hq, hkv, T, d, bs, cache, mask, drafts, parts, heads=sorted({0, Hq // 2, Hq - 1}))
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
-@pytest.mark.parametrize("splits", [1, 2, 7, 64, 256])
-def test_splits_of_a_long_sequence(cache, splits):
-    _run(5, [4000, 1, 2047], 8, 2, 2, 128, 16, cache, None, [2, 1, 2], splits, heads=[0, 7])
+@pytest.mark.parametrize("parts", [1, 2, 7, 64, 256])
+def test_parts_of_a_long_sequence(cache, parts):
+    _run(5, [4000, 1, 2047], 8, 2, 2, 128, 16, cache, None, [2, 1, 2], parts, heads=[0, 7])
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
@@ -80,7 +80,7 @@ def test_large_scores_and_rising_maxima(cache):
     def rising(name, b, x):
         if name == "k":
             x *= np.linspace(0.1, 3, x.shape[1])[None, :, None]
-    _run(7, [1500, 1000], 4, 2, 4, 128, 32, cache, "tree", splits=2, q_scale=8.0, edit=rising)
+    _run(7, [1500, 1000], 4, 2, 4, 128, 32, cache, "tree", parts=2, q_scale=8.0, edit=rising)
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
@@ -89,7 +89,7 @@ def test_value_rows_of_very_different_size(cache):
         if name == "v":
             x *= np.exp2((np.arange(x.shape[1]) * 37 % 41) - 20.0)[None, :, None]
             x[:, 3] = 0.0
-    _run(8, [700, 513], 4, 2, 3, 128, 16, cache, "tree", splits=3, edit=spread)
+    _run(8, [700, 513], 4, 2, 3, 128, 16, cache, "tree", parts=3, edit=spread)
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
@@ -108,13 +108,13 @@ def test_what_unseen_drafted_keys_hold_does_not_matter(cache, value):
         rng = np.random.default_rng(9)
         p = Paged(rng, [n], 1, 128, 16, cache, edit=poison)
         q = bf16(rng.standard_normal((1, 2, T, 128))).cuda()
-        o, lse = (np64(x) for x in fa.decode_tree(q, *p.args(), tree_mask=_mask(mask), n_splits=2, **p.kw()))
+        o, lse = (np64(x) for x in fa.decode_tree(q, *p.args(), tree_mask=_mask(mask), max_parts=2, **p.kw()))
         assert np.isnan(o[:, :, 4]).all() and not np.isfinite(lse[:, :, 4]).any()
         mask2 = mask.copy()
         mask2[0, 4, 2] = False
         clean = Paged(np.random.default_rng(9), [n], 1, 128, 16, cache,
                       edit=lambda name, b, x: x.__setitem__((slice(None), x.shape[1] - T + 2), 0.0))
-        ro, rl = (np64(x) for x in fa.decode_tree(q, *clean.args(), tree_mask=_mask(mask2), n_splits=2, **clean.kw()))
+        ro, rl = (np64(x) for x in fa.decode_tree(q, *clean.args(), tree_mask=_mask(mask2), max_parts=2, **clean.kw()))
         rows = [0, 1, 2, 3, 5]
         assert np.array_equal(o[:, :, rows], ro[:, :, rows]) and np.array_equal(lse[:, :, rows], rl[:, :, rows])
 
@@ -129,20 +129,36 @@ def test_an_infinite_value_shows_in_its_columns_only():
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_what_is_not_finite_in_the_context_shows_in_every_row(cache):
+    def poison(name, b, x):
+        if b == 0:
+            x[:, 70, 9 if name == "v" else slice(None)] = np.nan if name == "v" else x[:, 70]
+        elif name == "k":
+            x[:, 3, 7] = np.nan
+    rng = np.random.default_rng(17)
+    p = Paged(rng, [300, 200, 250], 2, 128, 16, cache, edit=lambda n, b, x: poison(n, b, x) if b < 2 else None)
+    q = bf16(rng.standard_normal((3, 8, 3, 128))).cuda()
+    o, lse = (np64(t) for t in fa.decode_tree(q, *p.args(), **p.kw()))
+    assert np.isnan(o[0, :, :, 9]).all() and np.isfinite(np.delete(o[0], 9, 2)).all() and np.isfinite(lse[0]).all()
+    assert np.isnan(o[1]).all() and np.isnan(lse[1]).all()
+    assert np.isfinite(o[2]).all() and np.isfinite(lse[2]).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_layouts_masks_and_buffers_agree_bitwise(cache):
     import torch
     T, Hq, lens = 6, 8, [150, 77, 300]
     rng = np.random.default_rng(12)
     mask = random_tree(rng, 1, T)[0]
-    o, lse, q, p = _run(13, lens, Hq, 2, T, 128, 32, cache, np.stack([mask] * 3), splits=3)
-    kw = dict(n_splits=3, **p.kw())
+    o, lse, q, p = _run(13, lens, Hq, 2, T, 128, 32, cache, np.stack([mask] * 3), parts=3)
+    kw = dict(max_parts=3, **p.kw())
     qs = q.transpose(1, 2).contiguous().transpose(1, 2)
     out = torch.full((3, T, Hq, 128), 9.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
     a, b = fa.decode_tree(qs, *p.args(), tree_mask=_mask(mask), out=out, **kw)          # one mask for the batch
     assert a is out and torch.equal(a, o) and torch.equal(b, lse)
     a, b = fa.decode_tree(q, *p.args(), tree_mask=_mask(mask).to(torch.uint8) * 7, **kw)
     assert torch.equal(a, o) and torch.equal(b, lse)
-    ws = torch.full((fa.decode_tree_workspace_size(3, Hq, T, 128, 3),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((fa.decode_tree_workspace_size(3, Hq, 2, T, 128, 3),), 0xFF, dtype=torch.uint8, device="cuda")
     a, b = fa.decode_tree(q, *p.args(), tree_mask=_mask(mask), workspace=ws, **kw)      # NaN bits in the workspace
     assert torch.equal(a, o) and torch.equal(b, lse)
     if cache == "e4m3":
@@ -153,7 +169,7 @@ def test_layouts_masks_and_buffers_agree_bitwise(cache):
 
 def test_chain_of_one_is_the_paged_decode():
     import torch
-    o, lse, q, p = _run(14, [700, 33, 1], 28, 4, 1, 128, 16, "bf16", splits=2)
+    o, lse, q, p = _run(14, [700, 33, 1], 28, 4, 1, 128, 16, "bf16", parts=2)
     ro, rl = fa.decode_paged(q, *p.args(), n_splits=2)
     # two roundings of the same number to bf16, and both kernels' bf16 probabilities: 2·2^-8 relative each
     assert (o.float() - ro.float()).abs().max() <= 4 * 2.0 ** -8 * ro.float().abs().max()
@@ -196,7 +212,7 @@ def test_decode_tree_refuses():
                      (dict(tree_mask=one[:2]), ValueError), (dict(tree_mask=one.t().contiguous().t()), ValueError),
                      (dict(out=q.float()), ValueError), (dict(lse=torch.empty((2, 4), device="cuda")), ValueError),
                      (dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")), fa.FAError),
-                     (dict(q=q[:, :3]), fa.FAError), (dict(n_splits=0), fa.FAError), (dict(n_splits=1000), fa.FAError),
+                     (dict(q=q[:, :3]), fa.FAError), (dict(max_parts=-1), fa.FAError), (dict(max_parts=5000), fa.FAError),
                      (dict(scale=-1.0), fa.FAError), (dict(q=q.cpu()), ValueError),
                      (dict(k_cache=p.k_cache[:, :, ::2]), ValueError)):
         with pytest.raises(err):
