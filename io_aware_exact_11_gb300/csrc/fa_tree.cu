@@ -66,11 +66,7 @@ namespace {
 constexpr int kBN = 128;                 // keys per tile
 constexpr int kPBlock = kBN * 128;       // P̃ᵀ: one 128-byte row per key
 constexpr int kMaxRing = 8;
-constexpr int kThreads = 384;            // warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11
-// Registers per thread at launch and after the warpgroups' split (2·208 + 88 = 3·168): a softmax thread holds its
-// scores and partial sums, 2·NR values, and a spilled one would go to L2, shared memory leaving no L1.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
-static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch && kThreads == 384, "register split");
+constexpr int kMaxThreads = 640;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kScaleRing = 16;           // E4M3: tiles whose scale bytes are staged (V slots and four more)
 constexpr int kFRing = 4;                // pieces whose row factors may be live at once
@@ -79,6 +75,19 @@ constexpr int kBadRing = 8;              // pieces whose flags of bad values may
 // NR rows per stream; TILES = 1: both streams work on the same rows, 2: on two tiles of rows.
 template <int D, bool FP8, int NR, int TILES>
 struct Cfg {
+  // With 64 shared rows a stream has two warpgroups, each with half of the rows: four softmax warps per SM
+  // sub-partition hide one another's waits better than two with twice the rows each.
+  static constexpr int kSub = NR == 64 && TILES == 1 ? 2 : 1;
+  static constexpr int kNC = NR / kSub;                       // rows (TMEM columns) of a softmax thread
+  static constexpr int kSoftmax = 256 * kSub;                 // softmax threads; then warps for K, MMA, V, Q
+  static constexpr int kThreads = kSoftmax + 128;
+  // Registers per thread at launch and after the warpgroups' split.  A softmax thread holds its scores and partial
+  // sums, 2·kNC values, and a spilled one would go to L2, shared memory leaving next to no L1.
+  static constexpr int kRegsLaunch = kSub == 2 ? 96 : 168;
+  static constexpr int kRegsSoftmax = kSub == 2 ? 104 : 208;
+  static constexpr int kRegsOther = kSub == 2 ? 64 : 88;
+  static_assert(2 * kSub * kRegsSoftmax + kRegsOther <= (2 * kSub + 1) * kRegsLaunch && kThreads <= kMaxThreads,
+                "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
   static constexpr int kTerms = !FP8 && TILES == 1 ? 2 : 1;   // of P̃
   static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
@@ -109,18 +118,18 @@ struct Misc {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], v16_full[2], v16_empty[2];
   uint64_t sc_full[kScaleRing], q_full, q_empty, drain;
-  alignas(16) float m[2][NR];          // reference maxima (log2 units), −∞ while a row has seen nothing
+  alignas(16) float nm[2][NR];         // minus the reference maxima (log2 units), +∞ while a row has seen nothing
   alignas(16) float f[kFRing][2][NR];  // E4M3: what a row's raw scores are multiplied by
   float corr[2][NR];                   // factor of the last rescale; in the end what O is multiplied by
   float red[2][4][NR];                 // per-warp maxima or sums
   float lsum[2][NR];
   int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
   int64_t o_off[2][NR];                // its element offset in O
-  int kv_red[2][4], kv_ref[2];
+  int kv_red[2][2][4], kv_ref[2][2];   // per stream and warpgroup
   alignas(16) uint8_t k_scale[kScaleRing][kBN];  // written by bulk copies
   alignas(16) uint8_t v_scale[kScaleRing][kBN];
   uint32_t bad[kBadRing][8];           // drafted keys with non-finite values (one bit each)
-  long long warp_sum[kThreads / 32];
+  long long warp_sum[kMaxThreads / 32];
   int start_b, start_h, start_tile;
   uint32_t tmem_base;
   int abort_flag;
@@ -303,7 +312,7 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const Walk& w, uint8
   using C = Cfg<D, FP8, NR, TILES>;
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
   constexpr int kPer = (TILES * NR * kChunks + NT - 1) / NT;
-  constexpr int kBatch = kPer < 8 ? kPer : 8;  // loads in flight per thread
+  constexpr int kBatch = kPer < 4 ? kPer : 4;  // loads in flight per thread
   const int live = w.drafts * p.G - row0;
 #pragma unroll 1
   for (int i0 = 0; i0 < kPer; i0 += kBatch) {
@@ -369,10 +378,11 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const Walk& w, uint8
 }
 
 template <int D, bool FP8, int NR, int TILES>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, FP8, NR, TILES>;
   constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
-  constexpr int kSlot = C::kSlot;
+  constexpr int kSlot = C::kSlot, kThreads = C::kThreads, kSub = C::kSub;
+  constexpr int kWarp0 = C::kSoftmax / 32;  // first warp after the softmax ones
   // Rescale once a score exceeds the reference by kLazy; the reference is taken kBase below the maximum.
   constexpr float kLazy = FP8 ? 11.f : 8.f;
   constexpr float kBase = FP8 ? 3.f : 0.f;
@@ -398,14 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     for (int s = 0; s < C::kRV; ++s) {
       mbar_init(&ms->v_full[s], 1);
-      mbar_init(&ms->v_empty[s], FP8 ? 4 * TILES : 1);
+      mbar_init(&ms->v_empty[s], FP8 ? 4 * kSub * TILES : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
-      mbar_init(&ms->s_free[s], 128);
-      mbar_init(&ms->p_full[s], 128);
+      mbar_init(&ms->s_free[s], 128 * kSub);
+      mbar_init(&ms->p_full[s], 128 * kSub);
       mbar_init(&ms->p_free[s], 1);
-      mbar_init(&ms->v16_full[s], 256);
+      mbar_init(&ms->v16_full[s], C::kSoftmax);
       mbar_init(&ms->v16_empty[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
@@ -416,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     fence_barrier_init();
   }
   if (tid < kBadRing * 8) ms->bad[tid >> 3][tid & 7] = 0;
-  if (warp == 9) {
+  if (warp == kWarp0 + 1) {
     tmem_alloc(&ms->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
@@ -471,10 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
   if (count <= 0) {
     // nothing left for this CTA
-  } else if (warp == 8 || warp == 10) {
-    reg_dealloc<kRegsOther>();
-    // ------------------------------------------- loads of K (warp 8) and V (warp 10)
-    const bool is_v = warp == 10;
+  } else if (warp == kWarp0 || warp == kWarp0 + 2) {
+    reg_dealloc<C::kRegsOther>();
+    // ------------------------------------------- loads of K (first warp) and V (third)
+    const bool is_v = warp == kWarp0 + 2;
     const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
     uint64_t* full = is_v ? ms->v_full : ms->k_full;
     uint64_t* empty = is_v ? ms->v_empty : ms->k_empty;
@@ -544,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (FP8 && is_v) mbar_wait_drain_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, kDrainNs);
       }
     }
-  } else if (warp == 9) {
-    reg_dealloc<kRegsOther>();
+  } else if (warp == kWarp0 + 1) {
+    reg_dealloc<C::kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
     constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
@@ -643,36 +653,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mma_commit(&ms->drain);
       mbar_wait_drain_inl(&ms->drain, 0, kDrainNs);
     }
-  } else if (warp < 8) {
-    reg_alloc<kRegsSoftmax>();
-    // ------------------------------------- softmax: one key per thread, NR rows
-    const int g = warp >> 2;
-    const int bar = 1 + g;
+  } else if (warp < kWarp0) {
+    reg_alloc<C::kRegsSoftmax>();
+    // -------------------- softmax: one key per thread, the warpgroup's NC rows of the stream
+    constexpr int NC = C::kNC;
+    const int g = warp / (4 * kSub);
+    const int sub = kSub == 1 ? 0 : (warp >> 2) & 1;
+    const int col0 = sub * NC;                                // first row in the stream's tile
+    const int bar = 1 + g * kSub + sub;                       // the warpgroup's barrier
+    const int end_bar = TILES == 1 ? 5 + sub : bar;           // those that finish a piece together: the warpgroups
+    constexpr int kEndThreads = TILES == 1 ? 256 : 128;       // of both streams that share rows, or one alone
     const int kt = tid & 127;  // key in the tile, TMEM lane, head dim of O
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + g * C::kSCols;
-    const uint32_t o_addr = tmem + lane_base + C::kColO + g * C::kPCols;
-    float* m_ref = ms->m[g];
-    float* corr = ms->corr[g];
+    const uint32_t s_addr = tmem + lane_base + g * C::kSCols + col0;
+    const uint32_t o_addr = tmem + lane_base + C::kColO + g * C::kPCols + col0;
+    float* nm = ms->nm[g] + col0;
+    float* corr = ms->corr[g] + col0;
+    float* red = ms->red[g][0] + col0;        // + warp·NR
+    int64_t* row = ms->row[g] + col0;
+    int64_t* o_off = ms->o_off[g] + col0;
     int tile0 = 0;             // tiles of the pieces before, and those of this stream
     int used = 0;
     bool ok = true;
     Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
-    load_q<D, FP8, NR, TILES, 256>(p, w, smem + C::kOffQ, ms->f[0], row0, tid);
-    named_sync(3, 256);
+    load_q<D, FP8, NR, TILES, C::kSoftmax>(p, w, smem + C::kOffQ, ms->f[0], row0, tid);
+    named_sync(7, C::kSoftmax);
     if (warp == 0) mbar_arrive(&ms->q_full);
     do {
       const int n_tiles = w.t1 - w.t0;
       const int context = w.len - w.drafts;
-      const int my_row0 = row0 + (TILES == 1 ? 0 : g * NR);
-      const int live = w.drafts * p.G - my_row0;  // rows of this tile that belong to a drafted token
-      if (kt < NR) {
+      const int my_row0 = row0 + (TILES == 1 ? 0 : g * NR) + col0;
+      const int live = w.drafts * p.G - my_row0;  // rows of this warpgroup that belong to a drafted token
+      if (kt < NC) {
         const int rr = my_row0 + kt;
         const int t = rr / p.G;
         const int h = w.h * p.G + (rr - t * p.G);
-        ms->row[g][kt] = kt < live ? (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t : -1;
-        ms->o_off[g][kt] = w.b * p.so[0] + h * p.so[1] + static_cast<int64_t>(t) * p.so[2];
-        m_ref[kt] = -INFINITY;
+        row[kt] = kt < live ? (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t : -1;
+        o_off[kt] = w.b * p.so[0] + h * p.so[1] + static_cast<int64_t>(t) * p.so[2];
+        nm[kt] = INFINITY;
       }
       // Does row n of this tile (a live one) see drafted key u?
       auto sees = [&](int n, int u) -> bool {
@@ -680,12 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         return p.mask != nullptr ? p.mask[w.b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t;
       };
       named_sync(bar, 128);
-      float l[NR];
+      float l[NC];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) l[n] = 0.f;
+      for (int n = 0; n < NC; ++n) l[n] = 0.f;
       int kv_ref = -1024;
       int done = 0;  // tiles of this piece that this stream has worked on
-      const float* f_row = ms->f[w.index % kFRing][TILES == 1 ? 0 : g];
+      const float* f_row = ms->f[w.index % kFRing][TILES == 1 ? 0 : g] + col0;
       for (int i = TILES == 1 ? g : 0; i < n_tiles; i += TILES == 1 ? 2 : 1, ++done) {
         const int tile = tile0 + i;
         const int u = used + done;
@@ -698,12 +716,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (key < w.len && live > 0) {
             // Token by token: one byte of the mask stands for G rows.
             const int ta = my_row0 / p.G;
-            const int tb = min(w.drafts - 1, (my_row0 + min(NR, live) - 1) / p.G);
+            const int tb = min(w.drafts - 1, (my_row0 + min(NC, live) - 1) / p.G);
             const uint8_t* mk = p.mask != nullptr ? p.mask + w.b * p.mask_sb + (key - context) : nullptr;
 #pragma unroll 4
             for (int t = ta; t <= tb; ++t) {
               const bool on = mk != nullptr ? mk[static_cast<int64_t>(t) * p.T] != 0 : key - context <= t;
-              const int lo = max(0, t * p.G - my_row0), hi = min(NR, (t + 1) * p.G - my_row0);  // its rows
+              const int lo = max(0, t * p.G - my_row0), hi = min(NC, (t + 1) * p.G - my_row0);  // its rows
               const uint64_t bits = (hi - lo >= 64 ? ~0ull : (1ull << (hi - lo)) - 1) << lo;
               seen |= on ? bits : 0;
             }
@@ -719,8 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (key < w.len) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
         }
         if constexpr (FP8) {
-          // This key's value row (two row tiles: the stream's half of it) to fp16, while the scores are made.
-          constexpr int kN = D / 16 / TILES;
+          // This key's value row, or the warpgroup's share of it, to fp16, while the scores are made.
+          constexpr int kN = D / 16 / (TILES * kSub);
           const int buf = TILES == 1 ? g : tile & 1;
           const int slot = tile % C::kRV;
           ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, site(11)) && ok;
@@ -731,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
           uint8_t* dst = smem + C::kOffV16 + buf * C::kV16 + kt * 128;
-          const int c0 = TILES == 1 ? 0 : g * kN;
+          const int c0 = (TILES == 1 ? sub : g * kSub + sub) * kN;
           if (!tail) {
             widen_row<D, kN, false>(src, dst, kt, c0, false, false);
           } else if (widen_row<D, kN, true>(src, dst, kt, c0, key >= context, key >= w.len) && key < w.len) {
@@ -745,23 +763,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, site(7)) && ok;
         tc_fence_after();
         // x = score − reference, masked to −∞ where the row does not see the key.
-        float x[NR];
+        float x[NC];
         auto scores = [&](bool relative) {
-          // 16 rows at a time, the next ones on their way from TMEM meanwhile.
+          // 16 rows at a time; with registers to spare the next ones are on their way from TMEM meanwhile.
           constexpr int kC = 16;
-          uint32_t hi[2][kC], lo[2][kC];
-          tmem_ld(s_addr, hi[0]);
-          if constexpr (FP8) tmem_ld(s_addr + NR, lo[0]);  // the columns of q's second terms
+          constexpr int kBuf = kSub == 1 && NC > kC ? 2 : 1;
+          uint32_t hi[kBuf][kC], lo[kBuf][kC];
+          auto fetch = [&](int c, int to) {
+            tmem_ld(s_addr + c, hi[to]);
+            if constexpr (FP8) tmem_ld(s_addr + NR + c, lo[to]);  // the columns of q's second terms
+          };
+          fetch(0, 0);
 #pragma unroll
-          for (int c = 0; c < NR; c += kC) {
-            const int now = (c / kC) & 1;
+          for (int c = 0; c < NC; c += kC) {
+            const int now = (c / kC) % kBuf;
+            if (kBuf == 1 && c > 0) fetch(c, 0);
             tmem_wait_ld();
             reg_fence(hi[now]);
             if constexpr (FP8) reg_fence(lo[now]);
-            if (c + kC < NR) {
-              tmem_ld(s_addr + c + kC, hi[now ^ 1]);
-              if constexpr (FP8) tmem_ld(s_addr + NR + c + kC, lo[now ^ 1]);
-            }
+            if (kBuf == 2 && c + kC < NC) fetch(c + kC, now ^ 1);
 #pragma unroll
             for (int e = 0; e < kC; e += 4) {
               const int n = c + e;
@@ -777,24 +797,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 fmul2(f4.x, f4.y, f4.x, f4.y, ks, ks);
                 fmul2(f4.z, f4.w, f4.z, f4.w, ks, ks);
               }
-              const float4 m4 =
-                  relative ? *reinterpret_cast<const float4*>(&m_ref[n]) : make_float4(0.f, 0.f, 0.f, 0.f);
-              ffma2(x[n], x[n + 1], r4.x, r4.y, f4.x, f4.y, -m4.x, -m4.y);
-              ffma2(x[n + 2], x[n + 3], r4.z, r4.w, f4.z, f4.w, -m4.z, -m4.w);
+              const float4 m4 = relative ? *reinterpret_cast<const float4*>(&nm[n]) : make_float4(0.f, 0.f, 0.f, 0.f);
+              ffma2(x[n], x[n + 1], r4.x, r4.y, f4.x, f4.y, m4.x, m4.y);
+              ffma2(x[n + 2], x[n + 3], r4.z, r4.w, f4.z, f4.w, m4.z, m4.w);
             }
           }
           if (tail) {
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+            for (int n = 0; n < NC; ++n)
               if (!((seen >> n) & 1)) x[n] = -INFINITY;
           }
         };
         scores(true);
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int n = 4; n < NR; n += 8)
+        for (int n = 4; n < NC; n += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = n + 4 + e < NR ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NR]) : fmaxf(mx[e], x[n + e]);
+          for (int e = 0; e < 4; ++e)
+            mx[e] = n + 4 + e < NC ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NC]) : fmaxf(mx[e], x[n + e]);
         const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
         const bool over = top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
         if (named_any(bar, 128, over || !ok)) {
@@ -804,40 +824,40 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             break;
           }
           scores(false);
-          reduce_cols<NR>(x, lane, OpMax(), ms->red[g][warp & 3]);
+          reduce_cols<NC>(x, lane, OpMax(), red + (warp & 3) * NR);
           if constexpr (FP8) {
             const int top_kv = __reduce_max_sync(0xffffffffu, kv);
-            if (lane == 0) ms->kv_red[g][warp & 3] = top_kv;
+            if (lane == 0) ms->kv_red[g][sub][warp & 3] = top_kv;
           }
           named_sync(bar, 128);
           int kv_new = kv_ref;
           if constexpr (FP8) {
-            const int* kr = ms->kv_red[g];
+            const int* kr = ms->kv_red[g][sub];
             kv_new = max(kv_ref, max(max(kr[0], kr[1]), max(kr[2], kr[3])));
           }
-          if (kt < NR) {
-            const float old = m_ref[kt];
-            const float now = fmaxf(fmaxf(ms->red[g][0][kt], ms->red[g][1][kt]), fmaxf(ms->red[g][2][kt], ms->red[g][3][kt]));
+          if (kt < NC) {
+            const float old = -nm[kt];
+            const float now = fmaxf(fmaxf(red[kt], red[NR + kt]), fmaxf(red[2 * NR + kt], red[3 * NR + kt]));
             const bool up = now > -INFINITY && now - kBase > old;
             corr[kt] = up ? exp2f(old - (now - kBase)) : 1.f;  // 0 from −∞: nothing was summed yet
-            if (up) m_ref[kt] = now - kBase;
+            if (up) nm[kt] = kBase - now;
           }
           named_sync(bar, 128);
 #pragma unroll
-          for (int n = 0; n < NR; ++n) l[n] *= corr[n];
+          for (int n = 0; n < NC; ++n) l[n] *= corr[n];
           if (done > 0) {
             ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, site(8)) && ok;
             tc_fence_after();
             const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
-            rescale_cols<NR>(o_addr, corr, kf);
-            if constexpr (C::kTerms == 2) rescale_cols<NR>(o_addr + NR, corr, kf);
+            rescale_cols<NC>(o_addr, corr, kf);
+            if constexpr (C::kTerms == 2) rescale_cols<NC>(o_addr + NR, corr, kf);
           }
           kv_ref = kv_new;
           scores(true);
           // A row that has seen nothing has the reference −∞, and only masked scores: −∞ − (−∞) is −∞ here.
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
-            if (m_ref[n] == -INFINITY) x[n] = -INFINITY;
+          for (int n = 0; n < NC; ++n)
+            if (nm[n] == INFINITY) x[n] = -INFINITY;
         }
         tc_fence_before();
         mbar_arrive(&ms->s_free[g]);
@@ -849,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const float wv = !FP8 ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
         uint8_t* prow = smem + C::kOffP + g * C::kP + kt * 128;
 #pragma unroll
-        for (int ch = 0; ch < NR / 8; ++ch) {  // 8 rows per 16-byte chunk
+        for (int ch = 0; ch < NC / 8; ++ch) {  // 8 rows per 16-byte chunk
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -867,38 +887,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 lo[e] = pack_bf16x2(x[n] - __uint_as_float(hi[e] << 16), x[n + 1] - __uint_as_float(hi[e] & 0xffff0000u));
             }
           }
-          *reinterpret_cast<uint4*>(prow + ((ch ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          const int c1 = col0 / 8 + ch;
+          *reinterpret_cast<uint4*>(prow + ((c1 ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           if constexpr (C::kTerms == 2) {
-            const int c2 = ch + NR / 8;  // column chunk of the second term
+            const int c2 = c1 + NR / 8;  // column chunk of the second term
             *reinterpret_cast<uint4*>(prow + (c2 >> 3) * kPBlock + (((c2 & 7) ^ (kt & 7)) << 4)) =
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         if (!FP8 && tail && key >= context && (TILES == 1 || g == 0)) {
-          // This key's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
-          // (Two row tiles: the first stream does it for both, its product is issued first.)
+          // This key's value row, or the warpgroup's share of it: zeros past the end, and in place of what a drafted row
+          // holds that is not finite.  (Two row tiles: the first stream does it for both, its product is issued first.)
           const int slot = tile % C::kRV;
           ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, site(9)) && ok;
-          uint8_t* vt = smem + C::kOffV + slot * kSlot;
+          uint8_t* vr = smem + C::kOffV + slot * kSlot + (kPg5 ? (kt >> 3) * 2048 + (kt & 7) * 128 : kt * 128);
           bool bad = false;
 #pragma unroll
-          for (int kb = 0; kb < D / 64; ++kb) {
-            uint8_t* vr = kPg5 ? vt + (kt >> 3) * 2048 + kb * 1024 + (kt & 7) * 128 : vt + kt * 128;
+          for (int e8 = 0; e8 < D / 8 / kSub; ++e8) {
+            const int ch = sub * (D / 8 / kSub) + e8;
+            uint4* at = reinterpret_cast<uint4*>(vr + (ch >> 3) * 1024 + (ch & 7) * 16);
+            uint32_t v4[4] = {0, 0, 0, 0};
+            if (key < w.len) {
+              const uint4 v = *at;
+              v4[0] = v.x, v4[1] = v.y, v4[2] = v.z, v4[3] = v.w;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              uint4* at = reinterpret_cast<uint4*>(vr + q * 16);
-              uint32_t v4[4] = {0, 0, 0, 0};
-              if (key < w.len) {
-                const uint4 v = *at;
-                v4[0] = v.x, v4[1] = v.y, v4[2] = v.z, v4[3] = v.w;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((v4[e] & 0x7f80u) == 0x7f80u) v4[e] &= 0xffff0000u, bad = true;
-                  if ((v4[e] & 0x7f800000u) == 0x7f800000u) v4[e] &= 0xffffu, bad = true;
-                }
+              for (int e = 0; e < 4; ++e) {
+                if ((v4[e] & 0x7f80u) == 0x7f80u) v4[e] &= 0xffff0000u, bad = true;
+                if ((v4[e] & 0x7f800000u) == 0x7f800000u) v4[e] &= 0xffffu, bad = true;
               }
-              *at = make_uint4(v4[0], v4[1], v4[2], v4[3]);
             }
+            *at = make_uint4(v4[0], v4[1], v4[2], v4[3]);
           }
           if (bad) atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
         }
@@ -911,56 +929,57 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // ------------------------------------------------------------ end of the piece
       // (Its barriers are joined by all threads whatever the waits said.)
       if (done > 0) ok = ok && mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, site(10));
-      reduce_cols<NR>(l, lane, OpAdd(), ms->red[g][warp & 3]);
-      if (kt == 0) ms->kv_ref[g] = kv_ref;
+      reduce_cols<NC>(l, lane, OpAdd(), red + (warp & 3) * NR);
+      if (kt == 0) ms->kv_ref[g][sub] = kv_ref;
       tc_fence_before();
-      named_sync(TILES == 1 ? 3 : bar, TILES == 1 ? 256 : 128);
+      named_sync(end_bar, kEndThreads);
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.tiles;
       // The slot of a piece: numbered along the line, or two per part (a part has a piece at each end at most).
       const long long pair = static_cast<long long>(w.b) * p.Hkv + w.h;
       const long long slot = p.slots_by_pair ? pair + part : 2ll * part + (w.t0 > 0 ? 0 : 1);
-      if (kt < NR) {
-        // Both streams' sums in a fixed order: the same result every time.
-        float m = -INFINITY, sum = 0.f, wgt[2] = {0.f, 0.f};
-        if constexpr (TILES == 1) m = fmaxf(ms->m[0][kt], ms->m[1][kt]); else m = m_ref[kt];
+      if (kt < NC) {
+        // The streams' sums (both, where they share rows) in a fixed order: the same result every time.
+        float sums[2], m = -INFINITY, sum = 0.f, mine = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           if (TILES == 2 && e != g) continue;
-          const float s = (ms->red[e][0][kt] + ms->red[e][1][kt]) + (ms->red[e][2][kt] + ms->red[e][3][kt]);
-          wgt[e] = s == 0.f ? 0.f : exp2f(ms->m[e][kt] - m);
-          sum += s * wgt[e];
+          const float* r4 = ms->red[e][0] + col0 + kt;
+          sums[e] = (r4[0] + r4[NR]) + (r4[2 * NR] + r4[3 * NR]);
+          m = fmaxf(m, -ms->nm[e][col0 + kt]);
         }
-        const int64_t r = ms->row[g][kt];
-        if (ok && r >= 0 && (TILES == 2 || g == 0)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (TILES == 2 && e != g) continue;
+          const float wgt = sums[e] == 0.f ? 0.f : exp2f(-ms->nm[e][col0 + kt] - m);
+          sum += sums[e] * wgt;
+          if (e == g) mine = wgt;
+        }
+        if (ok && row[kt] >= 0 && (TILES == 2 || g == 0)) {
           if (!whole) {
             float* ml = p.part_ml + (slot * p.T * p.G + my_row0 + kt) * 2;
             ml[0] = m;
             ml[1] = sum;
           } else if (p.lse != nullptr) {
-            p.lse[r] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            p.lse[row[kt]] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           }
         }
-        // What the streams' O is multiplied by.
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (e == g)
-            ms->lsum[e][kt] =
-                wgt[e] * inv * (FP8 ? exp2f(static_cast<float>(max(ms->kv_ref[e], -300))) : 1.f);
+        // What this stream's O is multiplied by.
+        mine *= sum != 0.f ? 1.f / sum : 0.f;
+        ms->lsum[g][col0 + kt] = mine * (FP8 ? exp2f(static_cast<float>(max(kv_ref, -300))) : 1.f);
       }
       if (w.t0 == 0 && rt == 0 && tid == 0) {
         // For the joining kernel: the pair's first part and how many parts it lies in.
         const long long start = static_cast<long long>(part) * per + (count - w.left - (w.t1 - w.t0));
         p.pieces[pair] = make_int2(part, static_cast<int>((start + w.tiles - 1) / per) - part + 1);
       }
-      named_sync(TILES == 1 ? 3 : bar, TILES == 1 ? 256 : 128);
+      named_sync(end_bar, kEndThreads);
       const uint32_t* bad = ms->bad[w.index % kBadRing];
       bool any_bad = false;
       for (int e = 0; e < 8; ++e) any_bad = any_bad || bad[e] != 0;
-      // Rows of this group: half of the shared ones, or its own, 16 or 32 at a time.
-      constexpr int kOut = TILES == 1 ? NR / 2 : NR;
-      constexpr int kStep = kOut < 32 ? kOut : 32;
+      // Rows that this warpgroup writes: half of the shared ones, or its own.
+      constexpr int kOut = TILES == 1 ? NC / 2 : NC;
+      constexpr int kStep = kOut < 16 ? kOut : 16;
       if (__all_sync(0xffffffffu, ok) && kt < D) {
 #pragma unroll
         for (int cc = 0; cc < kOut; cc += kStep) {
@@ -974,12 +993,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
             for (int term = 0; term < C::kTerms; ++term) {
               uint32_t r[kStep];
-              tmem_ld(tmem + lane_base + C::kColO + e * C::kPCols + term * NR + c0, r);
+              tmem_ld(tmem + lane_base + C::kColO + e * C::kPCols + term * NR + col0 + c0, r);
               tmem_wait_ld();
               reg_fence(r);
 #pragma unroll
               for (int q = 0; q < kStep; ++q) {
-                const float k = ms->lsum[e][c0 + q];
+                const float k = ms->lsum[e][col0 + c0 + q];
                 if (k != 0.f) o[q] += __uint_as_float(r[q]) * k;  // 0: a stream without keys has left O unwritten
               }
             }
@@ -1003,23 +1022,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
 #pragma unroll
           for (int q = 0; q < kStep; ++q) {
-            if (ms->row[g][c0 + q] >= 0) {
+            if (row[c0 + q] >= 0) {
               if (!whole)
                 p.part_o[(slot * p.T * p.G + my_row0 + c0 + q) * D + kt] = o[q];
               else
-                static_cast<__nv_bfloat16*>(p.o)[ms->o_off[g][c0 + q] + kt] = __float2bfloat16_rn(o[q]);
+                static_cast<__nv_bfloat16*>(p.o)[o_off[c0 + q] + kt] = __float2bfloat16_rn(o[q]);
             }
           }
         }
       }
       tc_fence_before();
       // All have read O and the statistics; any failed wait ends the walk for all.
-      ok = !named_any(TILES == 1 ? 3 : bar, TILES == 1 ? 256 : 128, !ok);
-      // The flags of three pieces ago: the other stream may still be at the piece before.
+      ok = !named_any(end_bar, kEndThreads, !ok);
+      // The flags of three pieces ago: other warpgroups may still be at the piece before.
       if (tid < 8) ms->bad[(w.index + kBadRing - 3) % kBadRing][tid] = 0;
     } while (ok && w.next());
   } else {
-    reg_dealloc<kRegsOther>();
+    reg_dealloc<C::kRegsOther>();
     // ------------------------- Q of every piece but the first, which the streams load
     Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
     while (w.next()) {
@@ -1032,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kWarp0 + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -1095,17 +1114,17 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
   constexpr int kSmem = Cfg<D, FP8, NR, TILES>::kOffMisc + static_cast<int>(sizeof(Misc<NR>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   using M = Misc<NR>;
-  static_assert(Cfg<D, FP8, NR, TILES>::kOffMisc % 16 == 0 && offsetof(M, m) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
+  static_assert(Cfg<D, FP8, NR, TILES>::kOffMisc % 16 == 0 && offsetof(M, nm) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
                     offsetof(M, k_scale) % 16 == 0 && offsetof(M, v_scale) % 16 == 0,
                 "16-byte accesses and bulk copies");
   // The register split draws on what the block was launched with.
   cudaFuncAttributes a;
   cudaError_t e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR, TILES>);
   if (e != cudaSuccess) return e;
-  if (a.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  if (a.numRegs < Cfg<D, FP8, NR, TILES>::kRegsLaunch) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, FP8, NR, TILES><<<static_cast<unsigned>(p.parts) * p.row_tiles, kThreads, kSmem, s>>>(p);
+  tree_kernel<D, FP8, NR, TILES><<<static_cast<unsigned>(p.parts) * p.row_tiles, Cfg<D, FP8, NR, TILES>::kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
