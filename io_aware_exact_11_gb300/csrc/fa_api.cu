@@ -1086,7 +1086,7 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B,
   for (int i = 0; i < d_rot / 2; ++i) {
     if (!std::isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "fa_rope: inv_freq[%d] is not finite", i);
     const double turns = inv_freq[i] / 6.283185307179586476925287;
-    const double part = std::ldexp(turns - std::floor(turns), 64);  // whole turns drop out: positions are whole
+    const double part = (turns - std::floor(turns)) * 18446744073709551616.0;  // whole turns drop out: positions are whole
     p.turns[i] = part < 18446744073709551616.0 ? static_cast<uint64_t>(part) : 0;
   }
   p.q = q;

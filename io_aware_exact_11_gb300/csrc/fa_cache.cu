@@ -15,6 +15,8 @@
 // the row maximum is log2(d/8) lane exchanges, so a row never leaves registers.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "fa_kernels.h"
 #include "sm103.cuh"
 
@@ -29,93 +31,139 @@ __device__ __forceinline__ void report(unsigned int* err, unsigned int what) {
 
 // The page of logical key t, or −1 (and a report) if the table's entry is no page.
 __device__ __forceinline__ int page_of(const CacheParams& p, int b, int t) {
-  const int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + t / p.block_size];
+  const int shift = 31 - __clz(p.block_size);  // a power of two
+  const int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + (t >> shift)];
   if (blk >= 0 && blk < p.num_blocks) return blk;
   report(p.err, kSiteBadBlock);
   return -1;
 }
 
-// Writes 8 elements of a row; the lanes of the row (8 or 16 neighbours) hold the rest of it.
+// The larger one of each of two 16-bit halves.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// Quantises 8 elements of a row; the lanes of the row (8 or 16 neighbours) hold
+// the rest of it.  Returns the codes; k is the row's exponent.  Magnitudes order
+// like their bits, so the row maximum is taken over packed pairs of 16 bits.
 template <int D>
-__device__ __forceinline__ void quantise_row(uint4 raw, uint8_t* codes, uint8_t* scale, int64_t row, int lane8,
-                                             bool live) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8];
-  uint32_t top = 0;
+__device__ __forceinline__ uint2 quantise8(uint4 raw, int& k) {
+  uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  auto row_max = [&](uint32_t top) -> uint32_t {
+#pragma unroll
+    for (int m = D / 16; m > 0; m >>= 1) top = max2(top, __shfl_xor_sync(0xffffffffu, top, m));
+    return max(top >> 16, top & 0xffffu);
+  };
+  uint32_t mag[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mag[i] = w[i] & 0x7fff7fffu;
+  uint32_t top = row_max(max2(max2(mag[0], mag[1]), max2(mag[2], mag[3])));
+  if (__any_sync(0xffffffffu, top >= 0x7f80u)) {
+    // Infinities and NaN somewhere in the warp's rows: they do not count for the maximum and become NaN.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] |= 0x7fffu, mag[i] &= 0xffff0000u;
+      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] |= 0x7fff0000u, mag[i] &= 0xffffu;
+    }
+    top = row_max(max2(max2(mag[0], mag[1]), max2(mag[2], mag[3])));
+  }
+  // top = 1.f·2^(e−127) with 7 bits of f; 448 = 1.75·2^8, so k = e − 127 − 8, one more when 1.f exceeds 1.75.
+  k = max(-126, static_cast<int>(top >> 7) - 135 + ((top & 0x7fu) > 0x60u ? 1 : 0));
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    float lo, hi;
+    fmul2(lo, hi, __uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u), inv, inv);
+    c[i] = pack_e4m3x2(lo, hi);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
-    if (a < 0x7f800000u) top = max(top, a);  // magnitudes order like their bits
-  }
-#pragma unroll
-  for (int m = D / 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-  // top = 1.f·2^(e−127); 448 = 1.75·2^8, so k = e − 127 − 8, one more when 1.f exceeds 1.75.
-  const int k = max(-126, static_cast<int>(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool finite = (__float_as_uint(x[i]) & 0x7fffffffu) < 0x7f800000u;
-    x[i] = finite ? x[i] * inv : __uint_as_float(0x7fffffffu);
-  }
-  if (!live) return;
-  uint2 out;
-  out.x = pack_e4m3x2(x[0], x[1]) | (pack_e4m3x2(x[2], x[3]) << 16);
-  out.y = pack_e4m3x2(x[4], x[5]) | (pack_e4m3x2(x[6], x[7]) << 16);
-  *reinterpret_cast<uint2*>(codes + row * D + lane8 * 8) = out;
-  if (lane8 == 0) scale[row] = static_cast<uint8_t>(k + 127);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-template <int D, bool FP8>
+// Item (b, group of R tokens, h), h fastest: 8 or 16 lanes for the R rows.
+template <int D, int R>
+struct Item {
+  static constexpr int kLanes = D / 8;
+  int b, n0, h, lane8;
+  bool in;
+  __device__ __forceinline__ explicit Item(const CacheParams& p) {
+    const int64_t id = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
+    lane8 = threadIdx.x % kLanes;
+    const int groups = (p.N + R - 1) / R;
+    const int64_t tok = id / p.Hkv;
+    h = static_cast<int>(id - tok * p.Hkv);
+    b = static_cast<int>(tok / groups);
+    n0 = static_cast<int>(tok - static_cast<int64_t>(b) * groups) * R;
+    in = b < p.B;
+  }
+};
+
+template <int D, bool FP8, int R>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ CacheParams p) {
-  constexpr int kLanes = D / 8;
-  const int64_t id = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;  // (b, n, h), h fastest
-  const int lane8 = threadIdx.x % kLanes;
-  const int64_t tok = id / p.Hkv;
-  const int h = static_cast<int>(id - tok * p.Hkv);
-  const int b = static_cast<int>(tok / p.N);
-  const int n = static_cast<int>(tok - static_cast<int64_t>(b) * p.N);
-  bool live = b < p.B;
-  int64_t row = 0;
-  if (live) {
-    int len = p.N;
-    if (p.lens != nullptr) {
-      len = p.lens[b];
-      if (len < 0 || len > p.N) {
-        report(p.err, kSiteBadLength);
-        len = 0;
-      }
-    }
-    live = n < len;
-    if (live) {
-      const int64_t t = static_cast<int64_t>(p.start[b]) + n;
-      if (t < 0 || t >= static_cast<int64_t>(p.max_blocks) * p.block_size) {
-        report(p.err, kSiteBadLength);
-        live = false;
-      } else {
-        const int blk = page_of(p, b, static_cast<int>(t));
-        live = blk >= 0;
-        row = (static_cast<int64_t>(blk) * p.Hkv + h) * p.block_size + t % p.block_size;
-      }
+  const Item<D, R> it(p);
+  const int shift = 31 - __clz(p.block_size);  // a power of two
+  int len = 0;
+  int64_t start = 0;
+  if (it.in) {
+    start = p.start[it.b];
+    len = p.lens != nullptr ? p.lens[it.b] : p.N;
+    if (len < 0 || len > p.N) {
+      report(p.err, kSiteBadLength);
+      len = 0;
     }
   }
-  uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
-  if (live) {
-    kr = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_rows) + b * p.sk[0] + h * p.sk[1] +
-                                         n * p.sk[2] + lane8 * 8);
-    vr = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_rows) + b * p.sv[0] + h * p.sv[1] +
-                                         n * p.sv[2] + lane8 * 8);
+  // The rows are on their way while their slots are looked up.
+  uint4 kr[R], vr[R];
+  const int count = min(R, len - it.n0);  // rows of this item that are written
+  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(p.k_rows) + it.b * p.sk[0] + it.h * p.sk[1] +
+                            it.n0 * p.sk[2] + it.lane8 * 8;
+  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(p.v_rows) + it.b * p.sv[0] + it.h * p.sv[1] +
+                            it.n0 * p.sv[2] + it.lane8 * 8;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    kr[r] = vr[r] = make_uint4(0, 0, 0, 0);
+    if (r < count) {
+      kr[r] = *reinterpret_cast<const uint4*>(kp + r * p.sk[2]);
+      vr[r] = *reinterpret_cast<const uint4*>(vp + r * p.sv[2]);
+    }
   }
-  if (FP8) {
-    quantise_row<D>(kr, static_cast<uint8_t*>(p.k_cache), p.k_scale, row, lane8, live);
-    quantise_row<D>(vr, static_cast<uint8_t*>(p.v_cache), p.v_scale, row, lane8, live);
-  } else if (live) {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_cache) + row * D + lane8 * 8) = kr;
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_cache) + row * D + lane8 * 8) = vr;
+  int64_t row[R];
+  if (count > 0) {
+    const int64_t t0 = start + it.n0;
+    const int64_t room = static_cast<int64_t>(p.max_blocks) * p.block_size;
+    if (t0 < 0 || t0 + count > room) report(p.err, kSiteBadLength);
+    int page = -1, blk = -1;  // the page of the token before and where it lies
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int t = static_cast<int>(t0) + r;
+      row[r] = -1;
+      if (r < count && t0 + r >= 0 && t0 + r < room) {
+        if (t >> shift != page) {
+          page = t >> shift;
+          blk = page_of(p, it.b, t);
+        }
+        if (blk >= 0) row[r] = ((static_cast<int64_t>(blk) * p.Hkv + it.h) << shift) + (t & (p.block_size - 1));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) row[r] = -1;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if constexpr (FP8) {
+      int ke, ve;
+      const uint2 kc = quantise8<D>(kr[r], ke), vc = quantise8<D>(vr[r], ve);
+      if (row[r] >= 0) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.k_cache) + row[r] * D + it.lane8 * 8) = kc;
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + row[r] * D + it.lane8 * 8) = vc;
+        if (it.lane8 == 0) {
+          p.k_scale[row[r]] = static_cast<uint8_t>(ke + 127);
+          p.v_scale[row[r]] = static_cast<uint8_t>(ve + 127);
+        }
+      }
+    } else if (row[r] >= 0) {
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_cache) + row[r] * D + it.lane8 * 8) = kr[r];
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_cache) + row[r] * D + it.lane8 * 8) = vr[r];
+    }
   }
 }
 
@@ -134,51 +182,74 @@ __device__ __forceinline__ uint4 dequantise8(uint2 c, uint32_t s) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int R>
 __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_constant__ CacheParams p) {
-  constexpr int kLanes = D / 8;
-  const int64_t id = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;  // (b, h, n), n fastest
-  const int lane8 = threadIdx.x % kLanes;
-  const int64_t bh = id / p.N;
-  const int n = static_cast<int>(id - bh * p.N);
-  const int b = static_cast<int>(bh / p.Hkv);
-  const int h = static_cast<int>(bh - static_cast<int64_t>(b) * p.Hkv);
-  if (b >= p.B) return;
-  int len = p.lens[b];
+  const Item<D, R> it(p);
+  if (!it.in) return;
+  int len = p.lens[it.b];
   if (len < 0 || len > static_cast<int64_t>(p.max_blocks) * p.block_size) {
     report(p.err, kSiteBadLength);
     len = 0;
   }
-  uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
-  const int blk = n < len ? page_of(p, b, n) : -1;
-  if (blk >= 0) {
-    const int64_t row = (static_cast<int64_t>(blk) * p.Hkv + h) * p.block_size + n % p.block_size;
-    if (FP8) {
-      const uint2 kc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.k_cache) + row * D + lane8 * 8);
-      const uint2 vc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.v_cache) + row * D + lane8 * 8);
-      kr = dequantise8(kc, p.k_scale[row]);
-      vr = dequantise8(vc, p.v_scale[row]);
-    } else {
-      kr = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + row * D + lane8 * 8);
-      vr = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_cache) + row * D + lane8 * 8);
+  using Raw = typename std::conditional<FP8, uint2, uint4>::type;  // 8 elements
+  Raw kr[R], vr[R];
+  uint32_t ks[R], vs[R];
+  bool live[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int n = it.n0 + r;
+    kr[r] = vr[r] = Raw{};
+    ks[r] = vs[r] = 127;
+    const int blk = n < len && n < p.N ? page_of(p, it.b, n) : -1;
+    live[r] = blk >= 0;
+    if (live[r]) {
+      const int64_t row = (static_cast<int64_t>(blk) * p.Hkv + it.h) * p.block_size + (n & (p.block_size - 1));
+      kr[r] = reinterpret_cast<const Raw*>(p.k_cache)[row * (D / 8) + it.lane8];
+      vr[r] = reinterpret_cast<const Raw*>(p.v_cache)[row * (D / 8) + it.lane8];
+      if constexpr (FP8) {
+        ks[r] = p.k_scale[row];
+        vs[r] = p.v_scale[row];
+      }
     }
   }
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_rows) + b * p.sk[0] + h * p.sk[1] + n * p.sk[2] +
-                            lane8 * 8) = kr;
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_rows) + b * p.sv[0] + h * p.sv[1] + n * p.sv[2] +
-                            lane8 * 8) = vr;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int n = it.n0 + r;
+    if (n >= p.N) break;
+    uint4 k8, v8;
+    if constexpr (FP8) {
+      k8 = dequantise8(kr[r], ks[r]);
+      v8 = dequantise8(vr[r], vs[r]);
+    } else {
+      k8 = kr[r];
+      v8 = vr[r];
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_rows) + it.b * p.sk[0] + it.h * p.sk[1] + n * p.sk[2] +
+                              it.lane8 * 8) = k8;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_rows) + it.b * p.sv[0] + it.h * p.sv[1] + n * p.sv[2] +
+                              it.lane8 * 8) = v8;
+  }
 }
 
-template <bool APPEND, int D, bool FP8>
-cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.B) * p.N * p.Hkv;
-  const int64_t blocks = (rows * (D / 8) + kThreads - 1) / kThreads;
+template <bool APPEND, int D, bool FP8, int R>
+cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
+  const int64_t items = static_cast<int64_t>(p.B) * ((p.N + R - 1) / R) * p.Hkv;
+  const int64_t blocks = (items * (D / 8) + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   if (APPEND)
-    cache_append_kernel<D, FP8><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    cache_append_kernel<D, FP8, R><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   else
-    cache_gather_kernel<D, FP8><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    cache_gather_kernel<D, FP8, R><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+// Four tokens per thread once one per thread would fill the machine several times over: the look-up of their slots
+// and the loads of their rows then overlap, where one per thread spends its life on that chain of loads.
+template <bool APPEND, int D, bool FP8>
+cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
+  const int64_t threads = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 8);
+  return p.N >= 4 && threads >= 4ll * 152 * 2048 ? launch_r<APPEND, D, FP8, 4>(p, stream)
+                                                 : launch_r<APPEND, D, FP8, 1>(p, stream);
 }
 
 template <bool APPEND>

@@ -121,7 +121,7 @@ struct RopeParams {
   int64_t pos_stride_b;
   int64_t sq[3], sk[3], sqo[3], sko[3];  // element strides (b, h, n)
   int B, Hq, Hk, N, d, rot;
-  int rot_cols, copy_cols, heads_per_thread;  // set by the launcher
+  int rot_cols, copy_cols, heads_per_thread, q_groups;  // set by the launcher
   int64_t position0;
   float magnitude, sign;
   uint64_t turns[128];  // w_i / 2π as 64-bit fractions of a turn

@@ -25,7 +25,7 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kHeadsInFlight = 4;  // loads outstanding per thread before the first use
+constexpr int kHeadsInFlight = 2;  // heads a thread loads before it turns them
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T x);
@@ -48,8 +48,14 @@ struct alignas(sizeof(T) * V == 16 ? 16 : alignof(T)) Vec {
 
 // HALF: a column is V pairs, two vectors r/2 apart.  INTER: one vector of V/2 pairs.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPairs = INTER ? V / 2 : V;
+  // The frequencies by (pair of a column, column), copied by one lane per warp: a constant that differs between the
+  // lanes is fetched once for each of them.
+  __shared__ uint64_t turns[128];
+  for (int i = threadIdx.x >> 5; i < p.rot / 2; i += kThreads / 32)
+    if ((threadIdx.x & 31) == 0) turns[i % kPairs * p.rot_cols + i / kPairs] = p.turns[i];
+  __syncthreads();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int cols = p.rot_cols + p.copy_cols;
   const int64_t tok = item / cols;
@@ -57,44 +63,50 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   if (tok >= static_cast<int64_t>(p.B) * p.N) return;
   const int b = static_cast<int>(tok / p.N);
   const int n = static_cast<int>(tok - static_cast<int64_t>(b) * p.N);
-  const int heads = p.Hq + p.Hk;
-  const int h0 = blockIdx.y * p.heads_per_thread;
-  const int h1 = min(heads, h0 + p.heads_per_thread);
+  // The block's heads are q's or k's.
+  const bool is_k = static_cast<int>(blockIdx.y) >= p.q_groups;
+  const int h0 = (blockIdx.y - (is_k ? p.q_groups : 0)) * p.heads_per_thread;
+  const int heads = min(p.heads_per_thread, (is_k ? p.Hk : p.Hq) - h0);
 
   const bool turn = col < p.rot_cols;
   const int e0 = turn ? col * V : p.rot + (col - p.rot_cols) * V;  // first element of the column
+  const int64_t* ss = is_k ? p.sk : p.sq;
+  const int64_t* ds = is_k ? p.sko : p.sqo;
+  const T* src = static_cast<const T*>(is_k ? p.k : p.q) + b * ss[0] + h0 * ss[1] + n * ss[2] + e0;
+  T* dst = static_cast<T*>(is_k ? p.k_out : p.q_out) + b * ds[0] + h0 * ds[1] + n * ds[2] + e0;
+  const int64_t src_h = ss[1], dst_h = ds[1];
+  const int half = p.rot >> 1;
+  Vec<T, V> a[kHeadsInFlight], c[kHeadsInFlight];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kHeadsInFlight; ++u) {
+      if (h + u < heads) {
+        a[u] = *reinterpret_cast<const Vec<T, V>*>(src);
+        if (!INTER && turn) c[u] = *reinterpret_cast<const Vec<T, V>*>(src + half);
+      }
+      src += src_h;
+    }
+  };
+  load(0);  // on their way while the angles are worked out
+
   float cs[kPairs], sn[kPairs];
   if (turn) {
     const int64_t pos = p.position0 + (p.positions != nullptr ? p.positions[b * p.pos_stride_b + n] : n);
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const uint64_t t = static_cast<uint64_t>(pos) * p.turns[col * kPairs + i];
-      const float half_turns = static_cast<float>(static_cast<int64_t>(t)) * 1.0842021724855044e-19f;  // 2^-63
+      const uint64_t t = static_cast<uint64_t>(pos) * turns[i * p.rot_cols + col];
+      const float half_turns = static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f;  // 2^-31
       sincospif(half_turns, &sn[i], &cs[i]);
       cs[i] *= p.magnitude;
       sn[i] *= p.sign * p.magnitude;
     }
   }
 
-  const T* q = static_cast<const T*>(p.q) + b * p.sq[0] + n * p.sq[2] + e0;
-  const T* k = static_cast<const T*>(p.k) + b * p.sk[0] + n * p.sk[2] + e0;
-  T* qo = static_cast<T*>(p.q_out) + b * p.sqo[0] + n * p.sqo[2] + e0;
-  T* ko = static_cast<T*>(p.k_out) + b * p.sko[0] + n * p.sko[2] + e0;
-  const int half = p.rot >> 1;
-  for (int h = h0; h < h1; h += kHeadsInFlight) {
-    Vec<T, V> a[kHeadsInFlight], c[kHeadsInFlight];
+  for (int h = 0; h < heads; h += kHeadsInFlight) {
+    if (h > 0) load(h);
 #pragma unroll
     for (int u = 0; u < kHeadsInFlight; ++u) {
-      if (h + u < h1) {
-        const T* src = h + u < p.Hq ? q + (h + u) * p.sq[1] : k + (h + u - p.Hq) * p.sk[1];
-        a[u] = *reinterpret_cast<const Vec<T, V>*>(src);
-        if (!INTER && turn) c[u] = *reinterpret_cast<const Vec<T, V>*>(src + half);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kHeadsInFlight; ++u) {
-      if (h + u < h1) {
-        T* dst = h + u < p.Hq ? qo + (h + u) * p.sqo[1] : ko + (h + u - p.Hq) * p.sko[1];
+      if (h + u < heads) {
         if (turn) {
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) {
@@ -108,6 +120,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
         *reinterpret_cast<Vec<T, V>*>(dst) = a[u];
       }
+      dst += dst_h;
     }
   }
 }
@@ -119,13 +132,14 @@ cudaError_t launch_v(RopeParams p, bool in_place, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.B) * p.N * (p.rot_cols + p.copy_cols);
   const int64_t blocks = (items + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const int heads = p.Hq + p.Hk;
-  // Heads per thread: all of them when the tokens alone give every SM about
-  // 1024 threads, fewer (down to one) when they do not.
-  int groups = 1;
-  while (groups < heads && blocks * groups < 152 * 8) groups *= 2;
-  p.heads_per_thread = (heads + groups - 1) / groups;
-  groups = (heads + p.heads_per_thread - 1) / p.heads_per_thread;
+  // Heads per thread: all of a tensor's when the tokens alone give every SM about 1024 threads, fewer (down to one)
+  // when they do not.
+  const int most = p.Hq > p.Hk ? p.Hq : p.Hk;
+  int per = most;
+  while (per > 1 && blocks * ((p.Hq + per - 1) / per + (p.Hk + per - 1) / per) < 152 * 8) per = (per + 1) / 2;
+  p.heads_per_thread = per;
+  p.q_groups = (p.Hq + per - 1) / per;
+  const int groups = p.q_groups + (p.Hk + per - 1) / per;
   rope_kernel<T, V, INTER><<<dim3(static_cast<unsigned>(blocks), groups), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }

@@ -57,6 +57,8 @@
 #include <cuda_fp16.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "fa_kernels.h"
 #include "sm103.cuh"
 
@@ -1117,11 +1119,16 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
   static_assert(Cfg<D, FP8, NR, TILES>::kOffMisc % 16 == 0 && offsetof(M, nm) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
                     offsetof(M, k_scale) % 16 == 0 && offsetof(M, v_scale) % 16 == 0,
                 "16-byte accesses and bulk copies");
-  // The register split draws on what the block was launched with.
-  cudaFuncAttributes a;
-  cudaError_t e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR, TILES>);
-  if (e != cudaSuccess) return e;
-  if (a.numRegs < Cfg<D, FP8, NR, TILES>::kRegsLaunch) return cudaErrorInvalidConfiguration;
+  // The register split draws on what the block is launched with, which is the compiled kernel's for good.
+  static std::atomic<bool> checked{false};
+  cudaError_t e;
+  if (!checked.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR, TILES>);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs < Cfg<D, FP8, NR, TILES>::kRegsLaunch) return cudaErrorInvalidConfiguration;
+    checked.store(true, std::memory_order_relaxed);
+  }
   e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   tree_kernel<D, FP8, NR, TILES><<<static_cast<unsigned>(p.parts) * p.row_tiles, Cfg<D, FP8, NR, TILES>::kThreads, kSmem, s>>>(p);

@@ -9,7 +9,6 @@ there is no fallback path.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -482,6 +481,8 @@ def backward(q, k, v, o, lse, do, scale: float | None = None, dq=None, dk=None, 
 #
 # These calls run on the tensors' own device.  Without ``stream`` they use that
 # device's current stream; with one, what they allocate belongs to that stream.
+# At single tokens the host side is most of a call's time, so it does little: one
+# look at the device, no contexts in the common case, plain integers to ctypes.
 
 
 def _device_of(*ts):
@@ -499,8 +500,8 @@ def _device_of(*ts):
     return dev
 
 
-def _on(dev, stream):
-    """Context in which ``dev`` is current, and ``stream`` where one is given."""
+def _elsewhere(dev, stream):
+    """None where ``dev`` is the current device and its current stream is wanted; else a context in which that is so."""
     torch = _torch()
     if stream is not None:
         if stream.device != dev:
@@ -508,22 +509,37 @@ def _on(dev, stream):
         return torch.cuda.stream(stream)
     if dev.index != torch.cuda.current_device():
         return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    return None
+
+
+def _current_stream(dev) -> int:
+    """Handle of the device's current stream."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _addr(t):
     return t.data_ptr() if t is not None else None
 
 
+_Strides6, _Strides12 = ctypes.c_int64 * 6, ctypes.c_int64 * 12
+
+
 def _strides(*ts):
     """Element strides of all but the last dimension (which must be contiguous), or None if all are contiguous."""
-    if all(t.is_contiguous() for t in ts):
-        return None
     for t in ts:
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        if not t.is_contiguous():
+            break
+    else:
+        return None
+    st = []
+    for t in ts:
+        x = t.stride()
+        if x[-1] != 1 and t.shape[-1] > 1:
             raise ValueError("the head dim must be contiguous")
-    st = [x for t in ts for x in t.stride()[:-1]]
-    return (ctypes.c_int64 * len(st))(*st)
+        st += x[:-1]
+    return (_Strides6 if len(st) == 6 else _Strides12)(*st)
 
 
 def _check_out(name, t, shape, dtype, dev):
@@ -567,41 +583,57 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
 def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, stream, inverse):
     torch = _torch()
     dev = _device_of(q, k, positions, out_q, out_k)
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, None, inverse)
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q must be [B, Hq, N, d] and k [B, Hk, N, d]")
     B, Hq, N, d = q.shape
-    dtype = _dtype_code(q)
-    if k is not None and k.dtype != q.dtype:
-        raise TypeError("q and k must share a dtype")
-    if k is None and out_k is not None:
+    code = _dtype_code(q)
+    Hk = 0
+    if k is not None:
+        if k.dtype != q.dtype:
+            raise TypeError("q and k must share a dtype")
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d:
+            raise ValueError("q must be [B, Hq, N, d] and k [B, Hk, N, d]")
+    elif out_k is not None:
         raise ValueError("out_k without k")
-    w = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if isinstance(inv_freq, torch.Tensor) and inv_freq.dtype == torch.float64 and not inv_freq.is_cuda:
+        w = inv_freq.contiguous()
+        w_ptr = w.data_ptr()
+    else:
+        w = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        w_ptr = w.ctypes.data
     if w.ndim != 1:
         raise ValueError("inv_freq must be one row of rot_dim/2 values")
-    pos_sb = 0
+    pos_ptr, pos_sb = None, 0
     if positions is not None:
         if positions.dtype != torch.int32:
             raise TypeError("positions must be int32")
-        if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+        shape = tuple(positions.shape)
+        if shape != (B, N) and shape != (N,) or (N > 1 and positions.stride(-1) != 1):
             raise ValueError("positions must be [N] or [B, N] with the last dim contiguous")
-        pos_sb = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    with _on(dev, stream):
-        if out_q is None:
-            out_q = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
+        pos_ptr = positions.data_ptr()
+        pos_sb = positions.stride(0) if len(shape) == 2 and B > 1 else 0
+    if out_q is None:
+        out_q = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
+    else:
+        _check_out("out_q", out_q, q.shape, q.dtype, dev)
+    if k is None:
+        st = _strides(q, q, out_q, out_q)
+    else:
+        if out_k is None:
+            out_k = torch.empty((B, Hk, N, d), dtype=q.dtype, device=dev)
         else:
-            _check_out("out_q", out_q, q.shape, q.dtype, dev)
-        ts = (q, q, out_q, out_q)
-        if k is not None:
-            if out_k is None:
-                out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
-            else:
-                _check_out("out_k", out_k, k.shape, q.dtype, dev)
-            ts = (q, k, out_q, out_k)
-        st = _strides(*ts)
-        _check(lib().fa_rope(q.data_ptr(), _addr(k), out_q.data_ptr(), _addr(out_k), B, Hq,
-                             k.shape[1] if k is not None else 0, N, d, 2 * w.shape[0], dtype, st, _addr(positions),
-                             pos_sb, int(position0), w.ctypes.data, float(magnitude),
-                             FA_ROPE_INTERLEAVED if interleaved else FA_ROPE_HALF, inverse, _stream_ptr()))
+            _check_out("out_k", out_k, k.shape, q.dtype, dev)
+        st = _strides(q, k, out_q, out_k)
+    status = lib().fa_rope(q.data_ptr(), _addr(k), out_q.data_ptr(), _addr(out_k), B, Hq, Hk, N, d, 2 * w.shape[0],
+                           code, st, pos_ptr, pos_sb, int(position0), w_ptr, float(magnitude),
+                           FA_ROPE_INTERLEAVED if interleaved else FA_ROPE_HALF, inverse, _current_stream(dev))
+    if status:
+        _check(status)
     return out_q, out_k
 
 
@@ -626,26 +658,27 @@ def rope_backward(dq, dk, inv_freq, positions=None, position0: int = 0, magnitud
 def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table):
     """Checks a paged cache; returns (num_blocks, Hkv, block_size, d, dtype code)."""
     torch = _torch()
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d]")
-    if v_cache.dtype != k_cache.dtype:
+    if v_cache.dtype != dtype:
         raise TypeError("k_cache and v_cache must share a dtype")
-    if k_cache.dtype == torch.bfloat16:
+    contiguous = k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()
+    if dtype == torch.bfloat16:
         code = FA_BF16
-    elif k_cache.dtype in (torch.float8_e4m3fn, torch.uint8):
+    elif dtype == torch.float8_e4m3fn or dtype == torch.uint8:
         code = FA_E4M3
         for s in (k_scale, v_scale):
-            if s is None or s.dtype != torch.uint8 or s.shape != k_cache.shape[:3]:
+            if s is None or s.dtype != torch.uint8 or s.shape != shape[:3]:
                 raise ValueError("an E4M3 cache needs uint8 k_scale and v_scale [num_blocks, Hkv, block_size]")
+            contiguous = contiguous and s.is_contiguous()
     else:
-        raise TypeError(f"unsupported cache dtype {k_cache.dtype} (bfloat16, float8_e4m3fn or uint8 codes)")
+        raise TypeError(f"unsupported cache dtype {dtype} (bfloat16, float8_e4m3fn or uint8 codes)")
     if block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise TypeError("block_table must be int32 [B, max_blocks]")
-    for t in (k_cache, v_cache, block_table) + ((k_scale, v_scale) if code == FA_E4M3 else ()):
-        if not t.is_contiguous():
-            raise ValueError("caches, scales and block_table must be contiguous")
-    nb, hkv, bs, d = k_cache.shape
-    return nb, hkv, bs, d, code
+    if not contiguous:
+        raise ValueError("caches, scales and block_table must be contiguous")
+    return *shape, code
 
 
 def _check_lens(name, t, B):
@@ -664,6 +697,10 @@ def cache_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, k_sc
     """
     torch = _torch()
     dev = _device_of(k, v, k_cache, v_cache, block_table, start, new_lens, k_scale, v_scale)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return cache_append(k, v, k_cache, v_cache, block_table, start, new_lens, k_scale, v_scale)
     nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
     B = block_table.shape[0]
     if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or k.shape[1] != hkv or k.shape[3] != d:
@@ -673,11 +710,12 @@ def cache_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, k_sc
     _check_lens("start", start, B)
     if new_lens is not None:
         _check_lens("new_lens", new_lens, B)
-    with _on(dev, stream):
-        _check(lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                     _addr(k_scale), _addr(v_scale), block_table.data_ptr(), start.data_ptr(),
-                                     _addr(new_lens), B, hkv, k.shape[2], nb, bs, block_table.shape[1], d, code,
-                                     _strides(k, v), _stream_ptr()))
+    status = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
+                                   _addr(v_scale), block_table.data_ptr(), start.data_ptr(), _addr(new_lens), B, hkv,
+                                   k.shape[2], nb, bs, block_table.shape[1], d, code, _strides(k, v),
+                                   _current_stream(dev))
+    if status:
+        _check(status)
 
 
 def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, v_scale=None, out_k=None, out_v=None,
@@ -685,24 +723,31 @@ def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, 
     """The first n keys and values of every sequence as bf16 [B,Hkv,n,d]; rows past seq_lens[b] are zero."""
     torch = _torch()
     dev = _device_of(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, out_k, out_v)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return cache_gather(k_cache, v_cache, block_table, seq_lens, n, k_scale, v_scale, out_k, out_v)
     nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
     B = block_table.shape[0]
     _check_lens("seq_lens", seq_lens, B)
     n = int(n)
     if n < 1:
         raise ValueError("n must be at least 1")
-    with _on(dev, stream):
-        shape = (B, hkv, n, d)
-        if out_k is None:
-            out_k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if out_v is None:
-            out_v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    shape = (B, hkv, n, d)
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
         _check_out("out_k", out_k, shape, torch.bfloat16, dev)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
         _check_out("out_v", out_v, shape, torch.bfloat16, dev)
-        _check(lib().fa_cache_gather(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
-                                     block_table.data_ptr(), seq_lens.data_ptr(), out_k.data_ptr(), out_v.data_ptr(),
-                                     B, hkv, n, nb, bs, block_table.shape[1], d, code, _strides(out_k, out_v),
-                                     _stream_ptr()))
+    status = lib().fa_cache_gather(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                   block_table.data_ptr(), seq_lens.data_ptr(), out_k.data_ptr(), out_v.data_ptr(), B,
+                                   hkv, n, nb, bs, block_table.shape[1], d, code, _strides(out_k, out_v),
+                                   _current_stream(dev))
+    if status:
+        _check(status)
     return out_k, out_v
 
 
@@ -726,7 +771,13 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
     torch = _torch()
     dev = _device_of(q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, k_scale, v_scale, out, lse,
                      workspace)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, k_scale, v_scale,
+                               max_parts, scale, out, lse, workspace)
     nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    max_blocks = block_table.shape[1]
     if q.dim() != 4 or q.shape[0] != block_table.shape[0] or q.shape[3] != d:
         raise ValueError(f"q must be [{block_table.shape[0]}, Hq, T, {d}], got {tuple(q.shape)}")
     if q.dtype != torch.bfloat16:
@@ -735,34 +786,37 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
     _check_lens("seq_lens", seq_lens, B)
     if draft_lens is not None:
         _check_lens("draft_lens", draft_lens, B)
-    mask_sb = 0
+    mask_ptr, mask_sb = None, 0
     if tree_mask is not None:
-        if tree_mask.dtype not in (torch.bool, torch.uint8):
+        if tree_mask.dtype != torch.bool and tree_mask.dtype != torch.uint8:
             raise TypeError("tree_mask must be bool or uint8")
-        if tuple(tree_mask.shape) not in ((T, T), (B, T, T)) or (T > 1 and tree_mask.stride()[-2:] != (T, 1)):
+        shape, step = tuple(tree_mask.shape), tree_mask.stride()
+        if shape != (B, T, T) and shape != (T, T) or (T > 1 and step[-2:] != (T, 1)):
             raise ValueError("tree_mask must be [T, T] or [B, T, T] with contiguous rows")
-        mask_sb = tree_mask.stride(0) if tree_mask.dim() == 3 and B > 1 else 0
+        mask_ptr = tree_mask.data_ptr()
+        mask_sb = step[0] if len(shape) == 3 and B > 1 else 0
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_out("out", out, q.shape, torch.bfloat16, dev)
-        if lse is None:
-            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-        else:
-            _check_out("lse", lse, (B, Hq, T), torch.float32, dev)
-            if not lse.is_contiguous():
-                raise ValueError("lse must be contiguous")
-        if workspace is None:
-            workspace = torch.empty(max(decode_tree_workspace_size(B, Hq, hkv, T, d, max_parts), 16), dtype=torch.uint8,
-                                    device=dev)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        _check(lib().fa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
-                                    _addr(v_scale), block_table.data_ptr(), seq_lens.data_ptr(), _addr(draft_lens),
-                                    _addr(tree_mask), mask_sb, out.data_ptr(), lse.data_ptr(), B, Hq, hkv, T, nb, bs,
-                                    block_table.shape[1], d, code, float(scale), _strides(q, out), int(max_parts),
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr()))
+    if out is None:
+        out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out("out", out, q.shape, torch.bfloat16, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _check_out("lse", lse, (B, Hq, T), torch.float32, dev)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    if workspace is None:
+        workspace = torch.empty(max(decode_tree_workspace_size(B, Hq, hkv, T, d, max_parts), 16), dtype=torch.uint8,
+                                device=dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    status = lib().fa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                  block_table.data_ptr(), seq_lens.data_ptr(), _addr(draft_lens), mask_ptr, mask_sb,
+                                  out.data_ptr(), lse.data_ptr(), B, Hq, hkv, T, nb, bs, max_blocks, d, code,
+                                  float(scale), _strides(q, out), int(max_parts), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _current_stream(dev))
+    if status:
+        _check(status)
     return out, lse
