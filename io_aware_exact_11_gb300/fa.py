@@ -485,38 +485,38 @@ def backward(q, k, v, o, lse, do, scale: float | None = None, dq=None, dk=None, 
 # look at the device, no contexts in the common case, plain integers to ctypes.
 
 
-def _device_of(*ts):
-    """The one CUDA device of the given tensors (None entries are skipped)."""
+def _device_of(*ts) -> int:
+    """Index of the one CUDA device that the given tensors live on (None entries are skipped)."""
     dev = None
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("all tensors must live on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("all tensors must live on the same CUDA device")
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if i < 0:
+                    raise ValueError("all tensors must live on a CUDA device")
+                if dev is not None:
+                    raise ValueError("all tensors must live on the same CUDA device")
+                dev = i
     return dev
 
 
-def _elsewhere(dev, stream):
+def _elsewhere(dev: int, stream):
     """None where ``dev`` is the current device and its current stream is wanted; else a context in which that is so."""
     torch = _torch()
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         return torch.cuda.device(dev)
     return None
 
 
-def _current_stream(dev) -> int:
+def _current_stream(dev: int) -> int:
     """Handle of the device's current stream."""
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _addr(t):
@@ -543,8 +543,8 @@ def _strides(*ts):
 
 
 def _check_out(name, t, shape, dtype, dev):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -612,20 +612,20 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
     if positions is not None:
         if positions.dtype != torch.int32:
             raise TypeError("positions must be int32")
-        shape = tuple(positions.shape)
+        shape = positions.shape
         if shape != (B, N) and shape != (N,) or (N > 1 and positions.stride(-1) != 1):
             raise ValueError("positions must be [N] or [B, N] with the last dim contiguous")
         pos_ptr = positions.data_ptr()
         pos_sb = positions.stride(0) if len(shape) == 2 and B > 1 else 0
     if out_q is None:
-        out_q = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
+        out_q = q.new_empty((B, Hq, N, d))
     else:
         _check_out("out_q", out_q, q.shape, q.dtype, dev)
     if k is None:
         st = _strides(q, q, out_q, out_q)
     else:
         if out_k is None:
-            out_k = torch.empty((B, Hk, N, d), dtype=q.dtype, device=dev)
+            out_k = k.new_empty((B, Hk, N, d))
         else:
             _check_out("out_k", out_k, k.shape, q.dtype, dev)
         st = _strides(q, k, out_q, out_k)
@@ -683,7 +683,7 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table):
 
 def _check_lens(name, t, B):
     torch = _torch()
-    if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous int32 [{B}]")
 
 
@@ -702,8 +702,9 @@ def cache_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, k_sc
         with there:
             return cache_append(k, v, k_cache, v_cache, block_table, start, new_lens, k_scale, v_scale)
     nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
-    B = block_table.shape[0]
-    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or k.shape[1] != hkv or k.shape[3] != d:
+    B, max_blocks = block_table.shape
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or shape[0] != B or shape[1] != hkv or shape[3] != d:
         raise ValueError(f"k and v must be [{B}, {hkv}, N, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("k and v must be bfloat16")
@@ -712,7 +713,7 @@ def cache_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, k_sc
         _check_lens("new_lens", new_lens, B)
     status = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
                                    _addr(v_scale), block_table.data_ptr(), start.data_ptr(), _addr(new_lens), B, hkv,
-                                   k.shape[2], nb, bs, block_table.shape[1], d, code, _strides(k, v),
+                                   shape[2], nb, bs, max_blocks, d, code, _strides(k, v),
                                    _current_stream(dev))
     if status:
         _check(status)
@@ -735,11 +736,11 @@ def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, 
         raise ValueError("n must be at least 1")
     shape = (B, hkv, n, d)
     if out_k is None:
-        out_k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out_k = k_cache.new_empty(shape, dtype=torch.bfloat16)
     else:
         _check_out("out_k", out_k, shape, torch.bfloat16, dev)
     if out_v is None:
-        out_v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out_v = k_cache.new_empty(shape, dtype=torch.bfloat16)
     else:
         _check_out("out_v", out_v, shape, torch.bfloat16, dev)
     status = lib().fa_cache_gather(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
@@ -777,12 +778,13 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
             return decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask, draft_lens, k_scale, v_scale,
                                max_parts, scale, out, lse, workspace)
     nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
-    max_blocks = block_table.shape[1]
-    if q.dim() != 4 or q.shape[0] != block_table.shape[0] or q.shape[3] != d:
-        raise ValueError(f"q must be [{block_table.shape[0]}, Hq, T, {d}], got {tuple(q.shape)}")
+    B, max_blocks = block_table.shape
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != d:
+        raise ValueError(f"q must be [{B}, Hq, T, {d}], got {tuple(shape)}")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16")
-    B, Hq, T, _ = q.shape
+    _, Hq, T, _ = shape
     _check_lens("seq_lens", seq_lens, B)
     if draft_lens is not None:
         _check_lens("draft_lens", draft_lens, B)
@@ -790,7 +792,7 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
     if tree_mask is not None:
         if tree_mask.dtype != torch.bool and tree_mask.dtype != torch.uint8:
             raise TypeError("tree_mask must be bool or uint8")
-        shape, step = tuple(tree_mask.shape), tree_mask.stride()
+        shape, step = tree_mask.shape, tree_mask.stride()
         if shape != (B, T, T) and shape != (T, T) or (T > 1 and step[-2:] != (T, 1)):
             raise ValueError("tree_mask must be [T, T] or [B, T, T] with contiguous rows")
         mask_ptr = tree_mask.data_ptr()
@@ -798,18 +800,17 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((B, Hq, T, d))
     else:
         _check_out("out", out, q.shape, torch.bfloat16, dev)
     if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, Hq, T), dtype=torch.float32)
     else:
         _check_out("lse", lse, (B, Hq, T), torch.float32, dev)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
     if workspace is None:
-        workspace = torch.empty(max(decode_tree_workspace_size(B, Hq, hkv, T, d, max_parts), 16), dtype=torch.uint8,
-                                device=dev)
+        workspace = q.new_empty(max(decode_tree_workspace_size(B, Hq, hkv, T, d, max_parts), 16), dtype=torch.uint8)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     status = lib().fa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
