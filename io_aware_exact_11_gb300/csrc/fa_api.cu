@@ -1218,6 +1218,8 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   memset(&p, 0, sizeof(p));
   if ((r = check_rows(who, strides, p.sq, p.so, H_q, T, d)) != FA_OK) return r;
   if (!rows_distinct(B, H_q, T, d, p.so)) return fail(FA_ERR_INVALID_ARG, "%s: o overlaps itself", who);
+  if ((static_cast<int64_t>(max_blocks) * block_size + 127) / 128 * H_kv > INT32_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "%s: max_blocks * block_size * H_kv too large", who);
   // A smaller workspace is taken with fewer parts; one part needs no room for pieces.
   const int64_t rows = static_cast<int64_t>(T) * (H_q / H_kv);
   const int64_t tiles = static_cast<int64_t>(B) * H_kv * ((static_cast<int64_t>(max_blocks) * block_size + 127) / 128);
@@ -1244,6 +1246,8 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part_ml);
   p.parts = static_cast<int>(parts);
   p.slots_by_pair = ws.by_pair ? 1 : 0;
+  const int group = H_q / H_kv;
+  p.g_magic = group > 1 ? static_cast<unsigned>((0x100000000ull + group - 1) / group) : 0;
   p.row_tiles = static_cast<int>((rows + fa::tree_cta_rows(rows) - 1) / fa::tree_cta_rows(rows));
   p.B = B;
   p.Hq = H_q;

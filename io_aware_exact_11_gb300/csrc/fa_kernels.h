@@ -164,6 +164,7 @@ struct TreeParams {
   float* part_o;   // [slot, T·G, d] fp32: o/ℓ of a cut pair's pieces
   float* part_ml;  // [slot, T·G, 2] fp32: (m in log2 units, ℓ)
   int B, Hq, Hkv, G, T, num_blocks, block_size, max_blocks;
+  unsigned g_magic;   // ceil(2^32 / G), for rows / G (G > 1)
   int row_tiles;      // CTA tiles of the T·G rows of a pair
   int parts;          // equal parts that the line of key tiles is cut into
   int slots_by_pair;  // a piece's slot: pair + part, else two per part
@@ -175,6 +176,7 @@ cudaError_t launch_rope(const RopeParams& p, bool fp32, bool inter, bool in_plac
 cudaError_t launch_cache_append(const CacheParams& p, int d, bool fp8, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheParams& p, int d, bool fp8, cudaStream_t s);
 int tree_cta_rows(int64_t rows);  // rows one CTA takes, for T·G rows in all
+cudaError_t launch_tree_wide(const TreeParams& p, int d, bool fp8, cudaStream_t s);  // more than 64 rows a pair
 cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s);
 
 cudaError_t launch_fwd_bf16(int d, const FwdParams& p, cudaStream_t s);

@@ -54,32 +54,29 @@
 // rows and not by others, and 0·NaN would reach the others through the product:
 // non-finite elements of drafted rows are zeroed there too, and added to the
 // rows that do see them at the end.
-#include <cuda_fp16.h>
 #include <stddef.h>
 
 #include <atomic>
 
-#include "fa_kernels.h"
-#include "sm103.cuh"
+#include "fa_tree.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kBN = 128;                 // keys per tile
+constexpr int kBN = kTreeBN;
 constexpr int kPBlock = kBN * 128;       // P̃ᵀ: one 128-byte row per key
 constexpr int kMaxRing = 8;
 constexpr int kMaxThreads = 640;
-constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kScaleRing = 16;           // E4M3: tiles whose scale bytes are staged (V slots and four more)
 constexpr int kFRing = 4;                // pieces whose row factors may be live at once
 constexpr int kBadRing = 8;              // pieces whose flags of bad values may be
 
-// NR rows per stream; TILES = 1: both streams work on the same rows, 2: on two tiles of rows.
-template <int D, bool FP8, int NR, int TILES>
+// NR rows of a pair, shared by both streams.
+template <int D, bool FP8, int NR>
 struct Cfg {
-  // With 64 shared rows a stream has two warpgroups, each with half of the rows: four softmax warps per SM
-  // sub-partition hide one another's waits better than two with twice the rows each.
-  static constexpr int kSub = NR == 64 && TILES == 1 ? 2 : 1;
+  // With 64 rows a stream has two warpgroups, each with half of them: four softmax warps per SM sub-partition hide
+  // one another's waits better than two with twice the rows each.
+  static constexpr int kSub = NR == 64 ? 2 : 1;
   static constexpr int kNC = NR / kSub;                       // rows (TMEM columns) of a softmax thread
   static constexpr int kSoftmax = 256 * kSub;                 // softmax threads; then warps for K, MMA, V, Q
   static constexpr int kThreads = kSoftmax + 128;
@@ -91,12 +88,12 @@ struct Cfg {
   static_assert(2 * kSub * kRegsSoftmax + kRegsOther <= (2 * kSub + 1) * kRegsLaunch && kThreads <= kMaxThreads,
                 "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
-  static constexpr int kTerms = !FP8 && TILES == 1 ? 2 : 1;   // of P̃
+  static constexpr int kTerms = FP8 ? 1 : 2;                  // of P̃
   static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
   static constexpr int kP = (kPCols + 63) / 64 * kPBlock;     // of one stream
   static constexpr int kQTile = FP8 ? 2 * NR * D : NR * D * 2;
-  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;          // one widened V tile, double buffered
-  static constexpr int kFixed = 2 * kV16 + 2 * kP + TILES * kQTile;
+  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;          // a stream's widened V tile
+  static constexpr int kFixed = 2 * kV16 + 2 * kP + kQTile;
   // K and V ring slots in what is left of 208 KB (V is needed later than K).
   static constexpr int kRing = (208 * 1024 - kFixed) / kSlot < 14 ? (208 * 1024 - kFixed) / kSlot : 14;
   static constexpr int kRK = kRing / 2;
@@ -106,7 +103,7 @@ struct Cfg {
   static constexpr int kOffV16 = kOffV + kRV * kSlot;
   static constexpr int kOffP = kOffV16 + 2 * kV16;
   static constexpr int kOffQ = kOffP + 2 * kP;
-  static constexpr int kOffMisc = kOffQ + TILES * kQTile;
+  static constexpr int kOffMisc = kOffQ + kQTile;
   static constexpr int kSCols = FP8 ? 2 * NR : NR;            // TMEM columns of one stream's S
   static constexpr int kColO = 2 * kSCols;
   static constexpr int kCols = kColO + 2 * kPCols;
@@ -118,88 +115,23 @@ struct Cfg {
 template <int NR>
 struct Misc {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], v16_full[2], v16_empty[2];
-  uint64_t sc_full[kScaleRing], q_full, q_empty, drain;
-  alignas(16) float nm[2][NR];         // minus the reference maxima (log2 units), +∞ while a row has seen nothing
-  alignas(16) float f[kFRing][2][NR];  // E4M3: what a row's raw scores are multiplied by
-  float corr[2][NR];                   // factor of the last rescale; in the end what O is multiplied by
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], sc_full[kScaleRing], q_full, q_empty, drain;
+  alignas(16) float nm[2][NR];         // minus the reference maxima (log2 units), 0 while a row has seen nothing
+  alignas(16) float f[kFRing][NR];     // E4M3: what a row's raw scores are multiplied by
+  float corr[2][NR];                   // factor of the last rescale
   float red[2][4][NR];                 // per-warp maxima or sums
-  float lsum[2][NR];
+  float scale[2][NR];                  // what a stream's O is multiplied by in the end
   int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
   int64_t o_off[2][NR];                // its element offset in O
-  int kv_red[2][2][4], kv_ref[2][2];   // per stream and warpgroup
+  int fresh[2][NR];                    // a live row that has seen nothing yet
+  int kv_red[2][2][4];                 // per stream, warpgroup and warp
   alignas(16) uint8_t k_scale[kScaleRing][kBN];  // written by bulk copies
   alignas(16) uint8_t v_scale[kScaleRing][kBN];
   uint32_t bad[kBadRing][8];           // drafted keys with non-finite values (one bit each)
   long long warp_sum[kMaxThreads / 32];
-  int start_b, start_h, start_tile;
+  int start[3];
   uint32_t tmem_base;
   int abort_flag;
-};
-
-__device__ __forceinline__ unsigned int site(unsigned int s) { return (kKernTree << 8) | s; }
-
-// Lengths of sequence b, checked: keys in all and drafted keys among them.
-// Lengths that cannot be are reported and taken as an empty sequence.
-__device__ __forceinline__ void seq_lengths(const TreeParams& p, int b, int& len, int& drafts) {
-  len = p.seq_lens[b];
-  drafts = p.draft_lens != nullptr ? p.draft_lens[b] : p.T;
-  if (p.draft_lens == nullptr && len == 0) drafts = 0;  // an unused batch slot
-  if (drafts < 0 || drafts > p.T || len < drafts || len > static_cast<int64_t>(p.max_blocks) * p.block_size) {
-    atomicCAS(p.err + 1, 0u, (kKernTree << 8) | kSiteBadLength);
-    len = drafts = 0;
-  }
-}
-// Key tiles of a sequence; one without drafted tokens has no rows and needs none.
-__device__ __forceinline__ int seq_tiles(int len, int drafts) { return drafts > 0 ? (len + kBN - 1) / kBN : 0; }
-
-__device__ __forceinline__ int checked_page(const TreeParams& p, int b, int index) {
-  const int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + index];
-  if (blk >= 0 && blk < p.num_blocks) return blk;
-  atomicCAS(p.err + 1, 0u, (kKernTree << 8) | kSiteBadBlock);
-  return 0;
-}
-
-// Tiles per part of the line of W tiles.  At least two, one for each stream.
-__device__ __forceinline__ long long part_tiles(long long W, int parts) {
-  const long long per = (W + parts - 1) / parts;
-  return per < 2 ? 2 : per;
-}
-
-// A CTA's walk over its part: one (b, key/value head) pair, or a piece of it, per step.
-struct Walk {
-  const TreeParams& p;
-  long long left;   // tiles of the part that remain, this piece's excluded
-  int b, h, len, drafts, tiles;
-  int t0, t1;       // the piece: tiles [t0, t1) of the pair
-  int index;        // pieces before this one
-
-  __device__ __forceinline__ Walk(const TreeParams& p_, int b0, int h0, int tile, long long count) : p(p_) {
-    b = b0;
-    h = h0;
-    seq_lengths(p, b, len, drafts);
-    tiles = seq_tiles(len, drafts);
-    t0 = tile;
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + count));
-    left = count - (t1 - t0);
-    index = 0;
-  }
-  __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    if (++h == p.Hkv) {
-      h = 0;
-      do {
-        if (++b >= p.B) return false;
-        seq_lengths(p, b, len, drafts);
-        tiles = seq_tiles(len, drafts);
-      } while (tiles == 0);
-    }
-    t0 = 0;
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
-    left -= t1;
-    ++index;
-    return true;
-  }
 };
 
 struct OpMax {
@@ -232,10 +164,8 @@ __device__ __forceinline__ void reduce_cols(float (&v)[N], int lane, Op op, floa
       v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], mask));
     }
   }
-  if (N >= 32 || (lane & (32 / (N < 32 ? N : 32) - 1)) == 0) {
-#pragma unroll
-    for (int i = 0; i < (N >= 32 ? N / 32 : 1); ++i) out[base + i] = v[i];
-  }
+  static_assert(N <= 32, "one total per lane");
+  if ((lane & (32 / N - 1)) == 0) out[base] = v[0];
 }
 
 // Widens chunks [C0, C0 + N) of 16 E4M3 codes of one value row of D codes to fp16.
@@ -286,36 +216,14 @@ __device__ __forceinline__ void rescale_cols(uint32_t addr, const float* w, floa
   tmem_wait_st();
 }
 
-// True on one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
-  return pred != 0;
-}
-
-// Position in a ring of N slots and the parity of its passes.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void advance() {
-    if (++slot == N) {
-      slot = 0;
-      parity ^= 1u;
-    }
-  }
-};
-
 // The query rows of a piece as a K-major operand (rows that are not there as
 // zeros), by NT threads.  E4M3: two terms per element and the factor of the row.
-template <int D, bool FP8, int NR, int TILES, int NT>
-__device__ __forceinline__ void load_q(const TreeParams& p, const Walk& w, uint8_t* q_smem, float (*f)[NR], int row0,
-                                       int id) {
-  using C = Cfg<D, FP8, NR, TILES>;
+template <int D, bool FP8, int NR, int NT, int kBatchMax>
+__device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, uint8_t* q_smem, float* f, int id) {
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-  constexpr int kPer = (TILES * NR * kChunks + NT - 1) / NT;
-  constexpr int kBatch = kPer < 4 ? kPer : 4;  // loads in flight per thread
-  const int live = w.drafts * p.G - row0;
+  constexpr int kPer = (NR * kChunks + NT - 1) / NT;
+  constexpr int kBatch = kPer < kBatchMax ? kPer : kBatchMax;  // loads in flight per thread
+  const int live = w.drafts * p.G;
 #pragma unroll 1
   for (int i0 = 0; i0 < kPer; i0 += kBatch) {
     uint4 q4[kBatch];
@@ -325,22 +233,19 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const Walk& w, uint8
       const int n = i / kChunks, ch = i % kChunks;
       q4[e] = make_uint4(0, 0, 0, 0);
       if (n < live) {
-        const int rr = row0 + n;
-        const int t = rr / p.G;
+        const int t = token_of(p, n);
         q4[e] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + w.b * p.sq[0] +
-                                                (w.h * p.G + rr - t * p.G) * p.sq[1] + t * p.sq[2] + ch * 8);
+                                                (w.h * p.G + n - t * p.G) * p.sq[1] + t * p.sq[2] + ch * 8);
       }
     }
 #pragma unroll
     for (int e8 = 0; e8 < kBatch; ++e8) {
       const int i = (i0 + e8) * NT + id;
-      const int n = i / kChunks, ch = i % kChunks;
-      const int tile = n / NR, r = n % NR;
-      if (n >= TILES * NR) continue;  // whole warps: a row is held by neighbouring lanes
+      const int r = i / kChunks, ch = i % kChunks;
+      if (r >= NR) continue;  // whole warps: a row is held by neighbouring lanes
       const uint4 v = q4[e8];
-      uint8_t* qt = q_smem + tile * C::kQTile;
       if constexpr (!FP8) {
-        *reinterpret_cast<uint4*>(qt + (ch >> 3) * NR * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+        *reinterpret_cast<uint4*>(q_smem + (ch >> 3) * NR * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
       } else {
         // 2⁻ᵃ brings the row's largest magnitude to at most 448.
         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
@@ -369,19 +274,19 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const Walk& w, uint8
         }
         // Rows of D bytes; chunk of 16 bytes XORed with the row (128-byte rows) or half of it (64-byte rows).
         const int sw = D == 128 ? r & 7 : (r >> 1) & 3;  // NR is a multiple of 16: the same for rows r and NR + r
-        uint8_t* dst = qt + r * D + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
+        uint8_t* dst = q_smem + r * D + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
         *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(dst + NR * D) = make_uint2(lo[0], lo[1]);
-        if (ch == 0) f[tile][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
+        if (ch == 0) f[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
       }
     }
   }
   fence_proxy_async_smem();
 }
 
-template <int D, bool FP8, int NR, int TILES>
-__global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-  using C = Cfg<D, FP8, NR, TILES>;
+template <int D, bool FP8, int NR>
+__global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  using C = Cfg<D, FP8, NR>;
   constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
   constexpr int kSlot = C::kSlot, kThreads = C::kThreads, kSub = C::kSub;
   constexpr int kWarp0 = C::kSoftmax / 32;  // first warp after the softmax ones
@@ -398,9 +303,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // broadcast: known to be the same in the warp
   const int lane = tid & 31;
-  const int rt = blockIdx.x % p.row_tiles;   // neighbours share their keys in L2
-  const int part = blockIdx.x / p.row_tiles;
-  const int row0 = rt * NR * TILES;
+  const int part = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this grid's end
 
   if (tid == 0) {
@@ -410,15 +313,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
     }
     for (int s = 0; s < C::kRV; ++s) {
       mbar_init(&ms->v_full[s], 1);
-      mbar_init(&ms->v_empty[s], FP8 ? 4 * kSub * TILES : 1);
+      mbar_init(&ms->v_empty[s], FP8 ? 4 * kSub : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
       mbar_init(&ms->s_free[s], 128 * kSub);
       mbar_init(&ms->p_full[s], 128 * kSub);
       mbar_init(&ms->p_free[s], 1);
-      mbar_init(&ms->v16_full[s], C::kSoftmax);
-      mbar_init(&ms->v16_empty[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
     mbar_init(&ms->q_full, 32);
@@ -432,56 +333,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
     tmem_alloc(&ms->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-
-  // This CTA's part of the line of tiles: sums over the sequences, one block of them per thread.
-  const int per_thread = (p.B + kThreads - 1) / kThreads;
-  const int sb0 = min(p.B, tid * per_thread), sb1 = min(p.B, sb0 + per_thread);
-  long long mine = 0;
-  for (int b = sb0; b < sb1; ++b) {
-    int len, drafts;
-    seq_lengths(p, b, len, drafts);
-    mine += seq_tiles(len, drafts);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) ms->warp_sum[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += ms->warp_sum[w];
-    total += ms->warp_sum[w];
-  }
-  total *= p.Hkv;
-  before *= p.Hkv;
-  const long long per = part_tiles(total, p.parts);
-  const long long first = part * per;
-  const long long count = min(per, total - first);
-  if (first >= before && first < before + mine * p.Hkv) {
-    long long at = first - before;
-    for (int b = sb0; b < sb1; ++b) {
-      int len, drafts;
-      seq_lengths(p, b, len, drafts);
-      const int n = seq_tiles(len, drafts);
-      if (at < static_cast<long long>(n) * p.Hkv) {
-        ms->start_b = b;
-        ms->start_h = static_cast<int>(at / n);
-        ms->start_tile = static_cast<int>(at % n);
-        break;
-      }
-      at -= static_cast<long long>(n) * p.Hkv;
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  const TreePart my = find_part<kThreads>(p, part, ms->warp_sum, ms->start);
   const uint32_t tmem = ms->tmem_base;
   const int bshift = 31 - __clz(p.block_size);  // a power of two
 
-  if (count <= 0) {
+  if (my.count <= 0) {
     // nothing left for this CTA
   } else if (warp == kWarp0 || warp == kWarp0 + 2) {
     reg_dealloc<C::kRegsOther>();
@@ -497,7 +353,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
     int slot = 0, sc = 0, issued = 0;
     uint32_t parity = 1;
     bool ok = true;
-    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
+    TreeWalk w(p, my);
     do {
       const int pages = (w.len + p.block_size - 1) >> bshift;
       const int32_t* table = p.block_table + static_cast<int64_t>(w.b) * p.max_blocks;
@@ -505,12 +361,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
       int page = w.t0 * npt + lane;
       int id = 0, ahead = page < pages ? table[page] : 0;
       int at = 32;  // the tile's first page in the group
-      for (int i = w.t0; ok && i < w.t1; ++i) {
+#pragma unroll 1
+      for (int i = w.t0; i < w.t1; ++i) {
         if (at == 32) {
           at = 0;
           id = page < pages ? ahead : -1;  // −1: past the end
           if (page < pages && (id < 0 || id >= p.num_blocks)) {
-            atomicCAS(p.err + 1, 0u, (kKernTree << 8) | kSiteBadBlock);
+            report_bad_page(p);
             id = 0;
           }
           page += 32;
@@ -518,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
         }
         const int blk = __shfl_sync(0xffffffffu, id, at + lane);
         at += npt;
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, site(is_v ? 2 : 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, tree_site(is_v ? 2 : 1)));
         if (!ok) break;
         const bool real = lane < npt && blk >= 0;
         const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
@@ -551,9 +408,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
       }
     } while (ok && w.next());
     if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA ends
+#pragma unroll 1
       for (int n = max(0, issued - ring); n < issued; ++n) {
-        mbar_wait_drain_inl(&full[n % ring], (n / ring) & 1, kDrainNs);
-        if (FP8 && is_v) mbar_wait_drain_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, kDrainNs);
+        mbar_wait_drain_inl(&full[n % ring], (n / ring) & 1, kTreeDrainNs);
+        if (FP8 && is_v) mbar_wait_drain_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, kTreeDrainNs);
       }
     }
   } else if (warp == kWarp0 + 1) {
@@ -563,97 +421,78 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
     constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
     constexpr uint32_t kIdescO = FP8 ? idesc_f16_f32(128, NR, true, true) : idesc_bf16_f32(128, C::kPCols, true, true);
     const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK), sP = smem_u32(smem + C::kOffP);
-    const uint32_t sV = smem_u32(smem + C::kOffV), sV16 = smem_u32(smem + C::kOffV16);
-    const bool leader = elect_one();
-    auto agree = [](bool v) { return static_cast<bool>(__all_sync(0xffffffffu, v)); };
+    const uint32_t sV = smem_u32(smem + (FP8 ? C::kOffV16 : C::kOffV));
+    const uint64_t q_desc = FP8 && D == 64 ? sdesc_sw64(sQ, 16, 512) : sdesc_sw128(sQ, 16, 1024);
+    const bool leader = elect_one_lane();
     Ring<C::kRK> rk;
     Ring<C::kRV> rv;
-    Ring<2> r16;                 // two row tiles: the widened V tile
     uint32_t s_par = 3, p_par = 0;  // parities of s_free and p_full to wait for, a bit per stream
     bool ok = true;
-    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
+    TreeWalk w(p, my);
     do {
-      // Step s: stream s & 1, tile s (or s / 2).  Broadcast, like the walk's end below, to keep the loop uniform.
-      const int steps = __shfl_sync(0xffffffffu, (w.t1 - w.t0) * TILES, 0);
-      ok = agree(mbar_wait_inl(&ms->q_full, w.index & 1, abort_flag, p.err, site(14)));
-      auto issue_s = [&](int s) -> bool {
+      // Tile s of the piece belongs to stream s & 1.  Broadcast, like the walk's end below, to keep the loop uniform.
+      const int tiles = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+      ok = mbar_wait_inl(&ms->q_full, w.index & 1, abort_flag, p.err, tree_site(14));
+      // S runs two tiles ahead, so that a stream's next scores are ready when it has stored P̃.
+#pragma unroll 1
+      for (int s = 0; s < tiles + 2; ++s) {
         const int g = s & 1;
-        const bool k_done = TILES == 1 || g == 1;  // the last use of the K tile
-        if (!agree(mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, site(5)) &&
-                   mbar_wait_inl(&ms->s_free[g], (s_par >> g) & 1u, abort_flag, p.err, site(6))))
-          return false;
-        s_par ^= 1u << g;
-        tc_fence_after();
-        const uint32_t kb = sK + rk.slot * kSlot;
-        const uint32_t qb = sQ + (TILES == 1 ? 0 : g * C::kQTile);
-        const uint32_t ds = tmem + g * C::kSCols;
-        if (leader) {
-          // Descriptors of the k-steps differ from the first ones by their start addresses alone.
-          if constexpr (FP8) {
-            const uint64_t ad = D == 128 ? sdesc_sw128(kb, 16, 1024) : sdesc_sw64(kb, 16, 512);
-            const uint64_t bd = D == 128 ? sdesc_sw128(qb, 16, 1024) : sdesc_sw64(qb, 16, 512);
+        if (s < tiles) {
+          ok = ok && mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, tree_site(5)) &&
+               mbar_wait_inl(&ms->s_free[g], (s_par >> g) & 1u, abort_flag, p.err, tree_site(6));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          s_par ^= 1u << g;
+          tc_fence_after();
+          const uint32_t kb = sK + rk.slot * kSlot;
+          const uint32_t ds = tmem + g * C::kSCols;
+          if (leader) {
+            // Descriptors of the k-steps differ from the first ones by their start addresses alone.
+            if constexpr (FP8) {
+              const uint64_t ad = D == 128 ? sdesc_sw128(kb, 16, 1024) : sdesc_sw64(kb, 16, 512);
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) mma_e4m3_ss(ds, ad + kk * 2, bd + kk * 2, kIdescS, kk > 0 ? 1u : 0u);
-          } else {
-            const uint64_t ad = sdesc_sw128(kb, 16, kPg5 ? 2048 : 1024);
-            const uint64_t bd = sdesc_sw128(qb, 16, 1024);
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_e4m3_ss(ds, ad + kk * 2, q_desc + kk * 2, kIdescS, kk > 0 ? 1u : 0u);
+            } else {
+              const uint64_t ad = sdesc_sw128(kb, 16, kPg5 ? 2048 : 1024);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ss(ds, ad + (kk >> 2) * 64 + (kk & 3) * 2, bd + (kk >> 2) * (NR * 8) + (kk & 3) * 2, kIdescS,
-                          kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_bf16_ss(ds, ad + (kk >> 2) * 64 + (kk & 3) * 2, q_desc + (kk >> 2) * (NR * 8) + (kk & 3) * 2,
+                            kIdescS, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&ms->s_full[g]);
+            mma_commit(&ms->k_empty[rk.slot]);
+            if (s == tiles - 1) mma_commit(&ms->q_empty);
           }
-          mma_commit(&ms->s_full[g]);
-          if (k_done) mma_commit(&ms->k_empty[rk.slot]);
-          if (s == steps - 1) mma_commit(&ms->q_empty);
+          rk.advance();
         }
-        if (k_done) rk.advance();
-        return true;
-      };
-      auto issue_pv = [&](int s) -> bool {
-        const int g = s & 1;
-        const bool v_done = TILES == 1 || g == 1;  // the last use of the V tile
-        bool ready = mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, site(3));
-        if constexpr (!FP8)
-          ready = mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, site(4)) && ready;
-        else if constexpr (TILES == 2)
-          ready = mbar_wait_inl(&ms->v16_full[r16.slot], r16.parity, abort_flag, p.err, site(4)) && ready;
-        if (!agree(ready)) return false;
-        p_par ^= 1u << g;
-        tc_fence_after();
-        const uint32_t vb = FP8 ? sV16 + (TILES == 1 ? g : r16.slot) * C::kV16 : sV + rv.slot * kSlot;
-        const uint32_t pb = sP + g * C::kP;
-        const uint32_t dst = tmem + C::kColO + g * C::kPCols;
-        if (leader) {
-          // A: 16 keys per k-step, the head dim along M in 64-element blocks (D = 64: the one block twice, the upper 64
-          // rows of the result are not read).  B: 16 keys of P̃ᵀ.
-          const uint64_t ad = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, D == 128 ? kBN * 128 : 0, 1024);
-          const uint64_t bd = sdesc_sw128(pb, kPBlock, 1024);
+        if (s >= 2) {  // the second product of tile s − 2, of the same stream
+          ok = ok && mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(3));
+          if constexpr (!FP8) ok = ok && mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(4));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          p_par ^= 1u << g;
+          tc_fence_after();
+          const uint32_t vb = sV + (FP8 ? g * C::kV16 : rv.slot * kSlot);
+          const uint32_t dst = tmem + C::kColO + g * C::kPCols;
+          if (leader) {
+            // A: 16 keys per k-step, the head dim along M in 64-element blocks (D = 64: the one block twice, the upper
+            // 64 rows of the result are not read).  B: 16 keys of P̃ᵀ.
+            const uint64_t ad = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, D == 128 ? kBN * 128 : 0, 1024);
+            const uint64_t bd = sdesc_sw128(sP + g * C::kP, kPBlock, 1024);
 #pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk)
-            mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + kk * 128, kIdescO, (s >= 2 || kk > 0) ? 1u : 0u);
-          mma_commit(&ms->p_free[g]);
-          if (v_done) {
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + kk * 128, kIdescO, (s >= 4 || kk > 0) ? 1u : 0u);
+            mma_commit(&ms->p_free[g]);
             if constexpr (!FP8) mma_commit(&ms->v_empty[rv.slot]);
-            else if constexpr (TILES == 2) mma_commit(&ms->v16_empty[r16.slot]);
           }
-        }
-        if (v_done) {
           rv.advance();
-          r16.advance();
         }
-        return true;
-      };
-      // S runs two steps ahead, so that a stream's next scores are ready when it has stored P̃.
-      ok = ok && issue_s(0);
-      if (ok && steps > 1) ok = issue_s(1);
-      for (int s = 0; ok && s < steps; ++s) {
-        if (s + 2 < steps) ok = issue_s(s + 2);
-        ok = ok && issue_pv(s);
       }
     } while (ok && __shfl_sync(0xffffffffu, w.next(), 0));
     if (*abort_flag && leader) {
       mma_commit(&ms->drain);
-      mbar_wait_drain_inl(&ms->drain, 0, kDrainNs);
+      mbar_wait_drain_inl(&ms->drain, 0, kTreeDrainNs);
     }
   } else if (warp < kWarp0) {
     reg_alloc<C::kRegsSoftmax>();
@@ -661,70 +500,68 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
     constexpr int NC = C::kNC;
     const int g = warp / (4 * kSub);
     const int sub = kSub == 1 ? 0 : (warp >> 2) & 1;
-    const int col0 = sub * NC;                                // first row in the stream's tile
-    const int bar = 1 + g * kSub + sub;                       // the warpgroup's barrier
-    const int end_bar = TILES == 1 ? 5 + sub : bar;           // those that finish a piece together: the warpgroups
-    constexpr int kEndThreads = TILES == 1 ? 256 : 128;       // of both streams that share rows, or one alone
-    const int kt = tid & 127;  // key in the tile, TMEM lane, head dim of O
+    const int col0 = sub * NC;             // first row of the warpgroup
+    const int bar = 1 + g * kSub + sub;    // the warpgroup's barrier
+    const int end_bar = 5 + sub;           // that of the warpgroups of both streams that share these rows
+    const int kt = tid & 127;              // key in the tile, TMEM lane, head dim of O
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lane_base + g * C::kSCols + col0;
     const uint32_t o_addr = tmem + lane_base + C::kColO + g * C::kPCols + col0;
     float* nm = ms->nm[g] + col0;
     float* corr = ms->corr[g] + col0;
-    float* red = ms->red[g][0] + col0;        // + warp·NR
+    float* red = ms->red[g][0] + col0;     // + warp·NR
     int64_t* row = ms->row[g] + col0;
     int64_t* o_off = ms->o_off[g] + col0;
-    int tile0 = 0;             // tiles of the pieces before, and those of this stream
+    int* fresh = ms->fresh[g] + col0;
+    int tile0 = 0;                         // tiles of the pieces before, and those of this stream
     int used = 0;
     bool ok = true;
-    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
-    load_q<D, FP8, NR, TILES, C::kSoftmax>(p, w, smem + C::kOffQ, ms->f[0], row0, tid);
+    TreeWalk w(p, my);
+    load_q<D, FP8, NR, C::kSoftmax, 4>(p, w, smem + C::kOffQ, ms->f[0], tid);
     named_sync(7, C::kSoftmax);
     if (warp == 0) mbar_arrive(&ms->q_full);
+#pragma unroll 1
     do {
       const int n_tiles = w.t1 - w.t0;
       const int context = w.len - w.drafts;
-      const int my_row0 = row0 + (TILES == 1 ? 0 : g * NR) + col0;
-      const int live = w.drafts * p.G - my_row0;  // rows of this warpgroup that belong to a drafted token
+      const int live = w.drafts * p.G - col0;  // rows of this warpgroup that belong to a drafted token
       if (kt < NC) {
-        const int rr = my_row0 + kt;
-        const int t = rr / p.G;
+        const int rr = col0 + kt;
+        const int t = token_of(p, rr);
         const int h = w.h * p.G + (rr - t * p.G);
         row[kt] = kt < live ? (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t : -1;
         o_off[kt] = w.b * p.so[0] + h * p.so[1] + static_cast<int64_t>(t) * p.so[2];
-        nm[kt] = INFINITY;
+        nm[kt] = 0.f;
+        fresh[kt] = kt < live;
       }
-      // Does row n of this tile (a live one) see drafted key u?
-      auto sees = [&](int n, int u) -> bool {
-        const int t = (my_row0 + n) / p.G;
-        return p.mask != nullptr ? p.mask[w.b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t;
-      };
       named_sync(bar, 128);
+      bool unseen = true;  // some row of the warpgroup may have seen nothing yet
       float l[NC];
 #pragma unroll
       for (int n = 0; n < NC; ++n) l[n] = 0.f;
       int kv_ref = -1024;
       int done = 0;  // tiles of this piece that this stream has worked on
-      const float* f_row = ms->f[w.index % kFRing][TILES == 1 ? 0 : g] + col0;
-      for (int i = TILES == 1 ? g : 0; i < n_tiles; i += TILES == 1 ? 2 : 1, ++done) {
+      const float* f_row = ms->f[w.index % kFRing] + col0;
+#pragma unroll 1
+      for (int i = g; i < n_tiles; i += 2, ++done) {
         const int tile = tile0 + i;
         const int u = used + done;
         const int key = (w.t0 + i) * kBN + kt;
         const bool tail = (w.t0 + i + 1) * kBN > context;  // the tile holds drafted keys or the end
         // Which rows see this key (bit per row); context keys are seen by all.
-        uint64_t seen = ~0ull;
+        uint32_t seen = 0xffffffffu;
         if (tail && key >= context) {
           seen = 0;
           if (key < w.len && live > 0) {
             // Token by token: one byte of the mask stands for G rows.
-            const int ta = my_row0 / p.G;
-            const int tb = min(w.drafts - 1, (my_row0 + min(NC, live) - 1) / p.G);
+            const int ta = token_of(p, col0);
+            const int tb = token_of(p, col0 + min(NC, live) - 1);
             const uint8_t* mk = p.mask != nullptr ? p.mask + w.b * p.mask_sb + (key - context) : nullptr;
 #pragma unroll 4
             for (int t = ta; t <= tb; ++t) {
               const bool on = mk != nullptr ? mk[static_cast<int64_t>(t) * p.T] != 0 : key - context <= t;
-              const int lo = max(0, t * p.G - my_row0), hi = min(NC, (t + 1) * p.G - my_row0);  // its rows
-              const uint64_t bits = (hi - lo >= 64 ? ~0ull : (1ull << (hi - lo)) - 1) << lo;
+              const int lo = max(0, t * p.G - col0), hi = min(NC, (t + 1) * p.G - col0);  // its rows
+              const uint32_t bits = (0xffffffffu >> (32 - (hi - lo))) << lo;
               seen |= on ? bits : 0;
             }
           }
@@ -733,40 +570,34 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
         float ks = 1.f;
         int kv = -1024;
         if constexpr (FP8) {
-          ok = mbar_wait_inl(&ms->sc_full[tile % kScaleRing], (tile / kScaleRing) & 1, abort_flag, p.err, site(13)) && ok;
+          ok = mbar_wait_inl(&ms->sc_full[tile % kScaleRing], (tile / kScaleRing) & 1, abort_flag, p.err, tree_site(13)) && ok;
           const uint32_t sk = ms->k_scale[tile % kScaleRing][kt];
           ks = sk == 0 ? 5.877471754111438e-39f : __uint_as_float(sk << 23);
           if (key < w.len) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
-        }
-        if constexpr (FP8) {
-          // This key's value row, or the warpgroup's share of it, to fp16, while the scores are made.
-          constexpr int kN = D / 16 / (TILES * kSub);
-          const int buf = TILES == 1 ? g : tile & 1;
+          // This key's value row, or the warpgroup's half of it, to fp16, while the scores are made.
+          constexpr int kN = D / 16 / kSub;
           const int slot = tile % C::kRV;
-          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, site(11)) && ok;
-          if constexpr (TILES == 1) {
-            if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, site(8)) && ok;
-          } else {
-            ok = mbar_wait_inl(&ms->v16_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, site(12)) && ok;
-          }
+          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(11)) && ok;
+          if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
           const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
-          uint8_t* dst = smem + C::kOffV16 + buf * C::kV16 + kt * 128;
-          const int c0 = (TILES == 1 ? sub : g * kSub + sub) * kN;
+          uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
           if (!tail) {
-            widen_row<D, kN, false>(src, dst, kt, c0, false, false);
-          } else if (widen_row<D, kN, true>(src, dst, kt, c0, key >= context, key >= w.len) && key < w.len) {
+            widen_row<D, kN, false>(src, dst, kt, sub * kN, false, false);
+          } else if (widen_row<D, kN, true>(src, dst, kt, sub * kN, key >= context, key >= w.len) && key < w.len) {
             atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
           }
           fence_proxy_async_smem();
-          if constexpr (TILES == 2) mbar_arrive(&ms->v16_full[buf]);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
         }
-        ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, site(7)) && ok;
+        ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, tree_site(7)) && ok;
         tc_fence_after();
-        // x = score − reference, masked to −∞ where the row does not see the key.
+        // x = score − reference, masked to −∞ where the row does not see the key.  A second time where a reference
+        // has moved.
         float x[NC];
-        auto scores = [&](bool relative) {
+        bool dead = false;  // a wait of some thread of the warpgroup has failed
+#pragma unroll 1
+        for (bool again = false;; again = true) {
           // 16 rows at a time; with registers to spare the next ones are on their way from TMEM meanwhile.
           constexpr int kC = 16;
           constexpr int kBuf = kSub == 1 && NC > kC ? 2 : 1;
@@ -799,7 +630,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
                 fmul2(f4.x, f4.y, f4.x, f4.y, ks, ks);
                 fmul2(f4.z, f4.w, f4.z, f4.w, ks, ks);
               }
-              const float4 m4 = relative ? *reinterpret_cast<const float4*>(&nm[n]) : make_float4(0.f, 0.f, 0.f, 0.f);
+              const float4 m4 = *reinterpret_cast<const float4*>(&nm[n]);
               ffma2(x[n], x[n + 1], r4.x, r4.y, f4.x, f4.y, m4.x, m4.y);
               ffma2(x[n + 2], x[n + 3], r4.z, r4.w, f4.z, f4.w, m4.z, m4.w);
             }
@@ -809,23 +640,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
             for (int n = 0; n < NC; ++n)
               if (!((seen >> n) & 1)) x[n] = -INFINITY;
           }
-        };
-        scores(true);
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+          if (again) break;
+          float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int n = 4; n < NC; n += 8)
+          for (int n = 4; n < NC; n += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = n + 4 + e < NC ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NC]) : fmaxf(mx[e], x[n + e]);
-        const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-        const bool over = top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
-        if (named_any(bar, 128, over || !ok)) {
+            for (int e = 0; e < 4; ++e)
+              mx[e] = n + 4 + e < NC ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NC]) : fmaxf(mx[e], x[n + e]);
+          const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          const bool over = unseen || top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
+          if (!named_any(bar, 128, over || !ok)) break;
           // A reference moves (the first tile always does): exchange the tile's maxima, rescale ℓ and O.
           if (named_any(bar, 128, !ok)) {
             ok = false;
+            dead = true;
             break;
           }
-          scores(false);
           reduce_cols<NC>(x, lane, OpMax(), red + (warp & 3) * NR);
           if constexpr (FP8) {
             const int top_kv = __reduce_max_sync(0xffffffffu, kv);
@@ -837,36 +667,37 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
             const int* kr = ms->kv_red[g][sub];
             kv_new = max(kv_ref, max(max(kr[0], kr[1]), max(kr[2], kr[3])));
           }
+          bool still = false;
           if (kt < NC) {
-            const float old = -nm[kt];
+            // Maxima relative to the old reference (0 for a row that has seen nothing).
             const float now = fmaxf(fmaxf(red[kt], red[NR + kt]), fmaxf(red[2 * NR + kt], red[3 * NR + kt]));
-            const bool up = now > -INFINITY && now - kBase > old;
-            corr[kt] = up ? exp2f(old - (now - kBase)) : 1.f;  // 0 from −∞: nothing was summed yet
-            if (up) nm[kt] = kBase - now;
+            const bool first = fresh[kt] != 0;
+            const bool up = now > -INFINITY && (first || now > kBase);
+            corr[kt] = !up ? 1.f : first ? 0.f : exp2f(kBase - now);
+            if (up) {
+              nm[kt] += kBase - now;
+              fresh[kt] = 0;
+            }
+            still = first && !up;
           }
-          named_sync(bar, 128);
+          unseen = named_any(bar, 128, still);
 #pragma unroll
           for (int n = 0; n < NC; ++n) l[n] *= corr[n];
           if (done > 0) {
-            ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, site(8)) && ok;
+            ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
             tc_fence_after();
             const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
-            rescale_cols<NC>(o_addr, corr, kf);
-            if constexpr (C::kTerms == 2) rescale_cols<NC>(o_addr + NR, corr, kf);
+#pragma unroll 1
+            for (int term = 0; term < C::kTerms; ++term) rescale_cols<NC>(o_addr + term * NR, corr, kf);
           }
           kv_ref = kv_new;
-          scores(true);
-          // A row that has seen nothing has the reference −∞, and only masked scores: −∞ − (−∞) is −∞ here.
-#pragma unroll
-          for (int n = 0; n < NC; ++n)
-            if (nm[n] == INFINITY) x[n] = -INFINITY;
         }
+        if (dead) break;
         tc_fence_before();
         mbar_arrive(&ms->s_free[g]);
 
-        // P̃'s buffer is free once the product of the stream's tile before has run.
-        if ((!FP8 || TILES == 2) && u > 0)
-          ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, site(8)) && ok;
+        // P̃'s buffer is free once the product of the stream's tile before has run (E4M3 has waited for it above).
+        if (!FP8 && u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
         // E4M3: the value row's scale relative to the running maximum, a power of two, at most 2^kKvLazy.
         const float wv = !FP8 ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
         uint8_t* prow = smem + C::kOffP + g * C::kP + kt * 128;
@@ -885,28 +716,26 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
               hi[e] = pack_f16x2(a, d);
             } else {
               hi[e] = pack_bf16x2(x[n], x[n + 1]);
-              if constexpr (C::kTerms == 2)
-                lo[e] = pack_bf16x2(x[n] - __uint_as_float(hi[e] << 16), x[n + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+              lo[e] = pack_bf16x2(x[n] - __uint_as_float(hi[e] << 16), x[n + 1] - __uint_as_float(hi[e] & 0xffff0000u));
             }
           }
           const int c1 = col0 / 8 + ch;
           *reinterpret_cast<uint4*>(prow + ((c1 ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if constexpr (C::kTerms == 2) {
+          if constexpr (!FP8) {
             const int c2 = c1 + NR / 8;  // column chunk of the second term
             *reinterpret_cast<uint4*>(prow + (c2 >> 3) * kPBlock + (((c2 & 7) ^ (kt & 7)) << 4)) =
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
-        if (!FP8 && tail && key >= context && (TILES == 1 || g == 0)) {
-          // This key's value row, or the warpgroup's share of it: zeros past the end, and in place of what a drafted row
-          // holds that is not finite.  (Two row tiles: the first stream does it for both, its product is issued first.)
+        if (!FP8 && tail && key >= context) {
+          // This key's value row, or the warpgroup's half of it: zeros past the end, and in place of what a drafted row
+          // holds that is not finite.
           const int slot = tile % C::kRV;
-          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, site(9)) && ok;
+          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(9)) && ok;
           uint8_t* vr = smem + C::kOffV + slot * kSlot + (kPg5 ? (kt >> 3) * 2048 + (kt & 7) * 128 : kt * 128);
           bool bad = false;
-#pragma unroll
-          for (int e8 = 0; e8 < D / 8 / kSub; ++e8) {
-            const int ch = sub * (D / 8 / kSub) + e8;
+#pragma unroll 2
+          for (int ch = sub * (D / 8 / kSub); ch < (sub + 1) * (D / 8 / kSub); ++ch) {
             uint4* at = reinterpret_cast<uint4*>(vr + (ch >> 3) * 1024 + (ch & 7) * 16);
             uint32_t v4[4] = {0, 0, 0, 0};
             if (key < w.len) {
@@ -930,123 +759,119 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR, TILES>::kThreads, 1) tree_kern
       used += done;
       // ------------------------------------------------------------ end of the piece
       // (Its barriers are joined by all threads whatever the waits said.)
-      if (done > 0) ok = ok && mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, site(10));
+      if (done > 0) ok = ok && mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, tree_site(10));
       reduce_cols<NC>(l, lane, OpAdd(), red + (warp & 3) * NR);
-      if (kt == 0) ms->kv_ref[g][sub] = kv_ref;
       tc_fence_before();
-      named_sync(end_bar, kEndThreads);
+      named_sync(end_bar, 256);
       tc_fence_after();
-      const bool whole = w.t0 == 0 && w.t1 == w.tiles;
-      // The slot of a piece: numbered along the line, or two per part (a part has a piece at each end at most).
-      const long long pair = static_cast<long long>(w.b) * p.Hkv + w.h;
-      const long long slot = p.slots_by_pair ? pair + part : 2ll * part + (w.t0 > 0 ? 0 : 1);
+      const bool whole = w.whole();
+      const int64_t slot_row = w.slot(part) * p.T * p.G + col0;  // first row of the piece's slot
       if (kt < NC) {
-        // The streams' sums (both, where they share rows) in a fixed order: the same result every time.
+        // Both streams' sums in a fixed order: the same result every time.
         float sums[2], m = -INFINITY, sum = 0.f, mine = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (TILES == 2 && e != g) continue;
           const float* r4 = ms->red[e][0] + col0 + kt;
           sums[e] = (r4[0] + r4[NR]) + (r4[2 * NR] + r4[3 * NR]);
-          m = fmaxf(m, -ms->nm[e][col0 + kt]);
+          if (sums[e] != 0.f) m = fmaxf(m, -ms->nm[e][col0 + kt]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (TILES == 2 && e != g) continue;
           const float wgt = sums[e] == 0.f ? 0.f : exp2f(-ms->nm[e][col0 + kt] - m);
           sum += sums[e] * wgt;
           if (e == g) mine = wgt;
         }
-        if (ok && row[kt] >= 0 && (TILES == 2 || g == 0)) {
+        if (ok && row[kt] >= 0 && g == 0) {
           if (!whole) {
-            float* ml = p.part_ml + (slot * p.T * p.G + my_row0 + kt) * 2;
-            ml[0] = m;
-            ml[1] = sum;
+            p.part_ml[(slot_row + kt) * 2] = m;
+            p.part_ml[(slot_row + kt) * 2 + 1] = sum;
           } else if (p.lse != nullptr) {
             p.lse[row[kt]] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           }
         }
         // What this stream's O is multiplied by.
         mine *= sum != 0.f ? 1.f / sum : 0.f;
-        ms->lsum[g][col0 + kt] = mine * (FP8 ? exp2f(static_cast<float>(max(kv_ref, -300))) : 1.f);
+        ms->scale[g][col0 + kt] = mine * (FP8 ? exp2f(static_cast<float>(max(kv_ref, -300))) : 1.f);
       }
-      if (w.t0 == 0 && rt == 0 && tid == 0) {
-        // For the joining kernel: the pair's first part and how many parts it lies in.
-        const long long start = static_cast<long long>(part) * per + (count - w.left - (w.t1 - w.t0));
-        p.pieces[pair] = make_int2(part, static_cast<int>((start + w.tiles - 1) / per) - part + 1);
-      }
-      named_sync(end_bar, kEndThreads);
+      if (w.t0 == 0 && tid == 0) p.pieces[w.pair()] = w.pieces(part, my.per);
+      named_sync(end_bar, 256);
       const uint32_t* bad = ms->bad[w.index % kBadRing];
-      bool any_bad = false;
-      for (int e = 0; e < 8; ++e) any_bad = any_bad || bad[e] != 0;
-      // Rows that this warpgroup writes: half of the shared ones, or its own.
-      constexpr int kOut = TILES == 1 ? NC / 2 : NC;
-      constexpr int kStep = kOut < 16 ? kOut : 16;
+      // Rows that this warpgroup writes: half of the shared ones.
+      constexpr int kOut = NC / 2;
+      const int c0 = g * kOut;
       if (__all_sync(0xffffffffu, ok) && kt < D) {
+        float o[kOut];
 #pragma unroll
-        for (int cc = 0; cc < kOut; cc += kStep) {
-          const int c0 = (TILES == 1 ? g * kOut : 0) + cc;
-          float o[kStep];
+        for (int q = 0; q < kOut; ++q) o[q] = 0.f;
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {  // streams
+#pragma unroll 1
+          for (int term = 0; term < C::kTerms; ++term) {
+            uint32_t r[kOut];
+            tmem_ld(tmem + lane_base + C::kColO + e * C::kPCols + term * NR + col0 + c0, r);
+            tmem_wait_ld();
+            reg_fence(r);
 #pragma unroll
-          for (int e = 0; e < kStep; ++e) o[e] = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // streams
-            if (TILES == 2 && e != g) continue;
-#pragma unroll
-            for (int term = 0; term < C::kTerms; ++term) {
-              uint32_t r[kStep];
-              tmem_ld(tmem + lane_base + C::kColO + e * C::kPCols + term * NR + col0 + c0, r);
-              tmem_wait_ld();
-              reg_fence(r);
-#pragma unroll
-              for (int q = 0; q < kStep; ++q) {
-                const float k = ms->lsum[e][col0 + c0 + q];
-                if (k != 0.f) o[q] += __uint_as_float(r[q]) * k;  // 0: a stream without keys has left O unwritten
-              }
+            for (int q = 0; q < kOut; ++q) {
+              const float k = ms->scale[e][col0 + c0 + q];
+              if (k != 0.f) o[q] += __uint_as_float(r[q]) * k;  // 0: a stream without keys has left O unwritten
             }
           }
-          if (any_bad) {
-            for (int u = 0; u < w.drafts; ++u) {
-              if (!((bad[u >> 5] >> (u & 31)) & 1)) continue;
-              const int key = context + u;
-              const int64_t at = ((static_cast<int64_t>(checked_page(p, w.b, key >> bshift)) * p.Hkv + w.h) * p.block_size +
-                                  (key & (p.block_size - 1))) * D + kt;
-              float v;
-              if (FP8)
-                v = (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
-              else
-                v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
-              if (fabsf(v) <= 3.4028234663852886e38f) continue;
+        }
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + kt;
+        float* part_o = p.part_o + (slot_row + c0) * D + kt;
 #pragma unroll
-              for (int q = 0; q < kStep; ++q)
-                if (c0 + q < live && sees(c0 + q, u)) o[q] += v;
-            }
+        for (int q = 0; q < kOut; ++q) {
+          if (row[c0 + q] >= 0) {
+            if (!whole)
+              part_o[q * D] = o[q];
+            else
+              out[o_off[c0 + q]] = __float2bfloat16_rn(o[q]);
           }
-#pragma unroll
-          for (int q = 0; q < kStep; ++q) {
-            if (row[c0 + q] >= 0) {
-              if (!whole)
-                p.part_o[(slot * p.T * p.G + my_row0 + c0 + q) * D + kt] = o[q];
-              else
-                static_cast<__nv_bfloat16*>(p.o)[o_off[c0 + q] + kt] = __float2bfloat16_rn(o[q]);
-            }
+        }
+        // What was taken out of drafted value rows goes to the rows that see them.
+        for (int u = 0; u < w.drafts; ++u) {
+          if (bad[u >> 5] == 0) {
+            u |= 31;
+            continue;
+          }
+          if (!((bad[u >> 5] >> (u & 31)) & 1)) continue;
+          const int key = context + u;
+          int blk = p.block_table[static_cast<int64_t>(w.b) * p.max_blocks + (key >> bshift)];
+          if (blk < 0 || blk >= p.num_blocks) blk = 0;
+          const int64_t at =
+              (((static_cast<int64_t>(blk) * p.Hkv + w.h) << bshift) + (key & (p.block_size - 1))) * D + kt;
+          float v;
+          if (FP8)
+            v = (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
+          else
+            v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
+          if (fabsf(v) <= 3.4028234663852886e38f) continue;
+#pragma unroll 1
+          for (int q = 0; q < kOut; ++q) {
+            if (row[c0 + q] < 0 || !token_sees(p, w.b, token_of(p, col0 + c0 + q), u)) continue;
+            if (!whole)
+              part_o[q * D] += v;
+            else
+              out[o_off[c0 + q]] = __float2bfloat16_rn(__bfloat162float(out[o_off[c0 + q]]) + v);
           }
         }
       }
       tc_fence_before();
       // All have read O and the statistics; any failed wait ends the walk for all.
-      ok = !named_any(end_bar, kEndThreads, !ok);
-      // The flags of three pieces ago: other warpgroups may still be at the piece before.
+      ok = !named_any(end_bar, 256, !ok);
+      // The flags of three pieces ago: the other warpgroups may still be at the piece before.
       if (tid < 8) ms->bad[(w.index + kBadRing - 3) % kBadRing][tid] = 0;
     } while (ok && w.next());
   } else {
     reg_dealloc<C::kRegsOther>();
     // ------------------------- Q of every piece but the first, which the streams load
-    Walk w(p, ms->start_b, ms->start_h, ms->start_tile, count);
+    TreeWalk w(p, my);
+#pragma unroll 1
     while (w.next()) {
       // Once the first products of the piece before are done.
-      if (!__all_sync(0xffffffffu, mbar_wait_inl(&ms->q_empty, (w.index & 1) ^ 1, abort_flag, p.err, site(15)))) break;
-      load_q<D, FP8, NR, TILES, 32>(p, w, smem + C::kOffQ, ms->f[w.index % kFRing], row0, lane);
+      if (!__all_sync(0xffffffffu, mbar_wait_inl(&ms->q_empty, (w.index & 1) ^ 1, abort_flag, p.err, tree_site(15)))) break;
+      load_q<D, FP8, NR, 32, 2>(p, w, smem + C::kOffQ, ms->f[w.index % kFRing], lane);
       mbar_arrive(&ms->q_full);
     }
   }
@@ -1111,12 +936,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   if (p.lse != nullptr && lane == 0) p.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D, bool FP8, int NR, int TILES>
+template <int D, bool FP8, int NR>
 cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
-  constexpr int kSmem = Cfg<D, FP8, NR, TILES>::kOffMisc + static_cast<int>(sizeof(Misc<NR>)) + 1024;
+  constexpr int kSmem = Cfg<D, FP8, NR>::kOffMisc + static_cast<int>(sizeof(Misc<NR>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   using M = Misc<NR>;
-  static_assert(Cfg<D, FP8, NR, TILES>::kOffMisc % 16 == 0 && offsetof(M, nm) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
+  static_assert(Cfg<D, FP8, NR>::kOffMisc % 16 == 0 && offsetof(M, nm) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
                     offsetof(M, k_scale) % 16 == 0 && offsetof(M, v_scale) % 16 == 0,
                 "16-byte accesses and bulk copies");
   // The register split draws on what the block is launched with, which is the compiled kernel's for good.
@@ -1124,24 +949,24 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
   cudaError_t e;
   if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR, TILES>);
+    e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR>);
     if (e != cudaSuccess) return e;
-    if (a.numRegs < Cfg<D, FP8, NR, TILES>::kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (a.numRegs < Cfg<D, FP8, NR>::kRegsLaunch) return cudaErrorInvalidConfiguration;
     checked.store(true, std::memory_order_relaxed);
   }
-  e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, FP8, NR, TILES><<<static_cast<unsigned>(p.parts) * p.row_tiles, Cfg<D, FP8, NR, TILES>::kThreads, kSmem, s>>>(p);
+  tree_kernel<D, FP8, NR><<<static_cast<unsigned>(p.parts), Cfg<D, FP8, NR>::kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool FP8>
 cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
-  cudaError_t e = rows <= 16   ? launch_rows<D, FP8, 16, 1>(p, s)
-                  : rows <= 32 ? launch_rows<D, FP8, 32, 1>(p, s)
-                  : rows <= 64 ? launch_rows<D, FP8, 64, 1>(p, s)
-                               : launch_rows<D, FP8, 64, 2>(p, s);
+  cudaError_t e = rows <= 16   ? launch_rows<D, FP8, 16>(p, s)
+                  : rows <= 32 ? launch_rows<D, FP8, 32>(p, s)
+                  : rows <= 64 ? launch_rows<D, FP8, 64>(p, s)
+                               : launch_tree_wide(p, D, FP8, s);
   if (e != cudaSuccess) return e;
   // The joining kernel's blocks may come up while the first kernel runs; they wait for its end.
   cudaLaunchConfig_t cfg = {};
@@ -1157,8 +982,6 @@ cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
 }
 
 }  // namespace
-
-int tree_cta_rows(int64_t rows) { return rows <= 64 ? 64 : 128; }
 
 cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s) {
   if (static_cast<int64_t>(p.B) * p.Hq * p.T > (1ll << 32) || static_cast<int64_t>(p.parts) * p.row_tiles > 0x7fffffff)

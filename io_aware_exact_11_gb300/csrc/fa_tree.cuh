@@ -1,0 +1,179 @@
+// fa_tree.cuh — what the kernels of drafted-token attention share: the walk over
+// a CTA's part of the key tiles, the slots of cut pairs, and widening E4M3 rows.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "fa_kernels.h"
+#include "sm103.cuh"
+
+namespace fa {
+
+constexpr int kTreeBN = 128;                // keys per tile
+constexpr uint64_t kTreeDrainNs = 200000000ull;
+
+__device__ __forceinline__ unsigned int tree_site(unsigned int s) { return (kKernTree << 8) | s; }
+
+// Lengths of sequence b: keys in all and drafted keys among them.  Lengths that
+// cannot be are taken as an empty sequence, and false is returned.
+__device__ __forceinline__ bool seq_lengths(const TreeParams& p, int b, int& len, int& drafts) {
+  len = p.seq_lens[b];
+  drafts = p.draft_lens != nullptr ? p.draft_lens[b] : p.T;
+  if (p.draft_lens == nullptr && len == 0) drafts = 0;  // an unused batch slot
+  const bool fine = drafts >= 0 && drafts <= p.T && len >= drafts && len <= p.max_blocks * p.block_size;
+  if (!fine) len = drafts = 0;
+  return fine;
+}
+// Key tiles of a sequence; one without drafted tokens has no rows and needs none.
+__device__ __forceinline__ int seq_tiles(int len, int drafts) {
+  return drafts > 0 ? (len + kTreeBN - 1) / kTreeBN : 0;
+}
+
+__device__ __forceinline__ void report_bad_page(const TreeParams& p) {
+  atomicCAS(p.err + 1, 0u, (kKernTree << 8) | kSiteBadBlock);
+}
+
+// Row rr of the T·G rows of a pair belongs to token rr / G.
+__device__ __forceinline__ int token_of(const TreeParams& p, int rr) {
+  return p.G == 1 ? rr : static_cast<int>(__umulhi(static_cast<unsigned>(rr), p.g_magic));
+}
+
+// Does token t see drafted key u?
+__device__ __forceinline__ bool token_sees(const TreeParams& p, int b, int t, int u) {
+  return p.mask != nullptr ? p.mask[b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t;
+}
+
+// A CTA's part of the line of key tiles of all (b, key/value head) pairs.
+struct TreePart {
+  long long per, count;   // tiles per part, and of this one
+  int b, h, tile;         // where it begins
+};
+
+// Finds it, by all NT threads of the block: sums over the sequences, one block of
+// them per thread.  Reports lengths that cannot be.  Contains block barriers.
+template <int NT>
+__device__ __forceinline__ TreePart find_part(const TreeParams& p, int part, long long* warp_sum, int* start) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_thread = (p.B + NT - 1) / NT;
+  const int b0 = min(p.B, tid * per_thread), b1 = min(p.B, b0 + per_thread);
+  long long mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    int len, drafts;
+    if (!seq_lengths(p, b, len, drafts)) atomicCAS(p.err + 1, 0u, (kKernTree << 8) | kSiteBadLength);
+    mine += seq_tiles(len, drafts);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll 1
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  total *= p.Hkv;
+  before *= p.Hkv;
+  TreePart r;
+  r.per = max(2ll, (total + p.parts - 1) / p.parts);  // at least two tiles, one for each stream
+  const long long first = part * r.per;
+  r.count = min(r.per, total - first);
+  if (first >= before && first < before + mine * p.Hkv) {
+    long long at = first - before;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      int len, drafts;
+      seq_lengths(p, b, len, drafts);
+      const int n = seq_tiles(len, drafts);
+      if (at < static_cast<long long>(n) * p.Hkv) {  // fits 32 bits: the host checks tiles · Hkv
+        start[0] = b;
+        start[1] = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(n));
+        start[2] = static_cast<int>(static_cast<unsigned>(at) % static_cast<unsigned>(n));
+        break;
+      }
+      at -= static_cast<long long>(n) * p.Hkv;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  r.b = start[0];
+  r.h = start[1];
+  r.tile = start[2];
+  return r;
+}
+
+// The walk over a part: one pair, or a piece of it, per step.
+struct TreeWalk {
+  const TreeParams& p;
+  long long left;   // tiles of the part that remain, this piece's excluded
+  int b, h, len, drafts, tiles;
+  int t0, t1;       // the piece: tiles [t0, t1) of the pair
+  int index;        // pieces before this one
+
+  __device__ __forceinline__ TreeWalk(const TreeParams& p_, const TreePart& s) : p(p_) {
+    b = s.b;
+    h = s.h;
+    seq_lengths(p, b, len, drafts);
+    tiles = seq_tiles(len, drafts);
+    t0 = s.tile;
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + s.count));
+    left = s.count - (t1 - t0);
+    index = 0;
+  }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    if (++h == p.Hkv) {
+      h = 0;
+      do {
+        if (++b >= p.B) return false;
+        seq_lengths(p, b, len, drafts);
+        tiles = seq_tiles(len, drafts);
+      } while (tiles == 0);
+    }
+    t0 = 0;
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
+    left -= t1;
+    ++index;
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+  __device__ __forceinline__ int64_t pair() const { return static_cast<int64_t>(b) * p.Hkv + h; }
+  // The slot of a piece of a cut pair: numbered along the line, or two per part (a part has one at each end at most).
+  __device__ __forceinline__ int64_t slot(int part) const {
+    return p.slots_by_pair ? pair() + part : 2ll * part + (t0 > 0 ? 0 : 1);
+  }
+  // For the joining kernel, at a pair's first piece: its part and how many parts the pair lies in.
+  __device__ __forceinline__ int2 pieces(int part, long long per) const {
+    const int rest = tiles - (t1 - t0);
+    const int step = static_cast<int>(min(per, 1ll << 30));
+    return make_int2(part, rest > 0 ? 2 + (rest - 1) / step : 1);
+  }
+};
+
+// True on one lane of a converged warp.
+__device__ __forceinline__ bool elect_one_lane() {
+  uint32_t pred = 0;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+  return pred != 0;
+}
+
+// Position in a ring of N slots and the parity of its passes.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+}  // namespace fa

@@ -118,7 +118,7 @@ def test_decode_tree_workspace(L):
     # three parts of one pair: slots 0, 1, 2
     assert size(1, 4, 1, 1, 64, 3) == 256 + 3 * 4 * 64 * 4 + 256
     assert size(2, 28, 4, 8, 128, 0) == size(2, 28, 4, 8, 128, 152)         # no device here: 152 SMs
-    assert size(1, 8, 1, 64, 128, 0) == size(1, 8, 1, 64, 128, 152 // 4)    # 512 rows: four CTAs of 128 per part
+    assert size(1, 8, 1, 64, 128, 0) == size(1, 8, 1, 64, 128, 152 // 2)    # 512 rows: two CTAs of 256 per part
     for bad in ((0, 28, 4, 8, 128, 0), (2, 28, 5, 8, 128, 0), (2, 28, 4, 0, 128, 0), (2, 28, 4, 8, 128, -1)):
         assert size(*bad) == 0
 
