@@ -66,7 +66,11 @@ namespace {
 constexpr int kBN = kTreeBN;
 constexpr int kPBlock = kBN * 128;       // P̃ᵀ: one 128-byte row per key
 constexpr int kMaxRing = 8;
-constexpr int kMaxThreads = 640;
+constexpr int kThreads = 384;            // warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11
+// Registers per thread at launch and after the warpgroups' split.  A softmax thread holds its scores and partial
+// sums, 2·NR values, and a spilled one would go to L2, shared memory leaving next to no L1.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch && kThreads == 384, "register split");
 constexpr int kScaleRing = 16;           // E4M3: tiles whose scale bytes are staged (V slots and four more)
 constexpr int kFRing = 4;                // pieces whose row factors may be live at once
 constexpr int kBadRing = 8;              // pieces whose flags of bad values may be
@@ -74,19 +78,6 @@ constexpr int kBadRing = 8;              // pieces whose flags of bad values may
 // NR rows of a pair, shared by both streams.
 template <int D, bool FP8, int NR>
 struct Cfg {
-  // With 64 rows a stream has two warpgroups, each with half of them: four softmax warps per SM sub-partition hide
-  // one another's waits better than two with twice the rows each.
-  static constexpr int kSub = NR == 64 ? 2 : 1;
-  static constexpr int kNC = NR / kSub;                       // rows (TMEM columns) of a softmax thread
-  static constexpr int kSoftmax = 256 * kSub;                 // softmax threads; then warps for K, MMA, V, Q
-  static constexpr int kThreads = kSoftmax + 128;
-  // Registers per thread at launch and after the warpgroups' split.  A softmax thread holds its scores and partial
-  // sums, 2·kNC values, and a spilled one would go to L2, shared memory leaving next to no L1.
-  static constexpr int kRegsLaunch = kSub == 2 ? 96 : 168;
-  static constexpr int kRegsSoftmax = kSub == 2 ? 104 : 208;
-  static constexpr int kRegsOther = kSub == 2 ? 64 : 88;
-  static_assert(2 * kSub * kRegsSoftmax + kRegsOther <= (2 * kSub + 1) * kRegsLaunch && kThreads <= kMaxThreads,
-                "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
   static constexpr int kTerms = FP8 ? 1 : 2;                  // of P̃
   static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
@@ -124,11 +115,11 @@ struct Misc {
   int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
   int64_t o_off[2][NR];                // its element offset in O
   int fresh[2][NR];                    // a live row that has seen nothing yet
-  int kv_red[2][2][4];                 // per stream, warpgroup and warp
+  int kv_red[2][4];                    // per stream and warp
   alignas(16) uint8_t k_scale[kScaleRing][kBN];  // written by bulk copies
   alignas(16) uint8_t v_scale[kScaleRing][kBN];
   uint32_t bad[kBadRing][8];           // drafted keys with non-finite values (one bit each)
-  long long warp_sum[kMaxThreads / 32];
+  long long warp_sum[kThreads / 32];
   int start[3];
   uint32_t tmem_base;
   int abort_flag;
@@ -168,17 +159,16 @@ __device__ __forceinline__ void reduce_cols(float (&v)[N], int lane, Op op, floa
   if ((lane & (32 / N - 1)) == 0) out[base] = v[0];
 }
 
-// Widens chunks [C0, C0 + N) of 16 E4M3 codes of one value row of D codes to fp16.
-// src: the row in its slot, swizzled as TMA wrote it; dst: the row in the first
-// 64-column block of the fp16 tile.  EDGE: the row may be a drafted one, whose NaN
-// codes are taken out and reported by the result, or lie past the end (dead).
-template <int D, int N, bool EDGE>
-__device__ __forceinline__ bool widen_row(const uint8_t* src, uint8_t* dst, int r, int c0, bool drafted, bool dead) {
+// Widens one value row of D E4M3 codes to fp16.  src: the row in its slot,
+// swizzled as TMA wrote it; dst: the row in the first 64-column block of the fp16
+// tile.  EDGE: the row may be a drafted one, whose NaN codes are taken out and
+// reported by the result, or lie past the end (dead).
+template <int D, bool EDGE>
+__device__ __forceinline__ bool widen_row(const uint8_t* src, uint8_t* dst, int r, bool drafted, bool dead) {
   const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
   bool bad = false;
 #pragma unroll
-  for (int c = 0; c < N; ++c) {
-    const int ch = c0 + c;
+  for (int ch = 0; ch < D / 16; ++ch) {
     const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if (EDGE && drafted) {
@@ -285,11 +275,10 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, u
 }
 
 template <int D, bool FP8, int NR>
-__global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, FP8, NR>;
   constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
-  constexpr int kSlot = C::kSlot, kThreads = C::kThreads, kSub = C::kSub;
-  constexpr int kWarp0 = C::kSoftmax / 32;  // first warp after the softmax ones
+  constexpr int kSlot = C::kSlot;
   // Rescale once a score exceeds the reference by kLazy; the reference is taken kBase below the maximum.
   constexpr float kLazy = FP8 ? 11.f : 8.f;
   constexpr float kBase = FP8 ? 3.f : 0.f;
@@ -313,12 +302,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
     }
     for (int s = 0; s < C::kRV; ++s) {
       mbar_init(&ms->v_full[s], 1);
-      mbar_init(&ms->v_empty[s], FP8 ? 4 * kSub : 1);
+      mbar_init(&ms->v_empty[s], FP8 ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
-      mbar_init(&ms->s_free[s], 128 * kSub);
-      mbar_init(&ms->p_full[s], 128 * kSub);
+      mbar_init(&ms->s_free[s], 128);
+      mbar_init(&ms->p_full[s], 128);
       mbar_init(&ms->p_free[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
@@ -329,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
     fence_barrier_init();
   }
   if (tid < kBadRing * 8) ms->bad[tid >> 3][tid & 7] = 0;
-  if (warp == kWarp0 + 1) {
+  if (warp == 9) {
     tmem_alloc(&ms->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
@@ -339,10 +328,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
 
   if (my.count <= 0) {
     // nothing left for this CTA
-  } else if (warp == kWarp0 || warp == kWarp0 + 2) {
-    reg_dealloc<C::kRegsOther>();
-    // ------------------------------------------- loads of K (first warp) and V (third)
-    const bool is_v = warp == kWarp0 + 2;
+  } else if (warp == 8 || warp == 10) {
+    reg_dealloc<kRegsOther>();
+    // ------------------------------------------- loads of K (warp 8) and V (warp 10)
+    const bool is_v = warp == 10;
     const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
     uint64_t* full = is_v ? ms->v_full : ms->k_full;
     uint64_t* empty = is_v ? ms->v_empty : ms->k_empty;
@@ -414,8 +403,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
         if (FP8 && is_v) mbar_wait_drain_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, kTreeDrainNs);
       }
     }
-  } else if (warp == kWarp0 + 1) {
-    reg_dealloc<C::kRegsOther>();
+  } else if (warp == 9) {
+    reg_dealloc<kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
     constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
@@ -494,54 +483,49 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       mma_commit(&ms->drain);
       mbar_wait_drain_inl(&ms->drain, 0, kTreeDrainNs);
     }
-  } else if (warp < kWarp0) {
-    reg_alloc<C::kRegsSoftmax>();
-    // -------------------- softmax: one key per thread, the warpgroup's NC rows of the stream
-    constexpr int NC = C::kNC;
-    const int g = warp / (4 * kSub);
-    const int sub = kSub == 1 ? 0 : (warp >> 2) & 1;
-    const int col0 = sub * NC;             // first row of the warpgroup
-    const int bar = 1 + g * kSub + sub;    // the warpgroup's barrier
-    const int end_bar = 5 + sub;           // that of the warpgroups of both streams that share these rows
+  } else if (warp < 8) {
+    reg_alloc<kRegsSoftmax>();
+    // ----------------------------- softmax: one key per thread, the stream's NR rows
+    const int g = warp >> 2;
+    const int bar = 1 + g;                 // the stream's barrier
     const int kt = tid & 127;              // key in the tile, TMEM lane, head dim of O
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + g * C::kSCols + col0;
-    const uint32_t o_addr = tmem + lane_base + C::kColO + g * C::kPCols + col0;
-    float* nm = ms->nm[g] + col0;
-    float* corr = ms->corr[g] + col0;
-    float* red = ms->red[g][0] + col0;     // + warp·NR
-    int64_t* row = ms->row[g] + col0;
-    int64_t* o_off = ms->o_off[g] + col0;
-    int* fresh = ms->fresh[g] + col0;
+    const uint32_t s_addr = tmem + lane_base + g * C::kSCols;
+    const uint32_t o_addr = tmem + lane_base + C::kColO + g * C::kPCols;
+    float* nm = ms->nm[g];
+    float* corr = ms->corr[g];
+    float* red = ms->red[g][0];            // + warp·NR
+    int64_t* row = ms->row[g];
+    int64_t* o_off = ms->o_off[g];
+    int* fresh = ms->fresh[g];
     int tile0 = 0;                         // tiles of the pieces before, and those of this stream
     int used = 0;
     bool ok = true;
     TreeWalk w(p, my);
-    load_q<D, FP8, NR, C::kSoftmax, 4>(p, w, smem + C::kOffQ, ms->f[0], tid);
-    named_sync(7, C::kSoftmax);
+    load_q<D, FP8, NR, 256, 4>(p, w, smem + C::kOffQ, ms->f[0], tid);
+    named_sync(3, 256);
     if (warp == 0) mbar_arrive(&ms->q_full);
 #pragma unroll 1
     do {
       const int n_tiles = w.t1 - w.t0;
       const int context = w.len - w.drafts;
-      const int live = w.drafts * p.G - col0;  // rows of this warpgroup that belong to a drafted token
-      if (kt < NC) {
-        const int rr = col0 + kt;
-        const int t = token_of(p, rr);
-        const int h = w.h * p.G + (rr - t * p.G);
+      const int live = w.drafts * p.G;  // rows that belong to a drafted token
+      if (kt < NR) {
+        const int t = token_of(p, kt);
+        const int h = w.h * p.G + (kt - t * p.G);
         row[kt] = kt < live ? (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t : -1;
         o_off[kt] = w.b * p.so[0] + h * p.so[1] + static_cast<int64_t>(t) * p.so[2];
         nm[kt] = 0.f;
         fresh[kt] = kt < live;
       }
       named_sync(bar, 128);
-      bool unseen = true;  // some row of the warpgroup may have seen nothing yet
-      float l[NC];
+      bool unseen = true;  // some row may have seen nothing yet
+      float l[NR];
 #pragma unroll
-      for (int n = 0; n < NC; ++n) l[n] = 0.f;
+      for (int n = 0; n < NR; ++n) l[n] = 0.f;
       int kv_ref = -1024;
       int done = 0;  // tiles of this piece that this stream has worked on
-      const float* f_row = ms->f[w.index % kFRing] + col0;
+      const float* f_row = ms->f[w.index % kFRing];
 #pragma unroll 1
       for (int i = g; i < n_tiles; i += 2, ++done) {
         const int tile = tile0 + i;
@@ -554,14 +538,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
           seen = 0;
           if (key < w.len && live > 0) {
             // Token by token: one byte of the mask stands for G rows.
-            const int ta = token_of(p, col0);
-            const int tb = token_of(p, col0 + min(NC, live) - 1);
             const uint8_t* mk = p.mask != nullptr ? p.mask + w.b * p.mask_sb + (key - context) : nullptr;
 #pragma unroll 4
-            for (int t = ta; t <= tb; ++t) {
+            for (int t = 0; t < w.drafts; ++t) {
               const bool on = mk != nullptr ? mk[static_cast<int64_t>(t) * p.T] != 0 : key - context <= t;
-              const int lo = max(0, t * p.G - col0), hi = min(NC, (t + 1) * p.G - col0);  // its rows
-              const uint32_t bits = (0xffffffffu >> (32 - (hi - lo))) << lo;
+              const uint32_t bits = (0xffffffffu >> (32 - p.G)) << (t * p.G);  // its rows
               seen |= on ? bits : 0;
             }
           }
@@ -574,16 +555,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
           const uint32_t sk = ms->k_scale[tile % kScaleRing][kt];
           ks = sk == 0 ? 5.877471754111438e-39f : __uint_as_float(sk << 23);
           if (key < w.len) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
-          // This key's value row, or the warpgroup's half of it, to fp16, while the scores are made.
-          constexpr int kN = D / 16 / kSub;
+          // This key's value row to fp16, while the scores are made.
           const int slot = tile % C::kRV;
           ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(11)) && ok;
           if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
           const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
           uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
           if (!tail) {
-            widen_row<D, kN, false>(src, dst, kt, sub * kN, false, false);
-          } else if (widen_row<D, kN, true>(src, dst, kt, sub * kN, key >= context, key >= w.len) && key < w.len) {
+            widen_row<D, false>(src, dst, kt, false, false);
+          } else if (widen_row<D, true>(src, dst, kt, key >= context, key >= w.len) && key < w.len) {
             atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
           }
           fence_proxy_async_smem();
@@ -594,13 +574,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
         tc_fence_after();
         // x = score − reference, masked to −∞ where the row does not see the key.  A second time where a reference
         // has moved.
-        float x[NC];
-        bool dead = false;  // a wait of some thread of the warpgroup has failed
+        float x[NR];
+        bool dead = false;  // a wait of some thread of the stream has failed
 #pragma unroll 1
         for (bool again = false;; again = true) {
           // 16 rows at a time; with registers to spare the next ones are on their way from TMEM meanwhile.
           constexpr int kC = 16;
-          constexpr int kBuf = kSub == 1 && NC > kC ? 2 : 1;
+          constexpr int kBuf = NR > kC ? 2 : 1;
           uint32_t hi[kBuf][kC], lo[kBuf][kC];
           auto fetch = [&](int c, int to) {
             tmem_ld(s_addr + c, hi[to]);
@@ -608,13 +588,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
           };
           fetch(0, 0);
 #pragma unroll
-          for (int c = 0; c < NC; c += kC) {
+          for (int c = 0; c < NR; c += kC) {
             const int now = (c / kC) % kBuf;
-            if (kBuf == 1 && c > 0) fetch(c, 0);
             tmem_wait_ld();
             reg_fence(hi[now]);
             if constexpr (FP8) reg_fence(lo[now]);
-            if (kBuf == 2 && c + kC < NC) fetch(c + kC, now ^ 1);
+            if (kBuf == 2 && c + kC < NR) fetch(c + kC, now ^ 1);
 #pragma unroll
             for (int e = 0; e < kC; e += 4) {
               const int n = c + e;
@@ -637,16 +616,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
           }
           if (tail) {
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
+            for (int n = 0; n < NR; ++n)
               if (!((seen >> n) & 1)) x[n] = -INFINITY;
           }
           if (again) break;
           float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int n = 4; n < NC; n += 8)
+          for (int n = 4; n < NR; n += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              mx[e] = n + 4 + e < NC ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NC]) : fmaxf(mx[e], x[n + e]);
+              mx[e] = n + 4 + e < NR ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NR]) : fmaxf(mx[e], x[n + e]);
           const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
           const bool over = unseen || top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
           if (!named_any(bar, 128, over || !ok)) break;
@@ -656,19 +635,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
             dead = true;
             break;
           }
-          reduce_cols<NC>(x, lane, OpMax(), red + (warp & 3) * NR);
+          reduce_cols<NR>(x, lane, OpMax(), red + (warp & 3) * NR);
           if constexpr (FP8) {
             const int top_kv = __reduce_max_sync(0xffffffffu, kv);
-            if (lane == 0) ms->kv_red[g][sub][warp & 3] = top_kv;
+            if (lane == 0) ms->kv_red[g][warp & 3] = top_kv;
           }
           named_sync(bar, 128);
           int kv_new = kv_ref;
           if constexpr (FP8) {
-            const int* kr = ms->kv_red[g][sub];
+            const int* kr = ms->kv_red[g];
             kv_new = max(kv_ref, max(max(kr[0], kr[1]), max(kr[2], kr[3])));
           }
           bool still = false;
-          if (kt < NC) {
+          if (kt < NR) {
             // Maxima relative to the old reference (0 for a row that has seen nothing).
             const float now = fmaxf(fmaxf(red[kt], red[NR + kt]), fmaxf(red[2 * NR + kt], red[3 * NR + kt]));
             const bool first = fresh[kt] != 0;
@@ -682,13 +661,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
           }
           unseen = named_any(bar, 128, still);
 #pragma unroll
-          for (int n = 0; n < NC; ++n) l[n] *= corr[n];
+          for (int n = 0; n < NR; ++n) l[n] *= corr[n];
           if (done > 0) {
             ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
             tc_fence_after();
             const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
 #pragma unroll 1
-            for (int term = 0; term < C::kTerms; ++term) rescale_cols<NC>(o_addr + term * NR, corr, kf);
+            for (int term = 0; term < C::kTerms; ++term) rescale_cols<NR>(o_addr + term * NR, corr, kf);
           }
           kv_ref = kv_new;
         }
@@ -702,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
         const float wv = !FP8 ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
         uint8_t* prow = smem + C::kOffP + g * C::kP + kt * 128;
 #pragma unroll
-        for (int ch = 0; ch < NC / 8; ++ch) {  // 8 rows per 16-byte chunk
+        for (int ch = 0; ch < NR / 8; ++ch) {  // 8 rows per 16-byte chunk
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -719,23 +698,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
               lo[e] = pack_bf16x2(x[n] - __uint_as_float(hi[e] << 16), x[n + 1] - __uint_as_float(hi[e] & 0xffff0000u));
             }
           }
-          const int c1 = col0 / 8 + ch;
-          *reinterpret_cast<uint4*>(prow + ((c1 ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(prow + ((ch ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           if constexpr (!FP8) {
-            const int c2 = c1 + NR / 8;  // column chunk of the second term
+            const int c2 = ch + NR / 8;  // column chunk of the second term
             *reinterpret_cast<uint4*>(prow + (c2 >> 3) * kPBlock + (((c2 & 7) ^ (kt & 7)) << 4)) =
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         if (!FP8 && tail && key >= context) {
-          // This key's value row, or the warpgroup's half of it: zeros past the end, and in place of what a drafted row
-          // holds that is not finite.
+          // This key's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
           const int slot = tile % C::kRV;
           ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(9)) && ok;
           uint8_t* vr = smem + C::kOffV + slot * kSlot + (kPg5 ? (kt >> 3) * 2048 + (kt & 7) * 128 : kt * 128);
           bool bad = false;
 #pragma unroll 2
-          for (int ch = sub * (D / 8 / kSub); ch < (sub + 1) * (D / 8 / kSub); ++ch) {
+          for (int ch = 0; ch < D / 8; ++ch) {
             uint4* at = reinterpret_cast<uint4*>(vr + (ch >> 3) * 1024 + (ch & 7) * 16);
             uint32_t v4[4] = {0, 0, 0, 0};
             if (key < w.len) {
@@ -760,24 +737,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       // ------------------------------------------------------------ end of the piece
       // (Its barriers are joined by all threads whatever the waits said.)
       if (done > 0) ok = ok && mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, tree_site(10));
-      reduce_cols<NC>(l, lane, OpAdd(), red + (warp & 3) * NR);
+      reduce_cols<NR>(l, lane, OpAdd(), red + (warp & 3) * NR);
       tc_fence_before();
-      named_sync(end_bar, 256);
+      named_sync(3, 256);
       tc_fence_after();
       const bool whole = w.whole();
-      const int64_t slot_row = w.slot(part) * p.T * p.G + col0;  // first row of the piece's slot
-      if (kt < NC) {
+      const int64_t slot_row = w.slot(part) * p.T * p.G;  // first row of the piece's slot
+      if (kt < NR) {
         // Both streams' sums in a fixed order: the same result every time.
         float sums[2], m = -INFINITY, sum = 0.f, mine = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float* r4 = ms->red[e][0] + col0 + kt;
+          const float* r4 = ms->red[e][0] + kt;
           sums[e] = (r4[0] + r4[NR]) + (r4[2 * NR] + r4[3 * NR]);
-          if (sums[e] != 0.f) m = fmaxf(m, -ms->nm[e][col0 + kt]);
+          if (sums[e] != 0.f) m = fmaxf(m, -ms->nm[e][kt]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float wgt = sums[e] == 0.f ? 0.f : exp2f(-ms->nm[e][col0 + kt] - m);
+          const float wgt = sums[e] == 0.f ? 0.f : exp2f(-ms->nm[e][kt] - m);
           sum += sums[e] * wgt;
           if (e == g) mine = wgt;
         }
@@ -791,13 +768,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
         }
         // What this stream's O is multiplied by.
         mine *= sum != 0.f ? 1.f / sum : 0.f;
-        ms->scale[g][col0 + kt] = mine * (FP8 ? exp2f(static_cast<float>(max(kv_ref, -300))) : 1.f);
+        ms->scale[g][kt] = mine * (FP8 ? exp2f(static_cast<float>(max(kv_ref, -300))) : 1.f);
       }
       if (w.t0 == 0 && tid == 0) p.pieces[w.pair()] = w.pieces(part, my.per);
-      named_sync(end_bar, 256);
+      named_sync(3, 256);
       const uint32_t* bad = ms->bad[w.index % kBadRing];
-      // Rows that this warpgroup writes: half of the shared ones.
-      constexpr int kOut = NC / 2;
+      // Rows that this stream writes: half of them.
+      constexpr int kOut = NR / 2;
       const int c0 = g * kOut;
       if (__all_sync(0xffffffffu, ok) && kt < D) {
         float o[kOut];
@@ -808,12 +785,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
 #pragma unroll 1
           for (int term = 0; term < C::kTerms; ++term) {
             uint32_t r[kOut];
-            tmem_ld(tmem + lane_base + C::kColO + e * C::kPCols + term * NR + col0 + c0, r);
+            tmem_ld(tmem + lane_base + C::kColO + e * C::kPCols + term * NR + c0, r);
             tmem_wait_ld();
             reg_fence(r);
 #pragma unroll
             for (int q = 0; q < kOut; ++q) {
-              const float k = ms->scale[e][col0 + c0 + q];
+              const float k = ms->scale[e][c0 + q];
               if (k != 0.f) o[q] += __uint_as_float(r[q]) * k;  // 0: a stream without keys has left O unwritten
             }
           }
@@ -849,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
           if (fabsf(v) <= 3.4028234663852886e38f) continue;
 #pragma unroll 1
           for (int q = 0; q < kOut; ++q) {
-            if (row[c0 + q] < 0 || !token_sees(p, w.b, token_of(p, col0 + c0 + q), u)) continue;
+            if (row[c0 + q] < 0 || !token_sees(p, w.b, token_of(p, c0 + q), u)) continue;
             if (!whole)
               part_o[q * D] += v;
             else
@@ -859,12 +836,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       }
       tc_fence_before();
       // All have read O and the statistics; any failed wait ends the walk for all.
-      ok = !named_any(end_bar, 256, !ok);
-      // The flags of three pieces ago: the other warpgroups may still be at the piece before.
+      ok = !named_any(3, 256, !ok);
+      // The flags of three pieces ago: the other stream may still be at the piece before.
       if (tid < 8) ms->bad[(w.index + kBadRing - 3) % kBadRing][tid] = 0;
     } while (ok && w.next());
   } else {
-    reg_dealloc<C::kRegsOther>();
+    reg_dealloc<kRegsOther>();
     // ------------------------- Q of every piece but the first, which the streams load
     TreeWalk w(p, my);
 #pragma unroll 1
@@ -878,7 +855,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarp0 + 1) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -951,12 +928,12 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
     cudaFuncAttributes a;
     e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR>);
     if (e != cudaSuccess) return e;
-    if (a.numRegs < Cfg<D, FP8, NR>::kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (a.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     checked.store(true, std::memory_order_relaxed);
   }
   e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, FP8, NR><<<static_cast<unsigned>(p.parts), Cfg<D, FP8, NR>::kThreads, kSmem, s>>>(p);
+  tree_kernel<D, FP8, NR><<<static_cast<unsigned>(p.parts), kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -965,7 +942,6 @@ cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
   cudaError_t e = rows <= 16   ? launch_rows<D, FP8, 16>(p, s)
                   : rows <= 32 ? launch_rows<D, FP8, 32>(p, s)
-                  : rows <= 64 ? launch_rows<D, FP8, 64>(p, s)
                                : launch_tree_wide(p, D, FP8, s);
   if (e != cudaSuccess) return e;
   // The joining kernel's blocks may come up while the first kernel runs; they wait for its end.

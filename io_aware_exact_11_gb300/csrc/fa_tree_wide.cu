@@ -49,6 +49,7 @@ struct Cfg {
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
   static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;
   static constexpr int kQTile = kRowTile * D * 2;        // bf16, or two E4M3 terms
+  static constexpr int kTerms = !FP8 && TILES == 1 ? 2 : 1;  // of P̃
   static constexpr int kFixed = TILES * kQTile + 2 * kV16;
   static constexpr int kMisc = (FP8 ? 10 : 2) * 1024 + (TILES == 1 ? 4 * 1024 : 0);
   static constexpr int kRoom = 226 * 1024 - kFixed - kMisc;  // 227 KB less the alignment pad
@@ -343,9 +344,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           if (leader) {
             const uint64_t bd = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, kBN * 128, 1024);
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)  // A: P̃ over S's columns, 16 keys in 8 of them
-              mma_bf16_ts(tmem + C::kColO + g * D, ts + kk * 8, bd + kk * (kPg5 ? 256 : 128), kIdescO,
-                          (s >= 4 || kk > 0) ? 1u : 0u);
+            for (int term = 0; term < C::kTerms; ++term)
+#pragma unroll
+              for (int kk = 0; kk < kBN / 16; ++kk)  // A: P̃ over S's columns, 16 keys in 8 of them
+                mma_bf16_ts(tmem + C::kColO + g * D, ts + term * 64 + kk * 8, bd + kk * (kPg5 ? 256 : 128), kIdescO,
+                            (s >= 4 || term > 0 || kk > 0) ? 1u : 0u);
             mma_commit(&ms->o_full[g]);
             if (last_use) mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
           }
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
+          uint32_t pk[32], lo[C::kTerms == 2 ? 32 : 1];
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             float* x = s + half * 64 + e;
@@ -530,8 +533,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             fadd2(sum[2], sum[3], sum[2], sum[3], x[2], x[3]);
             pk[e / 2] = FP8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
             pk[e / 2 + 1] = FP8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
+            if constexpr (C::kTerms == 2) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t h2 = pk[e / 2 + q];
+                lo[e / 2 + q] = pack_bf16x2(x[2 * q] - __uint_as_float(h2 << 16),
+                                            x[2 * q + 1] - __uint_as_float(h2 & 0xffff0000u));
+              }
+            }
           }
           tmem_st32(s_addr + half * 32, pk);
+          if constexpr (C::kTerms == 2) tmem_st32(s_addr + 64 + half * 32, lo);
         }
         l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         if (!FP8 && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
