@@ -108,15 +108,15 @@ __device__ __forceinline__ TreePart find_part(const TreeParams& p, int part, lon
   return r;
 }
 
-// The walk over a part: one pair, or a piece of it, per step.
+// The walk over a part: one pair, or a piece of it, per step.  Plain data, so that
+// a warpgroup with no registers to spare keeps it in shared memory.
 struct TreeWalk {
-  const TreeParams& p;
   long long left;   // tiles of the part that remain, this piece's excluded
   int b, h, len, drafts, tiles;
   int t0, t1;       // the piece: tiles [t0, t1) of the pair
   int index;        // pieces before this one
 
-  __device__ __forceinline__ TreeWalk(const TreeParams& p_, const TreePart& s) : p(p_) {
+  __device__ __forceinline__ void begin(const TreeParams& p, const TreePart& s) {
     b = s.b;
     h = s.h;
     seq_lengths(p, b, len, drafts);
@@ -126,7 +126,7 @@ struct TreeWalk {
     left = s.count - (t1 - t0);
     index = 0;
   }
-  __device__ __forceinline__ bool next() {
+  __device__ __forceinline__ bool next(const TreeParams& p) {
     if (left <= 0) return false;
     if (++h == p.Hkv) {
       h = 0;
@@ -143,10 +143,10 @@ struct TreeWalk {
     return true;
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
-  __device__ __forceinline__ int64_t pair() const { return static_cast<int64_t>(b) * p.Hkv + h; }
+  __device__ __forceinline__ int64_t pair(const TreeParams& p) const { return static_cast<int64_t>(b) * p.Hkv + h; }
   // The slot of a piece of a cut pair: numbered along the line, or two per part (a part has one at each end at most).
-  __device__ __forceinline__ int64_t slot(int part) const {
-    return p.slots_by_pair ? pair() + part : 2ll * part + (t0 > 0 ? 0 : 1);
+  __device__ __forceinline__ int64_t slot(const TreeParams& p, int part) const {
+    return p.slots_by_pair ? pair(p) + part : 2ll * part + (t0 > 0 ? 0 : 1);
   }
   // For the joining kernel, at a pair's first piece: its part and how many parts the pair lies in.
   __device__ __forceinline__ int2 pieces(int part, long long per) const {

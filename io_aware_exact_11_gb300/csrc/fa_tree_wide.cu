@@ -36,7 +36,7 @@ constexpr int kBN = kTreeBN;
 constexpr int kRowTile = 128;
 constexpr int kMaxRing = 8;
 constexpr int kScaleRing = 16;
-constexpr int kTileRing = 4;   // E4M3: tiles whose converted scales are kept
+constexpr int kTileRing = 8;   // E4M3: tiles whose converted scales are kept
 
 template <int D, bool FP8, int TILES>
 struct Cfg {
@@ -51,7 +51,7 @@ struct Cfg {
   static constexpr int kQTile = kRowTile * D * 2;        // bf16, or two E4M3 terms
   static constexpr int kTerms = !FP8 && TILES == 1 ? 2 : 1;  // of P̃
   static constexpr int kFixed = TILES * kQTile + 2 * kV16;
-  static constexpr int kMisc = (FP8 ? 10 : 2) * 1024 + (TILES == 1 ? 4 * 1024 : 0);
+  static constexpr int kMisc = (FP8 ? 13 : 2) * 1024 + (TILES == 1 ? 4 * 1024 : 0);
   static constexpr int kRoom = 226 * 1024 - kFixed - kMisc;  // 227 KB less the alignment pad
   static constexpr int kRing = kRoom / kSlot < 14 ? kRoom / kSlot : 14;
   static constexpr int kRK = kRing / 2;
@@ -69,9 +69,11 @@ struct Cfg {
 
 struct Bars {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t s_full[2], p_full[2], o_full[2], v16_full[2], v16_empty[2], sc_full[kScaleRing], q_full, drain;
+  uint64_t s_full[2], p_full[2], o_full[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing], q_full, drain;
   uint32_t bad[8][8];       // drafted keys with non-finite values, of up to eight pieces
   long long warp_sum[16];
+  TreeWalk walk[2];         // of the streams
+  int more[2];
   int start[3];
   uint32_t tmem_base;
   int abort_flag;
@@ -87,7 +89,7 @@ struct Scales {
   alignas(16) uint8_t v_scale[kScaleRing][kBN];
   alignas(16) float ks[kTileRing][kBN];  // the keys' powers of two
   int ref[kTileRing];                    // exponent that the tile's widened values are relative to
-  int top[2][4];
+  alignas(16) int top[2][4];
   float f[2 * kRowTile];                 // what a row's raw scores are multiplied by
 };
 
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       mbar_init(&ms->v16_empty[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
+    for (int s = 0; s < kTileRing; ++s) mbar_init(&ms->ks_full[s], 128);
     mbar_init(&ms->q_full, 256);
     mbar_init(&ms->drain, 1);
     ms->abort_flag = 0;
@@ -248,7 +251,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     int slot = 0, ss = 0, issued = 0;
     uint32_t parity = 1;
     bool ok = true;
-    TreeWalk w(p, my);
+    TreeWalk w;
+    w.begin(p, my);
     do {
       const int pages = (w.len + p.block_size - 1) >> bshift;
       const int32_t* table = p.block_table + static_cast<int64_t>(w.b) * p.max_blocks;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           parity ^= 1u;
         }
       }
-    } while (ok && w.next());
+    } while (ok && w.next(p));
     if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA ends
 #pragma unroll 1
       for (int n = max(0, issued - ring); n < issued; ++n) {
@@ -319,10 +323,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     const bool leader = elect_one_lane();
     Ring<C::kRK> rk;
     Ring<C::kRV> rv;
-    int v16 = 0;
+    int v16 = 0;         // E4M3: the widened tile's place and parity
+    uint32_t v16_par = 0;
     uint32_t p_par = 0;  // parity of p_full to wait for, a bit per stream
     bool ok = true;
-    TreeWalk w(p, my);
+    TreeWalk w;
+    w.begin(p, my);
     do {
       // Step s: stream s & 1, tile s (or s / 2).  Broadcast, like the walk's end below, to keep the loop uniform.
       const int steps = __shfl_sync(0xffffffffu, (w.t1 - w.t0) * TILES, 0);
@@ -334,8 +340,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         const uint32_t ts = tmem + g * kBN;
         if (s >= 2) {  // P̃V of step s − 2, of the same stream
           ok = ok && mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(0x23));
-          if constexpr (!FP8)
-            ok = ok && mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24));
+          ok = ok && (FP8 ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(0x2f))
+                          : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24)));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           p_par ^= 1u << g;
@@ -355,6 +361,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           if (last_use) {
             rv.advance();
             v16 ^= 1;
+            v16_par ^= v16 == 0;
           }
         }
         if (s < steps) {
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           if (last_use) rk.advance();
         }
       }
-    } while (ok && __shfl_sync(0xffffffffu, w.next(), 0));
+    } while (ok && __shfl_sync(0xffffffffu, w.next(p), 0));
     if (*abort_flag && leader) {
       mma_commit(&ms->drain);
       mbar_wait_drain_inl(&ms->drain, 0, kTreeDrainNs);
@@ -406,14 +413,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     const uint32_t o_addr = tmem + lane_base + C::kColO + g * D;
     int tile0 = 0, used = 0;       // tiles of the pieces before, and those of this stream
     bool ok = true;
-    TreeWalk w(p, my);
+    const TreeWalk& w = ms->walk[g];
+    if (kt == 0) ms->walk[g].begin(p, my);
+    named_sync(1 + g, 128);
 #pragma unroll 1
-    do {
+    while (true) {
       const int n_tiles = w.t1 - w.t0;
       const int context = w.len - w.drafts;
       const int rr = my_row0 + kt;
       const int t = token_of(p, rr);
       const bool live = rr < w.drafts * p.G;
+      const bool busy = __any_sync(0xffffffffu, live);
       const int h = w.h * p.G + (rr - t * p.G);
       // Q of the piece: the stream's tile, or both streams' shares of the one tile.  The products of the piece before
       // that read its place are done: their results have been taken (by both streams, which end a shared piece together).
@@ -447,8 +457,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             }
           }
         }
-        if constexpr (FP8)  // the keys' powers of two and the widened values
-          ok = mbar_wait_inl(&ms->v16_full[tile & 1], (tile >> 1) & 1, abort_flag, p.err, tree_site(0x26)) && ok;
+        if constexpr (FP8)  // the keys' powers of two
+          ok = mbar_wait_inl(&ms->ks_full[tile % kTileRing], (tile / kTileRing) & 1, abort_flag, p.err, tree_site(0x26)) && ok;
         ok = mbar_wait_inl(&ms->s_full[g], (used + done) & 1, abort_flag, p.err, tree_site(0x27)) && ok;
         // P̃V of the stream's tile before has run, S was issued behind it; this keeps the barrier's phases in step.
         if (done > 0) ok = mbar_wait_inl(&ms->o_full[g], (used + done - 1) & 1, abort_flag, p.err, tree_site(0x28)) && ok;
@@ -457,6 +467,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           break;
         }
         tc_fence_after();
+        // A warp without live rows leaves its P̃ as it is: it only reaches its own rows of O, which nobody reads.
+        if (busy) {
         float s[kBN];
         {
           uint32_t r0[32], r1[32], r2[32], r3[32];
@@ -546,6 +558,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           if constexpr (C::kTerms == 2) tmem_st32(s_addr + 64 + half * 32, lo);
         }
         l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
         if (!FP8 && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
           // Key kt's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
           // (Two row tiles: the first stream does it for both, its product is issued first.)
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       // ------------------------------------------------------------ end of the piece
       if (done > 0) ok = ok && mbar_wait_inl(&ms->o_full[g], (used - 1) & 1, abort_flag, p.err, tree_site(0x2a));
       const bool whole = w.whole();
-      const int64_t slot_row = w.slot(part) * p.T * p.G + rr;
+      const int64_t slot_row = w.slot(p, part) * p.T * p.G + rr;
       float m = l_run != 0.f ? m_run : -INFINITY, sum = l_run;
       float scale[2] = {0.f, 0.f};  // what the streams' O is multiplied by
       if constexpr (TILES == 1) {
@@ -620,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
               sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
         }
       }
-      if (w.t0 == 0 && blockIdx.x == 0 && tid == 0) p.pieces[w.pair()] = w.pieces(part, my.per);
+      if (w.t0 == 0 && blockIdx.x == 0 && tid == 0) p.pieces[w.pair(p)] = w.pieces(part, my.per);
       // The row's columns, or with shared rows this stream's half of them, 32 at a time.
       if (fine) {
         constexpr int kHalf = TILES == 1 ? D / 2 : D;
@@ -690,58 +703,61 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       ok = !named_any(TILES == 1 ? 3 : 1 + g, TILES == 1 ? 256 : 128, !ok);
       // The flags of three pieces ago: the other stream may still be at the piece before.
       if (tid < 8) ms->bad[(w.index + 5) & 7][tid] = 0;
-    } while (ok && w.next());
+      if (!ok) break;
+      if (kt == 0) ms->more[g] = ms->walk[g].next(p);
+      named_sync(1 + g, 128);
+      if (!ms->more[g]) break;
+    }
   } else if (FP8 && warp >= 12) {
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------ converters: one value row and one key's scale per thread
     const int r = tid - 384;
     int tile = 0, ref = 0;
     bool ok = true;
-    TreeWalk w(p, my);
+    TreeWalk w;
+    w.begin(p, my);
     do {
       const int context = w.len - w.drafts;
-#pragma unroll 1
-      for (int i = w.t0; i < w.t1; ++i, ++tile) {
-        const int slot = tile % C::kRV;
-        ok = mbar_wait_inl(&ms->sc_full[tile % kScaleRing], (tile / kScaleRing) & 1, abort_flag, p.err, tree_site(0x2b)) &&
-             mbar_wait_inl(&ms->v16_empty[tile & 1], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x2c)) &&
-             mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(0x2d));
-        const int key = i * kBN + r;
-        // (Byte 0 stands for 2^−127, below the normal numbers.)
-        const uint32_t kb = sc->k_scale[tile % kScaleRing][r];
-        const int kv = key < w.len ? static_cast<int>(sc->v_scale[tile % kScaleRing][r]) - 127 : -1024;
+      int exponent = 0;  // of this thread's value row, relative to the reference
+      // The scales of tile i of the pair, the n-th of the part: the softmax wants them before the widened values.
+      // Slot n % 8 was read for tile n − 8, whose second product the wait for a place to widen into has told the end of.
+      auto scales = [&](int i, int n) {
+        ok = mbar_wait_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, abort_flag, p.err, tree_site(0x2b));
+        const uint32_t kb = sc->k_scale[n % kScaleRing][r];
+        const int kv =
+            i * kBN + r < w.len ? static_cast<int>(sc->v_scale[n % kScaleRing][r]) - 127 : -1024;
         const int top = __reduce_max_sync(0xffffffffu, kv);
-        if (lane == 0) sc->top[tile & 1][warp - 12] = top;
+        if (lane == 0) sc->top[n & 1][warp - 12] = top;
+        // (Byte 0 stands for 2^−127, below the normal numbers.)
+        sc->ks[n % kTileRing][r] = kb == 0 ? 5.877471754111438e-39f : __uint_as_float(kb << 23);
         ok = !named_any(4, 128, !ok);  // joined by all converters; any failed wait ends them all
-        if (!ok) break;
-        const int* tp = sc->top[tile & 1];
-        const int most = max(max(tp[0], tp[1]), max(tp[2], tp[3]));
+        const int4 tp = *reinterpret_cast<const int4*>(sc->top[n & 1]);
+        const int most = max(max(tp.x, tp.y), max(tp.z, tp.w));
         if (i == w.t0 || most > ref + kKvLazy) ref = most;
-        sc->ks[tile % kTileRing][r] = kb == 0 ? 5.877471754111438e-39f : __uint_as_float(kb << 23);
-        if (r == 0) sc->ref[tile % kTileRing] = ref;
-        // 2^(kv − ref) as fp16, at most 2^7; far below the reference it fades into fp16's subnormals and out.
-        const int e = kv - ref;
+        if (r == 0) sc->ref[n % kTileRing] = ref;
+        exponent = kv - ref;
+        mbar_arrive(&ms->ks_full[n % kTileRing]);
+      };
+      scales(w.t0, tile);
+#pragma unroll 1
+      for (int i = w.t0; ok && i < w.t1; ++i, ++tile) {
+        // 2^exponent as fp16, at most 2^7; far below the reference it fades into fp16's subnormals and out.
+        const int e = exponent;
         const uint32_t f1 = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
         const uint32_t f2 = f1 | (f1 << 16);
         const __half2 scale2 = *reinterpret_cast<const __half2*>(&f2);
-        const bool edge = key >= context;
+        if (i + 1 < w.t1) {
+          scales(i + 1, tile + 1);
+          if (!ok) break;
+        }
+        const int slot = tile % C::kRV;
+        ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(0x2d)) &&
+             mbar_wait_inl(&ms->v16_empty[tile & 1], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x2c));
+        const int key = i * kBN + r;
         const uint8_t* src = smem + C::kOffV + slot * kSlot + r * D;
         uint8_t* dst = smem + C::kOffV16 + (tile & 1) * C::kV16 + r * 128;
         const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
-        bool bad = false;
-#pragma unroll 2
-        for (int ch = 0; ch < D / 16; ++ch) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
-          uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-          if (edge) {  // drafted keys: NaN codes out; past the end: everything out
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-#pragma unroll
-              for (int b8 = 0; b8 < 4; ++b8)
-                if (((w4[q] >> (8 * b8)) & 0x7f) == 0x7f) w4[q] &= ~(0xffu << (8 * b8)), bad = key < w.len;
-              if (key >= w.len) w4[q] = 0;
-            }
-          }
+        auto widen = [&](int ch, const uint32_t(&w4)[4]) {
           uint32_t o[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -752,14 +768,45 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           uint8_t* block = dst + (ch >> 2) * kBN * 128;  // 64 elements per 128-byte row
           *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        };
+        if ((i + 1) * kBN <= context) {
+#pragma unroll
+          for (int c4 = 0; c4 < D / 16; c4 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (((c4 + q) ^ sw) << 4));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t w4[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+              widen(c4 + q, w4);
+            }
+          }
+        } else {
+          // The tile holds drafted keys, whose NaN codes are taken out and flagged, or the end: everything out behind it.
+          bool bad = false;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 16; ++ch) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
+            uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+            if (key >= context) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (int b8 = 0; b8 < 4; ++b8)
+                  if (((w4[q] >> (8 * b8)) & 0x7f) == 0x7f) w4[q] &= ~(0xffu << (8 * b8)), bad = key < w.len;
+                if (key >= w.len) w4[q] = 0;
+              }
+            }
+            widen(ch, w4);
+          }
+          if (bad) atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
         }
-        if (bad) atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
         fence_proxy_async_smem();
         mbar_arrive(&ms->v16_full[tile & 1]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
       }
-    } while (ok && w.next());
+    } while (ok && w.next(p));
   } else {
     reg_dealloc<C::kRegsOther>();  // idle until the end
   }
