@@ -43,9 +43,9 @@
 // E4M3 cache: K is multiplied as it is; q enters as two E4M3 terms
 // q·2⁻ᵃ = hi + lo/16 in separate columns (exact for elements down to 2⁻¹⁴ of the
 // row's largest, below that off by 2⁻²² of it), and the key's power of two
-// multiplies the score in fp32.  Four converter warps widen V to fp16, each row
-// times its power of two relative to a reference that O shares, and lay out the
-// keys' powers of two as floats; P̃ is fp16 (2⁻¹¹).  The reference is
+// multiplies the score in fp32.  V is widened to fp16 (exact) by the softmax
+// warps before they take up the tile's scores, so P̃ is fp16 (2⁻¹¹); the value
+// row's power of two is folded into P̃ relative to a running maximum.  The reference is
 // taken 2^3 below the maximum and P̃ stays below 2^15, so fp16's subnormals begin
 // 2⁻¹⁷ below a row's largest weight and weights are off by at most 2⁻²⁸ of it.
 //
@@ -66,22 +66,18 @@ namespace {
 constexpr int kBN = kTreeBN;
 constexpr int kPBlock = kBN * 128;       // P̃ᵀ: one 128-byte row per key
 constexpr int kMaxRing = 8;
+constexpr int kThreads = 384;            // warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11
+// Registers per thread at launch and after the warpgroups' split.  A softmax thread holds its scores and partial
+// sums, 2·NR values, and a spilled one would go to L2, shared memory leaving next to no L1.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch && kThreads == 384, "register split");
 constexpr int kScaleRing = 16;           // E4M3: tiles whose scale bytes are staged (V slots and four more)
-constexpr int kTileRing = 8;             // E4M3: tiles whose converted scales are kept
 constexpr int kFRing = 4;                // pieces whose row factors may be live at once
 constexpr int kBadRing = 8;              // pieces whose flags of bad values may be
 
 // NR rows of a pair, shared by both streams.
 template <int D, bool FP8, int NR>
 struct Cfg {
-  // Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11; E4M3: converters 12–15.  Registers per
-  // thread at launch and after the warpgroups' split: a softmax thread holds its scores and partial sums, 2·NR values,
-  // and a spilled one would go to L2, shared memory leaving next to no L1.
-  static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-  static constexpr int kRegsSoftmax = FP8 ? 168 : 208;
-  static constexpr int kRegsOther = 88;
-  static_assert(2 * kRegsSoftmax + (FP8 ? 2 : 1) * kRegsOther <= (FP8 ? 4 : 3) * kRegsLaunch, "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
   static constexpr int kTerms = FP8 ? 1 : 2;                  // of P̃
   static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
@@ -89,10 +85,10 @@ struct Cfg {
   static constexpr int kPNext = kPCols <= 32 ? kPCols * 2 : kPBlock;  // from a stream's rows to the other's
   static constexpr int kP = kPCols <= 32 ? kPBlock : 2 * kPBlock;
   static constexpr int kQTile = FP8 ? 2 * NR * D : NR * D * 2;
-  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;          // a widened V tile, double buffered
+  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;          // a stream's widened V tile
   static constexpr int kFixed = 2 * kV16 + kP + kQTile;
   // K and V ring slots in what is left of 227 KB after this, the bookkeeping and the alignment pad.
-  static constexpr int kMisc = (FP8 ? 13 : 6) * 1024;
+  static constexpr int kMisc = (FP8 ? 9 : 6) * 1024;
   static constexpr int kRoom = 226 * 1024 - kMisc - kFixed;
   static constexpr int kRing = kRoom / kSlot < 14 ? kRoom / kSlot : 14;
   static constexpr int kRK = kRing / 2;
@@ -114,7 +110,7 @@ struct Cfg {
 template <int NR, bool FP8>
 struct Misc {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing], q_full, q_empty, drain;
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], sc_full[kScaleRing], q_full, q_empty, drain;
   alignas(16) float nm[2][NR];         // minus the reference maxima (log2 units), 0 while a row has seen nothing
   alignas(16) float f[kFRing][NR];     // E4M3: what a row's raw scores are multiplied by
   float corr[2][NR];                   // factor of the last rescale
@@ -123,13 +119,11 @@ struct Misc {
   int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
   int64_t o_off[2][NR];                // its element offset in O
   int fresh[2][NR];                    // a live row that has seen nothing yet
-  alignas(16) int top[2][4];           // E4M3: converters' maxima of the value rows' exponents
-  int ref[kTileRing];                  // E4M3: exponent that a tile's widened values are relative to
-  alignas(16) float ks[FP8 ? kTileRing : 1][kBN];  // E4M3: the keys' powers of two
+  int kv_red[2][4];                    // per stream and warp
   alignas(16) uint8_t k_scale[FP8 ? kScaleRing : 1][kBN];  // written by bulk copies
   alignas(16) uint8_t v_scale[FP8 ? kScaleRing : 1][kBN];
   uint32_t bad[kBadRing][8];           // drafted keys with non-finite values (one bit each)
-  long long warp_sum[16];
+  long long warp_sum[kThreads / 32];
   int start[3];
   uint32_t tmem_base;
   int abort_flag;
@@ -167,6 +161,36 @@ __device__ __forceinline__ void reduce_cols(float (&v)[N], int lane, Op op, floa
   }
   static_assert(N <= 32, "one total per lane");
   if ((lane & (32 / N - 1)) == 0) out[base] = v[0];
+}
+
+// Widens one value row of D E4M3 codes to fp16.  src: the row in its slot,
+// swizzled as TMA wrote it; dst: the row in the first 64-column block of the fp16
+// tile.  EDGE: the row may be a drafted one, whose NaN codes are taken out and
+// reported by the result, or lie past the end (dead).
+template <int D, bool EDGE>
+__device__ __forceinline__ bool widen_row(const uint8_t* src, uint8_t* dst, int r, bool drafted, bool dead) {
+  const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+  bool bad = false;
+#pragma unroll
+  for (int ch = 0; ch < D / 16; ++ch) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (EDGE && drafted) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (((w[e] >> (8 * q)) & 0x7f) == 0x7f) w[e] &= ~(0xffu << (8 * q)), bad = true;
+    }
+    if (EDGE && dead) w[0] = w[1] = w[2] = w[3] = 0;
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = e4m3x2_to_f16x2(w[e >> 1] >> (16 * (e & 1)));
+    uint8_t* block = dst + (ch >> 2) * kBN * 128;  // 64 elements per 128-byte row
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  return bad;
 }
 
 // Multiplies N columns of this thread's lane by w[i]·k.
@@ -255,14 +279,14 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, u
 }
 
 template <int D, bool FP8, int NR>
-__global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, FP8, NR>;
   constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
   constexpr int kSlot = C::kSlot;
   // Rescale once a score exceeds the reference by kLazy; the reference is taken kBase below the maximum.
   constexpr float kLazy = FP8 ? 11.f : 8.f;
   constexpr float kBase = FP8 ? 3.f : 0.f;
-  constexpr int kKvLazy = 7;  // E4M3: widened values stay below 448·2^7
+  constexpr int kKvLazy = 4;  // fp16 P̃ stays below 2^(11 + 4)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
@@ -289,11 +313,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       mbar_init(&ms->s_free[s], 128);
       mbar_init(&ms->p_full[s], 128);
       mbar_init(&ms->p_free[s], 1);
-      mbar_init(&ms->v16_full[s], 128);
-      mbar_init(&ms->v16_empty[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
-    for (int s = 0; s < kTileRing; ++s) mbar_init(&ms->ks_full[s], 128);
     mbar_init(&ms->q_full, 32);
     mbar_init(&ms->q_empty, 1);
     mbar_init(&ms->drain, 1);
@@ -305,14 +326,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
     tmem_alloc(&ms->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-  const TreePart my = find_part<C::kThreads>(p, part, ms->warp_sum, ms->start);
+  const TreePart my = find_part<kThreads>(p, part, ms->warp_sum, ms->start);
   const uint32_t tmem = ms->tmem_base;
   const int bshift = 31 - __clz(p.block_size);  // a power of two
 
   if (my.count <= 0) {
     // nothing left for this CTA
   } else if (warp == 8 || warp == 10) {
-    reg_dealloc<C::kRegsOther>();
+    reg_dealloc<kRegsOther>();
     // ------------------------------------------- loads of K (warp 8) and V (warp 10)
     const bool is_v = warp == 10;
     const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
@@ -354,7 +375,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
         const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
         if (lane == 0) {
           mbar_arrive_expect_tx(&full[slot], kSlot);
-          // The slot is free: the tile kRV before it has been widened, and its scale bytes read.
+          // The slot is free: the tile kRV before it has been widened, so the tile kRV + 3 before is done with, and
+          // so are its scale bytes.
           if (FP8 && is_v) mbar_arrive_expect_tx(&ms->sc_full[sc], 2 * n_real * p.block_size);
         }
         __syncwarp();
@@ -387,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       }
     }
   } else if (warp == 9) {
-    reg_dealloc<C::kRegsOther>();
+    reg_dealloc<kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
     constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
@@ -398,8 +420,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
     const bool leader = elect_one_lane();
     Ring<C::kRK> rk;
     Ring<C::kRV> rv;
-    int v16 = 0;                    // E4M3: the widened tile's place and parity
-    uint32_t v16_par = 0;
     uint32_t s_par = 3, p_par = 0;  // parities of s_free and p_full to wait for, a bit per stream
     bool ok = true;
     TreeWalk w;
@@ -443,13 +463,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
         }
         if (s >= 2) {  // the second product of tile s − 2, of the same stream
           ok = ok && mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(3));
-          ok = ok && (FP8 ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(4))
-                          : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(4)));
+          if constexpr (!FP8) ok = ok && mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(4));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           p_par ^= 1u << g;
           tc_fence_after();
-          const uint32_t vb = sV + (FP8 ? v16 * C::kV16 : rv.slot * kSlot);
+          const uint32_t vb = sV + (FP8 ? g * C::kV16 : rv.slot * kSlot);
           const uint32_t dst = tmem + C::kColO + g * C::kPCols;
           if (leader) {
             // A: 16 keys per k-step, the head dim along M in 64-element blocks (D = 64: the one block twice, the upper
@@ -460,11 +479,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
             for (int kk = 0; kk < kBN / 16; ++kk)
               mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + kk * 128, kIdescO, (s >= 4 || kk > 0) ? 1u : 0u);
             mma_commit(&ms->p_free[g]);
-            mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
+            if constexpr (!FP8) mma_commit(&ms->v_empty[rv.slot]);
           }
           rv.advance();
-          v16 ^= 1;
-          v16_par ^= v16 == 0;
         }
       }
     } while (ok && __shfl_sync(0xffffffffu, w.next(p), 0));
@@ -473,7 +490,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       mbar_wait_drain_inl(&ms->drain, 0, kTreeDrainNs);
     }
   } else if (warp < 8) {
-    reg_alloc<C::kRegsSoftmax>();
+    reg_alloc<kRegsSoftmax>();
     // ----------------------------- softmax: one key per thread, the stream's NR rows
     const int g = warp >> 2;
     const int bar = 1 + g;                 // the stream's barrier
@@ -513,7 +530,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       float l[NR];
 #pragma unroll
       for (int n = 0; n < NR; ++n) l[n] = 0.f;
-      int kv_ref = 0;
+      int kv_ref = -1024;
       int done = 0;  // tiles of this piece that this stream has worked on
       const float* f_row = ms->f[w.index % kFRing];
 #pragma unroll 1
@@ -537,13 +554,28 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
             }
           }
         }
-        // E4M3: the key's power of two, and the exponent that the widened values are relative to.
+        // E4M3: the powers of two of the key (byte 0 stands for 2^−127, below the normal numbers) and the value row.
         float ks = 1.f;
-        int ref = kv_ref;
+        int kv = -1024;
         if constexpr (FP8) {
-          ok = mbar_wait_inl(&ms->ks_full[tile % kTileRing], (tile / kTileRing) & 1, abort_flag, p.err, tree_site(13)) && ok;
-          ks = ms->ks[tile % kTileRing][kt];
-          ref = ms->ref[tile % kTileRing];
+          ok = mbar_wait_inl(&ms->sc_full[tile % kScaleRing], (tile / kScaleRing) & 1, abort_flag, p.err, tree_site(13)) && ok;
+          const uint32_t sk = ms->k_scale[tile % kScaleRing][kt];
+          ks = sk == 0 ? 5.877471754111438e-39f : __uint_as_float(sk << 23);
+          if (key < w.len) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
+          // This key's value row to fp16, while the scores are made.
+          const int slot = tile % C::kRV;
+          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(11)) && ok;
+          if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
+          const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
+          uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
+          if (!tail) {
+            widen_row<D, false>(src, dst, kt, false, false);
+          } else if (widen_row<D, true>(src, dst, kt, key >= context, key >= w.len) && key < w.len) {
+            atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
         }
         ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, tree_site(7)) && ok;
         tc_fence_after();
@@ -602,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
             for (int e = 0; e < 4; ++e)
               mx[e] = n + 4 + e < NR ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NR]) : fmaxf(mx[e], x[n + e]);
           const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          const bool over = unseen || top > kLazy || ref != kv_ref;
+          const bool over = unseen || top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
           if (!named_any(bar, 128, over || !ok)) break;
           // A reference moves (the first tile always does): exchange the tile's maxima, rescale ℓ and O.
           if (named_any(bar, 128, !ok)) {
@@ -611,7 +643,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
             break;
           }
           reduce_cols<NR>(x, lane, OpMax(), red + (warp & 3) * NR);
+          if constexpr (FP8) {
+            const int top_kv = __reduce_max_sync(0xffffffffu, kv);
+            if (lane == 0) ms->kv_red[g][warp & 3] = top_kv;
+          }
           named_sync(bar, 128);
+          int kv_new = kv_ref;
+          if constexpr (FP8) {
+            const int* kr = ms->kv_red[g];
+            kv_new = max(kv_ref, max(max(kr[0], kr[1]), max(kr[2], kr[3])));
+          }
           bool still = false;
           if (kt < NR) {
             // Maxima relative to the old reference (0 for a row that has seen nothing).
@@ -631,18 +672,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
           if (done > 0) {
             ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
             tc_fence_after();
-            const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - ref, -200))) : 1.f;
+            const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
 #pragma unroll 1
             for (int term = 0; term < C::kTerms; ++term) rescale_cols<NR>(o_addr + term * NR, corr, kf);
           }
-          kv_ref = ref;
+          kv_ref = kv_new;
         }
         if (dead) break;
         tc_fence_before();
         mbar_arrive(&ms->s_free[g]);
 
-        // P̃'s buffer is free once the product of the stream's tile before has run.
-        if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
+        // P̃'s buffer is free once the product of the stream's tile before has run (E4M3 has waited for it above).
+        if (!FP8 && u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
+        // E4M3: the value row's scale relative to the running maximum, a power of two, at most 2^kKvLazy.
+        const float wv = !FP8 ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
         // 16-byte chunks of the key's row, XORed with the key; the stream's begin at `first`.
         uint8_t* prow = smem + C::kOffP + (C::kPNext == kPBlock ? g * kPBlock : 0) + kt * 128;
         const int first = C::kPNext == kPBlock ? 0 : g * (C::kPNext / 16);
@@ -656,7 +699,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
             x[n + 1] = ex2_approx(x[n + 1]);
             fadd2(l[n], l[n + 1], l[n], l[n + 1], x[n], x[n + 1]);
             if constexpr (FP8) {
-              hi[e] = pack_f16x2(x[n], x[n + 1]);
+              float a, d;
+              fmul2(a, d, x[n], x[n + 1], wv, wv);
+              hi[e] = pack_f16x2(a, d);
             } else {
               hi[e] = pack_bf16x2(x[n], x[n + 1]);
               lo[e] = pack_bf16x2(x[n] - __uint_as_float(hi[e] << 16), x[n + 1] - __uint_as_float(hi[e] & 0xffff0000u));
@@ -804,107 +849,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NR>::kThreads, 1) tree_kernel(cons
       // The flags of three pieces ago: the other stream may still be at the piece before.
       if (tid < 8) ms->bad[(w.index + kBadRing - 3) % kBadRing][tid] = 0;
     } while (ok && w.next(p));
-  } else if (FP8 && warp >= 12) {
-    reg_dealloc<C::kRegsOther>();
-    // ------------------------------------ converters: one value row and one key's scale per thread
-    const int r = tid - 384;
-    int tile = 0, ref = 0;
-    bool ok = true;
-    TreeWalk w;
-    w.begin(p, my);
-    do {
-      const int context = w.len - w.drafts;
-      int exponent = 0;  // of this thread's value row, relative to the reference
-      // The scales of tile i of the pair, the n-th of the part: the softmax wants them before the widened values.
-      // Slot n % 8 was read for tile n − 8, whose second product the wait for a place to widen into has told the end of.
-      auto scales = [&](int i, int n) {
-        ok = mbar_wait_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, abort_flag, p.err, tree_site(0x2b));
-        const uint32_t kb = ms->k_scale[n % kScaleRing][r];
-        const int kv =
-            i * kBN + r < w.len ? static_cast<int>(ms->v_scale[n % kScaleRing][r]) - 127 : -1024;
-        const int top = __reduce_max_sync(0xffffffffu, kv);
-        if (lane == 0) ms->top[n & 1][warp - 12] = top;
-        // (Byte 0 stands for 2^−127, below the normal numbers.)
-        ms->ks[n % kTileRing][r] = kb == 0 ? 5.877471754111438e-39f : __uint_as_float(kb << 23);
-        ok = !named_any(4, 128, !ok);  // joined by all converters; any failed wait ends them all
-        const int4 tp = *reinterpret_cast<const int4*>(ms->top[n & 1]);
-        const int most = max(max(tp.x, tp.y), max(tp.z, tp.w));
-        if (i == w.t0 || most > ref + kKvLazy) ref = most;
-        if (r == 0) ms->ref[n % kTileRing] = ref;
-        exponent = kv - ref;
-        mbar_arrive(&ms->ks_full[n % kTileRing]);
-      };
-      scales(w.t0, tile);
-#pragma unroll 1
-      for (int i = w.t0; ok && i < w.t1; ++i, ++tile) {
-        // 2^exponent as fp16, at most 2^7; far below the reference it fades into fp16's subnormals and out.
-        const int e = exponent;
-        const uint32_t f1 = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
-        const uint32_t f2 = f1 | (f1 << 16);
-        const __half2 scale2 = *reinterpret_cast<const __half2*>(&f2);
-        if (i + 1 < w.t1) {
-          scales(i + 1, tile + 1);
-          if (!ok) break;
-        }
-        const int slot = tile % C::kRV;
-        ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(0x2d)) &&
-             mbar_wait_inl(&ms->v16_empty[tile & 1], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x2c));
-        const int key = i * kBN + r;
-        const uint8_t* src = smem + C::kOffV + slot * kSlot + r * D;
-        uint8_t* dst = smem + C::kOffV16 + (tile & 1) * C::kV16 + r * 128;
-        const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
-        auto widen = [&](int ch, const uint32_t(&w4)[4]) {
-          uint32_t o[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t wide = e4m3x2_to_f16x2(w4[q >> 1] >> (16 * (q & 1)));
-            const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&wide), scale2);
-            o[q] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          uint8_t* block = dst + (ch >> 2) * kBN * 128;  // 64 elements per 128-byte row
-          *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-        };
-        if ((i + 1) * kBN <= context) {
-#pragma unroll
-          for (int c4 = 0; c4 < D / 16; c4 += 4) {
-            uint4 v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (((c4 + q) ^ sw) << 4));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t w4[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-              widen(c4 + q, w4);
-            }
-          }
-        } else {
-          // The tile holds drafted keys, whose NaN codes are taken out and flagged, or the end: everything out behind it.
-          bool bad = false;
-#pragma unroll 1
-          for (int ch = 0; ch < D / 16; ++ch) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
-            uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-            if (key >= context) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                for (int b8 = 0; b8 < 4; ++b8)
-                  if (((w4[q] >> (8 * b8)) & 0x7f) == 0x7f) w4[q] &= ~(0xffu << (8 * b8)), bad = key < w.len;
-                if (key >= w.len) w4[q] = 0;
-              }
-            }
-            widen(ch, w4);
-          }
-          if (bad) atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&ms->v16_full[tile & 1]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
-      }
-    } while (ok && w.next(p));
   } else {
-    reg_dealloc<C::kRegsOther>();
+    reg_dealloc<kRegsOther>();
     // ------------------------- Q of every piece but the first, which the streams load
     TreeWalk w;
     w.begin(p, my);
@@ -980,10 +926,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
 template <int D, bool FP8, int NR>
 cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
   constexpr int kSmem = Cfg<D, FP8, NR>::kOffMisc + static_cast<int>(sizeof(Misc<NR, FP8>)) + 1024;
-  static_assert(sizeof(Misc<NR, FP8>) <= Cfg<D, FP8, NR>::kMisc && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
   using M = Misc<NR, FP8>;
   static_assert(Cfg<D, FP8, NR>::kOffMisc % 16 == 0 && offsetof(M, nm) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
-                    offsetof(M, ks) % 16 == 0 && offsetof(M, k_scale) % 16 == 0 && offsetof(M, v_scale) % 16 == 0,
+                    offsetof(M, k_scale) % 16 == 0 && offsetof(M, v_scale) % 16 == 0,
                 "16-byte accesses and bulk copies");
   // The register split draws on what the block is launched with, which is the compiled kernel's for good.
   static std::atomic<bool> checked{false};
@@ -992,12 +938,12 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
     cudaFuncAttributes a;
     e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR>);
     if (e != cudaSuccess) return e;
-    if (a.numRegs < Cfg<D, FP8, NR>::kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (a.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     checked.store(true, std::memory_order_relaxed);
   }
   e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, FP8, NR><<<static_cast<unsigned>(p.parts), Cfg<D, FP8, NR>::kThreads, kSmem, s>>>(p);
+  tree_kernel<D, FP8, NR><<<static_cast<unsigned>(p.parts), kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
