@@ -82,8 +82,8 @@ struct Cfg {
   static constexpr int kTerms = FP8 ? 1 : 2;                  // of P̃
   static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
   // A key's P̃ᵀ row is 2·kPCols bytes; the streams' rows lie side by side in 128 bytes where both fit.
-  static constexpr int kPNext = kPCols <= 32 ? kPCols * 2 : kPBlock;  // from a stream's rows to the other's
-  static constexpr int kP = kPCols <= 32 ? kPBlock : 2 * kPBlock;
+  static constexpr int kPNext = !FP8 && kPCols <= 32 ? kPCols * 2 : kPBlock;  // from a stream's rows to the other's
+  static constexpr int kP = !FP8 && kPCols <= 32 ? kPBlock : 2 * kPBlock;
   static constexpr int kQTile = FP8 ? 2 * NR * D : NR * D * 2;
   static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;          // a stream's widened V tile
   static constexpr int kFixed = 2 * kV16 + kP + kQTile;
