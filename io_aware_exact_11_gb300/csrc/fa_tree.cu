@@ -902,19 +902,38 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
       return p.slots_by_pair ? pair + pieces.x + i : 2ll * (pieces.x + i) + (i > 0 ? 0 : 1);
     };
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    for (int i = 0; i < pieces.y; ++i) m = fmaxf(m, ml[slot(i) * rows + rr].x);
-#pragma unroll 4
-    for (int i = 0; i < pieces.y; ++i) {
-      const float2 x = ml[slot(i) * rows + rr];
-      const float* src = p.part_o + (slot(i) * rows + rr) * D + lane * E;
-      float v[E];
+    // Four pieces' statistics and rows are on their way at once.
+    constexpr int kBatch = 4;
+#pragma unroll 1
+    for (int i = 0; i < pieces.y; i += kBatch) {
+      float2 x[kBatch];
+      float v[kBatch][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = src[e];
-      if (x.y == 0.f) continue;
-      const float w = exp2f(x.x - m) * x.y;
-      l += w;
+      for (int j = 0; j < kBatch; ++j) {
+        x[j] = make_float2(-INFINITY, 0.f);
+        if (i + j < pieces.y) {
+          const int64_t at = slot(i + j) * rows + rr;
+          x[j] = ml[at];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += w * v[e];
+          for (int e = 0; e < E; ++e) v[j][e] = p.part_o[at * D + lane * E + e];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, x[j].x);
+      const float keep = l != 0.f ? exp2f(m - top) : 0.f;
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= keep;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (x[j].y == 0.f) continue;
+        const float w = exp2f(x[j].x - top) * x[j].y;
+        l += w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += w * v[j][e];
+      }
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;

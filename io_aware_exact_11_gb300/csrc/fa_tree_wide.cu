@@ -62,6 +62,7 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kRK * kSlot;
   static constexpr int kOffMisc = kOffV + kRV * kSlot;
   static constexpr int kSmem = kOffMisc + kMisc + 1024;
+  static constexpr int kHalves = FP8 ? 2 : 1;
   static constexpr uint32_t kColO = 256;                 // TMEM: S of the streams at 0 and 128, O at 256 and 256 + D
   static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && kRV + 4 <= kScaleRing && kSmem <= 227 * 1024, "rings");
   static_assert(kSlot % 1024 == 0 && kQTile % 1024 == 0, "swizzle atoms");
@@ -69,7 +70,7 @@ struct Cfg {
 
 struct Bars {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t s_full[2], p_full[2], o_full[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing], q_full, drain;
+  uint64_t s_full[2], p_half[2], p_full[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing], q_full, drain;
   uint32_t bad[8][8];       // drafted keys with non-finite values, of up to eight pieces
   long long warp_sum[16];
   TreeWalk walk[2];         // of the streams
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
       mbar_init(&ms->p_full[s], 128);
-      mbar_init(&ms->o_full[s], 1);
+      mbar_init(&ms->p_half[s], 128);
       mbar_init(&ms->v16_full[s], 128);
       mbar_init(&ms->v16_empty[s], 1);
     }
@@ -336,26 +337,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
 #pragma unroll 1
       for (int s = 0; s < steps + 2; ++s) {
         const int g = s & 1;
-        const bool last_use = TILES == 1 || g == 1;  // of the K or V tile
+        const bool first_use = TILES == 1 || g == 0, last_use = TILES == 1 || g == 1;  // of the K or V tile
         const uint32_t ts = tmem + g * kBN;
+        // The waits for K and V come first: what follows P̃'s arrival is on the streams' critical path.
+        if (first_use && s < steps)
+          ok = ok && mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, tree_site(0x25));
         if (s >= 2) {  // P̃V of step s − 2, of the same stream
-          ok = ok && mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(0x23));
-          ok = ok && (FP8 ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(0x2f))
-                          : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24)));
+          if (first_use)
+            ok = ok && (FP8 ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(0x2f))
+                            : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24)));
+          ok = ok && mbar_wait_inl(C::kHalves == 2 ? &ms->p_half[g] : &ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(0x28));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          p_par ^= 1u << g;
           tc_fence_after();
           const uint32_t vb = sV + (FP8 ? v16 * C::kV16 : rv.slot * kSlot);
+          const uint64_t bd = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, kBN * 128, 1024);
+          constexpr int kSteps = kBN / 16 / C::kHalves;
+          // The first 64 keys, then the others, which the softmax warps have written meanwhile.
+#pragma unroll
+          for (int half = 0; half < C::kHalves; ++half) {
+            if (half == 1) {
+              ok = mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(0x23));
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (leader) {
+#pragma unroll
+              for (int term = 0; term < C::kTerms; ++term)
+#pragma unroll
+                for (int kk = half * kSteps; kk < (half + 1) * kSteps; ++kk)  // A: P̃ over S's columns, 16 keys in 8 of them
+                  mma_bf16_ts(tmem + C::kColO + g * D, ts + term * 64 + kk * 8, bd + kk * (kPg5 ? 256 : 128), kIdescO,
+                              (s >= 4 || half + term > 0 || kk > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          p_par ^= 1u << g;
           if (leader) {
-            const uint64_t bd = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, kBN * 128, 1024);
-#pragma unroll
-            for (int term = 0; term < C::kTerms; ++term)
-#pragma unroll
-              for (int kk = 0; kk < kBN / 16; ++kk)  // A: P̃ over S's columns, 16 keys in 8 of them
-                mma_bf16_ts(tmem + C::kColO + g * D, ts + term * 64 + kk * 8, bd + kk * (kPg5 ? 256 : 128), kIdescO,
-                            (s >= 4 || term > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&ms->o_full[g]);
+            if (s >= steps) mma_commit(&ms->s_full[g]);  // no scores follow: O is complete
             if (last_use) mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
           }
           if (last_use) {
@@ -366,7 +385,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         }
         if (s < steps) {
           // S over what P̃V has just read: the tensor pipe runs them in this order.
-          ok = ok && mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, tree_site(0x25));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -411,7 +429,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lane_base + g * kBN;
     const uint32_t o_addr = tmem + lane_base + C::kColO + g * D;
-    int tile0 = 0, used = 0;       // tiles of the pieces before, and those of this stream
+    int tile0 = 0;                 // tiles of the pieces before
+    uint32_t s_par = 0;            // parity of s_full to wait for: scores of each tile, then O of the piece
     bool ok = true;
     const TreeWalk& w = ms->walk[g];
     if (kt == 0) ms->walk[g].begin(p, my);
@@ -459,9 +478,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         }
         if constexpr (FP8)  // the keys' powers of two
           ok = mbar_wait_inl(&ms->ks_full[tile % kTileRing], (tile / kTileRing) & 1, abort_flag, p.err, tree_site(0x26)) && ok;
-        ok = mbar_wait_inl(&ms->s_full[g], (used + done) & 1, abort_flag, p.err, tree_site(0x27)) && ok;
-        // P̃V of the stream's tile before has run, S was issued behind it; this keeps the barrier's phases in step.
-        if (done > 0) ok = mbar_wait_inl(&ms->o_full[g], (used + done - 1) & 1, abort_flag, p.err, tree_site(0x28)) && ok;
+        // (P̃V of the stream's tile before has run too: S was issued behind it.)
+        ok = mbar_wait_inl(&ms->s_full[g], s_par, abort_flag, p.err, tree_site(0x27)) && ok;
+        s_par ^= 1u;
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -556,6 +575,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           }
           tmem_st32(s_addr + half * 32, pk);
           if constexpr (C::kTerms == 2) tmem_st32(s_addr + 64 + half * 32, lo);
+          if (C::kHalves == 2 && half == 0 && (FP8 || !tail)) {  // the first half goes early, unless value rows are still to be cleared
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&ms->p_half[g]);
+          }
         }
         l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
@@ -588,12 +612,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         __syncwarp();
         tmem_wait_st();
         tc_fence_before();
+        if (C::kHalves == 2 && (!busy || (!FP8 && tail))) mbar_arrive(&ms->p_half[g]);
         mbar_arrive(&ms->p_full[g]);
       }
       tile0 += n_tiles;
-      used += done;
       // ------------------------------------------------------------ end of the piece
-      if (done > 0) ok = ok && mbar_wait_inl(&ms->o_full[g], (used - 1) & 1, abort_flag, p.err, tree_site(0x2a));
+      if (done > 0) {
+        ok = ok && mbar_wait_inl(&ms->s_full[g], s_par, abort_flag, p.err, tree_site(0x2a));
+        s_par ^= 1u;
+      }
       const bool whole = w.whole();
       const int64_t slot_row = w.slot(p, part) * p.T * p.G + rr;
       float m = l_run != 0.f ? m_run : -INFINITY, sum = l_run;
