@@ -1012,7 +1012,7 @@ TreeWorkspace tree_workspace(int B, int H_kv, int64_t rows, int d, int64_t parts
   w.by_pair = pairs + parts - 1 < 2 * parts;
   const size_t slots = parts == 1 ? 0 : static_cast<size_t>(w.by_pair ? pairs + parts - 1 : 2 * parts);
   w.part_o = round256(static_cast<size_t>(pairs) * 8);
-  w.part_ml = w.part_o + round256(slots * rows * d * 4);
+  w.part_ml = w.part_o + round256(slots * fa::tree_piece_rows(rows) * d * 4);
   w.bytes = w.part_ml + round256(slots * rows * 2 * 4);
   return w;
 }

@@ -161,7 +161,7 @@ struct TreeParams {
   const uint8_t* mask;     // mask[b·mask_sb + t·T + u], or null: u <= t
   int64_t mask_sb;
   int2* pieces;    // [B·Hkv]: first part of a pair and the number of parts it lies in
-  float* part_o;   // [slot, T·G, d] fp32: o/ℓ of a cut pair's pieces
+  float* part_o;   // [slot, tree_piece_rows(T·G), d] fp32: o/ℓ of a cut pair's pieces
   float* part_ml;  // [slot, T·G, 2] fp32: (m in log2 units, ℓ)
   int B, Hq, Hkv, G, T, num_blocks, block_size, max_blocks;
   unsigned g_magic;   // ceil(2^32 / G), for rows / G (G > 1)
@@ -176,7 +176,12 @@ cudaError_t launch_rope(const RopeParams& p, bool fp32, bool inter, bool in_plac
 cudaError_t launch_cache_append(const CacheParams& p, int d, bool fp8, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheParams& p, int d, bool fp8, cudaStream_t s);
 int tree_cta_rows(int64_t rows);  // rows one CTA takes, for T·G rows in all
-cudaError_t launch_tree_wide(const TreeParams& p, int d, bool fp8, cudaStream_t s);  // more than 64 rows a pair
+constexpr int kTreeNarrowRows = 32;  // up to here a kernel of its own
+// Rows of a cut pair's piece in part_o: beyond the narrow kernel whole groups of 32.
+__host__ __device__ constexpr int64_t tree_piece_rows(int64_t rows) {
+  return rows > kTreeNarrowRows ? (rows + 31) / 32 * 32 : rows;
+}
+cudaError_t launch_tree_wide(const TreeParams& p, int d, bool fp8, cudaStream_t s);  // more rows than that
 cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s);
 
 cudaError_t launch_fwd_bf16(int d, const FwdParams& p, cudaStream_t s);

@@ -872,36 +872,51 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 }
 
 // Joins the pieces of a cut pair, which hold o/ℓ: weights w = 2^(m − max)·ℓ, O = Σ w·(o/ℓ) / Σ w.  Rows that see
-// nothing are written here too.  One warp per row (b, h, t).
-constexpr int kMergeWarps = 4;
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
-  if (r >= static_cast<int64_t>(p.B) * p.Hq * p.T) return;
-  const int t = static_cast<int>(r % p.T);
-  const int64_t bh = r / p.T;
-  const int h = static_cast<int>(bh % p.Hq);
-  const int b = static_cast<int>(bh / p.Hq);
+// nothing are written here too.  A thread takes E columns of a row; a warp takes a row, or, where the kernel for many
+// rows has stored chunks of four columns for 32 rows side by side (WIDE), those columns of 32 rows.
+constexpr int kMergeWarps = 4, kMergeWarpsWide = 8;
+template <int D, bool WIDE>
+__global__ void __launch_bounds__((WIDE ? kMergeWarpsWide : kMergeWarps) * 32)
+    tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int E = WIDE ? D / kMergeWarpsWide : D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = p.T * p.G;
+  int64_t pair;
+  int rr, c0;
+  if constexpr (WIDE) {
+    const int groups = (rows + 31) >> 5;
+    pair = blockIdx.x / groups;
+    rr = static_cast<int>(blockIdx.x - pair * groups) * 32 + lane;
+    c0 = warp * E;
+    if (rr >= rows) return;
+  } else {
+    const unsigned r = blockIdx.x * kMergeWarps + warp;
+    pair = r / rows;
+    rr = static_cast<int>(r - pair * rows);
+    c0 = lane * E;
+    if (pair >= static_cast<int64_t>(p.B) * p.Hkv) return;
+  }
+  const int b = static_cast<int>(static_cast<unsigned>(pair) / p.Hkv);
+  const int t = token_of(p, rr);
+  const int h = static_cast<int>(pair - static_cast<int64_t>(b) * p.Hkv) * p.G + rr - t * p.G;
   int len, drafts;
   seq_lengths(p, b, len, drafts);
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + b * p.so[0] + h * p.so[1] + t * p.so[2] + lane * E;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + b * p.so[0] + h * p.so[1] + t * p.so[2] + c0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   float m = -INFINITY, l = 0.f;
   if (t < drafts) {
-    const int64_t pair = static_cast<int64_t>(b) * p.Hkv + h / p.G;
     const int2 pieces = p.pieces[pair];
     if (pieces.y == 1) return;  // not cut: the first kernel has written it
-    const int64_t rows = static_cast<int64_t>(p.T) * p.G;
-    const int64_t rr = static_cast<int64_t>(t) * p.G + h % p.G;
     auto slot = [&](int i) -> int64_t {
       return p.slots_by_pair ? pair + pieces.x + i : 2ll * (pieces.x + i) + (i > 0 ? 0 : 1);
     };
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    const int piece_rows = tree_piece_rows(rows);
+    const int first = WIDE ? c0 * 32 - lane * (D - 4) : c0;  // the columns, from row rr's place in [piece_rows, D]
+    constexpr int kStep = E < 4 ? E : 4;
     // Four pieces' statistics and rows are on their way at once.
     constexpr int kBatch = 4;
 #pragma unroll 1
@@ -914,8 +929,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
         if (i + j < pieces.y) {
           const int64_t at = slot(i + j) * rows + rr;
           x[j] = ml[at];
+          const float* src = p.part_o + (slot(i + j) * piece_rows + rr) * D + first;
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] = p.part_o[at * D + lane * E + e];
+          for (int e = 0; e < E; e += kStep) {
+            if constexpr (kStep == 4) {
+              const float4 y = *reinterpret_cast<const float4*>(src + (WIDE ? e * 32 : e));
+              v[j][e] = y.x, v[j][e + 1] = y.y, v[j][e + 2] = y.z, v[j][e + 3] = y.w;
+            } else {
+              const float2 y = *reinterpret_cast<const float2*>(src + e);
+              v[j][e] = y.x, v[j][e + 1] = y.y;
+            }
+          }
         }
       }
       float top = m;
@@ -938,8 +962,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16_rn(l != 0.f ? o[e] * inv : 0.f);
-  if (p.lse != nullptr && lane == 0) p.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = l != 0.f ? pack_bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
+  if (p.lse != nullptr && c0 == 0)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + t] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, bool WIDE>
+cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(p.T) * p.G, pairs = static_cast<int64_t>(p.B) * p.Hkv;
+  const int64_t blocks = WIDE ? pairs * ((rows + 31) / 32) : (pairs * rows + kMergeWarps - 1) / kMergeWarps;
+  // Its blocks may come up while the first kernel runs; they wait for its end.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3((WIDE ? kMergeWarpsWide : kMergeWarps) * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, WIDE>, p);
 }
 
 template <int D, bool FP8, int NR>
@@ -969,27 +1012,18 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
 template <int D, bool FP8>
 cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
-  cudaError_t e = rows <= 16   ? launch_rows<D, FP8, 16>(p, s)
-                  : rows <= 32 ? launch_rows<D, FP8, 32>(p, s)
-                               : launch_tree_wide(p, D, FP8, s);
+  const bool wide = rows > kTreeNarrowRows;
+  cudaError_t e = wide         ? launch_tree_wide(p, D, FP8, s)
+                  : rows <= 16 ? launch_rows<D, FP8, 16>(p, s)
+                               : launch_rows<D, FP8, 32>(p, s);
   if (e != cudaSuccess) return e;
-  // The joining kernel's blocks may come up while the first kernel runs; they wait for its end.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.B) * p.Hq * p.T + kMergeWarps - 1) / kMergeWarps));
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p);
+  return wide ? launch_merge<D, true>(p, s) : launch_merge<D, false>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s) {
-  if (static_cast<int64_t>(p.B) * p.Hq * p.T > (1ll << 32) || static_cast<int64_t>(p.parts) * p.row_tiles > 0x7fffffff)
+  if (static_cast<int64_t>(p.B) * p.Hq * p.T >= (1ll << 31) || static_cast<int64_t>(p.parts) * p.row_tiles > 0x7fffffff)
     return cudaErrorInvalidValue;
   if (d == 128) return fp8 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
   if (d == 64) return fp8 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);

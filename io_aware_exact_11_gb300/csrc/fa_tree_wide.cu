@@ -101,7 +101,9 @@ __device__ __forceinline__ void load_q_tile(const TreeParams& p, const TreeWalk&
                                             int id) {
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
   constexpr int kPer = kRowTile * kChunks / NT;
-  constexpr int kBatch = 4;       // loads in flight per thread
+  // Loads in flight per thread (bf16 with shared rows spills registers with eight).
+  constexpr int kBatch = NT == 256 && !FP8 ? 4 : kPer < 8 ? kPer : 8;
+  static_assert(kPer % kBatch == 0, "rows of the tile");
   const int live = w.drafts * p.G - row0;
 #pragma unroll 1
   for (int i0 = 0; i0 < kPer; i0 += kBatch) {
@@ -338,20 +340,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       for (int s = 0; s < steps + 2; ++s) {
         const int g = s & 1;
         const bool first_use = TILES == 1 || g == 0, last_use = TILES == 1 || g == 1;  // of the K or V tile
-        const uint32_t ts = tmem + g * kBN;
-        // The waits for K and V come first: what follows P̃'s arrival is on the streams' critical path.
-        if (first_use && s < steps)
-          ok = ok && mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, tree_site(0x25));
-        if (s >= 2) {  // P̃V of step s − 2, of the same stream
-          if (first_use)
+        const bool scores = s < steps, product = s >= 2;
+        // Everything that can be is done before P̃ arrives: what follows is on the streams' critical path, and this
+        // warp gets an instruction through every dozen cycles while the softmax warps run.
+        if (first_use) {
+          if (scores) ok = ok && mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, tree_site(0x25));
+          if (product)
             ok = ok && (FP8 ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(0x2f))
                             : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24)));
-          ok = ok && mbar_wait_inl(C::kHalves == 2 ? &ms->p_half[g] : &ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(0x28));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t vb = sV + (FP8 ? v16 * C::kV16 : rv.slot * kSlot);
-          const uint64_t bd = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, kBN * 128, 1024);
+        }
+        const uint32_t ts = tmem + g * kBN;
+        const uint32_t to = tmem + C::kColO + g * D;
+        const uint32_t vb = sV + (FP8 ? v16 * C::kV16 : rv.slot * kSlot);
+        const uint32_t kb = sK + rk.slot * kSlot;
+        const uint32_t qb = sQ + (TILES == 1 ? 0 : g * C::kQTile);
+        const uint64_t vd = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, kBN * 128, 1024);
+        const uint64_t qd = FP8 && D == 64 ? sdesc_sw64(qb, 16, 512) : sdesc_sw128(qb, 16, 1024);
+        const uint64_t kd = FP8 && D == 64 ? sdesc_sw64(kb, 16, 512) : sdesc_sw128(kb, 16, kPg5 ? 2048 : 1024);
+        if (product)
+          ok = ok && mbar_wait_inl(C::kHalves == 2 ? &ms->p_half[g] : &ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err,
+                                   tree_site(0x28));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (product) {  // P̃V of step s − 2, of the same stream
           constexpr int kSteps = kBN / 16 / C::kHalves;
           // The first 64 keys, then the others, which the softmax warps have written meanwhile.
 #pragma unroll
@@ -367,52 +379,40 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
               for (int term = 0; term < C::kTerms; ++term)
 #pragma unroll
                 for (int kk = half * kSteps; kk < (half + 1) * kSteps; ++kk)  // A: P̃ over S's columns, 16 keys in 8 of them
-                  mma_bf16_ts(tmem + C::kColO + g * D, ts + term * 64 + kk * 8, bd + kk * (kPg5 ? 256 : 128), kIdescO,
+                  mma_bf16_ts(to, ts + term * 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), kIdescO,
                               (s >= 4 || half + term > 0 || kk > 0) ? 1u : 0u);
             }
           }
           if (!ok) break;
           p_par ^= 1u << g;
-          if (leader) {
-            if (s >= steps) mma_commit(&ms->s_full[g]);  // no scores follow: O is complete
-            if (last_use) mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
-          }
-          if (last_use) {
-            rv.advance();
-            v16 ^= 1;
-            v16_par ^= v16 == 0;
+          // With shared rows the value slot is given back at once (after the scores' issue: 1 us of 104 slower); with two
+          // row tiles the scores' issue comes first (the other way round: 135 instead of 130 us, 256 rows, 8 x 16384 keys).
+          if (TILES == 1 && leader) mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
+        }
+        if (scores && leader) {  // S over what P̃V has just read: the tensor pipe runs them in this order
+          if constexpr (FP8) {
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_e4m3_ss(ts, qd + term * (kRowTile * D / 16) + kk * 2, kd + kk * 2, kIdescS, (term > 0 || kk > 0) ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ss(ts, qd + (kk >> 2) * (kRowTile * 8) + (kk & 3) * 2, kd + (kk >> 2) * 64 + (kk & 3) * 2, kIdescS,
+                          kk > 0 ? 1u : 0u);
           }
         }
-        if (s < steps) {
-          // S over what P̃V has just read: the tensor pipe runs them in this order.
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t kb = sK + rk.slot * kSlot;
-          const uint32_t qb = sQ + (TILES == 1 ? 0 : g * C::kQTile);
-          if (leader) {
-            if constexpr (FP8) {
-              const uint64_t bd = D == 128 ? sdesc_sw128(kb, 16, 1024) : sdesc_sw64(kb, 16, 512);
-#pragma unroll
-              for (int term = 0; term < 2; ++term) {
-                const uint32_t qt = qb + term * kRowTile * D;
-                const uint64_t ad = D == 128 ? sdesc_sw128(qt, 16, 1024) : sdesc_sw64(qt, 16, 512);
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                  mma_e4m3_ss(ts, ad + kk * 2, bd + kk * 2, kIdescS, (term > 0 || kk > 0) ? 1u : 0u);
-              }
-            } else {
-              const uint64_t ad = sdesc_sw128(qb, 16, 1024);
-              const uint64_t bd = sdesc_sw128(kb, 16, kPg5 ? 2048 : 1024);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                mma_bf16_ss(ts, ad + (kk >> 2) * (kRowTile * 8) + (kk & 3) * 2,
-                            bd + (kk >> 2) * 64 + (kk & 3) * 2, kIdescS, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&ms->s_full[g]);
-            if (last_use) mma_commit(&ms->k_empty[rk.slot]);
-          }
-          if (last_use) rk.advance();
+        if (leader) {
+          if (scores || product) mma_commit(&ms->s_full[g]);  // scores, or, where none follow, O of the piece
+          if (last_use && scores) mma_commit(&ms->k_empty[rk.slot]);
+          if (TILES == 2 && last_use && product) mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
+        }
+        if (last_use && scores) rk.advance();
+        if (last_use && product) {
+          rv.advance();
+          v16 ^= 1;
+          v16_par ^= v16 == 0;
         }
       }
     } while (ok && __shfl_sync(0xffffffffu, w.next(p), 0));
@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         s_par ^= 1u;
       }
       const bool whole = w.whole();
-      const int64_t slot_row = w.slot(p, part) * p.T * p.G + rr;
+      const int64_t slot = w.slot(p, part);
+      const int64_t slot_row = slot * p.T * p.G + rr;
       float m = l_run != 0.f ? m_run : -INFINITY, sum = l_run;
       float scale[2] = {0.f, 0.f};  // what the streams' O is multiplied by
       if constexpr (TILES == 1) {
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         const int c0 = TILES == 1 ? g * kHalf : 0;
         __nv_bfloat16* out =
             static_cast<__nv_bfloat16*>(p.o) + w.b * p.so[0] + h * p.so[1] + static_cast<int64_t>(t) * p.so[2];
-        float* part_o = p.part_o + slot_row * D;
+        // A cut pair's row is stored in chunks of four columns, 32 rows' chunks side by side: a warp's stores are whole lines.
+        float* part_o = p.part_o + (slot * tree_piece_rows(p.T * p.G) + rr - lane) * D + lane * 4;
 #pragma unroll 1
         for (int c = c0; c < c0 + kHalf; c += 32) {
           float o[32];
@@ -689,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             if (!whole) {
 #pragma unroll
               for (int q = 0; q < 32; q += 4)
-                *reinterpret_cast<float4*>(part_o + c + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+                *reinterpret_cast<float4*>(part_o + (c + q) * 32) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
             } else {
 #pragma unroll
               for (int q = 0; q < 32; q += 8)
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
               v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at + c]);
             if (fabsf(v) <= 3.4028234663852886e38f) continue;
             if (!whole)
-              part_o[c] += v;
+              part_o[(c & ~3) * 32 + (c & 3)] += v;
             else
               out[c] = __float2bfloat16_rn(__bfloat162float(out[c]) + v);
           }

@@ -113,8 +113,9 @@ def test_decode_tree_workspace(L):
     size = L.fa_decode_tree_workspace_size
     # one part: a pair of words per (sequence, key/value head) and no pieces
     assert size(2, 28, 4, 8, 128, 1) == 256
-    # three parts of eight pairs: two slots per part beat 8 + 2; of 7·8 rows, 128 values and (m, ℓ)
-    assert size(2, 28, 4, 8, 128, 3) == 256 + 6 * 56 * 128 * 4 + -(-6 * 56 * 8 // 256) * 256
+    # three parts of eight pairs: two slots per part beat 8 + 2; of 7·8 rows (o in
+    # groups of 32 rows), 128 values and (m, ℓ)
+    assert size(2, 28, 4, 8, 128, 3) == 256 + 6 * 64 * 128 * 4 + -(-6 * 56 * 8 // 256) * 256
     # three parts of one pair: slots 0, 1, 2
     assert size(1, 4, 1, 1, 64, 3) == 256 + 3 * 4 * 64 * 4 + 256
     assert size(2, 28, 4, 8, 128, 0) == size(2, 28, 4, 8, 128, 152)         # no device here: 152 SMs
