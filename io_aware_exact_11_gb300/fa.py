@@ -618,14 +618,14 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
         pos_ptr = positions.data_ptr()
         pos_sb = positions.stride(0) if len(shape) == 2 and B > 1 else 0
     if out_q is None:
-        out_q = q.new_empty((B, Hq, N, d))
+        out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _check_out("out_q", out_q, q.shape, q.dtype, dev)
     if k is None:
         st = _strides(q, q, out_q, out_q)
     else:
         if out_k is None:
-            out_k = k.new_empty((B, Hk, N, d))
+            out_k = torch.empty_like(k, memory_format=torch.contiguous_format)
         else:
             _check_out("out_k", out_k, k.shape, q.dtype, dev)
         st = _strides(q, k, out_q, out_k)
@@ -736,11 +736,11 @@ def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, 
         raise ValueError("n must be at least 1")
     shape = (B, hkv, n, d)
     if out_k is None:
-        out_k = k_cache.new_empty(shape, dtype=torch.bfloat16)
+        out_k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
     else:
         _check_out("out_k", out_k, shape, torch.bfloat16, dev)
     if out_v is None:
-        out_v = k_cache.new_empty(shape, dtype=torch.bfloat16)
+        out_v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
     else:
         _check_out("out_v", out_v, shape, torch.bfloat16, dev)
     status = lib().fa_cache_gather(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
@@ -800,17 +800,18 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = q.new_empty((B, Hq, T, d))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _check_out("out", out, q.shape, torch.bfloat16, dev)
     if lse is None:
-        lse = q.new_empty((B, Hq, T), dtype=torch.float32)
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
     else:
         _check_out("lse", lse, (B, Hq, T), torch.float32, dev)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
     if workspace is None:
-        workspace = q.new_empty(max(decode_tree_workspace_size(B, Hq, hkv, T, d, max_parts), 16), dtype=torch.uint8)
+        size = max(decode_tree_workspace_size(B, Hq, hkv, T, d, max_parts), 16)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     status = lib().fa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
