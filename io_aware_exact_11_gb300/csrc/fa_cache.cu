@@ -13,6 +13,12 @@
 // Bound: device memory.  Writing: 2·(2d) bytes read and 2·(d + 1) written per
 // token and head (bf16: 2·2d); d/8 lanes hold one row, 16 bytes of it each, and
 // the row maximum is log2(d/8) lane exchanges, so a row never leaves registers.
+//
+// Measured on GB300 (d = 128): gathering 4 sequences of 32768 E4M3 keys, 8 heads: 124 us,
+// 6.5 TB/s, 0.97 of a device copy; writing 8 ragged sequences of up to 8192 tokens as
+// E4M3, 4 heads: 35 us, 4.5 TB/s, 0.67 (it quantises on the way, and a block's rows end
+// in several short ones); a token for each of 64 sequences: the launch (11 us a call
+// from Python).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -244,7 +250,8 @@ cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
 }
 
 // Four tokens per thread once one per thread would fill the machine several times over: the look-up of their slots
-// and the loads of their rows then overlap, where one per thread spends its life on that chain of loads.
+// and the loads of their rows then overlap, where one per thread spends its life on that chain of loads.  (Four and
+// one, replaying a graph: gathering 4 x 32768 E4M3 keys 128 and 151 us, writing 8 x 8192 tokens 40 and 44 us.)
 template <bool APPEND, int D, bool FP8>
 cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
   const int64_t threads = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 8);

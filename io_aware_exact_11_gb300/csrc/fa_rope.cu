@@ -10,14 +10,18 @@
 // so w_i/2π is held as a 64-bit fraction of a turn and p times it is one 64-bit
 // product that wraps exactly where whole turns drop out.  Far positions lose
 // nothing: the error is p·2⁻⁶⁴ turns (plus the float64 rounding of w_i), where
-// a float32 product would be off by p·2⁻²⁴ radians.  sincospif of the signed
-// fraction then has float32 accuracy.
+// a float32 product would be off by p·2⁻²⁴ radians.  Of the product the upper 32
+// bits are kept (2⁻³² turns, 1.5e-9 rad) and rounded to float32, half turns in
+// [−1, 1): 2⁻²⁵ of them, π·2⁻²⁵ rad at most.  sincospif adds its own 2 ulp.
 //
 // Bound: device memory, q and k read once and written once.  A thread owns one
 // 16-byte column of one token and walks over heads with it, so that the sines
 // are computed once for all of them and kept in registers; with few tokens
 // there are few heads per thread (the launcher splits them until the grid fills
 // the machine).
+//
+// Measured on GB300: the gradients of 16 + 16 heads of 128 elements at 2 x 8192 tokens, bf16: 49 us, 5.5 TB/s,
+// 0.82 of a device copy; one token: the launch (17 us a call from Python).
 #include "fa_kernels.h"
 #include "sm103.cuh"
 
@@ -133,7 +137,8 @@ cudaError_t launch_v(RopeParams p, bool in_place, cudaStream_t stream) {
   const int64_t blocks = (items + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   // Heads per thread: all of a tensor's when the tokens alone give every SM about 1024 threads, fewer (down to one)
-  // when they do not.
+  // when they do not.  All heads, this rule and one head a thread, replaying
+  // a graph: one token of 28 + 4 heads 16, 9, 9 us; 2 x 8192 tokens of 16 + 16 heads 51, 51, 105 us.
   const int most = p.Hq > p.Hk ? p.Hq : p.Hk;
   int per = most;
   while (per > 1 && blocks * ((p.Hq + per - 1) / per + (p.Hk + per - 1) / per) < 152 * 8) per = (per + 1) / 2;

@@ -1,5 +1,6 @@
 // fa_tree.cu — attention of T drafted tokens per sequence over a paged cache
-// (T = 1: plain decode), bf16 or E4M3, on tcgen05 tensor cores.
+// (T = 1: plain decode), bf16 or E4M3, on tcgen05 tensor cores: the kernel for up
+// to 32 query rows (T·G, G query heads per key/value head) and the joining kernel.
 //
 // Sequence b holds len keys, the last m of them those of its m ≤ T drafted
 // tokens.  Token t sees every key of the context [0, len − m) and drafted key u
@@ -9,8 +10,8 @@
 // Products.  Both run transposed, with the keys (or the head dim) on the 128
 // matrix rows and the T·G query rows of a key/value head on the N side:
 //   Sᵀ[key, row] = K Qᵀ,  Oᵀ[dim, row] += Vᵀ P̃ᵀ.
-// N is as small as the rows are few, where putting 1 … 64 query rows on the
-// 128-row side would pay for 128 rows of products and exponentials.  K and V go
+// N is as small as the rows are few (16 or 32), where putting them on the 128-row
+// side would pay for 128 rows of products and exponentials.  K and V go
 // from the pages into shared memory as they lie (a page of one head is one TMA
 // box) and are the A operand both times: K with its head dim contiguous, V with
 // its head dim along M.  A softmax thread owns one key of the tile (TMEM lane)
@@ -19,10 +20,8 @@
 //
 // Two streams.  A tile's softmax is a chain of waits (scores out of TMEM, the
 // group's vote, exponentials, P̃ into shared memory, the second product), so two
-// warpgroups run two of them at once, each with its own S, P̃, O and statistics.
-// Up to 64 rows they take alternate key tiles and are joined at the end; above,
-// they take two tiles of 64 rows over the same keys, so that K and V are fetched
-// once for 128 rows.
+// warpgroups run two of them at once on alternate key tiles, each with its own S,
+// P̃, O and statistics, and are joined at the end of a piece.
 //
 // Row maxima lie across threads in this layout, so they are not recomputed per
 // tile: a row keeps its reference m while every score is less than 2^8 above it,
@@ -30,16 +29,14 @@
 // and O and ℓ rescaled.  ℓ stays in per-thread partial sums until the end.
 //
 // Work.  The 128-key tiles of all (b, key/value head) pairs form one line that is
-// cut into equal parts, one per CTA (per CTA group where there are several row
-// tiles), so ragged batches load every SM alike and short ones spread over the
-// machine.  A CTA walks over its part without draining its pipeline between
+// cut into equal parts, one per CTA, so ragged batches load every SM alike and
+// short ones spread over the machine.  A CTA walks over its part without draining its pipeline between
 // pairs.  A pair that is cut leaves o/ℓ, m, ℓ of each piece in the workspace,
 // and a second kernel joins them.
 //
-// bf16 cache: up to 64 rows, where device memory bounds it, P̃ enters as two bf16
-// terms p ≈ hi + lo in separate columns (good to 2⁻¹⁷; one term alone adds an
-// error as large as O's own rounding to bf16).  Above 64 rows the products bound
-// it and P̃ is one bf16 term, as in the prefill forward.
+// bf16 cache: P̃ enters as two bf16 terms p ≈ hi + lo in separate columns (good to
+// 2⁻¹⁷; one term alone adds an error as large as O's own rounding to bf16), which
+// costs nothing here, where device memory bounds it.
 // E4M3 cache: K is multiplied as it is; q enters as two E4M3 terms
 // q·2⁻ᵃ = hi + lo/16 in separate columns (exact for elements down to 2⁻¹⁴ of the
 // row's largest, below that off by 2⁻²² of it), and the key's power of two
@@ -54,6 +51,13 @@
 // rows and not by others, and 0·NaN would reach the others through the product:
 // non-finite elements of drafted rows are zeroed there too, and added to the
 // rows that do see them at the end.
+//
+// Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements:
+//   4 / 16 / 32 rows, bf16   93 / 93 / 95 us   5.75 TB/s, 0.86 of a device copy: bound by device memory
+//   4 / 16 / 32 rows, E4M3   60 / 60 / 72 us   4.5 / 4.5 / 3.8 TB/s: bound by the softmax warps, which widen V
+// E4M3, not kept: four or eight converter warps beside the softmax warps (64 and 67 us at 4 rows, 82 and 83 at 32);
+// V widened by integer operations instead of the conversion instruction (slower, and it loses NaN); P̃ as two E4M3
+// terms over V as it is (the terms span too few binades).
 #include <stddef.h>
 
 #include <atomic>
@@ -1012,6 +1016,11 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
 template <int D, bool FP8>
 cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
+  // By the rows of a pair; 8 sequences of 16384 keys, 8 key/value heads, us with the one and the other:
+  //   4 and 16 rows as 16 columns or 32    E4M3 59, 60 | 65, 68    bf16 92, 93 | 93, 93
+  //   16 and 32 rows here or in the kernel for many rows    E4M3 60, 72 | 77, 80    bf16 93, 95 | 98, 100
+  // (32 rows are the most that fit here without tiles of rows; 64 columns spilled registers and took 81 us where the
+  // other kernel took 69: 8 tokens of 7 heads a group, 16 ragged sequences of up to 8192 bf16 keys.)
   const bool wide = rows > kTreeNarrowRows;
   cudaError_t e = wide         ? launch_tree_wide(p, D, FP8, s)
                   : rows <= 16 ? launch_rows<D, FP8, 16>(p, s)
