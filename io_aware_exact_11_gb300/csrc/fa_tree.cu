@@ -566,20 +566,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const uint32_t sk = ms->k_scale[tile % kScaleRing][kt];
           ks = sk == 0 ? 5.877471754111438e-39f : __uint_as_float(sk << 23);
           if (key < w.len) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
-          // This key's value row to fp16, while the scores are made.
-          const int slot = tile % C::kRV;
-          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(11)) && ok;
-          if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
-          const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
-          uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
-          if (!tail) {
-            widen_row<D, false>(src, dst, kt, false, false);
-          } else if (widen_row<D, true>(src, dst, kt, key >= context, key >= w.len) && key < w.len) {
-            atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
         }
         ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, tree_site(7)) && ok;
         tc_fence_after();
@@ -686,8 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tc_fence_before();
         mbar_arrive(&ms->s_free[g]);
 
-        // P̃'s buffer is free once the product of the stream's tile before has run (E4M3 has waited for it above).
-        if (!FP8 && u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
+        // P̃'s buffer, and E4M3's widened values', are free once the product of the stream's tile before has run.
+        if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
         // E4M3: the value row's scale relative to the running maximum, a power of two, at most 2^kKvLazy.
         const float wv = !FP8 ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
         // 16-byte chunks of the key's row, XORed with the key; the stream's begin at `first`.
@@ -718,6 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
+        if constexpr (FP8) {  // this key's value row to fp16
+          const int slot = tile % C::kRV;
+          ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(11)) && ok;
+          const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
+          uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
+          if (!tail) {
+            widen_row<D, false>(src, dst, kt, false, false);
+          } else if (widen_row<D, true>(src, dst, kt, key >= context, key >= w.len) && key < w.len) {
+            atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
+          }
+        }
         if (!FP8 && tail && key >= context) {
           // This key's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
           const int slot = tile % C::kRV;
@@ -744,6 +741,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&ms->p_full[g]);
+        if constexpr (FP8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->v_empty[tile % C::kRV]);
+        }
       }
       tile0 += n_tiles;
       used += done;
