@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import numpy as np
@@ -523,11 +524,12 @@ def _addr(t):
     return t.data_ptr() if t is not None else None
 
 
-_Strides6, _Strides12 = ctypes.c_int64 * 6, ctypes.c_int64 * 12
+_pack6, _pack12 = struct.Struct("=6q").pack, struct.Struct("=12q").pack
 
 
 def _strides(*ts):
-    """Element strides of all but the last dimension (which must be contiguous), or None if all are contiguous."""
+    """Element strides of all but the last dimension (which must be contiguous) as the bytes of int64 values, or None if
+    all are contiguous."""
     for t in ts:
         if not t.is_contiguous():
             break
@@ -539,7 +541,7 @@ def _strides(*ts):
         if x[-1] != 1 and t.shape[-1] > 1:
             raise ValueError("the head dim must be contiguous")
         st += x[:-1]
-    return (_Strides6 if len(st) == 6 else _Strides12)(*st)
+    return (_pack6 if len(st) == 6 else _pack12)(*st)
 
 
 def _check_out(name, t, shape, dtype, dev):
@@ -605,7 +607,7 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
         w_ptr = w.data_ptr()
     else:
         w = np.ascontiguousarray(inv_freq, dtype=np.float64)
-        w_ptr = w.ctypes.data
+        w_ptr = w.tobytes()  # a copy costs less than the array's address
     if w.ndim != 1:
         raise ValueError("inv_freq must be one row of rot_dim/2 values")
     pos_ptr, pos_sb = None, 0
