@@ -360,6 +360,7 @@ FA_API fa_status fa_cache_append(const void* k, const void* v, void* k_cache, vo
  *   n >= seq_lens[b] are set to zero.  E4M3 codes are multiplied by their row's
  *   power of two, which is exact.  seq_lens outside [0, max_blocks·block_size]
  *   and bad page ids give zero rows and FA_ERR_INVALID_ARG from fa_device_status.
+ *   k and v must not overlap themselves or each other.
  */
 FA_API fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                                  const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* k,
@@ -386,9 +387,12 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   tree_mask[b·mask_stride_b + t·T + u] != 0 (device bytes; NULL: u <= t).  A
  *   row that sees no key, padding rows t >= m_b among them, gives O = 0 and
  *   LSE = −∞.  Keys a row does not see do not reach its results, whatever they
- *   hold; slots past a sequence's end are not read into results.
+ *   hold; slots past a sequence's end are not read into results.  (With an E4M3
+ *   cache the values of a sequence share one range: a key's share of O is off by
+ *   up to 2^-27 of the largest |v| among the keys that some row sees.)
  *   q, o [B,H_q,T,d] bf16; strides NULL or 6 element strides {q_b, q_h, q_t, o_…},
- *   multiples of 8, >= 0 (o must not overlap itself); lse [B,H_q,T] float32 or NULL.
+ *   multiples of 8, >= 0 (o must not overlap itself, and may be q only with q's
+ *   strides); lse [B,H_q,T] float32 or NULL.
  *   Caches, scales and block_table as for fa_cache_append.
  *   draft_lens outside [0, T], seq_lens outside [m_b, max_blocks·block_size]
  *   and bad page ids are caught on the device (the sequence counts as empty,

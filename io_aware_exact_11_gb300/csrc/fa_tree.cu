@@ -45,6 +45,7 @@
 // row's power of two is folded into P̃ relative to a running maximum.  The reference is
 // taken 2^3 below the maximum and P̃ stays below 2^15, so fp16's subnormals begin
 // 2⁻¹⁷ below a row's largest weight and weights are off by at most 2⁻²⁸ of it.
+// In all a key's share of O is off by 2⁻²⁷ of the largest value that some row sees.
 //
 // Values in masked places.  Cache slots past the sequence end are zeroed in
 // shared memory before V is used.  A drafted key's value row is seen by some
@@ -565,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           ok = mbar_wait_inl(&ms->sc_full[tile % kScaleRing], (tile / kScaleRing) & 1, abort_flag, p.err, tree_site(13)) && ok;
           const uint32_t sk = ms->k_scale[tile % kScaleRing][kt];
           ks = sk == 0 ? 5.877471754111438e-39f : __uint_as_float(sk << 23);
-          if (key < w.len) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
+          // (A drafted key that no row sees takes no part in the maximum, whatever it holds.)
+          if (key < w.len && seen != 0) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
         }
         ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, tree_site(7)) && ok;
         tc_fence_after();

@@ -771,8 +771,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       auto scales = [&](int i, int n) {
         ok = mbar_wait_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, abort_flag, p.err, tree_site(0x2b));
         const uint32_t kb = sc->k_scale[n % kScaleRing][r];
-        const int kv =
-            i * kBN + r < w.len ? static_cast<int>(sc->v_scale[n % kScaleRing][r]) - 127 : -1024;
+        const int key = i * kBN + r;
+        bool used = key < w.len;
+        if (used && key >= context && p.mask != nullptr) {  // a drafted key that no row sees takes no part
+          used = false;
+          const uint8_t* mk = p.mask + w.b * p.mask_sb + (key - context);
+#pragma unroll 8
+          for (int t = 0; t < w.drafts; ++t) used = used || mk[static_cast<int64_t>(t) * p.T] != 0;
+        }
+        const int kv = used ? static_cast<int>(sc->v_scale[n % kScaleRing][r]) - 127 : -1024;
         const int top = __reduce_max_sync(0xffffffffu, kv);
         if (lane == 0) sc->top[n & 1][warp - 12] = top;
         // (Byte 0 stands for 2^−127, below the normal numbers.)

@@ -631,6 +631,8 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
         else:
             _check_out("out_k", out_k, k.shape, q.dtype, dev)
         st = _strides(q, k, out_q, out_k)
+    if not -(1 << 31) <= position0 < 1 << 31:
+        raise ValueError("position0 must be an int32")
     status = lib().fa_rope(q.data_ptr(), _addr(k), out_q.data_ptr(), _addr(out_k), B, Hq, Hk, N, d, 2 * w.shape[0],
                            code, st, pos_ptr, pos_sb, int(position0), w_ptr, float(magnitude),
                            FA_ROPE_INTERLEAVED if interleaved else FA_ROPE_HALF, inverse, _current_stream(dev))
@@ -734,8 +736,8 @@ def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, 
     B = block_table.shape[0]
     _check_lens("seq_lens", seq_lens, B)
     n = int(n)
-    if n < 1:
-        raise ValueError("n must be at least 1")
+    if not 1 <= n < 1 << 31:
+        raise ValueError("n must be at least 1, and an int32")
     shape = (B, hkv, n, d)
     if out_k is None:
         out_k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
@@ -799,6 +801,8 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
             raise ValueError("tree_mask must be [T, T] or [B, T, T] with contiguous rows")
         mask_ptr = tree_mask.data_ptr()
         mask_sb = step[0] if len(shape) == 3 and B > 1 else 0
+    if not -(1 << 31) <= max_parts < 1 << 31:
+        raise ValueError("max_parts must be an int32")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:

@@ -323,6 +323,37 @@ def test_writes_stay_inside_their_tensors(cache, T):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [6, 40])
+@pytest.mark.parametrize("value", [3e38, -3e38])
+def test_a_drafted_key_that_nobody_sees_may_hold_the_largest_numbers(cache, T, value):
+    import torch
+    mask = np.tril(np.ones((1, T, T), dtype=bool))
+    mask[:, :, 2] = False
+
+    def huge(name, b, x):
+        x[:, x.shape[1] - T + 2] = value
+    for n in (T, 131, 128 + T):
+        p = Paged(np.random.default_rng(n), [n], 2, 128, 16, cache, edit=huge)
+        q = bf16(np.random.default_rng(9).standard_normal((1, 4, T, 128))).cuda()
+        o, lse = fa.decode_tree(q, *p.args(), tree_mask=torch.from_numpy(mask).cuda(), max_parts=2, **p.kw())
+        p.k[0][:, n - T + 2] = p.v[0][:, n - T + 2] = 0.0  # (what it holds is no part of the bounds either)
+        check_tree(o, lse, q, p, [T], mask, 128 ** -0.5)
+    fa.device_status()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [2, 40])
+def test_output_in_place_of_the_queries(cache, T):
+    import torch
+    p = Paged(np.random.default_rng(T), [900, 50, 0, 300], 2, 128, 32, cache)
+    for parts in (1, 5):
+        q = bf16(np.random.default_rng(1).standard_normal((4, 8, T, 128))).cuda()
+        want, lse = fa.decode_tree(q, *p.args(), max_parts=parts, **p.kw())
+        got, lse2 = fa.decode_tree(q, *p.args(), max_parts=parts, out=q, **p.kw())
+        assert got is q and torch.equal(got, want) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_sequences_that_share_pages(cache):
     """A common prefix is stored once: two rows of the table name the same pages."""
     import torch
@@ -364,6 +395,19 @@ def test_pages_beyond_32_bit_offsets(cache):
     del far, got
     torch.cuda.empty_cache()
     fa.device_status()
+
+
+def test_numbers_beyond_int32_are_refused():
+    import torch
+    p = Paged(np.random.default_rng(3), [20], 1, 64, 16, "bf16")
+    q = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for position0 in (1 << 31, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="int32"):
+            fa.rope(q, None, [1.0], position0=position0)
+    with pytest.raises(ValueError, match="int32"):
+        fa.decode_tree(q, *p.args(), max_parts=1 << 32)
+    with pytest.raises(ValueError, match="int32"):
+        fa.cache_gather(*p.args(), 1 << 32)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
