@@ -43,6 +43,15 @@ __device__ __forceinline__ bool token_sees(const TreeParams& p, int b, int t, in
   return p.mask != nullptr ? p.mask[b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t;
 }
 
+// Does any of the first `drafts` tokens see the drafted key whose column of the mask begins at mk?  (Out of line: few
+// tiles need it, and the kernels' loops are short of instruction cache.)
+static __device__ __noinline__ bool any_token_sees(const uint8_t* mk, int drafts, int T) {
+  bool sees = false;
+#pragma unroll 8
+  for (int t = 0; t < drafts; ++t) sees |= mk[static_cast<int64_t>(t) * T] != 0;
+  return sees;
+}
+
 // A CTA's part of the line of key tiles of all (b, key/value head) pairs.
 struct TreePart {
   long long per, count;   // tiles per part, and of this one

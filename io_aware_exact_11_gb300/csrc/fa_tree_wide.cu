@@ -774,10 +774,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         const int key = i * kBN + r;
         bool used = key < w.len;
         if (used && key >= context && p.mask != nullptr) {  // a drafted key that no row sees takes no part
-          used = false;
-          const uint8_t* mk = p.mask + w.b * p.mask_sb + (key - context);
-#pragma unroll 8
-          for (int t = 0; t < w.drafts; ++t) used = used || mk[static_cast<int64_t>(t) * p.T] != 0;
+          used = any_token_sees(p.mask + w.b * p.mask_sb + (key - context), w.drafts, p.T);
         }
         const int kv = used ? static_cast<int>(sc->v_scale[n % kScaleRing][r]) - 127 : -1024;
         const int top = __reduce_max_sync(0xffffffffu, kv);
