@@ -124,6 +124,7 @@ struct Misc {
   int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
   int64_t o_off[2][NR];                // its element offset in O
   int fresh[2][NR];                    // a live row that has seen nothing yet
+  int far[2];                          // E4M3: the stream's tile has gone over to bf16
   int kv_red[2][4];                    // per stream and warp
   alignas(16) uint8_t k_scale[FP8 ? kScaleRing : 1][kBN];  // written by bulk copies
   alignas(16) uint8_t v_scale[FP8 ? kScaleRing : 1][kBN];
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   constexpr float kLazy = FP8 ? 11.f : 8.f;
   constexpr float kBase = FP8 ? 3.f : 0.f;
   constexpr int kKvLazy = 4;  // fp16 P̃ stays below 2^(11 + 4)
+  constexpr int kKvFar = 8;   // value rows that are smaller by more than this need bf16's range
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
@@ -419,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
     constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
     constexpr uint32_t kIdescO = FP8 ? idesc_f16_f32(128, NR, true, true) : idesc_bf16_f32(128, C::kPCols, true, true);
+    constexpr uint32_t kIdescFar = idesc_bf16_f32(128, NR, true, true);
     const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK), sP = smem_u32(smem + C::kOffP);
     const uint32_t sV = smem_u32(smem + (FP8 ? C::kOffV16 : C::kOffV));
     const uint64_t q_desc = FP8 && D == 64 ? sdesc_sw64(sQ, 16, 512) : sdesc_sw128(sQ, 16, 1024);
@@ -475,14 +478,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           tc_fence_after();
           const uint32_t vb = sV + (FP8 ? g * C::kV16 : rv.slot * kSlot);
           const uint32_t dst = tmem + C::kColO + g * C::kPCols;
+          const bool far = FP8 && *static_cast<volatile int*>(&ms->far[g]) != 0;
           if (leader) {
             // A: 16 keys per k-step, the head dim along M in 64-element blocks (D = 64: the one block twice, the upper
             // 64 rows of the result are not read).  B: 16 keys of P̃ᵀ.
             const uint64_t ad = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, D == 128 ? kBN * 128 : 0, 1024);
             const uint64_t bd = sdesc_sw128(sP + g * C::kPNext, kPBlock, 1024);
+#pragma unroll 1
+            for (int term = 0; term < (far ? 2 : 1); ++term)
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + kk * 128, kIdescO, (s >= 4 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + term * (NR / 8) + kk * 128, far ? kIdescFar : kIdescO,
+                            (s >= 4 || term > 0 || kk > 0) ? 1u : 0u);
             mma_commit(&ms->p_free[g]);
             if constexpr (!FP8) mma_commit(&ms->v_empty[rv.slot]);
           }
@@ -574,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // x = score − reference, masked to −∞ where the row does not see the key.  A second time where a reference
         // has moved.
         float x[NR];
+        bool far = false;   // E4M3: value rows too far apart for fp16
         bool dead = false;  // a wait of some thread of the stream has failed
 #pragma unroll 1
         for (bool again = false;; again = true) {
@@ -626,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             for (int e = 0; e < 4; ++e)
               mx[e] = n + 4 + e < NR ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NR]) : fmaxf(mx[e], x[n + e]);
           const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          const bool over = unseen || top > kLazy || (FP8 && kv > kv_ref + kKvLazy);
+          const bool over = unseen || top > kLazy || (FP8 && (kv > kv_ref + kKvLazy || (kv > -126 && kv < kv_ref - kKvFar)));
           if (!named_any(bar, 128, over || !ok)) break;
           // A reference moves (the first tile always does): exchange the tile's maxima, rescale ℓ and O.
           if (named_any(bar, 128, !ok)) {
@@ -644,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if constexpr (FP8) {
             const int* kr = ms->kv_red[g];
             kv_new = max(kv_ref, max(max(kr[0], kr[1]), max(kr[2], kr[3])));
+            far = named_any(bar, 128, kv > -126 && kv < kv_new - kKvFar);  // (−126: next to nothing, or zeros)
           }
           bool still = false;
           if (kt < NR) {
@@ -677,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // P̃'s buffer, and E4M3's widened values', are free once the product of the stream's tile before has run.
         if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
         // E4M3: the value row's scale relative to the running maximum, a power of two, at most 2^kKvLazy.
-        const float wv = !FP8 ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
+        const float wv = !FP8 || far ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
         // 16-byte chunks of the key's row, XORed with the key; the stream's begin at `first`.
         uint8_t* prow = smem + C::kOffP + (C::kPNext == kPBlock ? g * kPBlock : 0) + kt * 128;
         const int first = C::kPNext == kPBlock ? 0 : g * (C::kPNext / 16);
@@ -706,14 +715,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
+        if (FP8 && far) {  // the weights as two bf16 terms, from what this thread has just stored
+#pragma unroll 1
+          for (int ch = 0; ch < NR / 8; ++ch) {
+            uint4* at = reinterpret_cast<uint4*>(prow + (((first + ch) ^ (kt & 7)) << 4));
+            uint4 a = *at, d;
+            split_f16x2(a.x, a.x, d.x);
+            split_f16x2(a.y, a.y, d.y);
+            split_f16x2(a.z, a.z, d.z);
+            split_f16x2(a.w, a.w, d.w);
+            *at = a;
+            *reinterpret_cast<uint4*>(prow + (((first + ch + NR / 8) ^ (kt & 7)) << 4)) = d;
+          }
+        }
         if constexpr (FP8) {  // this key's value row to fp16
           const int slot = tile % C::kRV;
           ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(11)) && ok;
           const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
           uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
-          if (!tail) {
+          if (kt == 0) ms->far[g] = far;
+          if (!tail && !far) {
             widen_row<D, false>(src, dst, kt, false, false);
-          } else if (widen_row<D, true>(src, dst, kt, key >= context, key >= w.len) && key < w.len) {
+          } else if (far ? widen_row_far<D>(src, dst, kt, kv - kv_ref, key >= context, key >= w.len)
+                         : widen_row<D, true>(src, dst, kt, key >= context, key >= w.len) && key < w.len) {
             atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
           }
         }

@@ -52,6 +52,45 @@ static __device__ __noinline__ bool any_token_sees(const uint8_t* mk, int drafts
   return sees;
 }
 
+// Widens one value row of D E4M3 codes times 2^e to bf16, into a tile laid out as the fp16 one: for tiles whose value
+// rows lie too far apart for fp16.  drafted: NaN codes are taken out and reported by the result; dead: zeros.
+template <int D>
+__device__ __noinline__ bool widen_row_far(const uint8_t* src, uint8_t* dst, int r, int e, bool drafted, bool dead) {
+  const float f = __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
+  const float f2 = e >= -126 ? 1.f : e < -252 ? 0.f : __uint_as_float(static_cast<uint32_t>(e + 126 + 127) << 23);
+  const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+  bool bad = false;
+#pragma unroll 1
+  for (int ch = 0; ch < D / 16; ++ch) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t c = w[i >> 1] >> (16 * (i & 1)) & 0xffffu;
+      if (drafted) {
+        if ((c & 0x7fu) == 0x7fu) c &= 0xff00u, bad = true;
+        if ((c & 0x7f00u) == 0x7f00u) c &= 0xffu, bad = true;
+      }
+      if (dead) c = 0;
+      const uint32_t h = e4m3x2_to_f16x2(c);
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      o[i] = pack_bf16x2(x.x * f * f2, x.y * f * f2);
+    }
+    uint8_t* block = dst + (ch >> 2) * kTreeBN * 128;  // 64 elements per 128-byte row
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  return bad && !dead;
+}
+
+// A pair of fp16 weights as bf16 terms hi + lo (exact: 11 bits in 8 and 8).
+__device__ __forceinline__ void split_f16x2(uint32_t pair, uint32_t& hi, uint32_t& lo) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+  hi = pack_bf16x2(x.x, x.y);
+  lo = pack_bf16x2(x.x - __uint_as_float(hi << 16), x.y - __uint_as_float(hi & 0xffff0000u));
+}
+
 // A CTA's part of the line of key tiles of all (b, key/value head) pairs.
 struct TreePart {
   long long per, count;   // tiles per part, and of this one

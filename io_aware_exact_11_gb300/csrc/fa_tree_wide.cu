@@ -103,7 +103,7 @@ struct Scales {
   alignas(16) uint8_t k_scale[kScaleRing][kBN];
   alignas(16) uint8_t v_scale[kScaleRing][kBN];
   alignas(16) float ks[kTileRing][kBN];  // the keys' powers of two
-  int ref[kTileRing];                    // exponent that the tile's widened values are relative to
+  int ref[kTileRing];                    // 2·(exponent that the tile's widened values are relative to) + (they are bf16)
   alignas(16) int top[2][4];
   float f[2 * kRowTile];                 // what a row's raw scores are multiplied by
 };
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
   constexpr float kLazy = 8.f;             // rescale once the maximum exceeds the reference by this …
   constexpr float kBase = FP8 ? 3.f : 0.f; // … the new reference lies this below the maximum
   constexpr int kKvLazy = 7;               // E4M3: widened values stay below 448·2^7
+  constexpr int kKvFar = 16;               // value rows that are smaller by more than this need bf16's range
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
     constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, kBN, false, false) : idesc_bf16_f32(128, kBN, false, false);
+    constexpr uint32_t kIdescFar = idesc_bf16_f32(128, D, false, true);
     constexpr uint32_t kIdescO = FP8 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
     const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK);
     const uint32_t sV = smem_u32(smem + (FP8 ? C::kOffV16 : C::kOffV));
@@ -342,6 +344,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     Ring<C::kRV> rv;
     int v16 = 0;         // E4M3: the widened tile's place and parity
     uint32_t v16_par = 0;
+    int vt = 0;          // E4M3: tile of the part that P̃ is multiplied with
     uint32_t p_par = 0;  // parity of p_full to wait for, a bit per stream
     bool ok = true;
     TreeWalk w;
@@ -363,6 +366,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             ok = ok && (FP8 ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(0x2f))
                             : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24)));
         }
+        const bool far = FP8 && product && (*static_cast<volatile int*>(&sc->ref[vt % kTileRing]) & 1);
+        const uint32_t idesc = far ? kIdescFar : kIdescO;
         const uint32_t ts = tmem + g * kBN;
         const uint32_t to = tmem + C::kColO + g * D;
         const uint32_t vb = sV + (FP8 ? v16 * C::kV16 : rv.slot * kSlot);
@@ -393,8 +398,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
               for (int term = 0; term < C::kTerms; ++term)
 #pragma unroll
                 for (int kk = half * kSteps; kk < (half + 1) * kSteps; ++kk)  // A: P̃ over S, 16 keys in 8 columns
-                  mma_bf16_ts(to, ts + term * 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), kIdescO,
+                  mma_bf16_ts(to, ts + term * 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc,
                               (s >= 4 || half + term > 0 || kk > 0) ? 1u : 0u);
+              if (FP8 && far) {  // the second terms
+#pragma unroll 1
+                for (int kk = half * kSteps; kk < (half + 1) * kSteps; ++kk)
+                  mma_bf16_ts(to, ts + 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc, 1u);
+              }
             }
           }
           if (!ok) break;
@@ -426,6 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         if (last_use && scores) rk.advance();
         if (last_use && product) {
           rv.advance();
+          ++vt;
           v16 ^= 1;
           v16_par ^= v16 == 0;
         }
@@ -502,6 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           break;
         }
         tc_fence_after();
+        bool late = false;  // the first half of P̃ goes with the second
         // A warp without live rows leaves its P̃ as it is: it only reaches its own rows of O, which nobody reads.
         if (busy) {
           float s[kBN];
@@ -554,8 +566,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           float corr = need ? ex2_approx(m_run - m_new) : 1.f;
           l_run *= corr;
           bool moved = need;
+          bool far = false;  // E4M3: the tile has gone over to bf16
           if constexpr (FP8) {
-            const int ref = sc->ref[tile % kTileRing];
+            const int code = sc->ref[tile % kTileRing];
+          const int ref = code >> 1;
+          far = code & 1;
             if (done > 0 && ref != kv_ref) {  // the widened values are relative to another exponent
               corr *= exp2f(static_cast<float>(max(kv_ref - ref, -200)));
               moved = true;
@@ -591,14 +606,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             }
             tmem_st32(s_addr + half * 32, pk);
             if constexpr (C::kTerms == 2) tmem_st32(s_addr + 64 + half * 32, lo);
-            // The first half goes early, unless value rows are still to be cleared.
-            if (C::kHalves == 2 && half == 0 && (FP8 || !tail)) {
+            // The first half goes early, unless value rows are still to be cleared (bf16) or P̃ split (E4M3).
+            if (C::kHalves == 2 && half == 0 && (FP8 ? !far : !tail)) {
               tmem_wait_st();
               tc_fence_before();
               mbar_arrive(&ms->p_half[g]);
             }
           }
           l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          if (FP8 && far) {  // the weights as two bf16 terms, from what this thread has just stored
+            tmem_wait_st();
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 8) {
+              uint32_t hi[8], lo[8];
+              tmem_ld(s_addr + c, hi);
+              tmem_wait_ld();
+              reg_fence(hi);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) split_f16x2(hi[e], hi[e], lo[e]);
+              tmem_st(s_addr + c, hi);
+              tmem_st(s_addr + 64 + c, lo);
+            }
+            if (C::kHalves == 2) late = true;
+          }
         }
         if (!FP8 && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
           // Key kt's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
@@ -629,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         __syncwarp();
         tmem_wait_st();
         tc_fence_before();
-        if (C::kHalves == 2 && (!busy || (!FP8 && tail))) mbar_arrive(&ms->p_half[g]);
+        if (C::kHalves == 2 && (!busy || (FP8 ? late : tail))) mbar_arrive(&ms->p_half[g]);
         mbar_arrive(&ms->p_full[g]);
       }
       tile0 += n_tiles;
@@ -766,6 +796,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     do {
       const int context = w.len - w.drafts;
       int exponent = 0;  // of this thread's value row, relative to the reference
+      bool far_next = false;
       // The scales of tile i of the pair, the n-th of the part: the softmax wants them before the widened values.
       // Slot n % 8 was read for tile n − 8, whose second product the wait for a place to widen into has told the end of.
       auto scales = [&](int i, int n) {
@@ -777,15 +808,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           used = any_token_sees(p.mask + w.b * p.mask_sb + (key - context), w.drafts, p.T);
         }
         const int kv = used ? static_cast<int>(sc->v_scale[n % kScaleRing][r]) - 127 : -1024;
+        // The largest and the smallest exponent (−126, next to nothing or zeros, does not count), as two halves of a word.
         const int top = __reduce_max_sync(0xffffffffu, kv);
-        if (lane == 0) sc->top[n & 1][warp - 12] = top;
+        const int low = __reduce_min_sync(0xffffffffu, kv > -126 ? kv : 2047);
+        if (lane == 0) sc->top[n & 1][warp - 12] = ((top + 2048) << 16) | (2048 - low);
         // (Byte 0 stands for 2^−127, below the normal numbers.)
         sc->ks[n % kTileRing][r] = kb == 0 ? 5.877471754111438e-39f : __uint_as_float(kb << 23);
         ok = !named_any(4, 128, !ok);  // joined by all converters; any failed wait ends them all
         const int4 tp = *reinterpret_cast<const int4*>(sc->top[n & 1]);
-        const int most = max(max(tp.x, tp.y), max(tp.z, tp.w));
+        const uint32_t both = __vmaxu2(__vmaxu2(tp.x, tp.y), __vmaxu2(tp.z, tp.w));
+        const int most = static_cast<int>(both >> 16) - 2048;
         if (i == w.t0 || most > ref + kKvLazy) ref = most;
-        if (r == 0) sc->ref[n % kTileRing] = ref;
+        far_next = 2048 - static_cast<int>(both & 0xffffu) < ref - kKvFar;
+        if (r == 0) sc->ref[n % kTileRing] = ref * 2 + (far_next ? 1 : 0);
         exponent = kv - ref;
         mbar_arrive(&ms->ks_full[n % kTileRing]);
       };
@@ -794,6 +829,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       for (int i = w.t0; ok && i < w.t1; ++i, ++tile) {
         // 2^exponent as fp16, at most 2^7; far below the reference it fades into fp16's subnormals and out.
         const int e = exponent;
+        const bool far = far_next;
         const uint32_t f1 = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
         const uint32_t f2 = f1 | (f1 << 16);
         const __half2 scale2 = *reinterpret_cast<const __half2*>(&f2);
@@ -820,7 +856,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         };
-        if ((i + 1) * kBN <= context) {
+        if (far) {
+          if (widen_row_far<D>(src, dst, r, e, key >= context, key >= w.len))
+            atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
+        } else if ((i + 1) * kBN <= context) {
 #pragma unroll 1
           for (int c4 = 0; c4 < D / 16; c4 += 4) {
             uint4 v[4];

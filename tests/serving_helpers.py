@@ -103,7 +103,10 @@ def check_tree(o, lse, q, paged, drafts, mask, scale, heads=None):
     product as two E4M3 terms, 2^-18 of the row's largest element), so each is
     off by at most 2^-16 of the largest Σ|q||k|·σ plus 2^-18·max|q|·Σ|k|·σ,
     which moves a probability by twice that, relatively; exponential, row sum and
-    division are fp32 (2^-18 together).
+    division are fp32 (2^-18 together).  fp16 probabilities (E4M3 cache) are kept
+    relative to a reference at most 2^-3 of the row's largest one, and below
+    2^-14 they are multiples of 2^-24: off by half of that, 2^-28 of the largest
+    one, and never by more than they are, since 0 is a multiple too.
     """
     o, lse, q = np64(o), np64(lse), np64(q)
     B, Hq, T, d = q.shape
@@ -125,6 +128,8 @@ def check_tree(o, lse, q, paged, drafts, mask, scale, heads=None):
                           + 2.0 ** -18 * np.abs(q[b, h]).max(1) * kf.sum(1).max())
             assert np.all(np.abs(lse[b, h][fin] - rl[fin]) <= (es + 2.0 ** -18 * (1 + np.abs(rl)))[fin]), (b, h)
             bound = 2.0 ** -8 * np.abs(ro) + (p_type + 2 * es[:, None] + 2.0 ** -18) * (p @ vf)
+            if paged.cache == "e4m3":
+                bound = bound + np.minimum(p, 2.0 ** -28 * p.max(1, keepdims=True)) @ vf
             ok = np.isfinite(ro) & fin[:, None]
             assert np.array_equal(np.isfinite(o[b, h])[fin], np.isfinite(ro)[fin]), (b, h)
             err = np.abs(o[b, h][ok] - ro[ok])

@@ -341,6 +341,36 @@ def test_a_drafted_key_that_nobody_sees_may_hold_the_largest_numbers(cache, T, v
     fa.device_status()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [2, 6, 12, 40, 70])
+@pytest.mark.parametrize("power", [12, 30, 90])
+def test_value_rows_that_are_large_where_they_hardly_count(T, power, d):
+    """E4M3: some value rows are larger than the others by 2^power, but rows either do not see them or give them next to
+    no weight.  The bounds are relative to Σ p|v|, so the small rows have to come through."""
+    import torch
+    rng = np.random.default_rng(T + power)
+    mask = random_tree(rng, 2, T)
+    mask[:, 1:, 0] = False                       # drafted token 0 is seen by itself only
+    n = [T + 300, T + 128]
+
+    def far(name, b, x):
+        if name == "v":
+            x[:, n[b] - T] *= 2.0 ** power       # its value row
+            x[:, [3, 90, 120]] *= 2.0 ** power  # and three of the context
+            x[:, 40:60] *= 2.0 ** -20
+            x[:, 61] = 0.0
+        else:
+            x[:, [3, 90, 120], 0] = -1000.0     # whose scores lie far below all others
+    p = Paged(rng, n, 2, d, 32, "e4m3", edit=far)
+    q = rng.standard_normal((2, 8, T, d))
+    q[..., 0] = 8.0
+    q = bf16(q).cuda()
+    for parts in (1, 3):
+        o, lse = fa.decode_tree(q, *p.args(), tree_mask=torch.from_numpy(mask).cuda(), max_parts=parts, **p.kw())
+        fa.device_status()
+        check_tree(o, lse, q, p, [T, T], mask, d ** -0.5)
+
+
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 @pytest.mark.parametrize("T", [2, 40])
 def test_output_in_place_of_the_queries(cache, T):
