@@ -169,26 +169,15 @@ __device__ __forceinline__ void reduce_cols(float (&v)[N], int lane, Op op, floa
   if ((lane & (32 / N - 1)) == 0) out[base] = v[0];
 }
 
-// Widens one value row of D E4M3 codes to fp16.  src: the row in its slot,
-// swizzled as TMA wrote it; dst: the row in the first 64-column block of the fp16
-// tile.  EDGE: the row may be a drafted one, whose NaN codes are taken out and
-// reported by the result, or lie past the end (dead).
-template <int D, bool EDGE>
-__device__ __forceinline__ bool widen_row(const uint8_t* src, uint8_t* dst, int r, bool drafted, bool dead) {
+// Widens one value row of D E4M3 codes to fp16 (all of context keys).  src: the row in its slot, swizzled as TMA wrote
+// it; dst: the row in the first 64-column block of the fp16 tile.
+template <int D>
+__device__ __forceinline__ void widen_row(const uint8_t* src, uint8_t* dst, int r) {
   const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
-  bool bad = false;
 #pragma unroll
   for (int ch = 0; ch < D / 16; ++ch) {
     const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if (EDGE && drafted) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (((w[e] >> (8 * q)) & 0x7f) == 0x7f) w[e] &= ~(0xffu << (8 * q)), bad = true;
-    }
-    if (EDGE && dead) w[0] = w[1] = w[2] = w[3] = 0;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = e4m3x2_to_f16x2(w[e >> 1] >> (16 * (e & 1)));
@@ -196,7 +185,6 @@ __device__ __forceinline__ bool widen_row(const uint8_t* src, uint8_t* dst, int 
     *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
   }
-  return bad;
 }
 
 // Multiplies N columns of this thread's lane by w[i]·k.
@@ -735,9 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
           if (kt == 0) ms->far[g] = far;
           if (!tail && !far) {
-            widen_row<D, false>(src, dst, kt, false, false);
+            widen_row<D>(src, dst, kt);
           } else if (far ? widen_row_far<D>(src, dst, kt, kv - kv_ref, key >= context, key >= w.len)
-                         : widen_row<D, true>(src, dst, kt, key >= context, key >= w.len) && key < w.len) {
+                         : widen_row_edge<D>(src, dst, kt, 0x3c003c00u, key >= context, key >= w.len)) {
             atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
           }
         }

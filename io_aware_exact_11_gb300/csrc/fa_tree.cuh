@@ -43,13 +43,50 @@ __device__ __forceinline__ bool token_sees(const TreeParams& p, int b, int t, in
   return p.mask != nullptr ? p.mask[b * p.mask_sb + static_cast<int64_t>(t) * p.T + u] != 0 : u <= t;
 }
 
-// Does any of the first `drafts` tokens see the drafted key whose column of the mask begins at mk?  (Out of line: few
-// tiles need it, and the kernels' loops are short of instruction cache.)
+// What few tiles need stands out of line: the kernels' loops are short of instruction cache (inlining the routine for
+// far value rows cost the kernel for many rows 6 % on tiles that have none).
+
+// Does any of the first `drafts` tokens see the drafted key whose column of the mask begins at mk?
 static __device__ __noinline__ bool any_token_sees(const uint8_t* mk, int drafts, int T) {
   bool sees = false;
 #pragma unroll 8
   for (int t = 0; t < drafts; ++t) sees |= mk[static_cast<int64_t>(t) * T] != 0;
   return sees;
+}
+
+// Widens one value row of D E4M3 codes to fp16, times the pair of scales.  src: the row in its slot, swizzled as TMA
+// wrote it; dst: the row in the first 64-column block of the fp16 tile.  drafted: NaN codes are taken out and reported by
+// the result; dead: zeros.
+template <int D>
+__device__ __noinline__ bool widen_row_edge(const uint8_t* src, uint8_t* dst, int r, uint32_t scale2, bool drafted,
+                                            bool dead) {
+  const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+  bool bad = false;
+#pragma unroll 1
+  for (int ch = 0; ch < D / 16; ++ch) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (drafted) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (((w[e] >> (8 * q)) & 0x7f) == 0x7f) w[e] &= ~(0xffu << (8 * q)), bad = true;
+      }
+      if (dead) w[e] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t h = e4m3x2_to_f16x2(w[i >> 1] >> (16 * (i & 1)));
+      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&scale2));
+      o[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    uint8_t* block = dst + (ch >> 2) * kTreeBN * 128;  // 64 elements per 128-byte row
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  return bad && !dead;
 }
 
 // Widens one value row of D E4M3 codes times 2^e to bf16, into a tile laid out as the fp16 one: for tiles whose value

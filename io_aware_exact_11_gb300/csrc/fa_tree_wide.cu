@@ -194,6 +194,41 @@ __device__ __forceinline__ void rescale_row(uint32_t addr, float k) {
   tmem_wait_st();
 }
 
+// Which keys of a tile token t sees: all before `context` (a place in the tile, maybe before it) and, up to `end`, the
+// drafted ones behind that its row of the mask names.
+static __device__ __noinline__ uint4 seen_keys(const uint8_t* row, int t, int context, int end) {
+  uint32_t seen[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int before = context - q * 32;  // context keys among these 32
+    seen[q] = before >= 32 ? 0xffffffffu : before > 0 ? (1u << before) - 1 : 0;
+  }
+#pragma unroll 8
+  for (int j = max(0, context); j < end; ++j) {
+    const uint32_t on = (row != nullptr ? row[j - context] != 0 : j - context <= t) ? 1u << (j & 31) : 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) seen[q] |= (j >> 5) == q ? on : 0u;
+  }
+  return make_uint4(seen[0], seen[1], seen[2], seen[3]);
+}
+
+// Turns a row's fp16 weights, as this thread has stored them, into two bf16 terms, the second 64 columns further.
+static __device__ __noinline__ void split_weights(uint32_t addr) {
+  tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 8) {
+    uint32_t hi[8], lo[8];
+    tmem_ld(addr + c, hi);
+    tmem_wait_ld();
+    reg_fence(hi);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split_f16x2(hi[e], hi[e], lo[e]);
+    tmem_st(addr + c, hi);
+    tmem_st(addr + 64 + c, lo);
+  }
+  tmem_wait_st();
+}
+
 template <int D, bool FP8, int TILES>
 __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, FP8, TILES>;
@@ -489,19 +524,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         const bool tail = k0 + kBN > context;  // the tile holds drafted keys or the end
         uint32_t seen[4];                      // which of its keys this row sees
         if (tail) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int before = context - k0 - q * 32;  // context keys among these 32
-            seen[q] = before >= 32 ? 0xffffffffu : before > 0 ? (1u << before) - 1 : 0;
-          }
-          if (live) {
-#pragma unroll 8
-            for (int j = max(0, context - k0); j < min(kBN, w.len - k0); ++j) {
-              const uint32_t on = token_sees(p, w.b, t, k0 + j - context) ? 1u << (j & 31) : 0u;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) seen[q] |= (j >> 5) == q ? on : 0u;
-            }
-          }
+          const uint8_t* row = p.mask != nullptr ? p.mask + w.b * p.mask_sb + static_cast<int64_t>(t) * p.T : nullptr;
+          const uint4 s4 = seen_keys(row, t, context - k0, live ? min(kBN, w.len - k0) : 0);
+          seen[0] = s4.x, seen[1] = s4.y, seen[2] = s4.z, seen[3] = s4.w;
         }
         if constexpr (FP8)  // the keys' powers of two
           ok = mbar_wait_inl(&ms->ks_full[tile % kTileRing], (tile / kTileRing) & 1, abort_flag, p.err, tree_site(0x26)) && ok;
@@ -614,20 +639,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             }
           }
           l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          if (FP8 && far) {  // the weights as two bf16 terms, from what this thread has just stored
-            tmem_wait_st();
-#pragma unroll 1
-            for (int c = 0; c < 64; c += 8) {
-              uint32_t hi[8], lo[8];
-              tmem_ld(s_addr + c, hi);
-              tmem_wait_ld();
-              reg_fence(hi);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) split_f16x2(hi[e], hi[e], lo[e]);
-              tmem_st(s_addr + c, hi);
-              tmem_st(s_addr + 64 + c, lo);
-            }
-            if (C::kHalves == 2) late = true;
+          if (FP8 && far) {
+            split_weights(s_addr);
+            late = true;
           }
         }
         if (!FP8 && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
@@ -873,23 +887,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           }
         } else {
           // The tile holds drafted keys, whose NaN codes are taken out and flagged, or the end: everything out behind it.
-          bool bad = false;
-#pragma unroll 1
-          for (int ch = 0; ch < D / 16; ++ch) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
-            uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-            if (key >= context) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                for (int b8 = 0; b8 < 4; ++b8)
-                  if (((w4[q] >> (8 * b8)) & 0x7f) == 0x7f) w4[q] &= ~(0xffu << (8 * b8)), bad = key < w.len;
-                if (key >= w.len) w4[q] = 0;
-              }
-            }
-            widen(ch, w4);
-          }
-          if (bad) atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
+          if (widen_row_edge<D>(src, dst, r, f2, key >= context, key >= w.len))
+            atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
         }
         fence_proxy_async_smem();
         mbar_arrive(&ms->v16_full[tile & 1]);
