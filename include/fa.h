@@ -387,9 +387,9 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   tree_mask[b·mask_stride_b + t·T + u] != 0 (device bytes; NULL: u <= t).  A
  *   row that sees no key, padding rows t >= m_b among them, gives O = 0 and
  *   LSE = −∞.  Keys a row does not see do not reach its results, whatever they
- *   hold; slots past a sequence's end are not read into results.  (With an E4M3
- *   cache the values of a sequence share one range: a key's share of O is off by
- *   up to 2^-27 of the largest |v| among the keys that some row sees.)
+ *   hold; slots past a sequence's end are not read into results.  Weights enter
+ *   the second product as bf16, or with an E4M3 cache as fp16: off by 2^-11, and
+ *   below 2^-17 of the row's largest weight by up to 2^-28 of that.
  *   q, o [B,H_q,T,d] bf16; strides NULL or 6 element strides {q_b, q_h, q_t, o_…},
  *   multiples of 8, >= 0 (o must not overlap itself, and may be q only with q's
  *   strides); lse [B,H_q,T] float32 or NULL.

@@ -45,7 +45,9 @@
 // row's power of two is folded into P̃ relative to a running maximum.  The reference is
 // taken 2^3 below the maximum and P̃ stays below 2^15, so fp16's subnormals begin
 // 2⁻¹⁷ below a row's largest weight and weights are off by at most 2⁻²⁸ of it.
-// In all a key's share of O is off by 2⁻²⁷ of the largest value that some row sees.
+// Where a tile's value rows lie further apart than 2^8, folding their powers of two
+// into P̃ would push it out of fp16's range: such a tile is widened to bf16 with its
+// powers of two, P̃ goes as two bf16 terms, and the product runs as bf16.
 //
 // Values in masked places.  Cache slots past the sequence end are zeroed in
 // shared memory before V is used.  A drafted key's value row is seen by some

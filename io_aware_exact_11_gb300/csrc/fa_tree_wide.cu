@@ -7,7 +7,7 @@
 // read from there by O += P̃ V.  Per 128 × 128 scores that reads 96 KB of shared
 // memory against 160 KB (and 32 KB of P̃ stored) in the transposed products of the
 // kernel for few rows, and a row's maximum needs no other thread: with tiles of 64
-// and 128 rows that one took 445 us where this one takes 239 (8 sequences of 32768
+// and 128 rows that one took 445 us where this one takes 249 (8 sequences of 32768
 // E4M3 keys, 8 key/value heads, 256 rows each).
 //
 // Two streams (warpgroups): with up to 128 rows they share them and take alternate
@@ -26,12 +26,13 @@
 // that off by at most 2⁻¹⁸ of it); four converter warps widen V to fp16, each row
 // times its power of two relative to a reference that P̃ and O share, and lay out
 // the keys' powers of two as floats.  P̃ is fp16, its reference 2^3 below the maximum.
+// A tile whose value rows lie further apart than 2^16 goes through bf16 (fa_tree.cu).
 //
 // The rest (parts, pieces, masks, values in masked places) is as in fa_tree.cu.
 //
 // Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements:
 //   64 / 128 / 256 rows, bf16   102 / 108 / 130 us   0.79 / 0.75 of a device copy, 1056 TFLOP/s
-//   64 / 128 / 256 rows, E4M3    84 /  88 / 141 us   411 / 778 / 973 TFLOP/s
+//   64 / 128 / 256 rows, E4M3    86 /  89 / 144 us   402 / 771 / 954 TFLOP/s
 // With two row tiles a step (one tile's P̃V and S, 1024 tensor cycles) takes about 1750 cycles: the issuing
 // warp's own instructions, of which it gets one through every dozen cycles beside the softmax warps, and the wait
 // for P̃ (S to P̃ is a chain of about 1400 cycles).  E4M3 with shared rows waits for the converters (2400 cycles a
