@@ -388,8 +388,9 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   row that sees no key, padding rows t >= m_b among them, gives O = 0 and
  *   LSE = −∞.  Keys a row does not see do not reach its results, whatever they
  *   hold; slots past a sequence's end are not read into results.  Weights enter
- *   the second product as bf16, or with an E4M3 cache as fp16: off by 2^-11, and
- *   below 2^-17 of the row's largest weight by up to 2^-28 of that.
+ *   the second product as bf16 (off by 2^-8 of themselves or less), or with an
+ *   E4M3 cache as fp16 (2^-11, and below 2^-17 of the row's largest weight up to
+ *   2^-28 of that).
  *   q, o [B,H_q,T,d] bf16; strides NULL or 6 element strides {q_b, q_h, q_t, o_…},
  *   multiples of 8, >= 0 (o must not overlap itself, and may be q only with q's
  *   strides); lse [B,H_q,T] float32 or NULL.
