@@ -47,41 +47,55 @@ __device__ __forceinline__ int page_of(const CacheParams& p, int b, int t) {
 // The larger one of each of two 16-bit halves.
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// Quantises 8 elements of a row; the lanes of the row (8 or 16 neighbours) hold
-// the rest of it.  Returns the codes; k is the row's exponent.  Magnitudes order
-// like their bits, so the row maximum is taken over packed pairs of 16 bits.
+// Quantises 8 elements of a key's row and 8 of its value's; the lanes of the rows (8 or 16 neighbours) hold the rest.
+// Magnitudes order like their bits, so a maximum is taken over 16-bit halves, and both rows' go through the lane
+// exchanges in one word.
 template <int D>
-__device__ __forceinline__ uint2 quantise8(uint4 raw, int& k) {
-  uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  auto row_max = [&](uint32_t top) -> uint32_t {
+__device__ __forceinline__ void quantise8(uint4 k, uint4 v, uint2& kc, uint2& vc, int& ke, int& ve) {
+  uint32_t w[2][4] = {{k.x, k.y, k.z, k.w}, {v.x, v.y, v.z, v.w}};
+  auto row_max = [](const uint32_t(&x)[2][4]) -> uint32_t {  // the key row's in the lower half
+    uint32_t t[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) t[j] = max2(max2(x[j][0], x[j][1]), max2(x[j][2], x[j][3]));
+    uint32_t top = __byte_perm(max2(t[0], t[0] >> 16), max2(t[1], t[1] << 16), 0x7610);
 #pragma unroll
     for (int m = D / 16; m > 0; m >>= 1) top = max2(top, __shfl_xor_sync(0xffffffffu, top, m));
-    return max(top >> 16, top & 0xffffu);
+    return top;
   };
-  uint32_t mag[4];
+  uint32_t mag[2][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) mag[i] = w[i] & 0x7fff7fffu;
-  uint32_t top = row_max(max2(max2(mag[0], mag[1]), max2(mag[2], mag[3])));
-  if (__any_sync(0xffffffffu, top >= 0x7f80u)) {
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mag[j][i] = w[j][i] & 0x7fff7fffu;
+  uint32_t top = row_max(mag);
+  if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u)) {
     // Infinities and NaN somewhere in the warp's rows: they do not count for the maximum and become NaN.
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] |= 0x7fffu, mag[i] &= 0xffff0000u;
-      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] |= 0x7fff0000u, mag[i] &= 0xffffu;
-    }
-    top = row_max(max2(max2(mag[0], mag[1]), max2(mag[2], mag[3])));
-  }
-  // top = 1.f·2^(e−127) with 7 bits of f; 448 = 1.75·2^8, so k = e − 127 − 8, one more when 1.f exceeds 1.75.
-  k = max(-126, static_cast<int>(top >> 7) - 135 + ((top & 0x7fu) > 0x60u ? 1 : 0));
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-  uint32_t c[4];
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    fmul2(lo, hi, __uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u), inv, inv);
-    c[i] = pack_e4m3x2(lo, hi);
+      for (int i = 0; i < 4; ++i) {
+        if ((w[j][i] & 0x7f80u) == 0x7f80u) w[j][i] |= 0x7fffu, mag[j][i] &= 0xffff0000u;
+        if ((w[j][i] & 0x7f800000u) == 0x7f800000u) w[j][i] |= 0x7fff0000u, mag[j][i] &= 0xffffu;
+      }
+    top = row_max(mag);
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  // A maximum is 1.f·2^(e−127) with 7 bits of f; 448 = 1.75·2^8, so k = e − 127 − 8, one more when 1.f exceeds 1.75.
+  auto exponent = [](uint32_t t) { return max(-126, static_cast<int>(t >> 7) - 135 + ((t & 0x7fu) > 0x60u ? 1 : 0)); };
+  ke = exponent(top & 0xffffu);
+  ve = exponent(top >> 16);
+  uint32_t c[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - (j == 0 ? ke : ve)) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      fmul2(lo, hi, __uint_as_float(w[j][i] << 16), __uint_as_float(w[j][i] & 0xffff0000u), inv, inv);
+      c[j][i] = pack_e4m3x2(lo, hi);
+    }
+  }
+  kc = make_uint2(c[0][0] | (c[0][1] << 16), c[0][2] | (c[0][3] << 16));
+  vc = make_uint2(c[1][0] | (c[1][1] << 16), c[1][2] | (c[1][3] << 16));
 }
 
 // Item (b, group of R tokens, h), h fastest: 8 or 16 lanes for the R rows.
@@ -157,7 +171,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   for (int r = 0; r < R; ++r) {
     if constexpr (FP8) {
       int ke, ve;
-      const uint2 kc = quantise8<D>(kr[r], ke), vc = quantise8<D>(vr[r], ve);
+      uint2 kc, vc;
+      quantise8<D>(kr[r], vr[r], kc, vc, ke, ve);
       if (row[r] >= 0) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.k_cache) + row[r] * D + it.lane8 * 8) = kc;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + row[r] * D + it.lane8 * 8) = vc;
