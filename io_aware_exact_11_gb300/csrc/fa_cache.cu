@@ -29,7 +29,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ void report(unsigned int* err, unsigned int what) {
   atomicCAS(err + 1, 0u, (kKernCache << 8) | what);
@@ -145,16 +145,23 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       vr[r] = *reinterpret_cast<const uint4*>(vp + r * p.sv[2]);
     }
   }
+  // The usual item's tokens lie in one page: its rows follow one another.
+  const int64_t t0 = start + it.n0;
+  const int64_t room = static_cast<int64_t>(p.max_blocks) * p.block_size;
+  const bool together = count == R && t0 >= 0 && t0 + R <= room && t0 >> shift == (t0 + R - 1) >> shift;
   int64_t row[R];
-  if (count > 0) {
-    const int64_t t0 = start + it.n0;
-    const int64_t room = static_cast<int64_t>(p.max_blocks) * p.block_size;
+#pragma unroll
+  for (int r = 0; r < R; ++r) row[r] = -1;
+  if (together) {
+    const int t = static_cast<int>(t0);
+    const int blk = page_of(p, it.b, t);
+    if (blk >= 0) row[0] = ((static_cast<int64_t>(blk) * p.Hkv + it.h) << shift) + (t & (p.block_size - 1));
+  } else if (count > 0) {
     if (t0 < 0 || t0 + count > room) report(p.err, kSiteBadLength);
     int page = -1, blk = -1;  // the page of the token before and where it lies
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int t = static_cast<int>(t0) + r;
-      row[r] = -1;
       if (r < count && t0 + r >= 0 && t0 + r < room) {
         if (t >> shift != page) {
           page = t >> shift;
@@ -163,28 +170,58 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         if (blk >= 0) row[r] = ((static_cast<int64_t>(blk) * p.Hkv + it.h) << shift) + (t & (p.block_size - 1));
       }
     }
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r) row[r] = -1;
   }
+  using Out = typename std::conditional<FP8, uint2, uint4>::type;  // 8 elements
+  Out kc[R], vc[R];
+  int ke[R], ve[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if constexpr (FP8) {
-      int ke, ve;
-      uint2 kc, vc;
-      quantise8<D>(kr[r], vr[r], kc, vc, ke, ve);
-      if (row[r] >= 0) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.k_cache) + row[r] * D + it.lane8 * 8) = kc;
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + row[r] * D + it.lane8 * 8) = vc;
-        if (it.lane8 == 0) {
-          p.k_scale[row[r]] = static_cast<uint8_t>(ke + 127);
-          p.v_scale[row[r]] = static_cast<uint8_t>(ve + 127);
-        }
-      }
-    } else if (row[r] >= 0) {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_cache) + row[r] * D + it.lane8 * 8) = kr[r];
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_cache) + row[r] * D + it.lane8 * 8) = vr[r];
+      quantise8<D>(kr[r], vr[r], kc[r], vc[r], ke[r], ve[r]);
+    } else {
+      kc[r] = kr[r];
+      vc[r] = vr[r];
     }
+  }
+  auto scales = [&](int64_t at, int r) {
+    if (FP8 && it.lane8 == 0) {
+      p.k_scale[at] = static_cast<uint8_t>(ke[r] + 127);
+      p.v_scale[at] = static_cast<uint8_t>(ve[r] + 127);
+    }
+  };
+  Out* const k_out = static_cast<Out*>(p.k_cache) + it.lane8;
+  Out* const v_out = static_cast<Out*>(p.v_cache) + it.lane8;
+  if (together) {
+    if (row[0] >= 0) {
+      Out* kd = k_out + row[0] * (D / 8);
+      Out* vd = v_out + row[0] * (D / 8);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        kd[r * (D / 8)] = kc[r];
+        vd[r * (D / 8)] = vc[r];
+      }
+      if (R == 4 && FP8 && (row[0] & 3) == 0) {  // four scale bytes at once
+        if (it.lane8 == 0) {
+          auto four = [](const int(&e)[R]) {
+            return static_cast<uint32_t>((e[0] + 127) | (e[1 % R] + 127) << 8 | (e[2 % R] + 127) << 16) |
+                   static_cast<uint32_t>(e[3 % R] + 127) << 24;
+          };
+          *reinterpret_cast<uint32_t*>(p.k_scale + row[0]) = four(ke);
+          *reinterpret_cast<uint32_t*>(p.v_scale + row[0]) = four(ve);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) scales(row[0] + r, r);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (row[r] >= 0) {
+        k_out[row[r] * (D / 8)] = kc[r];
+        v_out[row[r] * (D / 8)] = vc[r];
+        scales(row[r], r);
+      }
   }
 }
 
