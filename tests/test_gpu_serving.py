@@ -483,3 +483,45 @@ def test_largest_grids_of_small_work():
     ref, bound = _rope_bound(q, np.ones((B, 1)), w)
     assert np.all(np.abs(np64(y) - ref) <= bound)
     fa.device_status()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_calls_agree_with_small_ones(cache, d):
+    """Large calls give each thread several tokens; the same tokens in small calls, bit for bit, and the same report of a
+    page that is none."""
+    import torch
+    rng = np.random.default_rng(d)
+    hkv, bs, N = 8, 16, 1801
+    starts = [0, 5, 31, 14, 2, 1] * (1 if d == 128 else 2)
+    B = len(starts)
+    lens = [N, 1800, 0, 1, 1799, 777] * (B // 6)
+    per = (31 + N + bs - 1) // bs
+    table = _i32(rng.permutation(B * per).reshape(B, per).tolist())
+    table[0, 50] = -1
+    k, v = (torch.randn((B, hkv, N, d), device="cuda").bfloat16() for _ in "kv")
+    k *= torch.exp2(torch.randint(-9, 9, (B, hkv, N, 1), device="cuda").float()).bfloat16()
+    k[1, 0, 7, 3], v[1, 2, 100, 5], v[4, 3, 9] = float("nan"), float("inf"), -float("inf")
+    assert B * N * hkv * d // 8 >= 4 * 152 * 2048  # where a call counts as large
+    got = []
+    for step in (N, 150):
+        pools, sc = _pools(B * per, hkv, bs, d, cache)
+        for x in sc.values():
+            if x is not None:
+                x.zero_()
+        for n in range(0, N, step):
+            part = slice(n, min(n + step, N))
+            fa.cache_append(k[:, :, part], v[:, :, part], *pools, table, _i32([s + n for s in starts]),
+                            new_lens=_i32([min(max(m - n, 0), part.stop - n) for m in lens]), **sc)
+        with pytest.raises(fa.FAError, match="block-table"):
+            fa.device_status()
+        got.append([x.view(torch.uint8) for x in (*pools, *sc.values()) if x is not None])
+    assert _same(*got)
+    table[0, 50] = int(table[0, 49])
+    ends = [s + m for s, m in zip(starts, lens)]
+    n = max(ends)
+    many = fa.cache_gather(*pools, table, _i32(ends), n, **sc)
+    for b in range(B):
+        one = fa.cache_gather(*pools, table[b : b + 1], _i32(ends[b : b + 1]), n, **sc)
+        assert all(torch.equal(x[b : b + 1].view(torch.int16), y.view(torch.int16)) for x, y in zip(many, one))
+    fa.device_status()
