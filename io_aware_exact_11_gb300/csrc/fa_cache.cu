@@ -16,9 +16,8 @@
 //
 // Measured on GB300 (d = 128): gathering 4 sequences of 32768 E4M3 keys, 8 heads: 124 us,
 // 6.5 TB/s, 0.97 of a device copy; writing 8 ragged sequences of up to 8192 tokens as
-// E4M3, 4 heads: 35 us, 4.5 TB/s, 0.67 (it quantises on the way, and a block's rows end
-// in several short ones); a token for each of 64 sequences: the launch (11 us a call
-// from Python).
+// E4M3, 4 heads: 31 us, 5.1 TB/s, 0.77 (it quantises on the way); a token for each of 64
+// sequences: the launch (11 us a call from Python).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -303,7 +302,8 @@ cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
 
 // Four tokens per thread once one per thread would fill the machine several times over: the look-up of their slots
 // and the loads of their rows then overlap, where one per thread spends its life on that chain of loads.  (Four and
-// one, replaying a graph: gathering 4 x 32768 E4M3 keys 128 and 151 us, writing 8 x 8192 tokens 40 and 44 us.)
+// one, replaying a graph: gathering 4 x 32768 E4M3 keys 128 and 151 us, writing 8 x 8192 tokens 40 and 44 us.  Two:
+// writing 40 us where four took 38.)
 template <bool APPEND, int D, bool FP8>
 cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
   const int64_t threads = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 8);

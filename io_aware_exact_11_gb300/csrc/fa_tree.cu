@@ -57,7 +57,9 @@
 //
 // Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements:
 //   4 / 16 / 32 rows, bf16   93 / 93 / 95 us   5.75 TB/s, 0.86 of a device copy: bound by device memory
-//   4 / 16 / 32 rows, E4M3   60 / 60 / 72 us   4.5 / 4.5 / 3.8 TB/s: bound by the softmax warps, which widen V
+//   4 / 16 / 32 rows, E4M3   60 / 61 / 72 us   4.5 / 4.4 / 3.8 TB/s: inside a piece 4 and 16 rows run at the memory's
+//                            rate; start, piece ends and the joining kernel take 15 us, and with 32 rows the softmax
+//                            warps, which also widen V, are the bound
 // E4M3, not kept: four or eight converter warps beside the softmax warps (64 and 67 us at 4 rows, 82 and 83 at 32);
 // V widened by integer operations instead of the conversion instruction (slower, and it loses NaN); P̃ as two E4M3
 // terms over V as it is (the terms span too few binades).
@@ -474,12 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             // 64 rows of the result are not read).  B: 16 keys of P̃ᵀ.
             const uint64_t ad = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, D == 128 ? kBN * 128 : 0, 1024);
             const uint64_t bd = sdesc_sw128(sP + g * C::kPNext, kPBlock, 1024);
-#pragma unroll 1
-            for (int term = 0; term < (far ? 2 : 1); ++term)
+            const uint32_t idesc = far ? kIdescFar : kIdescO;
 #pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + kk * 128, idesc, (s >= 4 || kk > 0) ? 1u : 0u);
+            if (far) {  // the second terms
+#pragma unroll 1
               for (int kk = 0; kk < kBN / 16; ++kk)
-                mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + term * (NR / 8) + kk * 128, far ? kIdescFar : kIdescO,
-                            (s >= 4 || term > 0 || kk > 0) ? 1u : 0u);
+                mma_bf16_ss(dst, ad + kk * (kPg5 ? 256 : 128), bd + NR / 8 + kk * 128, idesc, 1u);
+            }
             mma_commit(&ms->p_free[g]);
             if constexpr (!FP8) mma_commit(&ms->v_empty[rv.slot]);
           }
