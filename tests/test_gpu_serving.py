@@ -525,3 +525,37 @@ def test_large_calls_agree_with_small_ones(cache, d):
         one = fa.cache_gather(*pools, table[b : b + 1], _i32(ends[b : b + 1]), n, **sc)
         assert all(torch.equal(x[b : b + 1].view(torch.int16), y.view(torch.int16)) for x, y in zip(many, one))
     fa.device_status()
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing needs a call before the capture: a fresh process captures every kernel's first launch."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from io_aware_exact_11_gb300 import fa
+torch.zeros(1, device="cuda")
+table = torch.arange(64, dtype=torch.int32, device="cuda").view(2, 32)
+lens = torch.full((2,), 300, dtype=torch.int32, device="cuda")
+w, _ = fa.rope_frequencies(128)
+q, k = (torch.ones((2, h, 40, 128), device="cuda", dtype=torch.bfloat16) for h in (8, 2))
+for dt, sc in ((torch.bfloat16, {}), (torch.float8_e4m3fn, {n: torch.full((64, 2, 16), 127, dtype=torch.uint8, device="cuda")
+                                                              for n in ("k_scale", "v_scale")})):
+    kc, vc = (torch.zeros((64, 2, 16, 128), device="cuda").to(dt) for _ in "kv")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q2, k2 = fa.rope(q, k, w)
+        fa.cache_append(k2, k, kc, vc, table, lens - 40, **sc)
+        few, _ = fa.decode_tree(q2[:, :, :2], kc, vc, table, lens, **sc)
+        many, _ = fa.decode_tree(q2, kc, vc, table, lens, **sc)
+        gk, gv = fa.cache_gather(kc, vc, table, lens, 300, **sc)
+    g.replay()
+    torch.cuda.synchronize()
+    fa.device_status()
+    assert (gv[:, :, 260:] == 1).all() and torch.isfinite(many).all() and many.any() and few.any()
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=280,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
