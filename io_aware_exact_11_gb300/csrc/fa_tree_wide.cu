@@ -7,7 +7,7 @@
 // read from there by O += P̃ V.  Per 128 × 128 scores that reads 96 KB of shared
 // memory against 160 KB (and 32 KB of P̃ stored) in the transposed products of the
 // kernel for few rows, and a row's maximum needs no other thread: with tiles of 64
-// and 128 rows that one took 445 us where this one takes 249 (8 sequences of 32768
+// and 128 rows that one took 445 us where this one takes 243 (8 sequences of 32768
 // E4M3 keys, 8 key/value heads, 256 rows each).
 //
 // Two streams (warpgroups): with up to 128 rows they share them and take alternate
@@ -15,9 +15,7 @@
 // of 128 rows over the same keys (TILES = 2), row tiles beyond that being other
 // CTAs that work on the same keys at the same time.  The MMA warp alternates: P̃₀V,
 // S₀ of the next tile, P̃₁V, S₁.  One commit after a tile's scores says both that they
-// are there and that O is stable.  With E4M3, P̃ is handed over in halves of 64 keys, so
-// that the first half's product runs under the other half's exponentials (141 us,
-// 144 without, 256 rows); bf16 measured 1 % slower with it.
+// are there and that O is stable.
 //
 // bf16 cache: with shared rows P̃ enters as two bf16 terms, as in the other kernel; with
 // two row tiles as one, as in the prefill forward: there the products and exponentials
@@ -32,7 +30,7 @@
 //
 // Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements:
 //   64 / 128 / 256 rows, bf16   102 / 108 / 130 us   0.79 / 0.75 of a device copy, 1056 TFLOP/s
-//   64 / 128 / 256 rows, E4M3    86 /  89 / 144 us   402 / 771 / 954 TFLOP/s
+//   64 / 128 / 256 rows, E4M3    85 /  89 / 143 us   406 / 774 / 961 TFLOP/s
 // With two row tiles a step (one tile's P̃V and S, 1024 tensor cycles) takes about 1750 cycles: the issuing
 // warp's own instructions, of which it gets one through every dozen cycles beside the softmax warps, and the wait
 // for P̃ (S to P̃ is a chain of about 1400 cycles).  E4M3 with shared rows waits for the converters (2400 cycles a
@@ -76,7 +74,6 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kRK * kSlot;
   static constexpr int kOffMisc = kOffV + kRV * kSlot;
   static constexpr int kSmem = kOffMisc + kMisc + 1024;
-  static constexpr int kHalves = FP8 ? 2 : 1;
   static constexpr uint32_t kColO = 256;                 // TMEM: S of the streams at 0 and 128, O at 256 and 256 + D
   static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && kRV + 4 <= kScaleRing && kSmem <= 227 * 1024, "rings");
   static_assert(kSlot % 1024 == 0 && kQTile % 1024 == 0, "swizzle atoms");
@@ -84,7 +81,7 @@ struct Cfg {
 
 struct Bars {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t s_full[2], p_half[2], p_full[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing];
+  uint64_t s_full[2], p_full[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing];
   uint64_t q_full, drain;
   uint32_t bad[8][8];       // drafted keys with non-finite values, of up to eight pieces
   long long warp_sum[16];
@@ -269,7 +266,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
       mbar_init(&ms->p_full[s], 128);
-      mbar_init(&ms->p_half[s], 128);
       mbar_init(&ms->v16_full[s], 128);
       mbar_init(&ms->v16_empty[s], 1);
     }
@@ -413,37 +409,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         const uint64_t qd = FP8 && D == 64 ? sdesc_sw64(qb, 16, 512) : sdesc_sw128(qb, 16, 1024);
         const uint64_t kd = FP8 && D == 64 ? sdesc_sw64(kb, 16, 512) : sdesc_sw128(kb, 16, kPg5 ? 2048 : 1024);
         if (product)
-          ok = ok && mbar_wait_inl(C::kHalves == 2 ? &ms->p_half[g] : &ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err,
-                                   tree_site(0x28));
+          ok = ok && mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(0x23));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         if (product) {  // P̃V of step s − 2, of the same stream
-          constexpr int kSteps = kBN / 16 / C::kHalves;
-          // The first 64 keys, then the others, which the softmax warps have written meanwhile.
+          if (leader) {
 #pragma unroll
-          for (int half = 0; half < C::kHalves; ++half) {
-            if (half == 1) {
-              ok = mbar_wait_inl(&ms->p_full[g], (p_par >> g) & 1u, abort_flag, p.err, tree_site(0x23));
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            if (leader) {
+            for (int term = 0; term < C::kTerms; ++term)
 #pragma unroll
-              for (int term = 0; term < C::kTerms; ++term)
-#pragma unroll
-                for (int kk = half * kSteps; kk < (half + 1) * kSteps; ++kk)  // A: P̃ over S, 16 keys in 8 columns
-                  mma_bf16_ts(to, ts + term * 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc,
-                              (s >= 4 || half + term > 0 || kk > 0) ? 1u : 0u);
-              if (FP8 && far) {  // the second terms
+              for (int kk = 0; kk < kBN / 16; ++kk)  // A: P̃ over S, 16 keys in 8 columns
+                mma_bf16_ts(to, ts + term * 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc,
+                            (s >= 4 || term > 0 || kk > 0) ? 1u : 0u);
+            if (FP8 && far) {  // the second terms
 #pragma unroll 1
-                for (int kk = half * kSteps; kk < (half + 1) * kSteps; ++kk)
-                  mma_bf16_ts(to, ts + 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc, 1u);
-              }
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_bf16_ts(to, ts + 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc, 1u);
             }
           }
-          if (!ok) break;
           p_par ^= 1u << g;
           // With shared rows the value slot is given back at once (after the scores' issue: 1 us of 104 slower); with two
           // row tiles the scores' issue comes first (the other way round 135 instead of 130 us: 256 rows, 8 x 16384 keys).
@@ -539,7 +522,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           break;
         }
         tc_fence_after();
-        bool late = false;  // the first half of P̃ goes with the second
         // A warp without live rows leaves its P̃ as it is: it only reaches its own rows of O, which nobody reads.
         if (busy) {
           float s[kBN];
@@ -632,18 +614,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             }
             tmem_st32(s_addr + half * 32, pk);
             if constexpr (C::kTerms == 2) tmem_st32(s_addr + 64 + half * 32, lo);
-            // The first half goes early, unless value rows are still to be cleared (bf16) or P̃ split (E4M3).
-            if (C::kHalves == 2 && half == 0 && (FP8 ? !far : !tail)) {
-              tmem_wait_st();
-              tc_fence_before();
-              mbar_arrive(&ms->p_half[g]);
-            }
           }
           l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          if (FP8 && far) {
-            split_weights(s_addr);
-            late = true;
-          }
+          if (FP8 && far) split_weights(s_addr);
         }
         if (!FP8 && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
           // Key kt's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
@@ -674,7 +647,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         __syncwarp();
         tmem_wait_st();
         tc_fence_before();
-        if (C::kHalves == 2 && (!busy || (FP8 ? late : tail))) mbar_arrive(&ms->p_half[g]);
         mbar_arrive(&ms->p_full[g]);
       }
       tile0 += n_tiles;
@@ -804,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------ converters: one value row and one key's scale per thread
     const int r = tid - 384;
-    int tile = 0, ref = 0;
+    int next = 0, ref = 0;  // the tile of the part whose scales come next
     bool ok = true;
     TreeWalk w;
     w.begin(p, my);
@@ -839,9 +811,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         exponent = kv - ref;
         mbar_arrive(&ms->ks_full[n % kTileRing]);
       };
-      scales(w.t0, tile);
 #pragma unroll 1
-      for (int i = w.t0; ok && i < w.t1; ++i, ++tile) {
+      for (int i = w.t0 - 1; ok && i < w.t1; ++i) {
         // 2^exponent as fp16, at most 2^7; far below the reference it fades into fp16's subnormals and out.
         const int e = exponent;
         const bool far = far_next;
@@ -849,9 +820,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         const uint32_t f2 = f1 | (f1 << 16);
         const __half2 scale2 = *reinterpret_cast<const __half2*>(&f2);
         if (i + 1 < w.t1) {
-          scales(i + 1, tile + 1);
+          scales(i + 1, next++);
           if (!ok) break;
         }
+        if (i < w.t0) continue;  // (the first tile's scales come before its values)
+        const int tile = next - (i + 1 < w.t1 ? 2 : 1);
         const int slot = tile % C::kRV;
         ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(0x2d)) &&
              mbar_wait_inl(&ms->v16_empty[tile & 1], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x2c));
