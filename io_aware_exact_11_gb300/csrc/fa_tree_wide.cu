@@ -849,12 +849,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
         } else if ((i + 1) * kBN <= context) {
 #pragma unroll 1
-          for (int c4 = 0; c4 < D / 16; c4 += 4) {
-            uint4 v[4];
+          for (int c4 = 0; c4 < D / 16; c4 += 2) {
+            uint4 v[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (((c4 + q) ^ sw) << 4));
+            for (int q = 0; q < 2; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (((c4 + q) ^ sw) << 4));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               const uint32_t w4[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
               widen(c4 + q, w4);
             }
