@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         }
       }
     } while (ok && w.next(p));
-    if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA ends
+    // The copies in flight land before the CTA ends, also where a wait of another warp fails after this one is done.
+    if (lane == 0) {
 #pragma unroll 1
       for (int n = max(0, issued - ring); n < issued; ++n) {
         mbar_wait_drain_inl(&full[n % ring], (n / ring) & 1, kTreeDrainNs);
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         }
       }
     } while (ok && __shfl_sync(0xffffffffu, w.next(p), 0));
-    if (*abort_flag && leader) {
+    if (leader) {  // the same for the products, which the end frees the tensor memory of
       mma_commit(&ms->drain);
       mbar_wait_drain_inl(&ms->drain, 0, kTreeDrainNs);
     }
