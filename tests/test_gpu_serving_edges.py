@@ -29,7 +29,7 @@ def _i32(a):
 TOKENS = [1, 3, 8, 20, 64]
 
 
-@pytest.mark.parametrize("cache,T", [("bf16", 2), ("bf16", 20), ("bf16", 64), ("e4m3", 2)])
+@pytest.mark.parametrize("cache,T", [("bf16", 2), ("bf16", 20), ("bf16", 64), ("e4m3", 2), ("e4m3", 20), ("e4m3", 64)])
 def test_calls_behind_an_unread_timeout_end(cache, T):
     """A timeout that nobody has read makes the waits of later calls give up early, each for itself.  Such calls end, and
     the ones after the report are right.  (4 query heads a key/value head: 8, 80 and 256 rows.)"""
