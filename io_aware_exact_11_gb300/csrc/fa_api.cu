@@ -1218,6 +1218,8 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   memset(&p, 0, sizeof(p));
   if ((r = check_rows(who, strides, p.sq, p.so, H_q, T, d)) != FA_OK) return r;
   if (!rows_distinct(B, H_q, T, d, p.so)) return fail(FA_ERR_INVALID_ARG, "%s: o overlaps itself", who);
+  if (q == o && ((B > 1 && p.sq[0] != p.so[0]) || (H_q > 1 && p.sq[1] != p.so[1]) || (T > 1 && p.sq[2] != p.so[2])))
+    return fail(FA_ERR_INVALID_ARG, "%s: in place needs equal strides", who);
   if ((static_cast<int64_t>(max_blocks) * block_size + 127) / 128 * H_kv > INT32_MAX)
     return fail(FA_ERR_UNSUPPORTED, "%s: max_blocks * block_size * H_kv too large", who);
   // A smaller workspace is taken with fewer parts; one part needs no room for pieces.

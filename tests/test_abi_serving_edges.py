@@ -1,0 +1,41 @@
+"""Calls of the operators around attention that are refused at the edges of their ranges (no GPU)."""
+
+import ctypes
+import os
+
+import pytest
+
+from io_aware_exact_11_gb300 import fa
+
+FAKE = 1 << 20  # never dereferenced: validation fails first
+INV, UNS = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(fa.LIB_PATH):
+        from io_aware_exact_11_gb300 import build
+        build.build()
+    return fa.lib()
+
+
+def _st(*x):
+    return (ctypes.c_int64 * len(x))(*x)
+
+
+def _tree(L, **kw):
+    a = dict(q=FAKE, o=FAKE, B=2, Hq=4, Hkv=2, T=4, mb=16, d=64, st=None)
+    a.update(kw)
+    return L.fa_decode_tree(a["q"], FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, 0, a["o"], None, a["B"], a["Hq"], a["Hkv"],
+                            a["T"], 100, 16, a["mb"], a["d"], fa.FA_BF16, 0.1, a["st"], 4, FAKE, 1 << 30, None)
+
+
+@pytest.mark.parametrize("st", [(1024, 64, 256, 1024, 256, 64), (2048, 256, 64, 1024, 256, 64), (1024, 256, 64, 1024, 64, 256)])
+def test_decode_tree_in_place_needs_the_queries_strides(L, st):
+    """Rows would be written over queries that other blocks still read."""
+    assert _tree(L, st=_st(*st)) == INV
+    assert b"in place" in L.fa_get_last_error()
+    _tree(L, o=FAKE + (1 << 16), st=_st(*st))                          # elsewhere these strides are fine
+    assert b"in place" not in L.fa_get_last_error()
+    _tree(L, T=1, st=_st(1024, 256, 64, 1024, 256, 128))               # and so is a stride that takes no step
+    assert b"in place" not in L.fa_get_last_error()

@@ -47,3 +47,13 @@ def test_calls_behind_an_unread_timeout_end(cache, T):
     got, lse2 = fa.decode_tree(q, *p.args(), **p.kw())
     assert torch.equal(got, want) and torch.equal(lse, lse2)
     fa.device_status()
+
+
+def test_output_over_the_queries_needs_their_strides():
+    import torch
+    p = Paged(np.random.default_rng(7), [40, 50], 2, 64, 16, "bf16")
+    q = torch.zeros((2, 4, 4, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(fa.FAError, match="in place"):
+        fa.decode_tree(q, *p.args(), out=q.transpose(1, 2))
+    with pytest.raises(fa.FAError, match="in place"):
+        fa.decode_tree(q.transpose(1, 2), *p.args(), out=q)
