@@ -387,7 +387,9 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   tree_mask[b·mask_stride_b + t·T + u] != 0 (device bytes; NULL: u <= t).  A
  *   row that sees no key, padding rows t >= m_b among them, gives O = 0 and
  *   LSE = −∞.  Keys a row does not see do not reach its results, whatever they
- *   hold; slots past a sequence's end are not read into results.  Weights enter
+ *   hold; slots past a sequence's end are not read into results.  An infinite
+ *   value of a bf16 cache is infinite in the results of the rows that see it (NaN
+ *   under a weight below 2^-126 of the row's largest).  Weights enter
  *   the second product as bf16 (off by 2^-8 of themselves or less), or with an
  *   E4M3 cache as fp16 (2^-11, and below 2^-17 of the row's largest weight up to
  *   2^-28 of that).

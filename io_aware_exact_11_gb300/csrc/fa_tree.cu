@@ -35,8 +35,9 @@
 // and a second kernel joins them.
 //
 // bf16 cache: P̃ enters as two bf16 terms p ≈ hi + lo in separate columns (good to
-// 2⁻¹⁷; one term alone adds an error as large as O's own rounding to bf16), which
-// costs nothing here, where device memory bounds it.
+// 2⁻¹⁵; one term alone adds an error as large as O's own rounding to bf16), which
+// costs nothing here, where device memory bounds it.  Both terms are positive, so
+// that an infinite value stays one.
 // E4M3 cache: K is multiplied as it is; q enters as two E4M3 terms
 // q·2⁻ᵃ = hi + lo/16 in separate columns (exact for elements down to 2⁻¹⁴ of the
 // row's largest, below that off by 2⁻²² of it), and the key's power of two
@@ -700,8 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               fmul2(a, d, x[n], x[n + 1], wv, wv);
               hi[e] = pack_f16x2(a, d);
             } else {
-              hi[e] = pack_bf16x2(x[n], x[n + 1]);
-              lo[e] = pack_bf16x2(x[n] - __uint_as_float(hi[e] << 16), x[n + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+              split_weights2(x[n], x[n + 1], hi[e], lo[e]);
             }
           }
           *reinterpret_cast<uint4*>(prow + (((first + ch) ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);

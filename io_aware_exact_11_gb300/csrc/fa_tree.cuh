@@ -121,6 +121,16 @@ __device__ __noinline__ bool widen_row_far(const uint8_t* src, uint8_t* dst, int
   return bad && !dead;
 }
 
+// A pair of weights p as bf16 terms hi + lo, both positive where p is: an infinite value comes out of two products as
+// itself, where a term of the other sign, or zero, would make it NaN.  hi is p·(1 − 2⁻⁸) rounded down (its upper half),
+// so lo is between 2⁻⁸ and 2^-6.4 of p and its rounding at most 2⁻⁹ of that: the sum is off by 2⁻¹⁵ p.
+__device__ __forceinline__ void split_weights2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  fmul2(a, b, p0, p1, 0.99609375f, 0.99609375f);
+  hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  lo = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+}
+
 // A pair of fp16 weights as bf16 terms hi + lo (exact: 11 bits in 8 and 8).
 __device__ __forceinline__ void split_f16x2(uint32_t pair, uint32_t& hi, uint32_t& lo) {
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pair));

@@ -590,31 +590,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           if (done > 0 && __any_sync(0xffffffffu, moved)) rescale_row<D>(o_addr, corr);
           const float neg = m_new == -INFINITY ? 0.f : -m_new;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          // Keys whose weights are stored at once (two terms: 16, where 64 spilled registers and took 4 % more).
+          constexpr int kPer = C::kTerms == 2 ? 16 : 64;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t pk[32], lo[C::kTerms == 2 ? 32 : 1];
+          for (int k = 0; k < kBN; k += kPer) {
+            uint32_t pk[kPer / 2], lo[C::kTerms == 2 ? kPer / 2 : 1];
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-              float* x = s + half * 64 + e;
+            for (int e = 0; e < kPer; e += 4) {
+              float* x = s + k + e;
               ffma2(x[0], x[1], x[0], x[1], factor, factor, neg, neg);
               ffma2(x[2], x[3], x[2], x[3], factor, factor, neg, neg);
 #pragma unroll
               for (int q = 0; q < 4; ++q) x[q] = ex2_approx(x[q]);
               fadd2(sum[0], sum[1], sum[0], sum[1], x[0], x[1]);
               fadd2(sum[2], sum[3], sum[2], sum[3], x[2], x[3]);
-              pk[e / 2] = FP8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
-              pk[e / 2 + 1] = FP8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
               if constexpr (C::kTerms == 2) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const uint32_t h2 = pk[e / 2 + q];
-                  lo[e / 2 + q] = pack_bf16x2(x[2 * q] - __uint_as_float(h2 << 16),
-                                              x[2 * q + 1] - __uint_as_float(h2 & 0xffff0000u));
-                }
+                split_weights2(x[0], x[1], pk[e / 2], lo[e / 2]);
+                split_weights2(x[2], x[3], pk[e / 2 + 1], lo[e / 2 + 1]);
+              } else {
+                pk[e / 2] = FP8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+                pk[e / 2 + 1] = FP8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
               }
             }
-            tmem_st32(s_addr + half * 32, pk);
-            if constexpr (C::kTerms == 2) tmem_st32(s_addr + 64 + half * 32, lo);
+            tmem_st(s_addr + k / 2, pk);
+            if constexpr (C::kTerms == 2) tmem_st(s_addr + 64 + k / 2, lo);
           }
           l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           if (FP8 && far) split_weights(s_addr);

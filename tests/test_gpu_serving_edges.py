@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from io_aware_exact_11_gb300 import fa
-from tests.serving_helpers import Paged, bf16
+from tests.serving_helpers import Paged, bf16, check_tree, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,35 @@ def test_output_over_the_queries_needs_their_strides():
         fa.decode_tree(q, *p.args(), out=q.transpose(1, 2))
     with pytest.raises(fa.FAError, match="in place"):
         fa.decode_tree(q.transpose(1, 2), *p.args(), out=q)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", TOKENS)
+def test_an_infinite_value_in_the_context_is_infinite_in_every_row(T, d):
+    """Every weight is positive, so a column with one infinity is that infinity, and one with both is NaN."""
+    def edit(name, b, x):
+        if name == "v":
+            x[:, 70, 9], x[:, 200, 11], x[:, x.shape[1] - T - 1, 13] = np.inf, -np.inf, np.inf
+            x[:, 70, 20], x[:, 71, 20] = np.inf, -np.inf
+    p = Paged(np.random.default_rng(T), [300, 230 + T], 2, d, 32, "bf16", edit=edit)
+    q = bf16(np.random.default_rng(1).standard_normal((2, 8, T, d))).cuda()
+    for parts in (1, 3):
+        o, lse = fa.decode_tree(q, *p.args(), max_parts=parts)
+        with np.errstate(invalid="ignore"):  # inf - inf, as wanted
+            check_tree(o, lse, q, p, [T, T], None, d ** -0.5)
+        o = np64(o)
+        assert np.isposinf(o[..., [9, 13]]).all() and np.isneginf(o[..., 11]).all() and np.isnan(o[..., 20]).all()
+        assert np.isfinite(np.delete(o, [9, 11, 13, 20], 3)).all()
+
+
+@pytest.mark.parametrize("T", TOKENS)
+def test_an_infinite_value_under_a_weight_of_one(T):
+    import torch
+    def edit(name, b, x):
+        if name == "v":
+            x[:, 0, 9] = -np.inf
+    p = Paged(np.random.default_rng(T), [1 + T], 2, 128, 16, "bf16", edit=edit)
+    q = bf16(np.random.default_rng(2).standard_normal((1, 8, T, 128))).cuda()
+    o, _ = fa.decode_tree(q, *p.args(), tree_mask=torch.zeros((T, T), dtype=torch.bool, device="cuda"))
+    want = np.repeat(p.v[0][:, :1], 4, 0)  # one key: its weight is 1
+    assert np.array_equal(np64(o)[0], np.repeat(want, T, 1))
