@@ -41,13 +41,14 @@
 // E4M3 cache: K is multiplied as it is; q enters as two E4M3 terms
 // q·2⁻ᵃ = hi + lo/16 in separate columns (exact for elements down to 2⁻¹⁴ of the
 // row's largest, below that off by 2⁻²² of it), and the key's power of two
-// multiplies the score in fp32.  V is widened to fp16 (exact) by the softmax
-// warps before they take up the tile's scores, so P̃ is fp16 (2⁻¹¹); the value
-// row's power of two is folded into P̃ relative to a running maximum.  The reference is
-// taken 2^3 below the maximum and P̃ stays below 2^15, so fp16's subnormals begin
+// multiplies the score in fp32.  V is widened to fp16 by the softmax warps, times the
+// row's power of two relative to a running reference; from 2⁻¹⁵ to 2^7 that is exact
+// (E4M3's smallest step, 2⁻⁹, becomes fp16's, 2⁻²⁴).  So P̃ is fp16 (2⁻¹¹): its reference is
+// taken 2^3 below the maximum and P̃ stays below 2^11, fp16's subnormals begin
 // 2⁻¹⁷ below a row's largest weight and weights are off by at most 2⁻²⁸ of it.
-// Where a tile's value rows lie further apart than 2^8, folding their powers of two
-// into P̃ would push it out of fp16's range: such a tile is widened to bf16 with its
+// (Folded into P̃ instead, the powers of two of small value rows cost their weights as
+// many bits: rows made of such weights came out wrong by several times that.)
+// A tile with value rows further below the reference than 2^15 is widened to bf16 with its
 // powers of two, P̃ goes as two bf16 terms, and the product runs as bf16.
 //
 // Values in masked places.  Cache slots past the sequence end are zeroed in
@@ -174,10 +175,10 @@ __device__ __forceinline__ void reduce_cols(float (&v)[N], int lane, Op op, floa
   if ((lane & (32 / N - 1)) == 0) out[base] = v[0];
 }
 
-// Widens one value row of D E4M3 codes to fp16 (all of context keys).  src: the row in its slot, swizzled as TMA wrote
-// it; dst: the row in the first 64-column block of the fp16 tile.
+// Widens one value row of D E4M3 codes to fp16, times the pair of scales (all of context keys).  src: the row in its slot,
+// swizzled as TMA wrote it; dst: the row in the first 64-column block of the fp16 tile.
 template <int D>
-__device__ __forceinline__ void widen_row(const uint8_t* src, uint8_t* dst, int r) {
+__device__ __forceinline__ void widen_row(const uint8_t* src, uint8_t* dst, int r, uint32_t scale2) {
   const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
 #pragma unroll
   for (int ch = 0; ch < D / 16; ++ch) {
@@ -185,7 +186,11 @@ __device__ __forceinline__ void widen_row(const uint8_t* src, uint8_t* dst, int 
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = e4m3x2_to_f16x2(w[e >> 1] >> (16 * (e & 1)));
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = e4m3x2_to_f16x2(w[e >> 1] >> (16 * (e & 1)));
+      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&scale2));
+      o[e] = *reinterpret_cast<const uint32_t*>(&x);
+    }
     uint8_t* block = dst + (ch >> 2) * kBN * 128;  // 64 elements per 128-byte row
     *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(block + ((((ch & 3) * 2 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -285,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   // Rescale once a score exceeds the reference by kLazy; the reference is taken kBase below the maximum.
   constexpr float kLazy = FP8 ? 11.f : 8.f;
   constexpr float kBase = FP8 ? 3.f : 0.f;
-  constexpr int kKvLazy = 4;  // fp16 P̃ stays below 2^(11 + 4)
-  constexpr int kKvFar = 8;   // value rows that are smaller by more than this need bf16's range
+  constexpr int kKvLazy = 7;  // widened values stay below 448·2^7
+  constexpr int kKvFar = 15;  // value rows that are smaller by more than this need bf16's range
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
@@ -682,8 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
         // P̃'s buffer, and E4M3's widened values', are free once the product of the stream's tile before has run.
         if (u > 0) ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
-        // E4M3: the value row's scale relative to the running maximum, a power of two, at most 2^kKvLazy.
-        const float wv = !FP8 || far ? 1.f : kv - kv_ref < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(kv - kv_ref + 127) << 23);
         // 16-byte chunks of the key's row, XORed with the key; the stream's begin at `first`.
         uint8_t* prow = smem + C::kOffP + (C::kPNext == kPBlock ? g * kPBlock : 0) + kt * 128;
         const int first = C::kPNext == kPBlock ? 0 : g * (C::kPNext / 16);
@@ -697,9 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             x[n + 1] = ex2_approx(x[n + 1]);
             fadd2(l[n], l[n + 1], l[n], l[n + 1], x[n], x[n + 1]);
             if constexpr (FP8) {
-              float a, d;
-              fmul2(a, d, x[n], x[n + 1], wv, wv);
-              hi[e] = pack_f16x2(a, d);
+              hi[e] = pack_f16x2(x[n], x[n + 1]);
             } else {
               split_weights2(x[n], x[n + 1], hi[e], lo[e]);
             }
@@ -730,10 +731,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const uint8_t* src = smem + C::kOffV + slot * kSlot + kt * D;
           uint8_t* dst = smem + C::kOffV16 + g * C::kV16 + kt * 128;
           if (kt == 0) ms->far[g] = far;
+          const int e = kv - kv_ref;  // the row's power of two, at most 2^kKvLazy
           if (!tail && !far) {
-            widen_row<D>(src, dst, kt);
-          } else if (far ? widen_row_far<D>(src, dst, kt, kv - kv_ref, key >= context, key >= w.len)
-                         : widen_row_edge<D>(src, dst, kt, 0x3c003c00u, key >= context, key >= w.len)) {
+            widen_row<D>(src, dst, kt, power_f16x2(e));
+          } else if (far ? widen_row_far<D>(src, dst, kt, e, key >= context, key >= w.len)
+                         : widen_row_edge<D>(src, dst, kt, power_f16x2(e), key >= context, key >= w.len)) {
             atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
           }
         }

@@ -54,6 +54,12 @@ static __device__ __noinline__ bool any_token_sees(const uint8_t* mk, int drafts
   return sees;
 }
 
+// 2^e twice as fp16 (e <= 15); far below 1 it fades into fp16's subnormals and out.
+__device__ __forceinline__ uint32_t power_f16x2(int e) {
+  const uint32_t f = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+  return f | (f << 16);
+}
+
 // Widens one value row of D E4M3 codes to fp16, times the pair of scales.  src: the row in its slot, swizzled as TMA
 // wrote it; dst: the row in the first 64-column block of the fp16 tile.  drafted: NaN codes are taken out and reported by
 // the result; dead: zeros.

@@ -813,11 +813,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       };
 #pragma unroll 1
       for (int i = w.t0 - 1; i < w.t1; ++i) {
-        // 2^exponent as fp16, at most 2^7; far below the reference it fades into fp16's subnormals and out.
-        const int e = exponent;
+        const int e = exponent;  // at most kKvLazy
         const bool far = far_next;
-        const uint32_t f1 = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
-        const uint32_t f2 = f1 | (f1 << 16);
+        const uint32_t f2 = power_f16x2(e);
         const __half2 scale2 = *reinterpret_cast<const __half2*>(&f2);
         if (i + 1 < w.t1) {
           scales(i + 1, next++);

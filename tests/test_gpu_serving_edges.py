@@ -89,3 +89,30 @@ def test_an_infinite_value_under_a_weight_of_one(T):
     o, _ = fa.decode_tree(q, *p.args(), tree_mask=torch.zeros((T, T), dtype=torch.bool, device="cuda"))
     want = np.repeat(p.v[0][:, :1], 4, 0)  # one key: its weight is 1
     assert np.array_equal(np64(o)[0], np.repeat(want, T, 1))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [2, 6, 12, 40])
+@pytest.mark.parametrize("power", [1, 4, 6, 8, 9])
+def test_small_weights_beside_one_that_counts_for_nothing(T, power, d):
+    """E4M3: one key has nearly all of a row's weight and a value of zero, so the row's result is made of weights 2^-16 to
+    2^-22 of the largest, and a few value rows without weight are larger by 2^power.  Column 5 holds E4M3's smallest."""
+    for k0 in (8.0, 10.0, 11.0):
+        def edit(name, b, x):
+            if name == "k":
+                np.clip(x, -0.9, 0.9, out=x)
+                x[:, :, 0] = 0.0
+                x[:, 7, 0] = k0
+                x[:, 30::97, 0] = -448.0
+            else:
+                x[:] = 1.0 + 0.75 * np.abs(np.sin(np.arange(x.size))).reshape(x.shape)
+                x[..., 5] = 3 * 2.0 ** -17
+                x[:, 30::97] *= 2.0 ** power
+                x[:, 7] = 0.0
+        p = Paged(np.random.default_rng(T), [700, 400], 2, d, 32, "e4m3", edit=edit)
+        q = np.zeros((2, 8, T, d))
+        q[..., 0] = 11.3125
+        q = bf16(q).cuda()
+        for parts in (1, 3):
+            o, lse = fa.decode_tree(q, *p.args(), max_parts=parts, scale=0.125, **p.kw())
+            check_tree(o, lse, q, p, [T, T], None, 0.125, heads=[0, 7])
