@@ -24,7 +24,7 @@
 // that off by at most 2⁻¹⁸ of it); four converter warps widen V to fp16, each row
 // times its power of two relative to a reference that P̃ and O share, and lay out
 // the keys' powers of two as floats.  P̃ is fp16, its reference 2^3 below the maximum.
-// A tile whose value rows lie further apart than 2^16 goes through bf16 (fa_tree.cu).
+// A tile with value rows further below the reference than 2^15 goes through bf16 (fa_tree.cu).
 //
 // The rest (parts, pieces, masks, values in masked places) is as in fa_tree.cu.
 //
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
   constexpr float kLazy = 8.f;             // rescale once the maximum exceeds the reference by this …
   constexpr float kBase = FP8 ? 3.f : 0.f; // … the new reference lies this below the maximum
   constexpr int kKvLazy = 7;               // E4M3: widened values stay below 448·2^7
-  constexpr int kKvFar = 16;               // value rows that are smaller by more than this need bf16's range
+  constexpr int kKvFar = 15;               // value rows that are smaller by more than this need bf16's range
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;

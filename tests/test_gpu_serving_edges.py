@@ -93,7 +93,7 @@ def test_an_infinite_value_under_a_weight_of_one(T):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("T", [2, 6, 12, 40])
-@pytest.mark.parametrize("power", [1, 4, 6, 8, 9])
+@pytest.mark.parametrize("power", [1, 4, 6, 8, 9, 15, 16, 17])
 def test_small_weights_beside_one_that_counts_for_nothing(T, power, d):
     """E4M3: one key has nearly all of a row's weight and a value of zero, so the row's result is made of weights 2^-16 to
     2^-22 of the largest, and a few value rows without weight are larger by 2^power.  Column 5 holds E4M3's smallest."""
