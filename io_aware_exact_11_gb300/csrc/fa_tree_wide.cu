@@ -169,7 +169,8 @@ __device__ __forceinline__ void load_q_tile(const TreeParams& p, const TreeWalk&
         uint8_t* dst = q + r * D + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
         *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2*>(dst + kRowTile * D) = make_uint2(lo[0], lo[1]);
-        if (ch == 0) f[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
+        // (Not 0, however small: what a row does not see stands as −∞ when it is multiplied by this.)
+        if (ch == 0) f[r] = fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23), 1e-45f);
       }
     }
   }

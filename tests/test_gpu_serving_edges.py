@@ -116,3 +116,17 @@ def test_small_weights_beside_one_that_counts_for_nothing(T, power, d):
         for parts in (1, 3):
             o, lse = fa.decode_tree(q, *p.args(), max_parts=parts, scale=0.125, **p.kw())
             check_tree(o, lse, q, p, [T, T], None, 0.125, heads=[0, 7])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("scale", [2.0 ** -30, 1e-38])
+def test_zero_queries_and_the_smallest_scales(cache, T, scale):
+    p = Paged(np.random.default_rng(T), [300, 128 + T, T], 2, 128, 16, cache)
+    q = np.random.default_rng(3).standard_normal((3, 8, T, 128))
+    q[:, :, 0] = 0.0
+    q[:, 3] = 0.0
+    q[:, 5] *= 2.0 ** -100
+    q = bf16(q).cuda()
+    o, lse = fa.decode_tree(q, *p.args(), scale=scale, **p.kw())
+    check_tree(o, lse, q, p, [T] * 3, None, scale)
