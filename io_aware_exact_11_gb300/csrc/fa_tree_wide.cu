@@ -778,7 +778,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
     // ------------------------------------ converters: one value row and one key's scale per thread
     const int r = tid - 384;
     int next = 0, ref = 0;  // the tile of the part whose scales come next
-    bool ok = true;  // false for good once a wait of this thread has failed; all leave together, after a vote
+    // A wait that fails raises the abort flag, and all leave together, after a vote on it: until then a thread whose wait
+    // has failed goes on, since the others wait for it at the vote without a limit.
+    bool ok = true;
+    auto vote = [&] { ok = !named_any(4, 128, *abort_flag != 0); };
     TreeWalk w;
     w.begin(p, my);
     do {
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       // The scales of tile i of the pair, the n-th of the part: the softmax wants them before the widened values.
       // Slot n % 8 was read for tile n − 8, whose second product the wait for a place to widen into has told the end of.
       auto scales = [&](int i, int n) {
-        ok = mbar_wait_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, abort_flag, p.err, tree_site(0x2b)) && ok;
+        mbar_wait_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, abort_flag, p.err, tree_site(0x2b));
         const uint32_t kb = sc->k_scale[n % kScaleRing][r];
         const int key = i * kBN + r;
         bool used = key < w.len;
@@ -802,7 +805,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         if (lane == 0) sc->top[n & 1][warp - 12] = ((top + 2048) << 16) | (2048 - low);
         // (Byte 0 stands for 2^−127, below the normal numbers.)
         sc->ks[n % kTileRing][r] = kb == 0 ? 5.877471754111438e-39f : __uint_as_float(kb << 23);
-        ok = !named_any(4, 128, !ok);  // joined by all converters: any failed wait, of the tile before too, ends them all
+        vote();
         const int4 tp = *reinterpret_cast<const int4*>(sc->top[n & 1]);
         const uint32_t both = __vmaxu2(__vmaxu2(tp.x, tp.y), __vmaxu2(tp.z, tp.w));
         const int most = static_cast<int>(both >> 16) - 2048;
@@ -825,9 +828,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         if (i < w.t0) continue;  // (the first tile's scales come before its values)
         const int tile = next - (i + 1 < w.t1 ? 2 : 1);
         const int slot = tile % C::kRV;
-        // (A thread whose wait fails goes on to the next vote: the others wait for it there, without a limit.)
-        ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(0x2d)) && ok;
-        ok = mbar_wait_inl(&ms->v16_empty[tile & 1], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x2c)) && ok;
+        mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(0x2d));
+        mbar_wait_inl(&ms->v16_empty[tile & 1], ((tile >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x2c));
         const int key = i * kBN + r;
         const uint8_t* src = smem + C::kOffV + slot * kSlot + r * D;
         uint8_t* dst = smem + C::kOffV16 + (tile & 1) * C::kV16 + r * 128;
@@ -870,7 +872,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->v_empty[slot]);
       }
-      ok = !named_any(4, 128, !ok);  // the piece's last waits have had no vote
+      vote();  // the piece's last waits have had none
     } while (ok && w.next(p));
   } else {
     reg_dealloc<C::kRegsOther>();  // idle until the end
