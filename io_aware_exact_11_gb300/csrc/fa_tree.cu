@@ -127,6 +127,7 @@ struct Misc {
   float corr[2][NR];                   // factor of the last rescale
   float red[2][4][NR];                 // per-warp maxima or sums
   float scale[2][NR];                  // what a stream's O is multiplied by in the end
+  float kv_scale[2];                   // E4M3: and by this
   int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
   int64_t o_off[2][NR];                // its element offset in O
   int fresh[2][NR];                    // a live row that has seen nothing yet
@@ -804,10 +805,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             p.lse[row[kt]] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           }
         }
-        // What this stream's O is multiplied by.
-        mine *= sum != 0.f ? 1.f / sum : 0.f;
-        ms->scale[g][kt] = mine * (FP8 ? exp2f(static_cast<float>(max(kv_ref, -300))) : 1.f);
+        // What this stream's O is multiplied by, and then by the power of two that its values are relative to (not at
+        // once: the product of the two may be too small a number).
+        ms->scale[g][kt] = mine * (sum != 0.f ? 1.f / sum : 0.f);
       }
+      if (FP8 && kt == 0) ms->kv_scale[g] = exp2f(static_cast<float>(max(kv_ref, -300)));
       if (w.t0 == 0 && tid == 0) p.pieces[w.pair(p)] = w.pieces(part, my.per);
       named_sync(3, 256);
       const uint32_t* bad = ms->bad[w.index % kBadRing];
@@ -829,7 +831,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
             for (int q = 0; q < kOut; ++q) {
               const float k = ms->scale[e][c0 + q];
-              if (k != 0.f) o[q] += __uint_as_float(r[q]) * k;  // 0: a stream without keys has left O unwritten
+              if (k == 0.f) continue;  // a stream without keys has left O unwritten
+              o[q] += FP8 ? __uint_as_float(r[q]) * k * ms->kv_scale[e] : __uint_as_float(r[q]) * k;
             }
           }
         }

@@ -193,6 +193,9 @@ __device__ __forceinline__ void rescale_row(uint32_t addr, float k) {
   tmem_wait_st();
 }
 
+// 2^e for e from −127 on (0 below).
+__device__ __forceinline__ float power_f32(int e) { return __uint_as_float(static_cast<uint32_t>(max(e, -127) + 127) << 23); }
+
 // Which keys of a tile token t sees: all before `context` (a place in the tile, maybe before it) and, up to `end`, the
 // drafted ones behind that its row of the mask names.
 static __device__ __noinline__ uint4 seen_keys(const uint8_t* row, int t, int context, int end) {
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
       if constexpr (TILES == 1) {
         join->m[g][kt] = m;
         join->l[g][kt] = l_run;
-        if (kt == 0) join->kv[g] = kv_ref;
+        if (kt == 0) join->kv[g] = done > 0 ? kv_ref : -1024;
         tc_fence_before();
         named_sync(3, 256);
         tc_fence_after();
@@ -681,11 +684,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
         scale[g] = 1.f;
       }
       const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      // E4M3: times the power of two that the values are relative to, half of it here and half at the end: the whole of it
+      // may be too small a number.
+      const int half_kv = FP8 ? (TILES == 1 ? max(join->kv[0], join->kv[1]) : kv_ref) >> 1 : 0;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int kv = TILES == 1 ? join->kv[e] : kv_ref;
-        scale[e] *= inv * (FP8 ? exp2f(static_cast<float>(max(kv, -300))) : 1.f);
-      }
+      for (int e = 0; e < 2; ++e) scale[e] *= inv * (FP8 ? power_f32((TILES == 1 ? join->kv[e] : kv_ref) - half_kv) : 1.f);
       const bool fine = __all_sync(0xffffffffu, ok);
       if (fine && live && (TILES == 2 || g == 0)) {
         if (!whole) {
@@ -720,8 +723,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
             reg_fence(r);
             if (scale[e] != 0.f) {  // 0: a stream without keys has left O unwritten
 #pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] += __uint_as_float(r[q]) * scale[e];
+              for (int q = 0; q < 32; q += 2)
+                ffma2(o[q], o[q + 1], __uint_as_float(r[q]), __uint_as_float(r[q + 1]), scale[e], scale[e], o[q], o[q + 1]);
             }
+          }
+          if constexpr (FP8) {
+            const float power = power_f32(half_kv);
+#pragma unroll
+            for (int q = 0; q < 32; q += 2) fmul2(o[q], o[q + 1], o[q], o[q + 1], power, power);
           }
           if (live) {
             if (!whole) {

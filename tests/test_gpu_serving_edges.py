@@ -130,3 +130,19 @@ def test_zero_queries_and_the_smallest_scales(cache, T, scale):
     q = bf16(q).cuda()
     o, lse = fa.decode_tree(q, *p.args(), scale=scale, **p.kw())
     check_tree(o, lse, q, p, [T] * 3, None, scale)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("power", [100, 120, 122])
+def test_the_smallest_values_of_a_long_sequence(T, power):
+    """E4M3 rows near the smallest power of two, under a row sum in the tens of thousands."""
+    def edit(name, b, x):
+        if name == "v":
+            x[:] = (1.0 + 0.75 * np.abs(np.sin(np.arange(x.size))).reshape(x.shape)) * 2.0 ** -power
+        else:
+            x *= 2.0 ** -4
+    p = Paged(np.random.default_rng(T), [40000], 1, 64, 128, "e4m3", edit=edit)
+    q = bf16(np.random.default_rng(4).standard_normal((1, 2, T, 64))).cuda()
+    for parts in (1, 0):
+        o, lse = fa.decode_tree(q, *p.args(), max_parts=parts, **p.kw())
+        check_tree(o, lse, q, p, [T], None, 0.125, heads=[1])
