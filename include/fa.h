@@ -419,9 +419,11 @@ FA_API fa_status fa_decode_tree(const void* q, const void* k_cache, const void* 
                                 int max_parts, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * fa_device_status — synchronises `stream`, then reports FA_ERR_DEVICE_TIMEOUT
- * if any kernel of this library has given up on a bounded pipeline wait since
- * the last call (and clears that flag), FA_ERR_CUDA on a CUDA error, else FA_OK.
+ * fa_device_status — synchronises `stream`, then reports what the kernels of
+ *   this library have recorded on the current device: FA_ERR_DEVICE_TIMEOUT if
+ *   one has given up on a bounded pipeline wait, then FA_ERR_INVALID_ARG if one
+ *   has met a page id, length or position outside its range; the first of each
+ *   kind, one per call (and clears it).  FA_ERR_CUDA on a CUDA error, else FA_OK.
  */
 FA_API fa_status fa_device_status(void* stream);
 

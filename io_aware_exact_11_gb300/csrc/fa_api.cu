@@ -1299,25 +1299,23 @@ fa_status fa_device_status(void* stream) {
   unsigned int codes[2] = {0, 0};
   e = cudaMemcpy(codes, word, sizeof(codes), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "fa_device_status: read watchdog");
-  if (codes[0] != 0 || codes[1] != 0) {
-    const unsigned int zero[2] = {0, 0};
-    cudaMemcpy(word, zero, sizeof(zero), cudaMemcpyHostToDevice);
-  }
-  if (codes[0] == 0 && codes[1] != 0) {
-    const char* who = (codes[1] >> 8) == fa::kKernTree ? "decode tree" : "paged cache";
-    if ((codes[1] & 0xFFu) == fa::kSiteBadBlock)
+  // One report per call; the other word stays for the next call.
+  const int which = codes[0] != 0 ? 0 : 1;
+  const unsigned int code = codes[which];
+  if (code == 0) return ok();
+  const unsigned int zero = 0;
+  cudaMemcpy(word + which, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+  if (which == 1) {
+    const char* who = (code >> 8) == fa::kKernTree ? "decode tree" : "paged cache";
+    if ((code & 0xFFu) == fa::kSiteBadBlock)
       return fail(FA_ERR_INVALID_ARG, "%s: a block-table entry is outside [0, num_blocks)", who);
     return fail(FA_ERR_INVALID_ARG, "%s: a length or position is outside its range", who);
   }
-  const unsigned int code = codes[0];
-  if (code != 0) {
-    if ((code & 0xFFu) == fa::kSiteBadBlock)
-      return fail(FA_ERR_INVALID_ARG, "paged decode: a block-table entry is outside [0, num_blocks) (page 0 was read)");
-    if ((code & 0xFFu) == fa::kSiteBadLength)
-      return fail(FA_ERR_INVALID_ARG, "paged decode: a sequence length is outside [1, max_blocks * block_size]");
-    return fail(FA_ERR_DEVICE_TIMEOUT, "kernel %u gave up waiting at site %u", code >> 8, code & 0xFFu);
-  }
-  return ok();
+  if ((code & 0xFFu) == fa::kSiteBadBlock)
+    return fail(FA_ERR_INVALID_ARG, "paged decode: a block-table entry is outside [0, num_blocks) (page 0 was read)");
+  if ((code & 0xFFu) == fa::kSiteBadLength)
+    return fail(FA_ERR_INVALID_ARG, "paged decode: a sequence length is outside [1, max_blocks * block_size]");
+  return fail(FA_ERR_DEVICE_TIMEOUT, "kernel %u gave up waiting at site %u", code >> 8, code & 0xFFu);
 }
 
 }  // extern "C"

@@ -146,3 +146,19 @@ def test_the_smallest_values_of_a_long_sequence(T, power):
     for parts in (1, 0):
         o, lse = fa.decode_tree(q, *p.args(), max_parts=parts, **p.kw())
         check_tree(o, lse, q, p, [T], None, 0.125, heads=[1])
+
+
+def test_a_bad_page_is_reported_behind_a_timeout():
+    import torch
+    kc, vc = (torch.zeros((4, 1, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    x = torch.ones((1, 1, 3, 64), dtype=torch.bfloat16, device="cuda")
+    fa.watchdog_selftest()
+    fa.cache_append(x, x, kc, vc, _i32([[9]]), _i32([0]))
+    with pytest.raises(fa.FAError) as ei:
+        fa.device_status()
+    assert ei.value.status == fa.FA_ERR_DEVICE_TIMEOUT
+    with pytest.raises(fa.FAError, match="paged cache") as ei:
+        fa.device_status()
+    assert ei.value.status == fa.FA_ERR_INVALID_ARG
+    fa.device_status()
+    assert not kc.any()
