@@ -1306,15 +1306,14 @@ fa_status fa_device_status(void* stream) {
   const unsigned int zero = 0;
   cudaMemcpy(word + which, &zero, sizeof(zero), cudaMemcpyHostToDevice);
   if (which == 1) {
-    const char* who = (code >> 8) == fa::kKernTree ? "decode tree" : "paged cache";
-    if ((code & 0xFFu) == fa::kSiteBadBlock)
-      return fail(FA_ERR_INVALID_ARG, "%s: a block-table entry is outside [0, num_blocks)", who);
-    return fail(FA_ERR_INVALID_ARG, "%s: a length or position is outside its range", who);
+    const bool page = (code & 0xFFu) == fa::kSiteBadBlock;
+    if ((code >> 8) == fa::kKernDecode)
+      return fail(FA_ERR_INVALID_ARG, page ? "paged decode: a block-table entry is outside [0, num_blocks) (page 0 was read)"
+                                           : "paged decode: a sequence length is outside [1, max_blocks * block_size]");
+    return fail(FA_ERR_INVALID_ARG, page ? "%s: a block-table entry is outside [0, num_blocks)"
+                                         : "%s: a length or position is outside its range",
+                (code >> 8) == fa::kKernTree ? "decode tree" : "paged cache");
   }
-  if ((code & 0xFFu) == fa::kSiteBadBlock)
-    return fail(FA_ERR_INVALID_ARG, "paged decode: a block-table entry is outside [0, num_blocks) (page 0 was read)");
-  if ((code & 0xFFu) == fa::kSiteBadLength)
-    return fail(FA_ERR_INVALID_ARG, "paged decode: a sequence length is outside [1, max_blocks * block_size]");
   return fail(FA_ERR_DEVICE_TIMEOUT, "kernel %u gave up waiting at site %u", code >> 8, code & 0xFFu);
 }
 

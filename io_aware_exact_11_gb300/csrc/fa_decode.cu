@@ -65,7 +65,7 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4& u, float (&f)[8]) {
 __device__ __forceinline__ int checked_page(const DecodeParams& p, int b, int page) {
   int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + page];
   if (blk < 0 || blk >= p.num_blocks) {
-    atomicCAS(p.err, 0u, (kKernDecode << 8) | kSiteBadBlock);
+    atomicCAS(p.err + 1, 0u, (kKernDecode << 8) | kSiteBadBlock);
     blk = 0;
   }
   return blk;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) decode_split_kernel(const DecodePara
     // Per-sequence length; splits are whole 128-key multiples of it.
     len = p.seq_lens[b];
     if (len < 1 || len > p.max_blocks * p.block_size) {
-      if (tid == 0) atomicCAS(p.err, 0u, (kKernDecode << 8) | kSiteBadLength);
+      if (tid == 0) atomicCAS(p.err + 1, 0u, (kKernDecode << 8) | kSiteBadLength);
       len = min(max(len, 1), p.max_blocks * p.block_size);
     }
     chunk = (((len + p.n_splits - 1) / p.n_splits) + 127) & ~127;

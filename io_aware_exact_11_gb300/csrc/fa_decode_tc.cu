@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_gqa_tc_kernel(const __grid
   if (PAGED) {
     len = p.seq_lens[b];
     if (len < 1 || len > p.max_blocks * p.block_size) {
-      if (threadIdx.x == 0) atomicCAS(p.err, 0u, (kKernDecode << 8) | kSiteBadLength);
+      if (threadIdx.x == 0) atomicCAS(p.err + 1, 0u, (kKernDecode << 8) | kSiteBadLength);
       len = min(max(len, 1), p.max_blocks * p.block_size);
     }
     chunk = (((len + p.n_splits - 1) / p.n_splits) + 127) & ~127;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_gqa_tc_kernel(const __grid
       for (int i = lane; i < npages; i += 32) {
         int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + page0 + i];
         if (blk < 0 || blk >= p.num_blocks) {
-          atomicCAS(p.err, 0u, (kKernDecode << 8) | kSiteBadBlock);
+          atomicCAS(p.err + 1, 0u, (kKernDecode << 8) | kSiteBadBlock);
           blk = 0;
         }
         staged[i] = blk;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_gqa_tc_kernel(const __grid
       if (rel < kMaxStagedPages) return staged[rel];
       int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks + t0 / p.block_size];
       if (blk < 0 || blk >= p.num_blocks) {
-        atomicCAS(p.err, 0u, (kKernDecode << 8) | kSiteBadBlock);
+        atomicCAS(p.err + 1, 0u, (kKernDecode << 8) | kSiteBadBlock);
         blk = 0;
       }
       return blk;

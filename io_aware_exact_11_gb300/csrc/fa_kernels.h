@@ -65,10 +65,9 @@ struct DecodeParams {
   int d = 128;  // head dim: 64 or 128
 };
 
-// Device-side argument checks report with these sites: the decode kernels in the
-// watchdog word, the paged cache's and drafted tokens' ones in the word after it,
-// which no pipeline wait looks at (a bad page of one sequence leaves the others'
-// results, and other kernels, alone).
+// Device-side argument checks report with these sites in the word after the
+// watchdog's, which no pipeline wait looks at: a bad page of one sequence leaves
+// the others' results, and other kernels, alone.
 enum : unsigned int { kSiteBadBlock = 0xE1, kSiteBadLength = 0xE2 };
 
 // Grouped-query split-KV decode on tensor cores (fa_decode_tc.cu).

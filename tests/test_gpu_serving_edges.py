@@ -162,3 +162,33 @@ def test_a_bad_page_is_reported_behind_a_timeout():
     assert ei.value.status == fa.FA_ERR_INVALID_ARG
     fa.device_status()
     assert not kc.any()
+
+
+@pytest.mark.parametrize("bad", ["page", "length"])
+@pytest.mark.parametrize("Hq", [2, 8])
+def test_an_unread_report_of_the_paged_decode_leaves_later_calls_alone(Hq, bad):
+    """A bad page or length is one sequence's; the word that it is reported in is not the one that pipeline waits look at:
+    a timeout behind it is reported first, and then the page or length."""
+    import torch
+    p = Paged(np.random.default_rng(Hq), [3000, 700], 2, 128, 16, "bf16")
+    q = bf16(np.random.default_rng(1).standard_normal((2, Hq, 1, 128))).cuda()
+    want, _ = fa.decode_paged(q, *p.args())
+    tree, _ = fa.decode_tree(q, *p.args())
+    fa.device_status()
+    table, lens = p.table.clone(), p.seq_lens.clone()
+    if bad == "page":
+        table[1, 3] = -5
+    else:
+        lens[1] = 0
+    got, _ = fa.decode_paged(q, p.k_cache, p.v_cache, table, lens)
+    after, _ = fa.decode_paged(q, *p.args())
+    tree2, _ = fa.decode_tree(q, *p.args())
+    assert torch.equal(got[0], want[0]) and torch.equal(after, want) and torch.equal(tree2, tree)
+    fa.watchdog_selftest()
+    with pytest.raises(fa.FAError) as ei:
+        fa.device_status()
+    assert ei.value.status == fa.FA_ERR_DEVICE_TIMEOUT
+    with pytest.raises(fa.FAError, match="paged decode") as ei:
+        fa.device_status()
+    assert ei.value.status == fa.FA_ERR_INVALID_ARG
+    fa.device_status()
