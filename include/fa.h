@@ -320,9 +320,9 @@ FA_API fa_status fa_backward_masked(const void* q, const void* k, const void* v,
  *   element's is needed (16-byte alignment throughout is faster).
  *   positions: device int32, entry b·pos_stride_b + n (pos_stride_b = 0 shares
  *   one row among the batch), or NULL for n; position0 is added.  Any int32
- *   position is exact: angles are reduced in 64-bit fixed point.
- *   inv_freq: d_rot/2 float64 values on the HOST, read during the call; scaled
- *   contexts are scaled frequencies and a magnitude μ other than 1.
+ *   position is exact: angles are reduced in 64-bit fixed point (off by 2^-34 turns).
+ *   inv_freq: d_rot/2 float64 values below 2^64 on the HOST, read during the call;
+ *   scaled contexts are scaled frequencies and a magnitude μ other than 1.
  *   Supported: even d <= 256, even d_rot <= d.
  */
 FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k, int N,

@@ -939,6 +939,30 @@ fa_status fa_backward_masked(const void* q, const void* k, const void* v, const 
 
 namespace {
 
+// w/2π modulo 1 in units of 2^-64, to the nearest, for |w| < 2^64: the 53-bit significand of w times 1/2π to 192 bits, of
+// which the bits behind the binary point are kept.  (The float64 quotient would be off by 2^-53 of itself, which a
+// position of 2^31 makes 2^-22.)
+uint64_t turn_fraction(double w) {
+  using Wide = unsigned __int128;
+  constexpr uint64_t c2 = 0x28be60db9391054aull, c1 = 0x7f09d5f47d4d3770ull, c0 = 0x36d8a5664f10e410ull;
+  uint64_t raw;
+  memcpy(&raw, &w, sizeof(raw));
+  const int e = static_cast<int>(raw >> 52 & 0x7ff);
+  const uint64_t n = (raw & 0xfffffffffffffull) | 1ull << 52;  // |w| = n·2^(e − 1075); too small to matter for e = 0
+  // n/2π in units of 2^-64 (high) and the 64 bits behind them (low): |w|/2π = high·2^(e − 1139).
+  const Wide low = static_cast<Wide>(n) * c1 + static_cast<uint64_t>(static_cast<Wide>(n) * c0 >> 64);
+  const Wide high = static_cast<Wide>(n) * c2 + static_cast<uint64_t>(low >> 64);
+  const int at = 1075 - e;  // the fraction's last bit; the one below it rounds
+  uint64_t bits = 0;
+  if (at >= 1) {
+    bits = at < 128 ? static_cast<uint64_t>(high >> at) + static_cast<uint64_t>(high >> (at - 1) & 1) : 0;
+  } else {  // |w| >= 2^52: into the bits behind
+    const Wide next = high << 64 | static_cast<uint64_t>(low);
+    bits = static_cast<uint64_t>(next >> (64 + at)) + static_cast<uint64_t>(next >> (63 + at) & 1);
+  }
+  return raw >> 63 ? 0 - bits : bits;
+}
+
 // True if a [n0, n1, n2, d] tensor with these element strides stores every row in a place of its own.
 bool rows_distinct(int n0, int n1, int n2, int d, const int64_t* st) {
   std::pair<int64_t, int64_t> dim[3] = {{st[0], n0}, {st[1], n1}, {st[2], n2}};
@@ -1085,9 +1109,9 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B,
   const bool in_place = q == q_out && (H_k == 0 || k == k_out);
   for (int i = 0; i < d_rot / 2; ++i) {
     if (!std::isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "fa_rope: inv_freq[%d] is not finite", i);
-    const double turns = inv_freq[i] / 6.283185307179586476925287;
-    const double part = (turns - std::floor(turns)) * 18446744073709551616.0;  // whole turns drop out: positions are whole
-    p.turns[i] = part < 18446744073709551616.0 ? static_cast<uint64_t>(part) : 0;
+    if (std::fabs(inv_freq[i]) >= 18446744073709551616.0)
+      return fail(FA_ERR_UNSUPPORTED, "fa_rope: inv_freq[%d] must be below 2^64", i);
+    p.turns[i] = turn_fraction(inv_freq[i]);  // whole turns drop out: positions are whole
   }
   p.q = q;
   p.k = H_k > 0 ? k : nullptr;

@@ -7,9 +7,9 @@
 // gradient turns back by −θ with the same μ.
 //
 // Angles.  θ/2π = p·(w_i/2π) is only needed modulo 1 and p is a whole number,
-// so w_i/2π is held as a 64-bit fraction of a turn and p times it is one 64-bit
-// product that wraps exactly where whole turns drop out.  Far positions lose
-// nothing: the error is p·2⁻⁶⁴ turns (plus the float64 rounding of w_i), where
+// so w_i/2π is held as a 64-bit fraction of a turn, rounded from 192 bits of 1/2π, and
+// p times it is one 64-bit product that wraps exactly where whole turns drop out.  Far
+// positions lose nothing: the error is at most p·2⁻⁶⁵ turns for the float64 w_i given, where
 // a float32 product would be off by p·2⁻²⁴ radians.  Of the product the upper 32
 // bits are kept (2⁻³² turns, 1.5e-9 rad) and rounded to float32, half turns in
 // [−1, 1): 2⁻²⁵ of them, π·2⁻²⁵ rad at most.  sincospif adds its own 2 ulp.

@@ -3,6 +3,7 @@
 import ctypes
 import os
 
+import numpy as np
 import pytest
 
 from io_aware_exact_11_gb300 import fa
@@ -39,3 +40,11 @@ def test_decode_tree_in_place_needs_the_queries_strides(L, st):
     assert b"in place" not in L.fa_get_last_error()
     _tree(L, T=1, st=_st(1024, 256, 64, 1024, 256, 128))               # and so is a stride that takes no step
     assert b"in place" not in L.fa_get_last_error()
+
+
+@pytest.mark.parametrize("w,status", [(2.0 ** 64, UNS), (-1e300, UNS), (float("inf"), INV)])
+def test_rope_refuses_frequencies_without_a_fraction(L, w, status):
+    inv = np.array([1.0, w])
+    assert L.fa_rope(FAKE, None, FAKE, None, 1, 1, 0, 1, 4, 4, fa.FA_FP32, None, None, 0, 0, inv.ctypes.data, 1.0, 0, 0,
+                     None) == status
+    assert b"inv_freq[1]" in L.fa_get_last_error()

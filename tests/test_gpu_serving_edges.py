@@ -1,5 +1,8 @@
 """The operators around attention at the edges of their ranges."""
 
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -192,3 +195,28 @@ def test_an_unread_report_of_the_paged_decode_leaves_later_calls_alone(Hq, bad):
         fa.device_status()
     assert ei.value.status == fa.FA_ERR_INVALID_ARG
     fa.device_status()
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_is_exact_at_any_position_and_frequency(inverse):
+    """Against rational arithmetic.  fp32: the angle's fraction of a turn kept to 2^-32 and rounded to 24 bits (π·2^-25
+    radians, 2π·2^-32), sine and cosine within 2 ulp (2·2^-24), a product (2^-24): 4.6·2^-24 of |x₁| + |x₂|, and the
+    result's rounding."""
+    import torch
+    w = [1.0, 0.75, 3.3, 100.3, 12345.678, -2.5, 1e-5, 1e-19, 1e15, 1.7e19, 0.0, 5e-324, 2.0 ** -64, 6.283185307179586]
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 3, 1999999973, 16777217, 1, 0, -7, 1048577, 2 ** 30]
+    x = torch.randn((1, 3, len(pos), 2 * len(w)), generator=torch.Generator().manual_seed(5)).cuda()
+    f = fa.rope_backward if inverse else fa.rope
+    y, _ = f(x, None, np.array(w), positions=_i32(pos), interleaved=True)
+    x, y = np64(x)[0], np64(y)[0]
+    for n, p in enumerate(pos):
+        for i, wi in enumerate(w):
+            part = Fraction(p) * Fraction(wi) / (2 * PI)
+            angle = 2 * math.pi * float(part - math.floor(part)) * (-1 if inverse else 1)
+            c, s = math.cos(angle), math.sin(angle)
+            a, b = x[:, n, 2 * i], x[:, n, 2 * i + 1]
+            for got, ref in ((y[:, n, 2 * i], a * c - b * s), (y[:, n, 2 * i + 1], b * c + a * s)):
+                assert np.all(np.abs(got - ref) <= 2.0 ** -24 * (np.abs(ref) + 4.6 * (np.abs(a) + np.abs(b)))), (p, wi)
