@@ -25,10 +25,10 @@ def _st(*x):
 
 
 def _tree(L, **kw):
-    a = dict(q=FAKE, o=FAKE, B=2, Hq=4, Hkv=2, T=4, mb=16, d=64, st=None)
+    a = dict(q=FAKE, o=FAKE, B=2, Hq=4, Hkv=2, T=4, mb=16, d=64, st=None, wsb=1 << 30)
     a.update(kw)
     return L.fa_decode_tree(a["q"], FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, 0, a["o"], None, a["B"], a["Hq"], a["Hkv"],
-                            a["T"], 100, 16, a["mb"], a["d"], fa.FA_BF16, 0.1, a["st"], 4, FAKE, 1 << 30, None)
+                            a["T"], 100, 16, a["mb"], a["d"], fa.FA_BF16, 0.1, a["st"], 4, FAKE, a["wsb"], None)
 
 
 @pytest.mark.parametrize("st", [(1024, 64, 256, 1024, 256, 64), (2048, 256, 64, 1024, 256, 64), (1024, 256, 64, 1024, 64, 256)])
@@ -36,10 +36,11 @@ def test_decode_tree_in_place_needs_the_queries_strides(L, st):
     """Rows would be written over queries that other blocks still read."""
     assert _tree(L, st=_st(*st)) == INV
     assert b"in place" in L.fa_get_last_error()
-    _tree(L, o=FAKE + (1 << 16), st=_st(*st))                          # elsewhere these strides are fine
-    assert b"in place" not in L.fa_get_last_error()
-    _tree(L, T=1, st=_st(1024, 256, 64, 1024, 256, 128))               # and so is a stride that takes no step
-    assert b"in place" not in L.fa_get_last_error()
+    # Elsewhere these strides are fine, and so are ones that take no step: the next check refuses the workspace.
+    assert _tree(L, o=FAKE + (1 << 16), st=_st(*st), wsb=0) == INV
+    assert b"workspace" in L.fa_get_last_error()
+    assert _tree(L, T=1, st=_st(1024, 256, 64, 1024, 256, 128), wsb=0) == INV
+    assert b"workspace" in L.fa_get_last_error()
 
 
 @pytest.mark.parametrize("w,status", [(2.0 ** 64, UNS), (-1e300, UNS), (float("inf"), INV)])
