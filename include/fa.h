@@ -342,7 +342,8 @@ FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out,
  *   whole number for which the row's largest finite magnitude is <= 448·2^k.
  *   Infinities and NaN become NaN codes.  k_scale and v_scale are ignored for FA_BF16.
  *   strides: NULL for contiguous k, v, or 6 element strides {k_b, k_h, k_n, v_…},
- *   multiples of 8, >= 0.  Two tokens must not name the same slot in one call.
+ *   multiples of 8, >= 0 (those of dimensions of size 1 do not matter).  Two
+ *   tokens must not name the same slot in one call.
  *   Page ids and positions outside the table, and new_lens outside [0, N], are
  *   caught on the device: those tokens are not written and fa_device_status
  *   then reports FA_ERR_INVALID_ARG.

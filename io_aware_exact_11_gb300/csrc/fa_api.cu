@@ -1009,15 +1009,16 @@ fa_status check_cache(const char* who, const void* k_cache, const void* v_cache,
   return FA_OK;
 }
 
-// Two bf16 row tensors [B, H, N, d] with strides that are multiples of 16 bytes.
-fa_status check_rows(const char* who, const int64_t* strides, int64_t* a, int64_t* b, int H, int N, int d) {
+// Two bf16 row tensors [B, H, N, d] with strides that are multiples of 16 bytes, where a stride takes a step at all.
+fa_status check_rows(const char* who, const int64_t* strides, int64_t* a, int64_t* b, int B, int H, int N, int d) {
   if (strides == nullptr) {
     contiguous_strides(a, H, N, d);
     contiguous_strides(b, H, N, d);
     return FA_OK;
   }
+  const int size[3] = {B, H, N};
   for (int i = 0; i < 6; ++i)
-    if (strides[i] < 0 || strides[i] % 8 != 0)
+    if (size[i % 3] > 1 && (strides[i] < 0 || strides[i] % 8 != 0))
       return fail(FA_ERR_INVALID_ARG, "%s: stride[%d]=%lld must be >= 0 and a multiple of 8 elements", who, i,
                   static_cast<long long>(strides[i]));
   memcpy(a, strides, 3 * sizeof(int64_t));
@@ -1148,7 +1149,7 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_c
     return fail(FA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned (start, new_lens 4-byte)", who);
   fa::CacheParams p;
   memset(&p, 0, sizeof(p));
-  if ((r = check_rows(who, strides, p.sk, p.sv, H_kv, N, d)) != FA_OK) return r;
+  if ((r = check_rows(who, strides, p.sk, p.sv, B, H_kv, N, d)) != FA_OK) return r;
   if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
   p.k_rows = const_cast<void*>(k);
   p.v_rows = const_cast<void*>(v);
@@ -1184,7 +1185,7 @@ fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_
     return fail(FA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned (seq_lens 4-byte)", who);
   fa::CacheParams p;
   memset(&p, 0, sizeof(p));
-  if ((r = check_rows(who, strides, p.sk, p.sv, H_kv, N, d)) != FA_OK) return r;
+  if ((r = check_rows(who, strides, p.sk, p.sv, B, H_kv, N, d)) != FA_OK) return r;
   if (!rows_distinct(B, H_kv, N, d, p.sk) || !rows_distinct(B, H_kv, N, d, p.sv))
     return fail(FA_ERR_INVALID_ARG, "%s: k or v overlaps itself", who);
   if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
@@ -1240,7 +1241,7 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
     return fail(FA_ERR_INVALID_ARG, "%s: mask_stride_b must be 0 or >= T*T", who);
   fa::TreeParams p;
   memset(&p, 0, sizeof(p));
-  if ((r = check_rows(who, strides, p.sq, p.so, H_q, T, d)) != FA_OK) return r;
+  if ((r = check_rows(who, strides, p.sq, p.so, B, H_q, T, d)) != FA_OK) return r;
   if (!rows_distinct(B, H_q, T, d, p.so)) return fail(FA_ERR_INVALID_ARG, "%s: o overlaps itself", who);
   if (q == o && ((B > 1 && p.sq[0] != p.so[0]) || (H_q > 1 && p.sq[1] != p.so[1]) || (T > 1 && p.sq[2] != p.so[2])))
     return fail(FA_ERR_INVALID_ARG, "%s: in place needs equal strides", who);

@@ -49,3 +49,10 @@ def test_rope_refuses_frequencies_without_a_fraction(L, w, status):
     assert L.fa_rope(FAKE, None, FAKE, None, 1, 1, 0, 1, 4, 4, fa.FA_FP32, None, None, 0, 0, inv.ctypes.data, 1.0, 0, 0,
                      None) == status
     assert b"inv_freq[1]" in L.fa_get_last_error()
+
+
+def test_strides_of_dimensions_of_one_are_not_looked_at(L):
+    assert _tree(L, T=1, o=FAKE + (1 << 16), st=_st(1024, 256, 3, 1024, 256, -1), wsb=0) == INV
+    assert b"workspace" in L.fa_get_last_error()
+    assert _tree(L, T=2, o=FAKE + (1 << 16), st=_st(1024, 256, 3, 1024, 256, 64), wsb=0) == INV
+    assert b"stride[2]" in L.fa_get_last_error()

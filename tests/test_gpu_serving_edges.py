@@ -220,3 +220,25 @@ def test_rope_is_exact_at_any_position_and_frequency(inverse):
             a, b = x[:, n, 2 * i], x[:, n, 2 * i + 1]
             for got, ref in ((y[:, n, 2 * i], a * c - b * s), (y[:, n, 2 * i + 1], b * c + a * s)):
                 assert np.all(np.abs(got - ref) <= 2.0 ** -24 * (np.abs(ref) + 4.6 * (np.abs(a) + np.abs(b)))), (p, wi)
+
+
+def test_strides_of_dimensions_of_one_do_not_matter():
+    import torch
+    d, H = 128, 4
+    rng = np.random.default_rng(6)
+    p = Paged(rng, [40, 50], 2, d, 16, "bf16")
+    def odd(x):  # [B,H,1,d] with strides of the token dimension that no 16-byte access could take
+        B, h, _, _ = x.shape
+        y = torch.empty((B * (h + 1) * d,), dtype=x.dtype, device="cuda").as_strided(x.shape, ((h + 1) * d, d, 3, 1))
+        return y.copy_(x)
+    q, k, v = (bf16(rng.standard_normal((2, h, 1, d))).cuda() for h in (H, 2, 2))
+    o, lse = fa.decode_tree(q, *p.args())
+    o2, lse2 = fa.decode_tree(odd(q), *p.args(), out=odd(torch.zeros_like(q)))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    caches = [[t.clone() for t in (p.k_cache, p.v_cache)] for _ in range(2)]
+    fa.cache_append(k, v, *caches[0], p.table, p.seq_lens - 1)
+    fa.cache_append(odd(k), odd(v), *caches[1], p.table, p.seq_lens - 1)
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(*caches))
+    gk, gv = fa.cache_gather(*p.args(), 1)
+    ok, ov = fa.cache_gather(*p.args(), 1, out_k=odd(torch.zeros_like(k)), out_v=odd(torch.zeros_like(k)))
+    assert torch.equal(gk, ok) and torch.equal(gv, ov)
