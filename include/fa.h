@@ -347,7 +347,7 @@ FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out,
  *   Page ids and positions outside the table, and new_lens outside [0, N], are
  *   caught on the device: those tokens are not written and fa_device_status
  *   then reports FA_ERR_INVALID_ARG.
- *   Supported: d = 64 or 128, block_size ∈ {16, 32, 64, 128}.
+ *   Supported: d = 64 or 128, block_size ∈ {16, 32, 64, 128}, N <= 2^30.
  */
 FA_API fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, uint8_t* k_scale,
                                  uint8_t* v_scale, const int32_t* block_table, const int32_t* start,

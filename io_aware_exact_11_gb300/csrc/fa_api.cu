@@ -1009,6 +1009,15 @@ fa_status check_cache(const char* who, const void* k_cache, const void* v_cache,
   return FA_OK;
 }
 
+// Tokens that the cache kernels can count, and a grid hold.
+fa_status check_tokens(const char* who, int B, int H_kv, int N, int d) {
+  if (N <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (N > (1 << 30)) return fail(FA_ERR_UNSUPPORTED, "%s: N must be <= 2^30", who);
+  if (static_cast<int64_t>(B) * H_kv * N > (1ll << 38) / (d / 8))
+    return fail(FA_ERR_UNSUPPORTED, "%s: B * H_kv * N too large", who);
+  return FA_OK;
+}
+
 // Two bf16 row tensors [B, H, N, d] with strides that are multiples of 16 bytes, where a stride takes a step at all.
 fa_status check_rows(const char* who, const int64_t* strides, int64_t* a, int64_t* b, int B, int H, int N, int d) {
   if (strides == nullptr) {
@@ -1079,6 +1088,7 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B,
     return fail(FA_ERR_INVALID_ARG, "fa_rope: magnitude must be finite and > 0");
   if (B > 65535 || H_q > 32767 || H_k > 32767)
     return fail(FA_ERR_UNSUPPORTED, "fa_rope: B must be <= 65535, H_q and H_k <= 32767");
+  if (static_cast<int64_t>(B) * N > (1ll << 37) / d) return fail(FA_ERR_UNSUPPORTED, "fa_rope: B * N * d too large");
   const uintptr_t esz = dtype == FA_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(q) % esz || reinterpret_cast<uintptr_t>(k) % esz ||
       reinterpret_cast<uintptr_t>(q_out) % esz || reinterpret_cast<uintptr_t>(k_out) % esz || misaligned4(positions))
@@ -1144,7 +1154,7 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_c
   fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, num_blocks, block_size,
                             max_blocks, d, cache_dtype);
   if (r != FA_OK) return r;
-  if (N <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if ((r = check_tokens(who, B, H_kv, N, d)) != FA_OK) return r;
   if (!aligned16(k) || !aligned16(v) || misaligned4(start) || misaligned4(new_lens))
     return fail(FA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned (start, new_lens 4-byte)", who);
   fa::CacheParams p;
@@ -1180,7 +1190,7 @@ fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_
   fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, num_blocks, block_size,
                             max_blocks, d, cache_dtype);
   if (r != FA_OK) return r;
-  if (N <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if ((r = check_tokens(who, B, H_kv, N, d)) != FA_OK) return r;
   if (!aligned16(k) || !aligned16(v) || misaligned4(seq_lens))
     return fail(FA_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned (seq_lens 4-byte)", who);
   fa::CacheParams p;
@@ -1245,6 +1255,7 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   if (!rows_distinct(B, H_q, T, d, p.so)) return fail(FA_ERR_INVALID_ARG, "%s: o overlaps itself", who);
   if (q == o && ((B > 1 && p.sq[0] != p.so[0]) || (H_q > 1 && p.sq[1] != p.so[1]) || (T > 1 && p.sq[2] != p.so[2])))
     return fail(FA_ERR_INVALID_ARG, "%s: in place needs equal strides", who);
+  if (static_cast<int64_t>(B) * H_q * T > INT32_MAX) return fail(FA_ERR_UNSUPPORTED, "%s: B * H_q * T too large", who);
   if ((static_cast<int64_t>(max_blocks) * block_size + 127) / 128 * H_kv > INT32_MAX)
     return fail(FA_ERR_UNSUPPORTED, "%s: max_blocks * block_size * H_kv too large", who);
   // A smaller workspace is taken with fewer parts; one part needs no room for pieces.

@@ -56,3 +56,26 @@ def test_strides_of_dimensions_of_one_are_not_looked_at(L):
     assert b"workspace" in L.fa_get_last_error()
     assert _tree(L, T=2, o=FAKE + (1 << 16), st=_st(1024, 256, 3, 1024, 256, 64), wsb=0) == INV
     assert b"stride[2]" in L.fa_get_last_error()
+
+
+@pytest.mark.parametrize("N", [(1 << 31) - 1, (1 << 30) + 1])
+@pytest.mark.parametrize("call", ["append", "gather"])
+def test_cache_refuses_more_tokens_than_a_table_can_hold(L, call, N):
+    """Rounding these up to whole groups of tokens would pass the largest int."""
+    st = _st(0, 0, 0, 0, 0, 0) if call == "append" else None
+    f = L.fa_cache_append if call == "append" else L.fa_cache_gather
+    args = [FAKE] * 8 if call == "gather" else [FAKE] * 9
+    assert f(*args, 1, 1, N, 100, 16, 16, 64, fa.FA_BF16, st, None) == UNS
+    assert b"N must be" in L.fa_get_last_error()
+
+
+def test_more_work_than_a_grid_holds_is_refused(L):
+    zero = _st(0, 0, 0, 0, 0, 0)
+    assert L.fa_cache_append(*[FAKE] * 9, 65535, 65535, 1 << 20, 100, 16, 16, 64, fa.FA_BF16, zero, None) == UNS
+    assert b"too large" in L.fa_get_last_error()
+    w = np.ones(128)
+    assert L.fa_rope(FAKE, None, FAKE + (1 << 20), None, 65535, 1, 0, 1 << 24, 256, 256, fa.FA_FP32, None, None, 0, 0,
+                     w.ctypes.data, 1.0, 0, 0, None) == UNS
+    assert b"too large" in L.fa_get_last_error()
+    assert _tree(L, B=65535, Hq=1024, Hkv=1024, T=256) == UNS
+    assert b"too large" in L.fa_get_last_error()
