@@ -301,9 +301,12 @@ cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
 }
 
 // Four tokens per thread once one per thread would fill the machine several times over: the look-up of their slots
-// and the loads of their rows then overlap, where one per thread spends its life on that chain of loads.  (Four and
-// one, replaying a graph: gathering 4 x 32768 E4M3 keys 128 and 151 us, writing 8 x 8192 tokens 40 and 44 us.  Two:
-// writing 40 us where four took 38.)
+// and the loads of their rows then overlap, where one per thread spends its life on that chain of loads; below, more
+// threads with shorter chains are quicker.  One, two and four, replaying a graph, d = 128, us:
+//   writing E4M3, 4 heads   8 x 512 tokens 4.8, 4.7, 5.1   8 x 2048 11.9, 10.6, 11.1   8 x 8192 39.0, 32.2, 31.6
+//   reading E4M3            8 x 512 5.0, 4.9, 5.0   8 x 2048 12.2, 10.8, 10.8   4 x 32768, 8 heads 146, 122, 122
+//   bf16                    8 x 8192, 4 heads, writing 41.2, 41.4, 41.3 and reading 43.5, 42.0, 42.2
+// The rule turns to four between the second and the third size (4 x 152 x 2048 threads of one token).
 template <bool APPEND, int D, bool FP8>
 cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
   const int64_t threads = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 8);

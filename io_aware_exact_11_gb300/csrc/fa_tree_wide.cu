@@ -582,8 +582,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           bool far = false;  // E4M3: the tile has gone over to bf16
           if constexpr (FP8) {
             const int code = sc->ref[tile % kTileRing];
-          const int ref = code >> 1;
-          far = code & 1;
+            const int ref = code >> 1;
+            far = code & 1;
             if (done > 0 && ref != kv_ref) {  // the widened values are relative to another exponent
               corr *= exp2f(static_cast<float>(max(kv_ref - ref, -200)));
               moved = true;
