@@ -246,36 +246,13 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, u
       if constexpr (!FP8) {
         *reinterpret_cast<uint4*>(q_smem + (ch >> 3) * NR * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
       } else {
-        // 2⁻ᵃ brings the row's largest magnitude to at most 448.
-        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        float x[8];
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = __uint_as_float(e & 1 ? w4[e >> 1] & 0xffff0000u : w4[e >> 1] << 16);
-          const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
-          if (a < 0x7f800000u) top = max(top, a);
-          else x[e] = __uint_as_float(0x7fffffffu);
-        }
-#pragma unroll
-        for (int mk = kChunks / 2; mk > 0; mk >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, mk));
-        const int a = max(-126, static_cast<int>(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
-        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float y0 = x[e] * inv, y1 = x[e + 1] * inv;
-          const uint32_t h = pack_e4m3x2(y0, y1);
-          const uint32_t back = e4m3x2_to_f16x2(h);
-          const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&back));
-          hi[e >> 2] |= h << ((e & 2) * 8);
-          lo[e >> 2] |= pack_e4m3x2((y0 - z.x) * 16.f, (y1 - z.y) * 16.f) << ((e & 2) * 8);
-        }
+        uint2 hi, lo;
+        const int a = split_q8<kChunks, 4>(v, hi, lo);
         // Rows of D bytes; chunk of 16 bytes XORed with the row (128-byte rows) or half of it (64-byte rows).
         const int sw = D == 128 ? r & 7 : (r >> 1) & 3;  // NR is a multiple of 16: the same for rows r and NR + r
         uint8_t* dst = q_smem + r * D + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(dst + NR * D) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(dst) = hi;
+        *reinterpret_cast<uint2*>(dst + NR * D) = lo;
         if (ch == 0) f[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
       }
     }
@@ -334,7 +311,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
   const TreePart my = find_part<kThreads>(p, part, ms->warp_sum, ms->start);
   const uint32_t tmem = ms->tmem_base;
-  const int bshift = 31 - __clz(p.block_size);  // a power of two
 
   if (my.count <= 0) {
     // nothing left for this CTA
@@ -342,79 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     reg_dealloc<kRegsOther>();
     // ------------------------------------------- loads of K (warp 8) and V (warp 10)
     const bool is_v = warp == 10;
-    const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
-    uint64_t* full = is_v ? ms->v_full : ms->k_full;
-    uint64_t* empty = is_v ? ms->v_empty : ms->k_empty;
-    uint8_t* dst = smem + (is_v ? C::kOffV : C::kOffK) + lane * p.block_size * (kSlot / kBN);
-    const int ring = is_v ? C::kRV : C::kRK;
-    if (lane == 0) tma_prefetch_desc(tm);
-    const int npt = kBN >> bshift;  // pages per tile
-    int slot = 0, sc = 0, issued = 0;
-    uint32_t parity = 1;
-    bool ok = true;
-    TreeWalk w;
-    w.begin(p, my);
-    do {
-      const int pages = (w.len + p.block_size - 1) >> bshift;
-      const int32_t* table = p.block_table + static_cast<int64_t>(w.b) * p.max_blocks;
-      // The ids of 32 pages at a time, one per lane, loaded one group ahead and checked when they are due.
-      int page = w.t0 * npt + lane;
-      int id = 0, ahead = page < pages ? table[page] : 0;
-      int at = 32;  // the tile's first page in the group
-#pragma unroll 1
-      for (int i = w.t0; i < w.t1; ++i) {
-        if (at == 32) {
-          at = 0;
-          id = page < pages ? ahead : -1;  // −1: past the end
-          if (page < pages && (id < 0 || id >= p.num_blocks)) {
-            report_bad_page(p);
-            id = 0;
-          }
-          page += 32;
-          ahead = page < pages ? table[page] : 0;
-        }
-        const int blk = __shfl_sync(0xffffffffu, id, at + lane);
-        at += npt;
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, tree_site(is_v ? 2 : 1)));
-        if (!ok) break;
-        const bool real = lane < npt && blk >= 0;
-        const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[slot], kSlot);
-          // The slot is free: the tile kRV before it has been widened, so the tile kRV + 3 before is done with, and
-          // so are its scale bytes.
-          if (FP8 && is_v) mbar_arrive_expect_tx(&ms->sc_full[sc], 2 * n_real * p.block_size);
-        }
-        __syncwarp();
-        if (lane < npt) {
-          const int row = real ? 0 : p.block_size;  // a row past the page: TMA fills the box with zeros
-          const int head = (real ? blk : 0) * p.Hkv + w.h;
-          if constexpr (kPg5)
-            tma_load_5d(dst + slot * kSlot, tm, &full[slot], 0, 0, 0, row >> 3, head);
-          else
-            tma_load_4d(dst + slot * kSlot, tm, &full[slot], 0, row, w.h, real ? blk : 0);
-          if (FP8 && is_v && real) {
-            const int64_t from = static_cast<int64_t>(head) << bshift;
-            bulk_load(&ms->k_scale[sc][lane << bshift], p.k_scale + from, p.block_size, &ms->sc_full[sc]);
-            bulk_load(&ms->v_scale[sc][lane << bshift], p.v_scale + from, p.block_size, &ms->sc_full[sc]);
-          }
-        }
-        ++issued;
-        sc = (sc + 1) % kScaleRing;
-        if (++slot == ring) {
-          slot = 0;
-          parity ^= 1u;
-        }
-      }
-    } while (ok && w.next(p));
-    // The copies in flight land before the CTA ends, also where a wait of another warp fails after this one is done.
-    if (lane == 0) {
-#pragma unroll 1
-      for (int n = max(0, issued - ring); n < issued; ++n) {
-        mbar_wait_drain_inl(&full[n % ring], (n / ring) & 1, kTreeDrainNs);
-        if (FP8 && is_v) mbar_wait_drain_inl(&ms->sc_full[n % kScaleRing], (n / kScaleRing) & 1, kTreeDrainNs);
-      }
-    }
+    load_pages<D, FP8, kScaleRing>(p, my, is_v, smem + (is_v ? C::kOffV : C::kOffK), is_v ? C::kRV : C::kRK,
+                                   is_v ? ms->v_full : ms->k_full, is_v ? ms->v_empty : ms->k_empty, ms->sc_full,
+                                   ms->k_scale[0], ms->v_scale[0], abort_flag, tree_site(is_v ? 2 : 1));
   } else if (warp == 9) {
     reg_dealloc<kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
@@ -745,22 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const int slot = tile % C::kRV;
           ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(9)) && ok;
           uint8_t* vr = smem + C::kOffV + slot * kSlot + (kPg5 ? (kt >> 3) * 2048 + (kt & 7) * 128 : kt * 128);
-          bool bad = false;
-#pragma unroll 2
-          for (int ch = 0; ch < D / 8; ++ch) {
-            uint4* at = reinterpret_cast<uint4*>(vr + (ch >> 3) * 1024 + (ch & 7) * 16);
-            uint32_t v4[4] = {0, 0, 0, 0};
-            if (key < w.len) {
-              const uint4 v = *at;
-              v4[0] = v.x, v4[1] = v.y, v4[2] = v.z, v4[3] = v.w;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((v4[e] & 0x7f80u) == 0x7f80u) v4[e] &= 0xffff0000u, bad = true;
-                if ((v4[e] & 0x7f800000u) == 0x7f800000u) v4[e] &= 0xffffu, bad = true;
-              }
-            }
-            *at = make_uint4(v4[0], v4[1], v4[2], v4[3]);
-          }
+          const bool bad = clean_value_row<D>(vr, key >= w.len);
           if (bad) atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
         }
         fence_proxy_async_smem();
@@ -854,17 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             continue;
           }
           if (!((bad[u >> 5] >> (u & 31)) & 1)) continue;
-          const int key = context + u;
-          int blk = p.block_table[static_cast<int64_t>(w.b) * p.max_blocks + (key >> bshift)];
-          if (blk < 0 || blk >= p.num_blocks) blk = 0;
-          const int64_t at =
-              (((static_cast<int64_t>(blk) * p.Hkv + w.h) << bshift) + (key & (p.block_size - 1))) * D + kt;
-          float v;
-          if (FP8)
-            v = (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
-          else
-            v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
-          if (fabsf(v) <= 3.4028234663852886e38f) continue;
+          const float v = taken_out<FP8>(p, value_row<D>(p, w, u) + kt);
+          if (v == 0.f) continue;
 #pragma unroll 1
           for (int q = 0; q < kOut; ++q) {
             if (row[c0 + q] < 0 || !token_sees(p, w.b, token_of(p, c0 + q), u)) continue;

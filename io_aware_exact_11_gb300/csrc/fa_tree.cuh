@@ -257,6 +257,163 @@ struct TreeWalk {
   }
 };
 
+// Loads the tiles of a part into a ring, by one warp: K's, or V's and with them both scales' bytes (E4M3).  A page of one
+// head is one TMA box; full and empty are the ring's barriers, sc_full those of the scale bytes' own ring, which is longer:
+// the slot that V goes to is free, so the tile `ring` before it has been widened, and the scale bytes of the ones before
+// that have been read.
+template <int D, bool FP8, int kScaleRing>
+__device__ __forceinline__ void load_pages(const TreeParams& p, const TreePart& my, bool is_v, uint8_t* dst, int ring,
+                                           uint64_t* full, uint64_t* empty, uint64_t* sc_full, uint8_t* k_scale,
+                                           uint8_t* v_scale, volatile int* abort_flag, unsigned int site) {
+  constexpr bool kPg5 = !FP8 && D == 128;  // pages as [row group][half][8 rows][128 bytes]
+  constexpr int kSlot = kTreeBN * D * (FP8 ? 1 : 2);
+  const int lane = threadIdx.x & 31;
+  const int bshift = 31 - __clz(p.block_size);  // a power of two
+  const CUtensorMap* tm = is_v ? &p.tm_v : &p.tm_k;
+  dst += lane * p.block_size * (kSlot / kTreeBN);
+  if (lane == 0) tma_prefetch_desc(tm);
+  const int npt = kTreeBN >> bshift;  // pages per tile
+  int slot = 0, sc = 0, issued = 0;
+  uint32_t parity = 1;
+  bool ok = true;
+  TreeWalk w;
+  w.begin(p, my);
+  do {
+    const int pages = (w.len + p.block_size - 1) >> bshift;
+    const int32_t* table = p.block_table + static_cast<int64_t>(w.b) * p.max_blocks;
+    // The ids of 32 pages at a time, one per lane, loaded one group ahead and checked when they are due.
+    int page = w.t0 * npt + lane;
+    int id = 0, ahead = page < pages ? table[page] : 0;
+    int at = 32;  // the tile's first page in the group
+#pragma unroll 1
+    for (int i = w.t0; i < w.t1; ++i) {
+      if (at == 32) {
+        at = 0;
+        id = page < pages ? ahead : -1;  // −1: past the end
+        if (page < pages && (id < 0 || id >= p.num_blocks)) {
+          report_bad_page(p);
+          id = 0;
+        }
+        page += 32;
+        ahead = page < pages ? table[page] : 0;
+      }
+      const int blk = __shfl_sync(0xffffffffu, id, at + lane);
+      at += npt;
+      ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, site));
+      if (!ok) break;
+      const bool real = lane < npt && blk >= 0;
+      const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[slot], kSlot);
+        if (FP8 && is_v) mbar_arrive_expect_tx(&sc_full[sc], 2 * n_real * p.block_size);
+      }
+      __syncwarp();
+      if (lane < npt) {
+        const int row = real ? 0 : p.block_size;  // a row past the page: TMA fills the box with zeros
+        const int head = (real ? blk : 0) * p.Hkv + w.h;
+        if constexpr (kPg5)
+          tma_load_5d(dst + slot * kSlot, tm, &full[slot], 0, 0, 0, row >> 3, head);
+        else
+          tma_load_4d(dst + slot * kSlot, tm, &full[slot], 0, row, w.h, real ? blk : 0);
+        if (FP8 && is_v && real) {
+          const int64_t from = static_cast<int64_t>(head) << bshift;
+          const int to = sc * kTreeBN + (lane << bshift);
+          bulk_load(k_scale + to, p.k_scale + from, p.block_size, &sc_full[sc]);
+          bulk_load(v_scale + to, p.v_scale + from, p.block_size, &sc_full[sc]);
+        }
+      }
+      ++issued;
+      sc = (sc + 1) % kScaleRing;
+      if (++slot == ring) {
+        slot = 0;
+        parity ^= 1u;
+      }
+    }
+  } while (ok && w.next(p));
+  // The copies in flight land before the CTA ends, also where a wait of another warp fails after this one is done.
+  if (lane == 0) {
+#pragma unroll 1
+    for (int n = max(0, issued - ring); n < issued; ++n) {
+      mbar_wait_drain_inl(&full[n % ring], (n / ring) & 1, kTreeDrainNs);
+      if (FP8 && is_v) mbar_wait_drain_inl(&sc_full[n % kScaleRing], (n / kScaleRing) & 1, kTreeDrainNs);
+    }
+  }
+}
+
+// Eight elements of a query row, whose other ones the neighbouring kChunks − 1 lanes hold, as E4M3 terms
+// x·2⁻ᵃ = hi + lo·2^−kLow; 2⁻ᵃ, which is returned as a, brings the row's largest magnitude to at most 448.
+template <int kChunks, int kLow>
+__device__ __forceinline__ int split_q8(uint4 v, uint2& hi, uint2& lo) {
+  const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+  float x[8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = __uint_as_float(e & 1 ? w4[e >> 1] & 0xffff0000u : w4[e >> 1] << 16);
+    const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
+    if (a < 0x7f800000u) top = max(top, a);
+    else x[e] = __uint_as_float(0x7fffffffu);
+  }
+#pragma unroll
+  for (int mk = kChunks / 2; mk > 0; mk >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, mk));
+  const int a = max(-126, static_cast<int>(top >> 23) - 135 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+  constexpr float kUp = 1 << kLow;
+  uint32_t h2[2] = {0, 0}, l2[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float y0 = x[e] * inv, y1 = x[e + 1] * inv;
+    const uint32_t h = pack_e4m3x2(y0, y1);
+    const uint32_t back = e4m3x2_to_f16x2(h);
+    const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&back));
+    h2[e >> 2] |= h << ((e & 2) * 8);
+    l2[e >> 2] |= pack_e4m3x2((y0 - z.x) * kUp, (y1 - z.y) * kUp) << ((e & 2) * 8);
+  }
+  hi = make_uint2(h2[0], h2[1]);
+  lo = make_uint2(l2[0], l2[1]);
+  return a;
+}
+
+// Takes what is not finite out of a drafted key's bf16 value row where it lies (in pieces of 128 bytes), and says whether
+// there was any; a row past the end becomes zeros.
+template <int D>
+__device__ __forceinline__ bool clean_value_row(uint8_t* row, bool past_end) {
+  bool bad = false;
+#pragma unroll 2
+  for (int ch = 0; ch < D / 8; ++ch) {
+    uint4* at = reinterpret_cast<uint4*>(row + (ch >> 3) * 1024 + (ch & 7) * 16);
+    uint32_t v4[4] = {0, 0, 0, 0};
+    if (!past_end) {
+      const uint4 v = *at;
+      v4[0] = v.x, v4[1] = v.y, v4[2] = v.z, v4[3] = v.w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((v4[e] & 0x7f80u) == 0x7f80u) v4[e] &= 0xffff0000u, bad = true;
+        if ((v4[e] & 0x7f800000u) == 0x7f800000u) v4[e] &= 0xffffu, bad = true;
+      }
+    }
+    *at = make_uint4(v4[0], v4[1], v4[2], v4[3]);
+  }
+  return bad;
+}
+
+// Where drafted key u's value row of the walk's pair lies in the cache, for what was taken out of it: to be added to the
+// rows that see it (a page id that is none was read as page 0).
+template <int D>
+__device__ __forceinline__ int64_t value_row(const TreeParams& p, const TreeWalk& w, int u) {
+  const int bshift = 31 - __clz(p.block_size), key = w.len - w.drafts + u;
+  int blk = p.block_table[static_cast<int64_t>(w.b) * p.max_blocks + (key >> bshift)];
+  if (blk < 0 || blk >= p.num_blocks) blk = 0;
+  return (((static_cast<int64_t>(blk) * p.Hkv + w.h) << bshift) + (key & (p.block_size - 1))) * D;
+}
+// The element there if it is not finite, else 0.
+template <bool FP8>
+__device__ __forceinline__ float taken_out(const TreeParams& p, int64_t at) {
+  if (FP8) return (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
+  const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
+  return fabsf(v) <= 3.4028234663852886e38f ? 0.f : v;
+}
+
 // True on one lane of a converged warp.
 __device__ __forceinline__ bool elect_one_lane() {
   uint32_t pred = 0;
