@@ -393,7 +393,15 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   under a weight below 2^-126 of the row's largest).  Weights enter
  *   the second product as bf16 (off by 2^-8 of themselves or less), or with an
  *   E4M3 cache as fp16 (2^-11, and below 2^-17 of the row's largest weight up to
- *   2^-28 of that).
+ *   2^-28 of that).  Exponentials are fp32: weights below 2^-126 of the row's
+ *   largest are zero.  E4M3 cache: value rows of at most 448·2^-126 may count as
+ *   zero beside larger ones, and with more than 32 rows T·H_q/H_kv the scores of
+ *   keys above 2^110 may overflow.
+ *   One token over a bf16 cache is fa_decode_paged's case too.  Measured on GB300,
+ *   d = 64 and 128, batches of 1 to 64: where query heads share keys, that call takes
+ *   0.65 to 1.0 of this one's time up to 100 MB of keys and values, and 0.9 to 1.8
+ *   beyond (most with ragged lengths and 16-key pages); with one query head per
+ *   key/value head the two are within 17 % of each other.
  *   q, o [B,H_q,T,d] bf16; strides NULL or 6 element strides {q_b, q_h, q_t, o_…},
  *   multiples of 8, >= 0 (o must not overlap itself, and may be q only with q's
  *   strides); lse [B,H_q,T] float32 or NULL.

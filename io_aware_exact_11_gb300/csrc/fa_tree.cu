@@ -57,12 +57,12 @@
 // non-finite elements of drafted rows are zeroed there too, and added to the
 // rows that do see them at the end.
 //
-// Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements:
-//   4 / 16 / 32 rows, bf16   93 / 93 / 95 us   5.75 TB/s, 0.86 of a device copy: bound by device memory
-//   4 / 16 / 32 rows, E4M3   60 / 61 / 72 us   4.5 / 4.4 / 3.8 TB/s: inside a piece 4 and 16 rows run at the memory's
+// Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements (replaying a graph over two caches):
+//   4 / 16 / 32 rows, bf16   88 / 90 / 92 us   6.1 / 6.0 / 5.8 TB/s, 0.91 of a device copy: bound by device memory
+//   4 / 16 / 32 rows, E4M3   55 / 56 / 66 us   4.9 / 4.8 / 4.1 TB/s: inside a piece 4 and 16 rows run at the memory's
 //                            rate; start, piece ends and the joining kernel take 15 us, and with 32 rows the softmax
 //                            warps, which also widen V, are the bound
-// E4M3, not kept: four or eight converter warps beside the softmax warps (64 and 67 us at 4 rows, 82 and 83 at 32);
+// E4M3, not kept: four or eight converter warps beside the softmax warps (7 and 12 % more at 4 rows, 15 % at 32);
 // V widened by integer operations instead of the conversion instruction (slower, and it loses NaN); P̃ as two E4M3
 // terms over V as it is (the terms span too few binades).
 #include <stddef.h>
@@ -927,8 +927,8 @@ template <int D, bool FP8>
 cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
   // By the rows of a pair; 8 sequences of 16384 keys, 8 key/value heads, us with the one and the other:
-  //   4 and 16 rows as 16 columns or 32    E4M3 59, 60 | 65, 68    bf16 92, 93 | 93, 93
-  //   16 and 32 rows here or in the kernel for many rows    E4M3 60, 72 | 77, 80    bf16 93, 95 | 98, 100
+  //   4 and 16 rows as 16 columns or 32    E4M3 55, 56 | 60, 62    bf16 89, 90 | 88, 90 (head dim 64 51, 52 | 54, 55)
+  //   16 and 32 rows here or in the kernel for many rows    E4M3 56, 66 | 72, 74    bf16 90, 92 | 93, 95
   // (32 rows are the most that fit here without tiles of rows; 64 columns spilled registers and took 81 us where the
   // other kernel took 69: 8 tokens of 7 heads a group, 16 ragged sequences of up to 8192 bf16 keys.)
   const bool wide = rows > kTreeNarrowRows;

@@ -7,8 +7,8 @@
 // read from there by O += P̃ V.  Per 128 × 128 scores that reads 96 KB of shared
 // memory against 160 KB (and 32 KB of P̃ stored) in the transposed products of the
 // kernel for few rows, and a row's maximum needs no other thread: with tiles of 64
-// and 128 rows that one took 445 us where this one takes 239 (8 sequences of 32768
-// E4M3 keys, 8 key/value heads, 256 rows each).
+// and 128 rows that one took 445 us where this one took 239 (8 sequences of 32768
+// E4M3 keys, 8 key/value heads, 256 rows each; 243 now).
 //
 // Two streams (warpgroups): with up to 128 rows they share them and take alternate
 // key tiles, joined at the end of a piece (TILES = 1); above, a CTA takes two tiles
@@ -28,9 +28,9 @@
 //
 // The rest (parts, pieces, masks, values in masked places) is as in fa_tree.cu.
 //
-// Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements:
-//   64 / 128 / 256 rows, bf16   102 / 108 / 130 us   0.79 / 0.75 of a device copy, 1056 TFLOP/s
-//   64 / 128 / 256 rows, E4M3    83 /  87 / 142 us   417 / 791 / 967 TFLOP/s
+// Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements (replaying a graph over two caches):
+//   64 / 128 / 256 rows, bf16    98 / 104 / 125 us   0.82 / 0.77 of a device copy, 1100 TFLOP/s
+//   64 / 128 / 256 rows, E4M3    76 /  84 / 140 us   452 / 818 / 982 TFLOP/s
 // With two row tiles a step (one tile's P̃V and S, 1024 tensor cycles) takes about 1750 cycles: the issuing
 // warp's own instructions, of which it gets one through every dozen cycles beside the softmax warps, and the wait
 // for P̃ (S to P̃ is a chain of about 1400 cycles).  E4M3 with shared rows waits for the converters (2400 cycles a
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           if (widen_row_far<D>(src, dst, r, e, key >= context, key >= w.len))
             atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
         } else if ((i + 1) * kBN <= context) {
-          // Two chunks at a time (64, 128 and 256 rows 83, 87, 142 us; four: 85, 89, 143; one: 87, 92, 143).
+          // Two chunks at a time (64, 128 and 256 rows 76, 84, 139 us; four: 79, 86, 140; one: 81, 89, 141).
 #pragma unroll 1
           for (int c4 = 0; c4 < D / 16; c4 += 2) {
             uint4 v[2];
@@ -804,7 +804,7 @@ cudaError_t launch(const TreeParams& p, cudaStream_t s) {
 }
 
 // Two row tiles share a CTA's keys where there are more than 128 rows.  Below, the second would be empty: 64 and 128
-// rows with shared rows or with two tiles, E4M3 84, 88 | 120, 124 us, bf16 102, 108 | 108, 115 us (8 x 16384 keys).
+// rows with shared rows or with two tiles, E4M3 76, 84 | 114, 121 us, bf16 98, 103 | 103, 109 us (8 x 16384 keys).
 template <int D, bool FP8>
 cudaError_t launch_tiles(const TreeParams& p, cudaStream_t s) {
   return p.T * p.G <= kRowTile ? launch<D, FP8, 1>(p, s) : launch<D, FP8, 2>(p, s);
