@@ -320,7 +320,7 @@ FA_API fa_status fa_backward_masked(const void* q, const void* k, const void* v,
  *   element's is needed (16-byte alignment throughout is faster).
  *   positions: device int32, entry b·pos_stride_b + n (pos_stride_b = 0 shares
  *   one row among the batch), or NULL for n; position0 is added.  Any int32
- *   position is exact: angles are reduced in 64-bit fixed point (off by 2^-34 turns).
+ *   position is exact: angles are reduced in 64-bit fixed point, to 2^-31 turns.
  *   inv_freq: d_rot/2 float64 values below 2^64 on the HOST, read during the call;
  *   scaled contexts are scaled frequencies and a magnitude μ other than 1.
  *   Supported: even d <= 256, even d_rot <= d.
@@ -389,8 +389,8 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   row that sees no key, padding rows t >= m_b among them, gives O = 0 and
  *   LSE = −∞.  Keys a row does not see do not reach its results, whatever they
  *   hold; slots past a sequence's end are not read into results.  An infinite
- *   value of a bf16 cache is infinite in the results of the rows that see it (NaN
- *   under a weight below 2^-126 of the row's largest).  Weights enter
+ *   value of a bf16 cache is infinite in the results of the rows that see it (NaN,
+ *   or left out, under a weight below 2^-126 of the row's largest).  Weights enter
  *   the second product as bf16 (off by 2^-8 of themselves or less), or with an
  *   E4M3 cache as fp16 (2^-11, and below 2^-17 of the row's largest weight up to
  *   2^-28 of that).  Exponentials are fp32: weights below 2^-126 of the row's
@@ -433,6 +433,8 @@ FA_API fa_status fa_decode_tree(const void* q, const void* k_cache, const void* 
  *   one has given up on a bounded pipeline wait, then FA_ERR_INVALID_ARG if one
  *   has met a page id, length or position outside its range; the first of each
  *   kind, one per call (and clears it).  FA_ERR_CUDA on a CUDA error, else FA_OK.
+ *   While a timeout stands unread, pipeline waits of later calls on the device give
+ *   up early, and their results are not to be used.
  */
 FA_API fa_status fa_device_status(void* stream);
 
