@@ -59,8 +59,8 @@ typedef enum fa_status {
   FA_ERR_DEVICE_TIMEOUT = 4
 } fa_status;
 
-/* FA_E4M3 is a storage type of the paged cache only (fa_cache_append, fa_cache_gather, fa_decode_tree). */
-typedef enum fa_dtype { FA_BF16 = 0, FA_FP32 = 1, FA_E4M3 = 2 } fa_dtype;
+/* FA_E4M3 and FA_E2M1 (four bits) are storage types of the paged cache only (fa_cache_*, fa_decode_tree). */
+typedef enum fa_dtype { FA_BF16 = 0, FA_FP32 = 1, FA_E4M3 = 2, FA_E2M1 = 3 } fa_dtype;
 
 /* Which elements of a head's rotated part form a pair: (i, i + d_rot/2) or (2i, 2i + 1). */
 typedef enum fa_rope_layout { FA_ROPE_HALF = 0, FA_ROPE_INTERLEAVED = 1 } fa_rope_layout;
@@ -331,6 +331,21 @@ FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out,
                          fa_rope_layout layout, int inverse, void* stream);
 
 /*
+ * fa_rope_axes — fa_rope with a position on each of several axes per token
+ *   (time, height and width of an image's or a video's patch).
+ *   Pair i turns by θ = p_a·w_i with a = axes[i] and p_a = positions[a·pos_stride_a
+ *   + b·pos_stride_b + n] (device int32; strides >= 0).  axes: d_rot/2 whole
+ *   numbers in [0, n_axes) on the HOST, read during the call: blocks of pairs for
+ *   each axis, or the axes in turn.  Everything else as for fa_rope, the gradient
+ *   (inverse = 1) and in place included.
+ *   Supported: n_axes <= 4, even d <= 256, even d_rot <= d.
+ */
+FA_API fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k, int N,
+                              int d, int d_rot, fa_dtype dtype, const int64_t* strides, const int32_t* positions,
+                              int n_axes, int64_t pos_stride_a, int64_t pos_stride_b, const int32_t* axes,
+                              const double* inv_freq, float magnitude, fa_rope_layout layout, int inverse, void* stream);
+
+/*
  * fa_cache_append — writes new keys and values into a paged cache.
  *   k, v: bf16 [B,H_kv,N,d]; k_cache, v_cache, block_table as for
  *   fa_decode_paged.  Token n of sequence b goes to logical position start[b] + n
@@ -341,6 +356,14 @@ FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out,
  *   k_scale, v_scale [num_blocks, H_kv, block_size], with k >= −126 the smallest
  *   whole number for which the row's largest finite magnitude is <= 448·2^k.
  *   Infinities and NaN become NaN codes.  k_scale and v_scale are ignored for FA_BF16.
+ *   FA_E2M1 quantises groups of 32 neighbouring elements: codes c = rn(x·2^−k) of
+ *   four bits (sign, two bits of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4,
+ *   6), element 2i in the low and 2i + 1 in the high half of byte i of k_cache,
+ *   v_cache [num_blocks, H_kv, block_size, d/2], and the byte k + 127 in k_scale,
+ *   v_scale [num_blocks, H_kv, block_size, d/32], with k in [−126, 125] the smallest
+ *   whole number for which the group's largest magnitude is <= 6·2^k (beyond
+ *   6·2^125 codes saturate).  A group that holds an infinity or NaN gets the byte
+ *   255 and reads as NaN.
  *   strides: NULL for contiguous k, v, or 6 element strides {k_b, k_h, k_n, v_…},
  *   multiples of 8, >= 0 (those of dimensions of size 1 do not matter).  Two
  *   tokens must not name the same slot in one call.
@@ -359,7 +382,7 @@ FA_API fa_status fa_cache_append(const void* k, const void* v, void* k_cache, vo
  *   as bf16 rows, e.g. for fa_forward over a cached prefix.
  *   Arguments as for fa_cache_append, k and v [B,H_kv,N,d] being written; rows
  *   n >= seq_lens[b] are set to zero.  E4M3 codes are multiplied by their row's
- *   power of two, which is exact.  seq_lens outside [0, max_blocks·block_size]
+ *   power of two and E2M1 codes by their group's, which is exact.  seq_lens outside [0, max_blocks·block_size]
  *   and bad page ids give zero rows and FA_ERR_INVALID_ARG from fa_device_status.
  *   k and v must not overlap themselves or each other.
  */
@@ -367,6 +390,90 @@ FA_API fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const
                                  const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* k,
                                  void* v, int B, int H_kv, int N, int num_blocks, int block_size, int max_blocks,
                                  int d, fa_dtype cache_dtype, const int64_t* strides, void* stream);
+
+/*
+ * fa_cache_compact — moves the kept rows of every sequence together, in place:
+ *   the accepted ones of drafted tokens, or what is left of a long sequence.
+ *   The row (key, value and scales) at position keep[b·keep_stride_b + i] of
+ *   sequence b goes to position first[b] + i, for i < keep_lens[b] (device int32
+ *   [B], NULL for N).  keep[…i] >= first[b] + i is required, in any order: then no
+ *   row is overwritten before it has been read.  Rows behind the moved ones keep
+ *   what they held.  Caches, scales and block_table as for fa_cache_append; pages
+ *   that are written must belong to one sequence alone.
+ *   Positions that break the rule or lie outside the table, and bad page ids, are
+ *   caught on the device: those rows are not moved; with first, keep_lens out of
+ *   range none of the sequence's is.  fa_device_status then reports FA_ERR_INVALID_ARG.
+ */
+FA_API fa_status fa_cache_compact(void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                  const int32_t* block_table, const int32_t* first, const int32_t* keep,
+                                  int64_t keep_stride_b, const int32_t* keep_lens, int B, int H_kv, int N,
+                                  int num_blocks, int block_size, int max_blocks, int d, fa_dtype cache_dtype,
+                                  void* stream);
+
+/*
+ * fa_cache_copy_pages — copies page src[i] to page dst[i] for i < n (device int32),
+ *   all heads, keys, values and scales; −1 in both is skipped.  No page may be
+ *   written twice in one call, or written and read.  Bad page ids are caught on the
+ *   device (nothing is copied for them) and reported as FA_ERR_INVALID_ARG.
+ *   Supported: n <= 65535.
+ */
+FA_API fa_status fa_cache_copy_pages(void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                     const int32_t* src, const int32_t* dst, int n, int H_kv, int num_blocks,
+                                     int block_size, int d, fa_dtype cache_dtype, void* stream);
+
+/*
+ * Pages shared among sequences.  Three device arrays describe a pool, and the
+ * calls below change them in place, so that a serving loop needs no host copy:
+ *   block_table [B, max_blocks] int32: page ids, −1 where a sequence has none;
+ *   seq_lens    [B] int32: tokens of each sequence;
+ *   holders     [num_blocks] int32: sequences whose table names the page, 0: free.
+ * The results are those of one sequence after the other in the order given,
+ * bit for bit.  The calls are to be ordered on one stream, as the cache's are.
+ *
+ * fa_pages_fork — sequence dst[i] (i < n), which is empty, takes the pages and the
+ *   length of sequence src[i]; each page has one holder more.  Nothing is copied.
+ *   Not a row of the table, a dst that is not empty or named before, and a src
+ *   that is also named in dst are caught on the device: that pair is left out.
+ */
+FA_API fa_status fa_pages_fork(int32_t* block_table, int32_t* seq_lens, int32_t* holders, const int32_t* src,
+                               const int32_t* dst, int n, int B, int num_blocks, int block_size, int max_blocks,
+                               void* stream);
+
+/*
+ * fa_pages_free — sequences seqs[i] (i < n) give up their pages, reserved ones
+ *   included, behind the first keep_lens[i] tokens (keep_lens NULL: all).  Entries
+ *   become −1, lengths min(seq_lens, keep_lens); pages without holders are free.
+ *   Not a row of the table, a sequence named before and a negative keep_lens[i] are
+ *   caught on the device (left out), and so is a page that nobody was said to hold.
+ */
+FA_API fa_status fa_pages_free(int32_t* block_table, int32_t* seq_lens, int32_t* holders, const int32_t* seqs,
+                               const int32_t* keep_lens, int n, int B, int num_blocks, int block_size, int max_blocks,
+                               void* stream);
+
+/* fa_pages_reserve_workspace_size — bytes of workspace fa_pages_reserve needs (0 for non-positive sizes). */
+FA_API size_t fa_pages_reserve_workspace_size(int B, int num_blocks);
+
+/*
+ * fa_pages_reserve — pages for the next new_lens[b] tokens of every sequence of the
+ *   table (device int32 [B]; 0: none).  Entries of the table that are missing get free
+ *   pages; entries reserved before stay.  If the next token goes into a page that
+ *   others hold too, the sequence gets one of its own in its place, and
+ *   copy_src[b], copy_dst[b] name the old and the new page (both −1 otherwise), to be
+ *   copied with fa_cache_copy_pages before anything is written: of sequences
+ *   that write into one page all but the last to hold it get a copy.
+ *   Sequences are served in order, free pages handed out by rising number.  From the
+ *   first sequence that finds too few on, none with tokens to come is served:
+ *   granted[b] = 0 and its entries stay as they were; else granted[b] = 1.  A length
+ *   that cannot be or that the table has no room for, and a bad page id under the next
+ *   token, are caught on the device: granted[b] = 0, the others are served.
+ *   seq_lens stay as they are.  workspace: fa_pages_reserve_workspace_size() bytes,
+ *   4-byte aligned, contents on entry do not matter.
+ *   Supported: B <= 4096, B·(max_blocks + 1) < 2^31.
+ */
+FA_API fa_status fa_pages_reserve(int32_t* block_table, const int32_t* seq_lens, int32_t* holders,
+                                  const int32_t* new_lens, int32_t* granted, int32_t* copy_src, int32_t* copy_dst,
+                                  int B, int num_blocks, int block_size, int max_blocks, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * fa_decode_tree_workspace_size — bytes of workspace with which fa_decode_tree
@@ -379,7 +486,7 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
 
 /*
  * fa_decode_tree — attention of T drafted tokens per sequence over a paged
- *   cache (T = 1 is plain decode), grouped query heads, bf16 or E4M3 cache.
+ *   cache (T = 1 is plain decode), grouped query heads, bf16, E4M3 or E2M1 cache.
  *   The drafted tokens' keys and values are in the cache already
  *   (fa_cache_append): sequence b holds seq_lens[b] keys, of which the last
  *   m_b = draft_lens[b] (device int32 [B], NULL for T) belong to its drafted
@@ -396,7 +503,8 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   2^-28 of that).  Exponentials are fp32: weights below 2^-126 of the row's
  *   largest are zero.  E4M3 cache: value rows of at most 448·2^-126 may count as
  *   zero beside larger ones, and with more than 32 rows T·H_q/H_kv the scores of
- *   keys above 2^110 may overflow.
+ *   keys above 2^110 may overflow.  E2M1 cache: codes times their power of two are exact in
+ *   bf16, and everything is as for a bf16 cache; a NaN group is NaN for the rows that see it.
  *   One token over a bf16 cache is fa_decode_paged's case too.  Measured on GB300,
  *   d = 64 and 128, batches of 1 to 64: where query heads share keys, that call takes
  *   0.65 to 1.0 of this one's time up to 100 MB of keys and values, and 0.9 to 1.8

@@ -989,9 +989,9 @@ fa_status check_cache(const char* who, const void* k_cache, const void* v_cache,
   if (!k_cache || !v_cache || !block_table) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
   if (B <= 0 || H_kv <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks <= 0 || d <= 0)
     return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
-  if (dtype != FA_BF16 && dtype != FA_FP32 && dtype != FA_E4M3)
+  if (dtype != FA_BF16 && dtype != FA_FP32 && dtype != FA_E4M3 && dtype != FA_E2M1)
     return fail(FA_ERR_INVALID_ARG, "%s: unknown cache dtype %d", who, static_cast<int>(dtype));
-  if (dtype == FA_FP32) return fail(FA_ERR_UNSUPPORTED, "%s: only bf16 and E4M3 caches are built", who);
+  if (dtype == FA_FP32) return fail(FA_ERR_UNSUPPORTED, "%s: only bf16, E4M3 and E2M1 caches are built", who);
   if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "%s: head dim %d not built (64, 128)", who, d);
   if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
     return fail(FA_ERR_UNSUPPORTED, "%s: block_size must be 16, 32, 64 or 128 (got %d)", who, block_size);
@@ -1000,13 +1000,18 @@ fa_status check_cache(const char* who, const void* k_cache, const void* v_cache,
     return fail(FA_ERR_UNSUPPORTED, "%s: max_blocks * block_size too large", who);
   if (static_cast<int64_t>(num_blocks) * H_kv > INT32_MAX)
     return fail(FA_ERR_UNSUPPORTED, "%s: num_blocks * H_kv too large", who);
-  if (dtype == FA_E4M3 && (!k_scale || !v_scale))
-    return fail(FA_ERR_INVALID_ARG, "%s: an E4M3 cache needs k_scale and v_scale", who);
+  if (dtype != FA_BF16 && (!k_scale || !v_scale))
+    return fail(FA_ERR_INVALID_ARG, "%s: an E4M3 or E2M1 cache needs k_scale and v_scale", who);
   if (!aligned16(k_cache) || !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(block_table) & 3u))
     return fail(FA_ERR_INVALID_ARG, "%s: caches must be 16-byte aligned (block_table 4-byte)", who);
-  if (dtype == FA_E4M3 && (!aligned16(k_scale) || !aligned16(v_scale)))
+  if (dtype != FA_BF16 && (!aligned16(k_scale) || !aligned16(v_scale)))
     return fail(FA_ERR_INVALID_ARG, "%s: k_scale and v_scale must be 16-byte aligned", who);
   return FA_OK;
+}
+
+// The kernels' name of a cache dtype that check_cache has passed.
+int cache_format(fa_dtype dtype) {
+  return dtype == FA_E4M3 ? fa::kCacheE4m3 : dtype == FA_E2M1 ? fa::kCacheE2m1 : fa::kCacheBf16;
 }
 
 // Tokens that the cache kernels can count, and a grid hold.
@@ -1065,35 +1070,33 @@ int64_t tree_parts(int64_t rows, int max_parts, int64_t tiles) {
 
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
-}  // namespace
-
-extern "C" {
-
-fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k, int N, int d,
-                  int d_rot, fa_dtype dtype, const int64_t* strides, const int32_t* positions, int64_t pos_stride_b,
-                  int position0, const double* inv_freq, float magnitude, fa_rope_layout layout, int inverse,
-                  void* stream) {
-  if (!q || !q_out || !inv_freq || (H_k > 0 && (!k || !k_out))) return fail(FA_ERR_INVALID_ARG, "fa_rope: null pointer");
+// fa_rope, and fa_rope_axes where there are axes (n_axes > 0).
+fa_status rope_impl(const char* who, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k,
+                    int N, int d, int d_rot, fa_dtype dtype, const int64_t* strides, const int32_t* positions, int n_axes,
+                    int64_t pos_stride_a, int64_t pos_stride_b, int position0, const int32_t* axes,
+                    const double* inv_freq, float magnitude, fa_rope_layout layout, int inverse, void* stream) {
+  if (!q || !q_out || !inv_freq || (H_k > 0 && (!k || !k_out))) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
   if (B <= 0 || H_q <= 0 || H_k < 0 || N <= 0 || d <= 0 || d_rot <= 0)
-    return fail(FA_ERR_INVALID_ARG, "fa_rope: sizes must be positive (B=%d H_q=%d H_k=%d N=%d d=%d d_rot=%d)", B, H_q,
+    return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive (B=%d H_q=%d H_k=%d N=%d d=%d d_rot=%d)", who, B, H_q,
                 H_k, N, d, d_rot);
-  if (dtype != FA_BF16 && dtype != FA_FP32) return fail(FA_ERR_INVALID_ARG, "fa_rope: unknown dtype %d", dtype);
-  if (d % 2 != 0 || d > 256) return fail(FA_ERR_UNSUPPORTED, "fa_rope: head dim %d not built (even, <= 256)", d);
+  if (dtype != FA_BF16 && dtype != FA_FP32) return fail(FA_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
+  if (d % 2 != 0 || d > 256) return fail(FA_ERR_UNSUPPORTED, "%s: head dim %d not built (even, <= 256)", who, d);
   if (d_rot % 2 != 0 || d_rot > d)
-    return fail(FA_ERR_INVALID_ARG, "fa_rope: d_rot must be even and <= d (got %d of %d)", d_rot, d);
+    return fail(FA_ERR_INVALID_ARG, "%s: d_rot must be even and <= d (got %d of %d)", who, d_rot, d);
   if (layout != FA_ROPE_HALF && layout != FA_ROPE_INTERLEAVED)
-    return fail(FA_ERR_INVALID_ARG, "fa_rope: unknown layout %d", static_cast<int>(layout));
-  if (inverse != 0 && inverse != 1) return fail(FA_ERR_INVALID_ARG, "fa_rope: inverse must be 0 or 1");
+    return fail(FA_ERR_INVALID_ARG, "%s: unknown layout %d", who, static_cast<int>(layout));
+  if (inverse != 0 && inverse != 1) return fail(FA_ERR_INVALID_ARG, "%s: inverse must be 0 or 1", who);
   if (!(std::isfinite(magnitude) && magnitude > 0.f))
-    return fail(FA_ERR_INVALID_ARG, "fa_rope: magnitude must be finite and > 0");
+    return fail(FA_ERR_INVALID_ARG, "%s: magnitude must be finite and > 0", who);
   if (B > 65535 || H_q > 32767 || H_k > 32767)
-    return fail(FA_ERR_UNSUPPORTED, "fa_rope: B must be <= 65535, H_q and H_k <= 32767");
-  if (static_cast<int64_t>(B) * N > (1ll << 37) / d) return fail(FA_ERR_UNSUPPORTED, "fa_rope: B * N * d too large");
+    return fail(FA_ERR_UNSUPPORTED, "%s: B must be <= 65535, H_q and H_k <= 32767", who);
+  if (static_cast<int64_t>(B) * N > (1ll << 37) / d) return fail(FA_ERR_UNSUPPORTED, "%s: B * N * d too large", who);
   const uintptr_t esz = dtype == FA_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(q) % esz || reinterpret_cast<uintptr_t>(k) % esz ||
       reinterpret_cast<uintptr_t>(q_out) % esz || reinterpret_cast<uintptr_t>(k_out) % esz || misaligned4(positions))
-    return fail(FA_ERR_INVALID_ARG, "fa_rope: pointers must be aligned to their element");
-  if (positions && pos_stride_b < 0) return fail(FA_ERR_INVALID_ARG, "fa_rope: pos_stride_b must be >= 0");
+    return fail(FA_ERR_INVALID_ARG, "%s: pointers must be aligned to their element", who);
+  if (positions && (pos_stride_a < 0 || pos_stride_b < 0))
+    return fail(FA_ERR_INVALID_ARG, "%s: strides of positions must be >= 0", who);
   fa::RopeParams p;
   memset(&p, 0, sizeof(p));
   if (strides == nullptr) {
@@ -1104,7 +1107,7 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B,
   } else {
     for (int i = 0; i < 12; ++i)
       if (strides[i] < 0)
-        return fail(FA_ERR_INVALID_ARG, "fa_rope: stride[%d]=%lld must be >= 0", i, static_cast<long long>(strides[i]));
+        return fail(FA_ERR_INVALID_ARG, "%s: stride[%d]=%lld must be >= 0", who, i, static_cast<long long>(strides[i]));
     memcpy(p.sq, strides, sizeof(p.sq));
     memcpy(p.sqo, strides + 6, sizeof(p.sqo));
     if (H_k > 0) {
@@ -1113,15 +1116,15 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B,
     }
   }
   if (!rows_distinct(B, H_q, N, d, p.sqo) || (H_k > 0 && !rows_distinct(B, H_k, N, d, p.sko)))
-    return fail(FA_ERR_INVALID_ARG, "fa_rope: an output overlaps itself");
+    return fail(FA_ERR_INVALID_ARG, "%s: an output overlaps itself", who);
   if ((q == q_out && memcmp(p.sq, p.sqo, sizeof(p.sq)) != 0) ||
       (H_k > 0 && k == k_out && memcmp(p.sk, p.sko, sizeof(p.sk)) != 0))
-    return fail(FA_ERR_INVALID_ARG, "fa_rope: in place needs equal strides");
+    return fail(FA_ERR_INVALID_ARG, "%s: in place needs equal strides", who);
   const bool in_place = q == q_out && (H_k == 0 || k == k_out);
   for (int i = 0; i < d_rot / 2; ++i) {
-    if (!std::isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "fa_rope: inv_freq[%d] is not finite", i);
+    if (!std::isfinite(inv_freq[i])) return fail(FA_ERR_INVALID_ARG, "%s: inv_freq[%d] is not finite", who, i);
     if (std::fabs(inv_freq[i]) >= 18446744073709551616.0)
-      return fail(FA_ERR_UNSUPPORTED, "fa_rope: inv_freq[%d] must be below 2^64", i);
+      return fail(FA_ERR_UNSUPPORTED, "%s: inv_freq[%d] must be below 2^64", who, i);
     p.turns[i] = turn_fraction(inv_freq[i]);  // whole turns drop out: positions are whole
   }
   p.q = q;
@@ -1137,12 +1140,43 @@ fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B,
   p.d = d;
   p.rot = d_rot;
   p.position0 = position0;
+  p.n_axes = n_axes;
+  p.pos_stride_a = pos_stride_a;
+  for (int i = 0; n_axes > 0 && i < d_rot / 2; ++i) {
+    if (axes[i] < 0 || axes[i] >= n_axes)
+      return fail(FA_ERR_INVALID_ARG, "%s: axes[%d]=%d is not in [0, %d)", who, i, axes[i], n_axes);
+    p.axis[i] = static_cast<uint8_t>(axes[i]);
+  }
   p.magnitude = magnitude;
   p.sign = inverse ? -1.f : 1.f;
   cudaError_t e = fa::launch_rope(p, dtype == FA_FP32, layout == FA_ROPE_INTERLEAVED, in_place,
                                   static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "fa_rope launch");
-  return check_launch("fa_rope", 1);
+  if (e != cudaSuccess) return cuda_fail(e, who);
+  return check_launch(who, 1);
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k, int N, int d,
+                  int d_rot, fa_dtype dtype, const int64_t* strides, const int32_t* positions, int64_t pos_stride_b,
+                  int position0, const double* inv_freq, float magnitude, fa_rope_layout layout, int inverse,
+                  void* stream) {
+  return rope_impl("fa_rope", q, k, q_out, k_out, B, H_q, H_k, N, d, d_rot, dtype, strides, positions, 0, 0,
+                   pos_stride_b, position0, nullptr, inv_freq, magnitude, layout, inverse, stream);
+}
+
+fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_k, int N, int d,
+                       int d_rot, fa_dtype dtype, const int64_t* strides, const int32_t* positions, int n_axes,
+                       int64_t pos_stride_a, int64_t pos_stride_b, const int32_t* axes, const double* inv_freq,
+                       float magnitude, fa_rope_layout layout, int inverse, void* stream) {
+  if (!positions || !axes) return fail(FA_ERR_INVALID_ARG, "fa_rope_axes: null pointer");
+  if (n_axes <= 0) return fail(FA_ERR_INVALID_ARG, "fa_rope_axes: n_axes must be positive");
+  if (n_axes > fa::kRopeMaxAxes)
+    return fail(FA_ERR_UNSUPPORTED, "fa_rope_axes: at most %d axes (got %d)", fa::kRopeMaxAxes, n_axes);
+  return rope_impl("fa_rope_axes", q, k, q_out, k_out, B, H_q, H_k, N, d, d_rot, dtype, strides, positions, n_axes,
+                   pos_stride_a, pos_stride_b, 0, axes, inv_freq, magnitude, layout, inverse, stream);
 }
 
 fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, uint8_t* k_scale,
@@ -1176,7 +1210,7 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_c
   p.num_blocks = num_blocks;
   p.block_size = block_size;
   p.max_blocks = max_blocks;
-  cudaError_t e = fa::launch_cache_append(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_cache_append(p, d, cache_format(cache_dtype), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_cache_append launch");
   return check_launch(who, 1);
 }
@@ -1213,7 +1247,7 @@ fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_
   p.num_blocks = num_blocks;
   p.block_size = block_size;
   p.max_blocks = max_blocks;
-  cudaError_t e = fa::launch_cache_gather(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_cache_gather(p, d, cache_format(cache_dtype), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_cache_gather launch");
   return check_launch(who, 1);
 }
@@ -1299,7 +1333,7 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
   if (cache_dtype == FA_BF16 && d == 128) {  // one box per page of one head
     if ((r = make_page_map5(&p.tm_k, k_cache, num_blocks, H_kv, block_size, "k_cache")) != FA_OK) return r;
     if ((r = make_page_map5(&p.tm_v, v_cache, num_blocks, H_kv, block_size, "v_cache")) != FA_OK) return r;
-  } else {
+  } else if (cache_dtype != FA_E2M1) {  // (four bits are fetched without a map)
     const int64_t page = static_cast<int64_t>(block_size) * d;
     const bool fp8 = cache_dtype == FA_E4M3;
     if ((r = make_map(&p.tm_k, k_cache, num_blocks, H_kv, block_size, d, H_kv * page, page, d, "k_cache", block_size,
@@ -1309,9 +1343,197 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
                       fp8)) != FA_OK)
       return r;
   }
-  cudaError_t e = fa::launch_decode_tree(p, d, cache_dtype == FA_E4M3, static_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_decode_tree(p, d, cache_format(cache_dtype), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_decode_tree launch");
   return check_launch(who, 2);
+}
+
+}  // extern "C"
+
+// -------------------------------------------------- rows moved, pages copied, shared, freed and reserved
+
+namespace {
+
+// Checks shared by the calls on pages.
+fa_status check_pages(const char* who, const void* block_table, const void* seq_lens, const void* holders, int B,
+                      int num_blocks, int block_size, int max_blocks) {
+  if (!block_table || !seq_lens || !holders) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (B <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks <= 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
+    return fail(FA_ERR_UNSUPPORTED, "%s: block_size must be 16, 32, 64 or 128 (got %d)", who, block_size);
+  if (B > 65535) return fail(FA_ERR_UNSUPPORTED, "%s: B must be <= 65535", who);
+  if (static_cast<int64_t>(max_blocks) * block_size > (1 << 30))
+    return fail(FA_ERR_UNSUPPORTED, "%s: max_blocks * block_size too large", who);
+  if (misaligned4(block_table) || misaligned4(seq_lens) || misaligned4(holders))
+    return fail(FA_ERR_INVALID_ARG, "%s: pointers must be 4-byte aligned", who);
+  return FA_OK;
+}
+
+fa::PageParams page_params(int32_t* block_table, int32_t* seq_lens, int32_t* holders, int B, int num_blocks,
+                           int block_size, int max_blocks) {
+  fa::PageParams p;
+  memset(&p, 0, sizeof(p));
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.holders = holders;
+  p.B = B;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  return p;
+}
+
+fa::MoveParams move_params(void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int H_kv, int num_blocks,
+                           int block_size) {
+  fa::MoveParams p;
+  memset(&p, 0, sizeof(p));
+  p.cache[0] = static_cast<uint8_t*>(k_cache);
+  p.cache[1] = static_cast<uint8_t*>(v_cache);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.Hkv = H_kv;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  return p;
+}
+
+constexpr int kMaxReserved = 4096;  // sequences of one fa_pages_reserve
+
+size_t reserve_segments(int num_blocks) {
+  return (static_cast<size_t>(num_blocks) + fa::kPageSegment - 1) / fa::kPageSegment;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_cache_compact(void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, const int32_t* block_table,
+                           const int32_t* first, const int32_t* keep, int64_t keep_stride_b, const int32_t* keep_lens,
+                           int B, int H_kv, int N, int num_blocks, int block_size, int max_blocks, int d,
+                           fa_dtype cache_dtype, void* stream) {
+  const char* who = "fa_cache_compact";
+  if (!first || !keep) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, block_table, B, H_kv, num_blocks, block_size,
+                            max_blocks, d, cache_dtype);
+  if (r != FA_OK) return r;
+  if (N <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (misaligned4(first) || misaligned4(keep) || misaligned4(keep_lens))
+    return fail(FA_ERR_INVALID_ARG, "%s: first, keep and keep_lens must be 4-byte aligned", who);
+  if (keep_stride_b < 0) return fail(FA_ERR_INVALID_ARG, "%s: keep_stride_b must be >= 0", who);
+  if (static_cast<int64_t>(B) * H_kv > (1 << 27)) return fail(FA_ERR_UNSUPPORTED, "%s: B * H_kv too large", who);
+  fa::MoveParams p = move_params(k_cache, v_cache, k_scale, v_scale, H_kv, num_blocks, block_size);
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  p.block_table = block_table;
+  p.first = first;
+  p.keep = keep;
+  p.keep_sb = keep_stride_b;
+  p.keep_lens = keep_lens;
+  p.B = B;
+  p.N = N;
+  p.max_blocks = max_blocks;
+  cudaError_t e = fa::launch_cache_compact(p, d, cache_format(cache_dtype), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_cache_compact launch");
+  return check_launch(who, 1);
+}
+
+fa_status fa_cache_copy_pages(void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, const int32_t* src,
+                              const int32_t* dst, int n, int H_kv, int num_blocks, int block_size, int d,
+                              fa_dtype cache_dtype, void* stream) {
+  const char* who = "fa_cache_copy_pages";
+  if (!src || !dst) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_cache(who, k_cache, v_cache, k_scale, v_scale, src, 1, H_kv, num_blocks, block_size, 1, d,
+                            cache_dtype);
+  if (r != FA_OK) return r;
+  if (n <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (n > 65535) return fail(FA_ERR_UNSUPPORTED, "%s: at most 65535 pages a call (got %d)", who, n);
+  if (misaligned4(dst)) return fail(FA_ERR_INVALID_ARG, "%s: src and dst must be 4-byte aligned", who);
+  fa::MoveParams p = move_params(k_cache, v_cache, k_scale, v_scale, H_kv, num_blocks, block_size);
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  p.src = src;
+  p.dst = dst;
+  cudaError_t e = fa::launch_cache_copy(p, d, cache_format(cache_dtype), n, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_cache_copy_pages launch");
+  return check_launch(who, 1);
+}
+
+fa_status fa_pages_fork(int32_t* block_table, int32_t* seq_lens, int32_t* holders, const int32_t* src,
+                        const int32_t* dst, int n, int B, int num_blocks, int block_size, int max_blocks, void* stream) {
+  const char* who = "fa_pages_fork";
+  if (!src || !dst) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_pages(who, block_table, seq_lens, holders, B, num_blocks, block_size, max_blocks);
+  if (r != FA_OK) return r;
+  if (n <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (n > 65535) return fail(FA_ERR_UNSUPPORTED, "%s: at most 65535 sequences a call (got %d)", who, n);
+  if (misaligned4(src) || misaligned4(dst)) return fail(FA_ERR_INVALID_ARG, "%s: pointers must be 4-byte aligned", who);
+  fa::PageParams p = page_params(block_table, seq_lens, holders, B, num_blocks, block_size, max_blocks);
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  p.src = src;
+  p.dst = dst;
+  p.n = n;
+  cudaError_t e = fa::launch_pages_fork(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_pages_fork launch");
+  return check_launch(who, 1);
+}
+
+fa_status fa_pages_free(int32_t* block_table, int32_t* seq_lens, int32_t* holders, const int32_t* seqs,
+                        const int32_t* keep_lens, int n, int B, int num_blocks, int block_size, int max_blocks,
+                        void* stream) {
+  const char* who = "fa_pages_free";
+  if (!seqs) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_pages(who, block_table, seq_lens, holders, B, num_blocks, block_size, max_blocks);
+  if (r != FA_OK) return r;
+  if (n <= 0) return fail(FA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (n > 65535) return fail(FA_ERR_UNSUPPORTED, "%s: at most 65535 sequences a call (got %d)", who, n);
+  if (misaligned4(seqs) || misaligned4(keep_lens))
+    return fail(FA_ERR_INVALID_ARG, "%s: pointers must be 4-byte aligned", who);
+  fa::PageParams p = page_params(block_table, seq_lens, holders, B, num_blocks, block_size, max_blocks);
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  p.src = seqs;
+  p.lens = keep_lens;
+  p.n = n;
+  cudaError_t e = fa::launch_pages_free(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_pages_free launch");
+  return check_launch(who, 1);
+}
+
+size_t fa_pages_reserve_workspace_size(int B, int num_blocks) {
+  if (B <= 0 || num_blocks <= 0) return 0;
+  return round256((reserve_segments(num_blocks) + 3 * static_cast<size_t>(B) + 1) * 4);
+}
+
+fa_status fa_pages_reserve(int32_t* block_table, const int32_t* seq_lens, int32_t* holders, const int32_t* new_lens,
+                           int32_t* granted, int32_t* copy_src, int32_t* copy_dst, int B, int num_blocks,
+                           int block_size, int max_blocks, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "fa_pages_reserve";
+  if (!new_lens || !granted || !copy_src || !copy_dst || !workspace)
+    return fail(FA_ERR_INVALID_ARG, "%s: null pointer", who);
+  fa_status r = check_pages(who, block_table, seq_lens, holders, B, num_blocks, block_size, max_blocks);
+  if (r != FA_OK) return r;
+  if (B > kMaxReserved) return fail(FA_ERR_UNSUPPORTED, "%s: B must be <= %d", who, kMaxReserved);
+  if (static_cast<int64_t>(B) * (max_blocks + 1ll) > INT32_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "%s: B * max_blocks too large", who);
+  if (misaligned4(new_lens) || misaligned4(granted) || misaligned4(copy_src) || misaligned4(copy_dst) ||
+      misaligned4(workspace))
+    return fail(FA_ERR_INVALID_ARG, "%s: pointers must be 4-byte aligned", who);
+  const size_t need = fa_pages_reserve_workspace_size(B, num_blocks);
+  if (workspace_bytes < need)
+    return fail(FA_ERR_INVALID_ARG, "%s: workspace %zu bytes, need at least %zu", who, workspace_bytes, need);
+  fa::PageParams p =
+      page_params(block_table, const_cast<int32_t*>(seq_lens), holders, B, num_blocks, block_size, max_blocks);
+  if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
+  p.lens = new_lens;
+  p.granted = granted;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.total = static_cast<int*>(workspace);
+  p.seg = p.total + 1;
+  p.last = p.seg + reserve_segments(num_blocks);
+  p.from = p.last + B;
+  p.want = p.from + B;
+  cudaError_t e = fa::launch_pages_reserve(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_pages_reserve launch");
+  return check_launch(who, 3);
 }
 
 }  // extern "C"
@@ -1343,12 +1565,18 @@ fa_status fa_device_status(void* stream) {
   cudaMemcpy(word + which, &zero, sizeof(zero), cudaMemcpyHostToDevice);
   if (which == 1) {
     const bool page = (code & 0xFFu) == fa::kSiteBadBlock;
+    if ((code & 0xFFu) == fa::kSiteBadHolders)
+      return fail(FA_ERR_INVALID_ARG, "pages: a page was freed that nobody holds");
+    if ((code & 0xFFu) == fa::kSiteBadSequence)
+      return fail(FA_ERR_INVALID_ARG, "pages: a sequence is no row of the table, is named twice or is not empty");
     if ((code >> 8) == fa::kKernDecode)
       return fail(FA_ERR_INVALID_ARG, page ? "paged decode: a block-table entry is outside [0, num_blocks) (page 0 was read)"
                                            : "paged decode: a sequence length is outside [1, max_blocks * block_size]");
     return fail(FA_ERR_INVALID_ARG, page ? "%s: a block-table entry is outside [0, num_blocks)"
                                          : "%s: a length or position is outside its range",
-                (code >> 8) == fa::kKernTree ? "decode tree" : "paged cache");
+                (code >> 8) == fa::kKernTree    ? "decode tree"
+                : (code >> 8) == fa::kKernPages ? "pages"
+                                                : "paged cache");
   }
   return fail(FA_ERR_DEVICE_TIMEOUT, "kernel %u gave up waiting at site %u", code >> 8, code & 0xFFu);
 }

@@ -10,6 +10,11 @@
 // values within their binades.  Infinities and NaN do not count for the
 // maximum and become the NaN code.
 //
+// E2M1: a group of 32 elements of a row is held as 4-bit codes, two to a byte (the first in the low half), and one byte
+// k + 127 with the smallest k for which max|x_i| ≤ 6·2ᵏ, from −126 to 125 (6 is E2M1's largest value, and 6·2^125 the
+// largest one that bf16 holds; x beyond saturates).  The rounding to E2M1 is at most half a step, 2⁻² relative from 1 on.
+// The codes have no infinities and no NaN: a group that holds one gets the byte 255 and reads as NaN.
+//
 // Bound: device memory.  Writing: 2·(2d) bytes read and 2·(d + 1) written per
 // token and head (bf16: 2·2d); d/8 lanes hold one row, 16 bytes of it each, and
 // the row maximum is log2(d/8) lane exchanges, so a row never leaves registers.
@@ -97,6 +102,37 @@ __device__ __forceinline__ void quantise8(uint4 k, uint4 v, uint2& kc, uint2& vc
   vc = make_uint2(c[1][0] | (c[1][1] << 16), c[1][2] | (c[1][3] << 16));
 }
 
+// Quantises 8 elements of a key's row and 8 of its value's to E2M1; the group's others are with the three neighbours.
+// (Magnitudes order like their bits, so what is not finite shows in the maximum.)
+__device__ __forceinline__ void quantise8_e2m1(uint4 k, uint4 v, uint32_t& kc, uint32_t& vc, int& ks, int& vs) {
+  uint32_t w[2][4] = {{k.x, k.y, k.z, k.w}, {v.x, v.y, v.z, v.w}};
+  uint32_t t[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t m = 0x7fff7fffu;
+    t[j] = max2(max2(w[j][0] & m, w[j][1] & m), max2(w[j][2] & m, w[j][3] & m));
+  }
+  uint32_t top = __byte_perm(max2(t[0], t[0] >> 16), max2(t[1], t[1] << 16), 0x7610);
+#pragma unroll
+  for (int m = kE2m1Group / 16; m > 0; m >>= 1) top = max2(top, __shfl_xor_sync(0xffffffffu, top, m));
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t mine = j == 0 ? top & 0xffffu : top >> 16;
+    const bool fine = mine < 0x7f80u;
+    // 6 = 1.5·2^2: as for E4M3.
+    const int e = min(125, max(-126, static_cast<int>(mine >> 7) - 129 + ((mine & 0x7fu) > 0x40u ? 1 : 0)));
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = fine ? w[j][i] : 0u;
+      fmul2(x[2 * i], x[2 * i + 1], __uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u), inv, inv);
+    }
+    (j == 0 ? kc : vc) = pack_e2m1x8(x);
+    (j == 0 ? ks : vs) = fine ? e + 127 : 255;
+  }
+}
+
 // Item (b, group of R tokens, h), h fastest: 8 or 16 lanes for the R rows.
 template <int D, int R>
 struct Item {
@@ -115,8 +151,9 @@ struct Item {
   }
 };
 
-template <int D, bool FP8, int R>
+template <int D, int F, int R>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ CacheParams p) {
+  constexpr bool FP8 = F == kCacheE4m3, FP4 = F == kCacheE2m1;
   const Item<D, R> it(p);
   const int shift = 31 - __clz(p.block_size);  // a power of two
   int len = 0;
@@ -170,13 +207,15 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       }
     }
   }
-  using Out = typename std::conditional<FP8, uint2, uint4>::type;  // 8 elements
+  using Out = typename std::conditional<FP4, uint32_t, typename std::conditional<FP8, uint2, uint4>::type>::type;  // 8 elements
   Out kc[R], vc[R];
   int ke[R], ve[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if constexpr (FP8) {
       quantise8<D>(kr[r], vr[r], kc[r], vc[r], ke[r], ve[r]);
+    } else if constexpr (FP4) {
+      quantise8_e2m1(kr[r], vr[r], kc[r], vc[r], ke[r], ve[r]);
     } else {
       kc[r] = kr[r];
       vc[r] = vr[r];
@@ -186,6 +225,10 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     if (FP8 && it.lane8 == 0) {
       p.k_scale[at] = static_cast<uint8_t>(ke[r] + 127);
       p.v_scale[at] = static_cast<uint8_t>(ve[r] + 127);
+    }
+    if (FP4 && (it.lane8 & 3) == 0) {  // one byte per group, whole as it stands
+      p.k_scale[at * (D / kE2m1Group) + it.lane8 / 4] = static_cast<uint8_t>(ke[r]);
+      p.v_scale[at * (D / kE2m1Group) + it.lane8 / 4] = static_cast<uint8_t>(ve[r]);
     }
   };
   Out* const k_out = static_cast<Out*>(p.k_cache) + it.lane8;
@@ -224,7 +267,19 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   }
 }
 
-// Eight codes times 2^(s−127) as bf16.
+// Eight E2M1 codes times 2^(s−127) as bf16, exact; s = 255 stands for NaN.
+__device__ __forceinline__ uint4 dequantise8(uint32_t c, uint32_t s) {
+  const float f = s == 0 ? 5.877471754111438e-39f : s == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = e2m1x2_to_f16x2(c >> (8 * i));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    out[i] = pack_bf16x2(v.x * f, v.y * f);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+// Eight E4M3 codes times 2^(s−127) as bf16.
 __device__ __forceinline__ uint4 dequantise8(uint2 c, uint32_t s) {
   const uint32_t w[2] = {c.x, c.y};
   uint32_t out[4];
@@ -239,8 +294,9 @@ __device__ __forceinline__ uint4 dequantise8(uint2 c, uint32_t s) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <int D, bool FP8, int R>
+template <int D, int F, int R>
 __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_constant__ CacheParams p) {
+  constexpr bool FP8 = F == kCacheE4m3, FP4 = F == kCacheE2m1;
   const Item<D, R> it(p);
   if (!it.in) return;
   int len = p.lens[it.b];
@@ -248,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
     report(p.err, kSiteBadLength);
     len = 0;
   }
-  using Raw = typename std::conditional<FP8, uint2, uint4>::type;  // 8 elements
+  using Raw = typename std::conditional<FP4, uint32_t, typename std::conditional<FP8, uint2, uint4>::type>::type;  // 8 elements
   Raw kr[R], vr[R];
   uint32_t ks[R], vs[R];
   bool live[R];
@@ -267,6 +323,10 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
         ks[r] = p.k_scale[row];
         vs[r] = p.v_scale[row];
       }
+      if constexpr (FP4) {
+        ks[r] = p.k_scale[row * (D / kE2m1Group) + it.lane8 / 4];
+        vs[r] = p.v_scale[row * (D / kE2m1Group) + it.lane8 / 4];
+      }
     }
   }
 #pragma unroll
@@ -274,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
     const int n = it.n0 + r;
     if (n >= p.N) break;
     uint4 k8, v8;
-    if constexpr (FP8) {
+    if constexpr (FP8 || FP4) {
       k8 = dequantise8(kr[r], ks[r]);
       v8 = dequantise8(vr[r], vs[r]);
     } else {
@@ -288,15 +348,15 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_con
   }
 }
 
-template <bool APPEND, int D, bool FP8, int R>
+template <bool APPEND, int D, int F, int R>
 cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.B) * ((p.N + R - 1) / R) * p.Hkv;
   const int64_t blocks = (items * (D / 8) + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   if (APPEND)
-    cache_append_kernel<D, FP8, R><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    cache_append_kernel<D, F, R><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   else
-    cache_gather_kernel<D, FP8, R><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    cache_gather_kernel<D, F, R><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -307,27 +367,36 @@ cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
 //   reading E4M3            8 x 512 5.0, 4.9, 5.0   8 x 2048 12.2, 10.8, 10.8   4 x 32768, 8 heads 146, 122, 122
 //   bf16                    8 x 8192, 4 heads, writing 41.2, 41.4, 41.3 and reading 43.5, 42.0, 42.2
 // The rule turns to four between the second and the third size (4 x 152 x 2048 threads of one token).
-template <bool APPEND, int D, bool FP8>
+template <bool APPEND, int D, int F>
 cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
   const int64_t threads = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 8);
-  return p.N >= 4 && threads >= 4ll * 152 * 2048 ? launch_r<APPEND, D, FP8, 4>(p, stream)
-                                                 : launch_r<APPEND, D, FP8, 1>(p, stream);
+  return p.N >= 4 && threads >= 4ll * 152 * 2048 ? launch_r<APPEND, D, F, 4>(p, stream)
+                                                 : launch_r<APPEND, D, F, 1>(p, stream);
 }
 
-template <bool APPEND>
-cudaError_t launch(const CacheParams& p, int d, bool fp8, cudaStream_t stream) {
-  if (d == 128) return fp8 ? launch_d<APPEND, 128, true>(p, stream) : launch_d<APPEND, 128, false>(p, stream);
-  if (d == 64) return fp8 ? launch_d<APPEND, 64, true>(p, stream) : launch_d<APPEND, 64, false>(p, stream);
+template <bool APPEND, int D>
+cudaError_t launch(const CacheParams& p, int format, cudaStream_t stream) {
+  switch (format) {
+    case kCacheBf16: return launch_d<APPEND, D, kCacheBf16>(p, stream);
+    case kCacheE4m3: return launch_d<APPEND, D, kCacheE4m3>(p, stream);
+    case kCacheE2m1: return launch_d<APPEND, D, kCacheE2m1>(p, stream);
+  }
   return cudaErrorInvalidValue;
+}
+template <bool APPEND>
+cudaError_t launch(const CacheParams& p, int d, int format, cudaStream_t stream) {
+  return d == 128 ? launch<APPEND, 128>(p, format, stream)
+         : d == 64 ? launch<APPEND, 64>(p, format, stream)
+                   : cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_cache_append(const CacheParams& p, int d, bool fp8, cudaStream_t s) {
-  return launch<true>(p, d, fp8, s);
+cudaError_t launch_cache_append(const CacheParams& p, int d, int format, cudaStream_t s) {
+  return launch<true>(p, d, format, s);
 }
-cudaError_t launch_cache_gather(const CacheParams& p, int d, bool fp8, cudaStream_t s) {
-  return launch<false>(p, d, fp8, s);
+cudaError_t launch_cache_gather(const CacheParams& p, int d, int format, cudaStream_t s) {
+  return launch<false>(p, d, format, s);
 }
 
 }  // namespace fa

@@ -15,6 +15,7 @@ enum : unsigned int {
   kKernBwd = 3,
   kKernTree = 4,
   kKernCache = 5,
+  kKernPages = 6,
   kKernSelftest = 15,  // fa_watchdog_selftest
 };
 
@@ -68,7 +69,7 @@ struct DecodeParams {
 // Device-side argument checks report with these sites in the word after the
 // watchdog's, which no pipeline wait looks at: a bad page of one sequence leaves
 // the others' results, and other kernels, alone.
-enum : unsigned int { kSiteBadBlock = 0xE1, kSiteBadLength = 0xE2 };
+enum : unsigned int { kSiteBadBlock = 0xE1, kSiteBadLength = 0xE2, kSiteBadHolders = 0xE3, kSiteBadSequence = 0xE4 };
 
 // Grouped-query split-KV decode on tensor cores (fa_decode_tc.cu).
 struct DecodeTcParams {
@@ -124,21 +125,74 @@ struct RopeParams {
   int64_t position0;
   float magnitude, sign;
   uint64_t turns[128];  // w_i / 2π as 64-bit fractions of a turn
+  // Several axes: pair i turns by the position of axis axis[i], positions[a·pos_stride_a + b·pos_stride_b + n].
+  int n_axes;           // 0: one position per token
+  int64_t pos_stride_a;
+  uint8_t axis[128];
 };
+constexpr int kRopeMaxAxes = 4;
+
+// How the rows of a paged cache are held.
+enum CacheFormat : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheE2m1 = 2 };
+constexpr int kE2m1Group = 32;  // elements of a row that share a power of two
+// Bytes of a row's elements and of its scales.
+__host__ __device__ constexpr int cache_row_bytes(int d, int format) {
+  return format == kCacheBf16 ? 2 * d : format == kCacheE4m3 ? d : d / 2;
+}
+__host__ __device__ constexpr int cache_row_scales(int d, int format) {
+  return format == kCacheBf16 ? 0 : format == kCacheE4m3 ? 1 : d / kE2m1Group;
+}
 
 // Paged cache writes and reads (fa_cache.cu).
 struct CacheParams {
   void* k_rows;  // [B, Hkv, N, d] bf16, read by the append and written by the gather
   void* v_rows;
   int64_t sk[3], sv[3];  // their element strides (b, h, n)
-  void* k_cache;  // [num_blocks, Hkv, block_size, d] bf16 or E4M3
+  void* k_cache;  // [num_blocks, Hkv, block_size, d] bf16 or E4M3, [.., d/2] pairs of E2M1
   void* v_cache;
-  uint8_t* k_scale;  // E4M3: [num_blocks, Hkv, block_size] E8M0 bytes
+  uint8_t* k_scale;  // E8M0 bytes: E4M3 [num_blocks, Hkv, block_size], E2M1 [.., d/32]
   uint8_t* v_scale;
   const int* block_table;  // [B, max_blocks]
   const int* start;        // append: logical position of the first new token
   const int* lens;         // append: new tokens (null: N each); gather: sequence lengths
   int B, Hkv, N, num_blocks, block_size, max_blocks;
+  unsigned int* err;
+};
+
+// Rows of a paged cache moved together, and whole pages copied (fa_pages.cu).
+struct MoveParams {
+  uint8_t* cache[2];      // keys, values
+  uint8_t* scale[2];      // their scale bytes, or null
+  const int* block_table; // [B, max_blocks]
+  const int* first;       // [B] where the kept rows go
+  const int* keep;        // keep[b·keep_sb + i]: position of the i-th row kept
+  const int* keep_lens;   // [B] or null (N each)
+  int64_t keep_sb;
+  const int* src;         // copies: pages, −1 for none
+  const int* dst;
+  int B, Hkv, N, num_blocks, block_size, max_blocks;
+  unsigned int* err;
+};
+
+// Pages shared, freed and reserved (fa_pages.cu).
+constexpr int kPageSegment = 4096;  // pages that one block of the reserving kernels looks at
+struct PageParams {
+  int* block_table;  // [B, max_blocks], −1 where there is no page
+  int* seq_lens;     // [B]
+  int* holders;      // [num_blocks] sequences that hold a page, 0: free
+  const int* src;    // fork: [n] sequences; free: [n] sequences
+  const int* dst;    // fork: [n] sequences
+  const int* lens;   // free: [n] tokens to keep or null; reserve: [B] tokens to come
+  int* granted;      // reserve: [B]
+  int* copy_src;
+  int* copy_dst;
+  // reserve's workspace
+  int* seg;    // [segments] free pages, then those before
+  int* last;   // [B] page that the next token goes into, −1 where that is a new one (or none)
+  int* from;   // [B] first entry of the table that is missing
+  int* want;   // [B] pages missing, then where they begin among the free pages
+  int* total;  // [1] pages handed out
+  int B, n, num_blocks, block_size, max_blocks;
   unsigned int* err;
 };
 
@@ -150,9 +204,9 @@ struct TreeParams {
   void* o;        // bf16, so
   float* lse;     // [B, Hq, T] or null
   int64_t sq[3], so[3];
-  const void* k_cache;  // [num_blocks, Hkv, block_size, d] bf16 or E4M3
+  const void* k_cache;  // [num_blocks, Hkv, block_size, d] bf16 or E4M3, [.., d/2] pairs of E2M1
   const void* v_cache;
-  const uint8_t* k_scale;  // E4M3: [num_blocks, Hkv, block_size] E8M0 bytes
+  const uint8_t* k_scale;  // E8M0 bytes: E4M3 [num_blocks, Hkv, block_size], E2M1 [.., d/32]
   const uint8_t* v_scale;
   const int* block_table;  // [B, max_blocks]
   const int* seq_lens;     // [B] keys, the drafted ones included
@@ -172,16 +226,21 @@ struct TreeParams {
 };
 
 cudaError_t launch_rope(const RopeParams& p, bool fp32, bool inter, bool in_place, cudaStream_t s);
-cudaError_t launch_cache_append(const CacheParams& p, int d, bool fp8, cudaStream_t s);
-cudaError_t launch_cache_gather(const CacheParams& p, int d, bool fp8, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheParams& p, int d, int format, cudaStream_t s);
+cudaError_t launch_cache_gather(const CacheParams& p, int d, int format, cudaStream_t s);
+cudaError_t launch_cache_compact(const MoveParams& p, int d, int format, cudaStream_t s);
+cudaError_t launch_cache_copy(const MoveParams& p, int d, int format, int n, cudaStream_t s);
+cudaError_t launch_pages_fork(const PageParams& p, cudaStream_t s);
+cudaError_t launch_pages_free(const PageParams& p, cudaStream_t s);
+cudaError_t launch_pages_reserve(const PageParams& p, cudaStream_t s);  // three kernels
 int tree_cta_rows(int64_t rows);  // rows one CTA takes, for T·G rows in all
 constexpr int kTreeNarrowRows = 32;  // up to here a kernel of its own
 // Rows of a cut pair's piece in part_o: beyond the narrow kernel whole groups of 32.
 __host__ __device__ constexpr int64_t tree_piece_rows(int64_t rows) {
   return rows > kTreeNarrowRows ? (rows + 31) / 32 * 32 : rows;
 }
-cudaError_t launch_tree_wide(const TreeParams& p, int d, bool fp8, cudaStream_t s);  // more rows than that
-cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s);
+cudaError_t launch_tree_wide(const TreeParams& p, int d, int format, cudaStream_t s);  // more rows than that
+cudaError_t launch_decode_tree(const TreeParams& p, int d, int format, cudaStream_t s);
 
 cudaError_t launch_fwd_bf16(int d, const FwdParams& p, cudaStream_t s);
 // Unmasked bf16 forward at d = 64 with 3 or 4 query tiles of 128 rows per CTA

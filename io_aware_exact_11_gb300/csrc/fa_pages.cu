@@ -1,0 +1,490 @@
+// fa_pages.cu — the paged cache's pages and rows moved about: rows of a sequence
+// brought together, pages copied, and pages shared among sequences, freed and
+// reserved.
+//
+// Rows.  The i-th row kept of a sequence goes from position keep[i] to first + i,
+// in place.  With keep[i] ≥ first + i no row is written before all that read it
+// have: the place first + i is read for rows j with keep[j] = first + i ≥ first + j,
+// that is j ≤ i.  So a block that walks over the rows in chunks, and reads each chunk
+// (and the one after it) before it writes any of it, needs no second copy and no order
+// among the rows of a chunk.  Blocks share a sequence by heads and by columns of 64
+// bytes, which never meet, not by rows, which would have to wait for one another.
+//
+// Pages.  holders[p] counts the sequences whose table names page p; 0 is free.
+// Sharing a sequence's pages adds one to each, freeing takes one away, and who is to
+// write into a page that others hold too gets one of its own (the caller copies its
+// contents).  All results are those of one sequence after the other in the order
+// given, with free pages handed out by rising number, whatever order the blocks run
+// in: counts are sums of whole numbers, and which sequence gets which page follows
+// from prefix sums, not from atomics.  A page that c sequences are about to write
+// into and r hold is copied by all of them but the last, and by the last too if r > c:
+// when its turn comes, r − (c − 1) sequences still hold it.
+//
+// Bound: copies and moves by device memory, each byte read and written once; the
+// tables by the launches and the chains of dependent loads (length → table → count).
+//
+// Reserving takes three kernels: free pages per segment and missing pages per sequence
+// (a block per segment, a warp per sequence), prefix sums over both (one block), and the
+// hand-out, in which every free page finds its sequence by a search in the prefix
+// sums: no list of free pages is kept or written.
+#include "fa_kernels.h"
+#include "sm103.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void report(unsigned int* err, unsigned int what) {
+  atomicCAS(err + 1, 0u, (kKernPages << 8) | what);
+}
+
+// ------------------------------------------------------------------ rows and pages
+
+// Moves the 16-byte columns [c0, c0 + LANES) of the rows kept of sequence b, one head, keys or values.  SB: bytes of a
+// row's scales, moved by the block of the first columns.
+template <int RB, int SB, int LANES>
+__global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_constant__ MoveParams p) {
+  constexpr int kCols = RB / (16 * LANES);
+  constexpr int kRows = kThreads / LANES;  // a pass of the block
+  constexpr int U = 4;                     // passes of a chunk
+  const int lane = threadIdx.x % LANES, r = threadIdx.x / LANES;
+  const int part = blockIdx.x % (2 * kCols);
+  const int64_t pair = blockIdx.x / (2 * kCols);
+  const int b = static_cast<int>(pair / p.Hkv), h = static_cast<int>(pair - static_cast<int64_t>(b) * p.Hkv);
+  const int col = part >> 1, which = part & 1;
+  const bool scales = SB > 0 && col == 0 && lane == 0;
+  uint8_t* const cache = p.cache[which] + (col * LANES + lane) * 16;
+  uint8_t* const scale = p.scale[which];
+  const int shift = 31 - __clz(p.block_size);  // a power of two
+  const int room = p.max_blocks << shift;
+  const int first = p.first[b], n = p.keep_lens != nullptr ? p.keep_lens[b] : p.N;
+  if (n < 0 || n > p.N || first < 0 || first > room - n) {
+    if (threadIdx.x == 0) report(p.err, kSiteBadLength);
+    return;
+  }
+  const int* keep = p.keep + b * p.keep_sb;
+  const int* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+  auto row_of = [&](int t) -> int64_t {
+    const int blk = table[t >> shift];
+    if (blk >= 0 && blk < p.num_blocks)
+      return ((static_cast<int64_t>(blk) * p.Hkv + h) << shift) + (t & (p.block_size - 1));
+    report(p.err, kSiteBadBlock);
+    return -1;
+  };
+  struct Chunk {
+    int64_t to[U];  // −1: nothing to write
+    uint4 x[U];
+    uint32_t s[U];
+  };
+  auto load = [&](Chunk& c, int i0) {
+    int64_t from[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kRows + r;
+      from[u] = c.to[u] = -1;
+      if (i >= n) continue;
+      const int t = keep[i];
+      if (t < first + i || t >= room) {
+        report(p.err, kSiteBadLength);
+      } else if (t != first + i) {
+        from[u] = row_of(t);
+        if (from[u] >= 0) c.to[u] = row_of(first + i);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c.to[u] < 0) continue;
+      c.x[u] = *reinterpret_cast<const uint4*>(cache + from[u] * RB);
+      if (scales) {
+        if constexpr (SB == 1) c.s[u] = scale[from[u]];
+        if constexpr (SB == 2) c.s[u] = reinterpret_cast<const uint16_t*>(scale)[from[u]];
+        if constexpr (SB == 4) c.s[u] = reinterpret_cast<const uint32_t*>(scale)[from[u]];
+      }
+    }
+  };
+  auto store = [&](const Chunk& c) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c.to[u] < 0) continue;
+      *reinterpret_cast<uint4*>(cache + c.to[u] * RB) = c.x[u];
+      if (scales) {
+        if constexpr (SB == 1) scale[c.to[u]] = static_cast<uint8_t>(c.s[u]);
+        if constexpr (SB == 2) reinterpret_cast<uint16_t*>(scale)[c.to[u]] = static_cast<uint16_t>(c.s[u]);
+        if constexpr (SB == 4) reinterpret_cast<uint32_t*>(scale)[c.to[u]] = c.s[u];
+      }
+    }
+  };
+  constexpr int kStep = kRows * U;
+  Chunk a, next;
+  if (n > 0) load(a, 0);
+#pragma unroll 1
+  for (int i = 0; i < n; i += kStep) {
+    if (i + kStep < n) load(next, i + kStep);
+    __syncthreads();  // all of the chunk has been read
+    store(a);
+    a = next;
+  }
+}
+
+// Whole pages: block (piece, pair of pages), 16 bytes a thread and pass, keys then values.
+constexpr int kCopyPass = 4;
+__global__ void __launch_bounds__(kThreads) cache_copy_kernel(const __grid_constant__ MoveParams p, int64_t page_bytes,
+                                                              int scale_bytes) {
+  const int src = p.src[blockIdx.y], dst = p.dst[blockIdx.y];
+  if (src == -1 && dst == -1) return;
+  if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
+    if (threadIdx.x == 0) report(p.err, kSiteBadBlock);
+    return;
+  }
+  if (src == dst) return;
+  const int64_t words = page_bytes / 16;
+  uint4 x[2][kCopyPass];
+  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kThreads * kCopyPass + threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int u = 0; u < kCopyPass; ++u)
+      if (w0 + u * kThreads < words)
+        x[j][u] = reinterpret_cast<const uint4*>(p.cache[j] + src * page_bytes)[w0 + u * kThreads];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int u = 0; u < kCopyPass; ++u)
+      if (w0 + u * kThreads < words) reinterpret_cast<uint4*>(p.cache[j] + dst * page_bytes)[w0 + u * kThreads] = x[j][u];
+  if (scale_bytes > 0) {  // a multiple of 16: block_size is
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+    for (int64_t w = at; w < scale_bytes / 16; w += step)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        reinterpret_cast<uint4*>(p.scale[j] + static_cast<int64_t>(dst) * scale_bytes)[w] =
+            reinterpret_cast<const uint4*>(p.scale[j] + static_cast<int64_t>(src) * scale_bytes)[w];
+  }
+}
+
+// ------------------------------------------------------------------ shared and freed
+
+// Is x among list[0 … n)?  By all threads of the block, which get the answer.
+__device__ __forceinline__ bool among(const int* list, int n, int x) {
+  bool found = false;
+  for (int j = threadIdx.x; j < n; j += kThreads) found |= list[j] == x;
+  return __syncthreads_or(found);
+}
+
+// A block per pair (src, dst): dst, which holds nothing, takes src's pages.
+__global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_constant__ PageParams p) {
+  const int src = p.src[blockIdx.x], dst = p.dst[blockIdx.x];
+  const int shift = 31 - __clz(p.block_size);  // a power of two
+  bool fine = src >= 0 && src < p.B && dst >= 0 && dst < p.B;
+  // A sequence that two pairs fill, or that is filled and read, would depend on the order: the first pair to fill it
+  // counts, and no pair reads one that is filled.
+  fine = !among(p.dst, blockIdx.x, dst) && fine;
+  fine = !among(p.dst, p.n, src) && fine;
+  if (!fine) {
+    if (threadIdx.x == 0) report(p.err, kSiteBadSequence);
+    return;
+  }
+  const int len = p.seq_lens[src];
+  const int* from = p.block_table + static_cast<int64_t>(src) * p.max_blocks;
+  int* to = p.block_table + static_cast<int64_t>(dst) * p.max_blocks;
+  bool holds = p.seq_lens[dst] != 0;
+  for (int j = threadIdx.x; j < p.max_blocks; j += kThreads) holds |= to[j] >= 0;
+  holds = __syncthreads_or(holds);
+  const bool fits = len >= 0 && len <= static_cast<int64_t>(p.max_blocks) << shift;
+  if (holds || !fits) {
+    if (threadIdx.x == 0) report(p.err, holds ? kSiteBadSequence : kSiteBadLength);
+    return;
+  }
+  const int used = (len + p.block_size - 1) >> shift;
+  for (int j = threadIdx.x; j < used; j += kThreads) {
+    const int page = from[j];
+    if (page >= 0 && page < p.num_blocks)
+      atomicAdd(p.holders + page, 1);
+    else
+      report(p.err, kSiteBadBlock);
+    to[j] = page;
+  }
+  for (int j = used + threadIdx.x; j < p.max_blocks; j += kThreads) to[j] = -1;
+  if (threadIdx.x == 0) p.seq_lens[dst] = len;
+}
+
+// A block per sequence: its pages behind the first lens[i] tokens (all, without lens) lose a holder.
+__global__ void __launch_bounds__(kThreads) pages_free_kernel(const __grid_constant__ PageParams p) {
+  const int b = p.src[blockIdx.x];
+  const int keep = p.lens != nullptr ? p.lens[blockIdx.x] : 0;
+  const int shift = 31 - __clz(p.block_size);  // a power of two
+  const bool twice = among(p.src, blockIdx.x, b);  // the first entry of a sequence counts
+  if (b < 0 || b >= p.B || twice || keep < 0) {
+    if (threadIdx.x == 0) report(p.err, keep < 0 ? kSiteBadLength : kSiteBadSequence);
+    return;
+  }
+  int len = p.seq_lens[b];
+  const int64_t room = static_cast<int64_t>(p.max_blocks) << shift;
+  if (len < 0 || len > room) {
+    if (threadIdx.x == 0) report(p.err, kSiteBadLength);
+    len = len < 0 ? 0 : static_cast<int>(room);
+  }
+  __syncthreads();  // all have read the length
+  len = min(len, keep);
+  int* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+  for (int j = static_cast<int>((static_cast<int64_t>(len) + p.block_size - 1) >> shift) + threadIdx.x; j < p.max_blocks;
+       j += kThreads) {
+    const int page = table[j];
+    if (page == -1) continue;
+    table[j] = -1;
+    if (page < 0 || page >= p.num_blocks) {
+      report(p.err, kSiteBadBlock);
+    } else if (atomicSub(p.holders + page, 1) <= 0) {
+      atomicAdd(p.holders + page, 1);  // nobody was said to hold it
+      report(p.err, kSiteBadHolders);
+    }
+  }
+  if (threadIdx.x == 0) p.seq_lens[b] = len;
+}
+
+// ------------------------------------------------------------------------ reserved
+
+// Exclusive prefix sum over the block's threads, and the sum of all.
+template <int NT>
+__device__ __forceinline__ int block_prefix(int mine, int* warp_sum, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  __syncthreads();  // of the call before
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int x = warp_sum[w];
+    before += w < warp ? x : 0;
+    total += x;
+  }
+  return before + incl - mine;
+}
+
+// The free ones among 16 neighbouring pages, a bit each.
+__device__ __forceinline__ uint32_t free_pages(const PageParams& p, int page0) {
+  uint32_t bits = 0;
+  if (page0 + 16 <= p.num_blocks && (reinterpret_cast<uintptr_t>(p.holders) & 15u) == 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int4 x = reinterpret_cast<const int4*>(p.holders + page0)[q];
+      bits |= (x.x == 0 ? 1u : 0u) << (4 * q) | (x.y == 0 ? 2u : 0u) << (4 * q) | (x.z == 0 ? 4u : 0u) << (4 * q) |
+              (x.w == 0 ? 8u : 0u) << (4 * q);
+    }
+  } else {
+    for (int q = 0; q < 16 && page0 + q < p.num_blocks; ++q) bits |= p.holders[page0 + q] == 0 ? 1u << q : 0u;
+  }
+  return bits;
+}
+
+// Free pages of a segment, or what each of eight sequences misses.
+static_assert(kPageSegment == kThreads * 16, "16 pages a thread");
+__global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_constant__ PageParams p, int segments) {
+  __shared__ int warp_sum[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (static_cast<int>(blockIdx.x) < segments) {
+    int total;
+    block_prefix<kThreads>(__popc(free_pages(p, blockIdx.x * kPageSegment + threadIdx.x * 16)), warp_sum, total);
+    if (threadIdx.x == 0) p.seg[blockIdx.x] = total;
+    return;
+  }
+  const int b = (blockIdx.x - segments) * (kThreads / 32) + warp;
+  if (b >= p.B) return;
+  const int shift = 31 - __clz(p.block_size);  // a power of two
+  const int len = p.seq_lens[b], more = p.lens[b];
+  const int64_t room = static_cast<int64_t>(p.max_blocks) << shift;
+  const bool fine = len >= 0 && more >= 0 && static_cast<int64_t>(len) + more <= room;
+  int last = -1, from = 0, want = fine ? 0 : -1;  // −1: cannot be served
+  if (!fine) {
+    if (lane == 0) report(p.err, kSiteBadLength);
+  } else if (more > 0) {
+    const int* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+    const int have = static_cast<int>((static_cast<int64_t>(len) + p.block_size - 1) >> shift);
+    const int need = static_cast<int>((static_cast<int64_t>(len) + more + p.block_size - 1) >> shift);
+    if ((len & (p.block_size - 1)) != 0) {
+      last = table[have - 1];
+      if (last < 0 || last >= p.num_blocks) {
+        if (lane == 0) report(p.err, kSiteBadBlock);
+        want = -1;
+      }
+    }
+    // Pages reserved before come first; behind them the table is empty.
+    from = need;
+    for (int j0 = have; j0 < need; j0 += 32) {
+      const int j = j0 + lane;
+      const uint32_t missing = __ballot_sync(0xffffffffu, j < need && table[min(j, need - 1)] < 0);
+      if (missing != 0) {
+        from = j0 + __ffs(missing) - 1;
+        break;
+      }
+    }
+    if (want >= 0)
+      want = need - from;
+    else
+      last = -1;
+  }
+  if (lane == 0) {
+    p.last[b] = last;
+    p.from[b] = from;
+    p.want[b] = want;
+  }
+}
+
+// Prefix sums over segments and sequences, and who is served.
+constexpr int kScanThreads = 1024;
+constexpr int kMaxSequences = 4096;
+__global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(const __grid_constant__ PageParams p, int segments) {
+  __shared__ int last_of[kMaxSequences];
+  __shared__ int warp_sum[kScanThreads / 32];
+  __shared__ int first_short;
+  const int tid = threadIdx.x;
+  for (int b = tid; b < p.B; b += kScanThreads) last_of[b] = p.last[b];
+  if (tid == 0) first_short = p.B;
+  int frees = 0;
+  for (int s0 = 0; s0 < segments; s0 += kScanThreads) {
+    const int s = s0 + tid;
+    int total;
+    const int before = frees + block_prefix<kScanThreads>(s < segments ? p.seg[s] : 0, warp_sum, total);
+    if (s < segments) p.seg[s] = before;
+    frees += total;
+  }
+  __syncthreads();
+  int given = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
+    const int b = b0 + tid;
+    bool copies = false;
+    int want = 0;
+    if (b < p.B) {
+      want = p.want[b];
+      const int page = last_of[b];
+      const int held = page >= 0 ? p.holders[page] : 0;
+      if (held > 1) {
+        // Is there a later one that writes there?  Else, how many are there before?
+        bool later = false;
+        for (int j = b + 1; j < p.B && !later; ++j) later = last_of[j] == page;
+        int before = 0;
+        if (!later)
+          for (int j = 0; j < b; ++j) before += last_of[j] == page ? 1 : 0;
+        copies = later || held - before > 1;
+      }
+    }
+    const int mine = max(want, 0) + (copies ? 1 : 0);
+    int total;
+    const int at = given + block_prefix<kScanThreads>(mine, warp_sum, total);
+    // From the first one that finds too few pages on, nobody with tokens to come is served: a later one may count on
+    // the copy that an earlier one did not get.  (Sums stay below 2^31: the host bounds B · max_blocks.)
+    if (mine > 0 && at + mine > frees) atomicMin(&first_short, b);
+    __syncthreads();
+    if (b < p.B) {
+      const bool served = want >= 0 && (b < first_short || p.lens[b] == 0);
+      p.granted[b] = served ? 1 : 0;
+      p.copy_src[b] = served && copies ? last_of[b] : -1;
+      p.copy_dst[b] = -1;
+      p.want[b] = at;
+      if (b == first_short) *p.total = at;
+    }
+    given += total;
+    __syncthreads();
+  }
+  if (tid == 0 && first_short == p.B) *p.total = given;
+}
+
+// A block per segment: its free pages, as long as pages are handed out, go to their sequences.
+__global__ void __launch_bounds__(kThreads) pages_hand_out_kernel(const __grid_constant__ PageParams p) {
+  __shared__ int warp_sum[kThreads / 32];
+  const int total = *p.total, before = p.seg[blockIdx.x];
+  if (before >= total) return;
+  const int page0 = blockIdx.x * kPageSegment + threadIdx.x * 16;
+  uint32_t bits = free_pages(p, page0);
+  int sum;
+  int rank = before + block_prefix<kThreads>(__popc(bits), warp_sum, sum);
+  const int shift = 31 - __clz(p.block_size);  // a power of two
+  for (; bits != 0 && rank < total; bits &= bits - 1, ++rank) {
+    const int page = page0 + __ffs(bits) - 1;
+    int lo = 0, hi = p.B;  // the last sequence that begins at or before this page's place
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.want[mid] <= rank)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    int* table = p.block_table + static_cast<int64_t>(lo) * p.max_blocks;
+    const int shared = p.copy_src[lo];
+    const int i = rank - p.want[lo] - (shared >= 0 ? 1 : 0);
+    p.holders[page] = 1;
+    if (i < 0) {
+      table[p.seq_lens[lo] >> shift] = page;
+      p.copy_dst[lo] = page;
+      atomicSub(p.holders + shared, 1);
+    } else {
+      table[p.from[lo] + i] = page;
+    }
+  }
+}
+
+template <int RB, int SB>
+cudaError_t launch_compact(const MoveParams& p, cudaStream_t s) {
+  // Columns of 64 bytes (32-byte rows: 32): four lanes hold a row's part.  Whole rows per block would leave most SMs
+  // without one where there are few sequences and heads.
+  constexpr int kLanes = RB >= 64 ? 4 : RB / 16;
+  const int64_t blocks = static_cast<int64_t>(p.B) * p.Hkv * 2 * (RB / (16 * kLanes));
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  cache_compact_kernel<RB, SB, kLanes><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_compact(const MoveParams& p, int d, int format, cudaStream_t s) {
+  if (d == 128) {
+    if (format == kCacheBf16) return launch_compact<256, 0>(p, s);
+    if (format == kCacheE4m3) return launch_compact<128, 1>(p, s);
+    if (format == kCacheE2m1) return launch_compact<64, 4>(p, s);
+  } else if (d == 64) {
+    if (format == kCacheBf16) return launch_compact<128, 0>(p, s);
+    if (format == kCacheE4m3) return launch_compact<64, 1>(p, s);
+    if (format == kCacheE2m1) return launch_compact<32, 2>(p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_cache_copy(const MoveParams& p, int d, int format, int n, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(p.Hkv) * p.block_size;
+  const int64_t page = rows * cache_row_bytes(d, format);
+  const int64_t pieces = (page / 16 + kThreads * kCopyPass - 1) / (kThreads * kCopyPass);
+  if (pieces > 0x7fffffff || n > 65535) return cudaErrorInvalidValue;
+  cache_copy_kernel<<<dim3(static_cast<unsigned>(pieces), n), kThreads, 0, s>>>(
+      p, page, static_cast<int>(rows * cache_row_scales(d, format)));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PageParams& p, cudaStream_t s) {
+  pages_fork_kernel<<<p.n, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_free(const PageParams& p, cudaStream_t s) {
+  pages_free_kernel<<<p.n, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_reserve(const PageParams& p, cudaStream_t s) {
+  const int segments = static_cast<int>((static_cast<int64_t>(p.num_blocks) + kPageSegment - 1) / kPageSegment);
+  const int counts = segments + (p.B + kThreads / 32 - 1) / (kThreads / 32);
+  if (p.B > kMaxSequences) return cudaErrorInvalidValue;
+  pages_count_kernel<<<counts, kThreads, 0, s>>>(p, segments);
+  pages_scan_kernel<<<1, kScanThreads, 0, s>>>(p, segments);
+  pages_hand_out_kernel<<<segments, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -22,6 +22,8 @@
 //
 // Measured on GB300: the gradients of 16 + 16 heads of 128 elements at 2 x 8192 tokens, bf16: 49 us, 5.5 TB/s,
 // 0.82 of a device copy; one token: the launch (17 us a call from Python).
+#include <type_traits>
+
 #include "fa_kernels.h"
 #include "sm103.cuh"
 
@@ -51,14 +53,19 @@ struct alignas(sizeof(T) * V == 16 ? 16 : alignof(T)) Vec {
 };
 
 // HALF: a column is V pairs, two vectors r/2 apart.  INTER: one vector of V/2 pairs.
-template <typename T, int V, bool INTER>
+// AXES: a token has a position on each of several axes, and each pair goes by one of them.
+template <typename T, int V, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPairs = INTER ? V / 2 : V;
   // The frequencies by (pair of a column, column), copied by one lane per warp: a constant that differs between the
   // lanes is fetched once for each of them.
   __shared__ uint64_t turns[128];
+  __shared__ uint8_t axis[AXES ? 128 : 1];
   for (int i = threadIdx.x >> 5; i < p.rot / 2; i += kThreads / 32)
-    if ((threadIdx.x & 31) == 0) turns[i % kPairs * p.rot_cols + i / kPairs] = p.turns[i];
+    if ((threadIdx.x & 31) == 0) {
+      turns[i % kPairs * p.rot_cols + i / kPairs] = p.turns[i];
+      if (AXES) axis[i % kPairs * p.rot_cols + i / kPairs] = p.axis[i];
+    }
   __syncthreads();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int cols = p.rot_cols + p.copy_cols;
@@ -95,10 +102,25 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant
 
   float cs[kPairs], sn[kPairs];
   if (turn) {
-    const int64_t pos = p.position0 + (p.positions != nullptr ? p.positions[b * p.pos_stride_b + n] : n);
+    typename std::conditional<AXES, int32_t, int64_t>::type pos[AXES ? kRopeMaxAxes : 1];
+    if constexpr (AXES) {
+#pragma unroll
+      for (int a = 0; a < kRopeMaxAxes; ++a)
+        pos[a] = a < p.n_axes ? p.positions[a * p.pos_stride_a + b * p.pos_stride_b + n] : 0;
+    } else {
+      pos[0] = p.position0 + (p.positions != nullptr ? p.positions[b * p.pos_stride_b + n] : n);
+    }
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const uint64_t t = static_cast<uint64_t>(pos) * turns[i * p.rot_cols + col];
+      int64_t at = pos[0];  // sign-extended
+      if constexpr (AXES) {
+        const int mine = axis[i * p.rot_cols + col];
+        int32_t on = pos[0];
+#pragma unroll
+        for (int a = 1; a < kRopeMaxAxes; ++a) on = mine == a ? pos[a % kRopeMaxAxes] : on;
+        at = on;
+      }
+      const uint64_t t = static_cast<uint64_t>(at) * turns[i * p.rot_cols + col];
       const float half_turns = static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f;  // 2^-31
       sincospif(half_turns, &sn[i], &cs[i]);
       cs[i] *= p.magnitude;
@@ -145,7 +167,11 @@ cudaError_t launch_v(RopeParams p, bool in_place, cudaStream_t stream) {
   p.heads_per_thread = per;
   p.q_groups = (p.Hq + per - 1) / per;
   const int groups = p.q_groups + (p.Hk + per - 1) / per;
-  rope_kernel<T, V, INTER><<<dim3(static_cast<unsigned>(blocks), groups), kThreads, 0, stream>>>(p);
+  const dim3 grid(static_cast<unsigned>(blocks), groups);
+  if (p.n_axes > 0)
+    rope_kernel<T, V, INTER, true><<<grid, kThreads, 0, stream>>>(p);
+  else
+    rope_kernel<T, V, INTER, false><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

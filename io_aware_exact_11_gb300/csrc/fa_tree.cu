@@ -77,18 +77,24 @@ namespace {
 constexpr int kBN = kTreeBN;
 constexpr int kPBlock = kBN * 128;       // P̃ᵀ: one 128-byte row per key
 constexpr int kMaxRing = 8;
-constexpr int kThreads = 384;            // warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11
+constexpr int kMaxCodeRing = 16;
+// Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11; E2M1: all loads 8, expanders 12–15.
 // Registers per thread at launch and after the warpgroups' split.  A softmax thread holds its scores and partial
 // sums, 2·NR values, and a spilled one would go to L2, shared memory leaving next to no L1.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
-static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch && kThreads == 384, "register split");
 constexpr int kScaleRing = 16;           // E4M3: tiles whose scale bytes are staged (V slots and four more)
 constexpr int kFRing = 4;                // pieces whose row factors may be live at once
 constexpr int kBadRing = 8;              // pieces whose flags of bad values may be
 
 // NR rows of a pair, shared by both streams.
-template <int D, bool FP8, int NR>
+template <int D, int F, int NR>
 struct Cfg {
+  static constexpr bool FP8 = F == kCacheE4m3, FP4 = F == kCacheE2m1;
+  // E2M1: four warps more, which write the tiles out as bf16.
+  static constexpr int kThreads = FP4 ? 512 : 384;
+  static constexpr int kRegsLaunch = FP4 ? 128 : 168;
+  static constexpr int kRegsSoftmax = FP4 ? (NR == 16 ? 176 : 192) : 208;
+  static constexpr int kRegsOther = FP4 ? (NR == 16 ? 80 : 64) : 88;
+  static_assert(2 * kRegsSoftmax + (FP4 ? 2 : 1) * kRegsOther <= (FP4 ? 4 : 3) * kRegsLaunch, "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
   static constexpr int kTerms = FP8 ? 1 : 2;                  // of P̃
   static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
@@ -101,25 +107,32 @@ struct Cfg {
   // K and V ring slots in what is left of 227 KB after this, the bookkeeping and the alignment pad.
   static constexpr int kMisc = (FP8 ? 9 : 6) * 1024;
   static constexpr int kRoom = 226 * 1024 - kMisc - kFixed;
-  static constexpr int kRing = kRoom / kSlot < 14 ? kRoom / kSlot : 14;
+  static constexpr int kRing = FP4 ? (D == 128 ? 4 : 6) : kRoom / kSlot < 14 ? kRoom / kSlot : 14;
   static constexpr int kRK = kRing / 2;
   static constexpr int kRV = kRing - kRK;
+  // E2M1: half tiles of codes in what is left.
+  static constexpr int kCodeRoom = (kRoom - kRing * kSlot) / FourBit<D>::kHalf;
+  static constexpr int kCodeRing = !FP4 ? 1 : kCodeRoom < kMaxCodeRing ? kCodeRoom : kMaxCodeRing;
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kRK * kSlot;
   static constexpr int kOffV16 = kOffV + kRV * kSlot;
   static constexpr int kOffP = kOffV16 + 2 * kV16;
   static constexpr int kOffQ = kOffP + kP;
-  static constexpr int kOffMisc = kOffQ + kQTile;
+  static constexpr int kOffCodes = kOffQ + kQTile;
+  static constexpr int kOffMisc = kOffCodes + (FP4 ? kCodeRing * FourBit<D>::kHalf : 0);
   static constexpr int kSCols = FP8 ? 2 * NR : NR;            // TMEM columns of one stream's S
   static constexpr int kColO = 2 * kSCols;
   static constexpr int kCols = kColO + 2 * kPCols;
   static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && kRV + 4 <= kScaleRing, "rings");
   static_assert(kQTile % 1024 == 0 && kSlot % 1024 == 0 && kCols <= 512, "swizzle atoms, TMEM");
+  static_assert(!FP4 || kCodeRing >= 3, "codes on their way");
 };
 
-template <int NR, bool FP8>
+template <int NR, int F>
 struct Misc {
+  static constexpr bool FP8 = F == kCacheE4m3;
+  uint64_t code_full[F == kCacheE2m1 ? kMaxCodeRing : 1], code_empty[F == kCacheE2m1 ? kMaxCodeRing : 1];
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], sc_full[kScaleRing], q_full, q_empty, drain;
   alignas(16) float nm[2][NR];         // minus the reference maxima (log2 units), 0 while a row has seen nothing
@@ -136,7 +149,7 @@ struct Misc {
   alignas(16) uint8_t k_scale[FP8 ? kScaleRing : 1][kBN];  // written by bulk copies
   alignas(16) uint8_t v_scale[FP8 ? kScaleRing : 1][kBN];
   uint32_t bad[kBadRing][8];           // drafted keys with non-finite values (one bit each)
-  long long warp_sum[kThreads / 32];
+  long long warp_sum[16];
   int start[3];
   uint32_t tmem_base;
   int abort_flag;
@@ -260,9 +273,10 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, u
   fence_proxy_async_smem();
 }
 
-template <int D, bool FP8, int NR>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-  using C = Cfg<D, FP8, NR>;
+template <int D, int F, int NR>
+__global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  using C = Cfg<D, F, NR>;
+  constexpr bool FP8 = C::FP8, FP4 = C::FP4;
   constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
   constexpr int kSlot = C::kSlot;
   // Rescale once a score exceeds the reference by kLazy; the reference is taken kBase below the maximum.
@@ -273,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
-  Misc<NR, FP8>* ms = reinterpret_cast<Misc<NR, FP8>*>(smem + C::kOffMisc);
+  Misc<NR, F>* ms = reinterpret_cast<Misc<NR, F>*>(smem + C::kOffMisc);
   volatile int* abort_flag = &ms->abort_flag;
 
   const int tid = threadIdx.x;
@@ -284,11 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
   if (tid == 0) {
     for (int s = 0; s < C::kRK; ++s) {
-      mbar_init(&ms->k_full[s], 1);
+      mbar_init(&ms->k_full[s], FP4 ? 4 : 1);
       mbar_init(&ms->k_empty[s], 1);
     }
+    for (int s = 0; FP4 && s < C::kCodeRing; ++s) {
+      mbar_init(&ms->code_full[s], 1);
+      mbar_init(&ms->code_empty[s], 4);
+    }
     for (int s = 0; s < C::kRV; ++s) {
-      mbar_init(&ms->v_full[s], 1);
+      mbar_init(&ms->v_full[s], FP4 ? 4 : 1);
       mbar_init(&ms->v_empty[s], FP8 ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -309,20 +327,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     tmem_alloc(&ms->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-  const TreePart my = find_part<kThreads>(p, part, ms->warp_sum, ms->start);
+  const TreePart my = find_part<C::kThreads>(p, part, ms->warp_sum, ms->start);
   const uint32_t tmem = ms->tmem_base;
 
   if (my.count <= 0) {
     // nothing left for this CTA
-  } else if (warp == 8 || warp == 10) {
-    reg_dealloc<kRegsOther>();
+  } else if (FP4 && warp >= 12) {
+    reg_dealloc<C::kRegsOther>();
+    if constexpr (FP4)
+      expand_codes<D, C::kCodeRing, C::kRK, C::kRV>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty,
+                                                    smem + C::kOffK, ms->k_full, ms->k_empty, smem + C::kOffV, ms->v_full,
+                                                    ms->v_empty, abort_flag, tree_site(0x10), tid - 384);
+  } else if (FP4 && warp == 8) {
+    reg_dealloc<C::kRegsOther>();
+    if constexpr (FP4)
+      load_codes<D, C::kCodeRing>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty, abort_flag, tree_site(1));
+  } else if (!FP4 && (warp == 8 || warp == 10)) {
+    reg_dealloc<C::kRegsOther>();
     // ------------------------------------------- loads of K (warp 8) and V (warp 10)
     const bool is_v = warp == 10;
-    load_pages<D, FP8, kScaleRing>(p, my, is_v, smem + (is_v ? C::kOffV : C::kOffK), is_v ? C::kRV : C::kRK,
-                                   is_v ? ms->v_full : ms->k_full, is_v ? ms->v_empty : ms->k_empty, ms->sc_full,
-                                   ms->k_scale[0], ms->v_scale[0], abort_flag, tree_site(is_v ? 2 : 1));
+    if constexpr (!FP4)
+      load_pages<D, FP8, kScaleRing>(p, my, is_v, smem + (is_v ? C::kOffV : C::kOffK), is_v ? C::kRV : C::kRK,
+                                     is_v ? ms->v_full : ms->k_full, is_v ? ms->v_empty : ms->k_empty, ms->sc_full,
+                                     ms->k_scale[0], ms->v_scale[0], abort_flag, tree_site(is_v ? 2 : 1));
   } else if (warp == 9) {
-    reg_dealloc<kRegsOther>();
+    reg_dealloc<C::kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
     constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
@@ -411,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_wait_drain_inl(&ms->drain, 0, kTreeDrainNs);
     }
   } else if (warp < 8) {
-    reg_alloc<kRegsSoftmax>();
+    reg_alloc<C::kRegsSoftmax>();
     // ----------------------------- softmax: one key per thread, the stream's NR rows
     const int g = warp >> 2;
     const int bar = 1 + g;                 // the stream's barrier
@@ -745,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             continue;
           }
           if (!((bad[u >> 5] >> (u & 31)) & 1)) continue;
-          const float v = taken_out<FP8>(p, value_row<D>(p, w, u) + kt);
+          const float v = taken_out<F>(p, value_row<D>(p, w, u) + kt);
           if (v == 0.f) continue;
 #pragma unroll 1
           for (int q = 0; q < kOut; ++q) {
@@ -763,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // The flags of three pieces ago: the other stream may still be at the piece before.
       if (tid < 8) ms->bad[(w.index + kBadRing - 3) % kBadRing][tid] = 0;
     } while (ok && w.next(p));
-  } else {
-    reg_dealloc<kRegsOther>();
+  } else if (warp == 11) {
+    reg_dealloc<C::kRegsOther>();
     // ------------------------- Q of every piece but the first, which the streams load
     TreeWalk w;
     w.begin(p, my);
@@ -775,6 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       load_q<D, FP8, NR, 32, 2>(p, w, smem + C::kOffQ, ms->f[w.index % kFRing], lane);
       mbar_arrive(&ms->q_full);
     }
+  } else {
+    reg_dealloc<C::kRegsOther>();  // E2M1: idle until the end
   }
 
   tc_fence_before();
@@ -899,12 +930,12 @@ cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, WIDE>, p);
 }
 
-template <int D, bool FP8, int NR>
+template <int D, int F, int NR>
 cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
-  constexpr int kSmem = Cfg<D, FP8, NR>::kOffMisc + static_cast<int>(sizeof(Misc<NR, FP8>)) + 1024;
+  constexpr int kSmem = Cfg<D, F, NR>::kOffMisc + static_cast<int>(sizeof(Misc<NR, F>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  using M = Misc<NR, FP8>;
-  static_assert(Cfg<D, FP8, NR>::kOffMisc % 16 == 0 && offsetof(M, nm) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
+  using M = Misc<NR, F>;
+  static_assert(Cfg<D, F, NR>::kOffMisc % 16 == 0 && offsetof(M, nm) % 16 == 0 && offsetof(M, f) % 16 == 0 &&
                     offsetof(M, k_scale) % 16 == 0 && offsetof(M, v_scale) % 16 == 0,
                 "16-byte accesses and bulk copies");
   // The register split draws on what the block is launched with, which is the compiled kernel's for good.
@@ -912,18 +943,18 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
   cudaError_t e;
   if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, tree_kernel<D, FP8, NR>);
+    e = cudaFuncGetAttributes(&a, tree_kernel<D, F, NR>);
     if (e != cudaSuccess) return e;
-    if (a.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (a.numRegs < Cfg<D, F, NR>::kRegsLaunch) return cudaErrorInvalidConfiguration;
     checked.store(true, std::memory_order_relaxed);
   }
-  e = cudaFuncSetAttribute(tree_kernel<D, FP8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  e = cudaFuncSetAttribute(tree_kernel<D, F, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, FP8, NR><<<static_cast<unsigned>(p.parts), kThreads, kSmem, s>>>(p);
+  tree_kernel<D, F, NR><<<static_cast<unsigned>(p.parts), Cfg<D, F, NR>::kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, bool FP8>
+template <int D, int F>
 cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
   // By the rows of a pair; 8 sequences of 16384 keys, 8 key/value heads, us with the one and the other:
@@ -932,21 +963,29 @@ cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   // (32 rows are the most that fit here without tiles of rows; 64 columns spilled registers and took 81 us where the
   // other kernel took 69: 8 tokens of 7 heads a group, 16 ragged sequences of up to 8192 bf16 keys.)
   const bool wide = rows > kTreeNarrowRows;
-  cudaError_t e = wide         ? launch_tree_wide(p, D, FP8, s)
-                  : rows <= 16 ? launch_rows<D, FP8, 16>(p, s)
-                               : launch_rows<D, FP8, 32>(p, s);
+  cudaError_t e = wide         ? launch_tree_wide(p, D, F, s)
+                  : rows <= 16 ? launch_rows<D, F, 16>(p, s)
+                               : launch_rows<D, F, 32>(p, s);
   if (e != cudaSuccess) return e;
   return wide ? launch_merge<D, true>(p, s) : launch_merge<D, false>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_tree(const TreeParams& p, int d, bool fp8, cudaStream_t s) {
+template <int D>
+static cudaError_t launch_format(const TreeParams& p, int format, cudaStream_t s) {
+  switch (format) {
+    case kCacheBf16: return launch_d<D, kCacheBf16>(p, s);
+    case kCacheE4m3: return launch_d<D, kCacheE4m3>(p, s);
+    case kCacheE2m1: return launch_d<D, kCacheE2m1>(p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_decode_tree(const TreeParams& p, int d, int format, cudaStream_t s) {
   if (static_cast<int64_t>(p.B) * p.Hq * p.T >= (1ll << 31) || static_cast<int64_t>(p.parts) * p.row_tiles > 0x7fffffff)
     return cudaErrorInvalidValue;
-  if (d == 128) return fp8 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
-  if (d == 64) return fp8 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
-  return cudaErrorInvalidValue;
+  return d == 128 ? launch_format<128>(p, format, s) : d == 64 ? launch_format<64>(p, format, s) : cudaErrorInvalidValue;
 }
 
 }  // namespace fa

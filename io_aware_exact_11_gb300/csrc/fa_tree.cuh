@@ -12,6 +12,19 @@ namespace fa {
 constexpr int kTreeBN = 128;                // keys per tile
 constexpr uint64_t kTreeDrainNs = 200000000ull;
 
+// Position in a ring of N slots and the parity of its passes.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
 __device__ __forceinline__ unsigned int tree_site(unsigned int s) { return (kKernTree << 8) | s; }
 
 // Lengths of sequence b: keys in all and drafted keys among them.  Lengths that
@@ -340,6 +353,199 @@ __device__ __forceinline__ void load_pages(const TreeParams& p, const TreePart& 
   }
 }
 
+// ---------------------------------------------------------------- a cache in four bits
+//
+// A page of one head is contiguous: its codes and its scale bytes come by plain bulk copies into a ring of half tiles (the
+// keys or the values of 128 rows: K₀, K₁, V₀, K₂, V₁ … of each piece, the order in which they are used), and four warps
+// write them out as bf16 tiles where the bf16 kernels have theirs.  E2M1 times a power of two is exact in bf16, so from
+// there on the kernels are those of a bf16 cache.
+
+template <int D>
+struct FourBit {
+  static constexpr int kCodes = kTreeBN * D / 2, kScales = kTreeBN * D / kE2m1Group;
+  static constexpr int kHalf = kCodes + kScales;  // bytes of the ring per half tile
+};
+
+// Fetches the codes and scales of a part's tiles, by one warp.
+template <int D, int RING>
+__device__ __forceinline__ void load_codes(const TreeParams& p, const TreePart& my, uint8_t* ring, uint64_t* full,
+                                           uint64_t* empty, volatile int* abort_flag, unsigned int site) {
+  constexpr int kRow = D / 2, kRowScales = D / kE2m1Group;
+  const int lane = threadIdx.x & 31;
+  const int bshift = 31 - __clz(p.block_size);  // a power of two
+  const int npt = kTreeBN >> bshift;            // pages per tile
+  int slot = 0, issued = 0;
+  uint32_t parity = 1;
+  bool ok = true;
+  // The pages of this lane: one of the tile's, or −1 past the end.
+  auto half = [&](int blk, int h, bool is_v) {
+    ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, site));
+    if (!ok) return;
+    const bool real = lane < npt && blk >= 0;
+    const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot], n_real * ((kRow + kRowScales) << bshift));
+    __syncwarp();
+    if (real) {
+      const int64_t row = (static_cast<int64_t>(blk) * p.Hkv + h) << bshift;
+      uint8_t* to = ring + slot * FourBit<D>::kHalf;
+      bulk_load(to + ((lane << bshift) * kRow), static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + row * kRow,
+                kRow << bshift, &full[slot]);
+      bulk_load(to + FourBit<D>::kCodes + ((lane << bshift) * kRowScales),
+                (is_v ? p.v_scale : p.k_scale) + row * kRowScales, kRowScales << bshift, &full[slot]);
+    }
+    ++issued;
+    if (++slot == RING) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  };
+  TreeWalk w;
+  w.begin(p, my);
+  do {
+    const int pages = (w.len + p.block_size - 1) >> bshift;
+    const int32_t* table = p.block_table + static_cast<int64_t>(w.b) * p.max_blocks;
+    // The ids of 32 pages at a time, one per lane, loaded one group ahead and checked when they are due.
+    int page = w.t0 * npt + lane;
+    int id = 0, ahead = page < pages ? table[page] : 0;
+    int at = 32;  // the tile's first page in the group
+    int before = -1;
+#pragma unroll 1
+    for (int i = w.t0; i <= w.t1; ++i) {
+      int blk = -1;
+      if (i < w.t1) {
+        if (at == 32) {
+          at = 0;
+          id = page < pages ? ahead : -1;  // −1: past the end
+          if (page < pages && (id < 0 || id >= p.num_blocks)) {
+            report_bad_page(p);
+            id = 0;
+          }
+          page += 32;
+          ahead = page < pages ? table[page] : 0;
+        }
+        blk = __shfl_sync(0xffffffffu, id, at + lane);
+        at += npt;
+        half(blk, w.h, false);
+      }
+      if (ok && i > w.t0) half(before, w.h, true);
+      if (!ok) break;
+      before = blk;
+    }
+  } while (ok && w.next(p));
+  // The copies in flight land before the CTA ends.
+  if (lane == 0) {
+#pragma unroll 1
+    for (int n = max(0, issued - RING); n < issued; ++n) mbar_wait_drain_inl(&full[n % RING], (n / RING) & 1, kTreeDrainNs);
+  }
+}
+
+__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t selector) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(selector));
+  return r;
+}
+
+// 32 E2M1 codes times 2^(s−127) as bf16.  The eight magnitudes times the power of two are worked out once, and their
+// upper and lower bytes are picked by the codes, four at a time.
+struct Magnitudes {
+  uint32_t hi[2], lo[2];
+  __device__ __forceinline__ explicit Magnitudes(uint32_t s) {
+    // (Byte 0 stands for 2^−127, below the normal numbers, and 255 for NaN.)
+    const float f = s == 0 ? 5.877471754111438e-39f : s == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
+    const uint32_t v[4] = {pack_bf16x2(0.f * f, 0.5f * f), pack_bf16x2(f, 1.5f * f), pack_bf16x2(2.f * f, 3.f * f),
+                           pack_bf16x2(4.f * f, 6.f * f)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hi[i] = permute(v[2 * i], v[2 * i + 1], 0x7531);
+      lo[i] = permute(v[2 * i], v[2 * i + 1], 0x6420);
+    }
+  }
+  __device__ __forceinline__ uint4 expand(uint32_t codes) const {
+    uint32_t out[4];
+    const uint32_t which = codes & 0x77777777u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t sel = which >> (16 * i);
+      uint32_t up = permute(hi[0], hi[1], sel);
+      const uint32_t low = permute(lo[0], lo[1], sel);
+      // A selector's upper bit, the sign, spreads the picked byte's over it: 0x80 or 0xff.
+      up |= permute(0x80808080u, 0x80808080u, codes >> (16 * i)) << 1 & 0x80808080u;
+      out[2 * i] = permute(low, up, 0x5140);
+      out[2 * i + 1] = permute(low, up, 0x7362);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+  }
+};
+
+// Writes the fetched tiles of a part out as bf16, by 128 threads (thread id of them): K and V tiles of kSlot bytes in
+// rings of RK and RV, as the bf16 kernels' loads lay them out (D = 128: [8 rows][half][row][128 bytes], else a row of 128
+// bytes per key, 16-byte chunks XORed with the row).  Rows past the end become zeros.
+template <int D, int RING, int RK, int RV>
+__device__ __forceinline__ void expand_codes(const TreeParams& p, const TreePart& my, const uint8_t* ring, uint64_t* full,
+                                             uint64_t* empty, uint8_t* k_dst, uint64_t* k_full, uint64_t* k_empty,
+                                             uint8_t* v_dst, uint64_t* v_full, uint64_t* v_empty,
+                                             volatile int* abort_flag, unsigned int site, int id) {
+  constexpr int kGroups = D / kE2m1Group;            // of a row
+  constexpr int kItems = kTreeBN * kGroups / 128;    // groups of a thread
+  constexpr int kSlot = kTreeBN * D * 2;
+  constexpr int kItemRows = 128 / kGroups;           // rows from one of its groups to the next
+  const int r0 = id / kGroups, g = id % kGroups;
+  // The lanes of a pass over 128 bytes write different chunks: groups of the upper half begin with their third chunk.
+  const int late = D == 128 && g >= 2 ? 2 : 0;
+  const int x0 = ((g & 1) * 4) ^ late ^ (r0 & 7);
+  const int off = D == 128 ? (r0 >> 3) * 2048 + (g >> 1) * 1024 + (r0 & 7) * 128 : r0 * 128;
+  Ring<RING> rc;
+  Ring<RK> rk;
+  Ring<RV> rv;
+  bool ok = true;
+  auto half = [&](int live, uint8_t* dst, uint64_t* to_full, uint64_t* to_empty, uint32_t to_parity) {
+    ok = mbar_wait_inl(&full[rc.slot], rc.parity, abort_flag, p.err, site) &&
+         mbar_wait_inl(to_empty, to_parity ^ 1u, abort_flag, p.err, site + 1);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return;
+    const uint8_t* src = ring + rc.slot * FourBit<D>::kHalf;
+    const uint4* codes = reinterpret_cast<const uint4*>(src) + id;
+    const uint8_t* scales = src + FourBit<D>::kCodes + id;
+#pragma unroll
+    for (int it = 0; it < kItems; ++it) {
+      uint4 c = codes[it * 128];
+      uint32_t s = scales[it * 128];
+      if (r0 + it * kItemRows >= live) {
+        c = make_uint4(0, 0, 0, 0);
+        s = 127;
+      }
+      const Magnitudes m(s);
+      const uint32_t w[4] = {late ? c.z : c.x, late ? c.w : c.y, late ? c.x : c.z, late ? c.y : c.w};
+      uint8_t* to = dst + off + it * (kItemRows * D * 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(to + ((x0 ^ j) << 4)) = m.expand(w[j]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((id & 31) == 0) {
+      mbar_arrive(to_full);
+      mbar_arrive(&empty[rc.slot]);
+    }
+    rc.advance();
+  };
+  TreeWalk w;
+  w.begin(p, my);
+  do {
+#pragma unroll 1
+    for (int i = w.t0; i <= w.t1; ++i) {
+      if (i < w.t1) {
+        half(w.len - i * kTreeBN, k_dst + rk.slot * kSlot, &k_full[rk.slot], &k_empty[rk.slot], rk.parity);
+        rk.advance();
+      }
+      if (ok && i > w.t0) {
+        half(w.len - (i - 1) * kTreeBN, v_dst + rv.slot * kSlot, &v_full[rv.slot], &v_empty[rv.slot], rv.parity);
+        rv.advance();
+      }
+      if (!ok) break;
+    }
+  } while (ok && w.next(p));
+}
+
 // Eight elements of a query row, whose other ones the neighbouring kChunks − 1 lanes hold, as E4M3 terms
 // x·2⁻ᵃ = hi + lo·2^−kLow; 2⁻ᵃ, which is returned as a, brings the row's largest magnitude to at most 448.
 template <int kChunks, int kLow>
@@ -407,9 +613,10 @@ __device__ __forceinline__ int64_t value_row(const TreeParams& p, const TreeWalk
   return (((static_cast<int64_t>(blk) * p.Hkv + w.h) << bshift) + (key & (p.block_size - 1))) * D;
 }
 // The element there if it is not finite, else 0.
-template <bool FP8>
+template <int F>
 __device__ __forceinline__ float taken_out(const TreeParams& p, int64_t at) {
-  if (FP8) return (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
+  if (F == kCacheE2m1) return p.v_scale[at / kE2m1Group] == 255 ? NAN : 0.f;
+  if (F == kCacheE4m3) return (static_cast<const uint8_t*>(p.v_cache)[at] & 0x7f) == 0x7f ? NAN : 0.f;
   const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[at]);
   return fabsf(v) <= 3.4028234663852886e38f ? 0.f : v;
 }
@@ -420,18 +627,5 @@ __device__ __forceinline__ bool elect_one_lane() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
   return pred != 0;
 }
-
-// Position in a ring of N slots and the parity of its passes.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void advance() {
-    if (++slot == N) {
-      slot = 0;
-      parity ^= 1u;
-    }
-  }
-};
 
 }  // namespace fa

@@ -47,17 +47,21 @@ namespace {
 constexpr int kBN = kTreeBN;
 constexpr int kRowTile = 128;
 constexpr int kMaxRing = 8;
+constexpr int kMaxCodeRing = 8;
 constexpr int kScaleRing = 16;
 constexpr int kTileRing = 8;   // E4M3: tiles whose converted scales are kept
 
-template <int D, bool FP8, int TILES>
+template <int D, int F, int TILES>
 struct Cfg {
-  // Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, idle 11; E4M3: converters 12–15.
-  static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-  static constexpr int kRegsSoftmax = FP8 ? 200 : 208;
-  static constexpr int kRegsOther = FP8 ? 56 : 88;
-  static_assert(2 * kRegsSoftmax + (FP8 ? 2 : 1) * kRegsOther <= (FP8 ? 4 : 3) * kRegsLaunch, "register split");
+  static constexpr bool FP8 = F == kCacheE4m3, FP4 = F == kCacheE2m1;
+  // Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, idle 11; E4M3: converters 12–15; E2M1: all loads 8,
+  // expanders 12–15.
+  static constexpr bool kMore = FP8 || FP4;
+  static constexpr int kThreads = kMore ? 512 : 384;
+  static constexpr int kRegsLaunch = kMore ? 128 : 168;
+  static constexpr int kRegsSoftmax = kMore ? 200 : 208;
+  static constexpr int kRegsOther = kMore ? 56 : 88;
+  static_assert(2 * kRegsSoftmax + (kMore ? 2 : 1) * kRegsOther <= (kMore ? 4 : 3) * kRegsLaunch, "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
   static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;
   static constexpr int kQTile = kRowTile * D * 2;        // bf16, or two E4M3 terms
@@ -65,14 +69,19 @@ struct Cfg {
   static constexpr int kFixed = TILES * kQTile + 2 * kV16;
   static constexpr int kMisc = (FP8 ? 13 : 2) * 1024 + (TILES == 1 ? 4 * 1024 : 0);
   static constexpr int kRoom = 226 * 1024 - kFixed - kMisc;  // 227 KB less the alignment pad
-  static constexpr int kRing = kRoom / kSlot < 14 ? kRoom / kSlot : 14;
+  static constexpr int kRing = FP4 ? (D == 128 ? 4 : 6) : kRoom / kSlot < 14 ? kRoom / kSlot : 14;
   static constexpr int kRK = kRing / 2;
   static constexpr int kRV = kRing - kRK;
   static constexpr int kOffQ = 0;
   static constexpr int kOffV16 = kOffQ + TILES * kQTile;
   static constexpr int kOffK = kOffV16 + 2 * kV16;
   static constexpr int kOffV = kOffK + kRK * kSlot;
-  static constexpr int kOffMisc = kOffV + kRV * kSlot;
+  // E2M1: half tiles of codes in what is left.
+  static constexpr int kCodeRoom = (kRoom - kRing * kSlot) / FourBit<D>::kHalf;
+  static constexpr int kCodeRing = !FP4 ? 1 : kCodeRoom < kMaxCodeRing ? kCodeRoom : kMaxCodeRing;
+  static_assert(!FP4 || kCodeRing >= 3, "codes on their way");
+  static constexpr int kOffCodes = kOffV + kRV * kSlot;
+  static constexpr int kOffMisc = kOffCodes + (FP4 ? kCodeRing * FourBit<D>::kHalf : 0);
   static constexpr int kSmem = kOffMisc + kMisc + 1024;
   static constexpr uint32_t kColO = 256;                 // TMEM: S of the streams at 0 and 128, O at 256 and 256 + D
   static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && kRV + 4 <= kScaleRing && kSmem <= 227 * 1024, "rings");
@@ -80,6 +89,7 @@ struct Cfg {
 };
 
 struct Bars {
+  uint64_t code_full[kMaxCodeRing], code_empty[kMaxCodeRing];  // E2M1
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t s_full[2], p_full[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing];
   uint64_t q_full, drain;
@@ -208,9 +218,10 @@ static __device__ __noinline__ void split_weights(uint32_t addr) {
   tmem_wait_st();
 }
 
-template <int D, bool FP8, int TILES>
-__global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_kernel(const __grid_constant__ TreeParams p) {
-  using C = Cfg<D, FP8, TILES>;
+template <int D, int F, int TILES>
+__global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kernel(const __grid_constant__ TreeParams p) {
+  using C = Cfg<D, F, TILES>;
+  constexpr bool FP8 = C::FP8, FP4 = C::FP4;
   constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
   constexpr int kSlot = C::kSlot;
   constexpr float kLazy = 8.f;             // rescale once the maximum exceeds the reference by this …
@@ -237,11 +248,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
 
   if (tid == 0) {
     for (int s = 0; s < C::kRK; ++s) {
-      mbar_init(&ms->k_full[s], 1);
+      mbar_init(&ms->k_full[s], FP4 ? 4 : 1);
       mbar_init(&ms->k_empty[s], 1);
     }
+    for (int s = 0; FP4 && s < C::kCodeRing; ++s) {
+      mbar_init(&ms->code_full[s], 1);
+      mbar_init(&ms->code_empty[s], 4);
+    }
     for (int s = 0; s < C::kRV; ++s) {
-      mbar_init(&ms->v_full[s], 1);
+      mbar_init(&ms->v_full[s], FP4 ? 4 : 1);
       mbar_init(&ms->v_empty[s], FP8 ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -267,13 +282,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
 
   if (my.count <= 0) {
     // nothing left for this CTA
-  } else if (warp == 8 || warp == 10) {
+  } else if (FP4 && warp >= 12) {
+    reg_dealloc<C::kRegsOther>();
+    if constexpr (FP4)
+      expand_codes<D, C::kCodeRing, C::kRK, C::kRV>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty,
+                                                    smem + C::kOffK, ms->k_full, ms->k_empty, smem + C::kOffV, ms->v_full,
+                                                    ms->v_empty, abort_flag, tree_site(0x30), tid - 384);
+  } else if (FP4 && warp == 8) {
+    reg_dealloc<C::kRegsOther>();
+    if constexpr (FP4)
+      load_codes<D, C::kCodeRing>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty, abort_flag, tree_site(0x21));
+  } else if (!FP4 && (warp == 8 || warp == 10)) {
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------------- loads of K (warp 8) and V (warp 10)
     const bool is_v = warp == 10;
-    load_pages<D, FP8, kScaleRing>(p, my, is_v, smem + (is_v ? C::kOffV : C::kOffK), is_v ? C::kRV : C::kRK,
-                                   is_v ? ms->v_full : ms->k_full, is_v ? ms->v_empty : ms->k_empty, ms->sc_full,
-                                   sc->k_scale[0], sc->v_scale[0], abort_flag, tree_site(is_v ? 0x22 : 0x21));
+    if constexpr (!FP4)
+      load_pages<D, FP8, kScaleRing>(p, my, is_v, smem + (is_v ? C::kOffV : C::kOffK), is_v ? C::kRV : C::kRK,
+                                     is_v ? ms->v_full : ms->k_full, is_v ? ms->v_empty : ms->k_empty, ms->sc_full,
+                                     sc->k_scale[0], sc->v_scale[0], abort_flag, tree_site(is_v ? 0x22 : 0x21));
   } else if (warp == 9) {
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
@@ -648,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
           if (!((bad[u >> 5] >> (u & 31)) & 1) || !token_sees(p, w.b, t, u)) continue;
           const int64_t at = value_row<D>(p, w, u);
           for (int c = c0; c < c0 + kHalf; ++c) {
-            const float v = taken_out<FP8>(p, at + c);
+            const float v = taken_out<F>(p, at + c);
             if (v == 0.f) continue;
             if (!whole)
               part_o[(c & ~3) * 32 + (c & 3)] += v;
@@ -780,9 +806,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, TILES>::kThreads, 1) tree_wide_ker
   }
 }
 
-template <int D, bool FP8, int TILES>
+template <int D, int F, int TILES>
 cudaError_t launch(const TreeParams& p, cudaStream_t s) {
-  using C = Cfg<D, FP8, TILES>;
+  using C = Cfg<D, F, TILES>;
   static_assert(sizeof(Bars) % 8 == 0 && offsetof(Scales, k_scale) % 16 == 0 && offsetof(Scales, v_scale) % 16 == 0 &&
                     offsetof(Scales, ks) % 16 == 0 && C::kOffMisc % 16 == 0,
                 "bulk copies and 16-byte accesses");
@@ -791,33 +817,41 @@ cudaError_t launch(const TreeParams& p, cudaStream_t s) {
   cudaError_t e;
   if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, tree_wide_kernel<D, FP8, TILES>);
+    e = cudaFuncGetAttributes(&a, tree_wide_kernel<D, F, TILES>);
     if (e != cudaSuccess) return e;
     if (a.numRegs < C::kRegsLaunch) return cudaErrorInvalidConfiguration;
     checked.store(true, std::memory_order_relaxed);
   }
-  e = cudaFuncSetAttribute(tree_wide_kernel<D, FP8, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  e = cudaFuncSetAttribute(tree_wide_kernel<D, F, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  tree_wide_kernel<D, FP8, TILES>
+  tree_wide_kernel<D, F, TILES>
       <<<dim3(static_cast<unsigned>(p.row_tiles), static_cast<unsigned>(p.parts)), C::kThreads, C::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
 // Two row tiles share a CTA's keys where there are more than 128 rows.  Below, the second would be empty: 64 and 128
 // rows with shared rows or with two tiles, E4M3 76, 84 | 114, 121 us, bf16 98, 103 | 103, 109 us (8 x 16384 keys).
-template <int D, bool FP8>
+template <int D, int F>
 cudaError_t launch_tiles(const TreeParams& p, cudaStream_t s) {
-  return p.T * p.G <= kRowTile ? launch<D, FP8, 1>(p, s) : launch<D, FP8, 2>(p, s);
+  return p.T * p.G <= kRowTile ? launch<D, F, 1>(p, s) : launch<D, F, 2>(p, s);
 }
 
 }  // namespace
 
 int tree_cta_rows(int64_t rows) { return rows <= kRowTile ? kRowTile : 2 * kRowTile; }
 
-cudaError_t launch_tree_wide(const TreeParams& p, int d, bool fp8, cudaStream_t s) {
-  if (d == 128) return fp8 ? launch_tiles<128, true>(p, s) : launch_tiles<128, false>(p, s);
-  if (d == 64) return fp8 ? launch_tiles<64, true>(p, s) : launch_tiles<64, false>(p, s);
+template <int D>
+static cudaError_t launch_format(const TreeParams& p, int format, cudaStream_t s) {
+  switch (format) {
+    case kCacheBf16: return launch_tiles<D, kCacheBf16>(p, s);
+    case kCacheE4m3: return launch_tiles<D, kCacheE4m3>(p, s);
+    case kCacheE2m1: return launch_tiles<D, kCacheE2m1>(p, s);
+  }
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_tree_wide(const TreeParams& p, int d, int format, cudaStream_t s) {
+  return d == 128 ? launch_format<128>(p, format, s) : d == 64 ? launch_format<64>(p, format, s) : cudaErrorInvalidValue;
 }
 
 }  // namespace fa

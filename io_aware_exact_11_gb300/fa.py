@@ -21,7 +21,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfa.so")
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_DEVICE_TIMEOUT = range(5)
-FA_BF16, FA_FP32, FA_E4M3 = 0, 1, 2
+FA_BF16, FA_FP32, FA_E4M3, FA_E2M1 = 0, 1, 2, 3
 FA_MASK_NONE, FA_MASK_CAUSAL = 0, 1
 FA_ROPE_HALF, FA_ROPE_INTERLEAVED = 0, 1
 
@@ -42,8 +42,15 @@ EXPORTED = (
     "fa_backward",
     "fa_backward_masked",
     "fa_rope",
+    "fa_rope_axes",
     "fa_cache_append",
     "fa_cache_gather",
+    "fa_cache_compact",
+    "fa_cache_copy_pages",
+    "fa_pages_fork",
+    "fa_pages_free",
+    "fa_pages_reserve_workspace_size",
+    "fa_pages_reserve",
     "fa_decode_tree_workspace_size",
     "fa_decode_tree",
     "fa_device_status",
@@ -101,10 +108,24 @@ def lib() -> ctypes.CDLL:
         L.fa_backward_masked.restype = i32
         L.fa_rope.argtypes = [vp] * 4 + [i32] * 7 + [vp, vp, ctypes.c_int64, i32, vp, f32, i32, i32, vp]
         L.fa_rope.restype = i32
+        L.fa_rope_axes.argtypes = [vp] * 4 + [i32] * 7 + [vp, vp, i32, ctypes.c_int64, ctypes.c_int64, vp, vp, f32, i32, i32, vp]
+        L.fa_rope_axes.restype = i32
         L.fa_cache_append.argtypes = [vp] * 9 + [i32] * 8 + [vp, vp]
         L.fa_cache_append.restype = i32
         L.fa_cache_gather.argtypes = [vp] * 8 + [i32] * 8 + [vp, vp]
         L.fa_cache_gather.restype = i32
+        L.fa_cache_compact.argtypes = [vp] * 7 + [ctypes.c_int64, vp] + [i32] * 8 + [vp]
+        L.fa_cache_compact.restype = i32
+        L.fa_cache_copy_pages.argtypes = [vp] * 6 + [i32] * 6 + [vp]
+        L.fa_cache_copy_pages.restype = i32
+        L.fa_pages_fork.argtypes = [vp] * 5 + [i32] * 5 + [vp]
+        L.fa_pages_fork.restype = i32
+        L.fa_pages_free.argtypes = [vp] * 5 + [i32] * 5 + [vp]
+        L.fa_pages_free.restype = i32
+        L.fa_pages_reserve_workspace_size.argtypes = [i32, i32]
+        L.fa_pages_reserve_workspace_size.restype = sz
+        L.fa_pages_reserve.argtypes = [vp] * 7 + [i32] * 4 + [vp, sz, vp]
+        L.fa_pages_reserve.restype = i32
         L.fa_decode_tree_workspace_size.argtypes = [i32] * 6
         L.fa_decode_tree_workspace_size.restype = sz
         L.fa_decode_tree.argtypes = [vp] * 9 + [ctypes.c_int64, vp, vp] + [i32] * 9 + [f32, vp, i32, vp, sz, vp]
@@ -582,13 +603,13 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     return w, 1.0
 
 
-def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, stream, inverse):
+def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, stream, inverse, axes=None):
     torch = _torch()
     dev = _device_of(q, k, positions, out_q, out_k)
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
-            return _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, None, inverse)
+            return _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, None, inverse, axes)
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q must be [B, Hq, N, d] and k [B, Hk, N, d]")
     B, Hq, N, d = q.shape
@@ -611,7 +632,24 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
     if w.ndim != 1:
         raise ValueError("inv_freq must be one row of rot_dim/2 values")
     pos_ptr, pos_sb = None, 0
-    if positions is not None:
+    if axes is not None:
+        if positions.dtype != torch.int32:
+            raise TypeError("positions must be int32")
+        shape, step = positions.shape, positions.stride()
+        if len(shape) not in (2, 3) or shape[1:] != (B, N)[3 - len(shape):] or (N > 1 and step[-1] != 1):
+            raise ValueError("positions must be [axes, N] or [axes, B, N] with the last dim contiguous")
+        if isinstance(axes, torch.Tensor) and axes.dtype == torch.int32 and not axes.is_cuda:
+            a = axes.contiguous()
+            a_ptr = a.data_ptr()
+        else:
+            a = np.ascontiguousarray(axes, dtype=np.int32)
+            a_ptr = a.tobytes()
+        if a.shape != w.shape:
+            raise ValueError("axes must name one axis for each of inv_freq's pairs")
+        pos_ptr = positions.data_ptr()
+        pos_sa = step[0] if shape[0] > 1 else 0
+        pos_sb = step[1] if len(shape) == 3 and B > 1 else 0
+    elif positions is not None:
         if positions.dtype != torch.int32:
             raise TypeError("positions must be int32")
         shape = positions.shape
@@ -631,6 +669,14 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
         else:
             _check_out("out_k", out_k, k.shape, q.dtype, dev)
         st = _strides(q, k, out_q, out_k)
+    if axes is not None:
+        status = lib().fa_rope_axes(q.data_ptr(), _addr(k), out_q.data_ptr(), _addr(out_k), B, Hq, Hk, N, d,
+                                    2 * w.shape[0], code, st, pos_ptr, shape[0], pos_sa, pos_sb, a_ptr, w_ptr,
+                                    float(magnitude), FA_ROPE_INTERLEAVED if interleaved else FA_ROPE_HALF, inverse,
+                                    _current_stream(dev))
+        if status:
+            _check(status)
+        return out_q, out_k
     if not -(1 << 31) <= position0 < 1 << 31:
         raise ValueError("position0 must be an int32")
     status = lib().fa_rope(q.data_ptr(), _addr(k), out_q.data_ptr(), _addr(out_k), B, Hq, Hk, N, d, 2 * w.shape[0],
@@ -659,17 +705,45 @@ def rope_backward(dq, dk, inv_freq, positions=None, position0: int = 0, magnitud
     return _rope(dq, dk, inv_freq, positions, position0, magnitude, interleaved, out_q, out_k, stream, 1)
 
 
+def rope_axes(q, k, inv_freq, axes, positions, magnitude: float = 1.0, interleaved: bool = False, out_q=None,
+              out_k=None, stream=None):
+    """Rotary positions with several axes (time, height and width of a patch, say); returns (q', k').
+
+    As ``rope``, with a position on each of up to four axes per token: ``positions`` is int32 [axes, N] or [axes, B, N] on
+    the device, and pair i turns by positions[axes[i]]·inv_freq[i].  ``axes`` (on the host, one number per pair) may give
+    each axis a block of pairs or take turns.
+    """
+    return _rope(q, k, inv_freq, positions, 0, magnitude, interleaved, out_q, out_k, stream, 0, axes)
+
+
+def rope_axes_backward(dq, dk, inv_freq, axes, positions, magnitude: float = 1.0, interleaved: bool = False, out_q=None,
+                       out_k=None, stream=None):
+    """Gradients of ``rope_axes``'s inputs from those of its outputs; same arguments as the forward call."""
+    return _rope(dq, dk, inv_freq, positions, 0, magnitude, interleaved, out_q, out_k, stream, 1, axes)
+
+
+E2M1_GROUP = 32  # elements of a row that share a scale byte
+
+
 def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table):
-    """Checks a paged cache; returns (num_blocks, Hkv, block_size, d, dtype code)."""
+    """Checks a paged cache; returns (num_blocks, Hkv, block_size, d, dtype code).  One-byte elements are E4M3 codes, or,
+    where the scales have a fourth dimension, pairs of E2M1 codes."""
     torch = _torch()
     shape, dtype = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, d]")
     if v_cache.dtype != dtype:
         raise TypeError("k_cache and v_cache must share a dtype")
-    contiguous = k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()
+    contiguous = k_cache.is_contiguous() and v_cache.is_contiguous() and (block_table is None or block_table.is_contiguous())
     if dtype == torch.bfloat16:
         code = FA_BF16
+    elif dtype == torch.uint8 and k_scale is not None and k_scale.dim() == 4:
+        code = FA_E2M1
+        shape = (*shape[:3], 2 * shape[3])
+        for s in (k_scale, v_scale):
+            if s is None or s.dtype != torch.uint8 or s.shape != (*shape[:3], shape[3] // E2M1_GROUP):
+                raise ValueError("an E2M1 cache needs uint8 k_scale and v_scale [num_blocks, Hkv, block_size, d/32]")
+            contiguous = contiguous and s.is_contiguous()
     elif dtype == torch.float8_e4m3fn or dtype == torch.uint8:
         code = FA_E4M3
         for s in (k_scale, v_scale):
@@ -678,7 +752,7 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table):
             contiguous = contiguous and s.is_contiguous()
     else:
         raise TypeError(f"unsupported cache dtype {dtype} (bfloat16, float8_e4m3fn or uint8 codes)")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+    if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2):
         raise TypeError("block_table must be int32 [B, max_blocks]")
     if not contiguous:
         raise ValueError("caches, scales and block_table must be contiguous")
@@ -697,7 +771,8 @@ def cache_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, k_sc
     Token n of sequence b goes to logical position start[b] + n (start: int32 [B]); with ``new_lens`` (int32 [B]) only
     the first new_lens[b] are written.  k_cache/v_cache [num_blocks, Hkv, block_size, d]: bfloat16 takes the rows as
     they are; float8_e4m3fn (or uint8 codes) quantises each row with the power of two whose E8M0 byte goes to
-    k_scale/v_scale (uint8 [num_blocks, Hkv, block_size]).
+    k_scale/v_scale (uint8 [num_blocks, Hkv, block_size]); uint8 [num_blocks, Hkv, block_size, d/2] with scales
+    [num_blocks, Hkv, block_size, d/32] holds E2M1 codes, two to a byte, with a power of two for every 32 elements.
     """
     torch = _torch()
     dev = _device_of(k, v, k_cache, v_cache, block_table, start, new_lens, k_scale, v_scale)
@@ -756,6 +831,148 @@ def cache_gather(k_cache, v_cache, block_table, seq_lens, n: int, k_scale=None, 
     return out_k, out_v
 
 
+def cache_compact(k_cache, v_cache, block_table, first, keep, keep_lens=None, k_scale=None, v_scale=None, stream=None):
+    """Moves the kept rows of every sequence together, in place (accepted drafts, or what an eviction leaves).
+
+    Row keep[b, i] of sequence b (a position; int32 [B,N] or [N]) goes to position first[b] + i (int32 [B]) for
+    i < keep_lens[b] (int32 [B]; None: N).  keep[b, i] >= first[b] + i, in any order.  Caches and scales as for
+    ``cache_append``; the pages written must not be shared with another sequence.
+    """
+    torch = _torch()
+    dev = _device_of(k_cache, v_cache, block_table, first, keep, keep_lens, k_scale, v_scale)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return cache_compact(k_cache, v_cache, block_table, first, keep, keep_lens, k_scale, v_scale)
+    nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    B, max_blocks = block_table.shape
+    _check_lens("first", first, B)
+    if keep_lens is not None:
+        _check_lens("keep_lens", keep_lens, B)
+    shape = keep.shape
+    if keep.dtype != torch.int32:
+        raise TypeError("keep must be int32")
+    if len(shape) not in (1, 2) or (len(shape) == 2 and shape[0] != B) or (shape[-1] > 1 and keep.stride(-1) != 1):
+        raise ValueError(f"keep must be [N] or [{B}, N] with the last dim contiguous")
+    status = lib().fa_cache_compact(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                    block_table.data_ptr(), first.data_ptr(), keep.data_ptr(),
+                                    keep.stride(0) if len(shape) == 2 and B > 1 else 0, _addr(keep_lens), B, hkv,
+                                    shape[-1], nb, bs, max_blocks, d, code, _current_stream(dev))
+    if status:
+        _check(status)
+
+
+def cache_copy_pages(k_cache, v_cache, src, dst, k_scale=None, v_scale=None, stream=None):
+    """Copies whole pages within a pool, page src[i] to page dst[i] (int32 [n]; −1 in both: nothing to copy).
+
+    No page may be written twice in one call, or written and read.
+    """
+    dev = _device_of(k_cache, v_cache, src, dst, k_scale, v_scale)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return cache_copy_pages(k_cache, v_cache, src, dst, k_scale, v_scale)
+    nb, hkv, bs, d, code = _cache_args(k_cache, v_cache, k_scale, v_scale, None)
+    n = src.shape[0] if src.dim() == 1 else -1
+    _check_lens("src", src, n)
+    _check_lens("dst", dst, n)
+    status = lib().fa_cache_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                       src.data_ptr(), dst.data_ptr(), n, hkv, nb, bs, d, code, _current_stream(dev))
+    if status:
+        _check(status)
+
+
+def _check_pages(block_table, seq_lens, holders):
+    """Checks the tables of a page pool; returns (B, max_blocks, num_blocks)."""
+    torch = _torch()
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise TypeError("block_table must be contiguous int32 [B, max_blocks]")
+    B, max_blocks = block_table.shape
+    _check_lens("seq_lens", seq_lens, B)
+    nb = holders.shape[0] if holders.dim() == 1 else -1
+    _check_lens("holders", holders, nb)
+    return B, max_blocks, nb
+
+
+def pages_fork(block_table, seq_lens, holders, src, dst, block_size: int, stream=None):
+    """Sequences dst[i], empty so far, take the pages and the length of sequences src[i] (int32 [n]), in place.
+
+    ``block_table`` int32 [B, max_blocks] (−1 where there is no page), ``seq_lens`` int32 [B] and ``holders`` int32
+    [num_blocks], the number of sequences that hold each page (0: free).  Nothing is copied: who writes into a page that
+    others hold gets one of its own from ``pages_reserve``.
+    """
+    dev = _device_of(block_table, seq_lens, holders, src, dst)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return pages_fork(block_table, seq_lens, holders, src, dst, block_size)
+    B, max_blocks, nb = _check_pages(block_table, seq_lens, holders)
+    n = src.shape[0] if src.dim() == 1 else -1
+    _check_lens("src", src, n)
+    _check_lens("dst", dst, n)
+    status = lib().fa_pages_fork(block_table.data_ptr(), seq_lens.data_ptr(), holders.data_ptr(), src.data_ptr(),
+                                 dst.data_ptr(), n, B, nb, block_size, max_blocks, _current_stream(dev))
+    if status:
+        _check(status)
+
+
+def pages_free(block_table, seq_lens, holders, seqs, block_size: int, keep_lens=None, stream=None):
+    """Sequences seqs[i] (int32 [n]) give up their pages, all but those of the first keep_lens[i] tokens (int32 [n]).
+
+    In place: their entries become −1, their lengths at most keep_lens[i] (0 without), and pages that nobody holds any
+    more are free.
+    """
+    dev = _device_of(block_table, seq_lens, holders, seqs, keep_lens)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return pages_free(block_table, seq_lens, holders, seqs, block_size, keep_lens)
+    B, max_blocks, nb = _check_pages(block_table, seq_lens, holders)
+    n = seqs.shape[0] if seqs.dim() == 1 else -1
+    _check_lens("seqs", seqs, n)
+    if keep_lens is not None:
+        _check_lens("keep_lens", keep_lens, n)
+    status = lib().fa_pages_free(block_table.data_ptr(), seq_lens.data_ptr(), holders.data_ptr(), seqs.data_ptr(),
+                                 _addr(keep_lens), n, B, nb, block_size, max_blocks, _current_stream(dev))
+    if status:
+        _check(status)
+
+
+def pages_reserve_workspace_size(B: int, num_blocks: int) -> int:
+    return int(lib().fa_pages_reserve_workspace_size(B, num_blocks))
+
+
+def pages_reserve(block_table, seq_lens, holders, new_lens, block_size: int, workspace=None, stream=None):
+    """Pages for the next new_lens[b] tokens of every sequence (int32 [B]); returns (granted, copy_src, copy_dst), int32 [B].
+
+    Missing table entries get free pages, and a sequence whose next token goes into a page that others hold too gets one
+    of its own in its place: copy_src[b] → copy_dst[b] (−1: nothing), to be copied with ``cache_copy_pages`` before
+    anything is written.  Sequences are served in order, from the free pages by rising number; from the first one that
+    finds too few on, none with tokens to come is (granted[b] = 0, its table as it was).
+    """
+    torch = _torch()
+    dev = _device_of(block_table, seq_lens, holders, new_lens, workspace)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return pages_reserve(block_table, seq_lens, holders, new_lens, block_size, workspace)
+    B, max_blocks, nb = _check_pages(block_table, seq_lens, holders)
+    _check_lens("new_lens", new_lens, B)
+    out = torch.empty((3, B), dtype=torch.int32, device=block_table.device)
+    if workspace is None:
+        workspace = torch.empty(max(pages_reserve_workspace_size(B, nb), 16), dtype=torch.uint8, device=block_table.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    granted, src, dst = out.unbind()
+    status = lib().fa_pages_reserve(block_table.data_ptr(), seq_lens.data_ptr(), holders.data_ptr(), new_lens.data_ptr(),
+                                    granted.data_ptr(), src.data_ptr(), dst.data_ptr(), B, nb, block_size, max_blocks,
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _current_stream(dev))
+    if status:
+        _check(status)
+    return granted, src, dst
+
+
 def decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, d: int, max_parts: int = 0) -> int:
     """Workspace bytes with which ``decode_tree`` uses the whole current device (or at most ``max_parts`` CTAs)."""
     return int(lib().fa_decode_tree_workspace_size(B, Hq, Hkv, T, d, max_parts))
@@ -769,8 +986,8 @@ def decode_tree(q, k_cache, v_cache, block_table, seq_lens, tree_mask=None, draf
     q [B,Hq,T,d] bf16 (strided or not).  The drafted tokens' keys are in the cache: seq_lens[b] counts them, and the
     last draft_lens[b] (int32 [B]; None: T) keys of sequence b are theirs.  Token t sees the context before them and
     drafted key u where tree_mask[b, t, u] (bool or uint8 [B,T,T] or [T,T]; None: u <= t).  Rows that see nothing,
-    padding rows t >= draft_lens[b] among them, give O = 0 and LSE = −inf.  The cache is bfloat16, or float8_e4m3fn
-    with k_scale/v_scale as ``cache_append`` writes it.  O like q (contiguous), LSE fp32 [B,Hq,T].  The work is cut
+    padding rows t >= draft_lens[b] among them, give O = 0 and LSE = −inf.  The cache is bfloat16, or E4M3 or E2M1 codes
+    with k_scale/v_scale as ``cache_append`` writes them.  O like q (contiguous), LSE fp32 [B,Hq,T].  The work is cut
     into equal parts over the machine (at most ``max_parts``, 0: no limit), fewer where a given workspace is small.
     """
     torch = _torch()

@@ -86,3 +86,117 @@ def tree_attention(q, k, v, drafts: int, mask, scale: float):
         lse[t] = m + np.log(e.sum())
         p_all[t, sees] = p
     return o, lse, p_all
+
+
+# ------------------------------------------------------------------ several axes, four bits, pages
+
+
+def rope_axes(x, positions, axes, inv_freq, magnitude: float = 1.0, interleaved: bool = False, inverse: bool = False):
+    """x [B,H,N,d], positions [A,B,N]: pair i turns by positions[axes[i]]·inv_freq[i], as in ``rope``."""
+    x, w = np.asarray(x, dtype=np.float64), np.asarray(inv_freq, dtype=np.float64)
+    r, out = 2 * len(w), np.array(x, dtype=np.float64)
+    for i, a in enumerate(axes):
+        turn = magnitude * np.exp((-1j if inverse else 1j) * (np.asarray(positions[int(a)], dtype=np.float64) * w[i]))[:, None]
+        one, two = (2 * i, 2 * i + 1) if interleaved else (i, i + r // 2)
+        z = (x[..., one] + 1j * x[..., two]) * turn
+        out[..., one], out[..., two] = z.real, z.imag
+    return out
+
+
+E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])  # code = index; bit 3 is the sign
+
+
+def round_e2m1(y):
+    """Codes of the nearest E2M1 values (ties to the even code, saturating), by search in the table of values."""
+    a = np.minimum(np.abs(np.asarray(y, dtype=np.float64)), 6.0)
+    hi = np.clip(np.searchsorted(E2M1_VALUES, a), 1, 7)
+    lo = hi - 1
+    dl, dh = a - E2M1_VALUES[lo], E2M1_VALUES[hi] - a
+    code = np.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)
+    return (code | np.where(np.signbit(y), 8, 0)).astype(np.uint8)
+
+
+def quantise_groups(x, group: int = 32):
+    """Rows [..., d] -> (codes [..., d], scale bytes [..., d/group], values [..., d]).
+
+    k is the smallest whole number in [−126, 125] with max|x| <= 6·2^k over the
+    group; a group with an infinity or NaN is NaN (byte 255, codes 0).
+    """
+    x = np.asarray(x, dtype=np.float64)
+    g = x.reshape(*x.shape[:-1], x.shape[-1] // group, group)
+    fine = np.isfinite(g).all(-1)
+    top = np.where(fine, np.abs(np.where(np.isfinite(g), g, 0)).max(-1), 0.0)
+    k = np.searchsorted(6.0 * 2.0 ** np.arange(-126.0, 125.0), top) - 126  # the first that is not below
+    power = 2.0 ** k[..., None].astype(np.float64)
+    codes = np.where(fine[..., None], round_e2m1(np.where(fine[..., None], g, 0.0) / power), 0).astype(np.uint8)
+    values = np.where(codes & 8, -1.0, 1.0) * E2M1_VALUES[codes & 7] * power
+    values = np.where(fine[..., None], values, np.nan)
+    return codes.reshape(x.shape), np.where(fine, k + 127, 255).astype(np.uint8), values.reshape(x.shape)
+
+
+class Pool:
+    """Pages shared, freed and reserved, one sequence after the other with plain lists.
+
+    ``table`` rows are lists of page ids padded with −1, ``holders`` counts the
+    sequences that name a page.
+    """
+
+    def __init__(self, table, lens, holders, bs: int):
+        self.table, self.lens, self.holders, self.bs = [list(r) for r in table], list(lens), list(holders), bs
+
+    def _pages(self, n):
+        return -(-n // self.bs)
+
+    def fork(self, src, dst):
+        was = list(self.lens), [list(r) for r in self.table]
+        for i, (s, t) in enumerate(zip(src, dst)):
+            B = len(self.lens)
+            if not (0 <= s < B and 0 <= t < B) or t in dst[:i] or s in dst:
+                continue
+            if was[0][t] != 0 or any(p >= 0 for p in was[1][t]):
+                continue
+            used = self._pages(self.lens[s])
+            self.table[t] = self.table[s][:used] + [-1] * (len(self.table[s]) - used)
+            self.lens[t] = self.lens[s]
+            for p in self.table[t][:used]:
+                self.holders[p] += 1
+
+    def free(self, seqs, keep=None):
+        for i, b in enumerate(seqs):
+            n = 0 if keep is None else keep[i]
+            if not 0 <= b < len(self.lens) or b in seqs[:i] or n < 0:
+                continue
+            self.lens[b] = min(self.lens[b], n)
+            for j in range(self._pages(self.lens[b]), len(self.table[b])):
+                if self.table[b][j] >= 0:
+                    self.holders[self.table[b][j]] -= 1
+                    self.table[b][j] = -1
+
+    def reserve(self, new):
+        B = len(self.lens)
+        granted, src, dst = [0] * B, [-1] * B, [-1] * B
+        free = [p for p, n in enumerate(self.holders) if n == 0]
+        short = False
+        for b in range(B):
+            row, n = self.table[b], self.lens[b]
+            if new[b] == 0:
+                granted[b] = 1
+                continue
+            if new[b] < 0 or n + new[b] > len(row) * self.bs:
+                continue
+            at = n // self.bs
+            own = n % self.bs != 0 and self.holders[row[at]] > 1
+            missing = [j for j in range(self._pages(n), self._pages(n + new[b])) if row[j] < 0]
+            short = short or own + len(missing) > len(free)
+            if short:
+                continue
+            granted[b] = 1
+            if own:
+                src[b], dst[b] = row[at], free.pop(0)
+                self.holders[src[b]] -= 1
+                self.holders[dst[b]] = 1
+                row[at] = dst[b]
+            for j in missing:
+                row[j] = free.pop(0)
+                self.holders[row[j]] = 1
+        return granted, src, dst
