@@ -77,8 +77,7 @@ namespace {
 constexpr int kBN = kTreeBN;
 constexpr int kPBlock = kBN * 128;       // P̃ᵀ: one 128-byte row per key
 constexpr int kMaxRing = 8;
-constexpr int kMaxCodeRing = 16;
-// Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11; E2M1: all loads 8, expanders 12–15.
+// Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, Q loads 11; E2M1: value converters 12–19, key converters 20–23.
 // Registers per thread at launch and after the warpgroups' split.  A softmax thread holds its scores and partial
 // sums, 2·NR values, and a spilled one would go to L2, shared memory leaving next to no L1.
 constexpr int kScaleRing = 16;           // E4M3: tiles whose scale bytes are staged (V slots and four more)
@@ -89,67 +88,75 @@ constexpr int kBadRing = 8;              // pieces whose flags of bad values may
 template <int D, int F, int NR>
 struct Cfg {
   static constexpr bool FP8 = F == kCacheE4m3, FP4 = F == kCacheE2m1;
-  // E2M1: four warps more, which write the tiles out as bf16.
-  static constexpr int kThreads = FP4 ? 512 : 384;
-  static constexpr int kRegsLaunch = FP4 ? 128 : 168;
-  static constexpr int kRegsSoftmax = FP4 ? (NR == 16 ? 176 : 192) : 208;
-  static constexpr int kRegsOther = FP4 ? (NR == 16 ? 80 : 64) : 88;
-  static_assert(2 * kRegsSoftmax + (FP4 ? 2 : 1) * kRegsOther <= (FP4 ? 4 : 3) * kRegsLaunch, "register split");
-  static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
-  static constexpr int kTerms = FP8 ? 1 : 2;                  // of P̃
+  static constexpr bool kWiden = FP8 || FP4;  // V is widened to fp16
+  // E2M1: a warpgroup more for each stream, which widens the values, and one which lays out the keys.
+  static constexpr int kThreads = FP4 ? 768 : 384;
+  static constexpr int kRegsLaunch = FP4 ? 80 : 168;
+  static constexpr int kRegsSoftmax = FP4 ? 120 : 208;
+  static constexpr int kRegsConvert = FP4 ? 64 : 0;
+  static constexpr int kRegsOther = FP4 ? 56 : 88;
+  static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + (FP4 ? 2 : 1) * kRegsOther <= kThreads / 128 * kRegsLaunch,
+                "register split");
+  static constexpr int kSlot = kBN * D * (kWiden ? 1 : 2);    // of a K tile as the products read it
+  static constexpr int kTerms = kWiden ? 1 : 2;               // of P̃
   static constexpr int kPCols = kTerms * NR;                  // columns of P̃ᵀ and of Oᵀ
-  // A key's P̃ᵀ row is 2·kPCols bytes; the streams' rows lie side by side in 128 bytes where both fit.
-  static constexpr int kPNext = !FP8 && kPCols <= 32 ? kPCols * 2 : kPBlock;  // from a stream's rows to the other's
-  static constexpr int kP = !FP8 && kPCols <= 32 ? kPBlock : 2 * kPBlock;
-  static constexpr int kQTile = FP8 ? 2 * NR * D : NR * D * 2;
-  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;          // a stream's widened V tile
+  // A key's P̃ᵀ row is 2·kPCols bytes (twice that for two terms of a tile in bf16); the streams' rows lie side by side in
+  // 128 bytes where both fit.
+  static constexpr int kPRow = FP8 ? 128 : FP4 ? 4 * NR : 2 * kPCols;
+  static constexpr int kPNext = kPRow <= 64 ? kPRow : kPBlock;  // from a stream's rows to the other's
+  static constexpr int kP = kPRow <= 64 ? kPBlock : 2 * kPBlock;
+  static constexpr int kQTile = kWiden ? 2 * NR * D : NR * D * 2;
+  static constexpr int kV16 = kWiden ? kBN * D * 2 : 0;       // a stream's widened V tile
   static constexpr int kFixed = 2 * kV16 + kP + kQTile;
   // K and V ring slots in what is left of 227 KB after this, the bookkeeping and the alignment pad.
   static constexpr int kMisc = (FP8 ? 9 : 6) * 1024;
   static constexpr int kRoom = 226 * 1024 - kMisc - kFixed;
-  static constexpr int kRing = FP4 ? (D == 128 ? 4 : 6) : kRoom / kSlot < 14 ? kRoom / kSlot : 14;
-  static constexpr int kRK = kRing / 2;
-  static constexpr int kRV = kRing - kRK;
-  // E2M1: half tiles of codes in what is left.
-  static constexpr int kCodeRoom = (kRoom - kRing * kSlot) / FourBit<D>::kHalf;
-  static constexpr int kCodeRing = !FP4 ? 1 : kCodeRoom < kMaxCodeRing ? kCodeRoom : kMaxCodeRing;
+  static constexpr int kRing = kRoom / kSlot < 14 ? kRoom / kSlot : 14;
+  static constexpr int kRK = FP4 ? 4 : kRing / 2;  // (E2M1: two for each stream)
+  // E2M1: codes of as many tiles as fit, in two rings.
+  static constexpr int kCodeRoom = (kRoom - kRK * kSlot) / (2 * FourBit<D>::kHalf);
+  static constexpr int kRC = !FP4 ? 1 : kCodeRoom < kMaxRing ? kCodeRoom : kMaxRing;
+  static constexpr int kRV = FP4 ? kRC : kRing - kRK;
   static constexpr int kOffK = 0;
-  static constexpr int kOffV = kOffK + kRK * kSlot;
-  static constexpr int kOffV16 = kOffV + kRV * kSlot;
+  static constexpr int kOffV16 = kOffK + kRK * kSlot + (FP4 ? 0 : kRV * kSlot);
   static constexpr int kOffP = kOffV16 + 2 * kV16;
   static constexpr int kOffQ = kOffP + kP;
-  static constexpr int kOffCodes = kOffQ + kQTile;
-  static constexpr int kOffMisc = kOffCodes + (FP4 ? kCodeRing * FourBit<D>::kHalf : 0);
-  static constexpr int kSCols = FP8 ? 2 * NR : NR;            // TMEM columns of one stream's S
+  static constexpr int kOffCodes = kOffQ + kQTile;            // E2M1: of keys, then of values
+  static constexpr int kOffV = FP4 ? kOffCodes + kRC * FourBit<D>::kHalf : kOffK + kRK * kSlot;
+  static constexpr int kOffMisc = FP4 ? kOffV + kRV * FourBit<D>::kHalf : kOffCodes;
+  static constexpr int kSCols = kWiden ? 2 * NR : NR;         // TMEM columns of one stream's S
   static constexpr int kColO = 2 * kSCols;
-  static constexpr int kCols = kColO + 2 * kPCols;
+  static constexpr int kColScales = kColO + 2 * kPCols;       // E2M1: of each K tile's scales, and of ones
+  static constexpr int kCols = kColScales + (FP4 ? 20 : 0);
   static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && kRV + 4 <= kScaleRing, "rings");
+  static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && (!FP8 || kRV + 4 <= kScaleRing), "rings");
   static_assert(kQTile % 1024 == 0 && kSlot % 1024 == 0 && kCols <= 512, "swizzle atoms, TMEM");
-  static_assert(!FP4 || kCodeRing >= 3, "codes on their way");
 };
 
 template <int NR, int F>
 struct Misc {
   static constexpr bool FP8 = F == kCacheE4m3;
-  uint64_t code_full[F == kCacheE2m1 ? kMaxCodeRing : 1], code_empty[F == kCacheE2m1 ? kMaxCodeRing : 1];
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
+  uint64_t code_full[F == kCacheE2m1 ? kMaxRing : 1], code_empty[F == kCacheE2m1 ? kMaxRing : 1];
+  uint64_t ref_full[2][2], v16_full[2];  // E2M1: per stream (and tile)
+  int ref[2][2];                       // E2M1: 2·(exponent that a stream's widened tile is relative to) + (it is bf16)
+  int range[2][2][4];                  // E2M1: per stream, tile and warp
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], sc_full[kScaleRing], q_full, q_empty, drain;
   alignas(16) float nm[2][NR];         // minus the reference maxima (log2 units), 0 while a row has seen nothing
-  alignas(16) float f[kFRing][NR];     // E4M3: what a row's raw scores are multiplied by
+  alignas(16) float f[kFRing][NR];     // E4M3, E2M1: what a row's raw scores are multiplied by
   float corr[2][NR];                   // factor of the last rescale
   float red[2][4][NR];                 // per-warp maxima or sums
   float scale[2][NR];                  // what a stream's O is multiplied by in the end
-  float kv_scale[2];                   // E4M3: and by this
+  float kv_scale[2];                   // E4M3, E2M1: and by this
   int64_t row[2][NR];                  // (b·Hq + h)·T + t of a live row, or −1
   int64_t o_off[2][NR];                // its element offset in O
   int fresh[2][NR];                    // a live row that has seen nothing yet
-  int far[2];                          // E4M3: the stream's tile has gone over to bf16
+  int far[2];                          // E4M3, E2M1: the stream's tile has gone over to bf16
   int kv_red[2][4];                    // per stream and warp
   alignas(16) uint8_t k_scale[FP8 ? kScaleRing : 1][kBN];  // written by bulk copies
   alignas(16) uint8_t v_scale[FP8 ? kScaleRing : 1][kBN];
   uint32_t bad[kBadRing][8];           // drafted keys with non-finite values (one bit each)
-  long long warp_sum[16];
+  long long warp_sum[24];
   int start[3];
   uint32_t tmem_base;
   int abort_flag;
@@ -229,8 +236,8 @@ __device__ __forceinline__ void rescale_cols(uint32_t addr, const float* w, floa
 }
 
 // The query rows of a piece as a K-major operand (rows that are not there as
-// zeros), by NT threads.  E4M3: two terms per element and the factor of the row.
-template <int D, bool FP8, int NR, int NT, int kBatchMax>
+// zeros), by NT threads.  E4M3, E2M1: two terms per element and the factor of the row.
+template <int D, int F, int NR, int NT, int kBatchMax>
 __device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, uint8_t* q_smem, float* f, int id) {
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
   constexpr int kPer = (NR * kChunks + NT - 1) / NT;
@@ -256,7 +263,7 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, u
       const int r = i / kChunks, ch = i % kChunks;
       if (r >= NR) continue;  // whole warps: a row is held by neighbouring lanes
       const uint4 v = q4[e8];
-      if constexpr (!FP8) {
+      if constexpr (F == kCacheBf16) {
         *reinterpret_cast<uint4*>(q_smem + (ch >> 3) * NR * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
       } else {
         uint2 hi, lo;
@@ -273,15 +280,263 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const TreeWalk& w, u
   fence_proxy_async_smem();
 }
 
+// E2M1: one warpgroup lays out the keys of both streams.  It spreads their codes as kind::mxf8f6f4 takes E2M1 elements
+// (sixteen to 16 bytes, in the lower eight: rows of as many bytes as E4M3 rows) and puts their scales into tensor memory.
+// Rows past the end become zeros.
+template <int D, int NR>
+__device__ __forceinline__ void convert_keys(const TreeParams& p, const TreePart& my, uint8_t* smem,
+                                             Misc<NR, kCacheE2m1>* ms, uint32_t tmem) {
+  using C = Cfg<D, kCacheE2m1, NR>;
+  constexpr int kGroups = D / kE2m1Group;          // of a row
+  constexpr int kItems = kTreeBN * kGroups / 128;  // 16-byte pieces of codes per thread
+  constexpr int kItemRows = 128 / kGroups;
+  volatile int* abort_flag = &ms->abort_flag;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
+  const uint32_t scales = tmem + (static_cast<uint32_t>(warp * 32) << 16) + C::kColScales;
+  const int r0 = r / kGroups, piece = r % kGroups;
+  const int sw = D == 128 ? r0 & 7 : (r0 >> 1) & 3;  // the same for all of a thread's rows
+  constexpr uint32_t kOnes = 0x7f7f7f7fu;            // the queries' scales, before the first keys are announced
+  tmem_st4(scales + 16, kOnes, kOnes, kOnes, kOnes);
+  Ring<C::kRC> rc;
+  uint32_t used[2] = {0, 0};  // tiles of each stream so far
+  bool ok = true;
+  TreeWalk w;
+  w.begin(p, my);
+  do {
+#pragma unroll 1
+    for (int i = w.t0; i < w.t1; ++i) {
+      // One of the stream's two K tiles and its scales.
+      const int g = (i - w.t0) & 1;
+      const uint32_t u = g == 0 ? used[0] : used[1];
+      const uint32_t place = 2 * g + (u & 1);
+      ok = mbar_wait_inl(&ms->code_full[rc.slot], rc.parity, abort_flag, p.err, tree_site(0x10)) &&
+           mbar_wait_inl(&ms->k_empty[place], ((u >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x11));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint8_t* src = smem + C::kOffCodes + rc.slot * FourBit<D>::kHalf;
+      uint32_t s[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint8_t* at = src + FourBit<D>::kCodes + (q * 32 + lane) * kGroups;
+        s[q] = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+      }
+      tmem_st4(scales + place * 4, s[0], s[1], s[2], s[3]);
+      const uint4* codes = reinterpret_cast<const uint4*>(src) + r;
+      const int live = w.len - i * kTreeBN - r0;
+      uint8_t* dst = smem + C::kOffK + place * C::kSlot + r0 * D;
+      uint4 c[kItems];
+#pragma unroll
+      for (int it = 0; it < kItems; ++it) c[it] = codes[it * 128];
+#pragma unroll
+      for (int it = 0; it < kItems; ++it) {
+        if (live < kTreeBN && it * kItemRows >= live) c[it] = make_uint4(0, 0, 0, 0);
+        uint8_t* to = dst + it * kItemRows * D;
+        *reinterpret_cast<uint4*>(to + (((2 * piece) ^ sw) << 4)) = make_uint4(c[it].x, c[it].y, 0, 0);
+        *reinterpret_cast<uint4*>(to + (((2 * piece + 1) ^ sw) << 4)) = make_uint4(c[it].z, c[it].w, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ms->k_full[place]);
+        mbar_arrive(&ms->code_empty[rc.slot]);
+      }
+      __syncwarp();
+      rc.advance();
+      used[0] += g == 0;
+      used[1] += g;
+    }
+  } while (ok && w.next(p));
+}
+
+// E2M1: a warpgroup of each stream widens the values to fp16, each group times its power of two relative to a running
+// reference, which it tells the softmax.  Rows past the end become zeros.
+//
+// fp16 holds E2M1 values from 2⁻²³ to 2^13 of the reference exactly.  A tile with value groups further below it is widened
+// to bf16 instead, as with E4M3.
+constexpr int kFourLazy = 13, kFourFar = 23;
+template <int D, int NR>
+__device__ __forceinline__ void convert_values(const TreeParams& p, const TreePart& my, uint8_t* smem,
+                                              Misc<NR, kCacheE2m1>* ms, int g) {
+  using C = Cfg<D, kCacheE2m1, NR>;
+  constexpr int kGroups = D / kE2m1Group;          // of a row
+  volatile int* abort_flag = &ms->abort_flag;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
+  uint8_t* const v_tile = smem + C::kOffV16 + g * C::kV16 + r * 128;
+  // A wait that fails raises the abort flag, and all leave together, after a vote on it: until then a thread whose wait
+  // has failed goes on, since the others wait for it at the vote without a limit.
+  bool ok = true;
+  int used = 0, ref = 0;  // tiles of this stream so far, and what the last one's values were relative to
+  int tile0 = 0;  // tiles of the pieces before
+  TreeWalk w;
+  w.begin(p, my);
+  do {
+    const int n_tiles = w.t1 - w.t0, context = w.len - w.drafts;
+#pragma unroll 1
+    for (int i = g; i < n_tiles; i += 2) {
+      // The values' powers of two: the largest and the smallest that count set the reference.  (Groups of NaN, rows that no
+      // row sees, and 2^−126, next to nothing or zeros, do not.)
+      const int slot = (tile0 + i) % C::kRV, key = (w.t0 + i) * kTreeBN + r;
+      mbar_wait_inl(&ms->v_full[slot], ((tile0 + i) / C::kRV) & 1, abort_flag, p.err, tree_site(0x12));
+      __syncwarp();
+      const uint8_t* src = smem + C::kOffV + slot * FourBit<D>::kHalf;
+      const uint8_t* at = src + FourBit<D>::kCodes + r * kGroups;
+      const uint32_t bytes = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+      bool counts = key < w.len;
+      if (counts && key >= context && p.mask != nullptr)
+        counts = any_token_sees(p.mask + w.b * p.mask_sb + (key - context), w.drafts, p.T);
+      // Usually all lie where fp16 is exact, and none is NaN (byte 255) or next to nothing (2^−126 and below, or zeros):
+      // then nothing changes.
+      bool outside = i == g;
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        const int e = static_cast<int>(bytes >> (8 * j) & 0xffu);
+        outside |= counts && static_cast<unsigned>(e - 127 - ref + kFourFar) > static_cast<unsigned>(kFourLazy + kFourFar);
+      }
+      bool far = false;
+      __syncwarp();
+      if (named_any(4 + g, 128, outside || *abort_flag != 0)) {
+        ok = !named_any(4 + g, 128, *abort_flag != 0);
+        if (!ok) break;
+        int top = 0, low = 255;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          const int e = static_cast<int>(bytes >> (8 * j) & 0xffu);
+          if (e != 255) top = max(top, e);
+          if (e > 1) low = min(low, e);
+        }
+        top = __reduce_max_sync(0xffffffffu, counts ? top : 0);
+        low = __reduce_min_sync(0xffffffffu, counts ? low : 255);
+        if (lane == 0) ms->range[g][used & 1][warp] = top << 8 | (255 - low);
+        __syncwarp();
+        named_sync(4 + g, 128);
+        int most = 0, least = 255;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int x = ms->range[g][used & 1][q];
+          most = max(most, x >> 8);
+          least = min(least, 255 - (x & 0xff));
+        }
+        if (i == g || most - 127 > ref + kFourLazy) ref = most - 127;
+        far = least - 127 < ref - kFourFar;
+      }
+      // (The softmax has read the one two tiles ago: its product was waited for below.  It may not have read the last one,
+      // so there are two barriers.)
+      if (r == 0) {
+        ms->ref[g][used & 1] = ref * 2 + (far ? 1 : 0);
+        mbar_arrive(&ms->ref_full[g][used & 1]);
+      }
+      // The stream's widened tile is free once the second product before has run.
+      if (used > 0) mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, tree_site(0x13));
+      __syncwarp();
+      if (!far && (w.t0 + i + 1) * kTreeBN <= context) {
+        widen_codes<D>(src + r * (D / 2), bytes, v_tile, r, ref);
+      } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, v_tile, r, ref, key >= context, !counts, far)) {
+        atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ms->v16_full[g]);
+        mbar_arrive(&ms->v_empty[slot]);
+      }
+      ++used;
+    }
+    tile0 += n_tiles;
+    // Both streams' converters begin a piece together: one whose stream has no tiles in some pieces would run ahead of the
+    // loads by more than a barrier's two phases can tell.  (And the piece's last waits have had no vote.)
+    __syncwarp();
+    ok = !named_any(6, 256, !ok || *abort_flag != 0);
+  } while (ok && w.next(p));
+}
+
+// E2M1: the products of one stream, by a warp each.  The whole warp runs the loop, which keeps descriptors warp-uniform,
+// and one elected lane issues.
+template <int D, int NR>
+__device__ __forceinline__ void issue_products(const TreeParams& p, const TreePart& my, uint8_t* smem,
+                                               Misc<NR, kCacheE2m1>* ms, uint32_t tmem, int g) {
+  using C = Cfg<D, kCacheE2m1, NR>;
+  constexpr uint32_t kIdescO = idesc_f16_f32(128, NR, true, true), kIdescFar = idesc_bf16_f32(128, NR, true, true);
+  volatile int* abort_flag = &ms->abort_flag;
+  const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK) + 2 * g * C::kSlot;
+  const uint64_t q_desc = D == 64 ? sdesc_sw64(sQ, 16, 512) : sdesc_sw128(sQ, 16, 1024);
+  const uint64_t k_desc = D == 64 ? sdesc_sw64(sK, 16, 512) : sdesc_sw128(sK, 16, 1024);
+  const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::kOffV16) + g * C::kV16, D == 128 ? kBN * 128 : 0, 1024);
+  const uint64_t p_desc = sdesc_sw128(smem_u32(smem + C::kOffP) + g * C::kPNext, kPBlock, 1024);
+  const uint32_t ds = tmem + g * C::kSCols, dst = tmem + C::kColO + g * C::kPCols;
+  const uint32_t scales = tmem + C::kColScales + 8 * g, ones = tmem + C::kColScales + 16;
+  const bool leader = elect_one_lane();
+  uint32_t u = 0;  // tiles of this stream whose scores have been issued
+  bool ok = true;
+  TreeWalk w;
+  w.begin(p, my);
+  do {
+    const int tiles = __shfl_sync(0xffffffffu, (w.t1 - w.t0 + 1 - g) >> 1, 0);  // of the piece, this stream's
+    ok = mbar_wait_inl(&ms->q_full, w.index & 1, abort_flag, p.err, tree_site(14));
+    // S runs a tile ahead, so that the next scores are ready when the softmax has stored P̃.
+#pragma unroll 1
+    for (int s = 0; s <= tiles; ++s) {
+      if (s < tiles) {
+        const uint32_t b = u & 1u;
+        ok = ok && mbar_wait_inl(&ms->k_full[2 * g + b], (u >> 1) & 1u, abort_flag, p.err, tree_site(5)) &&
+             mbar_wait_inl(&ms->s_free[g], (u & 1u) ^ 1u, abort_flag, p.err, tree_site(6));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          // A k-step is a group of 32 elements, whose power of two the product applies.  Both of q's terms are columns.
+          const uint64_t ad = k_desc + b * (C::kSlot >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_mx_ss(ds, ad + kk * 2, q_desc + kk * 2, idesc_mx_e2m1_e4m3(128, 2 * NR, kk), scales + 4 * b, ones,
+                      kk > 0 ? 1u : 0u);
+          mma_commit(&ms->s_full[g]);
+          mma_commit(&ms->k_empty[2 * g + b]);
+        }
+        ++u;
+      }
+      if (s == max(tiles - 1, 0) && leader) mma_commit(&ms->q_empty);  // (without tiles too: the barrier counts both streams)
+      if (s > 0) {  // the second product of the tile before
+        const uint32_t before = u - (s < tiles ? 2u : 1u);
+        ok = ok && mbar_wait_inl(&ms->v16_full[g], before & 1u, abort_flag, p.err, tree_site(12)) &&
+             mbar_wait_inl(&ms->p_full[g], before & 1u, abort_flag, p.err, tree_site(3));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const bool far = *static_cast<volatile int*>(&ms->far[g]) != 0;
+        if (leader) {
+          const uint32_t idesc = far ? kIdescFar : kIdescO;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_bf16_ss(dst, v_desc + kk * 128, p_desc + kk * 128, idesc, (s > 1 || kk > 0) ? 1u : 0u);
+          if (far) {  // the second terms
+#pragma unroll 1
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              mma_bf16_ss(dst, v_desc + kk * 128, p_desc + NR / 8 + kk * 128, idesc, 1u);
+          }
+          mma_commit(&ms->p_free[g]);
+        }
+      }
+    }
+  } while (ok && __shfl_sync(0xffffffffu, w.next(p), 0));
+  if (leader) {  // the products are done before the end frees the tensor memory
+    mma_commit(&ms->drain);
+    mbar_wait_drain_inl(&ms->drain, 0, kTreeDrainNs);
+  }
+}
+
 template <int D, int F, int NR>
 __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, F, NR>;
-  constexpr bool FP8 = C::FP8, FP4 = C::FP4;
-  constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
+  constexpr bool FP8 = C::FP8, FP4 = C::FP4, kWiden = C::kWiden;
+  constexpr bool kPg5 = !kWiden && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
   constexpr int kSlot = C::kSlot;
   // Rescale once a score exceeds the reference by kLazy; the reference is taken kBase below the maximum.
-  constexpr float kLazy = FP8 ? 11.f : 8.f;
-  constexpr float kBase = FP8 ? 3.f : 0.f;
+  constexpr float kLazy = kWiden ? 11.f : 8.f;
+  constexpr float kBase = kWiden ? 3.f : 0.f;
   constexpr int kKvLazy = 7;  // widened values stay below 448·2^7
   constexpr int kKvFar = 15;  // value rows that are smaller by more than this need bf16's range
   extern __shared__ uint8_t smem_raw[];
@@ -301,13 +556,18 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
       mbar_init(&ms->k_full[s], FP4 ? 4 : 1);
       mbar_init(&ms->k_empty[s], 1);
     }
-    for (int s = 0; FP4 && s < C::kCodeRing; ++s) {
+    for (int s = 0; FP4 && s < C::kRC; ++s) {
       mbar_init(&ms->code_full[s], 1);
       mbar_init(&ms->code_empty[s], 4);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ms->ref_full[s][0], 1);
+      mbar_init(&ms->ref_full[s][1], 1);
+      mbar_init(&ms->v16_full[s], 4);
+    }
     for (int s = 0; s < C::kRV; ++s) {
-      mbar_init(&ms->v_full[s], FP4 ? 4 : 1);
-      mbar_init(&ms->v_empty[s], FP8 ? 4 : 1);
+      mbar_init(&ms->v_full[s], 1);
+      mbar_init(&ms->v_empty[s], kWiden ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
@@ -317,8 +577,8 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
     mbar_init(&ms->q_full, 32);
-    mbar_init(&ms->q_empty, 1);
-    mbar_init(&ms->drain, 1);
+    mbar_init(&ms->q_empty, FP4 ? 2 : 1);
+    mbar_init(&ms->drain, FP4 ? 2 : 1);
     ms->abort_flag = 0;
     fence_barrier_init();
   }
@@ -333,15 +593,35 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
   if (my.count <= 0) {
     // nothing left for this CTA
   } else if (FP4 && warp >= 12) {
-    reg_dealloc<C::kRegsOther>();
-    if constexpr (FP4)
-      expand_codes<D, C::kCodeRing, C::kRK, C::kRV>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty,
-                                                    smem + C::kOffK, ms->k_full, ms->k_empty, smem + C::kOffV, ms->v_full,
-                                                    ms->v_empty, abort_flag, tree_site(0x10), tid - 384);
+    if (warp < 20) {
+      reg_dealloc<C::kRegsConvert>();
+      if constexpr (FP4) convert_values<D, NR>(p, my, smem, ms, (warp - 12) >> 2);
+    } else {
+      reg_dealloc<C::kRegsOther>();
+      if constexpr (FP4) convert_keys<D, NR>(p, my, smem, ms, tmem);
+    }
   } else if (FP4 && warp == 8) {
     reg_dealloc<C::kRegsOther>();
     if constexpr (FP4)
-      load_codes<D, C::kCodeRing>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty, abort_flag, tree_site(1));
+      load_codes<D, C::kRC, kKeyCodes>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty, abort_flag, tree_site(1),
+                                       [](const TreeWalk&) { return true; });
+  } else if (FP4 && warp == 11) {
+    reg_dealloc<C::kRegsOther>();
+    // The values, and Q of every piece but the first, which the streams load, once the products of the piece before are
+    // done with it.
+    if constexpr (FP4)
+      load_codes<D, C::kRV, kValueCodes>(p, my, smem + C::kOffV, ms->v_full, ms->v_empty, abort_flag, tree_site(2),
+                                         [&](const TreeWalk& w) {
+        if (w.index == 0) return true;
+        if (!__all_sync(0xffffffffu, mbar_wait_inl(&ms->q_empty, (w.index & 1) ^ 1, abort_flag, p.err, tree_site(15))))
+          return false;
+        load_q<D, F, NR, 32, 2>(p, w, smem + C::kOffQ, ms->f[w.index % kFRing], lane);
+        mbar_arrive(&ms->q_full);
+        return true;
+      });
+  } else if (FP4 && (warp == 9 || warp == 10)) {
+    reg_dealloc<C::kRegsOther>();
+    if constexpr (FP4) issue_products<D, NR>(p, my, smem, ms, tmem, warp - 9);
   } else if (!FP4 && (warp == 8 || warp == 10)) {
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------------- loads of K (warp 8) and V (warp 10)
@@ -350,16 +630,17 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
       load_pages<D, FP8, kScaleRing>(p, my, is_v, smem + (is_v ? C::kOffV : C::kOffK), is_v ? C::kRV : C::kRK,
                                      is_v ? ms->v_full : ms->k_full, is_v ? ms->v_empty : ms->k_empty, ms->sc_full,
                                      ms->k_scale[0], ms->v_scale[0], abort_flag, tree_site(is_v ? 2 : 1));
-  } else if (warp == 9) {
+  } else if (!FP4 && warp == 9) {
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
-    constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false) : idesc_bf16_f32(128, NR, false, false);
-    constexpr uint32_t kIdescO = FP8 ? idesc_f16_f32(128, NR, true, true) : idesc_bf16_f32(128, C::kPCols, true, true);
+    constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, 2 * NR, false, false)
+                                       : idesc_bf16_f32(128, NR, false, false);
+    constexpr uint32_t kIdescO = kWiden ? idesc_f16_f32(128, NR, true, true) : idesc_bf16_f32(128, C::kPCols, true, true);
     constexpr uint32_t kIdescFar = idesc_bf16_f32(128, NR, true, true);
     const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK), sP = smem_u32(smem + C::kOffP);
-    const uint32_t sV = smem_u32(smem + (FP8 ? C::kOffV16 : C::kOffV));
-    const uint64_t q_desc = FP8 && D == 64 ? sdesc_sw64(sQ, 16, 512) : sdesc_sw128(sQ, 16, 1024);
+    const uint32_t sV = smem_u32(smem + (kWiden ? C::kOffV16 : C::kOffV));
+    const uint64_t q_desc = kWiden && D == 64 ? sdesc_sw64(sQ, 16, 512) : sdesc_sw128(sQ, 16, 1024);
     const bool leader = elect_one_lane();
     Ring<C::kRK> rk;
     Ring<C::kRV> rv;
@@ -459,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
     bool ok = true;
     TreeWalk w;
     w.begin(p, my);
-    load_q<D, FP8, NR, 256, 4>(p, w, smem + C::kOffQ, ms->f[0], tid);
+    load_q<D, F, NR, 256, 4>(p, w, smem + C::kOffQ, ms->f[0], tid);
     named_sync(3, 256);
     if (warp == 0) mbar_arrive(&ms->q_full);
 #pragma unroll 1
@@ -514,22 +795,27 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
           // (A drafted key that no row sees takes no part in the maximum, whatever it holds.)
           if (key < w.len && seen != 0) kv = static_cast<int>(ms->v_scale[tile % kScaleRing][kt]) - 127;
         }
+        int code = 0;  // E2M1: the converters say what the tile's widened values are relative to
+        if constexpr (FP4) {
+          ok = mbar_wait_inl(&ms->ref_full[g][u & 1], (u >> 1) & 1, abort_flag, p.err, tree_site(13)) && ok;
+          code = *static_cast<volatile int*>(&ms->ref[g][u & 1]);
+        }
         ok = mbar_wait_inl(&ms->s_full[g], u & 1, abort_flag, p.err, tree_site(7)) && ok;
         tc_fence_after();
         // x = score − reference, masked to −∞ where the row does not see the key.  A second time where a reference
         // has moved.
         float x[NR];
-        bool far = false;   // E4M3: value rows too far apart for fp16
+        bool far = FP4 && (code & 1);  // value rows too far apart for fp16
         bool dead = false;  // a wait of some thread of the stream has failed
 #pragma unroll 1
         for (bool again = false;; again = true) {
           // 16 rows at a time; with registers to spare the next ones are on their way from TMEM meanwhile.
           constexpr int kC = 16;
-          constexpr int kBuf = NR > kC ? 2 : 1;
+          constexpr int kBuf = NR > kC && !FP4 ? 2 : 1;
           uint32_t hi[kBuf][kC], lo[kBuf][kC];
           auto fetch = [&](int c, int to) {
             tmem_ld(s_addr + c, hi[to]);
-            if constexpr (FP8) tmem_ld(s_addr + NR + c, lo[to]);  // the columns of q's second terms
+            if constexpr (kWiden) tmem_ld(s_addr + NR + c, lo[to]);  // the columns of q's second terms
           };
           fetch(0, 0);
 #pragma unroll
@@ -537,7 +823,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             const int now = (c / kC) % kBuf;
             tmem_wait_ld();
             reg_fence(hi[now]);
-            if constexpr (FP8) reg_fence(lo[now]);
+            if constexpr (kWiden) reg_fence(lo[now]);
             if (kBuf == 2 && c + kC < NR) fetch(c + kC, now ^ 1);
 #pragma unroll
             for (int e = 0; e < kC; e += 4) {
@@ -545,12 +831,14 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
               float4 r4 = make_float4(__uint_as_float(hi[now][e]), __uint_as_float(hi[now][e + 1]),
                                       __uint_as_float(hi[now][e + 2]), __uint_as_float(hi[now][e + 3]));
               float4 f4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-              if constexpr (FP8) {
+              if constexpr (kWiden) {
                 ffma2(r4.x, r4.y, __uint_as_float(lo[now][e]), __uint_as_float(lo[now][e + 1]), 0.0625f, 0.0625f, r4.x,
                       r4.y);
                 ffma2(r4.z, r4.w, __uint_as_float(lo[now][e + 2]), __uint_as_float(lo[now][e + 3]), 0.0625f, 0.0625f,
                       r4.z, r4.w);
                 f4 = *reinterpret_cast<const float4*>(&f_row[n]);
+              }
+              if constexpr (FP8) {
                 fmul2(f4.x, f4.y, f4.x, f4.y, ks, ks);
                 fmul2(f4.z, f4.w, f4.z, f4.w, ks, ks);
               }
@@ -558,6 +846,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
               ffma2(x[n], x[n + 1], r4.x, r4.y, f4.x, f4.y, m4.x, m4.y);
               ffma2(x[n + 2], x[n + 3], r4.z, r4.w, f4.z, f4.w, m4.z, m4.w);
             }
+            if (kBuf == 1 && c + kC < NR) fetch(c + kC, 0);
           }
           if (tail) {
 #pragma unroll
@@ -572,7 +861,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             for (int e = 0; e < 4; ++e)
               mx[e] = n + 4 + e < NR ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NR]) : fmaxf(mx[e], x[n + e]);
           const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          const bool over = unseen || top > kLazy || (FP8 && (kv > kv_ref + kKvLazy || (kv > -126 && kv < kv_ref - kKvFar)));
+          const bool over = unseen || top > kLazy || (FP8 && (kv > kv_ref + kKvLazy || (kv > -126 && kv < kv_ref - kKvFar))) || (FP4 && code >> 1 != kv_ref);
           if (!named_any(bar, 128, over || !ok)) break;
           // A reference moves (the first tile always does): exchange the tile's maxima, rescale ℓ and O.
           if (named_any(bar, 128, !ok)) {
@@ -586,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             if (lane == 0) ms->kv_red[g][warp & 3] = top_kv;
           }
           named_sync(bar, 128);
-          int kv_new = kv_ref;
+          int kv_new = FP4 ? code >> 1 : kv_ref;
           if constexpr (FP8) {
             const int* kr = ms->kv_red[g];
             kv_new = max(kv_ref, max(max(kr[0], kr[1]), max(kr[2], kr[3])));
@@ -611,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
           if (done > 0) {
             ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
             tc_fence_after();
-            const float kf = FP8 ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
+            const float kf = kWiden ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
 #pragma unroll 1
             for (int term = 0; term < C::kTerms; ++term) rescale_cols<NR>(o_addr + term * NR, corr, kf);
           }
@@ -635,20 +924,20 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             x[n] = ex2_approx(x[n]);
             x[n + 1] = ex2_approx(x[n + 1]);
             fadd2(l[n], l[n + 1], l[n], l[n + 1], x[n], x[n + 1]);
-            if constexpr (FP8) {
+            if constexpr (kWiden) {
               hi[e] = pack_f16x2(x[n], x[n + 1]);
             } else {
               split_weights2(x[n], x[n + 1], hi[e], lo[e]);
             }
           }
           *reinterpret_cast<uint4*>(prow + (((first + ch) ^ (kt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if constexpr (!FP8) {
+          if constexpr (!kWiden) {
             const int c2 = first + ch + NR / 8;  // column chunk of the second term
             *reinterpret_cast<uint4*>(prow + ((c2 ^ (kt & 7)) << 4)) =
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
-        if (FP8 && far) {  // the weights as two bf16 terms, from what this thread has just stored
+        if (kWiden && far) {  // the weights as two bf16 terms, from what this thread has just stored
 #pragma unroll 1
           for (int ch = 0; ch < NR / 8; ++ch) {
             uint4* at = reinterpret_cast<uint4*>(prow + (((first + ch) ^ (kt & 7)) << 4));
@@ -675,7 +964,8 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
           }
         }
-        if (!FP8 && tail && key >= context) {
+        if (FP4 && kt == 0) ms->far[g] = far;
+        if (!kWiden && tail && key >= context) {
           // This key's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
           const int slot = tile % C::kRV;
           ok = mbar_wait_inl(&ms->v_full[slot], (tile / C::kRV) & 1, abort_flag, p.err, tree_site(9)) && ok;
@@ -729,7 +1019,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
         // once: the product of the two may be too small a number).
         ms->scale[g][kt] = mine * (sum != 0.f ? 1.f / sum : 0.f);
       }
-      if (FP8 && kt == 0) ms->kv_scale[g] = exp2f(static_cast<float>(max(kv_ref, -300)));
+      if (kWiden && kt == 0) ms->kv_scale[g] = exp2f(static_cast<float>(max(kv_ref, -300)));
       if (w.t0 == 0 && tid == 0) p.pieces[w.pair(p)] = w.pieces(part, my.per);
       named_sync(3, 256);
       const uint32_t* bad = ms->bad[w.index % kBadRing];
@@ -752,7 +1042,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             for (int q = 0; q < kOut; ++q) {
               const float k = ms->scale[e][c0 + q];
               if (k == 0.f) continue;  // a stream without keys has left O unwritten
-              o[q] += FP8 ? __uint_as_float(r[q]) * k * ms->kv_scale[e] : __uint_as_float(r[q]) * k;
+              o[q] += kWiden ? __uint_as_float(r[q]) * k * ms->kv_scale[e] : __uint_as_float(r[q]) * k;
             }
           }
         }
@@ -792,7 +1082,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
       // The flags of three pieces ago: the other stream may still be at the piece before.
       if (tid < 8) ms->bad[(w.index + kBadRing - 3) % kBadRing][tid] = 0;
     } while (ok && w.next(p));
-  } else if (warp == 11) {
+  } else if (!FP4 && warp == 11) {
     reg_dealloc<C::kRegsOther>();
     // ------------------------- Q of every piece but the first, which the streams load
     TreeWalk w;
@@ -801,11 +1091,9 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
     while (w.next(p)) {
       // Once the first products of the piece before are done.
       if (!__all_sync(0xffffffffu, mbar_wait_inl(&ms->q_empty, (w.index & 1) ^ 1, abort_flag, p.err, tree_site(15)))) break;
-      load_q<D, FP8, NR, 32, 2>(p, w, smem + C::kOffQ, ms->f[w.index % kFRing], lane);
+      load_q<D, F, NR, 32, 2>(p, w, smem + C::kOffQ, ms->f[w.index % kFRing], lane);
       mbar_arrive(&ms->q_full);
     }
-  } else {
-    reg_dealloc<C::kRegsOther>();  // E2M1: idle until the end
   }
 
   tc_fence_before();
@@ -855,6 +1143,8 @@ __global__ void __launch_bounds__((WIDE ? kMergeWarpsWide : kMergeWarps) * 32)
   if (t < drafts) {
     const int2 pieces = p.pieces[pair];
     if (pieces.y == 1) return;  // not cut: the first kernel has written it
+    // A kernel that gave up on a wait may have left none.
+    if (pieces.x < 0 || pieces.y < 1 || pieces.y > p.parts - pieces.x) return;
     auto slot = [&](int i) -> int64_t {
       return p.slots_by_pair ? pair + pieces.x + i : 2ll * (pieces.x + i) + (i > 0 ? 0 : 1);
     };

@@ -363,13 +363,18 @@ __device__ __forceinline__ void load_pages(const TreeParams& p, const TreePart& 
 template <int D>
 struct FourBit {
   static constexpr int kCodes = kTreeBN * D / 2, kScales = kTreeBN * D / kE2m1Group;
-  static constexpr int kHalf = kCodes + kScales;  // bytes of the ring per half tile
+  static constexpr int kHalf = kCodes + kScales;  // bytes of a ring's slot
 };
 
-// Fetches the codes and scales of a part's tiles, by one warp.
-template <int D, int RING>
+// What load_codes fetches: both halves into one ring, in the order above, or the keys or the values alone.
+enum CodeParts : int { kBothHalves = 0, kKeyCodes = 1, kValueCodes = 2 };
+
+// Fetches the codes and scales of a part's tiles, by one warp, into a ring of RING halves.  at_piece is called at the start
+// of every piece.
+template <int D, int RING, CodeParts PARTS, class AtPiece>
 __device__ __forceinline__ void load_codes(const TreeParams& p, const TreePart& my, uint8_t* ring, uint64_t* full,
-                                           uint64_t* empty, volatile int* abort_flag, unsigned int site) {
+                                           uint64_t* empty, volatile int* abort_flag, unsigned int site,
+                                           AtPiece at_piece) {
   constexpr int kRow = D / 2, kRowScales = D / kE2m1Group;
   const int lane = threadIdx.x & 31;
   const int bshift = 31 - __clz(p.block_size);  // a power of two
@@ -377,9 +382,10 @@ __device__ __forceinline__ void load_codes(const TreeParams& p, const TreePart& 
   int slot = 0, issued = 0;
   uint32_t parity = 1;
   bool ok = true;
-  // The pages of this lane: one of the tile's, or −1 past the end.
+  // blk: the page of this lane, one of the tile's, or −1 past the end.
   auto half = [&](int blk, int h, bool is_v) {
-    ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, site));
+    ok = mbar_wait_inl(&empty[slot], parity, abort_flag, p.err, site);
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) return;
     const bool real = lane < npt && blk >= 0;
     const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
@@ -409,8 +415,9 @@ __device__ __forceinline__ void load_codes(const TreeParams& p, const TreePart& 
     int id = 0, ahead = page < pages ? table[page] : 0;
     int at = 32;  // the tile's first page in the group
     int before = -1;
+    if (!at_piece(w)) break;
 #pragma unroll 1
-    for (int i = w.t0; i <= w.t1; ++i) {
+    for (int i = w.t0; i < w.t1 + (PARTS == kBothHalves ? 1 : 0); ++i) {
       int blk = -1;
       if (i < w.t1) {
         if (at == 32) {
@@ -425,9 +432,9 @@ __device__ __forceinline__ void load_codes(const TreeParams& p, const TreePart& 
         }
         blk = __shfl_sync(0xffffffffu, id, at + lane);
         at += npt;
-        half(blk, w.h, false);
+        half(blk, w.h, PARTS == kValueCodes);
       }
-      if (ok && i > w.t0) half(before, w.h, true);
+      if (PARTS == kBothHalves && ok && i > w.t0) half(before, w.h, true);
       if (!ok) break;
       before = blk;
     }
@@ -544,6 +551,85 @@ __device__ __forceinline__ void expand_codes(const TreeParams& p, const TreePart
       if (!ok) break;
     }
   } while (ok && w.next(p));
+}
+
+// A value row's group g of 32 codes to its places in a 16-bit tile of rows of 128 bytes (64 columns), r: the row.
+template <class Convert>
+__device__ __forceinline__ void widen_group(uint4 c, uint8_t* dst, int r, int g, Convert convert) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint8_t* block = dst + (g >> 1) * kTreeBN * 128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(block + ((((g & 1) * 4 + j) ^ (r & 7)) << 4)) = convert(w[j]);
+}
+// Eight codes to fp16, times the pair of scales.
+__device__ __forceinline__ uint4 widen_e2m1x8(uint32_t w, uint32_t scale2) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = e2m1x2_to_f16x2(w >> (8 * i));
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&scale2));
+    o[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// The group a thread takes at step j: rows of 64 bytes lie four to a pass over the banks, so neighbouring pairs of rows
+// begin with different groups.
+template <int D>
+__device__ __forceinline__ int group_at(int j, int r) {
+  return D == 128 ? (j + (r >> 1)) & 3 : j;
+}
+
+// Widens one value row of E2M1 codes to fp16, each group times its power of two relative to 2^ref (context keys).
+// src: the row's codes, scales: its bytes.
+template <int D>
+__device__ __forceinline__ void widen_codes(const uint8_t* src, uint32_t scales, uint8_t* dst, int r, int ref) {
+#pragma unroll 1
+  for (int j = 0; j < D / kE2m1Group; ++j) {
+    const int g = group_at<D>(j, r);
+    const uint4 c = *reinterpret_cast<const uint4*>(src + g * 16);
+    const uint32_t s = scales >> (8 * g) & 0xffu;
+    const uint32_t scale2 = s == 255 ? 0x7e007e00u : power_f16x2(static_cast<int>(s) - 127 - ref);
+    widen_group(c, dst, r, g, [&](uint32_t w) { return widen_e2m1x8(w, scale2); });
+  }
+}
+// The same out of line for tiles that hold drafted keys (whose NaN groups are taken out and reported by the result), the
+// end (dead: zeros), or, far, value groups that lie too far apart for fp16 and go to bf16.
+template <int D>
+__device__ __noinline__ bool widen_codes_edge(const uint8_t* src, uint32_t scales, uint8_t* dst, int r, int ref,
+                                              bool drafted, bool dead, bool far) {
+  bool bad = false;
+#pragma unroll 1
+  for (int g = 0; g < D / kE2m1Group; ++g) {
+    uint4 c = *reinterpret_cast<const uint4*>(src + g * 16);
+    uint32_t s = scales >> (8 * g) & 0xffu;
+    const bool out = drafted && s == 255;
+    bad |= out;
+    if (out || dead) {
+      c = make_uint4(0, 0, 0, 0);
+      s = 127;
+    }
+    const int e = out || dead ? 0 : static_cast<int>(s) - 127 - ref;
+    if (far) {
+      // 2^e in two factors, as it may be too small a number by itself.
+      const float f = s == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
+      const float f2 = e >= -126 ? 1.f : e < -252 ? 0.f : __uint_as_float(static_cast<uint32_t>(e + 126 + 127) << 23);
+      widen_group(c, dst, r, g, [&](uint32_t w) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t h = e2m1x2_to_f16x2(w >> (8 * i));
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          o[i] = pack_bf16x2(x.x * f * f2, x.y * f * f2);
+        }
+        return make_uint4(o[0], o[1], o[2], o[3]);
+      });
+    } else {
+      const uint32_t scale2 = s == 255 ? 0x7e007e00u : power_f16x2(e);
+      widen_group(c, dst, r, g, [&](uint32_t w) { return widen_e2m1x8(w, scale2); });
+    }
+  }
+  return bad && !dead;
 }
 
 // Eight elements of a query row, whose other ones the neighbouring kChunks − 1 lanes hold, as E4M3 terms

@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
   } else if (FP4 && warp == 8) {
     reg_dealloc<C::kRegsOther>();
     if constexpr (FP4)
-      load_codes<D, C::kCodeRing>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty, abort_flag, tree_site(0x21));
+      load_codes<D, C::kCodeRing, kBothHalves>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty, abort_flag,
+                                               tree_site(0x21), [](const TreeWalk&) { return true; });
   } else if (!FP4 && (warp == 8 || warp == 10)) {
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------------- loads of K (warp 8) and V (warp 10)

@@ -5,7 +5,7 @@ from __future__ import annotations
 import numpy as np
 
 from oracle import serving
-from tests.serving_helpers import bf16, np64
+from tests.serving_helpers import bf16, check_tree, np64
 
 
 def pack(codes):
@@ -21,13 +21,20 @@ def values(packed, scales):
     return v * np.repeat(power, 32, axis=-1)
 
 
+def check_tree4(o, lse, q, paged, drafts, mask, scale, heads=None):
+    """``check_tree`` with the bounds that hold for a cache in four bits: up to 32 rows that share a key head its weights are
+    fp16 and q two E4M3 terms, as with E4M3 (the same roundings: fp16 weights are off by 2^-11 of themselves, or below 2^-14
+    by half of 2^-24 where the row's largest is at least 2^3); beyond, they are bf16, and q is as it is."""
+    rows = q.shape[2] * (q.shape[1] // paged.hkv)
+    paged.cache = "e4m3" if rows <= 32 else "bf16"
+    check_tree(o, lse, q, paged, drafts, mask, scale, heads)
+
+
 class Paged4:
     """Sequences of given lengths in a shuffled page pool in four bits whose other slots are NaN, tables padded with −1.
 
     ``k`` and ``v`` are lists of the live rows [H, len, d] in float64, as the cache holds them.
     """
-
-    cache = "e2m1"
 
     def __init__(self, rng, lens, hkv, d, bs, spare=3, edit=None):
         import torch

@@ -7,9 +7,9 @@ import pytest
 
 from io_aware_exact_11_gb300 import fa
 from oracle import serving
-from tests.four_bit_helpers import Paged4, pack, values
+from tests.four_bit_helpers import Paged4, check_tree4, pack, values
 from tests.gpu_helpers import Guarded
-from tests.serving_helpers import bf16, check_tree, np64, random_tree
+from tests.serving_helpers import bf16, np64, random_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -108,7 +108,7 @@ def test_every_code_and_scale_reads_back_exactly():
                            **{s: torch.from_numpy(scales).cuda() for s in ("k_scale", "v_scale")})
     want = values(codes, scales).reshape(1, 1, n, 128)
     # The two largest powers of two take the largest codes beyond bf16, whose values are infinite there.
-    want = np.where(np.abs(want) > 3.4e38, np.sign(want) * np.inf, want)
+    want = np.where(np.abs(want) > 3.4e38, np.copysign(np.inf, want), want)
     assert np.array_equal(np64(k), want, equal_nan=True) and np.array_equal(np64(v), want, equal_nan=True)
 
 
@@ -148,7 +148,7 @@ def _run(seed, lens, Hq, hkv, T, d, bs, mask=None, drafts=None, parts=0, heads=N
                             max_parts=parts, scale=scale, **p.kw(), **kw)
     fa.device_status()
     real = drafts if drafts is not None else [T if n else 0 for n in lens]
-    check_tree(o, lse, q, p, real, mask, scale, heads)
+    check_tree4(o, lse, q, p, real, mask, scale, heads)
     return o, lse, q, p
 
 
@@ -249,15 +249,15 @@ def test_strided_in_place_guarded_and_repeated(Hq, T):
     o, lse = fa.decode_tree(q, *p.args(), **p.kw())
     again, lse2 = fa.decode_tree(q, *p.args(), **p.kw())
     assert torch.equal(o, again) and torch.equal(lse, lse2)
-    check_tree(o, lse, q, p, [T, T], None, 0.125, [0, Hq - 1])
+    check_tree4(o, lse, q, p, [T, T], None, 0.125, [0, Hq - 1])
     got, ws = Guarded((2, Hq, T, 64), torch.bfloat16), Guarded((256,), torch.uint8)
     ls = Guarded((2, Hq, T), torch.float32)
     fa.decode_tree(q, *p.args(), out=got.t, lse=ls.t, workspace=ws.t, **p.kw())
-    check_tree(got.t, ls.t, q, p, [T, T], None, 0.125, [0, Hq - 1])
+    check_tree4(got.t, ls.t, q, p, [T, T], None, 0.125, [0, Hq - 1])
     assert got.intact() and ws.intact() and ls.intact()
     same = q.clone()
     fa.decode_tree(same, *p.args(), out=same, **p.kw())
-    check_tree(same, lse, q, p, [T, T], None, 0.125, [0, Hq - 1])
+    check_tree4(same, lse, q, p, [T, T], None, 0.125, [0, Hq - 1])
 
 
 def test_keys_beyond_32_bit_offsets():
@@ -275,11 +275,11 @@ def test_keys_beyond_32_bit_offsets():
     assert np.array_equal(np64(gk), y["k"]) and np.array_equal(np64(gv), y["v"])
 
     class Seen:
-        cache = "e2m1"
+        pass
     p = Seen()
     p.hkv, p.k, p.v = hkv, y["k"], y["v"]
     for G in (1, 5):
         q = bf16(rng.standard_normal((2, hkv * G, 4, d))).cuda()
         o, lse = fa.decode_tree(q, kc, vc, table, _i32([300, 300]), **sc)
-        check_tree(o, lse, q, p, [4, 4], None, 1 / math.sqrt(d), [0, hkv * G - 1])
+        check_tree4(o, lse, q, p, [4, 4], None, 1 / math.sqrt(d), [0, hkv * G - 1])
     fa.device_status()

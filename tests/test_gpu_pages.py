@@ -8,6 +8,7 @@ import pytest
 
 from io_aware_exact_11_gb300 import fa
 from oracle import serving
+from tests.four_bit_helpers import check_tree4
 from tests.gpu_helpers import Guarded
 from tests.serving_helpers import bf16, check_tree, np64
 
@@ -372,7 +373,7 @@ def test_a_loop_of_forked_sequences(cache):
         for b in range(B):
             assert np.array_equal(full.k[b], np.concatenate([rows[b][0], held(k[b])], 1))
             assert np.array_equal(full.v[b], np.concatenate([rows[b][1], held(v[b])], 1))
-        check_tree(o, lse, q, full, [T] * B, None, 1 / math.sqrt(d), [0, Hq - 1])
+        (check_tree4 if cache == "e2m1" else check_tree)(o, lse, q, full, [T] * B, None, 1 / math.sqrt(d), [0, Hq - 1])
         # Some drafts of each are accepted.
         taken = [sorted(rng.permutation(T)[: int(rng.integers(0, T + 1))].tolist()) for _ in range(B)]
         keep = np.zeros((B, T), dtype=np.int32)
