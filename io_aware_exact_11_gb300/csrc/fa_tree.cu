@@ -140,7 +140,7 @@ struct Misc {
   uint64_t code_full[F == kCacheE2m1 ? kMaxRing : 1], code_empty[F == kCacheE2m1 ? kMaxRing : 1];
   uint64_t ref_full[2][2], v16_full[2];  // E2M1: per stream (and tile)
   int ref[2][2];                       // E2M1: 2·(exponent that a stream's widened tile is relative to) + (it is bf16)
-  int range[2][2][4];                  // E2M1: per stream, tile and warp
+  int range[2][4];                     // E2M1: per stream and warp
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], sc_full[kScaleRing], q_full, q_empty, drain;
   alignas(16) float nm[2][NR];         // minus the reference maxima (log2 units), 0 while a row has seen nothing
   alignas(16) float f[kFRing][NR];     // E4M3, E2M1: what a row's raw scores are multiplied by
@@ -355,16 +355,14 @@ __device__ __forceinline__ void convert_keys(const TreeParams& p, const TreePart
 // E2M1: a warpgroup of each stream widens the values to fp16, each group times its power of two relative to a running
 // reference, which it tells the softmax.  Rows past the end become zeros.
 //
-// fp16 holds E2M1 values from 2⁻²³ to 2^13 of the reference exactly.  A tile with value groups further below it is widened
-// to bf16 instead, as with E4M3.
-constexpr int kFourLazy = 13, kFourFar = 23;
+// A tile with value groups too far below the reference is widened to bf16 instead, as with E4M3.
 template <int D, int NR>
 __device__ __forceinline__ void convert_values(const TreeParams& p, const TreePart& my, uint8_t* smem,
                                               Misc<NR, kCacheE2m1>* ms, int g) {
   using C = Cfg<D, kCacheE2m1, NR>;
   constexpr int kGroups = D / kE2m1Group;          // of a row
   volatile int* abort_flag = &ms->abort_flag;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
+  const int lane = threadIdx.x & 31, r = threadIdx.x & 127;
   uint8_t* const v_tile = smem + C::kOffV16 + g * C::kV16 + r * 128;
   // A wait that fails raises the abort flag, and all leave together, after a vote on it: until then a thread whose wait
   // has failed goes on, since the others wait for it at the vote without a limit.
@@ -388,40 +386,14 @@ __device__ __forceinline__ void convert_values(const TreeParams& p, const TreePa
       bool counts = key < w.len;
       if (counts && key >= context && p.mask != nullptr)
         counts = any_token_sees(p.mask + w.b * p.mask_sb + (key - context), w.drafts, p.T);
-      // Usually all lie where fp16 is exact, and none is NaN (byte 255) or next to nothing (2^−126 and below, or zeros):
-      // then nothing changes.
-      bool outside = i == g;
-#pragma unroll
-      for (int j = 0; j < kGroups; ++j) {
-        const int e = static_cast<int>(bytes >> (8 * j) & 0xffu);
-        outside |= counts && static_cast<unsigned>(e - 127 - ref + kFourFar) > static_cast<unsigned>(kFourLazy + kFourFar);
-      }
       bool far = false;
       __syncwarp();
-      if (named_any(4 + g, 128, outside || *abort_flag != 0)) {
+      if (named_any(4 + g, 128, i == g || (counts && outside_reference<kGroups>(bytes, ref)) || *abort_flag != 0)) {
         ok = !named_any(4 + g, 128, *abort_flag != 0);
         if (!ok) break;
-        int top = 0, low = 255;
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-          const int e = static_cast<int>(bytes >> (8 * j) & 0xffu);
-          if (e != 255) top = max(top, e);
-          if (e > 1) low = min(low, e);
-        }
-        top = __reduce_max_sync(0xffffffffu, counts ? top : 0);
-        low = __reduce_min_sync(0xffffffffu, counts ? low : 255);
-        if (lane == 0) ms->range[g][used & 1][warp] = top << 8 | (255 - low);
-        __syncwarp();
-        named_sync(4 + g, 128);
-        int most = 0, least = 255;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int x = ms->range[g][used & 1][q];
-          most = max(most, x >> 8);
-          least = min(least, 255 - (x & 0xff));
-        }
-        if (i == g || most - 127 > ref + kFourLazy) ref = most - 127;
-        far = least - 127 < ref - kFourFar;
+        const int2 range = exponent_range<kGroups>(bytes, counts, 4 + g, ms->range[g]);
+        if (i == g || range.x - 127 > ref + kFourLazy) ref = range.x - 127;
+        far = range.y - 127 < ref - kFourFar;
       }
       // (The softmax has read the one two tiles ago: its product was waited for below.  It may not have read the last one,
       // so there are two barriers.)

@@ -356,9 +356,48 @@ __device__ __forceinline__ void load_pages(const TreeParams& p, const TreePart& 
 // ---------------------------------------------------------------- a cache in four bits
 //
 // A page of one head is contiguous: its codes and its scale bytes come by plain bulk copies into a ring of half tiles (the
-// keys or the values of 128 rows: K₀, K₁, V₀, K₂, V₁ … of each piece, the order in which they are used), and four warps
-// write them out as bf16 tiles where the bf16 kernels have theirs.  E2M1 times a power of two is exact in bf16, so from
-// there on the kernels are those of a bf16 cache.
+// keys or the values of 128 rows; in one ring K₀, K₁, V₀, K₂, V₁ … of each piece, the order in which they are used), and
+// other warps widen them to fp16, each group times its power of two relative to a reference: from 2⁻²³ to 2^13 of it that
+// is exact.
+constexpr int kFourLazy = 13, kFourFar = 23;
+
+// Whether a row's groups have exponents that a reference does not fit: usually none has, and then it stays.  (NaN, byte 255,
+// and next to nothing, 2⁻¹²⁶ and below or zeros, are looked at more closely.)
+template <int G>
+__device__ __forceinline__ bool outside_reference(uint32_t bytes, int ref) {
+  bool outside = false;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int e = static_cast<int>(bytes >> (8 * j) & 0xffu) - 127 - ref;
+    outside |= static_cast<unsigned>(e + kFourFar) > static_cast<unsigned>(kFourLazy + kFourFar);
+  }
+  return outside;
+}
+// The largest and the smallest exponent byte of the rows of 128 threads that count, by all of them, with barrier `bar`
+// (0 and 255 if there is none).  NaN, and next to nothing for the smallest, do not count.
+template <int G>
+__device__ __forceinline__ int2 exponent_range(uint32_t bytes, bool counts, int bar, int* range) {
+  int top = 0, low = 255;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int e = static_cast<int>(bytes >> (8 * j) & 0xffu);
+    if (e != 255) top = max(top, e);
+    if (e > 1) low = min(low, e);
+  }
+  top = __reduce_max_sync(0xffffffffu, counts ? top : 0);
+  low = __reduce_min_sync(0xffffffffu, counts ? low : 255);
+  if ((threadIdx.x & 31) == 0) range[(threadIdx.x >> 5) & 3] = top << 8 | (255 - low);
+  __syncwarp();
+  named_sync(bar, 128);
+  int2 r = make_int2(0, 255);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int x = range[q];
+    r.x = max(r.x, x >> 8);
+    r.y = min(r.y, 255 - (x & 0xff));
+  }
+  return r;
+}
 
 template <int D>
 struct FourBit {
@@ -446,114 +485,7 @@ __device__ __forceinline__ void load_codes(const TreeParams& p, const TreePart& 
   }
 }
 
-__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t selector) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(selector));
-  return r;
-}
-
-// 32 E2M1 codes times 2^(s−127) as bf16.  The eight magnitudes times the power of two are worked out once, and their
-// upper and lower bytes are picked by the codes, four at a time.
-struct Magnitudes {
-  uint32_t hi[2], lo[2];
-  __device__ __forceinline__ explicit Magnitudes(uint32_t s) {
-    // (Byte 0 stands for 2^−127, below the normal numbers, and 255 for NaN.)
-    const float f = s == 0 ? 5.877471754111438e-39f : s == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(s << 23);
-    const uint32_t v[4] = {pack_bf16x2(0.f * f, 0.5f * f), pack_bf16x2(f, 1.5f * f), pack_bf16x2(2.f * f, 3.f * f),
-                           pack_bf16x2(4.f * f, 6.f * f)};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      hi[i] = permute(v[2 * i], v[2 * i + 1], 0x7531);
-      lo[i] = permute(v[2 * i], v[2 * i + 1], 0x6420);
-    }
-  }
-  __device__ __forceinline__ uint4 expand(uint32_t codes) const {
-    uint32_t out[4];
-    const uint32_t which = codes & 0x77777777u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t sel = which >> (16 * i);
-      uint32_t up = permute(hi[0], hi[1], sel);
-      const uint32_t low = permute(lo[0], lo[1], sel);
-      // A selector's upper bit, the sign, spreads the picked byte's over it: 0x80 or 0xff.
-      up |= permute(0x80808080u, 0x80808080u, codes >> (16 * i)) << 1 & 0x80808080u;
-      out[2 * i] = permute(low, up, 0x5140);
-      out[2 * i + 1] = permute(low, up, 0x7362);
-    }
-    return make_uint4(out[0], out[1], out[2], out[3]);
-  }
-};
-
-// Writes the fetched tiles of a part out as bf16, by 128 threads (thread id of them): K and V tiles of kSlot bytes in
-// rings of RK and RV, as the bf16 kernels' loads lay them out (D = 128: [8 rows][half][row][128 bytes], else a row of 128
-// bytes per key, 16-byte chunks XORed with the row).  Rows past the end become zeros.
-template <int D, int RING, int RK, int RV>
-__device__ __forceinline__ void expand_codes(const TreeParams& p, const TreePart& my, const uint8_t* ring, uint64_t* full,
-                                             uint64_t* empty, uint8_t* k_dst, uint64_t* k_full, uint64_t* k_empty,
-                                             uint8_t* v_dst, uint64_t* v_full, uint64_t* v_empty,
-                                             volatile int* abort_flag, unsigned int site, int id) {
-  constexpr int kGroups = D / kE2m1Group;            // of a row
-  constexpr int kItems = kTreeBN * kGroups / 128;    // groups of a thread
-  constexpr int kSlot = kTreeBN * D * 2;
-  constexpr int kItemRows = 128 / kGroups;           // rows from one of its groups to the next
-  const int r0 = id / kGroups, g = id % kGroups;
-  // The lanes of a pass over 128 bytes write different chunks: groups of the upper half begin with their third chunk.
-  const int late = D == 128 && g >= 2 ? 2 : 0;
-  const int x0 = ((g & 1) * 4) ^ late ^ (r0 & 7);
-  const int off = D == 128 ? (r0 >> 3) * 2048 + (g >> 1) * 1024 + (r0 & 7) * 128 : r0 * 128;
-  Ring<RING> rc;
-  Ring<RK> rk;
-  Ring<RV> rv;
-  bool ok = true;
-  auto half = [&](int live, uint8_t* dst, uint64_t* to_full, uint64_t* to_empty, uint32_t to_parity) {
-    ok = mbar_wait_inl(&full[rc.slot], rc.parity, abort_flag, p.err, site) &&
-         mbar_wait_inl(to_empty, to_parity ^ 1u, abort_flag, p.err, site + 1);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return;
-    const uint8_t* src = ring + rc.slot * FourBit<D>::kHalf;
-    const uint4* codes = reinterpret_cast<const uint4*>(src) + id;
-    const uint8_t* scales = src + FourBit<D>::kCodes + id;
-#pragma unroll
-    for (int it = 0; it < kItems; ++it) {
-      uint4 c = codes[it * 128];
-      uint32_t s = scales[it * 128];
-      if (r0 + it * kItemRows >= live) {
-        c = make_uint4(0, 0, 0, 0);
-        s = 127;
-      }
-      const Magnitudes m(s);
-      const uint32_t w[4] = {late ? c.z : c.x, late ? c.w : c.y, late ? c.x : c.z, late ? c.y : c.w};
-      uint8_t* to = dst + off + it * (kItemRows * D * 2);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(to + ((x0 ^ j) << 4)) = m.expand(w[j]);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((id & 31) == 0) {
-      mbar_arrive(to_full);
-      mbar_arrive(&empty[rc.slot]);
-    }
-    rc.advance();
-  };
-  TreeWalk w;
-  w.begin(p, my);
-  do {
-#pragma unroll 1
-    for (int i = w.t0; i <= w.t1; ++i) {
-      if (i < w.t1) {
-        half(w.len - i * kTreeBN, k_dst + rk.slot * kSlot, &k_full[rk.slot], &k_empty[rk.slot], rk.parity);
-        rk.advance();
-      }
-      if (ok && i > w.t0) {
-        half(w.len - (i - 1) * kTreeBN, v_dst + rv.slot * kSlot, &v_full[rv.slot], &v_empty[rv.slot], rv.parity);
-        rv.advance();
-      }
-      if (!ok) break;
-    }
-  } while (ok && w.next(p));
-}
-
-// A value row's group g of 32 codes to its places in a 16-bit tile of rows of 128 bytes (64 columns), r: the row.
+// A row's group g of 32 codes to its places in a 16-bit tile of rows of 128 bytes (64 columns), r: the row.
 template <class Convert>
 __device__ __forceinline__ void widen_group(uint4 c, uint8_t* dst, int r, int g, Convert convert) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -580,7 +512,7 @@ __device__ __forceinline__ int group_at(int j, int r) {
   return D == 128 ? (j + (r >> 1)) & 3 : j;
 }
 
-// Widens one value row of E2M1 codes to fp16, each group times its power of two relative to 2^ref (context keys).
+// Widens one row of E2M1 codes to fp16, each group times its power of two relative to 2^ref.
 // src: the row's codes, scales: its bytes.
 template <int D>
 __device__ __forceinline__ void widen_codes(const uint8_t* src, uint32_t scales, uint8_t* dst, int r, int ref) {

@@ -38,6 +38,7 @@
 #include <stddef.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "fa_tree.cuh"
 
@@ -54,34 +55,33 @@ constexpr int kTileRing = 8;   // E4M3: tiles whose converted scales are kept
 template <int D, int F, int TILES>
 struct Cfg {
   static constexpr bool FP8 = F == kCacheE4m3, FP4 = F == kCacheE2m1;
-  // Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, idle 11; E4M3: converters 12–15; E2M1: all loads 8,
-  // expanders 12–15.
-  static constexpr bool kMore = FP8 || FP4;
-  static constexpr int kThreads = kMore ? 512 : 384;
-  static constexpr int kRegsLaunch = kMore ? 128 : 168;
-  static constexpr int kRegsSoftmax = kMore ? 200 : 208;
-  static constexpr int kRegsOther = kMore ? 56 : 88;
-  static_assert(2 * kRegsSoftmax + (kMore ? 2 : 1) * kRegsOther <= (kMore ? 4 : 3) * kRegsLaunch, "register split");
+  static constexpr bool kWiden = FP8 || FP4;  // V, and with E2M1 K too, is widened to fp16
+  // Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, idle 11; E4M3 and E2M1: converters 12–15; E2M1: all loads 8.
+  static constexpr int kThreads = kWiden ? 512 : 384;
+  static constexpr int kRegsLaunch = kWiden ? 128 : 168;
+  static constexpr int kRegsSoftmax = kWiden ? 200 : 208;
+  static constexpr int kRegsOther = kWiden ? 56 : 88;
+  static_assert(2 * kRegsSoftmax + (kWiden ? 2 : 1) * kRegsOther <= (kWiden ? 4 : 3) * kRegsLaunch, "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
-  static constexpr int kV16 = FP8 ? kBN * D * 2 : 0;
-  static constexpr int kQTile = kRowTile * D * 2;        // bf16, or two E4M3 terms
-  static constexpr int kTerms = !FP8 && TILES == 1 ? 2 : 1;  // of P̃
+  static constexpr int kV16 = kWiden ? kBN * D * 2 : 0;
+  static constexpr int kQTile = kRowTile * D * 2;        // bf16, fp16 or two E4M3 terms
+  static constexpr int kTerms = !kWiden && TILES == 1 ? 2 : 1;  // of P̃
   static constexpr int kFixed = TILES * kQTile + 2 * kV16;
-  static constexpr int kMisc = (FP8 ? 13 : 2) * 1024 + (TILES == 1 ? 4 * 1024 : 0);
+  static constexpr int kMisc = (FP8 ? 13 : FP4 ? 4 : 2) * 1024 + (TILES == 1 ? 4 * 1024 : 0);
   static constexpr int kRoom = 226 * 1024 - kFixed - kMisc;  // 227 KB less the alignment pad
-  static constexpr int kRing = FP4 ? (D == 128 ? 4 : 6) : kRoom / kSlot < 14 ? kRoom / kSlot : 14;
-  static constexpr int kRK = kRing / 2;
-  static constexpr int kRV = kRing - kRK;
+  static constexpr int kRing = kRoom / kSlot < 14 ? kRoom / kSlot : 14;
+  static constexpr int kRK = FP4 ? 2 : kRing / 2;
+  static constexpr int kRV = FP4 ? 2 : kRing - kRK;
   static constexpr int kOffQ = 0;
   static constexpr int kOffV16 = kOffQ + TILES * kQTile;
   static constexpr int kOffK = kOffV16 + 2 * kV16;
   static constexpr int kOffV = kOffK + kRK * kSlot;
   // E2M1: half tiles of codes in what is left.
-  static constexpr int kCodeRoom = (kRoom - kRing * kSlot) / FourBit<D>::kHalf;
+  static constexpr int kCodeRoom = (kRoom - kRK * kSlot) / FourBit<D>::kHalf;
   static constexpr int kCodeRing = !FP4 ? 1 : kCodeRoom < kMaxCodeRing ? kCodeRoom : kMaxCodeRing;
   static_assert(!FP4 || kCodeRing >= 3, "codes on their way");
-  static constexpr int kOffCodes = kOffV + kRV * kSlot;
-  static constexpr int kOffMisc = kOffCodes + (FP4 ? kCodeRing * FourBit<D>::kHalf : 0);
+  static constexpr int kOffCodes = kOffV;
+  static constexpr int kOffMisc = FP4 ? kOffCodes + kCodeRing * FourBit<D>::kHalf : kOffV + kRV * kSlot;
   static constexpr int kSmem = kOffMisc + kMisc + 1024;
   static constexpr uint32_t kColO = 256;                 // TMEM: S of the streams at 0 and 128, O at 256 and 256 + D
   static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && kRV + 4 <= kScaleRing && kSmem <= 227 * 1024, "rings");
@@ -116,15 +116,47 @@ struct Scales {
   float f[2 * kRowTile];                 // what a row's raw scores are multiplied by
 };
 
+// E2M1 only.
+struct Refs {
+  int ref[kTileRing];   // as with E4M3
+  int kref[kTileRing];  // exponent that the tile's widened keys are relative to
+  int range[4];
+  float f[2 * kRowTile];
+};
+
+// Eight elements of a query row, whose other ones the neighbouring kChunks − 1 lanes hold, as fp16 x·2⁻ᵃ; 2⁻ᵃ, which is
+// returned as a, brings the row's largest magnitude to between 2^14 and 2^15.  Exact down to 2⁻³¹ of it.
+template <int kChunks>
+__device__ __forceinline__ int scale_q8(uint4 v, uint4& out) {
+  const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t lo = w4[e] << 16 & 0x7fffffffu, hi = w4[e] & 0x7fff0000u;
+    if (lo < 0x7f800000u) top = max(top, lo);
+    if (hi < 0x7f800000u) top = max(top, hi);
+  }
+#pragma unroll
+  for (int mk = kChunks / 2; mk > 0; mk >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, mk));
+  const int a = max(-126, static_cast<int>(top >> 23) - 127 - 14);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    o[e] = pack_f16x2(__uint_as_float(w4[e] << 16) * inv, __uint_as_float(w4[e] & 0xffff0000u) * inv);
+  out = make_uint4(o[0], o[1], o[2], o[3]);
+  return a;
+}
+
 // Rows of a tile as a K-major operand (rows that are not there as zeros), by the 128 threads of a stream (TILES = 2)
-// or the 256 of both.  E4M3: two terms per element and the factor of the row.
-template <int D, bool FP8, int NT>
+// or the 256 of both.  E4M3: two terms per element and the factor of the row; E2M1: fp16 and the factor.
+template <int D, int F, int NT>
 __device__ __forceinline__ void load_q_tile(const TreeParams& p, const TreeWalk& w, uint8_t* q, float* f, int row0,
                                             int id) {
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row
   constexpr int kPer = kRowTile * kChunks / NT;
   // Loads in flight per thread (bf16 with shared rows spills registers with eight).
-  constexpr int kBatch = NT == 256 && !FP8 ? 4 : kPer < 8 ? kPer : 8;
+  constexpr int kBatch = NT == 256 && F != kCacheE4m3 ? 4 : kPer < 8 ? kPer : 8;
   static_assert(kPer % kBatch == 0, "rows of the tile");
   const int live = w.drafts * p.G - row0;
 #pragma unroll 1
@@ -146,7 +178,12 @@ __device__ __forceinline__ void load_q_tile(const TreeParams& p, const TreeWalk&
       const int i = (i0 + e8) * NT + id;
       const int r = i / kChunks, ch = i % kChunks;
       const uint4 v = q4[e8];
-      if constexpr (!FP8) {
+      if constexpr (F == kCacheE2m1) {
+        uint4 x;
+        const int a = scale_q8<kChunks>(v, x);
+        *reinterpret_cast<uint4*>(q + (ch >> 3) * kRowTile * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+        if (ch == 0) f[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
+      } else if constexpr (F == kCacheBf16) {
         *reinterpret_cast<uint4*>(q + (ch >> 3) * kRowTile * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
       } else {
         uint2 hi, lo;
@@ -218,14 +255,104 @@ static __device__ __noinline__ void split_weights(uint32_t addr) {
   tmem_wait_st();
 }
 
+// E2M1: four warps widen the codes, keys and values alike, a row per thread.  The keys' reference goes with their tile; the
+// values' is a running one, as with E4M3.  Rows past the end become zeros.
+template <int D, int TILES>
+__device__ __forceinline__ void convert_halves(const TreeParams& p, const TreePart& my, uint8_t* smem, Bars* ms, Refs* sc,
+                                              int r) {
+  using C = Cfg<D, kCacheE2m1, TILES>;
+  constexpr int kGroups = D / kE2m1Group;
+  volatile int* abort_flag = &ms->abort_flag;
+  Ring<C::kCodeRing> rc;
+  Ring<C::kRK> rk;
+  int n_k = 0, n_v = 0;      // tiles of the part whose keys and values have been widened
+  int k_ref = 0, v_ref = 0;
+  // As with E4M3, all leave together after a vote on the abort flag.
+  bool ok = true;
+  TreeWalk w;
+  w.begin(p, my);
+  do {
+    const int context = w.len - w.drafts;
+#pragma unroll 1
+    for (int i = w.t0; i <= w.t1 && ok; ++i) {
+      // The keys of tile i, then the values of the one before.
+#pragma unroll 1
+      for (int is_v = i < w.t1 ? 0 : 1; is_v < (i > w.t0 ? 2 : 1); ++is_v) {
+        const int key = (i - is_v) * kBN + r;
+        mbar_wait_inl(&ms->code_full[rc.slot], rc.parity, abort_flag, p.err, tree_site(0x30));
+        __syncwarp();
+        const uint8_t* src = smem + C::kOffCodes + rc.slot * FourBit<D>::kHalf;
+        const uint8_t* at = src + FourBit<D>::kCodes + r * kGroups;
+        const uint32_t bytes = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+        bool counts = key < w.len;
+        if (is_v && counts && key >= context && p.mask != nullptr)  // a drafted key that no row sees takes no part
+          counts = any_token_sees(p.mask + w.b * p.mask_sb + (key - context), w.drafts, p.T);
+        int ref = is_v ? v_ref : k_ref;
+        const bool first = is_v && i == w.t0 + 1;
+        bool far = false;
+        __syncwarp();
+        if (named_any(4, 128, first || (counts && outside_reference<kGroups>(bytes, ref)) || *abort_flag != 0)) {
+          ok = !named_any(4, 128, *abort_flag != 0);
+          if (!ok) break;
+          const int2 range = exponent_range<kGroups>(bytes, counts, 4, sc->range);
+          if (!is_v) {
+            if (range.x > 0) ref = range.x - 127;
+          } else {
+            if (first || range.x - 127 > ref + kFourLazy) ref = range.x - 127;
+            far = range.y - 127 < ref - kFourFar;
+          }
+        }
+        uint8_t* dst;
+        if (!is_v) {
+          k_ref = ref;
+          if (r == 0) sc->kref[n_k % kTileRing] = ref;  // (the scores say that it is there)
+          mbar_wait_inl(&ms->k_empty[rk.slot], rk.parity ^ 1u, abort_flag, p.err, tree_site(0x31));
+          dst = smem + C::kOffK + rk.slot * C::kSlot;
+        } else {
+          v_ref = ref;
+          if (r == 0) {
+            sc->ref[n_v % kTileRing] = ref * 2 + (far ? 1 : 0);
+            mbar_arrive(&ms->ks_full[n_v % kTileRing]);
+          }
+          mbar_wait_inl(&ms->v16_empty[n_v & 1], ((n_v >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x32));
+          dst = smem + C::kOffV16 + (n_v & 1) * C::kV16;
+        }
+        __syncwarp();
+        dst += r * 128;
+        if (!far && key - r + kBN <= (is_v ? context : w.len)) {
+          widen_codes<D>(src + r * (D / 2), bytes, dst, r, ref);
+        } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, dst, r, ref, is_v && key >= context, !counts, far)) {
+          atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((r & 31) == 0) {
+          mbar_arrive(is_v ? &ms->v16_full[n_v & 1] : &ms->k_full[rk.slot]);
+          mbar_arrive(&ms->code_empty[rc.slot]);
+        }
+        __syncwarp();
+        rc.advance();
+        if (!is_v) {
+          rk.advance();
+          ++n_k;
+        } else {
+          ++n_v;
+        }
+      }
+    }
+    __syncwarp();
+    ok = !named_any(4, 128, !ok || *abort_flag != 0);  // the piece's last waits have had none
+  } while (ok && w.next(p));
+}
+
 template <int D, int F, int TILES>
 __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, F, TILES>;
-  constexpr bool FP8 = C::FP8, FP4 = C::FP4;
-  constexpr bool kPg5 = !FP8 && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
+  constexpr bool FP8 = C::FP8, FP4 = C::FP4, kWiden = C::kWiden;
+  constexpr bool kPg5 = !kWiden && D == 128;  // K/V pages as [row group][half][8 rows][128 bytes]
   constexpr int kSlot = C::kSlot;
   constexpr float kLazy = 8.f;             // rescale once the maximum exceeds the reference by this …
-  constexpr float kBase = FP8 ? 3.f : 0.f; // … the new reference lies this below the maximum
+  constexpr float kBase = kWiden ? 3.f : 0.f; // … the new reference lies this below the maximum
   constexpr int kKvLazy = 7;               // E4M3: widened values stay below 448·2^7
   constexpr int kKvFar = 15;               // value rows that are smaller by more than this need bf16's range
   extern __shared__ uint8_t smem_raw[];
@@ -233,8 +360,9 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
   uint8_t* smem = smem_raw + pad;
   Bars* ms = reinterpret_cast<Bars*>(smem + C::kOffMisc);
   constexpr int kOffScales = (sizeof(Bars) + 15) / 16 * 16;
-  constexpr int kOffJoin = kOffScales + (FP8 ? (sizeof(Scales) + 15) / 16 * 16 : 0);
-  Scales* sc = reinterpret_cast<Scales*>(smem + C::kOffMisc + kOffScales);  // E4M3 only
+  using Sc = typename std::conditional<FP4, Refs, Scales>::type;
+  constexpr int kOffJoin = kOffScales + (kWiden ? (sizeof(Sc) + 15) / 16 * 16 : 0);
+  Sc* sc = reinterpret_cast<Sc*>(smem + C::kOffMisc + kOffScales);  // E4M3 and E2M1 only
   Join* join = reinterpret_cast<Join*>(smem + C::kOffMisc + kOffJoin);
   static_assert(kOffJoin + (TILES == 1 ? sizeof(Join) : 0) <= static_cast<size_t>(C::kMisc), "misc block");
   volatile int* abort_flag = &ms->abort_flag;
@@ -256,17 +384,17 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
       mbar_init(&ms->code_empty[s], 4);
     }
     for (int s = 0; s < C::kRV; ++s) {
-      mbar_init(&ms->v_full[s], FP4 ? 4 : 1);
+      mbar_init(&ms->v_full[s], 1);
       mbar_init(&ms->v_empty[s], FP8 ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms->s_full[s], 1);
       mbar_init(&ms->p_full[s], 128);
-      mbar_init(&ms->v16_full[s], 128);
+      mbar_init(&ms->v16_full[s], FP4 ? 4 : 128);
       mbar_init(&ms->v16_empty[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ms->sc_full[s], 1);
-    for (int s = 0; s < kTileRing; ++s) mbar_init(&ms->ks_full[s], 128);
+    for (int s = 0; s < kTileRing; ++s) mbar_init(&ms->ks_full[s], FP4 ? 1 : 128);
     mbar_init(&ms->q_full, 256);
     mbar_init(&ms->drain, 1);
     ms->abort_flag = 0;
@@ -284,10 +412,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
     // nothing left for this CTA
   } else if (FP4 && warp >= 12) {
     reg_dealloc<C::kRegsOther>();
-    if constexpr (FP4)
-      expand_codes<D, C::kCodeRing, C::kRK, C::kRV>(p, my, smem + C::kOffCodes, ms->code_full, ms->code_empty,
-                                                    smem + C::kOffK, ms->k_full, ms->k_empty, smem + C::kOffV, ms->v_full,
-                                                    ms->v_empty, abort_flag, tree_site(0x30), tid - 384);
+    if constexpr (FP4) convert_halves<D, TILES>(p, my, smem, ms, sc, tid - 384);
   } else if (FP4 && warp == 8) {
     reg_dealloc<C::kRegsOther>();
     if constexpr (FP4)
@@ -305,11 +430,13 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
     reg_dealloc<C::kRegsOther>();
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, which keeps descriptors warp-uniform, and one elected lane issues.
-    constexpr uint32_t kIdescS = FP8 ? idesc_e4m3_f32(128, kBN, false, false) : idesc_bf16_f32(128, kBN, false, false);
+    constexpr uint32_t kIdescS = FP8   ? idesc_e4m3_f32(128, kBN, false, false)
+                                 : FP4 ? idesc_f16_f32(128, kBN, false, false)
+                                       : idesc_bf16_f32(128, kBN, false, false);
     constexpr uint32_t kIdescFar = idesc_bf16_f32(128, D, false, true);
-    constexpr uint32_t kIdescO = FP8 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
+    constexpr uint32_t kIdescO = kWiden ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
     const uint32_t sQ = smem_u32(smem + C::kOffQ), sK = smem_u32(smem + C::kOffK);
-    const uint32_t sV = smem_u32(smem + (FP8 ? C::kOffV16 : C::kOffV));
+    const uint32_t sV = smem_u32(smem + (kWiden ? C::kOffV16 : C::kOffV));
     const bool leader = elect_one_lane();
     Ring<C::kRK> rk;
     Ring<C::kRV> rv;
@@ -334,14 +461,14 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
         if (first_use) {
           if (scores) ok = ok && mbar_wait_inl(&ms->k_full[rk.slot], rk.parity, abort_flag, p.err, tree_site(0x25));
           if (product)
-            ok = ok && (FP8 ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(0x2f))
-                            : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24)));
+            ok = ok && (kWiden ? mbar_wait_inl(&ms->v16_full[v16], v16_par, abort_flag, p.err, tree_site(0x2f))
+                               : mbar_wait_inl(&ms->v_full[rv.slot], rv.parity, abort_flag, p.err, tree_site(0x24)));
         }
-        const bool far = FP8 && product && (*static_cast<volatile int*>(&sc->ref[vt % kTileRing]) & 1);
+        const bool far = kWiden && product && (*static_cast<volatile int*>(&sc->ref[vt % kTileRing]) & 1);
         const uint32_t idesc = far ? kIdescFar : kIdescO;
         const uint32_t ts = tmem + g * kBN;
         const uint32_t to = tmem + C::kColO + g * D;
-        const uint32_t vb = sV + (FP8 ? v16 * C::kV16 : rv.slot * kSlot);
+        const uint32_t vb = sV + (kWiden ? v16 * C::kV16 : rv.slot * kSlot);
         const uint32_t kb = sK + rk.slot * kSlot;
         const uint32_t qb = sQ + (TILES == 1 ? 0 : g * C::kQTile);
         const uint64_t vd = kPg5 ? sdesc_sw128(vb, 1024, 2048) : sdesc_sw128(vb, kBN * 128, 1024);
@@ -360,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
               for (int kk = 0; kk < kBN / 16; ++kk)  // A: P̃ over S, 16 keys in 8 columns
                 mma_bf16_ts(to, ts + term * 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc,
                             (s >= 4 || term > 0 || kk > 0) ? 1u : 0u);
-            if (FP8 && far) {  // the second terms
+            if (kWiden && far) {  // the second terms
 #pragma unroll 1
               for (int kk = 0; kk < kBN / 16; ++kk)
                 mma_bf16_ts(to, ts + 64 + kk * 8, vd + kk * (kPg5 ? 256 : 128), idesc, 1u);
@@ -369,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
           p_par ^= 1u << g;
           // With shared rows the value slot is given back at once (after the scores' issue: 1 us of 104 slower); with two
           // row tiles the scores' issue comes first (the other way round 135 instead of 130 us: 256 rows, 8 x 16384 keys).
-          if (TILES == 1 && leader) mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
+          if (TILES == 1 && leader) mma_commit(kWiden ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
         }
         if (scores && leader) {  // S over what P̃V has just read: the tensor pipe runs them in this order
           if constexpr (FP8) {
@@ -382,14 +509,14 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
           } else {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ss(ts, qd + (kk >> 2) * (kRowTile * 8) + (kk & 3) * 2, kd + (kk >> 2) * 64 + (kk & 3) * 2, kIdescS,
+              mma_bf16_ss(ts, qd + (kk >> 2) * (kRowTile * 8) + (kk & 3) * 2, kd + (kk >> 2) * (FP4 ? kBN * 8 : 64) + (kk & 3) * 2, kIdescS,
                           kk > 0 ? 1u : 0u);
           }
         }
         if (leader) {
           if (scores || product) mma_commit(&ms->s_full[g]);  // scores, or, where none follow, O of the piece
           if (last_use && scores) mma_commit(&ms->k_empty[rk.slot]);
-          if (TILES == 2 && last_use && product) mma_commit(FP8 ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
+          if (TILES == 2 && last_use && product) mma_commit(kWiden ? &ms->v16_empty[v16] : &ms->v_empty[rv.slot]);
         }
         if (last_use && scores) rk.advance();
         if (last_use && product) {
@@ -431,10 +558,10 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
       // Q of the piece: the stream's tile, or both streams' shares of the one tile.  The products of the piece before
       // that read its place are done: their results have been taken (by both streams, which end a shared piece together).
       if constexpr (TILES == 2)
-        load_q_tile<D, FP8, 128>(p, w, smem + C::kOffQ + g * C::kQTile, FP8 ? sc->f + g * kRowTile : nullptr, my_row0,
+        load_q_tile<D, F, 128>(p, w, smem + C::kOffQ + g * C::kQTile, kWiden ? sc->f + g * kRowTile : nullptr, my_row0,
                                  kt);
       else
-        load_q_tile<D, FP8, 256>(p, w, smem + C::kOffQ, FP8 ? sc->f : nullptr, my_row0, tid);
+        load_q_tile<D, F, 256>(p, w, smem + C::kOffQ, kWiden ? sc->f : nullptr, my_row0, tid);
       mbar_arrive(&ms->q_full);
 
       float m_run = -INFINITY, l_run = 0.f;
@@ -451,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
           const uint4 s4 = seen_keys(row, t, context - k0, live ? min(kBN, w.len - k0) : 0);
           seen[0] = s4.x, seen[1] = s4.y, seen[2] = s4.z, seen[3] = s4.w;
         }
-        if constexpr (FP8)  // the keys' powers of two
+        if constexpr (kWiden)  // the keys' powers of two, and what the widened tile is relative to
           ok = mbar_wait_inl(&ms->ks_full[tile % kTileRing], (tile / kTileRing) & 1, abort_flag, p.err, tree_site(0x26)) && ok;
         // (P̃V of the stream's tile before has run too: S was issued behind it.)
         ok = mbar_wait_inl(&ms->s_full[g], s_par, abort_flag, p.err, tree_site(0x27)) && ok;
@@ -494,6 +621,9 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
               fmul2(s[e + 2], s[e + 3], s[e + 2], s[e + 3], k4.z, k4.w);
             }
           }
+          // (Not 0, as with E4M3.)
+          if constexpr (FP4)
+            factor = fmaxf(sc->f[(TILES == 1 ? 0 : g * kRowTile) + kt] * power_f32(sc->kref[tile % kTileRing]), 1e-45f);
           if (tail) {
 #pragma unroll
             for (int e = 0; e < kBN; ++e)
@@ -514,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
           l_run *= corr;
           bool moved = need;
           bool far = false;  // E4M3: the tile has gone over to bf16
-          if constexpr (FP8) {
+          if constexpr (kWiden) {
             const int code = sc->ref[tile % kTileRing];
             const int ref = code >> 1;
             far = code & 1;
@@ -546,17 +676,17 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
                 split_weights2(x[0], x[1], pk[e / 2], lo[e / 2]);
                 split_weights2(x[2], x[3], pk[e / 2 + 1], lo[e / 2 + 1]);
               } else {
-                pk[e / 2] = FP8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
-                pk[e / 2 + 1] = FP8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
+                pk[e / 2] = kWiden ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+                pk[e / 2 + 1] = kWiden ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
               }
             }
             tmem_st(s_addr + k / 2, pk);
             if constexpr (C::kTerms == 2) tmem_st(s_addr + 64 + k / 2, lo);
           }
           l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          if (FP8 && far) split_weights(s_addr);
+          if (kWiden && far) split_weights(s_addr);
         }
-        if (!FP8 && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
+        if (!kWiden && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
           // Key kt's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
           // (Two row tiles: the first stream does it for both, its product is issued first.)
           const int slot = tile % C::kRV;
@@ -605,9 +735,9 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
       const float inv = sum != 0.f ? 1.f / sum : 0.f;
       // E4M3: times the power of two that the values are relative to, half of it here and half at the end: the whole of it
       // may be too small a number.
-      const int half_kv = FP8 ? (TILES == 1 ? max(join->kv[0], join->kv[1]) : kv_ref) >> 1 : 0;
+      const int half_kv = kWiden ? (TILES == 1 ? max(join->kv[0], join->kv[1]) : kv_ref) >> 1 : 0;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) scale[e] *= inv * (FP8 ? power_f32((TILES == 1 ? join->kv[e] : kv_ref) - half_kv) : 1.f);
+      for (int e = 0; e < 2; ++e) scale[e] *= inv * (kWiden ? power_f32((TILES == 1 ? join->kv[e] : kv_ref) - half_kv) : 1.f);
       const bool fine = __all_sync(0xffffffffu, ok);
       if (fine && live && (TILES == 2 || g == 0)) {
         if (!whole) {
@@ -646,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
                 ffma2(o[q], o[q + 1], __uint_as_float(r[q]), __uint_as_float(r[q + 1]), scale[e], scale[e], o[q], o[q + 1]);
             }
           }
-          if constexpr (FP8) {
+          if constexpr (kWiden) {
             const float power = power_f32(half_kv);
 #pragma unroll
             for (int q = 0; q < 32; q += 2) fmul2(o[q], o[q + 1], o[q], o[q + 1], power, power);
@@ -696,6 +826,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
     }
   } else if (FP8 && warp >= 12) {
     reg_dealloc<C::kRegsOther>();
+    if constexpr (FP8) {
     // ------------------------------------ converters: one value row and one key's scale per thread
     const int r = tid - 384;
     int next = 0, ref = 0;  // the tile of the part whose scales come next
@@ -795,6 +926,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
       }
       vote();  // the piece's last waits have had none
     } while (ok && w.next(p));
+    }
   } else {
     reg_dealloc<C::kRegsOther>();  // idle until the end
   }

@@ -22,11 +22,11 @@ def values(packed, scales):
 
 
 def check_tree4(o, lse, q, paged, drafts, mask, scale, heads=None):
-    """``check_tree`` with the bounds that hold for a cache in four bits: up to 32 rows that share a key head its weights are
-    fp16 and q two E4M3 terms, as with E4M3 (the same roundings: fp16 weights are off by 2^-11 of themselves, or below 2^-14
-    by half of 2^-24 where the row's largest is at least 2^3); beyond, they are bf16, and q is as it is."""
-    rows = q.shape[2] * (q.shape[1] // paged.hkv)
-    paged.cache = "e4m3" if rows <= 32 else "bf16"
+    """``check_tree`` with the bounds of an E4M3 cache, which hold for one in four bits: its weights are fp16 too (off by 2^-11
+    of themselves, or below 2^-14 by half of 2^-24 where the row's largest is at least 2^3); up to 32 rows that share a key
+    head q goes in as two E4M3 terms, beyond as fp16 with 16 bits below the row's largest (both within 2^-18 of it); and
+    values times their groups' powers of two are exact."""
+    paged.cache = "e4m3"
     check_tree(o, lse, q, paged, drafts, mask, scale, heads)
 
 
