@@ -56,12 +56,15 @@ template <int D, int F, int TILES>
 struct Cfg {
   static constexpr bool FP8 = F == kCacheE4m3, FP4 = F == kCacheE2m1;
   static constexpr bool kWiden = FP8 || FP4;  // V, and with E2M1 K too, is widened to fp16
-  // Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, idle 11; E4M3 and E2M1: converters 12–15; E2M1: all loads 8.
-  static constexpr int kThreads = kWiden ? 512 : 384;
-  static constexpr int kRegsLaunch = kWiden ? 128 : 168;
-  static constexpr int kRegsSoftmax = kWiden ? 200 : 208;
+  // Warps: streams 0–3 and 4–7, K loads 8, MMA 9, V loads 10, idle 11; E4M3: converters 12–15; E2M1: all loads 8,
+  // converters of keys 12–15 and of values 16–19.
+  static constexpr int kThreads = FP4 ? 640 : FP8 ? 512 : 384;
+  static constexpr int kRegsLaunch = FP4 ? 96 : FP8 ? 128 : 168;
+  static constexpr int kRegsSoftmax = FP4 ? 144 : FP8 ? 200 : 208;
   static constexpr int kRegsOther = kWiden ? 56 : 88;
-  static_assert(2 * kRegsSoftmax + (kWiden ? 2 : 1) * kRegsOther <= (kWiden ? 4 : 3) * kRegsLaunch, "register split");
+  static constexpr int kRegsConvert = FP4 ? 64 : FP8 ? kRegsOther : 0;
+  static_assert(2 * kRegsSoftmax + kRegsOther + (FP4 ? 2 : 1) * kRegsConvert <= kThreads / 128 * kRegsLaunch,
+                "register split");
   static constexpr int kSlot = kBN * D * (FP8 ? 1 : 2);
   static constexpr int kV16 = kWiden ? kBN * D * 2 : 0;
   static constexpr int kQTile = kRowTile * D * 2;        // bf16, fp16 or two E4M3 terms
@@ -94,7 +97,7 @@ struct Bars {
   uint64_t s_full[2], p_full[2], v16_full[2], v16_empty[2], ks_full[kTileRing], sc_full[kScaleRing];
   uint64_t q_full, drain;
   uint32_t bad[8][8];       // drafted keys with non-finite values, of up to eight pieces
-  long long warp_sum[16];
+  long long warp_sum[20];
   TreeWalk walk[2];         // of the streams
   int more[2];
   int start[3];
@@ -120,7 +123,7 @@ struct Scales {
 struct Refs {
   int ref[kTileRing];   // as with E4M3
   int kref[kTileRing];  // exponent that the tile's widened keys are relative to
-  int range[4];
+  int range[2][4];      // of keys and values, per warp
   float f[2 * kRowTile];
 };
 
@@ -255,93 +258,76 @@ static __device__ __noinline__ void split_weights(uint32_t addr) {
   tmem_wait_st();
 }
 
-// E2M1: four warps widen the codes, keys and values alike, a row per thread.  The keys' reference goes with their tile; the
-// values' is a running one, as with E4M3.  Rows past the end become zeros.
-template <int D, int TILES>
+// E2M1: four warps widen the keys' codes and four the values', a row per thread.  The keys' reference goes with their
+// tile; the values' is a running one, as with E4M3.  Rows past the end become zeros.
+template <int D, int TILES, bool VALUES>
 __device__ __forceinline__ void convert_halves(const TreeParams& p, const TreePart& my, uint8_t* smem, Bars* ms, Refs* sc,
                                               int r) {
   using C = Cfg<D, kCacheE2m1, TILES>;
   constexpr int kGroups = D / kE2m1Group;
+  constexpr int kBar = VALUES ? 5 : 4;
   volatile int* abort_flag = &ms->abort_flag;
-  Ring<C::kCodeRing> rc;
-  Ring<C::kRK> rk;
-  int n_k = 0, n_v = 0;      // tiles of the part whose keys and values have been widened
-  int k_ref = 0, v_ref = 0;
+  int base = 0;          // halves of the pieces before
+  int used = 0, ref = 0; // tiles of the part that have been widened, and what the last one is relative to
   // As with E4M3, all leave together after a vote on the abort flag.
   bool ok = true;
   TreeWalk w;
   w.begin(p, my);
   do {
-    const int context = w.len - w.drafts;
+    const int context = w.len - w.drafts, tiles = w.t1 - w.t0;
 #pragma unroll 1
-    for (int i = w.t0; i <= w.t1 && ok; ++i) {
-      // The keys of tile i, then the values of the one before.
-#pragma unroll 1
-      for (int is_v = i < w.t1 ? 0 : 1; is_v < (i > w.t0 ? 2 : 1); ++is_v) {
-        const int key = (i - is_v) * kBN + r;
-        mbar_wait_inl(&ms->code_full[rc.slot], rc.parity, abort_flag, p.err, tree_site(0x30));
-        __syncwarp();
-        const uint8_t* src = smem + C::kOffCodes + rc.slot * FourBit<D>::kHalf;
-        const uint8_t* at = src + FourBit<D>::kCodes + r * kGroups;
-        const uint32_t bytes = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-        bool counts = key < w.len;
-        if (is_v && counts && key >= context && p.mask != nullptr)  // a drafted key that no row sees takes no part
-          counts = any_token_sees(p.mask + w.b * p.mask_sb + (key - context), w.drafts, p.T);
-        int ref = is_v ? v_ref : k_ref;
-        const bool first = is_v && i == w.t0 + 1;
-        bool far = false;
-        __syncwarp();
-        if (named_any(4, 128, first || (counts && outside_reference<kGroups>(bytes, ref)) || *abort_flag != 0)) {
-          ok = !named_any(4, 128, *abort_flag != 0);
-          if (!ok) break;
-          const int2 range = exponent_range<kGroups>(bytes, counts, 4, sc->range);
-          if (!is_v) {
-            if (range.x > 0) ref = range.x - 127;
-          } else {
-            if (first || range.x - 127 > ref + kFourLazy) ref = range.x - 127;
-            far = range.y - 127 < ref - kFourFar;
-          }
-        }
-        uint8_t* dst;
-        if (!is_v) {
-          k_ref = ref;
-          if (r == 0) sc->kref[n_k % kTileRing] = ref;  // (the scores say that it is there)
-          mbar_wait_inl(&ms->k_empty[rk.slot], rk.parity ^ 1u, abort_flag, p.err, tree_site(0x31));
-          dst = smem + C::kOffK + rk.slot * C::kSlot;
-        } else {
-          v_ref = ref;
-          if (r == 0) {
-            sc->ref[n_v % kTileRing] = ref * 2 + (far ? 1 : 0);
-            mbar_arrive(&ms->ks_full[n_v % kTileRing]);
-          }
-          mbar_wait_inl(&ms->v16_empty[n_v & 1], ((n_v >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x32));
-          dst = smem + C::kOffV16 + (n_v & 1) * C::kV16;
-        }
-        __syncwarp();
-        dst += r * 128;
-        if (!far && key - r + kBN <= (is_v ? context : w.len)) {
-          widen_codes<D>(src + r * (D / 2), bytes, dst, r, ref);
-        } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, dst, r, ref, is_v && key >= context, !counts, far)) {
-          atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if ((r & 31) == 0) {
-          mbar_arrive(is_v ? &ms->v16_full[n_v & 1] : &ms->k_full[rk.slot]);
-          mbar_arrive(&ms->code_empty[rc.slot]);
-        }
-        __syncwarp();
-        rc.advance();
-        if (!is_v) {
-          rk.advance();
-          ++n_k;
-        } else {
-          ++n_v;
+    for (int i = 0; i < tiles; ++i, ++used) {
+      const int at = base + (VALUES ? (i == tiles - 1 ? 2 * i + 1 : 2 * i + 2) : max(2 * i - 1, 0));  // place in the ring's order
+      const int slot = at % C::kCodeRing, key = (w.t0 + i) * kBN + r;
+      mbar_wait_inl(&ms->code_full[slot], (at / C::kCodeRing) & 1, abort_flag, p.err, tree_site(VALUES ? 0x32 : 0x30));
+      __syncwarp();
+      const uint8_t* src = smem + C::kOffCodes + slot * FourBit<D>::kHalf;
+      const uint8_t* sb = src + FourBit<D>::kCodes + r * kGroups;
+      const uint32_t bytes = D == 128 ? *reinterpret_cast<const uint32_t*>(sb) : *reinterpret_cast<const uint16_t*>(sb);
+      bool counts = key < w.len;
+      if (VALUES && counts && key >= context && p.mask != nullptr)  // a drafted key that no row sees takes no part
+        counts = any_token_sees(p.mask + w.b * p.mask_sb + (key - context), w.drafts, p.T);
+      bool far = false;
+      const bool first = VALUES && i == 0;
+      __syncwarp();
+      if (named_any(kBar, 128, first || (counts && outside_reference<kGroups>(bytes, ref)) || *abort_flag != 0)) {
+        ok = !named_any(kBar, 128, *abort_flag != 0);
+        if (!ok) break;
+        const int2 range = exponent_range<kGroups>(bytes, counts, kBar, sc->range[VALUES]);
+        if (VALUES) {
+          if (first || range.x - 127 > ref + kFourLazy) ref = range.x - 127;
+          far = range.y - 127 < ref - kFourFar;
+        } else if (range.x > 0) {
+          ref = range.x - 127;
         }
       }
+      if (VALUES) {
+        if (r == 0) {
+          sc->ref[used % kTileRing] = ref * 2 + (far ? 1 : 0);
+          mbar_arrive(&ms->ks_full[used % kTileRing]);
+        }
+        mbar_wait_inl(&ms->v16_empty[used & 1], ((used >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x33));
+      } else {
+        if (r == 0) sc->kref[used % kTileRing] = ref;  // (the scores say that it is there)
+        mbar_wait_inl(&ms->k_empty[used & 1], ((used >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x31));
+      }
+      __syncwarp();
+      uint8_t* dst = smem + (VALUES ? C::kOffV16 : C::kOffK) + (used & 1) * C::kSlot + r * 128;
+      if (!far && key - r + kBN <= (VALUES ? context : w.len)) {
+        widen_codes<D>(src + r * (D / 2), bytes, dst, r, ref);
+      } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, dst, r, ref, VALUES && key >= context, !counts, far)) {
+        atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if ((r & 31) == 0) {
+        mbar_arrive(VALUES ? &ms->v16_full[used & 1] : &ms->k_full[used & 1]);
+        mbar_arrive(&ms->code_empty[slot]);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-    ok = !named_any(4, 128, !ok || *abort_flag != 0);  // the piece's last waits have had none
+    base += 2 * tiles;
+    ok = !named_any(kBar, 128, !ok || *abort_flag != 0);  // the piece's last waits have had none
   } while (ok && w.next(p));
 }
 
@@ -411,8 +397,13 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
   if (my.count <= 0) {
     // nothing left for this CTA
   } else if (FP4 && warp >= 12) {
-    reg_dealloc<C::kRegsOther>();
-    if constexpr (FP4) convert_halves<D, TILES>(p, my, smem, ms, sc, tid - 384);
+    reg_dealloc<C::kRegsConvert>();
+    if constexpr (FP4) {
+      if (warp < 16)
+        convert_halves<D, TILES, false>(p, my, smem, ms, sc, tid & 127);
+      else
+        convert_halves<D, TILES, true>(p, my, smem, ms, sc, tid & 127);
+    }
   } else if (FP4 && warp == 8) {
     reg_dealloc<C::kRegsOther>();
     if constexpr (FP4)
@@ -589,7 +580,75 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
         }
         tc_fence_after();
         // A warp without live rows leaves its P̃ as it is: it only reaches its own rows of O, which nobody reads.
-        if (busy) {
+        if constexpr (FP4) {
+          if (busy) {
+            // The scores are read twice, 32 at a time, in loops that are not unrolled: with the converters' code beside it the
+            // other formats' way, which holds 128 scores and takes as much code, waited for instructions.
+            uint4 see = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (tail) see = make_uint4(seen[0], seen[1], seen[2], seen[3]);
+            auto fetch = [&](int c, uint32_t (&x)[32]) {
+              tmem_ld32(s_addr + c, x);
+              tmem_wait_ld();
+              reg_fence(x);
+              if (tail) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((see.x >> e) & 1)) x[e] = 0xff800000u;
+                see = make_uint4(see.y, see.z, see.w, see.x);
+              }
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kBN; c += 32) {
+              uint32_t x[32];
+              fetch(c, x);
+              float mx[4] = {top, __uint_as_float(x[29]), __uint_as_float(x[30]), __uint_as_float(x[31])};
+#pragma unroll
+              for (int e = 0; e < 28; e += 8)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  mx[q] = fmax3(mx[q], __uint_as_float(x[e + q]), __uint_as_float(x[e + 4 + q < 28 ? e + 4 + q : 28]));
+              top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+            }
+            // (Not 0, as with E4M3.)
+            const float factor =
+                fmaxf(sc->f[(TILES == 1 ? 0 : g * kRowTile) + kt] * power_f32(sc->kref[tile % kTileRing]), 1e-45f);
+            const float m_cand = top * factor;
+            const bool need = m_cand > m_run + kLazy;
+            const float m_new = need ? m_cand - kBase : m_run;
+            float corr = need ? ex2_approx(m_run - m_new) : 1.f;
+            l_run *= corr;
+            const int code = sc->ref[tile % kTileRing];
+            const bool moved = done > 0 && code >> 1 != kv_ref;  // the widened values are relative to another exponent
+            if (moved) corr *= exp2f(static_cast<float>(max(kv_ref - (code >> 1), -200)));
+            kv_ref = code >> 1;
+            m_run = m_new;
+            if (done > 0 && __any_sync(0xffffffffu, need || moved)) rescale_row<D>(o_addr, corr);
+            const float neg = m_new == -INFINITY ? 0.f : -m_new;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int c = 0; c < kBN; c += 32) {
+              uint32_t x[32], pk[16];
+              fetch(c, x);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                float y[4] = {__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
+                              __uint_as_float(x[e + 3])};
+                ffma2(y[0], y[1], y[0], y[1], factor, factor, neg, neg);
+                ffma2(y[2], y[3], y[2], y[3], factor, factor, neg, neg);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) y[q] = ex2_approx(y[q]);
+                fadd2(sum[0], sum[1], sum[0], sum[1], y[0], y[1]);
+                fadd2(sum[2], sum[3], sum[2], sum[3], y[2], y[3]);
+                pk[e / 2] = pack_f16x2(y[0], y[1]);
+                pk[e / 2 + 1] = pack_f16x2(y[2], y[3]);
+              }
+              tmem_st(s_addr + c / 2, pk);  // over scores that have been read
+            }
+            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (code & 1) split_weights(s_addr);
+          }
+        } else if (busy) {
           float s[kBN];
           {
             uint32_t r0[32], r1[32], r2[32], r3[32];
@@ -621,9 +680,6 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
               fmul2(s[e + 2], s[e + 3], s[e + 2], s[e + 3], k4.z, k4.w);
             }
           }
-          // (Not 0, as with E4M3.)
-          if constexpr (FP4)
-            factor = fmaxf(sc->f[(TILES == 1 ? 0 : g * kRowTile) + kt] * power_f32(sc->kref[tile % kTileRing]), 1e-45f);
           if (tail) {
 #pragma unroll
             for (int e = 0; e < kBN; ++e)
@@ -644,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
           l_run *= corr;
           bool moved = need;
           bool far = false;  // E4M3: the tile has gone over to bf16
-          if constexpr (kWiden) {
+          if constexpr (FP8) {
             const int code = sc->ref[tile % kTileRing];
             const int ref = code >> 1;
             far = code & 1;
@@ -676,15 +732,15 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
                 split_weights2(x[0], x[1], pk[e / 2], lo[e / 2]);
                 split_weights2(x[2], x[3], pk[e / 2 + 1], lo[e / 2 + 1]);
               } else {
-                pk[e / 2] = kWiden ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
-                pk[e / 2 + 1] = kWiden ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
+                pk[e / 2] = FP8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+                pk[e / 2 + 1] = FP8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
               }
             }
             tmem_st(s_addr + k / 2, pk);
             if constexpr (C::kTerms == 2) tmem_st(s_addr + 64 + k / 2, lo);
           }
           l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          if (kWiden && far) split_weights(s_addr);
+          if (FP8 && far) split_weights(s_addr);
         }
         if (!kWiden && tail && k0 + kt >= context && (TILES == 1 || g == 0)) {
           // Key kt's value row: zeros past the end, and in place of what a drafted row holds that is not finite.
