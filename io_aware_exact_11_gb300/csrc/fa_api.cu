@@ -1422,6 +1422,8 @@ fa_status fa_cache_compact(void* k_cache, void* v_cache, uint8_t* k_scale, uint8
     return fail(FA_ERR_INVALID_ARG, "%s: first, keep and keep_lens must be 4-byte aligned", who);
   if (keep_stride_b < 0) return fail(FA_ERR_INVALID_ARG, "%s: keep_stride_b must be >= 0", who);
   if (static_cast<int64_t>(B) * H_kv > (1 << 27)) return fail(FA_ERR_UNSUPPORTED, "%s: B * H_kv too large", who);
+  if (static_cast<int64_t>(num_blocks) * block_size > UINT32_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "%s: num_blocks * block_size too large", who);
   fa::MoveParams p = move_params(k_cache, v_cache, k_scale, v_scale, H_kv, num_blocks, block_size);
   if ((r = watchdog_ptr(&p.err)) != FA_OK) return r;
   p.block_table = block_table;

@@ -60,7 +60,8 @@ def _same(dev, kw, host):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("B,hkv,N,bs,first,kind", [
     (1, 1, 1, 16, [0], "some"), (3, 2, 8, 16, [0, 5, 40], "some"), (2, 4, 64, 32, [130, 3], "some"), (1, 2, 700, 64, [17], "rising"),
-    (2, 1, 1300, 16, [0, 9], "rising"), (1, 3, 1100, 128, [2], "any"), (2, 2, 600, 16, [1, 0], "same")])
+    (2, 1, 1300, 16, [0, 9], "rising"), (1, 3, 1100, 128, [2], "any"), (2, 2, 600, 16, [1, 0], "same"),
+    (1, 1, 9000, 16, [100], "any"), (20, 4, 1100, 16, [3 * b for b in range(20)], "rising")])
 def test_rows_are_moved_as_if_all_were_read_first(cache, d, B, hkv, N, bs, first, kind):
     rng = np.random.default_rng(N + d)
     reach = max(first) + 2 * N + 40
