@@ -175,7 +175,7 @@ struct MoveParams {
 };
 
 // Pages shared, freed and reserved (fa_pages.cu).
-constexpr int kPageSegment = 4096;  // pages that one block of the reserving kernels looks at
+constexpr int kPageSegment = 1024;  // pages that one block of the reserving kernels looks at
 struct PageParams {
   int* block_table;  // [B, max_blocks], −1 where there is no page
   int* seq_lens;     // [B]

@@ -958,12 +958,11 @@ def pages_reserve(block_table, seq_lens, holders, new_lens, block_size: int, wor
             return pages_reserve(block_table, seq_lens, holders, new_lens, block_size, workspace)
     B, max_blocks, nb = _check_pages(block_table, seq_lens, holders)
     _check_lens("new_lens", new_lens, B)
-    out = torch.empty((3, B), dtype=torch.int32, device=block_table.device)
+    granted, src, dst = torch.empty_like(new_lens), torch.empty_like(new_lens), torch.empty_like(new_lens)
     if workspace is None:
         workspace = torch.empty(max(pages_reserve_workspace_size(B, nb), 16), dtype=torch.uint8, device=block_table.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    granted, src, dst = out.unbind()
     status = lib().fa_pages_reserve(block_table.data_ptr(), seq_lens.data_ptr(), holders.data_ptr(), new_lens.data_ptr(),
                                     granted.data_ptr(), src.data_ptr(), dst.data_ptr(), B, nb, block_size, max_blocks,
                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
