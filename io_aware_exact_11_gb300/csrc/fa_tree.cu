@@ -405,7 +405,7 @@ __device__ __forceinline__ void convert_values(const TreeParams& p, const TreePa
       if (used > 0) mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, tree_site(0x13));
       __syncwarp();
       if (!far && (w.t0 + i + 1) * kTreeBN <= context) {
-        widen_codes<D>(src + r * (D / 2), bytes, v_tile, r, ref);
+        widen_codes<D, 1>(src + r * (D / 2), bytes, v_tile, r, ref);
       } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, v_tile, r, ref, key >= context, !counts, far)) {
         atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
       }
@@ -426,7 +426,8 @@ __device__ __forceinline__ void convert_values(const TreeParams& p, const TreePa
 }
 
 // E2M1: the products of one stream, by a warp each.  The whole warp runs the loop, which keeps descriptors warp-uniform,
-// and one elected lane issues.
+// and one elected lane issues, in loops that are not unrolled (64 ragged sequences of up to 8192 keys: 100 us instead of 103;
+// all roles compete for instruction fetches).
 template <int D, int NR>
 __device__ __forceinline__ void issue_products(const TreeParams& p, const TreePart& my, uint8_t* smem,
                                                Misc<NR, kCacheE2m1>* ms, uint32_t tmem, int g) {
@@ -461,7 +462,7 @@ __device__ __forceinline__ void issue_products(const TreeParams& p, const TreePa
         if (leader) {
           // A k-step is a group of 32 elements, whose power of two the product applies.  Both of q's terms are columns.
           const uint64_t ad = k_desc + b * (C::kSlot >> 4);
-#pragma unroll
+#pragma unroll 1
           for (int kk = 0; kk < D / 32; ++kk)
             mma_mx_ss(ds, ad + kk * 2, q_desc + kk * 2, idesc_mx_e2m1_e4m3(128, 2 * NR, kk), scales + 4 * b, ones,
                       kk > 0 ? 1u : 0u);
@@ -481,7 +482,7 @@ __device__ __forceinline__ void issue_products(const TreeParams& p, const TreePa
         const bool far = *static_cast<volatile int*>(&ms->far[g]) != 0;
         if (leader) {
           const uint32_t idesc = far ? kIdescFar : kIdescO;
-#pragma unroll
+#pragma unroll 1
           for (int kk = 0; kk < kBN / 16; ++kk)
             mma_bf16_ss(dst, v_desc + kk * 128, p_desc + kk * 128, idesc, (s > 1 || kk > 0) ? 1u : 0u);
           if (far) {  // the second terms

@@ -513,10 +513,12 @@ __device__ __forceinline__ int group_at(int j, int r) {
 }
 
 // Widens one row of E2M1 codes to fp16, each group times its power of two relative to 2^ref.
-// src: the row's codes, scales: its bytes.
-template <int D>
+// src: the row's codes, scales: its bytes.  A larger body costs instruction fetches, which all warps' roles compete for:
+// 8 x 32768 keys, 256 rows take 261 us with one group at a time, 255 with two, 289 with four; 64 ragged sequences of up to
+// 8192 keys in the kernel for few rows, which has more roles, 103, 111 and 123.
+template <int D, int UNROLL>
 __device__ __forceinline__ void widen_codes(const uint8_t* src, uint32_t scales, uint8_t* dst, int r, int ref) {
-#pragma unroll 1
+#pragma unroll UNROLL
   for (int j = 0; j < D / kE2m1Group; ++j) {
     const int g = group_at<D>(j, r);
     const uint4 c = *reinterpret_cast<const uint4*>(src + g * 16);

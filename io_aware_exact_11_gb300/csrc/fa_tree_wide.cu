@@ -314,7 +314,7 @@ __device__ __forceinline__ void convert_halves(const TreeParams& p, const TreePa
       __syncwarp();
       uint8_t* dst = smem + (VALUES ? C::kOffV16 : C::kOffK) + (used & 1) * C::kSlot + r * 128;
       if (!far && key - r + kBN <= (VALUES ? context : w.len)) {
-        widen_codes<D>(src + r * (D / 2), bytes, dst, r, ref);
+        widen_codes<D, 2>(src + r * (D / 2), bytes, dst, r, ref);
       } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, dst, r, ref, VALUES && key >= context, !counts, far)) {
         atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
       }
