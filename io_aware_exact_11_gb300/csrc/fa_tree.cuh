@@ -373,10 +373,10 @@ __device__ __forceinline__ bool outside_reference(uint32_t bytes, int ref) {
   }
   return outside;
 }
-// The largest and the smallest exponent byte of the rows of 128 threads that count, by all of them, with barrier `bar`
-// (0 and 255 if there is none).  NaN, and next to nothing for the smallest, do not count.
+// The largest and the smallest of G exponent bytes (0 and 255 if there is none).  NaN, and next to nothing for the smallest,
+// do not count.
 template <int G>
-__device__ __forceinline__ int2 exponent_range(uint32_t bytes, bool counts, int bar, int* range) {
+__device__ __forceinline__ int2 exponent_range(uint32_t bytes) {
   int top = 0, low = 255;
 #pragma unroll
   for (int j = 0; j < G; ++j) {
@@ -384,8 +384,14 @@ __device__ __forceinline__ int2 exponent_range(uint32_t bytes, bool counts, int 
     if (e != 255) top = max(top, e);
     if (e > 1) low = min(low, e);
   }
-  top = __reduce_max_sync(0xffffffffu, counts ? top : 0);
-  low = __reduce_min_sync(0xffffffffu, counts ? low : 255);
+  return make_int2(top, low);
+}
+// The same for the rows of 128 threads that count, by all of them, with barrier `bar`.
+template <int G>
+__device__ __forceinline__ int2 exponent_range(uint32_t bytes, bool counts, int bar, int* range) {
+  const int2 mine = exponent_range<G>(bytes);
+  const int top = __reduce_max_sync(0xffffffffu, counts ? mine.x : 0);
+  const int low = __reduce_min_sync(0xffffffffu, counts ? mine.y : 255);
   if ((threadIdx.x & 31) == 0) range[(threadIdx.x >> 5) & 3] = top << 8 | (255 - low);
   __syncwarp();
   named_sync(bar, 128);

@@ -122,9 +122,10 @@ struct Scales {
 // E2M1 only.
 struct Refs {
   int ref[kTileRing];   // as with E4M3
-  int kref[kTileRing];  // exponent that the tile's widened keys are relative to
+  int kref[kTileRing];  // 2·(exponent that the tile's widened keys are relative to), or 1: each to its own, in power
   int range[2][4];      // of keys and values, per warp
   float f[2 * kRowTile];
+  alignas(16) uint8_t power[kTileRing][kBN];
 };
 
 // Eight elements of a query row, whose other ones the neighbouring kChunks − 1 lanes hold, as fp16 x·2⁻ᵃ; 2⁻ᵃ, which is
@@ -223,6 +224,26 @@ __device__ __forceinline__ void rescale_row(uint32_t addr, float k) {
 // 2^e for e from −127 on (0 below).
 __device__ __forceinline__ float power_f32(int e) { return __uint_as_float(static_cast<uint32_t>(max(e, -127) + 127) << 23); }
 
+// E2M1, keys far apart: a row's scores times the keys' own powers of two (byte 0: 2^−127, below the normal numbers).
+static __device__ __noinline__ void scale_scores(uint32_t addr, const uint8_t* power) {
+#pragma unroll 1
+  for (int c = 0; c < kBN; c += 16) {
+    uint32_t x[16];
+    tmem_ld(addr + c, x);
+    tmem_wait_ld();
+    reg_fence(x);
+    const uint4 b = *reinterpret_cast<const uint4*>(power + c);
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t k = w[e >> 2] >> (8 * (e & 3)) & 0xffu;
+      x[e] = __float_as_uint(__uint_as_float(x[e]) * __uint_as_float(k == 0 ? 0x00400000u : k << 23));
+    }
+    tmem_st(addr + c, x);
+  }
+  tmem_wait_st();
+}
+
 // Which keys of a tile token t sees: all before `context` (a place in the tile, maybe before it) and, up to `end`, the
 // drafted ones behind that its row of the mask names.
 static __device__ __noinline__ uint4 seen_keys(const uint8_t* row, int t, int context, int end) {
@@ -258,8 +279,22 @@ static __device__ __noinline__ void split_weights(uint32_t addr) {
   tmem_wait_st();
 }
 
+// A key of a tile that holds the end (dead: zeros) or, with a place for its own power of two, of one whose keys lie far apart.
+template <int D>
+__device__ __noinline__ void widen_keys_edge(const uint8_t* src, uint32_t scales, uint8_t* dst, int r, int ref, bool dead,
+                                             uint8_t* power) {
+  if (power != nullptr) {
+    const int top = exponent_range<D / kE2m1Group>(scales).x;
+    *power = static_cast<uint8_t>(top);
+    ref = top - 127;
+  }
+  widen_codes_edge<D>(src, scales, dst, r, ref, false, dead, false);
+}
+
 // E2M1: four warps widen the keys' codes and four the values', a row per thread.  The keys' reference goes with their
-// tile; the values' is a running one, as with E4M3.  Rows past the end become zeros.
+// tile; the values' is a running one, as with E4M3.  Keys that lie too far apart for fp16 are each taken relative to
+// their own largest group, and the softmax multiplies their scores: a key may be seen by some rows only, and to the others
+// it must not matter how large it is.  Rows past the end become zeros.
 template <int D, int TILES, bool VALUES>
 __device__ __forceinline__ void convert_halves(const TreeParams& p, const TreePart& my, uint8_t* smem, Bars* ms, Refs* sc,
                                               int r) {
@@ -299,6 +334,7 @@ __device__ __forceinline__ void convert_halves(const TreeParams& p, const TreePa
           far = range.y - 127 < ref - kFourFar;
         } else if (range.x > 0) {
           ref = range.x - 127;
+          far = range.y - 127 < ref - kFourFar;
         }
       }
       if (VALUES) {
@@ -308,14 +344,16 @@ __device__ __forceinline__ void convert_halves(const TreeParams& p, const TreePa
         }
         mbar_wait_inl(&ms->v16_empty[used & 1], ((used >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x33));
       } else {
-        if (r == 0) sc->kref[used % kTileRing] = ref;  // (the scores say that it is there)
+        if (r == 0) sc->kref[used % kTileRing] = far ? 1 : ref * 2;  // (the scores say that it is there)
         mbar_wait_inl(&ms->k_empty[used & 1], ((used >> 1) & 1) ^ 1, abort_flag, p.err, tree_site(0x31));
       }
       __syncwarp();
       uint8_t* dst = smem + (VALUES ? C::kOffV16 : C::kOffK) + (used & 1) * C::kSlot + r * 128;
       if (!far && key - r + kBN <= (VALUES ? context : w.len)) {
         widen_codes<D, 2>(src + r * (D / 2), bytes, dst, r, ref);
-      } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, dst, r, ref, VALUES && key >= context, !counts, far)) {
+      } else if (!VALUES) {
+        widen_keys_edge<D>(src + r * (D / 2), bytes, dst, r, ref, !counts, far ? &sc->power[used % kTileRing][r] : nullptr);
+      } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, dst, r, ref, key >= context, !counts, far)) {
         atomicOr(&ms->bad[w.index & 7][(key - context) >> 5], 1u << ((key - context) & 31));
       }
       fence_proxy_async_smem();
@@ -597,6 +635,8 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
                 see = make_uint4(see.y, see.z, see.w, see.x);
               }
             };
+            const int kcode = sc->kref[tile % kTileRing];
+            if (kcode & 1) scale_scores(s_addr, sc->power[tile % kTileRing]);
             float top = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < kBN; c += 32) {
@@ -612,7 +652,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
             }
             // (Not 0, as with E4M3.)
             const float factor =
-                fmaxf(sc->f[(TILES == 1 ? 0 : g * kRowTile) + kt] * power_f32(sc->kref[tile % kTileRing]), 1e-45f);
+                fmaxf(sc->f[(TILES == 1 ? 0 : g * kRowTile) + kt] * power_f32(kcode >> 1), 1e-45f);
             const float m_cand = top * factor;
             const bool need = m_cand > m_run + kLazy;
             const float m_new = need ? m_cand - kBase : m_run;

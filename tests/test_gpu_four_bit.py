@@ -227,6 +227,52 @@ def test_what_unseen_drafted_keys_hold_does_not_matter(Hq):
         assert np.array_equal(o[:, :, rows], ro[:, :, rows]) and np.array_equal(lse[:, :, rows], rl[:, :, rows])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [2, 24, 60, 128])
+def test_huge_drafted_keys_reach_those_who_see_them_alone(Hq, d):
+    """Drafted token 2's key is 2^50 to 2^100 times the others'.  (Those are multiplied by whole powers of two less, which is
+    exact: rows that do not see it have the bits that they have without it.)"""
+    T = 6
+    mask = np.tril(np.ones((1, T, T), dtype=bool))
+    mask[:, :, 2] = False
+    for n in (T, 131, 128 + T):
+        for power in (50, 100):
+            def grow(name, b, x):
+                if name == "k":
+                    x[:, x.shape[1] - T + 2] = 2.0 ** power * np.where(np.arange(d) // 32 == 1, 2.0 ** -30, 1.0)
+            p = Paged4(np.random.default_rng(11), [n], 1, d, 16, edit=grow)
+            q = bf16(np.abs(np.random.default_rng(3).standard_normal((1, Hq, T, d)))).cuda()
+            clean = Paged4(np.random.default_rng(11), [n], 1, d, 16,
+                           edit=lambda name, b, x: x.__setitem__((slice(None), x.shape[1] - T + 2), 0.0) if name == "k" else None)
+            seen = mask.copy()
+            seen[0, 4, 2] = True
+            o, lse = (np64(x) for x in fa.decode_tree(q, *p.args(), tree_mask=_mask(seen), max_parts=2, **p.kw()))
+            ro, rl = (np64(x) for x in fa.decode_tree(q, *clean.args(), tree_mask=_mask(mask), max_parts=2, **clean.kw()))
+            rows = [0, 1, 2, 3, 5]
+            assert np.array_equal(o[:, :, rows], ro[:, :, rows]) and np.array_equal(lse[:, :, rows], rl[:, :, rows])
+            fa.device_status()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [3, 30, 90, 128])
+def test_a_huge_key_of_the_context_leaves_the_others_alone(Hq, d):
+    """Far below the others' scores it has no weight, however large it is: the same bits."""
+    def run(size):
+        def grow(name, b, x):
+            if name == "k":
+                x[:, 70] = size
+                x[:, 200, 32:] *= 2.0 ** -28
+        p = Paged4(np.random.default_rng(21), [400, 300], 1, d, 16, edit=grow)
+        q = bf16(np.abs(np.random.default_rng(4).standard_normal((2, Hq, 2, d)))).cuda()
+        o, lse = (np64(x) for x in fa.decode_tree(q, *p.args(), max_parts=3, **p.kw()))
+        fa.device_status()
+        return o, lse
+    o, lse = run(-2.0 ** 12)
+    for power in (40, 80, 110):
+        far, far_lse = run(-2.0 ** power)
+        assert np.array_equal(o, far) and np.array_equal(lse, far_lse)
+
+
 @pytest.mark.parametrize("Hq", [1, 20, 70])
 def test_a_nan_value_of_the_context_reaches_its_group_alone(Hq):
     def poison(name, b, x):
