@@ -382,8 +382,9 @@ FA_API fa_status fa_cache_append(const void* k, const void* v, void* k_cache, vo
  *   as bf16 rows, e.g. for fa_forward over a cached prefix.
  *   Arguments as for fa_cache_append, k and v [B,H_kv,N,d] being written; rows
  *   n >= seq_lens[b] are set to zero.  E4M3 codes are multiplied by their row's
- *   power of two and E2M1 codes by their group's, which is exact.  seq_lens outside [0, max_blocks·block_size]
- *   and bad page ids give zero rows and FA_ERR_INVALID_ARG from fa_device_status.
+ *   power of two and E2M1 codes by their group's, which is exact.  seq_lens outside
+ *   [0, max_blocks·block_size] and bad page ids give zero rows and
+ *   FA_ERR_INVALID_ARG from fa_device_status.
  *   k and v must not overlap themselves or each other.
  */
 FA_API fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
@@ -403,6 +404,7 @@ FA_API fa_status fa_cache_gather(const void* k_cache, const void* v_cache, const
  *   Positions that break the rule or lie outside the table, and bad page ids, are
  *   caught on the device: those rows are not moved; with first, keep_lens out of
  *   range none of the sequence's is.  fa_device_status then reports FA_ERR_INVALID_ARG.
+ *   Supported: B·H_kv <= 2^27, num_blocks·block_size < 2^32.
  */
 FA_API fa_status fa_cache_compact(void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
                                   const int32_t* block_table, const int32_t* first, const int32_t* keep,
@@ -503,8 +505,12 @@ FA_API size_t fa_decode_tree_workspace_size(int B, int H_q, int H_kv, int T, int
  *   2^-28 of that).  Exponentials are fp32: weights below 2^-126 of the row's
  *   largest are zero.  E4M3 cache: value rows of at most 448·2^-126 may count as
  *   zero beside larger ones, and with more than 32 rows T·H_q/H_kv the scores of
- *   keys above 2^110 may overflow.  E2M1 cache: codes times their power of two are exact in
- *   bf16, and everything is as for a bf16 cache; a NaN group is NaN for the rows that see it.
+ *   keys above 2^110 may overflow.  E2M1 cache: weights enter as with an E4M3 one,
+ *   value groups of at most 6·2^-126 may count as zero beside larger ones, the
+ *   scores of keys above 2^110 may overflow, and a group of NaN is NaN for the
+ *   rows that see it.  Elements of q that are small beside their row's largest are
+ *   exact down to 2^-14 of it with up to 32 rows (below that off by 2^-22 of it),
+ *   and to 2^-31 beyond.
  *   One token over a bf16 cache is fa_decode_paged's case too.  Measured on GB300,
  *   d = 64 and 128, batches of 1 to 64: where query heads share keys, that call takes
  *   0.65 to 1.0 of this one's time up to 100 MB of keys and values, and 0.9 to 1.8

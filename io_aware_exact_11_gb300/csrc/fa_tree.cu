@@ -1,6 +1,6 @@
 // fa_tree.cu — attention of T drafted tokens per sequence over a paged cache
-// (T = 1: plain decode), bf16 or E4M3, on tcgen05 tensor cores: the kernel for up
-// to 32 query rows (T·G, G query heads per key/value head) and the joining kernel.
+// (T = 1: plain decode), bf16, E4M3 or E2M1, on tcgen05 tensor cores: the kernel for
+// up to 32 query rows (T·G, G query heads per key/value head) and the joining kernel.
 //
 // Sequence b holds len keys, the last m of them those of its m ≤ T drafted
 // tokens.  Token t sees every key of the context [0, len − m) and drafted key u
@@ -50,6 +50,13 @@
 // many bits: rows made of such weights came out wrong by several times that.)
 // A tile with value rows further below the reference than 2^15 is widened to bf16 with its
 // powers of two, P̃ goes as two bf16 terms, and the product runs as bf16.
+// E2M1 cache: a key's groups have a power of two each, which kind::mxf8f6f4 products apply
+// to 32 elements at a time: K's codes stay E2M1 (spread to 16 bytes for sixteen, which is how
+// the products read them), their scales go to tensor memory, and q enters as E4M3's two terms
+// with scales of one.  V, whose groups lie across the second product's sum, is widened to fp16
+// and P̃ is fp16, as with E4M3; from 2⁻²³ to 2^13 of the reference that is exact.  Both take
+// warps of their own, as the codes need work before every product: one warpgroup for the keys
+// of both streams and one for each stream's values.
 //
 // Values in masked places.  Cache slots past the sequence end are zeroed in
 // shared memory before V is used.  A drafted key's value row is seen by some
@@ -62,6 +69,14 @@
 //   4 / 16 / 32 rows, E4M3   55 / 56 / 66 us   4.9 / 4.8 / 4.1 TB/s: inside a piece 4 and 16 rows run at the memory's
 //                            rate; start, piece ends and the joining kernel take 15 us, and with 32 rows the softmax
 //                            warps, which also widen V, are the bound
+//   4 / 16 / 32 rows, E2M1   58 / 62 / 88 us   2.5 / 2.3 / 1.6 TB/s: a stream's tile is a chain of waits of 3400 cycles (its
+//                            values' references 600, the place of the widened tile 500, widening 1850), shared memory
+//                            is busy for two thirds of it, and with 32 rows the softmax is the bound
+// E2M1, not kept: both halves written out as bf16 tiles by four warps, 195 us at 16 rows; codes of both halves fetched by one
+// warp, 72 at 4 rows; and with 16 rows worked on where there are 4 (60 us): both value warpgroups on one tile after the other
+// and its reference found by the keys' warpgroup, 80; a ring of three widened tiles for both streams, 61, and with the
+// references found by the fetching warp, 90.  Every role's instructions are fetched anew each tile, so that more of them
+// on a chain cost more than the waits they save.
 // E4M3, not kept: four or eight converter warps beside the softmax warps (7 and 12 % more at 4 rows, 15 % at 32);
 // V widened by integer operations instead of the conversion instruction (slower, and it loses NaN); P̃ as two E4M3
 // terms over V as it is (the terms span too few binades).
@@ -501,7 +516,8 @@ __device__ __forceinline__ void issue_products(const TreeParams& p, const TreePa
   }
 }
 
-template <int D, int F, int NR>
+// R: rows that the softmax works on, of the NR columns of the products.
+template <int D, int F, int NR, int R>
 __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, F, NR>;
   constexpr bool FP8 = C::FP8, FP4 = C::FP4, kWiden = C::kWiden;
@@ -695,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
     }
   } else if (warp < 8) {
     reg_alloc<C::kRegsSoftmax>();
-    // ----------------------------- softmax: one key per thread, the stream's NR rows
+    // ----------------------------- softmax: one key per thread, the stream's R rows
     const int g = warp >> 2;
     const int bar = 1 + g;                 // the stream's barrier
     const int kt = tid & 127;              // key in the tile, TMEM lane, head dim of O
@@ -704,7 +720,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
     const uint32_t o_addr = tmem + lane_base + C::kColO + g * C::kPCols;
     float* nm = ms->nm[g];
     float* corr = ms->corr[g];
-    float* red = ms->red[g][0];            // + warp·NR
+    float* red = ms->red[g][0];            // + warp·R
     int64_t* row = ms->row[g];
     int64_t* o_off = ms->o_off[g];
     int* fresh = ms->fresh[g];
@@ -716,6 +732,13 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
     load_q<D, F, NR, 256, 4>(p, w, smem + C::kOffQ, ms->f[0], tid);
     named_sync(3, 256);
     if (warp == 0) mbar_arrive(&ms->q_full);
+    if constexpr (R < NR) {  // P̃'s columns that no row is worked on for stay zeros
+#pragma unroll
+      for (int ch = 0; ch < 2 * NR / 8; ++ch)
+        if (ch % (NR / 8) >= R / 8)
+          *reinterpret_cast<uint4*>(smem + C::kOffP + kt * 128 + (((g * (C::kPNext / 16) + ch) ^ (kt & 7)) << 4)) =
+              make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll 1
     do {
       const int n_tiles = w.t1 - w.t0;
@@ -731,9 +754,9 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
       }
       named_sync(bar, 128);
       bool unseen = true;  // some row may have seen nothing yet
-      float l[NR];
+      float l[R];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) l[n] = 0.f;
+      for (int n = 0; n < R; ++n) l[n] = 0.f;
       int kv_ref = -1024;
       int done = 0;  // tiles of this piece that this stream has worked on
       const float* f_row = ms->f[w.index % kFRing];
@@ -777,14 +800,14 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
         tc_fence_after();
         // x = score − reference, masked to −∞ where the row does not see the key.  A second time where a reference
         // has moved.
-        float x[NR];
+        float x[R];
         bool far = FP4 && (code & 1);  // value rows too far apart for fp16
         bool dead = false;  // a wait of some thread of the stream has failed
 #pragma unroll 1
         for (bool again = false;; again = true) {
           // 16 rows at a time; with registers to spare the next ones are on their way from TMEM meanwhile.
-          constexpr int kC = 16;
-          constexpr int kBuf = NR > kC && !FP4 ? 2 : 1;
+          constexpr int kC = R < 16 ? R : 16;
+          constexpr int kBuf = R > kC && !FP4 ? 2 : 1;
           uint32_t hi[kBuf][kC], lo[kBuf][kC];
           auto fetch = [&](int c, int to) {
             tmem_ld(s_addr + c, hi[to]);
@@ -792,12 +815,12 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
           };
           fetch(0, 0);
 #pragma unroll
-          for (int c = 0; c < NR; c += kC) {
+          for (int c = 0; c < R; c += kC) {
             const int now = (c / kC) % kBuf;
             tmem_wait_ld();
             reg_fence(hi[now]);
             if constexpr (kWiden) reg_fence(lo[now]);
-            if (kBuf == 2 && c + kC < NR) fetch(c + kC, now ^ 1);
+            if (kBuf == 2 && c + kC < R) fetch(c + kC, now ^ 1);
 #pragma unroll
             for (int e = 0; e < kC; e += 4) {
               const int n = c + e;
@@ -819,20 +842,20 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
               ffma2(x[n], x[n + 1], r4.x, r4.y, f4.x, f4.y, m4.x, m4.y);
               ffma2(x[n + 2], x[n + 3], r4.z, r4.w, f4.z, f4.w, m4.z, m4.w);
             }
-            if (kBuf == 1 && c + kC < NR) fetch(c + kC, 0);
+            if (kBuf == 1 && c + kC < R) fetch(c + kC, 0);
           }
           if (tail) {
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+            for (int n = 0; n < R; ++n)
               if (!((seen >> n) & 1)) x[n] = -INFINITY;
           }
           if (again) break;
           float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int n = 4; n < NR; n += 8)
+          for (int n = 4; n < R; n += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              mx[e] = n + 4 + e < NR ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % NR]) : fmaxf(mx[e], x[n + e]);
+              mx[e] = n + 4 + e < R ? fmax3(mx[e], x[n + e], x[(n + 4 + e) % R]) : fmaxf(mx[e], x[n + e]);
           const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
           const bool over = unseen || top > kLazy || (FP8 && (kv > kv_ref + kKvLazy || (kv > -126 && kv < kv_ref - kKvFar))) || (FP4 && code >> 1 != kv_ref);
           if (!named_any(bar, 128, over || !ok)) break;
@@ -842,7 +865,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             dead = true;
             break;
           }
-          reduce_cols<NR>(x, lane, OpMax(), red + (warp & 3) * NR);
+          reduce_cols<R>(x, lane, OpMax(), red + (warp & 3) * R);
           if constexpr (FP8) {
             const int top_kv = __reduce_max_sync(0xffffffffu, kv);
             if (lane == 0) ms->kv_red[g][warp & 3] = top_kv;
@@ -855,9 +878,9 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
             far = named_any(bar, 128, kv > -126 && kv < kv_new - kKvFar);  // (−126: next to nothing, or zeros)
           }
           bool still = false;
-          if (kt < NR) {
+          if (kt < R) {
             // Maxima relative to the old reference (0 for a row that has seen nothing).
-            const float now = fmaxf(fmaxf(red[kt], red[NR + kt]), fmaxf(red[2 * NR + kt], red[3 * NR + kt]));
+            const float now = fmaxf(fmaxf(red[kt], red[R + kt]), fmaxf(red[2 * R + kt], red[3 * R + kt]));
             const bool first = fresh[kt] != 0;
             const bool up = now > -INFINITY && (first || now > kBase);
             corr[kt] = !up ? 1.f : first ? 0.f : exp2f(kBase - now);
@@ -869,13 +892,13 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
           }
           unseen = named_any(bar, 128, still);
 #pragma unroll
-          for (int n = 0; n < NR; ++n) l[n] *= corr[n];
+          for (int n = 0; n < R; ++n) l[n] *= corr[n];
           if (done > 0) {
             ok = mbar_wait_inl(&ms->p_free[g], (u - 1) & 1, abort_flag, p.err, tree_site(8)) && ok;
             tc_fence_after();
             const float kf = kWiden ? exp2f(static_cast<float>(max(kv_ref - kv_new, -200))) : 1.f;
 #pragma unroll 1
-            for (int term = 0; term < C::kTerms; ++term) rescale_cols<NR>(o_addr + term * NR, corr, kf);
+            for (int term = 0; term < C::kTerms; ++term) rescale_cols<R>(o_addr + term * NR, corr, kf);
           }
           kv_ref = kv_new;
         }
@@ -889,7 +912,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
         uint8_t* prow = smem + C::kOffP + (C::kPNext == kPBlock ? g * kPBlock : 0) + kt * 128;
         const int first = C::kPNext == kPBlock ? 0 : g * (C::kPNext / 16);
 #pragma unroll
-        for (int ch = 0; ch < NR / 8; ++ch) {  // 8 rows per 16-byte chunk
+        for (int ch = 0; ch < R / 8; ++ch) {  // 8 rows per 16-byte chunk
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -912,7 +935,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
         }
         if (kWiden && far) {  // the weights as two bf16 terms, from what this thread has just stored
 #pragma unroll 1
-          for (int ch = 0; ch < NR / 8; ++ch) {
+          for (int ch = 0; ch < R / 8; ++ch) {
             uint4* at = reinterpret_cast<uint4*>(prow + (((first + ch) ^ (kt & 7)) << 4));
             uint4 a = *at, d;
             split_f16x2(a.x, a.x, d.x);
@@ -959,19 +982,20 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
       // ------------------------------------------------------------ end of the piece
       // (Its barriers are joined by all threads whatever the waits said.)
       if (done > 0) ok = ok && mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, tree_site(10));
-      reduce_cols<NR>(l, lane, OpAdd(), red + (warp & 3) * NR);
+      reduce_cols<R>(l, lane, OpAdd(), red + (warp & 3) * R);
       tc_fence_before();
       named_sync(3, 256);
       tc_fence_after();
       const bool whole = w.whole();
       const int64_t slot_row = w.slot(p, part) * p.T * p.G;  // first row of the piece's slot
-      if (kt < NR) {
+      if (R < NR && kt >= R && kt < NR) ms->scale[g][kt] = 0.f;
+      if (kt < R) {
         // Both streams' sums in a fixed order: the same result every time.
         float sums[2], m = -INFINITY, sum = 0.f, mine = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float* r4 = ms->red[e][0] + kt;
-          sums[e] = (r4[0] + r4[NR]) + (r4[2 * NR] + r4[3 * NR]);
+          sums[e] = (r4[0] + r4[R]) + (r4[2 * R] + r4[3 * R]);
           if (sums[e] != 0.f) m = fmaxf(m, -ms->nm[e][kt]);
         }
 #pragma unroll
@@ -1193,7 +1217,7 @@ cudaError_t launch_merge(const TreeParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, WIDE>, p);
 }
 
-template <int D, int F, int NR>
+template <int D, int F, int NR, int R = NR>
 cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
   constexpr int kSmem = Cfg<D, F, NR>::kOffMisc + static_cast<int>(sizeof(Misc<NR, F>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -1206,14 +1230,14 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
   cudaError_t e;
   if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, tree_kernel<D, F, NR>);
+    e = cudaFuncGetAttributes(&a, tree_kernel<D, F, NR, R>);
     if (e != cudaSuccess) return e;
     if (a.numRegs < Cfg<D, F, NR>::kRegsLaunch) return cudaErrorInvalidConfiguration;
     checked.store(true, std::memory_order_relaxed);
   }
-  e = cudaFuncSetAttribute(tree_kernel<D, F, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  e = cudaFuncSetAttribute(tree_kernel<D, F, NR, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, F, NR><<<static_cast<unsigned>(p.parts), Cfg<D, F, NR>::kThreads, kSmem, s>>>(p);
+  tree_kernel<D, F, NR, R><<<static_cast<unsigned>(p.parts), Cfg<D, F, NR>::kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -1222,13 +1246,19 @@ cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
   // By the rows of a pair; 8 sequences of 16384 keys, 8 key/value heads, us with the one and the other:
   //   4 and 16 rows as 16 columns or 32    E4M3 55, 56 | 60, 62    bf16 89, 90 | 88, 90 (head dim 64 51, 52 | 54, 55)
+  //                                        E2M1 60, 62 | 80, 83 (head dim 64 52, 53 | 60, 64)
   //   16 and 32 rows here or in the kernel for many rows    E4M3 56, 66 | 72, 74    bf16 90, 92 | 93, 95
+  //                                                         E2M1 62, 88 | 88, 91 (head dim 64 53, 66 | 70, 72)
+  //   4 rows of which the softmax works on 8 or 16    E2M1 58 | 60 (head dim 64 49 | 52; 64 ragged sequences of up to 8192
+  //   keys, 7 rows 95 | 99); the others' softmax is no bound at so few
   // (32 rows are the most that fit here without tiles of rows; 64 columns spilled registers and took 81 us where the
   // other kernel took 69: 8 tokens of 7 heads a group, 16 ragged sequences of up to 8192 bf16 keys.)
   const bool wide = rows > kTreeNarrowRows;
-  cudaError_t e = wide         ? launch_tree_wide(p, D, F, s)
-                  : rows <= 16 ? launch_rows<D, F, 16>(p, s)
-                               : launch_rows<D, F, 32>(p, s);
+  constexpr int kFew = F == kCacheE2m1 ? 8 : 16;
+  cudaError_t e = wide           ? launch_tree_wide(p, D, F, s)
+                  : rows <= kFew ? launch_rows<D, F, 16, kFew>(p, s)
+                  : rows <= 16   ? launch_rows<D, F, 16>(p, s)
+                                 : launch_rows<D, F, 32>(p, s);
   if (e != cudaSuccess) return e;
   return wide ? launch_merge<D, true>(p, s) : launch_merge<D, false>(p, s);
 }

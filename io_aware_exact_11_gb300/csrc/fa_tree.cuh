@@ -1,5 +1,5 @@
 // fa_tree.cuh — what the kernels of drafted-token attention share: the walk over
-// a CTA's part of the key tiles, the slots of cut pairs, and widening E4M3 rows.
+// a CTA's part of the key tiles, the slots of cut pairs, and fetching and widening rows of codes.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -358,7 +358,9 @@ __device__ __forceinline__ void load_pages(const TreeParams& p, const TreePart& 
 // A page of one head is contiguous: its codes and its scale bytes come by plain bulk copies into a ring of half tiles (the
 // keys or the values of 128 rows; in one ring K₀, K₁, V₀, K₂, V₁ … of each piece, the order in which they are used), and
 // other warps widen them to fp16, each group times its power of two relative to a reference: from 2⁻²³ to 2^13 of it that
-// is exact.
+// is exact (the smallest code but zero, 0.5, becomes fp16's smallest step, 2⁻²⁴, and the largest, 6, stays below 65504).
+// (Copies of pages without a tensor map: a page of 16 keys is 1 KB of codes and 64 bytes of scales, and the products need
+// the codes rearranged anyway.)
 constexpr int kFourLazy = 13, kFourFar = 23;
 
 // Whether a row's groups have exponents that a reference does not fit: usually none has, and then it stays.  (NaN, byte 255,

@@ -25,16 +25,26 @@
 // times its power of two relative to a reference that P̃ and O share, and lay out
 // the keys' powers of two as floats.  P̃ is fp16, its reference 2^3 below the maximum.
 // A tile with value rows further below the reference than 2^15 goes through bf16 (fa_tree.cu).
+// E2M1 cache: eight converter warps widen K and V to fp16, each group times its power of two
+// relative to a reference: the keys' is their tile's largest group, which multiplies the scores
+// in fp32, the values' a running one.  From 2⁻²³ to 2^13 of it that is exact; keys further apart
+// are taken each to its own largest group, values go through bf16.  q is fp16, its largest
+// element between 2^14 and 2^15: exact down to 2⁻³¹ of that.  P̃ is fp16 as with E4M3.  (Products
+// over the codes themselves, as in the kernel for few rows, would take q in two E4M3 terms, twice
+// the tensor work at full width.)
 //
 // The rest (parts, pieces, masks, values in masked places) is as in fa_tree.cu.
 //
 // Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements (replaying a graph over two caches):
 //   64 / 128 / 256 rows, bf16    98 / 104 / 125 us   0.82 / 0.77 of a device copy, 1100 TFLOP/s
 //   64 / 128 / 256 rows, E4M3    76 /  84 / 140 us   452 / 818 / 982 TFLOP/s
+//   64 / 128 / 256 rows, E2M1    91 /  94 / 145 us   378 / 732 / 947 TFLOP/s (32768 keys, 256 rows: 258 us, 1063)
 // With two row tiles a step (one tile's P̃V and S, 1024 tensor cycles) takes about 1750 cycles: the issuing
 // warp's own instructions, of which it gets one through every dozen cycles beside the softmax warps, and the wait
 // for P̃ (S to P̃ is a chain of about 1400 cycles).  E4M3 with shared rows waits for the converters (2400 cycles a
-// tile).  A pair boundary costs a CTA 10000 to 15000 cycles (O out, Q in, the first scores).
+// tile).  E2M1 waits for the converters with shared rows and for the softmax, whose scores are read twice, with two row
+// tiles; with four converter warps for both halves and the scores held in registers the three took 131, 135 and 157 us.
+// A pair boundary costs a CTA 10000 to 15000 cycles (O out, Q in, the first scores).
 #include <stddef.h>
 
 #include <atomic>
@@ -50,7 +60,7 @@ constexpr int kRowTile = 128;
 constexpr int kMaxRing = 8;
 constexpr int kMaxCodeRing = 8;
 constexpr int kScaleRing = 16;
-constexpr int kTileRing = 8;   // E4M3: tiles whose converted scales are kept
+constexpr int kTileRing = 8;   // E4M3, E2M1: tiles whose converted scales and references are kept
 
 template <int D, int F, int TILES>
 struct Cfg {

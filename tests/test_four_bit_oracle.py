@@ -106,7 +106,7 @@ def test_four_bit_caches_are_checked(L, kw, status):
 @pytest.mark.parametrize("kw,status", FOUR_BAD + [
     (dict(first=None), INV), (dict(keep=None), INV), (dict(first=FAKE + 1), INV), (dict(keep=FAKE + 2), INV),
     (dict(lens=FAKE + 2), INV), (dict(N=0), INV), (dict(sb=-1), INV), (dict(table=None), INV), (dict(B=0), INV),
-    (dict(B=60000, Hkv=60000, nb=1), UNS)])
+    (dict(B=60000, Hkv=60000, nb=1), UNS), (dict(nb=1 << 25, bs=128, Hkv=1, mb=1), UNS)])
 def test_cache_compact_refuses(L, kw, status):
     a = dict(BASE, first=FAKE, keep=FAKE, sb=8, lens=None, N=8)
     a.update(kw)
