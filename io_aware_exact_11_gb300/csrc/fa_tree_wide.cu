@@ -42,8 +42,10 @@
 // With two row tiles a step (one tile's P̃V and S, 1024 tensor cycles) takes about 1750 cycles: the issuing
 // warp's own instructions, of which it gets one through every dozen cycles beside the softmax warps, and the wait
 // for P̃ (S to P̃ is a chain of about 1400 cycles).  E4M3 with shared rows waits for the converters (2400 cycles a
-// tile).  E2M1 waits for the converters with shared rows and for the softmax, whose scores are read twice, with two row
-// tiles; with four converter warps for both halves and the scores held in registers the three took 131, 135 and 157 us.
+// tile).  With E2M1 the softmax reads
+// its scores twice, in rolled loops; with four converter warps for both halves and the scores held in registers the three took
+// 131, 135 and 157 us.  Not kept: a second set of eight converter warps for every other tile, which takes registers from the
+// softmax (97 us at 64 rows), and rings and loading warps of their own for the keys' and the values' codes (98).
 // A pair boundary costs a CTA 10000 to 15000 cycles (O out, Q in, the first scores).
 #include <stddef.h>
 

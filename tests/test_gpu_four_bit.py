@@ -329,3 +329,40 @@ def test_keys_beyond_32_bit_offsets():
         o, lse = fa.decode_tree(q, kc, vc, table, _i32([300, 300]), **sc)
         check_tree4(o, lse, q, p, [4, 4], None, 1 / math.sqrt(d), [0, hkv * G - 1])
     fa.device_status()
+
+
+@pytest.mark.parametrize("T", [1, 4, 8, 20, 64])
+def test_calls_behind_an_unread_timeout_end(T):
+    """As with the other caches: their waits give up early, they end, and calls after the report are right.  (4 query heads a
+    key/value head: 4, 16, 32, 80 and 256 rows.)"""
+    import torch
+    p = Paged4(np.random.default_rng(T), [3000, 500, T], 2, 128, 16)
+    q = bf16(np.random.default_rng(1).standard_normal((3, 8, T, 128))).cuda()
+    want, lse = fa.decode_tree(q, *p.args(), **p.kw())
+    fa.device_status()
+    fa.watchdog_selftest()
+    for parts in (0, 1, 7):
+        fa.decode_tree(q, *p.args(), max_parts=parts, **p.kw())
+    with pytest.raises(fa.FAError) as ei:
+        fa.device_status()
+    assert ei.value.status == fa.FA_ERR_DEVICE_TIMEOUT
+    got, lse2 = fa.decode_tree(q, *p.args(), **p.kw())
+    assert torch.equal(got, want) and torch.equal(lse, lse2)
+    fa.device_status()
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its workspace: both have the bits that they have alone."""
+    import torch
+    calls = []
+    for T, seed in ((2, 1), (16, 2)):
+        p = Paged4(np.random.default_rng(seed), [2000, 900, 130], 2, 64, 32)
+        q = bf16(np.random.default_rng(seed).standard_normal((3, 8, T, 64))).cuda()
+        calls.append((p, q, fa.decode_tree(q, *p.args(), max_parts=8, **p.kw()), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [[fa.decode_tree(q, *p.args(), max_parts=8, stream=s, **p.kw()) for _ in range(4)] for p, q, _, s in calls]
+        torch.cuda.synchronize()
+        for (_, _, want, _), outs in zip(calls, got):
+            assert all(torch.equal(a, b) for out in outs for a, b in zip(out, want))
+    fa.device_status()
