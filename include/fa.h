@@ -445,6 +445,8 @@ FA_API fa_status fa_pages_fork(int32_t* block_table, int32_t* seq_lens, int32_t*
  * fa_pages_free — sequences seqs[i] (i < n) give up their pages, reserved ones
  *   included, behind the first keep_lens[i] tokens (keep_lens NULL: all).  Entries
  *   become −1, lengths min(seq_lens, keep_lens); pages without holders are free.
+ *   keep_lens may be seq_lens itself where seqs[i] = i (pages reserved in vain are
+ *   given back), and must not overlap it otherwise.
  *   Not a row of the table, a sequence named before and a negative keep_lens[i] are
  *   caught on the device (left out), and so is a page that nobody was said to hold.
  */

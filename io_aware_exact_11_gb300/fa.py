@@ -633,7 +633,7 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
         raise ValueError("inv_freq must be one row of rot_dim/2 values")
     pos_ptr, pos_sb = None, 0
     if axes is not None:
-        if positions.dtype != torch.int32:
+        if positions is None or positions.dtype != torch.int32:
             raise TypeError("positions must be int32")
         shape, step = positions.shape, positions.stride()
         if len(shape) not in (2, 3) or shape[1:] != (B, N)[3 - len(shape):] or (N > 1 and step[-1] != 1):
@@ -642,7 +642,11 @@ def _rope(q, k, inv_freq, positions, position0, magnitude, interleaved, out_q, o
             a = axes.contiguous()
             a_ptr = a.data_ptr()
         else:
-            a = np.ascontiguousarray(axes, dtype=np.int32)
+            a = np.asarray(axes)
+            if a.dtype != np.int32:
+                if a.dtype.kind not in "iu" or a.size and not 0 <= a.min() <= a.max() < 1 << 31:
+                    raise ValueError("axes must be whole numbers, one for each of inv_freq's pairs")
+                a = a.astype(np.int32)
             a_ptr = a.tobytes()
         if a.shape != w.shape:
             raise ValueError("axes must name one axis for each of inv_freq's pairs")
@@ -920,7 +924,7 @@ def pages_free(block_table, seq_lens, holders, seqs, block_size: int, keep_lens=
     """Sequences seqs[i] (int32 [n]) give up their pages, all but those of the first keep_lens[i] tokens (int32 [n]).
 
     In place: their entries become −1, their lengths at most keep_lens[i] (0 without), and pages that nobody holds any
-    more are free.
+    more are free.  ``keep_lens`` may be ``seq_lens`` itself where seqs[i] = i: pages reserved in vain are given back.
     """
     dev = _device_of(block_table, seq_lens, holders, seqs, keep_lens)
     there = _elsewhere(dev, stream)

@@ -162,8 +162,9 @@ def test_pages_reserve_refuses(L, kw, status):
 
 def test_pages_reserve_workspace(L):
     size = L.fa_pages_reserve_workspace_size
-    assert size(4, 100) == 256 and size(100, 4096) == -(-(1 + 300 + 1) * 4 // 256) * 256
-    assert size(100, 4097) == -(-(2 + 300 + 1) * 4 // 256) * 256
+    # a word for every 1024 pages, three for every sequence, one more
+    assert size(4, 100) == 256 and size(20, 3 * 1024) == 256 and size(20, 3 * 1024 + 1) == 512
+    assert size(4096, (1 << 31) - 1) == -(-((1 << 21) + 3 * 4096 + 1) * 4 // 256) * 256
     assert size(0, 5) == 0 and size(5, 0) == 0
 
 

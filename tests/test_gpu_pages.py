@@ -241,6 +241,25 @@ def test_many_sequences_write_into_shared_pages():
     fa.device_status()
 
 
+def test_reserved_pages_are_given_back_up_to_the_lengths_themselves():
+    import torch
+    B, bs, nb, per = 300, 16, 4000, 12
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 5 * bs, B)
+    table, held = np.full((B, per), -1), np.zeros(nb, dtype=int)
+    order = iter(rng.permutation(nb))
+    for b in range(B):
+        for j in range(-(-lens[b] // bs)):
+            table[b, j] = next(order)
+            held[table[b, j]] = 1
+    t, n, h = _i32(table), _i32(lens), _i32(held)
+    granted, _, _ = fa.pages_reserve(t, n, h, _i32(rng.integers(1, 6 * bs, B)), bs)
+    assert granted.all() and int(h.sum()) > held.sum()
+    fa.pages_free(t, n, h, _i32(np.arange(B)), bs, keep_lens=n)
+    fa.device_status()
+    assert torch.equal(t, _i32(table)) and torch.equal(n, _i32(lens)) and torch.equal(h, _i32(held))
+
+
 def test_bad_sequences_lengths_and_pages_are_left_out_and_reported():
     start = ([[0, 1, -1], [2, -1, -1], [-1] * 3, [-1] * 3], [20, 7, 0, 0], [1, 1, 1, 0, 0, 0, 0])
 

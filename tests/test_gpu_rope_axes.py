@@ -101,6 +101,15 @@ def test_strides_in_place_and_refusals():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     fa.rope_axes(q, k, w, axes, pos, out_q=q, out_k=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    q2, k2 = (x.clone() for x in want)
+    for same in (axes.tolist(), axes.long().numpy(), axes.numpy().astype(np.uint8)):
+        again = fa.rope_axes(q2, k2, w, same, pos)
+        assert all(torch.equal(a, b) for a, b in zip(again, fa.rope_axes(q2, k2, w, axes, pos)))
+    for bad in ([0.5] * 32, axes.double().numpy(), [1 << 32] * 32, np.full(32, 1 << 32), [-1] * 32):
+        with pytest.raises(ValueError):
+            fa.rope_axes(q, k, w, bad, pos)
+    with pytest.raises(TypeError):
+        fa.rope_axes(q, k, w, axes, None)
     with pytest.raises(TypeError):
         fa.rope_axes(q, k, w, axes, pos.long())
     with pytest.raises(ValueError):
