@@ -36,7 +36,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr unsigned int kNowhere = 0xffffffffu;  // of a row that stays
-constexpr int kPasses = 2;                      // of a block over the rows of a chunk
 
 __device__ __forceinline__ void report(unsigned int* err, unsigned int what) {
   atomicCAS(err + 1, 0u, (kKernPages << 8) | what);
@@ -73,14 +72,14 @@ __device__ __forceinline__ void cp_async_wait() {
 // Moves LANES 16-byte columns of the rows kept of one sequence and head, keys or values.  SB: bytes of a row's scales,
 // moved by the blocks of the first columns.  Of every chunk the blocks of a cluster take equal shares.
 //
-// 8 sequences of 16384 tokens, 8 heads, d = 128, 6000 rows kept of each: 81 us in bf16 (4.9 TB/s of reads and writes), 56 in
-// E4M3, 42 in E2M1.  Bound by the latency from a chunk's reads to its barrier while the SMs have two blocks each, and by
+// 8 sequences of 16384 tokens, 8 heads, d = 128, 6000 rows kept of each: 80 us in bf16 (4.9 TB/s of reads and writes), 56 in
+// E4M3, 38 in E2M1.  Bound by the latency from a chunk's reads to its barrier while the SMs have two blocks each, and by
 // device memory beyond that.
-template <int RB, int SB, int LANES>
+template <int RB, int SB, int LANES, int U>
 __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_constant__ MoveParams p) {
   constexpr int kCols = RB / (16 * LANES);
   constexpr int kRows = kThreads / LANES;  // a pass of the block
-  constexpr int U = kPasses, kDeep = 4;    // passes of a chunk, chunks on their way
+  constexpr int kDeep = 8 / U;             // chunks on their way, of U passes each
   constexpr int kStep = kRows * U, kPlan = 1024;
   const int lane = threadIdx.x % LANES, r = threadIdx.x / LANES;
   const int cl = static_cast<int>(cluster_blocks()), q = static_cast<int>(cluster_rank());
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
   const int* keep = p.keep + b * p.keep_sb;
   const int* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
   // A row that is moved takes three loads, each of which gives the next one's address: its position, its pages and itself.
-  // The first two are made for kPlan rows at a time (2048 rows: 87 us instead of 79 for the bf16 rows above).  The rows then
+  // The first two are made for kPlan rows at a time (2048 rows: 87 us instead of 80 for the bf16 rows above).  The rows then
   // go through shared memory: a barrier waits for all loads into registers before it, so only asynchronous copies can be on
   // their way across it (through registers 102 us, and 177 with the positions and pages loaded beside the rows).
   __shared__ uint2 plan[kPlan];  // places (page · page size + row in it) that a row comes from and goes to
@@ -527,15 +526,15 @@ __global__ void __launch_bounds__(kThreads) pages_hand_out_kernel(const __grid_c
 template <int RB, int SB>
 cudaError_t launch_compact(const MoveParams& p, cudaStream_t s) {
   // Columns of 64 bytes (32-byte rows: 32): four lanes hold a row's part.  Blocks that do not fill the SMs are clusters that
-  // share the rows: one sequence of 32768 tokens, 2 heads, 12000 rows kept, E4M3, 8 blocks: 28 us instead of 60 (with columns
+  // share the rows: one sequence of 32768 tokens, 2 heads, 12000 rows kept, E4M3, 8 blocks: 24 us instead of 60 (with columns
   // of 16 bytes and no clusters).  A cluster's barrier costs more than a block's, so where the SMs have a block each there
   // are none: 256 blocks take 56 us, 512 in pairs 63.
   constexpr int kLanes = RB >= 64 ? 4 : RB / 16;
-  constexpr int kStep = kThreads / kLanes * kPasses;
+  constexpr int kRows = kThreads / kLanes;
   const int64_t blocks = static_cast<int64_t>(p.B) * p.Hkv * 2 * (RB / (16 * kLanes));
   int cl = 1;
   if (blocks < 152) {
-    while (cl < 8 && blocks * cl < 304 && cl * kStep < p.N) cl *= 2;
+    while (cl < 8 && blocks * cl < 304 && cl * 2 * kRows < p.N) cl *= 2;
   }
   if (blocks * cl > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr = {};
@@ -548,7 +547,10 @@ cudaError_t launch_compact(const MoveParams& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_compact_kernel<RB, SB, kLanes>, p);
+  // Chunks of four passes where clusters wait for one another at each (two: 28 and 42 us instead of 24 and 38, E4M3 and
+  // E2M1 as above), of two otherwise (256 blocks that keep 6000 or fewer E4M3 rows: 49 us instead of 51).
+  return cl > 1 ? cudaLaunchKernelEx(&cfg, cache_compact_kernel<RB, SB, kLanes, 4>, p)
+                : cudaLaunchKernelEx(&cfg, cache_compact_kernel<RB, SB, kLanes, 2>, p);
 }
 
 }  // namespace
