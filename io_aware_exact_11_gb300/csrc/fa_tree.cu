@@ -69,14 +69,14 @@
 //   4 / 16 / 32 rows, E4M3   55 / 56 / 66 us   4.9 / 4.8 / 4.1 TB/s: inside a piece 4 and 16 rows run at the memory's
 //                            rate; start, piece ends and the joining kernel take 15 us, and with 32 rows the softmax
 //                            warps, which also widen V, are the bound
-//   4 / 16 / 32 rows, E2M1   58 / 62 / 88 us   2.5 / 2.3 / 1.6 TB/s: a stream's tile is a chain of waits of 3400 cycles (its
-//                            values' references 600, the place of the widened tile 500, widening 1850), shared memory
-//                            is busy for two thirds of it, and with 32 rows the softmax is the bound
+//   4 / 16 / 32 rows, E2M1   54 / 62 / 81 us   2.6 / 2.3 / 1.8 TB/s: a stream's tile is a chain of 3300 cycles (its values'
+//                            codes 550, their reference 600, the place of the widened tile 400, widening 1450) and both
+//                            streams' instructions take two thirds of it; with 32 rows the softmax adds to that
 // E2M1, not kept: both halves written out as bf16 tiles by four warps, 195 us at 16 rows; codes of both halves fetched by one
-// warp, 72 at 4 rows; and with 16 rows worked on where there are 4 (60 us): both value warpgroups on one tile after the other
-// and its reference found by the keys' warpgroup, 80; a ring of three widened tiles for both streams, 61, and with the
-// references found by the fetching warp, 90.  Every role's instructions are fetched anew each tile, so that more of them
-// on a chain cost more than the waits they save.
+// warp, 72 at 4 rows; and where the version at hand took 60 at 4 rows: both value warpgroups on one tile after the other and its
+// reference found by the keys' warpgroup, 80; a ring of three widened tiles for both streams, 61, and with the references
+// found by the fetching warp, 90.  Every role's instructions are fetched anew each tile, so that more of them on a chain
+// cost more than the waits they save.
 // E4M3, not kept: four or eight converter warps beside the softmax warps (7 and 12 % more at 4 rows, 15 % at 32);
 // V widened by integer operations instead of the conversion instruction (slower, and it loses NaN); P̃ as two E4M3
 // terms over V as it is (the terms span too few binades).
@@ -128,10 +128,12 @@ struct Cfg {
   static constexpr int kRoom = 226 * 1024 - kMisc - kFixed;
   static constexpr int kRing = kRoom / kSlot < 14 ? kRoom / kSlot : 14;
   static constexpr int kRK = FP4 ? 4 : kRing / 2;  // (E2M1: two for each stream)
-  // E2M1: codes of as many tiles as fit, in two rings.
-  static constexpr int kCodeRoom = (kRoom - kRK * kSlot) / (2 * FourBit<D>::kHalf);
-  static constexpr int kRC = !FP4 ? 1 : kCodeRoom < kMaxRing ? kCodeRoom : kMaxRing;
-  static constexpr int kRV = FP4 ? kRC : kRing - kRK;
+  // E2M1: codes of as many tiles as fit, in two rings.  The keys' are taken up sooner: three places of eight for them
+  // (8 x 16384 keys, 8 heads, 32 rows 81 us; with one half 88, with a quarter 98).
+  static constexpr int kCodeRoom = (kRoom - kRK * kSlot) / FourBit<D>::kHalf;
+  static constexpr int kForKeys = kCodeRoom * 3 / 8;
+  static constexpr int kRC = !FP4 ? 1 : kForKeys < kMaxRing ? kForKeys : kMaxRing;
+  static constexpr int kRV = !FP4 ? kRing - kRK : kCodeRoom - kRC < kMaxRing ? kCodeRoom - kRC : kMaxRing;
   static constexpr int kOffK = 0;
   static constexpr int kOffV16 = kOffK + kRK * kSlot + (FP4 ? 0 : kRV * kSlot);
   static constexpr int kOffP = kOffV16 + 2 * kV16;
@@ -144,7 +146,7 @@ struct Cfg {
   static constexpr int kColScales = kColO + 2 * kPCols;       // E2M1: of each K tile's scales, and of ones
   static constexpr int kCols = kColScales + (FP4 ? 20 : 0);
   static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kRK >= 2 && kRV >= 2 && kRV <= kMaxRing && (!FP8 || kRV + 4 <= kScaleRing), "rings");
+  static_assert(kRK >= 2 && kRV >= 2 && (!FP4 || kRC >= 2) && kRV <= kMaxRing && (!FP8 || kRV + 4 <= kScaleRing), "rings");
   static_assert(kQTile % 1024 == 0 && kSlot % 1024 == 0 && kCols <= 512, "swizzle atoms, TMEM");
 };
 
@@ -420,7 +422,9 @@ __device__ __forceinline__ void convert_values(const TreeParams& p, const TreePa
       if (used > 0) mbar_wait_inl(&ms->p_free[g], (used - 1) & 1, abort_flag, p.err, tree_site(0x13));
       __syncwarp();
       if (!far && (w.t0 + i + 1) * kTreeBN <= context) {
-        widen_codes<D, 1>(src + r * (D / 2), bytes, v_tile, r, ref);
+        // (Groups at a time 1, 2, 4: 54, 54, 53 us at 4 rows, 93, 84, 88 for 64 ragged sequences of up to 8192 keys in pages
+        // of 16; 1, 2, 4 with 32 rows: 88, 88, 94.)
+        widen_codes<D, NR == 16 ? 2 : 1>(src + r * (D / 2), bytes, v_tile, r, ref);
       } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, v_tile, r, ref, key >= context, !counts, far)) {
         atomicOr(&ms->bad[w.index % kBadRing][(key - context) >> 5], 1u << ((key - context) & 31));
       }
@@ -546,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
       mbar_init(&ms->k_empty[s], 1);
     }
     for (int s = 0; FP4 && s < C::kRC; ++s) {
-      mbar_init(&ms->code_full[s], 1);
+      mbar_init(&ms->code_full[s], kCodeArrivals);
       mbar_init(&ms->code_empty[s], 4);
     }
     for (int s = 0; s < 2; ++s) {
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, F, NR>::kThreads, 1) tree_kernel(const 
       mbar_init(&ms->v16_full[s], 4);
     }
     for (int s = 0; s < C::kRV; ++s) {
-      mbar_init(&ms->v_full[s], 1);
+      mbar_init(&ms->v_full[s], FP4 ? kCodeArrivals : 1);
       mbar_init(&ms->v_empty[s], kWiden ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -1246,11 +1250,11 @@ cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
   // By the rows of a pair; 8 sequences of 16384 keys, 8 key/value heads, us with the one and the other:
   //   4 and 16 rows as 16 columns or 32    E4M3 55, 56 | 60, 62    bf16 89, 90 | 88, 90 (head dim 64 51, 52 | 54, 55)
-  //                                        E2M1 60, 62 | 80, 83 (head dim 64 52, 53 | 60, 64)
+  //                                        E2M1 60, 61 | 81, 83 (head dim 64 52, 53 | 61, 64)
   //   16 and 32 rows here or in the kernel for many rows    E4M3 56, 66 | 72, 74    bf16 90, 92 | 93, 95
-  //                                                         E2M1 62, 88 | 88, 91 (head dim 64 53, 66 | 70, 72)
-  //   4 rows of which the softmax works on 8 or 16    E2M1 58 | 60 (head dim 64 49 | 52; 64 ragged sequences of up to 8192
-  //   keys, 7 rows 95 | 99); the others' softmax is no bound at so few
+  //                                                         E2M1 61, 81 | 84, 87 (head dim 64 53, 66 | 74, 75)
+  //   4 rows of which the softmax works on 8 or 16    E2M1 54 | 60 (head dim 64 47 | 52); the others' softmax is no bound
+  //   at so few
   // (32 rows are the most that fit here without tiles of rows; 64 columns spilled registers and took 81 us where the
   // other kernel took 69: 8 tokens of 7 heads a group, 16 ragged sequences of up to 8192 bf16 keys.)
   const bool wide = rows > kTreeNarrowRows;

@@ -416,6 +416,9 @@ struct FourBit {
 // What load_codes fetches: both halves into one ring, in the order above, or the keys or the values alone.
 enum CodeParts : int { kBothHalves = 0, kKeyCodes = 1, kValueCodes = 2 };
 
+// Arrivals that a half's barrier waits for: the warp's lanes, as their scales land, and the one that announces the codes.
+constexpr int kCodeArrivals = 33;
+
 // Fetches the codes and scales of a part's tiles, by one warp, into a ring of RING halves.  at_piece is called at the start
 // of every piece.
 template <int D, int RING, CodeParts PARTS, class AtPiece>
@@ -436,16 +439,23 @@ __device__ __forceinline__ void load_codes(const TreeParams& p, const TreePart& 
     if (!ok) return;
     const bool real = lane < npt && blk >= 0;
     const uint32_t n_real = __popc(__ballot_sync(0xffffffffu, real));
-    if (lane == 0) mbar_arrive_expect_tx(&full[slot], n_real * ((kRow + kRowScales) << bshift));
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot], n_real * (kRow << bshift));
     __syncwarp();
+    uint8_t* to = ring + slot * FourBit<D>::kHalf;
     if (real) {
       const int64_t row = (static_cast<int64_t>(blk) * p.Hkv + h) << bshift;
-      uint8_t* to = ring + slot * FourBit<D>::kHalf;
       bulk_load(to + ((lane << bshift) * kRow), static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + row * kRow,
                 kRow << bshift, &full[slot]);
-      bulk_load(to + FourBit<D>::kCodes + ((lane << bshift) * kRowScales),
-                (is_v ? p.v_scale : p.k_scale) + row * kRowScales, kRowScales << bshift, &full[slot]);
     }
+    // The scales by sixteen bytes a lane: bulk copies of so little cost as much as those of the codes (64 ragged sequences of
+    // up to 8192 keys in pages of 16: 88 us instead of 94).
+    const int row0 = lane * (16 / kRowScales);
+    const int from = __shfl_sync(0xffffffffu, blk, min(row0 >> bshift, 31));
+    if (lane < FourBit<D>::kScales / 16 && from >= 0)
+      cp_async16(to + FourBit<D>::kCodes + lane * 16,
+                 (is_v ? p.v_scale : p.k_scale) +
+                     (((static_cast<int64_t>(from) * p.Hkv + h) << bshift) + (row0 & (p.block_size - 1))) * kRowScales);
+    cp_async_arrive(&full[slot]);
     ++issued;
     if (++slot == RING) {
       slot = 0;
@@ -505,10 +515,10 @@ __device__ __forceinline__ void widen_group(uint4 c, uint8_t* dst, int r, int g,
 // Eight codes to fp16, times the pair of scales.
 __device__ __forceinline__ uint4 widen_e2m1x8(uint32_t w, uint32_t scale2) {
   uint32_t o[4];
+  e2m1x8_to_f16(w, o);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t h = e2m1x2_to_f16x2(w >> (8 * i));
-    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&scale2));
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), *reinterpret_cast<const __half2*>(&scale2));
     o[i] = *reinterpret_cast<const uint32_t*>(&x);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
@@ -521,18 +531,22 @@ __device__ __forceinline__ int group_at(int j, int r) {
 }
 
 // Widens one row of E2M1 codes to fp16, each group times its power of two relative to 2^ref.
-// src: the row's codes, scales: its bytes.  A larger body costs instruction fetches, which all warps' roles compete for:
-// 8 x 32768 keys, 256 rows take 261 us with one group at a time, 255 with two, 289 with four; 64 ragged sequences of up to
-// 8192 keys in the kernel for few rows, which has more roles, 103, 111 and 123.
+// src: the row's codes, scales: its bytes.  A larger body saves waits and costs instruction fetches, which all warps' roles
+// compete for, so how many groups are unrolled is the caller's choice.
 template <int D, int UNROLL>
 __device__ __forceinline__ void widen_codes(const uint8_t* src, uint32_t scales, uint8_t* dst, int r, int ref) {
+  // Rows are 128 bytes long and begin at multiples of that: the swizzle takes one operation a store.
+  const uint32_t to = smem_u32(dst) ^ ((r & 7) << 4);
 #pragma unroll UNROLL
   for (int j = 0; j < D / kE2m1Group; ++j) {
     const int g = group_at<D>(j, r);
     const uint4 c = *reinterpret_cast<const uint4*>(src + g * 16);
-    const uint32_t s = scales >> (8 * g) & 0xffu;
-    const uint32_t scale2 = s == 255 ? 0x7e007e00u : power_f16x2(static_cast<int>(s) - 127 - ref);
-    widen_group(c, dst, r, g, [&](uint32_t w) { return widen_e2m1x8(w, scale2); });
+    const int s = static_cast<int>(scales >> (8 * g) & 0xffu), e = s - 127 - ref;
+    uint32_t scale2 = static_cast<uint32_t>(e + 15) * 0x04000400u;  // 2^e twice, a normal number but for …
+    if (static_cast<unsigned>(e + 14) > 29u || s == 255) scale2 = s == 255 ? 0x7e007e00u : power_f16x2(e);
+    const uint32_t at = (to + (g >> 1) * (kTreeBN * 128)) ^ ((g & 1) << 6), w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) st_shared16(at ^ (q << 4), widen_e2m1x8(w[q], scale2));
   }
 }
 // The same out of line for tiles that hold drafted keys (whose NaN groups are taken out and reported by the result), the

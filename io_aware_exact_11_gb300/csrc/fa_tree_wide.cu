@@ -38,14 +38,14 @@
 // Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements (replaying a graph over two caches):
 //   64 / 128 / 256 rows, bf16    98 / 104 / 125 us   0.82 / 0.77 of a device copy, 1100 TFLOP/s
 //   64 / 128 / 256 rows, E4M3    76 /  84 / 140 us   452 / 818 / 982 TFLOP/s
-//   64 / 128 / 256 rows, E2M1    91 /  94 / 145 us   378 / 732 / 947 TFLOP/s (32768 keys, 256 rows: 258 us, 1063)
+//   64 / 128 / 256 rows, E2M1    87 /  90 / 144 us   395 / 761 / 957 TFLOP/s (32768 keys, 256 rows: 252 us, 1089)
 // With two row tiles a step (one tile's P̃V and S, 1024 tensor cycles) takes about 1750 cycles: the issuing
 // warp's own instructions, of which it gets one through every dozen cycles beside the softmax warps, and the wait
 // for P̃ (S to P̃ is a chain of about 1400 cycles).  E4M3 with shared rows waits for the converters (2400 cycles a
 // tile).  With E2M1 the softmax reads
 // its scores twice, in rolled loops; with four converter warps for both halves and the scores held in registers the three took
 // 131, 135 and 157 us.  Not kept: a second set of eight converter warps for every other tile, which takes registers from the
-// softmax (97 us at 64 rows), and rings and loading warps of their own for the keys' and the values' codes (98).
+// softmax (97 us at 64 rows, from 91), and rings and loading warps of their own for the keys' and the values' codes (98).
 // A pair boundary costs a CTA 10000 to 15000 cycles (O out, Q in, the first scores).
 #include <stddef.h>
 
@@ -362,7 +362,8 @@ __device__ __forceinline__ void convert_halves(const TreeParams& p, const TreePa
       __syncwarp();
       uint8_t* dst = smem + (VALUES ? C::kOffV16 : C::kOffK) + (used & 1) * C::kSlot + r * 128;
       if (!far && key - r + kBN <= (VALUES ? context : w.len)) {
-        widen_codes<D, 2>(src + r * (D / 2), bytes, dst, r, ref);
+        // (Groups at a time 1, 2, 4: 252, 253, 279 us for 256 rows over 8 x 32768 keys, 8 heads.)
+        widen_codes<D, 1>(src + r * (D / 2), bytes, dst, r, ref);
       } else if (!VALUES) {
         widen_keys_edge<D>(src + r * (D / 2), bytes, dst, r, ref, !counts, far ? &sc->power[used % kTileRing][r] : nullptr);
       } else if (widen_codes_edge<D>(src + r * (D / 2), bytes, dst, r, ref, key >= context, !counts, far)) {
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<D, F, TILES>::kThreads, 1) tree_wide_kerne
       mbar_init(&ms->k_empty[s], 1);
     }
     for (int s = 0; FP4 && s < C::kCodeRing; ++s) {
-      mbar_init(&ms->code_full[s], 1);
+      mbar_init(&ms->code_full[s], kCodeArrivals);
       mbar_init(&ms->code_empty[s], 4);
     }
     for (int s = 0; s < C::kRV; ++s) {

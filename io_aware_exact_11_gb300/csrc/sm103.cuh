@@ -469,6 +469,17 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ void cp_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+// Arrives once the thread's copies before have landed (one of the arrivals that the barrier counts).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // Two E2M1 codes (low half of the byte first) as fp16, exact; eight fp32 values as E2M1 codes, four bits each from the
 // lowest on (nearest even, saturating).
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t codes) {
@@ -477,6 +488,14 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t codes) {
       : "=r"(r)
       : "r"(codes));
   return r;
+}
+// Eight at once: bytes that are named apart need no shifts.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t codes, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\tmov.b32 {c0, c1, c2, c3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, c0;\n\tcvt.rn.f16x2.e2m1x2 %1, c1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c2;\n\tcvt.rn.f16x2.e2m1x2 %3, c3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(codes));
 }
 __device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8]) {
   uint32_t r;
