@@ -66,18 +66,28 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A chunk is U passes of the block over rows, of which kDeep are on their way, and kSteps chunks make a plan.  (Deeper rings
+// and longer plans leave room for fewer blocks: with 4 and 8 of two passes 48 us instead of 52 for the E4M3 rows below, and
+// 81 instead of 75 for twice as many.)
+template <int LANES, int U>
+struct Plan {
+  static constexpr int kStep = kThreads / LANES * U, kDeep = U == 2 ? 3 : 2, kSteps = U == 2 ? 6 : 5, kPlan = kSteps * kStep;
+  static_assert(kSteps - (kDeep - 1) > 3, "a barrier between a plan's places and the first look at them");
+  static constexpr int kSmem = kDeep * U * kThreads * 16 + 2 * kPlan * 8;
+};
+
 // Moves LANES 16-byte columns of the rows kept of one sequence and head, keys or values.  SB: bytes of a row's scales,
 // moved by the blocks of the first columns.  Of every chunk the blocks of a cluster take equal shares.
 //
-// 8 sequences of 16384 tokens, 8 heads, d = 128, 6000 rows kept of each: 80 us in bf16 (4.9 TB/s of reads and writes), 56 in
-// E4M3, 38 in E2M1.  Bound by the latency from a chunk's reads to its barrier while the SMs have two blocks each, and by
+// 8 sequences of 16384 tokens, 8 heads, d = 128, 6000 rows kept of each: 76 us in bf16 (5.2 TB/s of reads and writes), 52 in
+// E4M3, 36 in E2M1.  Bound by the latency from a chunk's reads to its barrier while the SMs have two blocks each, and by
 // device memory beyond that.
 template <int RB, int SB, int LANES, int U>
-__global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_constant__ MoveParams p) {
+__global__ void __launch_bounds__(kThreads, 4) cache_compact_kernel(const __grid_constant__ MoveParams p) {
   constexpr int kCols = RB / (16 * LANES);
   constexpr int kRows = kThreads / LANES;  // a pass of the block
-  constexpr int kDeep = 8 / U;             // chunks on their way, of U passes each
-  constexpr int kStep = kRows * U, kPlan = 1024;
+  using P = Plan<LANES, U>;
+  constexpr int kStep = P::kStep, kDeep = P::kDeep, NP = P::kPlan / kThreads;
   const int lane = threadIdx.x % LANES, r = threadIdx.x / LANES;
   const int cl = static_cast<int>(cluster_blocks()), q = static_cast<int>(cluster_rank());
   const int64_t group = blockIdx.x / cl;
@@ -98,11 +108,13 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
   const int* keep = p.keep + b * p.keep_sb;
   const int* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
   // A row that is moved takes three loads, each of which gives the next one's address: its position, its pages and itself.
-  // The first two are made for kPlan rows at a time (2048 rows: 87 us instead of 80 for the bf16 rows above).  The rows then
-  // go through shared memory: a barrier waits for all loads into registers before it, so only asynchronous copies can be on
-  // their way across it (through registers 102 us, and 177 with the positions and pages loaded beside the rows).
-  __shared__ uint2 plan[kPlan];  // places (page · page size + row in it) that a row comes from and goes to
-  __shared__ uint4 ring[kDeep][U][kThreads];
+  // The first two are made for a plan of several chunks at a time, while the chunks of the plan before are moved (between
+  // those 81 and 56 us instead of 76 and 52 for the bf16 and E4M3 rows above).  The rows go through shared memory: a barrier waits for all loads into
+  // registers before it, so only asynchronous copies can be on their way across it (through registers 102 us, and 177 with
+  // the positions and pages loaded beside the rows).
+  extern __shared__ uint4 ring[];                                             // [kDeep][U][kThreads]
+  uint2* const plans = reinterpret_cast<uint2*>(ring + kDeep * U * kThreads);  // of two plans, the places (page · page size +
+                                                                              // row in it) that a row comes from and goes to
   const int mask = p.block_size - 1;
   auto row = [&](unsigned int place) -> int64_t {
     return ((static_cast<int64_t>(place >> shift) * p.Hkv + h) << shift) + (place & mask);
@@ -113,77 +125,108 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
     else
       __syncthreads();
   };
-  for (int64_t i0 = 0; i0 < n; i0 += kPlan * cl) {
-    // Of every cl chunks this block takes the q-th: its i-th row is row_at(i) of those kept.
-    auto row_at = [&](int i) { return i0 + static_cast<int64_t>(i / kStep * cl + q) * kStep + i % kStep; };
-    const int steps = static_cast<int>((min(static_cast<int64_t>(kPlan) * cl, n - i0) + kStep * cl - 1) / (kStep * cl));
-    __syncthreads();  // the last plan is done with
-    uint32_t s[kPlan / kThreads];
+  // Of every cl chunks this block takes the q-th: the i-th row of its k-th plan is row_at(k, i) of those kept.
+  auto row_at = [&](int k, int i) {
+    return static_cast<int64_t>(k) * P::kPlan * cl + static_cast<int64_t>(i / kStep * cl + q) * kStep + i % kStep;
+  };
+  const int steps = static_cast<int>((n + static_cast<int64_t>(kStep) * cl - 1) / (static_cast<int64_t>(kStep) * cl));
+  int t[NP], x[NP], y[NP];
+  uint32_t s[NP];
+  auto positions = [&](int k) {
 #pragma unroll
-    for (int k = 0; k < kPlan / kThreads; ++k) {
-      const int i = k * kThreads + threadIdx.x;
-      uint2 e = make_uint2(kNowhere, 0);
-      if (row_at(i) >= n) {
-        plan[i] = e;
-        continue;
-      }
-      const int64_t to = first + row_at(i);
-      const int t = keep[row_at(i)];
-      if (t < to || t >= room) {
+    for (int j = 0; j < NP; ++j) {
+      const int64_t i = row_at(k, j * kThreads + threadIdx.x);
+      t[j] = i < n ? keep[i] : -1;
+    }
+  };
+  auto pages = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int64_t i = row_at(k, j * kThreads + threadIdx.x), to = first + i;
+      x[j] = y[j] = 0;
+      if (i >= n) continue;
+      if (t[j] < to || t[j] >= room) {
         report(p.err, kSiteBadLength);
-      } else if (t != to) {
-        const int x = table[t >> shift], y = table[to >> shift];
-        if (x < 0 || x >= p.num_blocks || y < 0 || y >= p.num_blocks)
+        t[j] = -1;
+      } else if (t[j] == to) {
+        t[j] = -1;
+      } else {
+        x[j] = table[t[j] >> shift];
+        y[j] = table[to >> shift];
+      }
+    }
+  };
+  auto places = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int i = j * kThreads + threadIdx.x;
+      uint2 e = make_uint2(kNowhere, 0);
+      if (t[j] >= 0) {
+        if (x[j] < 0 || x[j] >= p.num_blocks || y[j] < 0 || y[j] >= p.num_blocks)
           report(p.err, kSiteBadBlock);
         else
-          e = make_uint2((static_cast<unsigned int>(x) << shift) + (t & mask),
-                         (static_cast<unsigned int>(y) << shift) + static_cast<unsigned int>(to & mask));
+          e = make_uint2((static_cast<unsigned int>(x[j]) << shift) + (t[j] & mask),
+                         (static_cast<unsigned int>(y[j]) << shift) + static_cast<unsigned int>((first + row_at(k, i)) & mask));
       }
-      plan[i] = e;
+      plans[(k & 1) * P::kPlan + i] = e;
       if (scales && e.x != kNowhere) {
         const int64_t from = row(e.x);
-        if constexpr (SB == 1) s[k] = scale[from];
-        if constexpr (SB == 2) s[k] = reinterpret_cast<const uint16_t*>(scale)[from];
-        if constexpr (SB == 4) s[k] = reinterpret_cast<const uint32_t*>(scale)[from];
+        if constexpr (SB == 1) s[j] = scale[from];
+        if constexpr (SB == 2) s[j] = reinterpret_cast<const uint16_t*>(scale)[from];
+        if constexpr (SB == 4) s[j] = reinterpret_cast<const uint32_t*>(scale)[from];
       }
     }
-    if (SB > 0)
-      barrier();  // all scales of the plan have been read
-    else
-      __syncthreads();
-    if (scales) {
+  };
+  auto move_scales = [&](int k) {
 #pragma unroll
-      for (int k = 0; k < kPlan / kThreads; ++k) {
-        const int i = k * kThreads + threadIdx.x;
-        if (plan[i].x == kNowhere) continue;
-        const int64_t to = row(plan[i].y);
-        if constexpr (SB == 1) scale[to] = static_cast<uint8_t>(s[k]);
-        if constexpr (SB == 2) reinterpret_cast<uint16_t*>(scale)[to] = static_cast<uint16_t>(s[k]);
-        if constexpr (SB == 4) reinterpret_cast<uint32_t*>(scale)[to] = s[k];
-      }
+    for (int j = 0; SB > 0 && j < NP; ++j) {
+      if (!scales) break;
+      const uint2 e = plans[(k & 1) * P::kPlan + j * kThreads + threadIdx.x];
+      if (e.x == kNowhere) continue;
+      const int64_t to = row(e.y);
+      if constexpr (SB == 1) scale[to] = static_cast<uint8_t>(s[j]);
+      if constexpr (SB == 2) reinterpret_cast<uint16_t*>(scale)[to] = static_cast<uint16_t>(s[j]);
+      if constexpr (SB == 4) reinterpret_cast<uint32_t*>(scale)[to] = s[j];
     }
-    auto load = [&](int slot, int step) {
+  };
+  auto place = [&](int step, int u) {
+    return plans[(step / P::kSteps & 1) * P::kPlan + step % P::kSteps * kStep + u * kRows + r];
+  };
+  auto load = [&](int slot, int step) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const unsigned int from = step < steps ? plan[step * kStep + u * kRows + r].x : kNowhere;
-        if (from != kNowhere) cp_async16(&ring[slot][u][threadIdx.x], cache + row(from) * RB);
-      }
-      cp_async_commit();
-    };
+    for (int u = 0; u < U; ++u) {
+      const unsigned int from = step < steps ? place(step, u).x : kNowhere;
+      if (from != kNowhere) cp_async16(&ring[(slot * U + u) * kThreads + threadIdx.x], cache + row(from) * RB);
+    }
+    cp_async_commit();
+  };
+  positions(0);
+  pages(0);
+  places(0);
+  barrier();  // the plan's places are there, and its scales have been read
+  move_scales(0);
 #pragma unroll
-    for (int k = 0; k < kDeep - 1; ++k) load(k, k);
-    int slot = 0;
+  for (int k = 0; k < kDeep - 1; ++k) load(k, k);
+  int slot = 0;
 #pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
-      load(slot == 0 ? kDeep - 1 : slot - 1, step + kDeep - 1);
-      cp_async_wait<kDeep - 1>();
-      barrier();  // all of the chunk that is stored now has been read
+  for (int step = 0; step < steps; ++step) {
+    load(slot == 0 ? kDeep - 1 : slot - 1, step + kDeep - 1);
+    cp_async_wait<kDeep - 1>();
+    barrier();  // all of the chunk that is stored now has been read
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint2 e = plan[step * kStep + u * kRows + r];
-        if (e.x != kNowhere) *reinterpret_cast<uint4*>(cache + row(e.y) * RB) = ring[slot][u][threadIdx.x];
-      }
-      slot = slot == kDeep - 1 ? 0 : slot + 1;
+    for (int u = 0; u < U; ++u) {
+      const uint2 e = place(step, u);
+      if (e.x != kNowhere) *reinterpret_cast<uint4*>(cache + row(e.y) * RB) = ring[(slot * U + u) * kThreads + threadIdx.x];
+    }
+    slot = slot == kDeep - 1 ? 0 : slot + 1;
+    // The next plan: its places are written where the plan before lay, two chunks before the first one looks there.
+    const int next = step / P::kSteps + 1;
+    if (next * P::kSteps < steps) {
+      const int phase = step % P::kSteps;
+      if (phase == 0) positions(next);
+      if (phase == 1) pages(next);
+      if (phase == 2) places(next);
+      if (phase == 3) move_scales(next);  // (a barrier after they have been read)
     }
   }
 }
@@ -523,9 +566,9 @@ __global__ void __launch_bounds__(kThreads) pages_hand_out_kernel(const __grid_c
 template <int RB, int SB>
 cudaError_t launch_compact(const MoveParams& p, cudaStream_t s) {
   // Columns of 64 bytes (32-byte rows: 32): four lanes hold a row's part.  Blocks that do not fill the SMs are clusters that
-  // share the rows: one sequence of 32768 tokens, 2 heads, 12000 rows kept, E4M3, 8 blocks: 24 us instead of 60 (with columns
+  // share the rows: one sequence of 32768 tokens, 2 heads, 12000 rows kept, E4M3, 8 blocks: 22 us instead of 60 (with columns
   // of 16 bytes and no clusters).  A cluster's barrier costs more than a block's, so where the SMs have a block each there
-  // are none: 256 blocks take 56 us, 512 in pairs 63.
+  // are none (without plans ahead 256 blocks took 56 us, 512 in pairs 63).
   constexpr int kLanes = RB >= 64 ? 4 : RB / 16;
   constexpr int kRows = kThreads / kLanes;
   const int64_t blocks = static_cast<int64_t>(p.B) * p.Hkv * 2 * (RB / (16 * kLanes));
@@ -545,9 +588,15 @@ cudaError_t launch_compact(const MoveParams& p, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   // Chunks of four passes where clusters wait for one another at each (two: 28 and 42 us instead of 24 and 38, E4M3 and
-  // E2M1 as above), of two otherwise (256 blocks that keep 6000 or fewer E4M3 rows: 49 us instead of 51).
-  return cl > 1 ? cudaLaunchKernelEx(&cfg, cache_compact_kernel<RB, SB, kLanes, 4>, p)
-                : cudaLaunchKernelEx(&cfg, cache_compact_kernel<RB, SB, kLanes, 2>, p);
+  // E2M1 as above, without plans ahead), of two otherwise (256 blocks that keep 6000 or fewer E4M3 rows: 49 us instead of 51).
+  auto launch = [&](auto* kernel, int smem) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  };
+  return cl > 1 ? launch(cache_compact_kernel<RB, SB, kLanes, 4>, Plan<kLanes, 4>::kSmem)
+                : launch(cache_compact_kernel<RB, SB, kLanes, 2>, Plan<kLanes, 2>::kSmem);
 }
 
 }  // namespace
