@@ -355,8 +355,8 @@ __device__ __forceinline__ void load_pages(const TreeParams& p, const TreePart& 
 
 // ---------------------------------------------------------------- a cache in four bits
 //
-// A page of one head is contiguous: its codes and its scale bytes come by plain bulk copies into a ring of half tiles (the
-// keys or the values of 128 rows; in one ring K₀, K₁, V₀, K₂, V₁ … of each piece, the order in which they are used), and
+// A page of one head is contiguous: its codes come by one plain bulk copy, its scale bytes by the lanes' asynchronous ones, into
+// a ring of half tiles (the keys or the values of 128 rows; in one ring K₀, K₁, V₀, K₂, V₁ … of each piece, the order in which they are used), and
 // other warps widen them to fp16, each group times its power of two relative to a reference: from 2⁻²³ to 2^13 of it that
 // is exact (the smallest code but zero, 0.5, becomes fp16's smallest step, 2⁻²⁴, and the largest, 6, stays below 65504).
 // (Copies of pages without a tensor map: a page of 16 keys is 1 KB of codes and 64 bytes of scales, and the products need
