@@ -25,8 +25,8 @@
 // Measured on GB300 (d = 128): gathering 4 sequences of 32768 E4M3 keys, 8 heads: 124 us,
 // 6.5 TB/s, 0.97 of a device copy; writing 8 ragged sequences of up to 8192 tokens as
 // E4M3, 4 heads: 31 us, 5.1 TB/s, 0.77 (it quantises on the way), as E2M1 30 us, 4.5 TB/s, and reading those back behind
-// a prefix of 2048 tokens 37 us, 5.5 TB/s; a token for each of 64
-// sequences: the launch (11 us a call from Python).
+// a prefix of 2048 tokens 37 us, 5.5 TB/s; four bits of 4 x 32768 tokens, 8 heads, 105 and 107 us, 6.5 and 6.4 TB/s; a
+// token for each of 64 sequences: the launch (11 us a call from Python).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -370,6 +370,8 @@ cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
 //   writing E4M3, 4 heads   8 x 512 tokens 4.8, 4.7, 5.1   8 x 2048 11.9, 10.6, 11.1   8 x 8192 39.0, 32.2, 31.6
 //   reading E4M3            8 x 512 5.0, 4.9, 5.0   8 x 2048 12.2, 10.8, 10.8   4 x 32768, 8 heads 146, 122, 122
 //   bf16                    8 x 8192, 4 heads, writing 41.2, 41.4, 41.3 and reading 43.5, 42.0, 42.2
+//   E2M1, 4 heads           8 x 512 6.2 each way and always, 8 x 2048 writing 14.4, 12.3, 10.3 and reading 12.3, 10.3, 10.3,
+//                           8 x 8192 writing 43.1, 34.9, 31.2 and reading 39.1, 31.9, 31.2
 // The rule turns to four between the second and the third size (4 x 152 x 2048 threads of one token).
 template <bool APPEND, int D, int F>
 cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
