@@ -226,13 +226,16 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     }
   }
   auto scales = [&](int64_t at, int r) {
-    if (FP8 && it.lane8 == 0) {
-      p.k_scale[at] = static_cast<uint8_t>(ke[r] + 127);
-      p.v_scale[at] = static_cast<uint8_t>(ve[r] + 127);
-    }
-    if (FP4 && (it.lane8 & 3) == 0) {  // one byte per group, whole as it stands
-      p.k_scale[at * (D / kE2m1Group) + it.lane8 / 4] = static_cast<uint8_t>(ke[r]);
-      p.v_scale[at * (D / kE2m1Group) + it.lane8 / 4] = static_cast<uint8_t>(ve[r]);
+    if constexpr (FP8) {
+      if (it.lane8 == 0) {
+        p.k_scale[at] = static_cast<uint8_t>(ke[r] + 127);
+        p.v_scale[at] = static_cast<uint8_t>(ve[r] + 127);
+      }
+    } else if constexpr (FP4) {  // one byte per group, whole as it stands
+      if ((it.lane8 & 3) == 0) {
+        p.k_scale[at * (D / kE2m1Group) + it.lane8 / 4] = static_cast<uint8_t>(ke[r]);
+        p.v_scale[at * (D / kE2m1Group) + it.lane8 / 4] = static_cast<uint8_t>(ve[r]);
+      }
     }
   };
   Out* const k_out = static_cast<Out*>(p.k_cache) + it.lane8;
