@@ -373,14 +373,15 @@ cudaError_t launch_r(const CacheParams& p, cudaStream_t stream) {
 //   writing E4M3, 4 heads   8 x 512 tokens 4.8, 4.7, 5.1   8 x 2048 11.9, 10.6, 11.1   8 x 8192 39.0, 32.2, 31.6
 //   reading E4M3            8 x 512 5.0, 4.9, 5.0   8 x 2048 12.2, 10.8, 10.8   4 x 32768, 8 heads 146, 122, 122
 //   bf16                    8 x 8192, 4 heads, writing 41.2, 41.4, 41.3 and reading 43.5, 42.0, 42.2
-//   E2M1, 4 heads           8 x 512 6.2 each way and always, 8 x 2048 writing 14.4, 12.3, 10.3 and reading 12.3, 10.3, 10.3,
-//                           8 x 8192 writing 43.1, 34.9, 31.2 and reading 39.1, 31.9, 31.2
-// The rule turns to four between the second and the third size (4 x 152 x 2048 threads of one token).
+//   E2M1, 4 heads           8 x 2048 writing 14.4, 12.3, 10.3 and reading 12.3, 10.3, 10.3; 8 x 8192 writing 43.1, 34.9, 31.2
+//                           and reading 39.1, 31.9, 31.2; one and four, 8 x 600 6.2 and 6.2, 8 x 1024 8.3 and 6.2
+// The rule turns to four between the second and the third size (4 x 152 x 2048 threads of one token), in four bits, where
+// a thread has the fewest bytes, once they fill the machine.
 template <bool APPEND, int D, int F>
 cudaError_t launch_d(const CacheParams& p, cudaStream_t stream) {
   const int64_t threads = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 8);
-  return p.N >= 4 && threads >= 4ll * 152 * 2048 ? launch_r<APPEND, D, F, 4>(p, stream)
-                                                 : launch_r<APPEND, D, F, 1>(p, stream);
+  const bool four = p.N >= 4 && threads >= (F == kCacheE2m1 ? 1ll : 4ll) * 152 * 2048;
+  return four ? launch_r<APPEND, D, F, 4>(p, stream) : launch_r<APPEND, D, F, 1>(p, stream);
 }
 
 template <bool APPEND, int D>
