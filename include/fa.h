@@ -459,17 +459,21 @@ FA_API size_t fa_pages_reserve_workspace_size(int B, int num_blocks);
 
 /*
  * fa_pages_reserve — pages for the next new_lens[b] tokens of every sequence of the
- *   table (device int32 [B]; 0: none).  Entries of the table that are missing get free
- *   pages; entries reserved before stay.  If the next token goes into a page that
- *   others hold too, the sequence gets one of its own in its place, and
- *   copy_src[b], copy_dst[b] name the old and the new page (both −1 otherwise), to be
- *   copied with fa_cache_copy_pages before anything is written: of sequences
- *   that write into one page all but the last to hold it get a copy.
+ *   table (device int32 [B]; 0: none).  They go into its entries from
+ *   seq_lens[b] / block_size on.  Entries that are missing get free pages; entries
+ *   reserved before stay.  An entry whose page others hold too (after fa_pages_fork,
+ *   or where a length was set back without fa_pages_free) gets a page of its own in
+ *   its place, and the old one has a holder less: of sequences that write into one
+ *   page all but the last to hold it get another.  If tokens of the sequence lie in
+ *   the page (so only where the next one goes), copy_src[b], copy_dst[b] name the
+ *   old and the new page (both −1 otherwise), to be copied with fa_cache_copy_pages
+ *   before anything is written.
  *   Sequences are served in order, free pages handed out by rising number.  From the
  *   first sequence that finds too few on, none with tokens to come is served:
  *   granted[b] = 0 and its entries stay as they were; else granted[b] = 1.  A length
- *   that cannot be or that the table has no room for, and a bad page id under the next
- *   token, are caught on the device: granted[b] = 0, the others are served.
+ *   that cannot be or that the table has no room for, and among the entries a bad page
+ *   id, a page without holders or none under tokens that are there, are caught on the
+ *   device: granted[b] = 0, its entries stay, the others are served.
  *   seq_lens stay as they are.  workspace: fa_pages_reserve_workspace_size() bytes,
  *   4-byte aligned, contents on entry do not matter.
  *   Supported: B <= 4096, B·(max_blocks + 1) < 2^31.

@@ -1568,7 +1568,7 @@ fa_status fa_device_status(void* stream) {
   if (which == 1) {
     const bool page = (code & 0xFFu) == fa::kSiteBadBlock;
     if ((code & 0xFFu) == fa::kSiteBadHolders)
-      return fail(FA_ERR_INVALID_ARG, "pages: a page was freed that nobody holds");
+      return fail(FA_ERR_INVALID_ARG, "pages: a table names a page that nobody is said to hold");
     if ((code & 0xFFu) == fa::kSiteBadSequence)
       return fail(FA_ERR_INVALID_ARG, "pages: a sequence is no row of the table, is named twice or is not empty");
     if ((code >> 8) == fa::kKernDecode)

@@ -949,9 +949,9 @@ def pages_reserve_workspace_size(B: int, num_blocks: int) -> int:
 def pages_reserve(block_table, seq_lens, holders, new_lens, block_size: int, workspace=None, stream=None):
     """Pages for the next new_lens[b] tokens of every sequence (int32 [B]); returns (granted, copy_src, copy_dst), int32 [B].
 
-    Missing table entries get free pages, and a sequence whose next token goes into a page that others hold too gets one
-    of its own in its place: copy_src[b] → copy_dst[b] (−1: nothing), to be copied with ``cache_copy_pages`` before
-    anything is written.  Sequences are served in order, from the free pages by rising number; from the first one that
+    Missing table entries get free pages, and an entry that the tokens go into and whose page others hold too gets one of
+    its own in its place.  Where tokens of the sequence lie in it, copy_src[b] → copy_dst[b] (−1: nothing) are to be
+    copied with ``cache_copy_pages`` before anything is written.  Sequences are served in order, from the free pages by rising number; from the first one that
     finds too few on, none with tokens to come is (granted[b] = 0, its table as it was).
     """
     torch = _torch()

@@ -173,30 +173,37 @@ class Pool:
                     self.table[b][j] = -1
 
     def reserve(self, new):
-        B = len(self.lens)
+        """After the reservation and its copies, no page that the new tokens go into has another holder.
+
+        Of the entries from the next token's on, those that are missing get a free page, and those whose page others
+        hold too get one in its place, which is a copy where tokens of the sequence lie in the page.
+        """
+        B, held = len(self.lens), list(self.holders)
         granted, src, dst = [0] * B, [-1] * B, [-1] * B
-        free = [p for p, n in enumerate(self.holders) if n == 0]
+        free = [p for p, n in enumerate(held) if n == 0]
         short = False
         for b in range(B):
             row, n = self.table[b], self.lens[b]
             if new[b] == 0:
                 granted[b] = 1
                 continue
-            if new[b] < 0 or n + new[b] > len(row) * self.bs:
+            if new[b] < 0 or n < 0 or n + new[b] > len(row) * self.bs:
                 continue
-            at = n // self.bs
-            own = n % self.bs != 0 and self.holders[row[at]] > 1
-            missing = [j for j in range(self._pages(n), self._pages(n + new[b])) if row[j] < 0]
-            short = short or own + len(missing) > len(free)
+            entries = range(n // self.bs, self._pages(n + new[b]))
+            if any(row[j] >= len(held) or (row[j] < 0 and j * self.bs < n) or (row[j] >= 0 and held[row[j]] < 1)
+                   for j in entries):
+                continue
+            needs = [j for j in entries if row[j] < 0 or self.holders[row[j]] > 1]
+            short = short or len(needs) > len(free)
             if short:
                 continue
             granted[b] = 1
-            if own:
-                src[b], dst[b] = row[at], free.pop(0)
-                self.holders[src[b]] -= 1
-                self.holders[dst[b]] = 1
-                row[at] = dst[b]
-            for j in missing:
-                row[j] = free.pop(0)
-                self.holders[row[j]] = 1
+            for j in needs:
+                page = free.pop(0)
+                if row[j] >= 0:
+                    self.holders[row[j]] -= 1
+                    if j * self.bs < n:
+                        src[b], dst[b] = row[j], page
+                row[j] = page
+                self.holders[page] = 1
         return granted, src, dst
