@@ -460,14 +460,14 @@ FA_API size_t fa_pages_reserve_workspace_size(int B, int num_blocks);
 /*
  * fa_pages_reserve — pages for the next new_lens[b] tokens of every sequence of the
  *   table (device int32 [B]; 0: none).  They go into its entries from
- *   seq_lens[b] / block_size on.  Entries that are missing get free pages; entries
- *   reserved before stay.  An entry whose page others hold too (after fa_pages_fork,
- *   or where a length was set back without fa_pages_free) gets a page of its own in
- *   its place, and the old one has a holder less: of sequences that write into one
- *   page all but the last to hold it get another.  If tokens of the sequence lie in
- *   the page (so only where the next one goes), copy_src[b], copy_dst[b] name the
- *   old and the new page (both −1 otherwise), to be copied with fa_cache_copy_pages
- *   before anything is written.
+ *   seq_lens[b] / block_size on.  Entries that are missing (-1, wherever they are)
+ *   get free pages; entries reserved before stay.  An entry whose page others hold
+ *   too (after fa_pages_fork, or where a length was set back without fa_pages_free)
+ *   gets a page of its own in its place, and the old one has a holder less: of
+ *   sequences that write into one page all but the last to hold it get another.  If
+ *   tokens of the sequence lie in the page (so only where the next one goes),
+ *   copy_src[b], copy_dst[b] name the old and the new page (both −1 otherwise), to be
+ *   copied with fa_cache_copy_pages before anything is written.
  *   Sequences are served in order, free pages handed out by rising number.  From the
  *   first sequence that finds too few on, none with tokens to come is served:
  *   granted[b] = 0 and its entries stay as they were; else granted[b] = 1.  A length

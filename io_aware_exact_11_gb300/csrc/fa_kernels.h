@@ -189,7 +189,7 @@ struct PageParams {
   // reserve's workspace
   int* seg;    // [segments] free pages, then those before
   int* last;   // [B] page that the next token goes into, −1 where that is a new one (or none)
-  int* from;   // [B] first entry of the table that is missing; where pages behind the tokens are shared, ~(their first entry)
+  int* from;   // [B] first entry of the table that is missing; ~(the first behind the tokens) where some there are shared, or missing between others
   int* want;   // [B] pages missing, then where they begin among the free pages
   int* total;  // [1] pages handed out
   int B, n, num_blocks, block_size, max_blocks;

@@ -29,7 +29,8 @@
 // hand-out, in which every free page finds its sequence by a search in the prefix
 // sums: no list of free pages is kept or written.  Pages are shared up to the one that
 // holds a sequence's last token, unless a length was set back without giving up what lay
-// behind it.  Where a table names such pages, the middle kernel takes the sequences in turn.
+// behind it, and those reserved before have no gaps, unless the caller left some.  Where a
+// table names such pages, the middle kernel takes the sequences in turn.
 #include "fa_kernels.h"
 #include "sm103.cuh"
 
@@ -412,21 +413,21 @@ __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_cons
     const int lo = len >> shift;  // the next token's entry
     const int have = static_cast<int>((static_cast<int64_t>(len) + p.block_size - 1) >> shift);
     const int need = static_cast<int>((static_cast<int64_t>(len) + more + p.block_size - 1) >> shift);
-    // Pages reserved before come first; behind them the table is empty.
-    bool bad = false, unheld = false, shared = false;
+    // Mostly pages reserved before come first, and behind them the table is empty.
+    bool bad = false, unheld = false, in_turn = false;
     from = need;
     auto look = [&](int j, int page) {
       const int held = page >= 0 && page < p.num_blocks ? p.holders[page] : 1;
       bad |= page >= p.num_blocks || (j < have && page < 0);
       unheld |= held < 1;
-      shared |= j >= have && held > 1;
       const uint32_t missing = __ballot_sync(0xffffffffu, j < need && page < 0);
       if (missing != 0 && from == need) from = j - lane + __ffs(missing) - 1;
+      in_turn |= (j >= have && held > 1) || (page >= 0 && j > from);
     };
     const int first = lo + lane < need ? table[lo + lane] : -1;
     if (lo < have) last = __shfl_sync(0xffffffffu, first, 0);
     look(lo + lane, first);
-    // Mostly all is missing behind that.  (Every 32 looked at by themselves, 18 us instead of 15 for 8 x 2048 entries.)
+    // (Every 32 looked at by themselves, 18 us instead of 15 for 8 x 2048 entries.)
     constexpr int U = 16;
 #pragma unroll 1
     for (int j0 = lo + 32; j0 < need; j0 += 32 * U) {
@@ -451,8 +452,8 @@ __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_cons
     if (bad || unheld) {
       if (lane == 0) report(p.err, bad ? kSiteBadBlock : kSiteBadHolders);
       last = want = -1;
-    } else if (__any_sync(0xffffffffu, shared)) {
-      from = ~have;  // its turn will tell how many pages it misses
+    } else if (__any_sync(0xffffffffu, in_turn)) {
+      from = ~have;  // its turn will tell how many pages it needs, and where
     }
   }
   if (lane == 0) {
@@ -463,7 +464,8 @@ __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_cons
 }
 
 // One sequence after the other, by all threads of the scanning block: where tables name pages behind their sequences' tokens that
-// others hold too, how many a sequence needs depends on what those before it have given up.  Entries that are to get a page
+// others hold too, how many a sequence needs depends on what those before it have given up; and where entries are missing
+// between others, which those are has to be told to the hand-out.  Entries that are to get a page
 // become −2 − (their place among the sequence's), by which the hand-out finds them.  Some 2.6 us a sequence, all of it
 // latency: a state that a call leaves behind it for good.
 constexpr int kScanThreads = 1024;

@@ -1,5 +1,5 @@
 """Reservations for sequences whose tables name pages behind their tokens, on the GPU: lengths that the caller has set back
-after a fork, pages of each other at whatever entry."""
+after a fork, pages of each other at whatever entry, entries missing between others."""
 
 import numpy as np
 import pytest
@@ -82,6 +82,29 @@ def test_random_tables(B, per, spare, bs):
         if over:
             with pytest.raises(fa.FAError, match="length"):
                 fa.device_status()
+        fa.device_status()
+
+
+def test_entries_missing_between_others_get_pages_and_the_others_stay():
+    pool = serving.Pool([[0, -1, 4, -1], [1, -1, -1, -1]], [16, 5], [1, 1, 0, 0, 1, 0], 16)
+    assert _reserve(pool, [48, 12]) == [[1, 1], [-1, -1], [-1, -1]]
+    assert pool.table == [[0, 2, 4, 3], [1, 5, -1, -1]] and pool.holders == [1] * 6
+    fa.device_status()
+
+
+@pytest.mark.parametrize("B,per,spare,bs", [(1, 4, 3, 16), (6, 9, 12, 32), (50, 40, 900, 16), (7, 70, 400, 64), (4, 1500, 6000, 16),
+                                            (1100, 5, 3000, 16)])
+def test_random_tables_with_gaps(B, per, spare, bs):
+    for seed in range(5):
+        rng = np.random.default_rng(1000 * seed + B + per)
+        pool = random_pool(rng, B, per, spare, bs, gaps=True)
+        if seed % 2:  # every page held by one: the gaps alone
+            used = iter(rng.permutation(sum(p >= 0 for row in pool.table for p in row) + spare).tolist())
+            pool.table = [[next(used) if p >= 0 else -1 for p in row] for row in pool.table]
+            pool.holders = [0] * (max(list(used) + [p for row in pool.table for p in row]) + 1)
+            for p in (p for row in pool.table for p in row if p >= 0):
+                pool.holders[p] = 1
+        _reserve(pool, [int(rng.integers(0, per * bs - n + 1)) if rng.random() < 0.8 else 0 for n in pool.lens])
         fa.device_status()
 
 

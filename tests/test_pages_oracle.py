@@ -29,10 +29,11 @@ def test_the_last_to_hold_a_page_keeps_it():
     assert p.table == [[0, 2], [3, 4], [5, 1]] and p.holders == [1, 1, 1, 1, 1, 1, 0]
 
 
+@pytest.mark.parametrize("gaps", [False, True])
 @pytest.mark.parametrize("seed", range(200))
-def test_no_page_that_is_written_has_another_holder(seed):
+def test_no_page_that_is_written_has_another_holder(seed, gaps):
     rng = np.random.default_rng(seed)
-    pool = random_pool(rng, int(rng.integers(1, 9)), int(rng.integers(1, 7)), int(rng.integers(0, 25)), 16)
+    pool = random_pool(rng, int(rng.integers(1, 9)), int(rng.integers(1, 7)), int(rng.integers(0, 25)), 16, gaps)
     new = rng.integers(0, 40, len(pool.lens)).tolist()
     before, held = [list(r) for r in pool.table], list(pool.holders)
     out = pool.reserve(new)
