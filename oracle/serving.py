@@ -184,10 +184,10 @@ class Pool:
         short = False
         for b in range(B):
             row, n = self.table[b], self.lens[b]
+            if new[b] < 0 or n < 0 or n + new[b] > len(row) * self.bs:
+                continue
             if new[b] == 0:
                 granted[b] = 1
-                continue
-            if new[b] < 0 or n < 0 or n + new[b] > len(row) * self.bs:
                 continue
             entries = range(n // self.bs, self._pages(n + new[b]))
             if any(row[j] >= len(held) or (row[j] < 0 and j * self.bs < n) or (row[j] >= 0 and held[row[j]] < 1)

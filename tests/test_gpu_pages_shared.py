@@ -215,3 +215,13 @@ def test_captured_and_replayed():
         assert [x.tolist() for x in out] == [list(x) for x in want]
         assert [x.tolist() for x in dev] == [pool.table, pool.lens, pool.holders]
     fa.device_status()
+
+
+def test_a_length_that_cannot_be_is_not_served_without_tokens_either():
+    pool = serving.Pool([[0, -1], [1, -1], [2, -1]], [-1, 5, 33], [1, 1, 1], 16)
+    dev = _dev(pool)
+    got = fa.pages_reserve(*dev, _i32([0, 0, 0]), 16)
+    with pytest.raises(fa.FAError, match="length"):
+        fa.device_status()
+    assert [x.tolist() for x in got] == [list(x) for x in pool.reserve([0, 0, 0])] == [[0, 1, 0], [-1] * 3, [-1] * 3]
+    assert [x.tolist() for x in dev] == [pool.table, pool.lens, pool.holders]

@@ -38,3 +38,8 @@ def test_no_page_that_is_written_has_another_holder(seed, gaps):
     before, held = [list(r) for r in pool.table], list(pool.holders)
     out = pool.reserve(new)
     nobody_else_writes(pool, new, out, before, held)
+
+
+def test_a_length_that_cannot_be_is_not_served_without_tokens_either():
+    p = serving.Pool([[0, -1], [1, -1], [2, -1]], [-1, 5, 33], [1, 1, 1], 16)
+    assert p.reserve([0, 0, 0]) == ([0, 1, 0], [-1] * 3, [-1] * 3)
