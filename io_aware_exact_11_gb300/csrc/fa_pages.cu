@@ -70,8 +70,8 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // A chunk is U passes of the block over rows, of which kDeep are on their way, and kSteps chunks make a plan.  (Deeper rings
-// and longer plans leave room for fewer blocks: with 4 and 8 of two passes 48 us instead of 52 for the E4M3 rows below, and
-// 81 instead of 75 for twice as many.)
+// and longer plans leave room for fewer blocks: with 4 and 8 of two passes the E4M3 rows below take 50 us as now, those in bf16
+// 79 instead of 75, and twice as many E4M3 rows 81 instead of 75.)
 template <int LANES, int U>
 struct Plan {
   static constexpr int kStep = kThreads / LANES * U, kDeep = U == 2 ? 3 : 2, kSteps = U == 2 ? 6 : 5, kPlan = kSteps * kStep;
@@ -82,7 +82,7 @@ struct Plan {
 // Moves LANES 16-byte columns of the rows kept of one sequence and head, keys or values.  SB: bytes of a row's scales,
 // moved by the blocks of the first columns.  Of every chunk the blocks of a cluster take equal shares.
 //
-// 8 sequences of 16384 tokens, 8 heads, d = 128, 6000 rows kept of each: 76 us in bf16 (5.2 TB/s of reads and writes), 52 in
+// 8 sequences of 16384 tokens, 8 heads, d = 128, 6000 rows kept of each: 75 us in bf16 (5.2 TB/s of reads and writes), 50 in
 // E4M3, 36 in E2M1.  Bound by the latency from a chunk's reads to its barrier while the SMs have two blocks each, and by
 // device memory beyond that.
 template <int RB, int SB, int LANES, int U>
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_cons
 // One sequence after the other, by all threads of the scanning block: where tables name pages behind their sequences' tokens that
 // others hold too, how many a sequence needs depends on what those before it have given up; and where entries are missing
 // between others, which those are has to be told to the hand-out.  Entries that are to get a page
-// become −2 − (their place among the sequence's), by which the hand-out finds them.  Some 2.6 us a sequence, all of it
+// become −2 − (their place among the sequence's), by which the hand-out finds them.  Some 2.7 us a sequence, all of it
 // latency: a state that a call leaves behind it for good.
 constexpr int kScanThreads = 1024;
 static __device__ __noinline__ void reserve_in_turn(const PageParams& p, int frees, int* warp_sum) {
@@ -527,7 +527,7 @@ static __device__ __noinline__ void reserve_in_turn(const PageParams& p, int fre
     if (p.copy_src[b] >= 0) atomicAdd(p.holders + p.copy_src[b], 1);
 }
 
-// Prefix sums over segments and sequences, and who is served.  512 sequences that all write into shared pages: 14 us, most of
+// Prefix sums over segments and sequences, and who is served.  512 sequences that all write into shared pages: 13 us, most of
 // it every thread's count over all sequences' last pages (19 us with one page a load and a search that ends early).
 constexpr int kMaxSequences = 4096;
 __global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(const __grid_constant__ PageParams p, int segments) {
@@ -665,10 +665,11 @@ __global__ void __launch_bounds__(kThreads) pages_hand_out_kernel(const __grid_c
 
 template <int RB, int SB>
 cudaError_t launch_compact(const MoveParams& p, cudaStream_t s) {
-  // Columns of 64 bytes (32-byte rows: 32): four lanes hold a row's part.  Blocks that do not fill the SMs are clusters that
-  // share the rows: one sequence of 32768 tokens, 2 heads, 12000 rows kept, E4M3, 8 blocks: 22 us instead of 60 (with columns
-  // of 16 bytes and no clusters).  A cluster's barrier costs more than a block's, so where the SMs have a block each there
-  // are none (without plans ahead 256 blocks took 56 us, 512 in pairs 63).
+  // Columns of 64 bytes (32-byte rows: 32): four lanes hold a row's part (one lane, 16 bytes: 120 us instead of 50 for the E4M3
+  // rows above, 173 instead of 75 for bf16).  Blocks that do not fill the SMs are clusters that share the rows: one sequence of
+  // 32768 tokens, 2 heads, 12000 rows kept, E4M3, 8 blocks: 22 us, 67 without clusters; the E2M1 rows above, 128 blocks: 36 and
+  // 48.  A cluster's barrier costs more than a block's, so where the SMs have a block each there are none: the 256 blocks of the
+  // E4M3 rows take 54 us in pairs and 50 alone.
   constexpr int kLanes = RB >= 64 ? 4 : RB / 16;
   constexpr int kRows = kThreads / kLanes;
   const int64_t blocks = static_cast<int64_t>(p.B) * p.Hkv * 2 * (RB / (16 * kLanes));
@@ -687,8 +688,9 @@ cudaError_t launch_compact(const MoveParams& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  // Chunks of four passes where clusters wait for one another at each (two: 28 and 42 us instead of 24 and 38, E4M3 and
-  // E2M1 as above, without plans ahead), of two otherwise (256 blocks that keep 6000 or fewer E4M3 rows: 49 us instead of 51).
+  // Chunks of four passes where clusters wait for one another at each (two: 26 and 40 us instead of 22 and 36, the one sequence
+  // and the E2M1 rows above), of two otherwise (four: the E4M3 rows above 48 us instead of 50, but twice as many 91 instead of 75,
+  // and those in bf16 81 instead of 75).
   auto launch = [&](auto* kernel, int smem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

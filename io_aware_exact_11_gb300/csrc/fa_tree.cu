@@ -65,11 +65,11 @@
 // rows that do see them at the end.
 //
 // Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements (replaying a graph over two caches):
-//   4 / 16 / 32 rows, bf16   88 / 90 / 92 us   6.1 / 6.0 / 5.8 TB/s, 0.91 of a device copy: bound by device memory
-//   4 / 16 / 32 rows, E4M3   55 / 56 / 66 us   4.9 / 4.8 / 4.1 TB/s: inside a piece 4 and 16 rows run at the memory's
+//   4 / 16 / 32 rows, bf16   91 / 92 / 95 us   5.9 / 5.8 / 5.7 TB/s, 0.88 of a device copy: bound by device memory
+//   4 / 16 / 32 rows, E4M3   58 / 59 / 68 us   4.7 / 4.6 / 4.0 TB/s: inside a piece 4 and 16 rows run at the memory's
 //                            rate; start, piece ends and the joining kernel take 15 us, and with 32 rows the softmax
 //                            warps, which also widen V, are the bound
-//   4 / 16 / 32 rows, E2M1   54 / 62 / 81 us   2.6 / 2.3 / 1.8 TB/s: a stream's tile is a chain of 3300 cycles (its values'
+//   4 / 16 / 32 rows, E2M1   54 / 62 / 80 us   2.6 / 2.3 / 1.8 TB/s (8 rows 55, E4M3 58): a stream's tile is a chain of 3300 cycles (its values'
 //                            codes 550, their reference 600, the place of the widened tile 400, widening 1450) and both
 //                            streams' instructions take two thirds of it; with 32 rows the softmax adds to that
 // E2M1, not kept: both halves written out as bf16 tiles by four warps, 195 us at 16 rows; codes of both halves fetched by one
@@ -1249,11 +1249,11 @@ template <int D, int F>
 cudaError_t launch_d(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.T) * p.G;
   // By the rows of a pair; 8 sequences of 16384 keys, 8 key/value heads, us with the one and the other:
-  //   4 and 16 rows as 16 columns or 32    E4M3 55, 56 | 60, 62    bf16 89, 90 | 88, 90 (head dim 64 51, 52 | 54, 55)
-  //                                        E2M1 60, 61 | 81, 83 (head dim 64 52, 53 | 61, 64)
-  //   16 and 32 rows here or in the kernel for many rows    E4M3 56, 66 | 72, 74    bf16 90, 92 | 93, 95
-  //                                                         E2M1 61, 81 | 84, 87 (head dim 64 53, 66 | 74, 75)
-  //   4 rows of which the softmax works on 8 or 16    E2M1 54 | 60 (head dim 64 47 | 52); the others' softmax is no bound
+  //   4 and 16 rows as 16 columns or 32    E4M3 58, 59 | 64, 66    bf16 91, 92 | 91, 93 (head dim 64 54, 55 | 58, 58)
+  //                                        E2M1 54, 62 | 71, 76 (head dim 64 47, 53 | 61, 64)
+  //   16 and 32 rows here or in the kernel for many rows    E4M3 59, 68 | 76, 78    bf16 92, 95 | 95, 97
+  //                                                         E2M1 62, 80 | 85, 87 (head dim 64 53, 66 | 74, 75)
+  //   4 rows of which the softmax works on 8 or 16    E2M1 54 | 59 (head dim 64 47 | 51); the others' softmax is no bound
   //   at so few
   // (32 rows are the most that fit here without tiles of rows; 64 columns spilled registers and took 81 us where the
   // other kernel took 69: 8 tokens of 7 heads a group, 16 ragged sequences of up to 8192 bf16 keys.)

@@ -36,9 +36,9 @@
 // The rest (parts, pieces, masks, values in masked places) is as in fa_tree.cu.
 //
 // Measured on GB300, 8 sequences of 16384 keys, 8 key/value heads of 128 elements (replaying a graph over two caches):
-//   64 / 128 / 256 rows, bf16    98 / 104 / 125 us   0.82 / 0.77 of a device copy, 1100 TFLOP/s
-//   64 / 128 / 256 rows, E4M3    76 /  84 / 140 us   452 / 818 / 982 TFLOP/s
-//   64 / 128 / 256 rows, E2M1    87 /  90 / 144 us   395 / 761 / 957 TFLOP/s (32768 keys, 256 rows: 252 us, 1089)
+//   64 / 128 / 256 rows, bf16    99 / 105 / 125 us   0.81 / 0.76 of a device copy, 1097 TFLOP/s
+//   64 / 128 / 256 rows, E4M3    80 /  84 / 134 us   430 / 813 / 1023 TFLOP/s (32768 keys, 256 rows: 230 us, 1194)
+//   64 / 128 / 256 rows, E2M1    88 /  91 / 144 us   390 / 756 / 956 TFLOP/s (32768 keys, 256 rows: 253 us, 1088)
 // With two row tiles a step (one tile's P̃V and S, 1024 tensor cycles) takes about 1750 cycles: the issuing
 // warp's own instructions, of which it gets one through every dozen cycles beside the softmax warps, and the wait
 // for P̃ (S to P̃ is a chain of about 1400 cycles).  E4M3 with shared rows waits for the converters (2400 cycles a
@@ -1072,7 +1072,8 @@ cudaError_t launch(const TreeParams& p, cudaStream_t s) {
 }
 
 // Two row tiles share a CTA's keys where there are more than 128 rows.  Below, the second would be empty: 64 and 128
-// rows with shared rows or with two tiles, E4M3 76, 84 | 114, 121 us, bf16 98, 103 | 103, 109 us (8 x 16384 keys).
+// rows with shared rows or with two tiles, E4M3 80, 84 | 117, 121 us, bf16 99, 105 | 107, 113, E2M1 88, 91 | 125, 129
+// (8 x 16384 keys).
 template <int D, int F>
 cudaError_t launch_tiles(const TreeParams& p, cudaStream_t s) {
   return p.T * p.G <= kRowTile ? launch<D, F, 1>(p, s) : launch<D, F, 2>(p, s);
